@@ -25,6 +25,9 @@ STATUS_NONFINITE = 0x2
 OP_LOGPROB_ENTROPY, OP_GRPO_LOSS, OP_LMHEAD, OP_LMHEAD_BWD, OP_LMHEAD_TOPP = 0, 1, 2, 3, 4
 OP_CANONICAL = 5
 OP_CANONICAL_TOPP = 6
+OP_NORM_BWD = 7
+NORM_LAYER, NORM_RMS = 0, 1
+CHECKPOINT_BLOCK = 32   # columns that share one checkpoint scale
 SHARD_COUNTS_BYTES = 8224   # rlk_shard_counts: one row's window counts of one shard
 CANONICAL_TP, CANONICAL_VOCAB = 8, 152576
 SHARD_PARTIAL_WORDS = 8   # rlk_shard_partial: 32 bytes per (shard, row)
@@ -44,6 +47,12 @@ class LossConfig(ctypes.Structure):
                 ("baseline", ctypes.c_int), ("agg", ctypes.c_int)]
 
 
+class CheckpointBuffers(ctypes.Structure):
+    """rlk_checkpoint."""
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("ld_codes", ctypes.c_int64), ("ld_scales", ctypes.c_int64)]
+
+
 STAT_NAMES = ("loss", "tokens", "clip_low_frac", "clip_high_frac", "tis_mean",
               "tis_capped_frac", "k3_mean", "pg_mean")
 EXPORTS = ("rlk_version", "rlk_status_string", "rlk_workspace_size", "rlk_logprob_entropy",
@@ -55,7 +64,8 @@ EXPORTS = ("rlk_version", "rlk_status_string", "rlk_workspace_size", "rlk_logpro
            "rlk_logprob_entropy_canonical", "rlk_sample_top_p",
            "rlk_shard_window_counts", "rlk_shard_combine_topp",
            "rlk_logprob_entropy_canonical_topp",
-           "rlk_grpo_loss_noalloc")
+           "rlk_grpo_loss_noalloc", "rlk_checkpoint_pack", "rlk_checkpoint_unpack",
+           "rlk_norm_fwd", "rlk_norm_bwd")
 NOALLOC_MAX_SEQ = 16384
 DEBUG_EXPORTS = ("rlk_lmhead_logits_debug", "rlk_debug_inject_launch_failures",
                  "rlk_debug_set_wait_limit", "rlk_debug_withhold_copy",
@@ -169,6 +179,18 @@ def load(path: str | None = None):
         lib.rlk_grpo_loss_noalloc.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, i64, f32, f32,
                                               f32, f32, ctypes.c_int, vp, vp, vp, vp]
         lib.rlk_grpo_loss_noalloc.restype = ctypes.c_int
+        ck = ctypes.POINTER(CheckpointBuffers)
+        lib.rlk_checkpoint_pack.argtypes = [vp, ctypes.c_int, i64, i64, i64, ck, vp, vp]
+        lib.rlk_checkpoint_pack.restype = ctypes.c_int
+        lib.rlk_checkpoint_unpack.argtypes = [ck, i64, i64, vp, ctypes.c_int, i64, vp]
+        lib.rlk_checkpoint_unpack.restype = ctypes.c_int
+        lib.rlk_norm_fwd.argtypes = [vp, ctypes.c_int, i64, i64, i64, vp, vp, ctypes.c_int,
+                                     ctypes.c_int, f32, vp, ctypes.c_int, i64, vp, vp, ck, vp, vp]
+        lib.rlk_norm_fwd.restype = ctypes.c_int
+        lib.rlk_norm_bwd.argtypes = [vp, ctypes.c_int, i64, vp, ctypes.c_int, i64, ck, i64, i64, vp,
+                                     ctypes.c_int, ctypes.c_int, vp, vp, vp, ctypes.c_int, i64, vp,
+                                     vp, ctypes.c_int, vp, sz, vp]
+        lib.rlk_norm_bwd.restype = ctypes.c_int
         _lib = lib
         return lib
 
@@ -818,6 +840,202 @@ def sample_top_p(logits, temperature, top_p, uniforms, *, row_state=None, status
                                 _stream(logits.device))
     _check("rlk_sample_top_p", code)
     return out
+
+
+# ------------------------------------------- norm and activation checkpoints
+_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def _matrix(t, name):
+    """dtype index and row stride of a 2-D bf16 / fp32 tensor with unit stride along its rows."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be 2-D with unit stride along its rows")
+    dt = _DTYPES.get(t.dtype)
+    if dt is None:
+        raise ValueError(f"{name} must be bf16 or fp32")
+    return dt, (t.stride(0) if t.shape[0] > 1 else t.shape[1])
+
+
+def _params(H, *ts):
+    """dtype index of the parameter vectors given (fp32 when none is)."""
+    dts = {t.dtype for t in ts if t is not None}
+    if len(dts) > 1:
+        raise ValueError("weight and bias must have one dtype")
+    dt = _DTYPES.get(dts.pop()) if dts else 1
+    if dt is None:
+        raise ValueError("weight and bias must be bf16 or fp32")
+    for t in ts:
+        if t is not None and (t.dim() != 1 or t.numel() != H or not t.is_contiguous()):
+            raise ValueError(f"weight and bias must be contiguous [{H}]")
+    return dt
+
+
+class Checkpoint:
+    """An activation [T, H] kept in 8 bits (rlk_checkpoint): int8 ``codes``
+    [T, >= H] and uint8 ``scales`` [T, >= ceil(H / 32)]."""
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, T: int, H: int):
+        _need_cuda(codes, scales)
+        blocks = -(-H // CHECKPOINT_BLOCK)
+        if codes.dtype != torch.int8 or scales.dtype != torch.uint8:
+            raise ValueError("codes must be int8, scales uint8")
+        for t, cols in ((codes, H), (scales, blocks)):
+            if t.dim() != 2 or t.shape[0] != T or t.shape[1] < cols or not t.is_contiguous():
+                raise ValueError("codes and scales must be contiguous [T, >= H] and [T, >= ceil(H / 32)]")
+        self.codes, self.scales, self.T, self.H = codes, scales, T, H
+
+    @property
+    def shape(self):
+        return (self.T, self.H)
+
+    def buffers(self):
+        return CheckpointBuffers(self.codes.data_ptr(), self.scales.data_ptr(),
+                                 self.codes.shape[1], self.scales.shape[1])
+
+
+def new_checkpoint(T: int, H: int, device) -> Checkpoint:
+    """Room for the 8-bit checkpoint of an activation [T, H]."""
+    pad = lambda n: -(-n // 16) * 16
+    return Checkpoint(torch.empty((T, pad(H)), dtype=torch.int8, device=device),
+                      torch.empty((T, pad(-(-H // CHECKPOINT_BLOCK))), dtype=torch.uint8, device=device),
+                      T, H)
+
+
+def checkpoint_pack(x: torch.Tensor, *, out: Checkpoint | None = None, status_word=None) -> Checkpoint:
+    """The 8-bit checkpoint of x (CUDA [T, H] bf16 or fp32, rows may be strided)."""
+    lib = load()
+    _need_cuda(x, status_word)
+    dt, ld = _matrix(x, "x")
+    T, H = x.shape
+    if out is None:
+        out = new_checkpoint(T, H, x.device)
+    if out.shape != (T, H):
+        raise ValueError("out must be a checkpoint of x's shape")
+    b = out.buffers()
+    _check("rlk_checkpoint_pack",
+           lib.rlk_checkpoint_pack(_ptr(x), dt, T, H, ld, ctypes.byref(b), _ptr(status_word),
+                                   _stream(x.device)))
+    return out
+
+
+def checkpoint_unpack(checkpoint: Checkpoint, *, dtype=torch.bfloat16, out=None) -> torch.Tensor:
+    """The values a checkpoint stands for (exact in bf16 and fp32)."""
+    lib = load()
+    T, H = checkpoint.shape
+    if out is None:
+        out = torch.empty((T, H), dtype=dtype, device=checkpoint.codes.device)
+    _need_cuda(out)
+    dt, ld = _matrix(out, "out")
+    if tuple(out.shape) != (T, H):
+        raise ValueError("out must be [T, H]")
+    b = checkpoint.buffers()
+    _check("rlk_checkpoint_unpack",
+           lib.rlk_checkpoint_unpack(ctypes.byref(b), T, H, _ptr(out), dt, ld, _stream(out.device)))
+    return out
+
+
+def norm(x: torch.Tensor, weight=None, bias=None, *, kind: int = NORM_LAYER, eps: float = 1e-5,
+         out=None, out_dtype=None, checkpoint: Checkpoint | None = None, status_word=None):
+    """Layer or RMS norm of each row of x (CUDA [T, H] bf16 or fp32).  Returns
+    (y, mean, rstd); mean is None for NORM_RMS.  ``checkpoint`` (from
+    ``new_checkpoint``) receives x in 8 bits for ``norm_backward``."""
+    lib = load()
+    _need_cuda(x, weight, bias, out, status_word)
+    dt, ld = _matrix(x, "x")
+    T, H = x.shape
+    pdt = _params(H, weight, bias)
+    if out is None:
+        out = torch.empty((T, H), device=x.device, dtype=out_dtype or x.dtype)
+    ydt, ldy = _matrix(out, "out")
+    if tuple(out.shape) != (T, H):
+        raise ValueError("out must be [T, H]")
+    if checkpoint is not None and checkpoint.shape != (T, H):
+        raise ValueError("checkpoint must be of x's shape")
+    mean = None if kind == NORM_RMS else torch.empty(T, device=x.device, dtype=torch.float32)
+    rstd = torch.empty(T, device=x.device, dtype=torch.float32)
+    ck = None if checkpoint is None else ctypes.byref(checkpoint.buffers())
+    _check("rlk_norm_fwd",
+           lib.rlk_norm_fwd(_ptr(x), dt, T, H, ld, _ptr(weight), _ptr(bias), pdt, int(kind),
+                            float(eps), _ptr(out), ydt, ldy, _ptr(mean), _ptr(rstd), ck,
+                            _ptr(status_word), _stream(x.device)))
+    return out, mean, rstd
+
+
+def norm_backward(dy: torch.Tensor, x, weight, mean, rstd, *, kind: int = NORM_LAYER,
+                  grad_dtype=None, out=None, want_weight_grad: bool = True,
+                  want_bias_grad: bool = True, grad_weight=None, grad_bias=None,
+                  accumulate: bool = False, workspace=None):
+    """Gradients of ``norm``: (dL/dx, dL/dweight fp32 [H] or None, dL/dbias
+    fp32 [H] or None).  ``x`` is the forward's input or its ``Checkpoint``;
+    ``dy`` bf16 or fp32 (``lmhead_backward``'s grad_hidden).  ``accumulate``
+    adds into ``grad_weight`` / ``grad_bias``."""
+    lib = load()
+    kept = x if isinstance(x, Checkpoint) else None
+    _need_cuda(dy, None if kept else x, weight, mean, rstd, out, grad_weight, grad_bias)
+    gdt, ldg = _matrix(dy, "dy")
+    T, H = dy.shape
+    if tuple(x.shape) != (T, H):
+        raise ValueError("x must have dy's shape")
+    dt, ld = (0, H) if kept else _matrix(x, "x")
+    pdt = _params(H, weight)
+    for t in (mean, rstd):
+        if t is not None and (t.dtype != torch.float32 or t.numel() != T or not t.is_contiguous()):
+            raise ValueError("mean and rstd must be contiguous fp32 [T]")
+    if out is None:
+        out = torch.empty((T, H), device=dy.device,
+                          dtype=grad_dtype or (torch.bfloat16 if kept else x.dtype))
+    odt, ldo = _matrix(out, "out")
+    if tuple(out.shape) != (T, H):
+        raise ValueError("out must be [T, H]")
+    if accumulate and ((want_weight_grad and grad_weight is None) or (want_bias_grad and grad_bias is None)):
+        raise ValueError("accumulate needs grad_weight and grad_bias")
+    if grad_weight is None and want_weight_grad:
+        grad_weight = torch.empty(H, device=dy.device, dtype=torch.float32)
+    if grad_bias is None and want_bias_grad:
+        grad_bias = torch.empty(H, device=dy.device, dtype=torch.float32)
+    for t in (grad_weight, grad_bias):
+        if t is not None and (t.dtype != torch.float32 or t.numel() != H or not t.is_contiguous()):
+            raise ValueError("grad_weight and grad_bias must be contiguous fp32 [H]")
+    if workspace is None and (grad_weight is not None or grad_bias is not None):
+        workspace = torch.empty(max(int(lib.rlk_workspace_size(OP_NORM_BWD, T, H, 0)), 16),
+                                device=dy.device, dtype=torch.uint8)
+    ck = None if kept is None else ctypes.byref(kept.buffers())
+    _check("rlk_norm_bwd",
+           lib.rlk_norm_bwd(_ptr(dy), gdt, ldg, None if kept else _ptr(x), dt, ld, ck, T, H,
+                            _ptr(weight), pdt, int(kind), _ptr(mean), _ptr(rstd), _ptr(out), odt,
+                            ldo, _ptr(grad_weight), _ptr(grad_bias), int(bool(accumulate)),
+                            _ptr(workspace), 0 if workspace is None else workspace.numel(),
+                            _stream(dy.device)))
+    return out, grad_weight, grad_bias
+
+
+class _Norm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, kind, eps, keep8):
+        ck = new_checkpoint(x.shape[0], x.shape[1], x.device) if keep8 else None
+        y, mean, rstd = norm(x, weight, bias, kind=kind, eps=eps, checkpoint=ck)
+        ctx.save_for_backward(ck.codes if keep8 else x, ck.scales if keep8 else None, weight, mean, rstd)
+        ctx.kind, ctx.H, ctx.x_dtype = kind, x.shape[1], x.dtype
+        ctx.bias_dtype = None if bias is None else bias.dtype
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        kept, scales, weight, mean, rstd = ctx.saved_tensors
+        x = kept if scales is None else Checkpoint(kept, scales, kept.shape[0], ctx.H)
+        dx, dw, db = norm_backward(dy.contiguous(), x, weight, mean, rstd, kind=ctx.kind,
+                                   grad_dtype=ctx.x_dtype,
+                                   want_weight_grad=weight is not None and ctx.needs_input_grad[1],
+                                   want_bias_grad=ctx.bias_dtype is not None and ctx.needs_input_grad[2])
+        return (dx, None if dw is None else dw.to(weight.dtype),
+                None if db is None else db.to(ctx.bias_dtype), None, None, None)
+
+
+def norm_autograd(x: torch.Tensor, weight=None, bias=None, *, kind: int = NORM_LAYER,
+                  eps: float = 1e-5, keep_8bit: bool = False):
+    """``norm`` as a differentiable op; ``keep_8bit`` keeps x for the backward as
+    its 8-bit checkpoint instead of the tensor."""
+    return _Norm.apply(x, weight, bias, kind, eps, keep_8bit)
 
 
 def inject_launch_failures(n: int) -> int:

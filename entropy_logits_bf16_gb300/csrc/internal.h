@@ -180,6 +180,66 @@ struct SampleArgs {
   int32_t* out_ids;
   uint32_t* status;
 };
+// 8-bit activation checkpoints (checkpoint.cu); the buffers of rlk_checkpoint.
+struct CheckpointView {
+  int8_t* codes = nullptr;
+  uint8_t* scales = nullptr;
+  int64_t ldc = 0, lds = 0;
+};
+struct CheckpointArgs {
+  void* x;              // read by pack, written by unpack
+  int dtype;            // 0 bf16, 1 fp32
+  int64_t T, H, ldx;
+  CheckpointView ck;
+  uint32_t* status;
+};
+cudaError_t launch_checkpoint_pack(const CheckpointArgs& a, cudaStream_t stream);
+cudaError_t launch_checkpoint_unpack(const CheckpointArgs& a, cudaStream_t stream);
+
+// Layer / RMS norm (norm.cu).
+struct NormArgs {
+  const void* x;
+  int dtype;            // 0 bf16, 1 fp32
+  int64_t T, H, ldx;
+  const void* weight;   // [H] or NULL
+  const void* bias;     // [H] or NULL
+  int param_dtype;
+  int rms;
+  float eps;
+  void* y;
+  int y_dtype;
+  int64_t ldy;
+  float* mean;          // [T] or NULL
+  float* rstd;          // [T] or NULL
+  CheckpointView ck;    // codes NULL: none
+  uint32_t* status;
+};
+struct NormBwdArgs {
+  const void* dy;
+  int dy_dtype;
+  int64_t lddy;
+  const void* x;        // NULL: from ck
+  int dtype;
+  int64_t ldx;
+  CheckpointView ck;
+  int64_t T, H;
+  const void* weight;
+  int param_dtype;
+  int rms;
+  const float* mean;
+  const float* rstd;
+  void* dx;
+  int dx_dtype;
+  int64_t lddx;
+  float* dw;            // [H] or NULL
+  float* db;            // [H] or NULL
+  int accumulate;
+  float* workspace;     // [parts][2][H] partial parameter gradients
+};
+size_t norm_bwd_workspace_bytes(int64_t T, int64_t H);
+cudaError_t launch_norm_fwd(const NormArgs& a, cudaStream_t stream);
+cudaError_t launch_norm_bwd(const NormBwdArgs& a, cudaStream_t stream);
+
 cudaError_t launch_sample(const SampleArgs& a, cudaStream_t stream);
 cudaError_t launch_shard_partials(const ShardArgs& a, cudaStream_t stream);
 cudaError_t launch_shard_combine(const ShardCombineArgs& a, cudaStream_t stream);

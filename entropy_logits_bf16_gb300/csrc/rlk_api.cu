@@ -141,6 +141,7 @@ size_t rlk_workspace_size(int op, int64_t T, int64_t V, int64_t H) {
     case RLK_OP_LMHEAD: return rlk::lmhead_workspace_bytes(T, V, H);
     case RLK_OP_LMHEAD_BWD: return rlk::lmhead_bwd_workspace_bytes(T, V, H);
     case RLK_OP_LMHEAD_TOPP: return rlk::lmhead_topp_workspace_bytes(T, V, H);
+    case RLK_OP_NORM_BWD: return rlk::norm_bwd_workspace_bytes(T, V);
     case RLK_OP_CANONICAL:
       return V < 1 ? 0 : (size_t)V * (size_t)T * sizeof(rlk_shard_partial);
     case RLK_OP_CANONICAL_TOPP:
@@ -818,6 +819,163 @@ rlk_status rlk_lmhead_logprob_bwd(const void* hidden, const void* w_vocab, int64
       rlk::launch_lmhead_backward(a, reinterpret_cast<cudaStream_t>(stream));
   if (e == cudaErrorNotSupported) return RLK_ERR_UNSUPPORTED;
   return e == cudaSuccess ? RLK_OK : RLK_ERR_CUDA;
+}
+
+namespace {
+
+constexpr int64_t kMaxWidth = int64_t(1) << 20;
+
+bool good_dtype(rlk_dtype d) { return d == RLK_BF16 || d == RLK_F32; }
+int dtype_index(rlk_dtype d) { return d == RLK_BF16 ? 0 : 1; }
+bool aligned_to(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+bool elem_aligned(const void* p, rlk_dtype d) { return aligned_to(p, d == RLK_BF16 ? 2u : 4u); }
+
+// A checkpoint's buffers for rows of H columns (see rlk_checkpoint).
+bool checkpoint_ok(const rlk_checkpoint* c, int64_t H, rlk::CheckpointView& v) {
+  if (!c || !c->codes || !c->scales || !aligned_to(c->codes, 16)) return false;
+  if (c->ld_codes < H || c->ld_codes % 16 != 0) return false;
+  if (c->ld_scales < (H + RLK_CHECKPOINT_BLOCK - 1) / RLK_CHECKPOINT_BLOCK) return false;
+  v.codes = c->codes;
+  v.scales = c->scales;
+  v.ldc = c->ld_codes;
+  v.lds = c->ld_scales;
+  return true;
+}
+
+rlk_status checkpoint_args(const void* x, rlk_dtype dtype, int64_t T, int64_t H, int64_t ldx,
+                           const rlk_checkpoint* c, rlk::CheckpointArgs& a) {
+  if (!good_dtype(dtype) || T < 0 || H < 1 || H > kMaxWidth || ldx < H) return RLK_ERR_INVALID_ARG;
+  if (T == 0) return RLK_OK;
+  if (!x || !elem_aligned(x, dtype) || !checkpoint_ok(c, H, a.ck)) return RLK_ERR_INVALID_ARG;
+  a.x = const_cast<void*>(x);
+  a.dtype = dtype_index(dtype);
+  a.T = T;
+  a.H = H;
+  a.ldx = ldx;
+  a.status = nullptr;
+  return RLK_OK;
+}
+
+}  // namespace
+
+// The layout the Python binding mirrors.
+static_assert(sizeof(rlk_checkpoint) == 32 && offsetof(rlk_checkpoint, ld_codes) == 16,
+              "rlk_checkpoint layout");
+
+rlk_status rlk_checkpoint_pack(const void* x, rlk_dtype dtype, int64_t T, int64_t H, int64_t ldx,
+                               const rlk_checkpoint* out, uint32_t* out_status_word,
+                               rlk_stream stream) {
+  rlk::CheckpointArgs a{};
+  const rlk_status st = checkpoint_args(x, dtype, T, H, ldx, out, a);
+  if (st != RLK_OK || T == 0) return st;
+  a.status = out_status_word;
+  if (rlk::take_injected_failure()) return RLK_ERR_CUDA;
+  return rlk::launch_checkpoint_pack(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? RLK_OK
+             : RLK_ERR_CUDA;
+}
+
+rlk_status rlk_checkpoint_unpack(const rlk_checkpoint* in, int64_t T, int64_t H, void* out,
+                                 rlk_dtype dtype, int64_t ldo, rlk_stream stream) {
+  rlk::CheckpointArgs a{};
+  const rlk_status st = checkpoint_args(out, dtype, T, H, ldo, in, a);
+  if (st != RLK_OK || T == 0) return st;
+  if (rlk::take_injected_failure()) return RLK_ERR_CUDA;
+  return rlk::launch_checkpoint_unpack(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? RLK_OK
+             : RLK_ERR_CUDA;
+}
+
+rlk_status rlk_norm_fwd(const void* x, rlk_dtype dtype, int64_t T, int64_t H, int64_t ldx,
+                        const void* weight, const void* bias, rlk_dtype param_dtype,
+                        rlk_norm_kind kind, float eps, void* y, rlk_dtype y_dtype, int64_t ldy,
+                        float* out_mean, float* out_rstd, const rlk_checkpoint* out_checkpoint,
+                        uint32_t* out_status_word, rlk_stream stream) {
+  if (!good_dtype(dtype) || !good_dtype(param_dtype) || !good_dtype(y_dtype))
+    return RLK_ERR_INVALID_ARG;
+  if (kind != RLK_NORM_LAYER && kind != RLK_NORM_RMS) return RLK_ERR_INVALID_ARG;
+  if (T < 0 || H < 1 || H > kMaxWidth || ldx < H || ldy < H) return RLK_ERR_INVALID_ARG;
+  if (!(std::isfinite(eps) && eps >= 0.0f)) return RLK_ERR_INVALID_ARG;
+  if (T == 0) return RLK_OK;
+  if (!x || !y || !elem_aligned(x, dtype) || !elem_aligned(y, y_dtype) ||
+      !elem_aligned(weight, param_dtype) || !elem_aligned(bias, param_dtype))
+    return RLK_ERR_INVALID_ARG;
+  rlk::NormArgs a{};
+  if (out_checkpoint && !checkpoint_ok(out_checkpoint, H, a.ck)) return RLK_ERR_INVALID_ARG;
+  a.x = x;
+  a.dtype = dtype_index(dtype);
+  a.T = T;
+  a.H = H;
+  a.ldx = ldx;
+  a.weight = weight;
+  a.bias = bias;
+  a.param_dtype = dtype_index(param_dtype);
+  a.rms = kind == RLK_NORM_RMS;
+  a.eps = eps;
+  a.y = y;
+  a.y_dtype = dtype_index(y_dtype);
+  a.ldy = ldy;
+  a.mean = out_mean;
+  a.rstd = out_rstd;
+  a.status = out_status_word;
+  if (rlk::take_injected_failure()) return RLK_ERR_CUDA;
+  return rlk::launch_norm_fwd(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? RLK_OK
+             : RLK_ERR_CUDA;
+}
+
+rlk_status rlk_norm_bwd(const void* dy, rlk_dtype dy_dtype, int64_t lddy, const void* x,
+                        rlk_dtype dtype, int64_t ldx, const rlk_checkpoint* checkpoint, int64_t T,
+                        int64_t H, const void* weight, rlk_dtype param_dtype, rlk_norm_kind kind,
+                        const float* mean, const float* rstd, void* grad_x, rlk_dtype grad_dtype,
+                        int64_t ldg, float* grad_weight, float* grad_bias, int accumulate,
+                        void* workspace, size_t workspace_bytes, rlk_stream stream) {
+  if (!good_dtype(dy_dtype) || !good_dtype(dtype) || !good_dtype(param_dtype) ||
+      !good_dtype(grad_dtype))
+    return RLK_ERR_INVALID_ARG;
+  if (kind != RLK_NORM_LAYER && kind != RLK_NORM_RMS) return RLK_ERR_INVALID_ARG;
+  if (T < 0 || H < 1 || H > kMaxWidth || lddy < H || ldg < H || (!checkpoint && ldx < H))
+    return RLK_ERR_INVALID_ARG;
+  rlk::NormBwdArgs a{};
+  if (T > 0) {
+    if (!dy || !rstd || !grad_x || (kind == RLK_NORM_LAYER && !mean) || (!x == !checkpoint))
+      return RLK_ERR_INVALID_ARG;
+    if (!elem_aligned(dy, dy_dtype) || !elem_aligned(x, dtype) ||
+        !elem_aligned(weight, param_dtype) || !elem_aligned(grad_x, grad_dtype))
+      return RLK_ERR_INVALID_ARG;
+    if (checkpoint && !checkpoint_ok(checkpoint, H, a.ck)) return RLK_ERR_INVALID_ARG;
+  }
+  if (!aligned_to(grad_weight, 4) || !aligned_to(grad_bias, 4)) return RLK_ERR_INVALID_ARG;
+  if (T == 0 && !grad_weight && !grad_bias) return RLK_OK;
+  if (grad_weight || grad_bias) {
+    if (!workspace || workspace_bytes < rlk::norm_bwd_workspace_bytes(T, H) ||
+        !aligned_to(workspace, 16))
+      return RLK_ERR_WORKSPACE;
+  }
+  a.dy = dy;
+  a.dy_dtype = dtype_index(dy_dtype);
+  a.lddy = lddy;
+  a.x = x;
+  a.dtype = dtype_index(dtype);
+  a.ldx = ldx;
+  a.T = T;
+  a.H = H;
+  a.weight = weight;
+  a.param_dtype = dtype_index(param_dtype);
+  a.rms = kind == RLK_NORM_RMS;
+  a.mean = mean;
+  a.rstd = rstd;
+  a.dx = grad_x;
+  a.dx_dtype = dtype_index(grad_dtype);
+  a.lddx = ldg;
+  a.dw = grad_weight;
+  a.db = grad_bias;
+  a.accumulate = accumulate != 0;
+  a.workspace = static_cast<float*>(workspace);
+  if (rlk::take_injected_failure()) return RLK_ERR_CUDA;
+  return rlk::launch_norm_bwd(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? RLK_OK
+             : RLK_ERR_CUDA;
 }
 
 int rlk_debug_inject_launch_failures(int n) {

@@ -86,7 +86,7 @@ typedef enum {
 /* Operation ids for rlk_workspace_size. */
 enum { RLK_OP_LOGPROB_ENTROPY = 0, RLK_OP_GRPO_LOSS = 1, RLK_OP_LMHEAD = 2,
        RLK_OP_LMHEAD_BWD = 3, RLK_OP_LMHEAD_TOPP = 4, RLK_OP_CANONICAL = 5,
-       RLK_OP_CANONICAL_TOPP = 6 };
+       RLK_OP_CANONICAL_TOPP = 6, RLK_OP_NORM_BWD = 7 };
 
 /* Bits OR-ed into *out_status_word by the kernels. */
 #define RLK_STATUS_BAD_TOKEN_ID 0x1u   /* a token id outside [0, V)          */
@@ -149,6 +149,7 @@ const char* rlk_status_string(rlk_status status);
  *  RLK_OP_LMHEAD_TOPP:     the same (rlk_lmhead_logprob with top_p < 1)
  *  RLK_OP_CANONICAL:       T rows, V = the number of virtual shards, H unused
  *  RLK_OP_CANONICAL_TOPP:  the same (rlk_logprob_entropy_canonical_topp)
+ *  RLK_OP_NORM_BWD:        T rows, V = the row width H, H unused
  * Returns 0 for an unknown op or negative sizes. */
 size_t rlk_workspace_size(int op, int64_t T, int64_t V, int64_t H);
 
@@ -800,6 +801,125 @@ rlk_status rlk_logprob_entropy_canonical_topp(const void* logits, rlk_dtype dtyp
                                               float* out_entropy, int32_t* out_k,
                                               uint32_t* out_status_word, void* workspace,
                                               size_t workspace_bytes, rlk_stream stream);
+
+/* Activation checkpoints in 8 bits: what a forward keeps of an activation
+ * x[T, H] for its backward.  Each row is cut into blocks of
+ * RLK_CHECKPOINT_BLOCK columns (the last may be short); a block holds
+ *   k = the least whole number >= -126 with 127 2^k >= max |x|,
+ *   codes q_i = x_i 2^-k rounded to nearest even, |q_i| <= 127 (held to 63 at
+ *     k = 122, where 64 2^k would overflow fp32),
+ *   scale byte k + 127,
+ * and stands for the values q_i 2^k (every step but the rounding to q is
+ * exact, and q_i 2^k is exact in bf16), so |x_i - q_i 2^k| <= max|x| / 127
+ * (k = 122: <= max|x| / 64).
+ * A block with a NaN or an infinity has scale byte 255 and stands for NaN.
+ * 1.03 bytes an element. */
+#define RLK_CHECKPOINT_BLOCK 32
+typedef struct rlk_checkpoint {
+  int8_t* codes;       /* device [T][ld_codes], 16-byte aligned; columns [0, H)    */
+  uint8_t* scales;     /* device [T][ld_scales]; columns [0, ceil(H / 32))         */
+  int64_t ld_codes;    /* >= H, a multiple of 16                                   */
+  int64_t ld_scales;   /* >= ceil(H / 32)                                          */
+} rlk_checkpoint;
+
+/*
+ * rlk_checkpoint_pack -- the checkpoint of x.
+ *
+ * Arguments
+ *  x               device, dtype `dtype`, T x ldx elements (ldx >= H, unit
+ *                  stride along H; any alignment of its type).
+ *  T, H            rows, row width (1 <= H <= 2^20).
+ *  out             host pointer to the checkpoint's buffers (read before the
+ *                  call returns).  Columns of codes past H are not written.
+ *  out_status_word device uint32[1] or NULL: RLK_STATUS_NONFINITE when x holds a
+ *                  NaN or an infinity.
+ * Errors: RLK_ERR_INVALID_ARG for T < 0, H outside its range, ldx < H, a bad
+ *  dtype, null or misaligned pointers, strides outside the rules above.
+ *  T == 0 returns RLK_OK without launching.
+ */
+rlk_status rlk_checkpoint_pack(const void* x, rlk_dtype dtype, int64_t T, int64_t H, int64_t ldx,
+                               const rlk_checkpoint* out, uint32_t* out_status_word,
+                               rlk_stream stream);
+
+/*
+ * rlk_checkpoint_unpack -- the values a checkpoint stands for, exactly, in
+ * bf16 or fp32.
+ *
+ *  out             device, dtype `dtype`, T x ldo elements (ldo >= H).
+ * Errors: as rlk_checkpoint_pack.
+ */
+rlk_status rlk_checkpoint_unpack(const rlk_checkpoint* in, int64_t T, int64_t H, void* out,
+                                 rlk_dtype dtype, int64_t ldo, rlk_stream stream);
+
+typedef enum { RLK_NORM_LAYER = 0, RLK_NORM_RMS = 1 } rlk_norm_kind;
+
+/*
+ * rlk_norm_fwd -- layer or RMS norm of each row, with the 8-bit checkpoint of
+ * its input written on the way when one is asked for.
+ *
+ *   m_t = mean of x_t (RLK_NORM_RMS: 0),  r_t = (mean of (x_t - m_t)^2 + eps)^-1/2,
+ *   y = (x - m_t) r_t weight + bias,
+ * sums and statistics in fp32, the variance from the deviations (two passes
+ * over a row held on chip), y rounded once.
+ *
+ * Arguments
+ *  x               device, dtype `dtype`, T x ldx elements (ldx >= H).
+ *  T, H            rows, row width (1 <= H <= 2^20).
+ *  weight, bias    device [H] of param_dtype, or NULL (1 and 0).
+ *  eps             finite, >= 0.
+ *  y               device, y_dtype, T x ldy elements (ldy >= H); may not overlap x.
+ *  out_mean        device float[T] or NULL (RLK_NORM_RMS: not written).
+ *  out_rstd        device float[T] or NULL.
+ *  out_checkpoint  host pointer to the checkpoint's buffers, or NULL for none.
+ *  out_status_word device uint32[1] or NULL.  A row with a NaN or an infinity,
+ *                  or whose squares overflow fp32, gets NaN in y, mean and rstd
+ *                  and RLK_STATUS_NONFINITE.
+ * A row's results do not depend on the other rows; a layout in which some row
+ * does not start on a 16-byte boundary may sum a row in another order.
+ * Errors: RLK_ERR_INVALID_ARG for T < 0, H outside its range, a stride below
+ *  H, bad dtypes or kind, eps not finite and >= 0, null or misaligned pointers,
+ *  a checkpoint outside its rules.  T == 0 returns RLK_OK without launching.
+ */
+rlk_status rlk_norm_fwd(const void* x, rlk_dtype dtype, int64_t T, int64_t H, int64_t ldx,
+                        const void* weight, const void* bias, rlk_dtype param_dtype,
+                        rlk_norm_kind kind, float eps, void* y, rlk_dtype y_dtype, int64_t ldy,
+                        float* out_mean, float* out_rstd, const rlk_checkpoint* out_checkpoint,
+                        uint32_t* out_status_word, rlk_stream stream);
+
+/*
+ * rlk_norm_bwd -- gradients of rlk_norm_fwd.
+ *
+ * With h = (x - m_t) r_t (x from its 8-bit checkpoint when that is given) and
+ * g = dy weight:
+ *   grad_x = r_t (g - mean(g) - h mean(g h))      (RLK_NORM_RMS: without mean(g)),
+ *   grad_weight (+)= sum_t dy h,   grad_bias (+)= sum_t dy,
+ * in fp32, each output rounded once.  The parameter gradients are summed in an
+ * order that depends on T and H only: the same bits on every run.
+ *
+ * Arguments
+ *  dy              device, dy_dtype, T x lddy elements (rlk_lmhead_logprob_bwd's
+ *                  fp32 grad_hidden, or bf16).
+ *  x, dtype, ldx   the forward's input; or NULL with
+ *  checkpoint      the checkpoint of it (exactly one of the two).
+ *  weight, param_dtype, kind  the forward's.
+ *  mean, rstd      device float[T] from the forward (mean: RLK_NORM_LAYER only).
+ *  grad_x          device, grad_dtype, T x ldg elements (ldg >= H).
+ *  grad_weight     device float[H] or NULL.   grad_bias: device float[H] or NULL.
+ *  accumulate      non-zero: the two are added to, else overwritten (with 0 when
+ *                  T == 0).
+ *  workspace       at least rlk_workspace_size(RLK_OP_NORM_BWD, T, H, 0) bytes,
+ *                  16-byte aligned (may be NULL when grad_weight and grad_bias
+ *                  are); contents on entry do not matter.
+ * A row whose rstd is NaN (the forward could not normalise it) gives NaN in its
+ * grad_x row and in grad_weight.
+ * Errors: as rlk_norm_fwd; RLK_ERR_WORKSPACE for a missing or short workspace.
+ */
+rlk_status rlk_norm_bwd(const void* dy, rlk_dtype dy_dtype, int64_t lddy, const void* x,
+                        rlk_dtype dtype, int64_t ldx, const rlk_checkpoint* checkpoint, int64_t T,
+                        int64_t H, const void* weight, rlk_dtype param_dtype, rlk_norm_kind kind,
+                        const float* mean, const float* rstd, void* grad_x, rlk_dtype grad_dtype,
+                        int64_t ldg, float* grad_weight, float* grad_bias, int accumulate,
+                        void* workspace, size_t workspace_bytes, rlk_stream stream);
 
 #ifdef __cplusplus
 }  /* extern "C" */

@@ -1,0 +1,114 @@
+"""Refusals of the layer operators on the host, before any CUDA call, and the
+binding's own argument checks."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+import entropy_logits_bf16_gb300 as rlk
+
+FAKE = ctypes.c_void_p(0x10000)   # never dereferenced: validation fails first
+ODD = ctypes.c_void_p(0x10001)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    rlk.build()
+    return rlk.load()
+
+
+@pytest.fixture
+def armed(lib):
+    """A launch would return the injected CUDA error (4): refusals come first."""
+    lib.rlk_debug_inject_launch_failures(1000)
+    yield
+    lib.rlk_debug_inject_launch_failures(0)
+
+
+def ckpt(codes=0x10000, scales=0x10000, ldc=112, lds=4):
+    return ctypes.byref(rlk.CheckpointBuffers(codes, scales, ldc, lds))
+
+
+def pack(lib, **kw):
+    a = dict(x=FAKE, dtype=0, T=4, H=100, ldx=100, ck=ckpt())
+    a.update(kw)
+    return lib.rlk_checkpoint_pack(a["x"], a["dtype"], a["T"], a["H"], a["ldx"], a["ck"], None, None)
+
+
+def unpack(lib, **kw):
+    a = dict(x=FAKE, dtype=0, T=4, H=100, ldx=100, ck=ckpt())
+    a.update(kw)
+    return lib.rlk_checkpoint_unpack(a["ck"], a["T"], a["H"], a["x"], a["dtype"], a["ldx"], None)
+
+
+CKPT_BAD = [dict(T=-1), dict(H=0), dict(H=(1 << 20) + 1, ldx=1 << 21), dict(ldx=99), dict(dtype=2), dict(x=None),
+            dict(x=ODD), dict(ck=None), dict(ck=ckpt(codes=None)), dict(ck=ckpt(scales=None)),
+            dict(ck=ckpt(codes=0x10008)), dict(ck=ckpt(ldc=96)), dict(ck=ckpt(ldc=104)), dict(ck=ckpt(lds=3))]
+
+
+@pytest.mark.parametrize("kw", CKPT_BAD)
+def test_checkpoint_rejects(lib, armed, kw):
+    assert pack(lib, **kw) == 1 and unpack(lib, **kw) == 1
+
+
+def test_checkpoint_accepts(lib, armed):
+    assert pack(lib) == 4 and unpack(lib) == 4
+    assert pack(lib, T=0, x=None, ck=None) == 0 and unpack(lib, T=0, x=None, ck=None) == 0
+
+
+def norm_fwd(lib, **kw):
+    a = dict(x=FAKE, dtype=0, T=4, H=100, ldx=100, w=FAKE, b=FAKE, pd=1, kind=0, eps=1e-5, y=FAKE, yd=0, ldy=100,
+             mean=FAKE, rstd=FAKE, ck=None)
+    a.update(kw)
+    return lib.rlk_norm_fwd(a["x"], a["dtype"], a["T"], a["H"], a["ldx"], a["w"], a["b"], a["pd"], a["kind"], a["eps"],
+                            a["y"], a["yd"], a["ldy"], a["mean"], a["rstd"], a["ck"], None, None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(T=-1), dict(H=0), dict(H=(1 << 20) + 1, ldx=1 << 21, ldy=1 << 21), dict(ldx=99), dict(ldy=99), dict(dtype=2),
+    dict(pd=3), dict(yd=-1), dict(kind=2), dict(eps=-1e-5), dict(eps=math.nan), dict(eps=math.inf), dict(x=None),
+    dict(y=None), dict(x=ODD), dict(y=ODD), dict(w=ctypes.c_void_p(0x10002)), dict(b=ODD), dict(ck=ckpt(ldc=96))])
+def test_norm_fwd_rejects(lib, armed, kw):
+    assert norm_fwd(lib, **kw) == 1
+
+
+def test_norm_fwd_accepts(lib, armed):
+    assert norm_fwd(lib) == 4
+    assert norm_fwd(lib, w=None, b=None, mean=None, rstd=None, ck=ckpt()) == 4
+    assert norm_fwd(lib, T=0, x=None, y=None) == 0
+
+
+def norm_bwd(lib, **kw):
+    a = dict(dy=FAKE, dd=1, lddy=100, x=FAKE, dtype=0, ldx=100, ck=None, T=4, H=100, w=FAKE, pd=1, kind=0, mean=FAKE,
+             rstd=FAKE, dx=FAKE, gd=0, ldg=100, dw=FAKE, db=FAKE, acc=0, ws=FAKE, wsb=1 << 20)
+    a.update(kw)
+    return lib.rlk_norm_bwd(a["dy"], a["dd"], a["lddy"], a["x"], a["dtype"], a["ldx"], a["ck"], a["T"], a["H"], a["w"],
+                            a["pd"], a["kind"], a["mean"], a["rstd"], a["dx"], a["gd"], a["ldg"], a["dw"], a["db"],
+                            a["acc"], a["ws"], a["wsb"], None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(T=-1), dict(H=0), dict(lddy=99), dict(ldx=99), dict(ldg=99), dict(dd=2), dict(dtype=2), dict(gd=2), dict(pd=2),
+    dict(kind=5), dict(dy=None), dict(dx=None), dict(rstd=None), dict(mean=None), dict(x=None), dict(ck=ckpt()),
+    dict(x=None, ck=ckpt(ldc=96)), dict(dy=ctypes.c_void_p(0x10002)), dict(dx=ODD), dict(x=ODD), dict(dw=ODD)])
+def test_norm_bwd_rejects(lib, armed, kw):
+    assert norm_bwd(lib, **kw) == 1
+
+
+def test_norm_bwd_workspace_and_accepts(lib, armed):
+    need = lib.rlk_workspace_size(rlk.OP_NORM_BWD, 4, 100, 0)
+    assert need >= 4 * 2 * 100 * 4 and need % 256 == 0
+    assert norm_bwd(lib, ws=None) == 3 and norm_bwd(lib, wsb=need - 1) == 3 and norm_bwd(lib, ws=ctypes.c_void_p(0x10008)) == 3
+    assert norm_bwd(lib, wsb=need) == 4
+    assert norm_bwd(lib, kind=1, mean=None, x=None, ldx=0, ck=ckpt(), w=None) == 4
+    assert norm_bwd(lib, dw=None, db=None, ws=None, wsb=0) == 4
+    assert norm_bwd(lib, T=0, dw=None, db=None, ws=None, wsb=0) == 0
+
+
+def test_binding_refuses_cpu_tensors_and_shapes():
+    x = torch.zeros(4, 64)
+    for call in (lambda: rlk.norm(x), lambda: rlk.checkpoint_pack(x), lambda: rlk.norm_backward(x, x, None, None, None),
+                 lambda: rlk.new_checkpoint(4, 64, "cpu")):
+        with pytest.raises(ValueError):
+            call()
