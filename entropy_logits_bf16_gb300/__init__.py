@@ -26,6 +26,10 @@ OP_LOGPROB_ENTROPY, OP_GRPO_LOSS, OP_LMHEAD, OP_LMHEAD_BWD, OP_LMHEAD_TOPP = 0, 
 OP_CANONICAL = 5
 OP_CANONICAL_TOPP = 6
 OP_NORM_BWD = 7
+OP_PREFERENCE_LOSS = 8
+PREF_SIGMOID, PREF_IPO, PREF_HINGE = 0, 1, 2
+PREF_NSTATS = 6
+PREF_STAT_NAMES = ("loss", "pairs", "accuracy", "margin", "chosen", "rejected")
 NORM_LAYER, NORM_RMS = 0, 1
 CHECKPOINT_BLOCK = 32   # columns that share one checkpoint scale
 SHARD_COUNTS_BYTES = 8224   # rlk_shard_counts: one row's window counts of one shard
@@ -47,6 +51,13 @@ class LossConfig(ctypes.Structure):
                 ("baseline", ctypes.c_int), ("agg", ctypes.c_int)]
 
 
+class PrefConfig(ctypes.Structure):
+    """rlk_pref_config."""
+    _fields_ = [("type", ctypes.c_int), ("beta", ctypes.c_float),
+                ("label_smoothing", ctypes.c_float), ("margin", ctypes.c_float),
+                ("length_normalise", ctypes.c_int)]
+
+
 class CheckpointBuffers(ctypes.Structure):
     """rlk_checkpoint."""
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
@@ -65,7 +76,7 @@ EXPORTS = ("rlk_version", "rlk_status_string", "rlk_workspace_size", "rlk_logpro
            "rlk_shard_window_counts", "rlk_shard_combine_topp",
            "rlk_logprob_entropy_canonical_topp",
            "rlk_grpo_loss_noalloc", "rlk_checkpoint_pack", "rlk_checkpoint_unpack",
-           "rlk_norm_fwd", "rlk_norm_bwd")
+           "rlk_norm_fwd", "rlk_norm_bwd", "rlk_preference_loss")
 NOALLOC_MAX_SEQ = 16384
 DEBUG_EXPORTS = ("rlk_lmhead_logits_debug", "rlk_debug_inject_launch_failures",
                  "rlk_debug_set_wait_limit", "rlk_debug_withhold_copy",
@@ -191,6 +202,9 @@ def load(path: str | None = None):
                                      ctypes.c_int, ctypes.c_int, vp, vp, vp, ctypes.c_int, i64, vp,
                                      vp, ctypes.c_int, vp, sz, vp]
         lib.rlk_norm_bwd.restype = ctypes.c_int
+        lib.rlk_preference_loss.argtypes = [vp, vp, vp, vp, i32, i64, ctypes.POINTER(PrefConfig), vp,
+                                            vp, vp, vp, vp, sz, vp]
+        lib.rlk_preference_loss.restype = ctypes.c_int
         _lib = lib
         return lib
 
@@ -1036,6 +1050,43 @@ def norm_autograd(x: torch.Tensor, weight=None, bias=None, *, kind: int = NORM_L
     """``norm`` as a differentiable op; ``keep_8bit`` keeps x for the backward as
     its 8-bit checkpoint instead of the tensor."""
     return _Norm.apply(x, weight, bias, kind, eps, keep_8bit)
+
+
+# ------------------------------------------------------------ preference loss
+def preference_loss(logp, logp_ref, seq_offsets, *, loss_mask=None, loss_type: int = PREF_SIGMOID,
+                    beta: float = 0.1, label_smoothing: float = 0.0, margin: float = 0.0,
+                    length_normalise: bool = False, want_grad: bool = True,
+                    want_reward: bool = True, want_stats: bool = True, workspace=None):
+    """Paired preference loss over packed per-token log-probabilities (CUDA
+    fp32); sequences 2 i and 2 i + 1 are pair i's chosen and rejected response.
+    ``logp_ref`` None: reference-free.  Returns (loss[1], dL/dlogp or None,
+    rewards [2 pairs] or None, stats[PREF_NSTATS] or None)."""
+    lib = load()
+    _need_cuda(logp, logp_ref, seq_offsets, loss_mask)
+    for t in (logp, logp_ref):
+        if t is not None and (t.dtype != torch.float32 or t.dim() != 1 or not t.is_contiguous()
+                              or t.numel() != logp.numel()):
+            raise ValueError("log-probs must be contiguous fp32 [n_tok]")
+    if seq_offsets.dtype != torch.int32 or not seq_offsets.is_contiguous() or seq_offsets.numel() % 2 != 1:
+        raise ValueError("seq_offsets must be contiguous int32 [2 pairs + 1]")
+    if loss_mask is not None and (loss_mask.dtype != torch.uint8 or not loss_mask.is_contiguous()
+                                  or loss_mask.numel() != logp.numel()):
+        raise ValueError("loss_mask must be contiguous uint8 [n_tok]")
+    P, n_tok, dev = seq_offsets.numel() // 2, logp.numel(), logp.device
+    if workspace is None:
+        workspace = torch.empty(int(lib.rlk_workspace_size(OP_PREFERENCE_LOSS, n_tok, P, 0)),
+                                device=dev, dtype=torch.uint8)
+    cfg = PrefConfig(int(loss_type), float(beta), float(label_smoothing), float(margin),
+                     int(bool(length_normalise)))
+    loss = torch.empty(1, device=dev, dtype=torch.float32)
+    grad = torch.empty(n_tok, device=dev, dtype=torch.float32) if want_grad else None
+    reward = torch.empty(2 * P, device=dev, dtype=torch.float32) if want_reward else None
+    stats = torch.empty(PREF_NSTATS, device=dev, dtype=torch.float32) if want_stats else None
+    _check("rlk_preference_loss",
+           lib.rlk_preference_loss(_ptr(logp), _ptr(logp_ref), _ptr(loss_mask), _ptr(seq_offsets), P,
+                                   n_tok, ctypes.byref(cfg), _ptr(loss), _ptr(grad), _ptr(reward),
+                                   _ptr(stats), _ptr(workspace), workspace.numel(), _stream(dev)))
+    return loss, grad, reward, stats
 
 
 def inject_launch_failures(n: int) -> int:

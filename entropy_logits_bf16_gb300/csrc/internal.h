@@ -240,6 +240,29 @@ size_t norm_bwd_workspace_bytes(int64_t T, int64_t H);
 cudaError_t launch_norm_fwd(const NormArgs& a, cudaStream_t stream);
 cudaError_t launch_norm_bwd(const NormBwdArgs& a, cudaStream_t stream);
 
+// Paired preference loss (preference_loss.cu).
+struct PrefArgs {
+  const float* logp;
+  const float* logp_ref;   // or NULL
+  const uint8_t* mask;     // or NULL
+  const int32_t* seq_offsets;
+  int32_t n_pairs;
+  int64_t n_tok;
+  int type;                // rlk_pref_type
+  float beta, smoothing, margin;
+  int mean;
+  float* out_loss;
+  float* out_grad;
+  float* out_reward;
+  float* out_stats;
+  // set by the launcher
+  uint32_t* flag;          // 1: invalid offsets
+  float4* slots;           // segment sums (hi, lo, token count)
+  int split;               // CTAs per sequence
+};
+size_t pref_workspace_bytes(int64_t n_tok, int64_t n_pairs);
+cudaError_t launch_preference_loss(PrefArgs a, void* workspace, cudaStream_t stream);
+
 cudaError_t launch_sample(const SampleArgs& a, cudaStream_t stream);
 cudaError_t launch_shard_partials(const ShardArgs& a, cudaStream_t stream);
 cudaError_t launch_shard_combine(const ShardCombineArgs& a, cudaStream_t stream);

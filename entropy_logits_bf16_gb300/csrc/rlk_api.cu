@@ -142,6 +142,7 @@ size_t rlk_workspace_size(int op, int64_t T, int64_t V, int64_t H) {
     case RLK_OP_LMHEAD_BWD: return rlk::lmhead_bwd_workspace_bytes(T, V, H);
     case RLK_OP_LMHEAD_TOPP: return rlk::lmhead_topp_workspace_bytes(T, V, H);
     case RLK_OP_NORM_BWD: return rlk::norm_bwd_workspace_bytes(T, V);
+    case RLK_OP_PREFERENCE_LOSS: return rlk::pref_workspace_bytes(T, V);
     case RLK_OP_CANONICAL:
       return V < 1 ? 0 : (size_t)V * (size_t)T * sizeof(rlk_shard_partial);
     case RLK_OP_CANONICAL_TOPP:
@@ -974,6 +975,54 @@ rlk_status rlk_norm_bwd(const void* dy, rlk_dtype dy_dtype, int64_t lddy, const 
   a.workspace = static_cast<float*>(workspace);
   if (rlk::take_injected_failure()) return RLK_ERR_CUDA;
   return rlk::launch_norm_bwd(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? RLK_OK
+             : RLK_ERR_CUDA;
+}
+
+// The layout the Python binding mirrors (5 four-byte fields).
+static_assert(sizeof(rlk_pref_config) == 20 && offsetof(rlk_pref_config, length_normalise) == 16,
+              "rlk_pref_config layout");
+
+rlk_status rlk_preference_loss(const float* logp, const float* logp_ref, const uint8_t* loss_mask,
+                               const int32_t* seq_offsets, int32_t n_pairs, int64_t n_tok,
+                               const rlk_pref_config* config, float* out_loss, float* out_grad,
+                               float* out_reward, float* out_stats, void* workspace,
+                               size_t workspace_bytes, rlk_stream stream) {
+  if (!config) return RLK_ERR_INVALID_ARG;
+  const rlk_pref_config c = *config;
+  if (c.type != RLK_PREF_SIGMOID && c.type != RLK_PREF_IPO && c.type != RLK_PREF_HINGE)
+    return RLK_ERR_INVALID_ARG;
+  if (!finite_positive(c.beta) || !std::isfinite(c.margin)) return RLK_ERR_INVALID_ARG;
+  if (!(c.label_smoothing >= 0.0f && c.label_smoothing < 0.5f)) return RLK_ERR_INVALID_ARG;
+  if (c.type != RLK_PREF_SIGMOID && c.label_smoothing != 0.0f) return RLK_ERR_INVALID_ARG;
+  if (n_pairs < 0 || n_pairs > (1 << 24) || n_tok < 0 || n_tok > INT32_MAX)
+    return RLK_ERR_INVALID_ARG;
+  if (!seq_offsets || !out_loss || (n_tok > 0 && !logp)) return RLK_ERR_INVALID_ARG;
+  if (!aligned_to(logp, 4) || !aligned_to(logp_ref, 4) || !aligned_to(seq_offsets, 4) ||
+      !aligned_to(out_grad, 4) || !aligned_to(out_reward, 4))
+    return RLK_ERR_INVALID_ARG;
+  if (!workspace || workspace_bytes < rlk::pref_workspace_bytes(n_tok, n_pairs) ||
+      !aligned_to(workspace, 16))
+    return RLK_ERR_WORKSPACE;
+  rlk::PrefArgs a{};
+  a.logp = logp;
+  a.logp_ref = logp_ref;
+  a.mask = loss_mask;
+  a.seq_offsets = seq_offsets;
+  a.n_pairs = n_pairs;
+  a.n_tok = n_tok;
+  a.type = (int)c.type;
+  a.beta = c.beta;
+  a.smoothing = c.label_smoothing;
+  a.margin = c.margin;
+  a.mean = c.length_normalise != 0;
+  a.out_loss = out_loss;
+  a.out_grad = out_grad;
+  a.out_reward = out_reward;
+  a.out_stats = out_stats;
+  if (rlk::take_injected_failure()) return RLK_ERR_CUDA;
+  return rlk::launch_preference_loss(a, workspace, reinterpret_cast<cudaStream_t>(stream)) ==
+                 cudaSuccess
              ? RLK_OK
              : RLK_ERR_CUDA;
 }

@@ -86,7 +86,7 @@ typedef enum {
 /* Operation ids for rlk_workspace_size. */
 enum { RLK_OP_LOGPROB_ENTROPY = 0, RLK_OP_GRPO_LOSS = 1, RLK_OP_LMHEAD = 2,
        RLK_OP_LMHEAD_BWD = 3, RLK_OP_LMHEAD_TOPP = 4, RLK_OP_CANONICAL = 5,
-       RLK_OP_CANONICAL_TOPP = 6, RLK_OP_NORM_BWD = 7 };
+       RLK_OP_CANONICAL_TOPP = 6, RLK_OP_NORM_BWD = 7, RLK_OP_PREFERENCE_LOSS = 8 };
 
 /* Bits OR-ed into *out_status_word by the kernels. */
 #define RLK_STATUS_BAD_TOKEN_ID 0x1u   /* a token id outside [0, V)          */
@@ -150,6 +150,7 @@ const char* rlk_status_string(rlk_status status);
  *  RLK_OP_CANONICAL:       T rows, V = the number of virtual shards, H unused
  *  RLK_OP_CANONICAL_TOPP:  the same (rlk_logprob_entropy_canonical_topp)
  *  RLK_OP_NORM_BWD:        T rows, V = the row width H, H unused
+ *  RLK_OP_PREFERENCE_LOSS: T packed tokens, V = n_pairs, H unused
  * Returns 0 for an unknown op or negative sizes. */
 size_t rlk_workspace_size(int op, int64_t T, int64_t V, int64_t H);
 
@@ -920,6 +921,73 @@ rlk_status rlk_norm_bwd(const void* dy, rlk_dtype dy_dtype, int64_t lddy, const 
                         const float* mean, const float* rstd, void* grad_x, rlk_dtype grad_dtype,
                         int64_t ldg, float* grad_weight, float* grad_bias, int accumulate,
                         void* workspace, size_t workspace_bytes, rlk_stream stream);
+
+typedef enum {
+  RLK_PREF_SIGMOID = 0,   /* -(1 - s) ln sigma(h) - s ln sigma(-h), s the label smoothing */
+  RLK_PREF_IPO = 1,       /* (h / beta - 1 / (2 beta))^2                                  */
+  RLK_PREF_HINGE = 2      /* max(0, 1 - h), slope 0 at h = 1                              */
+} rlk_pref_type;
+
+typedef struct rlk_pref_config {
+  rlk_pref_type type;
+  float beta;               /* finite, > 0                                          */
+  float label_smoothing;    /* [0, 0.5); RLK_PREF_SIGMOID only                      */
+  float margin;             /* finite; subtracted from the rewards' difference      */
+  int length_normalise;     /* non-zero: D_s is the mean over its tokens            */
+} rlk_pref_config;
+
+enum {
+  RLK_PREF_STAT_LOSS = 0,          /* the loss value                                */
+  RLK_PREF_STAT_PAIRS = 1,         /* pairs that count                              */
+  RLK_PREF_STAT_ACCURACY = 2,      /* fraction of those with r_chosen > r_rejected  */
+  RLK_PREF_STAT_MARGIN = 3,        /* their mean r_chosen - r_rejected              */
+  RLK_PREF_STAT_CHOSEN = 4,        /* their mean r_chosen                           */
+  RLK_PREF_STAT_REJECTED = 5,      /* their mean r_rejected                         */
+  RLK_PREF_NSTATS = 6
+};
+
+/*
+ * rlk_preference_loss -- paired preference loss over packed log-probabilities,
+ * with its gradient.
+ *
+ * Sequences are packed as in rlk_grpo_loss; pair i is sequence 2 i (chosen) and
+ * 2 i + 1 (rejected), the responses to one prompt.  With mask m_t:
+ *   D_s = sum_t m_t (logp[t] - logp_ref[t])      (logp_ref NULL: 0)
+ *         / sum_t m_t when length_normalise,
+ *   r_s = beta D_s,   h_i = r_2i - r_2i+1 - margin,
+ *   L = (1 / n_pairs) sum_i l(h_i),   l by config->type,
+ *   dL/dlogp[t] = +-l'(h_i) beta m_t / n_pairs   (/ sum m when normalised;
+ *         + on the chosen side, - on the rejected one).
+ * A pair one of whose sequences has no unmasked token does not count: it adds
+ * nothing to L and its gradient is 0.  A masked token is never looked at (it may
+ * hold an infinity or a NaN).  An unmasked -inf (a token outside a retained set)
+ * goes through the formula.
+ *
+ * Arguments
+ *  logp, logp_ref  device float[n_tok]; logp_ref or NULL.
+ *  loss_mask       device uint8[n_tok] (0 / not 0) or NULL for all ones.
+ *  seq_offsets     device int32[2 n_pairs + 1], non-decreasing and within
+ *                  [0, n_tok] (checked on the device: otherwise the loss, the
+ *                  statistics, the rewards and the gradient come out NaN, and
+ *                  nothing outside the n_tok tokens is touched).
+ *  config          host pointer, read before the call returns.
+ *  out_loss        device float[1].
+ *  out_grad        device float[n_tok] or NULL (0 for a token of no sequence).
+ *  out_reward      device float[2 n_pairs] or NULL: r_s.
+ *  out_stats       device float[RLK_PREF_NSTATS] or NULL.
+ *  workspace       at least rlk_workspace_size(RLK_OP_PREFERENCE_LOSS, n_tok,
+ *                  n_pairs, 0) bytes, 16-byte aligned; contents on entry do not
+ *                  matter.
+ * A sequence's sum has a fixed order that depends on its length only.
+ * Errors: RLK_ERR_INVALID_ARG for negative sizes, n_pairs > 2^24, a NULL config,
+ *  parameters outside their ranges, null required pointers; RLK_ERR_WORKSPACE.
+ *  n_pairs == 0 gives loss 0.
+ */
+rlk_status rlk_preference_loss(const float* logp, const float* logp_ref, const uint8_t* loss_mask,
+                               const int32_t* seq_offsets, int32_t n_pairs, int64_t n_tok,
+                               const rlk_pref_config* config, float* out_loss, float* out_grad,
+                               float* out_reward, float* out_stats, void* workspace,
+                               size_t workspace_bytes, rlk_stream stream);
 
 #ifdef __cplusplus
 }  /* extern "C" */

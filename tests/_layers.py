@@ -70,3 +70,44 @@ def rows(T, H, dtype, seed, device="cuda", odd_layout=False):
 def randn(shape, seed, dtype=torch.float32, scale=1.0, device="cuda"):
     g = torch.Generator().manual_seed(seed)
     return (torch.randn(*shape, generator=g) * scale).to(dtype).to(device)
+
+
+def preference64(lp, ref, mask, off, kind, beta, smoothing, margin, mean):
+    """(loss, grad, reward, stats) of the preference loss, pair by pair in 64
+    bits; kind 0 sigmoid, 1 IPO, 2 hinge."""
+    import math
+    lp = lp.double().cpu()
+    ref = None if ref is None else ref.double().cpu()
+    P = (len(off) - 1) // 2
+    grad, reward = torch.zeros_like(lp), torch.zeros(2 * P, dtype=torch.float64)
+    on = [torch.arange(off[s], off[s + 1]) for s in range(2 * P)]
+    if mask is not None:
+        on = [i[mask.cpu()[i] != 0] for i in on]
+    for s, i in enumerate(on):
+        d = (lp[i] if ref is None else lp[i] - ref[i]).sum().item() if len(i) else 0.0
+        reward[s] = beta * (d / len(i) if mean and len(i) else d)
+    total, live = 0.0, []
+    for p in range(P):
+        if not len(on[2 * p]) or not len(on[2 * p + 1]):
+            continue
+        live.append(p)
+        h = (reward[2 * p] - reward[2 * p + 1]).item() - margin
+        if kind == 0:
+            sp = lambda v: max(v, 0.0) + math.log1p(math.exp(-abs(v)))
+            sg = lambda v: 1 / (1 + math.exp(-v)) if v > -700 else 0.0
+            total += (1 - smoothing) * sp(-h) + (smoothing * sp(h) if smoothing else 0.0)
+            slope = -(1 - smoothing) * sg(-h) + smoothing * sg(h)
+        elif kind == 1:
+            total += (h / beta - 0.5 / beta) ** 2
+            slope = 2 * (h / beta - 0.5 / beta) / beta
+        else:
+            total += max(0.0, 1 - h)
+            slope = -1.0 if h < 1 else 0.0
+        for s, sign in ((2 * p, 1.0), (2 * p + 1, -1.0)):
+            grad[on[s]] = sign * slope * beta / P / (len(on[s]) if mean else 1)
+    rc, rr = reward[0::2][live], reward[1::2][live]
+    n = max(1, len(live))
+    loss = total / P if P else 0.0
+    stats = torch.tensor([loss, len(live), (rc > rr).sum().item() / n, (rc - rr).sum().item() / n,
+                          rc.sum().item() / n, rr.sum().item() / n], dtype=torch.float64)
+    return loss, grad, reward, stats

@@ -112,3 +112,31 @@ def test_binding_refuses_cpu_tensors_and_shapes():
                  lambda: rlk.new_checkpoint(4, 64, "cpu")):
         with pytest.raises(ValueError):
             call()
+
+
+def pref(lib, n_pairs=2, n_tok=50, cfg=(0, 0.1, 0.0, 0.0, 0), lp=FAKE, ref=FAKE, off=FAKE, loss=FAKE, grad=FAKE,
+         reward=FAKE, ws=FAKE, wsb=1 << 20):
+    c = None if cfg is None else ctypes.byref(rlk.PrefConfig(*cfg))
+    return lib.rlk_preference_loss(lp, ref, None, off, n_pairs, n_tok, c, loss, grad, reward, None, ws, wsb, None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(cfg=None), dict(cfg=(3, 0.1, 0, 0, 0)), dict(cfg=(0, 0.0, 0, 0, 0)), dict(cfg=(0, math.nan, 0, 0, 0)),
+    dict(cfg=(0, 0.1, 0.5, 0, 0)), dict(cfg=(0, 0.1, -0.1, 0, 0)), dict(cfg=(1, 0.1, 0.1, 0, 0)),
+    dict(cfg=(0, 0.1, 0, math.inf, 0)), dict(n_pairs=-1), dict(n_pairs=(1 << 24) + 1), dict(n_tok=-1), dict(n_tok=1 << 31),
+    dict(lp=None), dict(off=None), dict(loss=None), dict(lp=ODD), dict(ref=ODD), dict(grad=ODD), dict(off=ODD)])
+def test_preference_rejects(lib, armed, kw):
+    assert pref(lib, **kw) == 1
+
+
+def test_preference_workspace_and_accepts(lib, armed):
+    need = lib.rlk_workspace_size(rlk.OP_PREFERENCE_LOSS, 50, 2, 0)
+    assert need % 256 == 0 and need > 0
+    assert pref(lib, ws=None) == 3 and pref(lib, wsb=need - 1) == 3 and pref(lib, ws=ctypes.c_void_p(0x10008)) == 3
+    assert pref(lib, wsb=need) == 4 and pref(lib, ref=None, grad=None, reward=None) == 4 and pref(lib, n_tok=0, lp=None) == 4
+
+
+def test_preference_binding_refuses():
+    x = torch.zeros(4)
+    with pytest.raises(ValueError):
+        rlk.preference_loss(x, None, torch.zeros(3, dtype=torch.int32))
