@@ -27,6 +27,8 @@ OP_CANONICAL = 5
 OP_CANONICAL_TOPP = 6
 OP_NORM_BWD = 7
 OP_PREFERENCE_LOSS = 8
+OP_LINEAR, OP_LINEAR_BWD = 9, 10
+ACT_NONE, ACT_GELU, ACT_SILU, ACT_RELU = 0, 1, 2, 3
 PREF_SIGMOID, PREF_IPO, PREF_HINGE = 0, 1, 2
 PREF_NSTATS = 6
 PREF_STAT_NAMES = ("loss", "pairs", "accuracy", "margin", "chosen", "rejected")
@@ -76,7 +78,8 @@ EXPORTS = ("rlk_version", "rlk_status_string", "rlk_workspace_size", "rlk_logpro
            "rlk_shard_window_counts", "rlk_shard_combine_topp",
            "rlk_logprob_entropy_canonical_topp",
            "rlk_grpo_loss_noalloc", "rlk_checkpoint_pack", "rlk_checkpoint_unpack",
-           "rlk_norm_fwd", "rlk_norm_bwd", "rlk_preference_loss")
+           "rlk_norm_fwd", "rlk_norm_bwd", "rlk_preference_loss", "rlk_linear_fwd",
+           "rlk_linear_bwd")
 NOALLOC_MAX_SEQ = 16384
 DEBUG_EXPORTS = ("rlk_lmhead_logits_debug", "rlk_debug_inject_launch_failures",
                  "rlk_debug_set_wait_limit", "rlk_debug_withhold_copy",
@@ -205,6 +208,13 @@ def load(path: str | None = None):
         lib.rlk_preference_loss.argtypes = [vp, vp, vp, vp, i32, i64, ctypes.POINTER(PrefConfig), vp,
                                             vp, vp, vp, vp, sz, vp]
         lib.rlk_preference_loss.restype = ctypes.c_int
+        lib.rlk_linear_fwd.argtypes = [vp, i64, vp, i64, vp, ctypes.c_int, vp, i64, i64, i64, i64,
+                                       ctypes.c_int, vp, ctypes.c_int, i64, vp, i64, vp, sz, vp]
+        lib.rlk_linear_fwd.restype = ctypes.c_int
+        lib.rlk_linear_bwd.argtypes = [vp, i64, vp, i64, ck, vp, i64, vp, i64, i64, i64, i64,
+                                       ctypes.c_int, vp, ctypes.c_int, i64, vp, ctypes.c_int, i64, vp,
+                                       ctypes.c_int, vp, sz, vp]
+        lib.rlk_linear_bwd.restype = ctypes.c_int
         _lib = lib
         return lib
 
@@ -1050,6 +1060,129 @@ def norm_autograd(x: torch.Tensor, weight=None, bias=None, *, kind: int = NORM_L
     """``norm`` as a differentiable op; ``keep_8bit`` keeps x for the backward as
     its 8-bit checkpoint instead of the tensor."""
     return _Norm.apply(x, weight, bias, kind, eps, keep_8bit)
+
+
+# ------------------------------------------------------------ linear
+def _bf16(t, name, shape=None):
+    """Row stride of a 2-D bf16 tensor (of ``shape``) with unit stride along its rows."""
+    dt, ld = _matrix(t, name)
+    if dt != 0:
+        raise ValueError(f"{name} must be bf16")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}")
+    return ld
+
+
+def linear(x: torch.Tensor, weight: torch.Tensor, bias=None, residual=None, *,
+           activation: int = ACT_NONE, return_preact: bool = False, out=None, out_dtype=None,
+           workspace=None):
+    """act(x weight^T + bias) + residual: x [M, K], weight [N, K], residual
+    [M, N] CUDA bf16 (rows may be strided), bias [N] bf16 or fp32.  Returns y
+    (bf16, or ``out_dtype`` fp32; ``out`` may be the residual itself), or
+    (y, z) with the bf16 pre-activation for ``linear_backward``."""
+    lib = load()
+    _need_cuda(x, weight, bias, residual, out, workspace)
+    ldx, ldw = _bf16(x, "x"), _bf16(weight, "weight")
+    M, K = x.shape
+    N = weight.shape[0]
+    if weight.shape[1] != K:
+        raise ValueError("x and weight disagree on K")
+    bdt = _params(N, bias)
+    ldr = 0 if residual is None else _bf16(residual, "residual", (M, N))
+    if out is None:
+        out = torch.empty((M, N), device=x.device, dtype=out_dtype or torch.bfloat16)
+    ydt, ldy = _matrix(out, "out")
+    if tuple(out.shape) != (M, N):
+        raise ValueError("out must be [M, N]")
+    z = torch.empty((M, N), device=x.device, dtype=torch.bfloat16) if return_preact else None
+    if workspace is None and (x.data_ptr() % 16 or ldx % 8 or weight.data_ptr() % 16 or ldw % 8):
+        workspace = torch.empty(int(lib.rlk_workspace_size(OP_LINEAR, M, N, K)), device=x.device,
+                                dtype=torch.uint8)
+    _check("rlk_linear_fwd",
+           lib.rlk_linear_fwd(_ptr(x), ldx, _ptr(weight), ldw, _ptr(bias), bdt, _ptr(residual), ldr,
+                              M, N, K, int(activation), _ptr(out), ydt, ldy, _ptr(z), N,
+                              _ptr(workspace), 0 if workspace is None else workspace.numel(),
+                              _stream(x.device)))
+    return (out, z) if return_preact else out
+
+
+def linear_backward(dy: torch.Tensor, x, weight: torch.Tensor, preact=None, *,
+                    activation: int = ACT_NONE, grad_dtype=torch.bfloat16,
+                    weight_grad_dtype=torch.float32, want_x_grad: bool = True,
+                    want_weight_grad: bool = True, want_bias_grad: bool = True, grad_weight=None,
+                    grad_bias=None, accumulate: bool = False, workspace=None):
+    """Gradients of ``linear``: (dL/dx [M, K], dL/dweight [N, K], dL/dbias fp32
+    [N]), None where not wanted; the residual's gradient is dy.  ``x`` is the
+    forward's input or its ``Checkpoint``.  ``accumulate`` adds into
+    ``grad_weight`` (fp32) and ``grad_bias``."""
+    lib = load()
+    kept = x if isinstance(x, Checkpoint) else None
+    _need_cuda(dy, None if kept else x, weight, preact, grad_weight, grad_bias, workspace)
+    lddy, ldw = _bf16(dy, "dy"), _bf16(weight, "weight")
+    M, N = dy.shape
+    K = weight.shape[1]
+    if weight.shape[0] != N or (x is not None and tuple(x.shape) != (M, K)):
+        raise ValueError("dy, x and weight disagree on M, N or K")
+    ldx = 0 if x is None or kept else _bf16(x, "x")
+    ldz = 0 if preact is None else _bf16(preact, "preact", (M, N))
+    if accumulate and ((want_weight_grad and grad_weight is None) or (want_bias_grad and grad_bias is None)):
+        raise ValueError("accumulate needs grad_weight and grad_bias")
+    dev = dy.device
+    dx = torch.empty((M, K), device=dev, dtype=grad_dtype) if want_x_grad else None
+    if grad_weight is None and want_weight_grad:
+        grad_weight = torch.empty((N, K), device=dev, dtype=weight_grad_dtype)
+    if grad_bias is None and want_bias_grad:
+        grad_bias = torch.empty(N, device=dev, dtype=torch.float32)
+    xdt = 0 if dx is None else _matrix(dx, "dx")[0]
+    wdt, ldgw = (1, K) if grad_weight is None else _matrix(grad_weight, "grad_weight")
+    if grad_weight is not None and tuple(grad_weight.shape) != (N, K):
+        raise ValueError("grad_weight must be [N, K]")
+    if grad_bias is not None and (grad_bias.dtype != torch.float32 or grad_bias.numel() != N
+                                  or not grad_bias.is_contiguous()):
+        raise ValueError("grad_bias must be contiguous fp32 [N]")
+    if workspace is None:
+        workspace = torch.empty(int(lib.rlk_workspace_size(OP_LINEAR_BWD, M, N, K)), device=dev,
+                                dtype=torch.uint8)
+    ck = None if kept is None else ctypes.byref(kept.buffers())
+    _check("rlk_linear_bwd",
+           lib.rlk_linear_bwd(_ptr(dy), lddy, None if kept else _ptr(x), ldx, ck, _ptr(weight), ldw,
+                              _ptr(preact), ldz, M, N, K, int(activation), _ptr(dx), xdt, K,
+                              _ptr(grad_weight), wdt, ldgw, _ptr(grad_bias), int(bool(accumulate)),
+                              _ptr(workspace), workspace.numel(), _stream(dev)))
+    return dx, grad_weight, grad_bias
+
+
+class _Linear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, residual, activation, keep8):
+        if activation == ACT_NONE:
+            y, z = linear(x, weight, bias, residual), None
+        else:
+            y, z = linear(x, weight, bias, residual, activation=activation, return_preact=True)
+        ck = checkpoint_pack(x) if keep8 else None
+        ctx.save_for_backward(ck.codes if keep8 else x, ck.scales if keep8 else None, weight, z)
+        ctx.activation, ctx.bias_dtype = activation, None if bias is None else bias.dtype
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        kept, scales, weight, z = ctx.saved_tensors
+        x = kept if scales is None else Checkpoint(kept, scales, kept.shape[0], weight.shape[1])
+        dy = dy.contiguous()
+        dx, dw, db = linear_backward(dy, x, weight, z, activation=ctx.activation,
+                                     weight_grad_dtype=weight.dtype,
+                                     want_x_grad=ctx.needs_input_grad[0],
+                                     want_weight_grad=ctx.needs_input_grad[1],
+                                     want_bias_grad=ctx.needs_input_grad[2])
+        return (dx, dw, None if db is None else db.to(ctx.bias_dtype),
+                dy if ctx.needs_input_grad[3] else None, None, None)
+
+
+def linear_autograd(x: torch.Tensor, weight: torch.Tensor, bias=None, residual=None, *,
+                    activation: int = ACT_NONE, keep_8bit: bool = False):
+    """``linear`` as a differentiable op; ``keep_8bit`` keeps x for the backward
+    as its 8-bit checkpoint instead of the tensor."""
+    return _Linear.apply(x, weight, bias, residual, activation, keep_8bit)
 
 
 # ------------------------------------------------------------ preference loss

@@ -263,6 +263,54 @@ struct PrefArgs {
 size_t pref_workspace_bytes(int64_t n_tok, int64_t n_pairs);
 cudaError_t launch_preference_loss(PrefArgs a, void* workspace, cudaStream_t stream);
 
+// Matrix product with a fused epilogue and its backward (linear.cu).
+struct LinearArgs {
+  const void* x;
+  int64_t ldx;
+  const void* w;
+  int64_t ldw;
+  const void* bias;
+  int bias_dtype;
+  const void* residual;
+  int64_t ldr;
+  int64_t M, N, K;
+  int act;              // rlk_activation
+  void* y;
+  int y_dtype;
+  int64_t ldy;
+  void* z;
+  int64_t ldz;
+  void* workspace;
+};
+struct LinearBwdArgs {
+  const void* dy;
+  int64_t lddy;
+  const void* x;        // NULL: from ck
+  int64_t ldx;
+  CheckpointView ck;
+  const void* w;
+  int64_t ldw;
+  const void* z;
+  int64_t ldz;
+  int64_t M, N, K;
+  int act;
+  void* dx;
+  int dx_dtype;
+  int64_t lddx;
+  void* dw;
+  int dw_dtype;
+  int64_t lddw;
+  float* db;
+  int accumulate;
+  void* workspace;
+};
+size_t linear_workspace_bytes(int64_t M, int64_t N, int64_t K);       // the most a call may need
+size_t linear_workspace_needed(const LinearArgs& a);                  // what this one needs
+size_t linear_bwd_workspace_bytes(int64_t M, int64_t N, int64_t K);
+size_t linear_bwd_workspace_needed(const LinearBwdArgs& a);
+cudaError_t launch_linear_fwd(const LinearArgs& a, cudaStream_t stream);
+cudaError_t launch_linear_bwd(const LinearBwdArgs& a, cudaStream_t stream);
+
 cudaError_t launch_sample(const SampleArgs& a, cudaStream_t stream);
 cudaError_t launch_shard_partials(const ShardArgs& a, cudaStream_t stream);
 cudaError_t launch_shard_combine(const ShardCombineArgs& a, cudaStream_t stream);

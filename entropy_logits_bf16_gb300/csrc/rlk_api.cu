@@ -143,6 +143,8 @@ size_t rlk_workspace_size(int op, int64_t T, int64_t V, int64_t H) {
     case RLK_OP_LMHEAD_TOPP: return rlk::lmhead_topp_workspace_bytes(T, V, H);
     case RLK_OP_NORM_BWD: return rlk::norm_bwd_workspace_bytes(T, V);
     case RLK_OP_PREFERENCE_LOSS: return rlk::pref_workspace_bytes(T, V);
+    case RLK_OP_LINEAR: return rlk::linear_workspace_bytes(T, V, H);
+    case RLK_OP_LINEAR_BWD: return rlk::linear_bwd_workspace_bytes(T, V, H);
     case RLK_OP_CANONICAL:
       return V < 1 ? 0 : (size_t)V * (size_t)T * sizeof(rlk_shard_partial);
     case RLK_OP_CANONICAL_TOPP:
@@ -975,6 +977,115 @@ rlk_status rlk_norm_bwd(const void* dy, rlk_dtype dy_dtype, int64_t lddy, const 
   a.workspace = static_cast<float*>(workspace);
   if (rlk::take_injected_failure()) return RLK_ERR_CUDA;
   return rlk::launch_norm_bwd(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? RLK_OK
+             : RLK_ERR_CUDA;
+}
+
+namespace {
+
+constexpr int64_t kMaxFeatures = int64_t(1) << 24;
+
+bool linear_sizes_ok(int64_t M, int64_t N, int64_t K, rlk_activation act) {
+  return M >= 0 && M <= INT32_MAX && N >= 1 && N <= kMaxFeatures && K >= 1 && K <= kMaxFeatures &&
+         (act == RLK_ACT_NONE || act == RLK_ACT_GELU || act == RLK_ACT_SILU || act == RLK_ACT_RELU);
+}
+bool workspace_ok(const void* workspace, size_t bytes, size_t need) {
+  return need == 0 || (workspace && bytes >= need && aligned_to(workspace, 16));
+}
+
+}  // namespace
+
+rlk_status rlk_linear_fwd(const void* x, int64_t ldx, const void* w, int64_t ldw, const void* bias,
+                          rlk_dtype bias_dtype, const void* residual, int64_t ldr, int64_t M,
+                          int64_t N, int64_t K, rlk_activation act, void* y, rlk_dtype y_dtype,
+                          int64_t ldy, void* z, int64_t ldz, void* workspace,
+                          size_t workspace_bytes, rlk_stream stream) {
+  if (!linear_sizes_ok(M, N, K, act) || !good_dtype(bias_dtype) || !good_dtype(y_dtype))
+    return RLK_ERR_INVALID_ARG;
+  if (ldx < K || ldw < K || ldy < N || (residual && ldr < N) || (z && ldz < N))
+    return RLK_ERR_INVALID_ARG;
+  if (M == 0) return RLK_OK;
+  if (!x || !w || !y || !aligned_to(x, 2) || !aligned_to(w, 2) || !elem_aligned(bias, bias_dtype) ||
+      !aligned_to(residual, 2) || !elem_aligned(y, y_dtype) || !aligned_to(z, 2))
+    return RLK_ERR_INVALID_ARG;
+  rlk::LinearArgs a{};
+  a.x = x;
+  a.ldx = ldx;
+  a.w = w;
+  a.ldw = ldw;
+  a.bias = bias;
+  a.bias_dtype = dtype_index(bias_dtype);
+  a.residual = residual;
+  a.ldr = ldr;
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.act = (int)act;
+  a.y = y;
+  a.y_dtype = dtype_index(y_dtype);
+  a.ldy = ldy;
+  a.z = z;
+  a.ldz = ldz;
+  a.workspace = workspace;
+  if (!workspace_ok(workspace, workspace_bytes, rlk::linear_workspace_needed(a)))
+    return RLK_ERR_WORKSPACE;
+  if (rlk::take_injected_failure()) return RLK_ERR_CUDA;
+  return rlk::launch_linear_fwd(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? RLK_OK
+             : RLK_ERR_CUDA;
+}
+
+rlk_status rlk_linear_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                          const rlk_checkpoint* checkpoint, const void* w, int64_t ldw,
+                          const void* z, int64_t ldz, int64_t M, int64_t N, int64_t K,
+                          rlk_activation act, void* grad_x, rlk_dtype grad_x_dtype, int64_t ldgx,
+                          void* grad_w, rlk_dtype grad_w_dtype, int64_t ldgw, float* grad_bias,
+                          int accumulate, void* workspace, size_t workspace_bytes,
+                          rlk_stream stream) {
+  if (!linear_sizes_ok(M, N, K, act) || !good_dtype(grad_x_dtype) || !good_dtype(grad_w_dtype))
+    return RLK_ERR_INVALID_ARG;
+  if (lddy < N || (grad_x && ldgx < K) || (grad_w && ldgw < K)) return RLK_ERR_INVALID_ARG;
+  if (!elem_aligned(grad_x, grad_x_dtype) || !elem_aligned(grad_w, grad_w_dtype) ||
+      !aligned_to(grad_bias, 4))
+    return RLK_ERR_INVALID_ARG;
+  rlk::LinearBwdArgs a{};
+  if (M > 0) {
+    if (!dy || !aligned_to(dy, 2)) return RLK_ERR_INVALID_ARG;
+    if (act != RLK_ACT_NONE && (!z || ldz < N || !aligned_to(z, 2))) return RLK_ERR_INVALID_ARG;
+    if (grad_x && (!w || ldw < K || !aligned_to(w, 2))) return RLK_ERR_INVALID_ARG;
+    if (grad_w) {
+      if (!x == !checkpoint) return RLK_ERR_INVALID_ARG;
+      if (x && (ldx < K || !aligned_to(x, 2))) return RLK_ERR_INVALID_ARG;
+      if (checkpoint && !checkpoint_ok(checkpoint, K, a.ck)) return RLK_ERR_INVALID_ARG;
+    }
+  }
+  if (accumulate && grad_w && grad_w_dtype != RLK_F32) return RLK_ERR_UNSUPPORTED;
+  a.dy = dy;
+  a.lddy = lddy;
+  a.x = x;
+  a.ldx = ldx;
+  a.w = w;
+  a.ldw = ldw;
+  a.z = z;
+  a.ldz = ldz;
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.act = (int)act;
+  a.dx = grad_x;
+  a.dx_dtype = dtype_index(grad_x_dtype);
+  a.lddx = ldgx;
+  a.dw = grad_w;
+  a.dw_dtype = dtype_index(grad_w_dtype);
+  a.lddw = ldgw;
+  a.db = grad_bias;
+  a.accumulate = accumulate != 0;
+  a.workspace = workspace;
+  if (!grad_w && !grad_bias && (M == 0 || !grad_x)) return RLK_OK;
+  if (M > 0 && !workspace_ok(workspace, workspace_bytes, rlk::linear_bwd_workspace_needed(a)))
+    return RLK_ERR_WORKSPACE;
+  if (rlk::take_injected_failure()) return RLK_ERR_CUDA;
+  return rlk::launch_linear_bwd(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? RLK_OK
              : RLK_ERR_CUDA;
 }

@@ -86,7 +86,8 @@ typedef enum {
 /* Operation ids for rlk_workspace_size. */
 enum { RLK_OP_LOGPROB_ENTROPY = 0, RLK_OP_GRPO_LOSS = 1, RLK_OP_LMHEAD = 2,
        RLK_OP_LMHEAD_BWD = 3, RLK_OP_LMHEAD_TOPP = 4, RLK_OP_CANONICAL = 5,
-       RLK_OP_CANONICAL_TOPP = 6, RLK_OP_NORM_BWD = 7, RLK_OP_PREFERENCE_LOSS = 8 };
+       RLK_OP_CANONICAL_TOPP = 6, RLK_OP_NORM_BWD = 7, RLK_OP_PREFERENCE_LOSS = 8,
+       RLK_OP_LINEAR = 9, RLK_OP_LINEAR_BWD = 10 };
 
 /* Bits OR-ed into *out_status_word by the kernels. */
 #define RLK_STATUS_BAD_TOKEN_ID 0x1u   /* a token id outside [0, V)          */
@@ -151,6 +152,8 @@ const char* rlk_status_string(rlk_status status);
  *  RLK_OP_CANONICAL_TOPP:  the same (rlk_logprob_entropy_canonical_topp)
  *  RLK_OP_NORM_BWD:        T rows, V = the row width H, H unused
  *  RLK_OP_PREFERENCE_LOSS: T packed tokens, V = n_pairs, H unused
+ *  RLK_OP_LINEAR:          T rows, V = N output features, H = K input features
+ *  RLK_OP_LINEAR_BWD:      the same (rlk_linear_bwd)
  * Returns 0 for an unknown op or negative sizes. */
 size_t rlk_workspace_size(int op, int64_t T, int64_t V, int64_t H);
 
@@ -803,6 +806,15 @@ rlk_status rlk_logprob_entropy_canonical_topp(const void* logits, rlk_dtype dtyp
                                               uint32_t* out_status_word, void* workspace,
                                               size_t workspace_bytes, rlk_stream stream);
 
+/*
+ * The operators around the log-probability path of a preference-training step
+ * (the pages stop at the loss over log-probabilities; these are the layers a
+ * trainer runs on either side of rlk_lmhead_logprob):
+ *
+ *   x -> rlk_linear_fwd -> rlk_norm_fwd -> rlk_lmhead_logprob_fwd -> rlk_preference_loss
+ *     -> rlk_lmhead_logprob_bwd -> rlk_norm_bwd -> rlk_linear_bwd
+ */
+
 /* Activation checkpoints in 8 bits: what a forward keeps of an activation
  * x[T, H] for its backward.  Each row is cut into blocks of
  * RLK_CHECKPOINT_BLOCK columns (the last may be short); a block holds
@@ -921,6 +933,83 @@ rlk_status rlk_norm_bwd(const void* dy, rlk_dtype dy_dtype, int64_t lddy, const 
                         const float* mean, const float* rstd, void* grad_x, rlk_dtype grad_dtype,
                         int64_t ldg, float* grad_weight, float* grad_bias, int accumulate,
                         void* workspace, size_t workspace_bytes, rlk_stream stream);
+
+typedef enum {
+  RLK_ACT_NONE = 0,
+  RLK_ACT_GELU = 1,   /* z Phi(z), Phi the normal distribution function (erf)  */
+  RLK_ACT_SILU = 2,   /* z / (1 + exp(-z))                                     */
+  RLK_ACT_RELU = 3    /* max(z, 0), slope 0 at z = 0                           */
+} rlk_activation;
+
+/*
+ * rlk_linear_fwd -- matrix product with bias, activation and residual.
+ *
+ *   z = x w^T + bias,   y = act(z) + residual,
+ * bf16 inputs, fp32 accumulation on the tensor cores, the epilogue in fp32, y
+ * and z rounded once each.
+ *
+ * Arguments
+ *  x               device bf16, M x ldx elements (ldx >= K).
+ *  w               device bf16, N x ldw elements (ldw >= K), one row an output
+ *                  feature.
+ *  bias            device [N] of bias_dtype, or NULL.
+ *  residual        device bf16, M x ldr elements (ldr >= N), or NULL.
+ *  M, N, K         M >= 0; 1 <= N, K <= 2^24.
+ *  y               device, y_dtype, M x ldy elements (ldy >= N); may not
+ *                  overlap the inputs, except that it may be the residual
+ *                  itself (same address and stride, bf16).
+ *  z               device bf16, M x ldz elements (ldz >= N), or NULL: the
+ *                  pre-activation, for rlk_linear_bwd.
+ *  workspace       aligned copies of x and w when their rows do not start on
+ *                  16-byte boundaries (base and stride): then at least
+ *                  rlk_workspace_size(RLK_OP_LINEAR, M, N, K) bytes serve, 16-byte
+ *                  aligned, contents on entry do not matter; else it may be NULL.
+ * Deterministic.  Calls of few rows split K over several CTAs, so a row's last
+ * bits may differ between calls of a different M (never between runs).
+ * NaN and infinities propagate as in the formula.
+ * Errors: RLK_ERR_INVALID_ARG for sizes or strides outside the rules, bad
+ *  dtypes or activation, null or misaligned pointers; RLK_ERR_WORKSPACE.
+ *  M == 0 returns RLK_OK without launching.
+ */
+rlk_status rlk_linear_fwd(const void* x, int64_t ldx, const void* w, int64_t ldw, const void* bias,
+                          rlk_dtype bias_dtype, const void* residual, int64_t ldr, int64_t M,
+                          int64_t N, int64_t K, rlk_activation act, void* y, rlk_dtype y_dtype,
+                          int64_t ldy, void* z, int64_t ldz, void* workspace,
+                          size_t workspace_bytes, rlk_stream stream);
+
+/*
+ * rlk_linear_bwd -- gradients of rlk_linear_fwd.
+ *
+ *   dz = dy act'(z),   grad_x = dz w,   grad_w (+)= dz^T x,   grad_bias (+)= sum_m dz;
+ * the residual's gradient is dy itself.  dz is formed in fp32; grad_bias sums
+ * it unrounded, and the two products take it rounded to bf16 (exact when act is
+ * RLK_ACT_NONE), as the tensor cores need.
+ *
+ * Arguments
+ *  dy              device bf16, M x lddy elements (lddy >= N).
+ *  x, ldx          the forward's input; or NULL with
+ *  checkpoint      its 8-bit checkpoint (exactly one of the two when grad_w is
+ *                  given, neither is needed otherwise).
+ *  w, ldw          the forward's.
+ *  z, ldz          the forward's pre-activation (may be NULL for RLK_ACT_NONE).
+ *  grad_x          device, grad_x_dtype, M x ldgx elements (ldgx >= K), or NULL.
+ *  grad_w          device, grad_w_dtype, N x ldgw elements (ldgw >= K), or NULL.
+ *  grad_bias       device float[N] or NULL.
+ *  accumulate      non-zero: grad_w (RLK_F32 only) and grad_bias are added to.
+ *  workspace       at least rlk_workspace_size(RLK_OP_LINEAR_BWD, M, N, K) bytes,
+ *                  16-byte aligned; contents on entry do not matter.
+ * Deterministic for given sizes.  A call that needs less than the size above
+ * (bf16 operands with 16-byte rows and no activation need no copies) accepts less.
+ * Errors: as rlk_linear_fwd; RLK_ERR_UNSUPPORTED for accumulate with a bf16
+ *  grad_w.  M == 0 zeroes grad_w and grad_bias (or leaves them, accumulating).
+ */
+rlk_status rlk_linear_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                          const rlk_checkpoint* checkpoint, const void* w, int64_t ldw,
+                          const void* z, int64_t ldz, int64_t M, int64_t N, int64_t K,
+                          rlk_activation act, void* grad_x, rlk_dtype grad_x_dtype, int64_t ldgx,
+                          void* grad_w, rlk_dtype grad_w_dtype, int64_t ldgw, float* grad_bias,
+                          int accumulate, void* workspace, size_t workspace_bytes,
+                          rlk_stream stream);
 
 typedef enum {
   RLK_PREF_SIGMOID = 0,   /* -(1 - s) ln sigma(h) - s ln sigma(-h), s the label smoothing */

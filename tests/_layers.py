@@ -111,3 +111,17 @@ def preference64(lp, ref, mask, off, kind, beta, smoothing, margin, mean):
     stats = torch.tensor([loss, len(live), (rc > rr).sum().item() / n, (rc - rr).sum().item() / n,
                           rc.sum().item() / n, rr.sum().item() / n], dtype=torch.float64)
     return loss, grad, reward, stats
+
+
+def act64(z, act):
+    """act(z) and act'(z) in 64 bits; 0 none, 1 GELU, 2 SiLU, 3 ReLU."""
+    z = z.double()
+    if act == 1:
+        phi = 0.5 * torch.erfc(-z * 0.5 ** 0.5)
+        return z * phi, phi + z * torch.exp(-0.5 * z * z) * (0.5 / torch.pi) ** 0.5
+    if act == 2:
+        s = torch.sigmoid(z)
+        return z * s, s * (1 + z * (1 - s))
+    if act == 3:
+        return z.clamp_min(0), (z > 0).double()
+    return z, torch.ones_like(z)

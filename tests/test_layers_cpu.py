@@ -140,3 +140,56 @@ def test_preference_binding_refuses():
     x = torch.zeros(4)
     with pytest.raises(ValueError):
         rlk.preference_loss(x, None, torch.zeros(3, dtype=torch.int32))
+
+
+def lin(lib, **kw):
+    a = dict(x=FAKE, ldx=64, w=FAKE, ldw=64, b=FAKE, bd=1, r=FAKE, ldr=32, M=4, N=32, K=64, act=1, y=FAKE, yd=0, ldy=32,
+             z=FAKE, ldz=32, ws=None, wsb=0)
+    a.update(kw)
+    return lib.rlk_linear_fwd(a["x"], a["ldx"], a["w"], a["ldw"], a["b"], a["bd"], a["r"], a["ldr"], a["M"], a["N"], a["K"],
+                              a["act"], a["y"], a["yd"], a["ldy"], a["z"], a["ldz"], a["ws"], a["wsb"], None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(M=-1), dict(M=1 << 31), dict(N=0), dict(K=0), dict(N=(1 << 24) + 1, ldy=1 << 25, ldr=1 << 25, ldz=1 << 25),
+    dict(K=(1 << 24) + 1, ldx=1 << 25, ldw=1 << 25), dict(act=4), dict(act=-1), dict(bd=2), dict(yd=2), dict(ldx=63), dict(ldw=63),
+    dict(ldy=31), dict(ldr=31), dict(ldz=31), dict(x=None), dict(w=None), dict(y=None), dict(x=ODD), dict(w=ODD), dict(y=ODD),
+    dict(z=ODD), dict(r=ODD), dict(b=ctypes.c_void_p(0x10002)), dict(y=ctypes.c_void_p(0x10002), yd=1)])
+def test_linear_rejects(lib, armed, kw):
+    assert lin(lib, **kw) == 1
+
+
+def test_linear_workspace_and_accepts(lib, armed):
+    assert lin(lib) == 4 and lin(lib, b=None, r=None, z=None, ldr=0, ldz=0) == 4 and lin(lib, M=0, x=None, w=None, y=None) == 0
+    need = lib.rlk_workspace_size(rlk.OP_LINEAR, 4, 32, 64)
+    for odd in (dict(x=ctypes.c_void_p(0x10002)), dict(ldx=65), dict(ldw=66)):
+        assert lin(lib, **odd) == 3 and lin(lib, **odd, ws=FAKE, wsb=need) == 4
+        assert lin(lib, **odd, ws=ctypes.c_void_p(0x10008), wsb=need) == 3 and lin(lib, **odd, ws=FAKE, wsb=16) == 3
+
+
+def lin_bwd(lib, **kw):
+    a = dict(dy=FAKE, lddy=32, x=FAKE, ldx=64, ck=None, w=FAKE, ldw=64, z=FAKE, ldz=32, M=4, N=32, K=64, act=1, dx=FAKE, xd=0,
+             ldgx=64, dw=FAKE, wd=1, ldgw=64, db=FAKE, acc=0, ws=FAKE, wsb=1 << 20)
+    a.update(kw)
+    return lib.rlk_linear_bwd(a["dy"], a["lddy"], a["x"], a["ldx"], a["ck"], a["w"], a["ldw"], a["z"], a["ldz"], a["M"], a["N"],
+                              a["K"], a["act"], a["dx"], a["xd"], a["ldgx"], a["dw"], a["wd"], a["ldgw"], a["db"], a["acc"],
+                              a["ws"], a["wsb"], None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(M=-1), dict(N=0), dict(K=0), dict(act=9), dict(xd=2), dict(wd=2), dict(lddy=31), dict(ldx=63), dict(ldw=63),
+    dict(ldz=31), dict(ldgx=63), dict(ldgw=63), dict(dy=None), dict(x=None), dict(ck=ckpt()), dict(x=None, ck=ckpt(ldc=48)),
+    dict(w=None), dict(z=None), dict(dy=ODD), dict(x=ODD), dict(w=ODD), dict(z=ODD), dict(dx=ODD), dict(dw=ODD), dict(db=ODD)])
+def test_linear_bwd_rejects(lib, armed, kw):
+    assert lin_bwd(lib, **kw) == 1
+
+
+def test_linear_bwd_workspace_and_accepts(lib, armed):
+    need = lib.rlk_workspace_size(rlk.OP_LINEAR_BWD, 4, 32, 64)
+    assert need % 256 == 0 and lin_bwd(lib, wsb=need) == 4
+    assert lin_bwd(lib, ws=None) == 3 and lin_bwd(lib, wsb=256) == 3 and lin_bwd(lib, ws=ctypes.c_void_p(0x10008)) == 3
+    assert lin_bwd(lib, act=0, z=None, db=None, ws=None, wsb=0) == 4            # no copies, no partial sums
+    assert lin_bwd(lib, x=None, ldx=0, ck=ckpt(), acc=1) == 4
+    assert lin_bwd(lib, dw=None, x=None, ldx=0) == 4 and lin_bwd(lib, dx=None, w=None) == 4
+    assert lin_bwd(lib, acc=1, wd=0) == 2
+    assert lin_bwd(lib, dx=None, dw=None, db=None) == 0 and lin_bwd(lib, M=0, dy=None, dw=None, db=None) == 0
