@@ -1,5 +1,10 @@
 // rlk_checkpoint_pack / rlk_checkpoint_unpack: an activation as 8-bit codes
 // with a power-of-two step per 32 columns, and back.
+//
+// A maximum, a multiplication and a conversion an element against 3 to 5 bytes of
+// traffic: bound by memory.  Rows that start on 16-byte boundaries go 16
+// columns a thread (two threads share a block, and each has the loads of two rows in
+// flight); others one column a lane, a block a warp, four blocks in flight.
 
 #include "checkpoint.cuh"
 #include "internal.h"
@@ -9,61 +14,230 @@ namespace rlk {
 namespace {
 
 constexpr int CT = 256;
+constexpr int ROWS = 2;     // rows a thread has in flight (16 columns a thread)
+constexpr int BLOCKS = 4;   // blocks a warp has in flight (one column a lane)
 
 __device__ __forceinline__ float ld_elem(const void* p, int dtype, int64_t i) {
   return dtype ? static_cast<const float*>(p)[i]
                : bf16_val(static_cast<const uint16_t*>(p)[i]);
 }
 
-// One warp per block of 32 columns, any layout.
-__global__ void __launch_bounds__(CT) checkpoint_pack_kernel(CheckpointArgs a) {
-  const int lane = threadIdx.x & 31;
-  const int64_t nb = (a.H + kCkBlock - 1) / kCkBlock;
-  const int64_t n = a.T * nb;
+// 16 columns from c on (0 past the row).
+template <int DT>
+__device__ __forceinline__ void load16(const void* p, int64_t at, int c, int H, float (&v)[16]) {
+  if (c + 16 <= H) {
+    if (DT) {
+      const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at + c);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float4 f = q[k];
+        v[4 * k] = f.x; v[4 * k + 1] = f.y; v[4 * k + 2] = f.z; v[4 * k + 3] = f.w;
+      }
+    } else {
+      const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at + c);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint4 f = q[k];
+        const uint32_t w[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          v[8 * k + 2 * j] = bf16_lo(w[j]);
+          v[8 * k + 2 * j + 1] = bf16_hi(w[j]);
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] = c + j < H ? ld_elem(p, DT, at + c + j) : 0.f;
+  }
+}
+
+// n threads a row (a power of two up to CT), ROWS rows a thread.
+template <int DT>
+__global__ void __launch_bounds__(CT) checkpoint_pack_kernel(CheckpointArgs a, int n) {
+  const int t = threadIdx.x & (n - 1), H = (int)a.H, per = CT / n;
+  const int64_t r0 = (int64_t)blockIdx.x * per * ROWS + threadIdx.x / n;
   bool bad = false;
-  for (int64_t u = (int64_t)blockIdx.x * (CT / 32) + (threadIdx.x >> 5); u < n;
-       u += (int64_t)gridDim.x * (CT / 32)) {
-    const int64_t t = u / nb, b = u - t * nb, c = b * kCkBlock + lane;
-    const float x = c < a.H ? ld_elem(a.x, a.dtype, t * a.ldx + c) : 0.f;
-    const uint32_t byte = ck_scale_byte(__reduce_max_sync(0xFFFFFFFFu, abs_bits(x)));
-    bad = bad || byte == 255u;
-    if (c < a.H) a.ck.codes[t * a.ck.ldc + c] = (int8_t)ck_code(x, byte);
-    if (lane == 0) a.ck.scales[t * a.ck.lds + b] = (uint8_t)byte;
+  // every thread of a pair makes every step: the shuffle needs both
+  for (int c0 = 0; c0 < H; c0 += n * 16) {
+    const int c = c0 + t * 16;
+    float v[ROWS][16];
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) {
+      const int64_t row = r0 + k * per;
+      if (row < a.T) {
+        load16<DT>(a.x, row * a.ldx, c, H, v[k]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[k][j] = 0.f;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) {
+      const int64_t row = r0 + k * per;
+      uint32_t amax = 0u;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) amax = max(amax, abs_bits(v[k][j]));
+      amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+      const uint32_t byte = ck_scale_byte(amax);
+      if (row >= a.T || c >= H) continue;
+      bad = bad || byte == 255u;
+      uint32_t q[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int j = 0; j < 16; ++j) q[j / 4] |= ((uint32_t)ck_code(v[k][j], byte) & 255u) << (8 * (j % 4));
+      int8_t* dst = a.ck.codes + row * a.ck.ldc + c;
+      if (c + 16 <= H) {
+        *reinterpret_cast<uint4*>(dst) = make_uint4(q[0], q[1], q[2], q[3]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          if (c + j < H) dst[j] = (int8_t)(q[j / 4] >> (8 * (j % 4)));
+      }
+      if ((t & 1) == 0) a.ck.scales[row * a.ck.lds + c / kCkBlock] = (uint8_t)byte;
+    }
+  }
+  if (bad && a.status) atomicOr(a.status, RLK_STATUS_NONFINITE);
+}
+
+template <int DT>
+__global__ void __launch_bounds__(CT) checkpoint_unpack_kernel(CheckpointArgs a, int n) {
+  const int t = threadIdx.x & (n - 1), H = (int)a.H, per = CT / n;
+  const int64_t r0 = (int64_t)blockIdx.x * per * ROWS + threadIdx.x / n;
+  for (int c = t * 16; c < H; c += n * 16) {
+    uint4 q[ROWS];
+    float step[ROWS];
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) {
+      const int64_t row = r0 + k * per;
+      if (row >= a.T) continue;
+      q[k] = *reinterpret_cast<const uint4*>(a.ck.codes + row * a.ck.ldc + c);   // ld_codes is a multiple of 16
+      step[k] = ck_step(a.ck.scales[row * a.ck.lds + c / kCkBlock]);
+    }
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) {
+      const int64_t row = r0 + k * per;
+      if (row >= a.T) continue;
+      const uint32_t w[4] = {q[k].x, q[k].y, q[k].z, q[k].w};
+      float v[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[j] = __fmul_rn((float)(int8_t)(w[j / 4] >> (8 * (j % 4))), step[k]);
+      if (DT) {
+        float* d = static_cast<float*>(a.x) + row * a.ldx + c;
+        if (c + 16 <= H) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            reinterpret_cast<float4*>(d)[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (c + j < H) d[j] = v[j];
+        }
+      } else {
+        __nv_bfloat16* d = static_cast<__nv_bfloat16*>(a.x) + row * a.ldx + c;
+        if (c + 16 <= H) {
+          uint32_t o[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+            o[j] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+          reinterpret_cast<uint4*>(d)[0] = make_uint4(o[0], o[1], o[2], o[3]);
+          reinterpret_cast<uint4*>(d)[1] = make_uint4(o[4], o[5], o[6], o[7]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (c + j < H) d[j] = __float2bfloat16_rn(v[j]);
+        }
+      }
+    }
+  }
+}
+
+// Any layout: a block a warp, `wpr` warps a row (a power of two up to 8).
+template <int DT>
+__global__ void __launch_bounds__(CT) checkpoint_pack_any_kernel(CheckpointArgs a, int wpr) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, per = CT / 32 / wpr;
+  const int H = (int)a.H, nb = (H + kCkBlock - 1) / kCkBlock;
+  bool bad = false;
+  for (int64_t row = (int64_t)blockIdx.x * per + warp / wpr; row < a.T; row += (int64_t)gridDim.x * per) {
+    for (int b0 = (warp & (wpr - 1)) * BLOCKS; b0 < nb; b0 += wpr * BLOCKS) {
+      float x[BLOCKS];
+#pragma unroll
+      for (int k = 0; k < BLOCKS; ++k) {
+        const int c = (b0 + k) * kCkBlock + lane;
+        x[k] = c < H ? ld_elem(a.x, DT, row * a.ldx + c) : 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < BLOCKS; ++k) {
+        const int c = (b0 + k) * kCkBlock + lane;
+        const uint32_t byte = ck_scale_byte(__reduce_max_sync(0xFFFFFFFFu, abs_bits(x[k])));
+        bad = bad || byte == 255u;
+        if (c < H) a.ck.codes[row * a.ck.ldc + c] = (int8_t)ck_code(x[k], byte);
+        if (lane == 0 && c < H) a.ck.scales[row * a.ck.lds + b0 + k] = (uint8_t)byte;
+      }
+    }
   }
   if (bad && lane == 0 && a.status) atomicOr(a.status, RLK_STATUS_NONFINITE);
 }
 
-__global__ void __launch_bounds__(CT) checkpoint_unpack_kernel(CheckpointArgs a) {
-  const int lane = threadIdx.x & 31;
-  const int64_t nb = (a.H + kCkBlock - 1) / kCkBlock;
-  const int64_t n = a.T * nb;
-  for (int64_t u = (int64_t)blockIdx.x * (CT / 32) + (threadIdx.x >> 5); u < n;
-       u += (int64_t)gridDim.x * (CT / 32)) {
-    const int64_t t = u / nb, b = u - t * nb, c = b * kCkBlock + lane;
-    if (c >= a.H) continue;
-    const float v = __fmul_rn((float)a.ck.codes[t * a.ck.ldc + c], ck_step(a.ck.scales[t * a.ck.lds + b]));
-    if (a.dtype) static_cast<float*>(a.x)[t * a.ldx + c] = v;
-    else static_cast<__nv_bfloat16*>(a.x)[t * a.ldx + c] = __float2bfloat16_rn(v);
+template <int DT>
+__global__ void __launch_bounds__(CT) checkpoint_unpack_any_kernel(CheckpointArgs a, int wpr) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, per = CT / 32 / wpr;
+  const int H = (int)a.H, nb = (H + kCkBlock - 1) / kCkBlock;
+  for (int64_t row = (int64_t)blockIdx.x * per + warp / wpr; row < a.T; row += (int64_t)gridDim.x * per) {
+    for (int b0 = (warp & (wpr - 1)) * BLOCKS; b0 < nb; b0 += wpr * BLOCKS) {
+      float v[BLOCKS];
+#pragma unroll
+      for (int k = 0; k < BLOCKS; ++k) {
+        const int c = (b0 + k) * kCkBlock + lane;
+        v[k] = c < H ? __fmul_rn((float)a.ck.codes[row * a.ck.ldc + c], ck_step(a.ck.scales[row * a.ck.lds + b0 + k])) : 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < BLOCKS; ++k) {
+        const int c = (b0 + k) * kCkBlock + lane;
+        if (c >= H) continue;
+        if (DT) static_cast<float*>(a.x)[row * a.ldx + c] = v[k];
+        else static_cast<__nv_bfloat16*>(a.x)[row * a.ldx + c] = __float2bfloat16_rn(v[k]);
+      }
+    }
   }
 }
 
-unsigned grid_for(int64_t units) {
-  const int64_t want = (units + CT / 32 - 1) / (CT / 32), cap = (int64_t)sm_count() * 8;
-  return (unsigned)(want < cap ? want : cap);
+// Whether every row of x starts on a 16-byte boundary.
+bool rows16(const CheckpointArgs& a) {
+  return reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.ldx % (a.dtype ? 4 : 8) == 0;
+}
+int pow2_up_to(int64_t want, int most) {
+  int n = 1;
+  while (n < most && n < want) n *= 2;
+  return n;
+}
+
+cudaError_t launch(const CheckpointArgs& a, void (*vec)(CheckpointArgs, int), void (*any)(CheckpointArgs, int),
+                   cudaStream_t stream) {
+  if (rows16(a)) {
+    const int n = a.H <= 32 ? 2 : pow2_up_to((a.H + 15) / 16, CT);   // whole pairs
+    const int64_t rows = CT / n * ROWS, grid = (a.T + rows - 1) / rows;
+    if (grid > INT32_MAX) return cudaErrorInvalidValue;
+    vec<<<(unsigned)grid, CT, 0, stream>>>(a, n);
+  } else {
+    const int wpr = pow2_up_to((a.H + kCkBlock * BLOCKS - 1) / (kCkBlock * BLOCKS), CT / 32);
+    const int64_t rows = CT / 32 / wpr, want = (a.T + rows - 1) / rows, cap = (int64_t)sm_count() * 64;
+    any<<<(unsigned)(want < cap ? want : cap), CT, 0, stream>>>(a, wpr);
+  }
+  return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_checkpoint_pack(const CheckpointArgs& a, cudaStream_t stream) {
-  const int64_t units = a.T * ((a.H + kCkBlock - 1) / kCkBlock);
-  checkpoint_pack_kernel<<<grid_for(units), CT, 0, stream>>>(a);
-  return cudaGetLastError();
+  return a.dtype ? launch(a, checkpoint_pack_kernel<1>, checkpoint_pack_any_kernel<1>, stream)
+                 : launch(a, checkpoint_pack_kernel<0>, checkpoint_pack_any_kernel<0>, stream);
 }
 
 cudaError_t launch_checkpoint_unpack(const CheckpointArgs& a, cudaStream_t stream) {
-  const int64_t units = a.T * ((a.H + kCkBlock - 1) / kCkBlock);
-  checkpoint_unpack_kernel<<<grid_for(units), CT, 0, stream>>>(a);
-  return cudaGetLastError();
+  return a.dtype ? launch(a, checkpoint_unpack_kernel<1>, checkpoint_unpack_any_kernel<1>, stream)
+                 : launch(a, checkpoint_unpack_kernel<0>, checkpoint_unpack_any_kernel<0>, stream);
 }
 
 }  // namespace rlk

@@ -5,10 +5,24 @@
 //   g = dy w,  dx = r (g - mean g - h mean(g h))  (RMS: without mean g),
 //   dw = sum_t dy h,  db = sum_t dy.
 //
-// Sums are fp32 in a fixed order; the parameter gradients go through per-part
-// partial sums in the workspace that a second kernel adds in part order.
+// A few flops an element: bound by memory.  A row of up to 16384 columns lives
+// in the registers of a group of threads, 16 or 32 columns a thread (4 to 512
+// threads), so each pass reads every element once:
+//  * forward: one row a group; deviations from the mean, then their squares.
+//  * backward: persistent CTAs; a thread keeps its columns of w and of the
+//    partial dw, db over all its rows, and copies its part of the next row into its own
+//    place in shared memory (cp.async) while it works on this one.  The CTAs' partials go to
+//    the workspace and a second kernel adds them in order.
+// Columns are taken 8 at a time (16-byte loads) where every row starts on a
+// 16-byte boundary, else one at a time with consecutive columns on
+// consecutive threads (2-byte loads still coalesce into whole lines).  Wider rows
+// take the any-width kernels: several passes over the row, and the parameter
+// gradients in a pass of their own.
+// Sums are fp32 in a fixed order.
 
 #include <math.h>
+
+#include <atomic>
 
 #include "checkpoint.cuh"
 #include "internal.h"
@@ -18,6 +32,8 @@ namespace rlk {
 namespace {
 
 constexpr int kNormParts = 304;   // most row parts of the parameter gradients
+// Floats of a part's dw (and db): rows of 16 bytes.
+__host__ __device__ __forceinline__ int64_t part_pitch(int64_t H) { return (H + 3) / 4 * 4; }
 
 __device__ __forceinline__ float ld_elem(const void* p, int dtype, int64_t i) {
   return dtype ? static_cast<const float*>(p)[i]
@@ -132,50 +148,568 @@ __global__ void __launch_bounds__(256) norm_param_wide_kernel(NormBwdArgs a, int
     dw = __fmaf_rn(dy, __fmul_rn(__fsub_rn(bwd_x(a, t, c), m), r), dw);
     db = __fadd_rn(db, dy);
   }
-  float* p = a.workspace + (int64_t)blockIdx.y * 2 * a.H;
+  float* p = a.workspace + (int64_t)blockIdx.y * 2 * part_pitch(a.H);
   p[c] = dw;
-  p[a.H + c] = db;
+  p[part_pitch(a.H) + c] = db;
 }
 
+// ------------------------------------------------------------ rows on chip
+// A thread has E = 16 columns, or 32 in rows of over 8192 columns.
+constexpr int kMaxGroup = 512;       // threads of a row, at most
+constexpr int64_t kOnChip = 32 * kMaxGroup;
+
+// Column of element e of thread t in a group of n threads: VW columns at a
+// time, consecutive threads on consecutive ones.
+template <int VW>
+__device__ __forceinline__ int col_of(int e, int t, int n) {
+  return ((e / VW) * n + t) * VW + e % VW;
+}
+
+// The same number, but computed anew by the compiler: column offsets that
+// depend on it are not kept in registers over all rows.
+__device__ __forceinline__ int fresh(int n) {
+  asm volatile("" : "+r"(n));
+  return n;
+}
+
+// A thread's columns of a row (0 past the end).
+template <int VW, int E>
+__device__ __forceinline__ void load_cols(const void* p, int dtype, int64_t at, int H, int t, int n,
+                                          float (&v)[E]) {
+  if (VW == 8) {
+#pragma unroll
+    for (int k = 0; k < E / 8; ++k) {
+      const int c = (k * n + t) * 8;
+      float* o = v + k * 8;
+      if (c + 8 <= H) {
+        if (dtype) {
+          const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + at + c);
+          const float4 b = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + at + c + 4);
+          o[0] = a.x; o[1] = a.y; o[2] = a.z; o[3] = a.w;
+          o[4] = b.x; o[5] = b.y; o[6] = b.z; o[7] = b.w;
+        } else {
+          const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at + c);
+          o[0] = bf16_lo(q.x); o[1] = bf16_hi(q.x); o[2] = bf16_lo(q.y); o[3] = bf16_hi(q.y);
+          o[4] = bf16_lo(q.z); o[5] = bf16_hi(q.z); o[6] = bf16_lo(q.w); o[7] = bf16_hi(q.w);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = c + j < H ? ld_elem(p, dtype, at + c + j) : 0.f;
+      }
+    }
+  } else {
+    n = fresh(n);
+    if (dtype) {
+      const float* q = static_cast<const float*>(p) + at + t;
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] = e * n < H - t ? q[e * n] : 0.f;
+    } else {
+      const uint16_t* q = static_cast<const uint16_t*>(p) + at + t;
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] = e * n < H - t ? bf16_val(q[e * n]) : 0.f;
+    }
+  }
+}
+template <int VW, int E>
+__device__ __forceinline__ void store_cols(void* p, int dtype, int64_t at, int H, int t, int n, const float (&v)[E]) {
+  if (VW == 8) {
+#pragma unroll
+    for (int k = 0; k < E / 8; ++k) {
+      const int c = (k * n + t) * 8;
+      const float* o = v + k * 8;
+      if (c + 8 <= H) {
+        if (dtype) {
+          float4* d = reinterpret_cast<float4*>(static_cast<float*>(p) + at + c);
+          d[0] = make_float4(o[0], o[1], o[2], o[3]);
+          d[1] = make_float4(o[4], o[5], o[6], o[7]);
+        } else {
+          uint32_t q[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const __nv_bfloat162 h2 = __floats2bfloat162_rn(o[2 * j], o[2 * j + 1]);
+            q[j] = *reinterpret_cast<const uint32_t*>(&h2);
+          }
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + at + c) = make_uint4(q[0], q[1], q[2], q[3]);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (c + j < H) st_elem(p, dtype, at + c + j, o[j]);
+      }
+    }
+  } else {
+    n = fresh(n);
+    if (dtype) {
+      float* q = static_cast<float*>(p) + at + t;
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (e * n < H - t) q[e * n] = v[e];
+    } else {
+      __nv_bfloat16* q = static_cast<__nv_bfloat16*>(p) + at + t;
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (e * n < H - t) q[e * n] = __float2bfloat16_rn(v[e]);
+    }
+  }
+}
+
+// Sums of two values over a group of n threads (a power of two, >= 4), on
+// every thread of it.  `buf` alternates between two halves of s_red, so one
+// barrier a sum is enough.
+__device__ __forceinline__ float2 group_sum(float2 v, int n, float2* s_red, int& buf) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int o = (n < 32 ? n : 32) / 2; o > 0; o >>= 1) {
+    v.x = __fadd_rn(v.x, __shfl_xor_sync(0xFFFFFFFFu, v.x, o));
+    v.y = __fadd_rn(v.y, __shfl_xor_sync(0xFFFFFFFFu, v.y, o));
+  }
+  if (n > 32) {
+    const int nw = n / 32;
+    float2* s = s_red + buf * 32;
+    buf ^= 1;
+    if (lane == 0) s[warp] = v;
+    __syncthreads();
+    v = s[(warp & ~(nw - 1)) + (lane & (nw - 1))];
+    for (int o = nw / 2; o > 0; o >>= 1) {
+      v.x = __fadd_rn(v.x, __shfl_xor_sync(0xFFFFFFFFu, v.x, o));
+      v.y = __fadd_rn(v.y, __shfl_xor_sync(0xFFFFFFFFu, v.y, o));
+    }
+  }
+  return v;
+}
+
+// The thread's columns of the row's checkpoint.  VW = 8: a block of 32 columns
+// is 4 neighbouring threads'; VW = 1: a warp's.
+template <int VW, int E>
+__device__ __forceinline__ void write_checkpoint(const CheckpointView& ck, int64_t t_row, bool live, int H, int t, int n,
+                                                 const float (&x)[E]) {
+#pragma unroll
+  for (int k = 0; k < E / VW; ++k) {
+    uint32_t amax = 0u;
+#pragma unroll
+    for (int j = 0; j < VW; ++j) amax = max(amax, abs_bits(x[k * VW + j]));
+    if (VW == 8) {
+      amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+      amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+    } else {
+      amax = __reduce_max_sync(0xFFFFFFFFu, amax);
+    }
+    const uint32_t byte = ck_scale_byte(amax);
+    const int c = (k * n + t) * VW;
+    if (!live || c >= H) continue;
+    int8_t* dst = ck.codes + t_row * ck.ldc + c;
+    if (VW == 8) {
+      uint32_t q[2] = {0u, 0u};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) q[j / 4] |= ((uint32_t)ck_code(x[k * 8 + j], byte) & 255u) << (8 * (j % 4));
+      if (c + 8 <= H) {
+        *reinterpret_cast<uint2*>(dst) = make_uint2(q[0], q[1]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (c + j < H) dst[j] = (int8_t)(q[j / 4] >> (8 * (j % 4)));
+      }
+    } else {
+      *dst = (int8_t)ck_code(x[k], byte);
+    }
+    if (c % kCkBlock == 0) ck.scales[t_row * ck.lds + c / kCkBlock] = (uint8_t)byte;
+  }
+}
+
+// n threads a row, blockDim.x / n rows a CTA.
+template <int XT, int VW, int E>
+__global__ void __launch_bounds__(kMaxGroup, E == 16 ? 2 : 1) norm_fwd_kernel(NormArgs a, int n) {
+  __shared__ float2 s_red[64];
+  int buf = 0;
+  const int t = threadIdx.x & (n - 1), H = (int)a.H;
+  const int64_t row = (int64_t)blockIdx.x * (blockDim.x / n) + threadIdx.x / n;
+  const bool live = row < a.T;
+  const float inv_h = __fdiv_rn(1.f, (float)H);
+  float x[E];
+  if (live) {
+    load_cols<VW>(a.x, XT, row * a.ldx, H, t, n, x);
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] = 0.f;
+  }
+  float m = 0.f;
+  if (!a.rms) {
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) s = __fadd_rn(s, x[e]);
+    m = __fmul_rn(group_sum(make_float2(s, 0.f), n, s_red, buf).x, inv_h);
+  }
+  float s = 0.f;
+  const int n2 = fresh(n);
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const float d = col_of<VW>(e, t, n2) < H ? __fsub_rn(x[e], m) : 0.f;
+    s = __fmaf_rn(d, d, s);
+  }
+  const float var = __fmul_rn(group_sum(make_float2(s, 0.f), n, s_red, buf).x, inv_h);
+  const bool bad = !isfinite(var);
+  const float r = bad ? NAN : __fdiv_rn(1.f, __fsqrt_rn(__fadd_rn(var, a.eps)));
+  if (bad) m = NAN;
+  if (live && t == 0) {
+    if (a.mean && !a.rms) a.mean[row] = m;
+    if (a.rstd) a.rstd[row] = r;
+    if (bad && a.status) atomicOr(a.status, RLK_STATUS_NONFINITE);
+  }
+  if (a.ck.codes) write_checkpoint<VW>(a.ck, row, live, H, t, n, x);
+  if (!live) return;
+  float p[E];
+  if (a.weight) {
+    load_cols<VW>(a.weight, a.param_dtype, 0, H, t, n, p);
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; ++e) p[e] = 1.f;
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) x[e] = __fmul_rn(__fmul_rn(__fsub_rn(x[e], m), r), p[e]);
+  if (a.bias) {
+    load_cols<VW>(a.bias, a.param_dtype, 0, H, t, n, p);
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] = __fadd_rn(x[e], p[e]);
+  }
+  store_cols<VW>(a.y, a.y_dtype, row * a.ldy, H, t, n, x);
+}
+
+constexpr int kFromCk = 2;   // backward: x from its checkpoint
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+// Bytes of one thread's 8 columns of a row in a type (0 bf16, 1 fp32, 2 codes).
+constexpr int piece_bytes(int type) { return type == 1 ? 32 : (type == 0 ? 16 : 8); }
+
+// Starts the copy of this thread's columns into its place (k-th piece of
+// thread t at (k n + t) piece_bytes); a piece past the row copies nothing.
+template <int TYPE, int E>
+__device__ __forceinline__ void copy_cols(uint32_t dst, const void* p, int64_t at, int H, int t, int n) {
+  constexpr int es = TYPE == 1 ? 4 : (TYPE == 0 ? 2 : 1);
+#pragma unroll
+  for (int k = 0; k < E / 8; ++k) {
+    const int c = (k * n + t) * 8;
+    const int have = (H - c < 8 ? H - c : 8) * es;
+    if (have <= 0) continue;
+    const char* src = static_cast<const char*>(p) + (at + c) * es;
+    const uint32_t d = dst + (uint32_t)((k * n + t) * piece_bytes(TYPE));
+    if (TYPE == kFromCk) {
+      cp_async8(d, src, have);
+    } else {
+      cp_async16(d, src, have < 16 ? have : 16);
+      if (TYPE == 1 && have > 16) cp_async16(d + 16, src + 16, have - 16);
+    }
+  }
+}
+template <int TYPE, int E>
+__device__ __forceinline__ void take_cols(const uint8_t* s, int H, int t, int n, const float (&step)[E / 8],
+                                          float (&v)[E]) {
+#pragma unroll
+  for (int k = 0; k < E / 8; ++k) {
+    const int c = (k * n + t) * 8;
+    const uint8_t* p = s + (k * n + t) * piece_bytes(TYPE);
+    float* o = v + 8 * k;
+    if (TYPE == 1) {
+      const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+      o[0] = a.x; o[1] = a.y; o[2] = a.z; o[3] = a.w;
+      o[4] = b.x; o[5] = b.y; o[6] = b.z; o[7] = b.w;
+    } else if (TYPE == 0) {
+      const uint4 q = *reinterpret_cast<const uint4*>(p);
+      o[0] = bf16_lo(q.x); o[1] = bf16_hi(q.x); o[2] = bf16_lo(q.y); o[3] = bf16_hi(q.y);
+      o[4] = bf16_lo(q.z); o[5] = bf16_hi(q.z); o[6] = bf16_lo(q.w); o[7] = bf16_hi(q.w);
+    } else {
+      const uint2 q = *reinterpret_cast<const uint2*>(p);
+      const uint32_t w2[2] = {q.x, q.y};
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        o[j] = __fmul_rn((float)(int8_t)(w2[j / 4] >> (8 * (j % 4))), step[k]);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (c + j >= H) o[j] = 0.f;
+  }
+}
+
+// XT: 0 bf16, 1 fp32, 2 a checkpoint; DT: type of dy.  E == 32: the partial dw,
+// db live in shared memory (a thread has no registers for 32 columns of
+// them).  `depth` rows (0, 1, 2) are on their way ahead of the one at work; 0:
+// the row is loaded when its turn comes (VW = 1, and rows that do not fit).
+template <int XT, int DT, int VW, int E>
+__global__ void __launch_bounds__(kMaxGroup, 1) norm_bwd_kernel(NormBwdArgs a, int n, int depth) {
+  constexpr bool SACC = E == 32;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float2 s_red[64];
+  int buf = 0;
+  const int t = threadIdx.x & (n - 1), H = (int)a.H, groups = blockDim.x / n, grp = threadIdx.x / n;
+  const float inv_h = __fdiv_rn(1.f, (float)H);
+  float* s_acc = reinterpret_cast<float*>(smem);   // SACC: [2][E n]
+  const int dy_bytes = E / 8 * n * piece_bytes(DT), x_bytes = E / 8 * n * piece_bytes(XT);
+  uint8_t* mine = smem + (SACC ? 2 * E * n * 4 : 0) + grp * depth * (dy_bytes + x_bytes);
+
+  float w[E], dw[SACC ? 1 : E], db[SACC ? 1 : E];
+  auto load_w = [&]() {
+    if (a.weight) {
+      load_cols<VW>(a.weight, a.param_dtype, 0, H, t, n, w);
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) w[e] = 1.f;
+    }
+  };
+  if (!SACC) load_w();   // else with each row: there are no registers to keep it in
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    if (SACC) s_acc[e * n + t] = s_acc[(E + e) * n + t] = 0.f;
+    else dw[e] = db[e] = 0.f;
+  }
+  const int64_t stride = (int64_t)gridDim.x * groups;
+  const int64_t row0 = (int64_t)blockIdx.x * groups;
+  const int iters = row0 < a.T ? (int)((a.T - row0 + stride - 1) / stride) : 0;
+
+  auto place = [&](int i) { return mine + (i & (depth - 1)) * (dy_bytes + x_bytes); };
+  auto start = [&](int i) {
+    const int64_t row = row0 + grp + i * stride;
+    if (i < iters && row < a.T) {
+      uint8_t* at = place(i);
+      copy_cols<DT, E>(smem_u32(at), a.dy, row * a.lddy, H, t, n);
+      if (XT == kFromCk) copy_cols<XT, E>(smem_u32(at + dy_bytes), a.ck.codes, row * a.ck.ldc, H, t, n);
+      else copy_cols<XT, E>(smem_u32(at + dy_bytes), a.x, row * a.ldx, H, t, n);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  if (VW == 8)
+    for (int i = 0; i < depth; ++i) start(i);
+
+  for (int i = 0; i < iters; ++i) {
+    const int64_t row = row0 + grp + i * stride;
+    const bool live = row < a.T;
+    const float m = live && !a.rms ? a.mean[row] : 0.f, r = live ? a.rstd[row] : 0.f;
+    float dy[E], h[E];
+    if (VW == 8 && depth > 0) {
+      float step[E / 8];
+      if (XT == kFromCk) {
+#pragma unroll
+        for (int k = 0; k < E / 8; ++k) {
+          const int c = (k * n + t) * 8;
+          step[k] = live && c < H ? ck_step(a.ck.scales[row * a.ck.lds + c / kCkBlock]) : 0.f;
+        }
+      }
+      // this row's copies have landed when at most depth - 1 later rows' are pending
+      if (depth == 1) asm volatile("cp.async.wait_group 0;" ::: "memory");
+      else asm volatile("cp.async.wait_group 1;" ::: "memory");
+      if (live) {
+        const uint8_t* at = place(i);
+        take_cols<DT>(at, H, t, n, step, dy);
+        take_cols<XT>(at + dy_bytes, H, t, n, step, h);
+      }
+      start(i + depth);   // into the place just read: a thread reads only what it copied itself
+    } else if (live) {
+      load_cols<VW>(a.dy, DT, row * a.lddy, H, t, n, dy);
+      if (XT == kFromCk) {
+        const int n2 = fresh(n);
+        const int8_t* q = a.ck.codes + row * a.ck.ldc;
+        const uint8_t* sc = a.ck.scales + row * a.ck.lds;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const int c = col_of<VW>(e, t, n2);
+          h[e] = c < H ? __fmul_rn((float)q[c], ck_step(sc[c / kCkBlock])) : 0.f;
+        }
+      } else {
+        load_cols<VW>(a.x, XT, row * a.ldx, H, t, n, h);
+      }
+    }
+    if (!live) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) dy[e] = h[e] = 0.f;
+    }
+    if (SACC) load_w();
+    float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int e = 0; e < E; ++e) {   // past the row dy is 0, and h does not matter
+      h[e] = __fmul_rn(__fsub_rn(h[e], m), r);
+      const float g = __fmul_rn(dy[e], w[e]);
+      s.x = __fadd_rn(s.x, g);
+      s.y = __fmaf_rn(g, h[e], s.y);
+      if (SACC) {
+        s_acc[e * n + t] = __fmaf_rn(dy[e], h[e], s_acc[e * n + t]);
+        s_acc[(E + e) * n + t] = __fadd_rn(s_acc[(E + e) * n + t], dy[e]);
+      } else {
+        dw[e] = __fmaf_rn(dy[e], h[e], dw[e]);
+        db[e] = __fadd_rn(db[e], dy[e]);
+      }
+      dy[e] = g;
+    }
+    s = group_sum(s, n, s_red, buf);
+    const float mg = a.rms ? 0.f : __fmul_rn(s.x, inv_h), mgh = __fmul_rn(s.y, inv_h);
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      h[e] = __fmul_rn(r, __fsub_rn(__fsub_rn(dy[e], mg), __fmul_rn(h[e], mgh)));
+    if (live) store_cols<VW>(a.dx, a.dx_dtype, row * a.lddx, H, t, n, h);
+  }
+  if (!a.workspace) return;
+  float* part = a.workspace + (int64_t)blockIdx.x * 2 * part_pitch(a.H);
+  if (SACC) {
+    float v[E];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] = s_acc[(k * E + e) * n + t];
+      store_cols<VW>(part + k * part_pitch(a.H), 1, 0, H, t, n, v);
+    }
+    return;
+  }
+  if constexpr (!SACC) {
+    // the CTA's groups, added in order (every copy has landed: the shared memory is free again)
+    if (groups > 1) {
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      for (int g = 0; g < groups; ++g) {
+        __syncthreads();
+        if (grp != g) continue;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          float* p = s_acc + e * n + t;
+          float* q = s_acc + (E + e) * n + t;
+          *p = dw[e] = g ? __fadd_rn(*p, dw[e]) : dw[e];
+          *q = db[e] = g ? __fadd_rn(*q, db[e]) : db[e];
+        }
+      }
+      if (grp != groups - 1) return;
+    }
+    store_cols<VW>(part, 1, 0, H, t, n, dw);
+    store_cols<VW>(part + part_pitch(a.H), 1, 0, H, t, n, db);
+  }
+}
+
+// Adds the parts in order: 32 columns a CTA, warp w takes parts w, w + 8, ...
 __global__ void __launch_bounds__(256) norm_param_sum_kernel(NormBwdArgs a, int parts) {
-  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (c >= a.H) return;
+  pdl_wait();
+  __shared__ float s[8][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float* out = blockIdx.y ? a.db : a.dw;
   if (!out) return;
+  const int64_t c = (int64_t)blockIdx.x * 32 + lane;
   float v = 0.f;
-  for (int p = 0; p < parts; ++p) v = __fadd_rn(v, a.workspace[((int64_t)p * 2 + blockIdx.y) * a.H + c]);
-  out[c] = a.accumulate ? __fadd_rn(out[c], v) : v;
+  if (c < a.H) {
+    const float* p = a.workspace + blockIdx.y * part_pitch(a.H) + c;
+#pragma unroll 8
+    for (int k = warp; k < parts; k += 8) v = __fadd_rn(v, p[(int64_t)k * 2 * part_pitch(a.H)]);
+  }
+  s[warp][lane] = v;
+  __syncthreads();
+  if (warp == 0 && c < a.H) {
+    for (int k = 1; k < 8; ++k) v = __fadd_rn(v, s[k][lane]);
+    out[c] = a.accumulate ? __fadd_rn(out[c], v) : v;
+  }
 }
 
+// ------------------------------------------------------------ host side
 int parts_for(int64_t T) { return (int)(T < kNormParts ? T : kNormParts); }
+
+// Columns of a thread and threads of a row on chip.
+int cols_for(int64_t H) { return H > 16 * kMaxGroup ? 32 : 16; }
+int group_for(int64_t H) {
+  int n = 4;
+  while ((int64_t)n * cols_for(H) < H) n *= 2;
+  return n;
+}
+bool rows16(const void* p, int dtype, int64_t ld) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % (dtype ? 4 : 8) == 0;
+}
+bool base16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+template <int XT, int E>
+cudaError_t fwd(const NormArgs& a, bool vec, cudaStream_t stream) {
+  // threads of one column each make whole blocks of a checkpoint only by the warp
+  const int n = !vec && a.ck.codes && group_for(a.H) < 32 ? 32 : group_for(a.H);
+  const int block = n < 256 ? 256 : n, rows = block / n;
+  const int64_t grid = (a.T + rows - 1) / rows;
+  if (grid > INT32_MAX) return cudaErrorInvalidValue;
+  if (vec) norm_fwd_kernel<XT, 8, E><<<(unsigned)grid, block, 0, stream>>>(a, n);
+  else norm_fwd_kernel<XT, 1, E><<<(unsigned)grid, block, 0, stream>>>(a, n);
+  return cudaGetLastError();
+}
+
+template <int XT, int DT, int VW, int E>
+cudaError_t bwd(const NormBwdArgs& a, int& parts, cudaStream_t stream) {
+  auto kernel = norm_bwd_kernel<XT, DT, VW, E>;
+  const int n = group_for(a.H), block = n < 256 ? 256 : n, groups = block / n;
+  constexpr size_t most = 227 * 1024 - 1024;
+  const size_t acc = (size_t)2 * E * n * sizeof(float);
+  const size_t row = (size_t)groups * (E / 8) * n * (piece_bytes(XT) + piece_bytes(DT));
+  // two rows ahead; one beside the sums in shared memory, if it fits there
+  int depth = VW == 8 ? (E == 16 ? 2 : 1) : 0;
+  if (E == 32 && acc + row > most) depth = 0;
+  size_t smem = depth * row;
+  if (E == 32) smem += acc;
+  else if (groups > 1 && smem < acc) smem = acc;
+  static std::atomic<int> done[64];
+  const int ds = device_slot();
+  if (ds < 0 || !done[ds].load()) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+    if (e != cudaSuccess) return e;
+    if (ds >= 0) done[ds].store(1);
+  }
+  // a CTA of 256 threads shares its SM with another
+  const int64_t want = (a.T + groups - 1) / groups, cap = n <= 256 ? kNormParts : kNormParts / 2;
+  parts = (int)(want < cap ? want : cap);
+  kernel<<<parts, block, smem, stream>>>(a, n, depth);
+  return cudaGetLastError();
+}
+template <int XT, int DT>
+cudaError_t bwd_for(const NormBwdArgs& a, bool vec, int& parts, cudaStream_t stream) {
+  if (cols_for(a.H) == 32) return vec ? bwd<XT, DT, 8, 32>(a, parts, stream) : bwd<XT, DT, 1, 32>(a, parts, stream);
+  return vec ? bwd<XT, DT, 8, 16>(a, parts, stream) : bwd<XT, DT, 1, 16>(a, parts, stream);
+}
 
 }  // namespace
 
 size_t norm_bwd_workspace_bytes(int64_t T, int64_t H) {
-  return ((size_t)parts_for(T) * 2 * (size_t)H * sizeof(float) + 255) & ~(size_t)255;
+  return ((size_t)parts_for(T) * 2 * (size_t)part_pitch(H) * sizeof(float) + 255) & ~(size_t)255;
 }
 
 cudaError_t launch_norm_fwd(const NormArgs& a, cudaStream_t stream) {
+  if (a.H <= kOnChip) {
+    const bool vec = rows16(a.x, a.dtype, a.ldx) && rows16(a.y, a.y_dtype, a.ldy) && base16(a.weight) && base16(a.bias);
+    if (cols_for(a.H) == 32) return a.dtype ? fwd<1, 32>(a, vec, stream) : fwd<0, 32>(a, vec, stream);
+    return a.dtype ? fwd<1, 16>(a, vec, stream) : fwd<0, 16>(a, vec, stream);
+  }
   const int64_t cap = (int64_t)sm_count() * 4;
   norm_fwd_wide_kernel<<<(unsigned)(a.T < cap ? a.T : cap), WT, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
-cudaError_t launch_norm_bwd(const NormBwdArgs& a, cudaStream_t stream) {
-  const int64_t cap = (int64_t)sm_count() * 4;
-  if (a.T > 0) {
+cudaError_t launch_norm_bwd(const NormBwdArgs& args, cudaStream_t stream) {
+  NormBwdArgs a = args;
+  if (!a.dw && !a.db) a.workspace = nullptr;
+  int parts = 0;
+  if (a.T > 0 && a.H <= kOnChip) {
+    const bool vec = rows16(a.dy, a.dy_dtype, a.lddy) && rows16(a.dx, a.dx_dtype, a.lddx) && base16(a.weight) &&
+                     (!a.x || rows16(a.x, a.dtype, a.ldx));
+    const int type = !a.x ? kFromCk : a.dtype;
+    cudaError_t e;
+    if (a.dy_dtype == 0)
+      e = type == 0 ? bwd_for<0, 0>(a, vec, parts, stream) : type == 1 ? bwd_for<1, 0>(a, vec, parts, stream)
+                                                                    : bwd_for<kFromCk, 0>(a, vec, parts, stream);
+    else
+      e = type == 0 ? bwd_for<0, 1>(a, vec, parts, stream) : type == 1 ? bwd_for<1, 1>(a, vec, parts, stream)
+                                                                    : bwd_for<kFromCk, 1>(a, vec, parts, stream);
+    if (e != cudaSuccess) return e;
+  } else if (a.T > 0) {
+    const int64_t cap = (int64_t)sm_count() * 4;
     norm_bwd_wide_kernel<<<(unsigned)(a.T < cap ? a.T : cap), WT, 0, stream>>>(a);
     if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
+    if (a.workspace) {
+      parts = parts_for(a.T);
+      norm_param_wide_kernel<<<dim3((unsigned)((a.H + 255) / 256), parts), 256, 0, stream>>>(a, parts);
+      if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
+    }
   }
-  if (!a.dw && !a.db) return cudaSuccess;
-  const int parts = parts_for(a.T);
-  const unsigned cols = (unsigned)((a.H + 255) / 256);
-  if (parts > 0) {
-    norm_param_wide_kernel<<<dim3(cols, parts), 256, 0, stream>>>(a, parts);
-    if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
-  }
-  norm_param_sum_kernel<<<dim3(cols, 2), 256, 0, stream>>>(a, parts);
-  return cudaGetLastError();
+  if (!a.workspace) return cudaSuccess;
+  const cudaError_t e = launch_after(norm_param_sum_kernel, dim3((unsigned)((a.H + 31) / 32), 2), dim3(256), 0, stream, a, parts);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace rlk
