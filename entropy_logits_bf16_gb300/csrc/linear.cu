@@ -7,8 +7,8 @@
 // operands may each be stored with K or with M / N contiguous, so neither w nor
 // x nor dz is transposed in memory.  bf16 operands arrive by TMA (128-byte
 // swizzle) in a ring of 64-deep stages, one thread issues the tcgen05 MMAs
-// (128 x 256 x 16, fp32 accumulators in TMEM), four warps run the epilogue on
-// registers read with tcgen05.ld, one row a thread.
+// (128 x 256 x 16, fp32 accumulators in TMEM), eight warps run the epilogue on
+// registers read with tcgen05.ld.
 //  * Many tiles: persistent CTAs, one an SM; two TMEM accumulators, so a tile's
 //    epilogue runs under the next tile's products.  Tiles are walked in groups
 //    of 16 row tiles, so the CTAs at work share 16 A tiles and about 10 B tiles
@@ -38,11 +38,13 @@
 namespace rlk {
 namespace {
 
-constexpr int BM = 128, BN = 256, BK = 64, STAGES = 4, THREADS = 192;
+constexpr int BM = 128, BN = 256, BK = 64, STAGES = 4;
+constexpr int EPI_WARPS = 8, THREADS = 64 + 32 * EPI_WARPS;
 constexpr uint32_t A_BYTES = BM * BK * 2, B_BYTES = BN * BK * 2, STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr uint32_t MN_BLOCK = 64 * BK * 2;   // a 64-element block of an MN-contiguous operand
 constexpr uint32_t TMEM_COLS = 512;
-constexpr size_t SMEM_BYTES = STAGES * STAGE_BYTES + 1024 + 256;
+constexpr uint32_t STAGING = 32 * 32 * 4;    // an epilogue warp's 32 x 32 piece of a tile
+constexpr size_t SMEM_BYTES = STAGES * STAGE_BYTES + EPI_WARPS * STAGING + 1024 + 256;
 constexpr int GROUP_M = 16;
 constexpr int PLD = BN + 4;   // row pitch (floats) of a partial tile: conflict-free float4 rows
 static_assert(BM * PLD * 4 <= STAGES * STAGE_BYTES, "a partial tile fits into the ring");
@@ -59,6 +61,7 @@ struct Epilogue {
   uint16_t* z;
   int64_t ldz;
   int accumulate;      // y (fp32) is added to
+  int vec;             // rows of y, z and residual start on 16-byte boundaries
 };
 struct GemmParams {
   int64_t M, N;
@@ -88,94 +91,80 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ bool aligned16(const void* p) {
-  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
-}
 
-// The epilogue of W columns of one row (columns [col, col + n) valid).
-template <int W>
-__device__ __forceinline__ void finish(const Epilogue& e, int64_t row, int64_t col, int n, float (&v)[W]) {
-  if (e.bias) {
-    if (e.bias_dtype == 0) {
-      const uint16_t* b = static_cast<const uint16_t*>(e.bias) + col;
+// The epilogue of 8 columns of one row whose y, z and residual start on 16-byte
+// boundaries there; n of the columns exist.
+__device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8], int n) {
+  if (n == 8) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                                              pack_bf16(v[6], v[7]));
+  } else {
 #pragma unroll
-      for (int j = 0; j < W; ++j)
-        if (j < n) v[j] = __fadd_rn(v[j], bf16_val(b[j]));
-    } else {
-      const float* b = static_cast<const float*>(e.bias) + col;
-#pragma unroll
-      for (int j = 0; j < W; ++j)
-        if (j < n) v[j] = __fadd_rn(v[j], b[j]);
-    }
+    for (int j = 0; j < 8; ++j)
+      if (j < n) p[j] = (uint16_t)pack_bf16(v[j], 0.f);
   }
-  if (e.z) {
-    uint16_t* z = e.z + row * e.ldz + col;
-    if (W % 8 == 0 && n == W && aligned16(z)) {
+}
+__device__ __forceinline__ float bias_at(const Epilogue& e, int64_t col) {
+  return e.bias_dtype ? static_cast<const float*>(e.bias)[col] : bf16_val(static_cast<const uint16_t*>(e.bias)[col]);
+}
+__device__ __forceinline__ uint4 residual8(const Epilogue& e, int64_t row, int64_t col, int n) {
+  const uint16_t* r = e.residual + row * e.ldr + col;
+  if (n == 8) return *reinterpret_cast<const uint4*>(r);
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-      for (int j = 0; j < W / 8; ++j)
-        reinterpret_cast<uint4*>(z)[j] =
-            make_uint4(pack_bf16(v[8 * j], v[8 * j + 1]), pack_bf16(v[8 * j + 2], v[8 * j + 3]),
-                       pack_bf16(v[8 * j + 4], v[8 * j + 5]), pack_bf16(v[8 * j + 6], v[8 * j + 7]));
-    } else {
+  for (int j = 0; j < 8; ++j)
+    if (j < n) w[j / 2] |= (uint32_t)r[j] << (16 * (j % 2));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void finish8(const Epilogue& e, int64_t row, int64_t col, int n, float (&v)[8],
+                                        const float (&bias)[8], uint4 res) {
 #pragma unroll
-      for (int j = 0; j < W; ++j)
-        if (j < n) z[j] = (uint16_t)pack_bf16(v[j], 0.f);
-    }
-  }
+  for (int j = 0; j < 8; ++j) v[j] = __fadd_rn(v[j], bias[j]);
+  if (e.z) store8(e.z + row * e.ldz + col, v, n);
   if (e.act != RLK_ACT_NONE) {
 #pragma unroll
-    for (int j = 0; j < W; ++j) v[j] = activate(v[j], e.act);
+    for (int j = 0; j < 8; ++j) v[j] = activate(v[j], e.act);
   }
   if (e.residual) {
-    const uint16_t* r = e.residual + row * e.ldr + col;
-    if (W % 8 == 0 && n == W && aligned16(r)) {
+    const uint32_t w[4] = {res.x, res.y, res.z, res.w};
 #pragma unroll
-      for (int j = 0; j < W / 8; ++j) {
-        const uint4 q = reinterpret_cast<const uint4*>(r)[j];
-        const uint32_t w4[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          v[8 * j + 2 * k] = __fadd_rn(v[8 * j + 2 * k], bf16_lo(w4[k]));
-          v[8 * j + 2 * k + 1] = __fadd_rn(v[8 * j + 2 * k + 1], bf16_hi(w4[k]));
-        }
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < W; ++j)
-        if (j < n) v[j] = __fadd_rn(v[j], bf16_val(r[j]));
+    for (int k = 0; k < 4; ++k) {
+      v[2 * k] = __fadd_rn(v[2 * k], bf16_lo(w[k]));
+      v[2 * k + 1] = __fadd_rn(v[2 * k + 1], bf16_hi(w[k]));
     }
   }
   if (e.y_dtype == 0) {
-    uint16_t* y = static_cast<uint16_t*>(e.y) + row * e.ldy + col;
-    if (W % 8 == 0 && n == W && aligned16(y)) {
+    store8(static_cast<uint16_t*>(e.y) + row * e.ldy + col, v, n);
+    return;
+  }
+  float* y = static_cast<float*>(e.y) + row * e.ldy + col;
+  if (n == 8) {
 #pragma unroll
-      for (int j = 0; j < W / 8; ++j)
-        reinterpret_cast<uint4*>(y)[j] =
-            make_uint4(pack_bf16(v[8 * j], v[8 * j + 1]), pack_bf16(v[8 * j + 2], v[8 * j + 3]),
-                       pack_bf16(v[8 * j + 4], v[8 * j + 5]), pack_bf16(v[8 * j + 6], v[8 * j + 7]));
-    } else {
-#pragma unroll
-      for (int j = 0; j < W; ++j)
-        if (j < n) y[j] = (uint16_t)pack_bf16(v[j], 0.f);
+    for (int k = 0; k < 2; ++k) {
+      float4 o = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+      if (e.accumulate) {
+        const float4 old = reinterpret_cast<const float4*>(y)[k];
+        o = make_float4(__fadd_rn(old.x, o.x), __fadd_rn(old.y, o.y), __fadd_rn(old.z, o.z), __fadd_rn(old.w, o.w));
+      }
+      reinterpret_cast<float4*>(y)[k] = o;
     }
   } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < n) y[j] = e.accumulate ? __fadd_rn(y[j], v[j]) : v[j];
+  }
+}
+// One column of one row, any alignment.
+__device__ __forceinline__ void finish1(const Epilogue& e, int64_t row, int64_t col, float v, float bias) {
+  v = __fadd_rn(v, bias);
+  if (e.z) e.z[row * e.ldz + col] = (uint16_t)pack_bf16(v, 0.f);
+  if (e.act != RLK_ACT_NONE) v = activate(v, e.act);
+  if (e.residual) v = __fadd_rn(v, bf16_val(e.residual[row * e.ldr + col]));
+  if (e.y_dtype == 0) {
+    static_cast<uint16_t*>(e.y)[row * e.ldy + col] = (uint16_t)pack_bf16(v, 0.f);
+  } else {
     float* y = static_cast<float*>(e.y) + row * e.ldy + col;
-    if (W % 4 == 0 && n == W && aligned16(y)) {
-#pragma unroll
-      for (int j = 0; j < W / 4; ++j) {
-        float4 o = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-        if (e.accumulate) {
-          const float4 old = reinterpret_cast<const float4*>(y)[j];
-          o = make_float4(__fadd_rn(old.x, o.x), __fadd_rn(old.y, o.y), __fadd_rn(old.z, o.z),
-                          __fadd_rn(old.w, o.w));
-        }
-        reinterpret_cast<float4*>(y)[j] = o;
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < W; ++j)
-        if (j < n) y[j] = e.accumulate ? __fadd_rn(y[j], v[j]) : v[j];
-    }
+    *y = e.accumulate ? __fadd_rn(*y, v) : v;
   }
 }
 
@@ -198,7 +187,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* base_ptr = smem_raw + (base - raw);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(base_ptr + STAGES * STAGE_BYTES);
+  float* staging = reinterpret_cast<float*>(base_ptr + STAGES * STAGE_BYTES);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(base_ptr + STAGES * STAGE_BYTES + EPI_WARPS * STAGING);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 2 * STAGES + 4);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 5);
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * STAGES;
@@ -214,7 +204,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(accf0 + 8 * a, 1);
-      mbar_init(acce0 + 8 * a, 4);   // one arrive per epilogue warp
+      mbar_init(acce0 + 8 * a, EPI_WARPS);   // one arrive per epilogue warp
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
@@ -306,8 +296,13 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   } else {
     // ------------------------------------------------------ epilogue
-    const int q = warp & 3;
+    // Two warps a TMEM quadrant (32 rows), each with half of the columns, 32 at
+    // a time: tcgen05.ld gives a thread 32 columns of one row; a turn through the
+    // warp's staging (16-byte units, swizzled: no bank conflicts) gives it 8
+    // columns of 4 rows, so that a warp reads and writes whole 64-byte pieces of 8 rows.
+    const int q = warp & 3, half = (warp - 2) >> 2;
     const uint32_t lane_base = (uint32_t)(q * 32) << 16;
+    float* st = staging + (warp - 2) * (STAGING / 4);
     uint32_t tile = 0;
     bool ok = true;
     for (int t = tile0; t < p.n_tiles; t += tile_step, ++tile) {
@@ -315,33 +310,71 @@ __global__ void __launch_bounds__(THREADS, 1)
       tile_coords(p, t, mt, nt);
       const uint32_t acc = tile & 1u, accph = (tile >> 1) & 1u;
       // after a wait has run out, this tile and the CTA's later ones are NaN
-      ok = ok && tc::wait(accf0 + 8 * acc, accph, abort_flag, p.wait_limit);
+      ok = __all_sync(0xFFFFFFFFu, ok && tc::wait(accf0 + 8 * acc, accph, abort_flag, p.wait_limit));
       tc::fence_after();
-      const int r = q * 32 + lane;
-      const int64_t row = (int64_t)mt * BM + r;
+      const int64_t row0 = (int64_t)mt * BM + q * 32;
 #pragma unroll 1
-      for (int ch = 0; ch < BN / 32; ++ch) {
+      for (int ch = 0; ch < BN / 64; ++ch) {
+        const int c0 = half * (BN / 2) + ch * 32;
+        const int64_t col0 = (int64_t)nt * BN + c0;
+        const int sub = lane & 3, r8 = lane >> 2;           // 8 columns, one of 8 rows
+        const int64_t col = col0 + sub * 8;
+        const int n = (int)(p.N - col < 8 ? (p.N - col > 0 ? p.N - col : 0) : 8);
+        uint4 res[4];
+        float bias[8];
+        if (!SPLIT && p.e.vec) {                             // these loads run under the wait below
+#pragma unroll
+          for (int it = 0; it < 4; ++it)
+            if (p.e.residual && n > 0 && row0 + it * 8 + r8 < p.M)
+              res[it] = residual8(p.e, row0 + it * 8 + r8, col, n);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) bias[j] = p.e.bias && j < n ? bias_at(p.e, col + j) : 0.f;
+        }
         float v[32];
         if (ok) {
-          tc::ld32(tmem + lane_base + acc * BN + ch * 32, v);
+          tc::ld32(tmem + lane_base + acc * BN + c0, v);
         } else {
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = NAN;
         }
-        const int64_t col = (int64_t)nt * BN + ch * 32;
-        if (row >= p.M || col >= p.N) continue;
-        if (SPLIT) {
-          float* part = reinterpret_cast<float*>(base_ptr) + r * PLD + ch * 32;
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            reinterpret_cast<float4*>(part)[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-        } else {
-          finish<32>(p.e, row, col, (int)(p.N - col < 32 ? p.N - col : 32), v);
+        if (ch == BN / 64 - 1) {   // the accumulator is in registers: its next tile may begin
+          tc::fence_before();
+          __syncwarp();
+          if (lane == 0 && ok) mbar_arrive(acce0 + 8 * acc);
         }
+        if (SPLIT) {
+          if (row0 + lane < p.M && col0 < p.N) {
+            float* part = reinterpret_cast<float*>(base_ptr) + (q * 32 + lane) * PLD + c0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              reinterpret_cast<float4*>(part)[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+          }
+          continue;
+        }
+        if (col0 >= p.N) continue;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          reinterpret_cast<float4*>(st + lane * 32)[j ^ (lane & 7)] =
+              make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        __syncwarp();
+        if (p.e.vec) {
+#pragma unroll
+          for (int it = 0; it < 4; ++it) {
+            const int r = it * 8 + r8;
+            const float4* src = reinterpret_cast<const float4*>(st + r * 32);
+            const float4 a = src[(2 * sub) ^ (r & 7)], b = src[(2 * sub + 1) ^ (r & 7)];
+            float o[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+            if (row0 + r < p.M && n > 0) finish8(p.e, row0 + r, col, n, o, bias, res[it]);
+          }
+        } else if (col0 + lane < p.N) {   // a column a lane: consecutive lanes share lines
+          const float b = p.e.bias ? bias_at(p.e, col0 + lane) : 0.f;
+          const int rows = (int)(p.M - row0 < 32 ? p.M - row0 : 32);
+#pragma unroll 4
+          for (int r = 0; r < rows; ++r)
+            finish1(p.e, row0 + r, col0 + lane, st[r * 32 + (((lane >> 2) ^ (r & 7)) << 2) + (lane & 3)], b);
+        }
+        __syncwarp();
       }
-      tc::fence_before();
-      __syncwarp();
-      if (lane == 0 && ok) mbar_arrive(acce0 + 8 * acc);
     }
   }
   if (SPLIT) {
@@ -350,27 +383,49 @@ __global__ void __launch_bounds__(THREADS, 1)
     bool dead = false;    // a wait of some CTA of the cluster ran out
     const uint32_t abort_at = smem_u32(bars + 2 * STAGES + 4);
     for (int k = 0; k < cluster; ++k) dead = tc::ld_peer_u32(tc::peer_addr(abort_at, (uint32_t)k)) != 0u || dead;
-    // this CTA's share of the columns, all rows: groups of 4 columns
+    // this CTA's share of the columns, all rows
     int mt, nt;
     tile_coords(p, tile0, mt, nt);
-    const int width = BN / cluster, quads = width / 4;
-    const int64_t row0 = (int64_t)mt * BM;
+    const int width = BN / cluster, c0 = (int)rank * width;
+    const int64_t row0 = (int64_t)mt * BM, col0 = (int64_t)nt * BN + c0;
     const int rows = (int)(p.M - row0 < BM ? p.M - row0 : BM);
-    for (int i = threadIdx.x; i < rows * quads; i += THREADS) {
-      const int r = i / quads, c = (int)rank * width + (i - r * quads) * 4;
-      const int64_t col = (int64_t)nt * BN + c;
-      if (col >= p.N) continue;
-      const uint32_t at = base + (uint32_t)(r * PLD + c) * 4u;
-      float v[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int k = 0; k < cluster; ++k) {
-        const float4 o = tc::ld_peer4(tc::peer_addr(at, (uint32_t)k));
-        v[0] = __fadd_rn(v[0], o.x);
-        v[1] = __fadd_rn(v[1], o.y);
-        v[2] = __fadd_rn(v[2], o.z);
-        v[3] = __fadd_rn(v[3], o.w);
+    if (p.e.vec) {
+      const int octs = width / 8;
+      for (int i = threadIdx.x; i < rows * octs; i += THREADS) {
+        const int r = i / octs, c = (i - r * octs) * 8;
+        const int64_t col = col0 + c;
+        if (col >= p.N) continue;
+        const int n = (int)(p.N - col < 8 ? p.N - col : 8);
+        uint4 res = make_uint4(0u, 0u, 0u, 0u);
+        if (p.e.residual) res = residual8(p.e, row0 + r, col, n);
+        float bias[8], v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          bias[j] = p.e.bias && j < n ? bias_at(p.e, col + j) : 0.f;
+          v[j] = 0.f;
+        }
+        const uint32_t at = base + (uint32_t)(r * PLD + c0 + c) * 4u;
+        for (int k = 0; k < cluster; ++k) {
+          const uint32_t peer = tc::peer_addr(at, (uint32_t)k);
+          const float4 a = tc::ld_peer4(peer), b = tc::ld_peer4(peer + 16u);
+          const float o[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] = __fadd_rn(v[j], o[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = dead ? NAN : v[j];
+        finish8(p.e, row0 + r, col, n, v, bias, res);
       }
-      if (dead) v[0] = v[1] = v[2] = v[3] = NAN;
-      finish<4>(p.e, row0 + r, col, (int)(p.N - col < 4 ? p.N - col : 4), v);
+    } else {
+      for (int i = threadIdx.x; i < rows * width; i += THREADS) {
+        const int r = i / width, c = i - r * width;
+        const int64_t col = col0 + c;
+        if (col >= p.N) continue;
+        const uint32_t at = base + (uint32_t)(r * PLD + c0 + c) * 4u;
+        float v = 0.f;
+        for (int k = 0; k < cluster; ++k) v = __fadd_rn(v, tc::ld_peer_f32(tc::peer_addr(at, (uint32_t)k)));
+        finish1(p.e, row0 + r, col, dead ? NAN : v, p.e.bias ? bias_at(p.e, col) : 0.f);
+      }
     }
     tc::cluster_sync();   // no CTA leaves while its shared memory is read
   }
@@ -391,30 +446,90 @@ __global__ void __launch_bounds__(ET) repack_kernel(const uint16_t* src, int64_t
 }
 
 // dz = dy act'(z) as bf16 and the partial column sums of the unrounded dz: part
-// blockIdx.y takes rows blockIdx.y, + parts, ...
-__global__ void __launch_bounds__(ET) linear_dz_kernel(LinearBwdArgs a, uint16_t* dz, int64_t ldd, float* db_part,
-                                                       int parts) {
-  const int64_t c = (int64_t)blockIdx.x * ET + threadIdx.x;
+// blockIdx.y takes rows blockIdx.y, + parts, ...  W = 8 columns a thread where
+// the rows of dy and z start on 16-byte boundaries (dz's do), else 1; DZ_ROWS rows in
+// flight.  Bound by memory (6 bytes an element).
+constexpr int DT = 128, DZ_ROWS = 4;
+
+template <int W>
+__global__ void __launch_bounds__(DT) linear_dz_kernel(LinearBwdArgs a, uint16_t* dz, int64_t ldd, float* db_part,
+                                                       int64_t pitch, int parts) {
+  const int64_t c = ((int64_t)blockIdx.x * DT + threadIdx.x) * W;
   if (c >= a.N) return;
-  const uint16_t* dy = static_cast<const uint16_t*>(a.dy);
-  const uint16_t* z = static_cast<const uint16_t*>(a.z);
-  float sum = 0.f;
-  for (int64_t m = blockIdx.y; m < a.M; m += parts) {
-    float g = bf16_val(dy[m * a.lddy + c]);
-    if (a.act != RLK_ACT_NONE) g = __fmul_rn(g, activation_slope(bf16_val(z[m * a.ldz + c]), a.act));
-    sum = __fadd_rn(sum, g);
-    if (dz) dz[m * ldd + c] = (uint16_t)pack_bf16(g, 0.f);
+  const uint16_t* dy = static_cast<const uint16_t*>(a.dy) + c;
+  const uint16_t* z = static_cast<const uint16_t*>(a.z) + c;
+  const bool whole = W == 1 || c + W <= a.N, act = a.act != RLK_ACT_NONE;
+  float sum[W];
+#pragma unroll
+  for (int j = 0; j < W; ++j) sum[j] = 0.f;
+  for (int64_t m0 = blockIdx.y; m0 < a.M; m0 += (int64_t)parts * DZ_ROWS) {
+    uint32_t g[DZ_ROWS][(W + 1) / 2], zz[DZ_ROWS][(W + 1) / 2];
+#pragma unroll
+    for (int k = 0; k < DZ_ROWS; ++k) {
+      const int64_t m = m0 + (int64_t)k * parts;
+#pragma unroll
+      for (int j = 0; j < (W + 1) / 2; ++j) g[k][j] = zz[k][j] = 0u;
+      if (m >= a.M) continue;
+      if (W == 8 && whole) {
+        const uint4 u = *reinterpret_cast<const uint4*>(dy + m * a.lddy);
+        g[k][0] = u.x; g[k][W / 8] = u.y; g[k][W / 4] = u.z; g[k][W / 2 - W / 8] = u.w;
+        if (act) {
+          const uint4 v = *reinterpret_cast<const uint4*>(z + m * a.ldz);
+          zz[k][0] = v.x; zz[k][W / 8] = v.y; zz[k][W / 4] = v.z; zz[k][W / 2 - W / 8] = v.w;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+          if (c + j < a.N) {
+            g[k][j / 2] |= (uint32_t)dy[m * a.lddy + j] << (16 * (j % 2));
+            if (act) zz[k][j / 2] |= (uint32_t)z[m * a.ldz + j] << (16 * (j % 2));
+          }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < DZ_ROWS; ++k) {
+      const int64_t m = m0 + (int64_t)k * parts;
+      if (m >= a.M) continue;
+      float v[W];
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        v[j] = j % 2 ? bf16_hi(g[k][j / 2]) : bf16_lo(g[k][j / 2]);
+        if (act) v[j] = __fmul_rn(v[j], activation_slope(j % 2 ? bf16_hi(zz[k][j / 2]) : bf16_lo(zz[k][j / 2]), a.act));
+        sum[j] = __fadd_rn(sum[j], v[j]);
+      }
+      if (!dz) continue;
+      uint16_t* d = dz + m * ldd + c;
+      if constexpr (W == 8) {
+        store8(d, v, whole ? 8 : (int)(a.N - c));
+      } else {
+        *d = (uint16_t)pack_bf16(v[0], 0.f);
+      }
+    }
   }
-  if (db_part) db_part[(int64_t)blockIdx.y * a.N + c] = sum;
+  if (!db_part) return;
+#pragma unroll
+  for (int j = 0; j < W; ++j)
+    if (c + j < a.N) db_part[(int64_t)blockIdx.y * pitch + c + j] = sum[j];
 }
 
-__global__ void __launch_bounds__(ET) linear_db_kernel(const float* part, int parts, int64_t N, float* db,
-                                                       int accumulate) {
-  const int64_t c = (int64_t)blockIdx.x * ET + threadIdx.x;
-  if (c >= N) return;
+// Adds the parts in order: 32 columns a CTA, warp w takes parts w, w + 8, ...
+__global__ void __launch_bounds__(256) linear_db_kernel(const float* part, int64_t pitch, int parts, int64_t N, float* db,
+                                                        int accumulate) {
+  pdl_wait();
+  __shared__ float s[8][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t c = (int64_t)blockIdx.x * 32 + lane;
   float v = 0.f;
-  for (int p = 0; p < parts; ++p) v = __fadd_rn(v, part[(int64_t)p * N + c]);
-  db[c] = accumulate ? __fadd_rn(db[c], v) : v;
+  if (c < N) {
+#pragma unroll 8
+    for (int k = warp; k < parts; k += 8) v = __fadd_rn(v, part[(int64_t)k * pitch + c]);
+  }
+  s[warp][lane] = v;
+  __syncthreads();
+  if (warp == 0 && c < N) {
+    for (int k = 1; k < 8; ++k) v = __fadd_rn(v, s[k][lane]);
+    db[c] = accumulate ? __fadd_rn(db[c], v) : v;
+  }
 }
 
 __global__ void __launch_bounds__(ET) linear_zero_kernel(void* p, int dtype, int64_t ld, int64_t rows, int64_t cols) {
@@ -462,7 +577,10 @@ bool make_map(CUtensorMap* map, const Operand& o, bool mn_major, int64_t mn, int
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool tma_rows(const void* p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0; }
+bool rows16(const void* p, int dtype, int64_t ld) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % (dtype ? 4 : 8) == 0;
+}
+bool tma_rows(const void* p, int64_t ld) { return rows16(p, 0, ld); }
 int64_t pad8(int64_t n) { return (n + 7) / 8 * 8; }
 size_t pad256(size_t n) { return (n + 255) & ~(size_t)255; }
 
@@ -501,6 +619,8 @@ cudaError_t gemm(const Operand& a, const Operand& b, int64_t M, int64_t N, int64
   p.k_steps = (int)((K + BK - 1) / BK);
   p.wait_limit = debug_wait_limit();
   p.e = epi;
+  p.e.vec = rows16(epi.y, epi.y_dtype, epi.ldy) && (!epi.z || rows16(epi.z, 0, epi.ldz)) &&
+            (!epi.residual || rows16(epi.residual, 0, epi.ldr));
   const int split = split_for(p.n_tiles, p.k_steps);
   if (split == 1) {
     if (cudaError_t e = set_smem<A_MN, B_MN, false>(); e != cudaSuccess) return e;
@@ -540,8 +660,8 @@ cudaError_t aligned_operand(Operand& o, int64_t rows, int64_t cols, char*& ws, c
 
 size_t copy_bytes(int64_t rows, int64_t cols) { return pad256((size_t)rows * pad8(cols) * 2); }
 
-constexpr int kDbParts = 64;
-size_t db_bytes(int64_t N) { return pad256((size_t)kDbParts * N * sizeof(float)); }
+constexpr int kDbParts = 304;   // most row parts of the bias gradient
+size_t db_bytes(int64_t N) { return pad256((size_t)kDbParts * pad8(N) * sizeof(float)); }
 
 }  // namespace
 
@@ -585,7 +705,6 @@ size_t linear_bwd_workspace_needed(const LinearBwdArgs& a) {
 
 cudaError_t launch_linear_bwd(const LinearBwdArgs& a, cudaStream_t stream) {
   char* ws = static_cast<char*>(a.workspace);
-  const unsigned ncols = (unsigned)((a.N + ET - 1) / ET);
   if (a.M == 0) {   // sums over no rows
     const int64_t cap = (int64_t)sm_count() * 8;
     if (a.dw && !a.accumulate)
@@ -610,12 +729,21 @@ cudaError_t launch_linear_bwd(const LinearBwdArgs& a, cudaStream_t stream) {
       part = reinterpret_cast<float*>(ws);
       ws += db_bytes(a.N);
     }
-    const int parts = (int)(a.M < kDbParts ? a.M : kDbParts);
-    linear_dz_kernel<<<dim3(ncols, parts), ET, 0, stream>>>(a, dst, ld, part, parts);
+    const int64_t pitch = pad8(a.N);
+    const bool vec = tma_rows(a.dy, a.lddy) && (a.act == RLK_ACT_NONE || tma_rows(a.z, a.ldz));
+    const unsigned cols = (unsigned)((a.N + DT * (vec ? 8 : 1) - 1) / (DT * (vec ? 8 : 1)));
+    // about 8 CTAs an SM, each with DZ_ROWS rows or more
+    int64_t parts = ((int64_t)sm_count() * 8 + cols - 1) / cols, most = (a.M + DZ_ROWS - 1) / DZ_ROWS;
+    if (parts > most) parts = most;
+    if (parts > kDbParts) parts = kDbParts;
+    const dim3 grid(cols, (unsigned)parts);
+    if (vec) linear_dz_kernel<8><<<grid, DT, 0, stream>>>(a, dst, ld, part, pitch, (int)parts);
+    else linear_dz_kernel<1><<<grid, DT, 0, stream>>>(a, dst, ld, part, pitch, (int)parts);
     if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
     if (a.db) {
-      linear_db_kernel<<<ncols, ET, 0, stream>>>(part, parts, a.N, a.db, a.accumulate);
-      if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
+      const cudaError_t e = launch_after(linear_db_kernel, dim3((unsigned)((a.N + 31) / 32)), dim3(256), 0, stream,
+                                         (const float*)part, pitch, (int)parts, a.N, a.db, a.accumulate);
+      if (e != cudaSuccess) return e;
     }
   }
   if (a.dx) {   // dx = dz w: K is N, w [N][K] holds its columns contiguously
