@@ -14,9 +14,9 @@
 //    of 16 row tiles, so the CTAs at work share 16 A tiles and about 10 B tiles
 //    in L2.
 //  * Few tiles (a call of few rows is bound by the weight's bytes, and needs
-//    every SM to fetch them): a cluster of 2, 4 or 8 CTAs splits K, leaves its
-//    partial tiles in shared memory, and each CTA adds the cluster's partials
-//    in rank order for its share of the columns.
+//    every SM to fetch them): tiles of 128 x 128, and a cluster of 2 or 4 CTAs
+//    splits K, leaves its partial tiles in shared memory, and each CTA adds the
+//    cluster's partials in rank order for its share of the columns.
 // TMA needs rows that start on 16-byte boundaries; an operand whose rows do not
 // is first copied into the workspace.
 //
@@ -38,16 +38,24 @@
 namespace rlk {
 namespace {
 
-constexpr int BM = 128, BN = 256, BK = 64, STAGES = 4;
+constexpr int BM = 128, BK = 64;
 constexpr int EPI_WARPS = 8, THREADS = 64 + 32 * EPI_WARPS;
-constexpr uint32_t A_BYTES = BM * BK * 2, B_BYTES = BN * BK * 2, STAGE_BYTES = A_BYTES + B_BYTES;
-constexpr uint32_t MN_BLOCK = 64 * BK * 2;   // a 64-element block of an MN-contiguous operand
-constexpr uint32_t TMEM_COLS = 512;
-constexpr uint32_t STAGING = 32 * 32 * 4;    // an epilogue warp's 32 x 32 piece of a tile
-constexpr size_t SMEM_BYTES = STAGES * STAGE_BYTES + EPI_WARPS * STAGING + 1024 + 256;
+constexpr uint32_t MN_BLOCK = 64 * BK * 2;     // a 64-element block of an MN-contiguous operand
+constexpr uint32_t STAGING = 32 * 32 * 4;      // an epilogue warp's 32 x 32 piece of a tile
+constexpr uint32_t RING = 192 * 1024;          // bytes of the stage ring
+constexpr size_t SMEM_BYTES = RING + EPI_WARPS * STAGING + 1024 + 256;
 constexpr int GROUP_M = 16;
-constexpr int PLD = BN + 4;   // row pitch (floats) of a partial tile: conflict-free float4 rows
-static_assert(BM * PLD * 4 <= STAGES * STAGE_BYTES, "a partial tile fits into the ring");
+constexpr int MAX_SPLIT = 4;                   // CTAs that share a tile's K, at most
+// The two tile shapes: 128 x 256 in four stages, 128 x 128 in six.
+template <bool SPLIT>
+struct Shape {
+  static constexpr int BN = SPLIT ? 128 : 256;
+  static constexpr uint32_t A_BYTES = BM * BK * 2, STAGE = A_BYTES + BN * BK * 2;
+  static constexpr int STAGES = (int)(RING / STAGE);
+  static constexpr uint32_t TMEM_COLS = 2 * BN;
+  static constexpr int PLD = BN + 4;           // row pitch (floats) of a partial tile: conflict-free float4 rows
+};
+static_assert(BM * Shape<true>::PLD * 4 <= RING, "a partial tile fits into the ring");
 
 struct Epilogue {
   const void* bias;
@@ -65,7 +73,8 @@ struct Epilogue {
 };
 struct GemmParams {
   int64_t M, N;
-  int n_mt, n_nt, n_tiles, k_steps;
+  int n_mt, n_nt, k_steps;
+  int first_tile, n_tiles;   // tiles [first_tile, n_tiles) of the n_mt x n_nt
   long long wait_limit;
   Epilogue e;
 };
@@ -155,11 +164,11 @@ __device__ __forceinline__ void finish8(const Epilogue& e, int64_t row, int64_t 
   }
 }
 // One column of one row, any alignment.
-__device__ __forceinline__ void finish1(const Epilogue& e, int64_t row, int64_t col, float v, float bias) {
+__device__ __forceinline__ void finish1(const Epilogue& e, int64_t row, int64_t col, float v, float bias, uint16_t res) {
   v = __fadd_rn(v, bias);
   if (e.z) e.z[row * e.ldz + col] = (uint16_t)pack_bf16(v, 0.f);
   if (e.act != RLK_ACT_NONE) v = activate(v, e.act);
-  if (e.residual) v = __fadd_rn(v, bf16_val(e.residual[row * e.ldr + col]));
+  if (e.residual) v = __fadd_rn(v, bf16_val(res));
   if (e.y_dtype == 0) {
     static_cast<uint16_t*>(e.y)[row * e.ldy + col] = (uint16_t)pack_bf16(v, 0.f);
   } else {
@@ -183,12 +192,15 @@ template <bool A_MN, bool B_MN, bool SPLIT>
 __global__ void __launch_bounds__(THREADS, 1)
     linear_gemm_kernel(const __grid_constant__ CUtensorMap map_a,
                        const __grid_constant__ CUtensorMap map_b, const GemmParams p, int cluster) {
+  using S = Shape<SPLIT>;
+  constexpr int BN = S::BN, STAGES = S::STAGES, PLD = S::PLD;
+  constexpr uint32_t A_BYTES = S::A_BYTES, STAGE_BYTES = S::STAGE, TMEM_COLS = S::TMEM_COLS;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* base_ptr = smem_raw + (base - raw);
-  float* staging = reinterpret_cast<float*>(base_ptr + STAGES * STAGE_BYTES);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(base_ptr + STAGES * STAGE_BYTES + EPI_WARPS * STAGING);
+  float* staging = reinterpret_cast<float*>(base_ptr + RING);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(base_ptr + RING + EPI_WARPS * STAGING);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 2 * STAGES + 4);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 5);
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * STAGES;
@@ -213,12 +225,13 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
   if (warp == 1) tc::alloc(smem_u32(tmem_slot), TMEM_COLS);
   tc::fence_before();
+  pdl_wait();   // the operands may come from the kernel before
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = *tmem_slot;
 
   const uint32_t rank = SPLIT ? tc::cluster_rank() : 0u;
-  const int tile0 = SPLIT ? (int)(blockIdx.x / (unsigned)cluster) : (int)blockIdx.x;
+  const int tile0 = p.first_tile + (SPLIT ? (int)(blockIdx.x / (unsigned)cluster) : (int)blockIdx.x);
   const int tile_step = SPLIT ? p.n_tiles : (int)gridDim.x;
   const int k0 = SPLIT ? (int)((int64_t)rank * p.k_steps / cluster) : 0;
   const int k1 = SPLIT ? (int)((int64_t)(rank + 1) * p.k_steps / cluster) : p.k_steps;
@@ -369,9 +382,17 @@ __global__ void __launch_bounds__(THREADS, 1)
         } else if (col0 + lane < p.N) {   // a column a lane: consecutive lanes share lines
           const float b = p.e.bias ? bias_at(p.e, col0 + lane) : 0.f;
           const int rows = (int)(p.M - row0 < 32 ? p.M - row0 : 32);
+#pragma unroll 1
+          for (int r0 = 0; r0 < rows; r0 += 8) {
+            uint16_t rv[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              rv[k] = p.e.residual && r0 + k < rows ? p.e.residual[(row0 + r0 + k) * p.e.ldr + col0 + lane] : 0;
 #pragma unroll 4
-          for (int r = 0; r < rows; ++r)
-            finish1(p.e, row0 + r, col0 + lane, st[r * 32 + (((lane >> 2) ^ (r & 7)) << 2) + (lane & 3)], b);
+            for (int k = 0; k < 8; ++k)
+              if (r0 + k < rows)
+                finish1(p.e, row0 + r0 + k, col0 + lane, st[(r0 + k) * 32 + (((lane >> 2) ^ k) << 2) + (lane & 3)], b, rv[k]);
+          }
         }
         __syncwarp();
       }
@@ -405,13 +426,22 @@ __global__ void __launch_bounds__(THREADS, 1)
           v[j] = 0.f;
         }
         const uint32_t at = base + (uint32_t)(r * PLD + c0 + c) * 4u;
-        for (int k = 0; k < cluster; ++k) {
-          const uint32_t peer = tc::peer_addr(at, (uint32_t)k);
-          const float4 a = tc::ld_peer4(peer), b = tc::ld_peer4(peer + 16u);
-          const float o[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        float4 part[2 * MAX_SPLIT];   // all in flight together
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] = __fadd_rn(v[j], o[j]);
-        }
+        for (int k = 0; k < MAX_SPLIT; ++k)
+          if (k < cluster) {
+            const uint32_t peer = tc::peer_addr(at, (uint32_t)k);
+            part[2 * k] = tc::ld_peer4(peer);
+            part[2 * k + 1] = tc::ld_peer4(peer + 16u);
+          }
+#pragma unroll
+        for (int k = 0; k < MAX_SPLIT; ++k)
+          if (k < cluster) {
+            const float4 a = part[2 * k], b = part[2 * k + 1];
+            const float o[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = __fadd_rn(v[j], o[j]);
+          }
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = dead ? NAN : v[j];
         finish8(p.e, row0 + r, col, n, v, bias, res);
@@ -422,9 +452,15 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int64_t col = col0 + c;
         if (col >= p.N) continue;
         const uint32_t at = base + (uint32_t)(r * PLD + c0 + c) * 4u;
-        float v = 0.f;
-        for (int k = 0; k < cluster; ++k) v = __fadd_rn(v, tc::ld_peer_f32(tc::peer_addr(at, (uint32_t)k)));
-        finish1(p.e, row0 + r, col, dead ? NAN : v, p.e.bias ? bias_at(p.e, col) : 0.f);
+        const uint16_t res = p.e.residual ? p.e.residual[(row0 + r) * p.e.ldr + col] : 0;
+        float part[MAX_SPLIT], v = 0.f;
+#pragma unroll
+        for (int k = 0; k < MAX_SPLIT; ++k)
+          if (k < cluster) part[k] = tc::ld_peer_f32(tc::peer_addr(at, (uint32_t)k));
+#pragma unroll
+        for (int k = 0; k < MAX_SPLIT; ++k)
+          if (k < cluster) v = __fadd_rn(v, part[k]);
+        finish1(p.e, row0 + r, col, dead ? NAN : v, p.e.bias ? bias_at(p.e, col) : 0.f, res);
       }
     }
     tc::cluster_sync();   // no CTA leaves while its shared memory is read
@@ -435,14 +471,108 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (warp == 1) tc::dealloc(tmem, TMEM_COLS);
 }
 
+// ------------------------------------------------------------ a few rows
+// Up to GEMV_ROWS rows: the weight's bytes bound the call and a tile of 128
+// rows would be almost empty, so each output feature is a dot product of its
+// own.  `wpf` warps share a feature (each takes every wpf-th piece of K), as
+// many as it takes to give every SM 32 warps; 16-byte loads, 8 in flight a lane.  Their
+// sums are joined in a fixed order.
+constexpr int GEMV_ROWS = 4, GEMV_T = 256;
+
+template <int R, bool VEC>
+__global__ void __launch_bounds__(GEMV_T) linear_gemv_kernel(const uint16_t* x, int64_t ldx, const uint16_t* w,
+                                                             int64_t ldw, int64_t N, int K, int wpf, Epilogue e) {
+  pdl_wait();
+  __shared__ float s_part[GEMV_T / 32][R];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp & (wpf - 1);
+  const int64_t f = (int64_t)blockIdx.x * (GEMV_T / 32 / wpf) + warp / wpf;
+  float acc[R];
+#pragma unroll
+  for (int m = 0; m < R; ++m) acc[m] = 0.f;
+  if (f < N) {
+    const uint16_t* wf = w + f * ldw;
+    if (VEC) {
+      constexpr int U = R == 1 ? 8 : 4;
+      for (int k0 = (part * 32 + lane) * 8; k0 < K; k0 += wpf * 256 * U) {
+        uint4 a[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int k = k0 + u * wpf * 256;
+          a[u] = k + 8 <= K ? __ldcs(reinterpret_cast<const uint4*>(wf + k)) : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int k = k0 + u * wpf * 256;
+          if (k + 8 > K) continue;
+          const uint32_t aw[4] = {a[u].x, a[u].y, a[u].z, a[u].w};
+#pragma unroll
+          for (int m = 0; m < R; ++m) {
+            const uint4 b = *reinterpret_cast<const uint4*>(x + m * ldx + k);
+            const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              acc[m] = __fmaf_rn(bf16_lo(aw[j]), bf16_lo(bw[j]), acc[m]);
+              acc[m] = __fmaf_rn(bf16_hi(aw[j]), bf16_hi(bw[j]), acc[m]);
+            }
+          }
+        }
+      }
+      const int k = (K & ~7) + lane;   // the last K % 8 columns
+      if (part == 0 && k < K) {
+#pragma unroll
+        for (int m = 0; m < R; ++m) acc[m] = __fmaf_rn(bf16_val(wf[k]), bf16_val(x[m * ldx + k]), acc[m]);
+      }
+    } else {
+#pragma unroll 8
+      for (int k = part * 32 + lane; k < K; k += wpf * 32) {
+        const float a = bf16_val(wf[k]);
+#pragma unroll
+        for (int m = 0; m < R; ++m) acc[m] = __fmaf_rn(a, bf16_val(x[m * ldx + k]), acc[m]);
+      }
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < R; ++m) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) acc[m] = __fadd_rn(acc[m], __shfl_xor_sync(0xFFFFFFFFu, acc[m], o));
+    if (lane == 0) s_part[warp][m] = acc[m];
+  }
+  __syncthreads();
+  if (part != 0 || f >= N || lane >= R) return;
+  float v = 0.f;
+  for (int k = 0; k < wpf; ++k) v = __fadd_rn(v, s_part[warp + k][lane]);
+  finish1(e, lane, f, v, e.bias ? bias_at(e, f) : 0.f, e.residual ? e.residual[lane * e.ldr + f] : 0);
+}
+
 // ------------------------------------------------------------ around the products
 constexpr int ET = 256;
 
-// A bf16 matrix copied to rows that start on 16-byte boundaries.
-__global__ void __launch_bounds__(ET) repack_kernel(const uint16_t* src, int64_t ld, int64_t rows, int64_t cols,
-                                                    uint16_t* dst, int64_t ldd) {
-  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
-    for (int64_t c = threadIdx.x; c < cols; c += ET) dst[r * ldd + c] = src[r * ld + c];
+// bf16 matrices copied to rows that start on 16-byte boundaries: a warp a row, 8
+// columns a lane.
+struct Repack {
+  const uint16_t* src;
+  int64_t ld, rows, cols;
+  uint16_t* dst;
+  int64_t ldd;
+};
+__global__ void __launch_bounds__(ET) repack_kernel(Repack a, Repack b) {
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  for (int64_t r = (int64_t)blockIdx.x * (ET / 32) + (threadIdx.x >> 5); r < a.rows + b.rows;
+       r += (int64_t)gridDim.x * (ET / 32)) {
+    const bool first = r < a.rows;
+    const int64_t row = first ? r : r - a.rows, cols = first ? a.cols : b.cols;
+    const uint16_t* src = first ? a.src + row * a.ld : b.src + row * b.ld;
+    uint16_t* dst = first ? a.dst + row * a.ldd : b.dst + row * b.ldd;
+#pragma unroll 2
+    for (int64_t c = lane * 8; c < cols; c += 256) {
+      uint32_t w[4] = {0u, 0u, 0u, 0u};   // columns past the end are filled with zeros
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (c + j < cols) w[j / 2] |= (uint32_t)src[c + j] << (16 * (j % 2));
+      *reinterpret_cast<uint4*>(dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
 }
 
 // dz = dy act'(z) as bf16 and the partial column sums of the unrounded dz: part
@@ -584,14 +714,6 @@ bool tma_rows(const void* p, int64_t ld) { return rows16(p, 0, ld); }
 int64_t pad8(int64_t n) { return (n + 7) / 8 * 8; }
 size_t pad256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-// CTAs that share a tile's K: as many (2, 4, 8) as keep the grid within the
-// SMs and leave each at least four stages.
-int split_for(int tiles, int k_steps) {
-  int s = 1;
-  while (s < 8 && tiles * 2 * s <= sm_count() && k_steps >= 8 * s) s *= 2;
-  return s;
-}
-
 template <bool A_MN, bool B_MN, bool SPLIT>
 cudaError_t set_smem() {
   static std::atomic<int> done[64];
@@ -603,62 +725,106 @@ cudaError_t set_smem() {
   return e;
 }
 
+// CTAs that share a tile's K when `tiles` tiles are left for all SMs: 4 or 2
+// where the SMs allow it and each keeps at least four stages of K.
+int split_for(int tiles, int k_steps) {
+  int s = 1;
+  while (s < MAX_SPLIT && tiles * 2 * s <= sm_count() && k_steps >= 8 * s) s *= 2;
+  return s;
+}
+
+// One launch over tiles [p.first_tile, p.n_tiles), as a programmatic dependent
+// of the kernel before it.
+template <bool A_MN, bool B_MN, bool SPLIT>
+cudaError_t launch_gemm(const CUtensorMap& ma, const CUtensorMap& mb, const GemmParams& p, int split,
+                        cudaStream_t stream) {
+  if (cudaError_t e = set_smem<A_MN, B_MN, SPLIT>(); e != cudaSuccess) return e;
+  const int tiles = p.n_tiles - p.first_tile;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(SPLIT ? tiles * split : (tiles < sm_count() ? tiles : sm_count())));
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = SMEM_BYTES;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)split;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = SPLIT ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, linear_gemm_kernel<A_MN, B_MN, SPLIT>, ma, mb, p, split);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 template <bool A_MN, bool B_MN>
 cudaError_t gemm(const Operand& a, const Operand& b, int64_t M, int64_t N, int64_t K, const Epilogue& epi,
                  cudaStream_t stream) {
-  CUtensorMap ma, mb;
-  if (!make_map(&ma, a, A_MN, M, K, BM) || !make_map(&mb, b, B_MN, N, K, BN)) return cudaErrorInvalidValue;
   GemmParams p{};
   p.M = M;
   p.N = N;
   p.n_mt = (int)((M + BM - 1) / BM);
-  p.n_nt = (int)((N + BN - 1) / BN);
-  const int64_t tiles = (int64_t)p.n_mt * p.n_nt;
-  if (tiles > (1 << 30)) return cudaErrorInvalidValue;
-  p.n_tiles = (int)tiles;
   p.k_steps = (int)((K + BK - 1) / BK);
   p.wait_limit = debug_wait_limit();
   p.e = epi;
   p.e.vec = rows16(epi.y, epi.y_dtype, epi.ldy) && (!epi.z || rows16(epi.z, 0, epi.ldz)) &&
             (!epi.residual || rows16(epi.residual, 0, epi.ldr));
-  const int split = split_for(p.n_tiles, p.k_steps);
-  if (split == 1) {
-    if (cudaError_t e = set_smem<A_MN, B_MN, false>(); e != cudaSuccess) return e;
-    const int grid = p.n_tiles < sm_count() ? p.n_tiles : sm_count();
-    linear_gemm_kernel<A_MN, B_MN, false><<<grid, THREADS, SMEM_BYTES, stream>>>(ma, mb, p, 1);
-    return cudaGetLastError();
+  const int64_t wide = (int64_t)p.n_mt * ((N + 255) / 256);
+  if (wide > (1 << 30)) return cudaErrorInvalidValue;
+  // Tiles of 128 x 256 that would leave half of the SMs idle: tiles of 128 x 128
+  // instead, with K split over a cluster while SMs are left.
+  const bool few = 2 * wide <= sm_count();
+  CUtensorMap ma, mb;
+  if (!make_map(&ma, a, A_MN, M, K, BM) || !make_map(&mb, b, B_MN, N, K, few ? 128 : 256)) return cudaErrorInvalidValue;
+  if (!few) {
+    p.n_nt = (int)((N + 255) / 256);
+    p.n_tiles = (int)wide;
+    return launch_gemm<A_MN, B_MN, false>(ma, mb, p, 1, stream);
   }
-  if (cudaError_t e = set_smem<A_MN, B_MN, true>(); e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(p.n_tiles * split));
-  cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = SMEM_BYTES;
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)split;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, linear_gemm_kernel<A_MN, B_MN, true>, ma, mb, p, split);
-  return e != cudaSuccess ? e : cudaGetLastError();
-}
-
-// The operand itself when TMA can read it, else its copy at *ws (advanced).
-cudaError_t aligned_operand(Operand& o, int64_t rows, int64_t cols, char*& ws, cudaStream_t stream) {
-  if (tma_rows(o.p, o.ld)) return cudaSuccess;
-  uint16_t* dst = reinterpret_cast<uint16_t*>(ws);
-  const int64_t ld = pad8(cols);
-  ws += pad256((size_t)rows * ld * 2);
-  const int64_t cap = (int64_t)sm_count() * 8;
-  repack_kernel<<<(unsigned)(rows < cap ? rows : cap), ET, 0, stream>>>(static_cast<const uint16_t*>(o.p), o.ld, rows,
-                                                                       cols, dst, ld);
-  o = Operand{dst, ld};
-  return cudaGetLastError();
+  p.n_nt = (int)((N + 127) / 128);
+  p.n_tiles = p.n_mt * p.n_nt;
+  return launch_gemm<A_MN, B_MN, true>(ma, mb, p, split_for(p.n_tiles, p.k_steps), stream);
 }
 
 size_t copy_bytes(int64_t rows, int64_t cols) { return pad256((size_t)rows * pad8(cols) * 2); }
+
+template <int R>
+cudaError_t gemv_rows(const LinearArgs& a, const Epilogue& e, cudaStream_t stream) {
+  const bool vec = tma_rows(a.x, a.ldx) && tma_rows(a.w, a.ldw);
+  const int64_t warps = (int64_t)sm_count() * 32, least = vec ? 512 : 64;   // columns of K that are worth a warp
+  int wpf = 1;
+  while (wpf < GEMV_T / 32 && a.N * wpf * 2 <= warps && a.K >= least * wpf * 2) wpf *= 2;
+  const dim3 grid((unsigned)((a.N * wpf + GEMV_T / 32 - 1) / (GEMV_T / 32)));
+  const uint16_t* x = static_cast<const uint16_t*>(a.x);
+  const uint16_t* w = static_cast<const uint16_t*>(a.w);
+  const cudaError_t err =
+      vec ? launch_after(linear_gemv_kernel<R, true>, grid, dim3(GEMV_T), 0, stream, x, a.ldx, w, a.ldw, a.N, (int)a.K, wpf, e)
+          : launch_after(linear_gemv_kernel<R, false>, grid, dim3(GEMV_T), 0, stream, x, a.ldx, w, a.ldw, a.N, (int)a.K, wpf, e);
+  return err != cudaSuccess ? err : cudaGetLastError();
+}
+
+// Up to two operands whose rows TMA cannot read are replaced by copies at *ws
+// (advanced), made in one launch.
+struct Copied {
+  Operand* o;
+  int64_t rows, cols;
+};
+cudaError_t aligned_operands(Copied x, Copied w, char*& ws, cudaStream_t stream) {
+  Repack r[2] = {};
+  int n = 0;
+  for (const Copied& c : {x, w}) {
+    if (!c.o || tma_rows(c.o->p, c.o->ld)) continue;
+    uint16_t* dst = reinterpret_cast<uint16_t*>(ws);
+    ws += copy_bytes(c.rows, c.cols);
+    r[n++] = Repack{static_cast<const uint16_t*>(c.o->p), c.o->ld, c.rows, c.cols, dst, pad8(c.cols)};
+    *c.o = Operand{dst, pad8(c.cols)};
+  }
+  if (n == 0) return cudaSuccess;
+  const int64_t want = (r[0].rows + r[1].rows + ET / 32 - 1) / (ET / 32), cap = (int64_t)sm_count() * 16;
+  const cudaError_t e = launch_after(repack_kernel, dim3((unsigned)(want < cap ? want : cap)), dim3(ET), 0, stream, r[0], r[1]);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
 
 constexpr int kDbParts = 304;   // most row parts of the bias gradient
 size_t db_bytes(int64_t N) { return pad256((size_t)kDbParts * pad8(N) * sizeof(float)); }
@@ -668,14 +834,13 @@ size_t db_bytes(int64_t N) { return pad256((size_t)kDbParts * pad8(N) * sizeof(f
 size_t linear_workspace_bytes(int64_t M, int64_t N, int64_t K) { return copy_bytes(M, K) + copy_bytes(N, K); }
 
 size_t linear_workspace_needed(const LinearArgs& a) {
+  if (a.M <= GEMV_ROWS) return 0;
   return (tma_rows(a.x, a.ldx) ? 0 : copy_bytes(a.M, a.K)) + (tma_rows(a.w, a.ldw) ? 0 : copy_bytes(a.N, a.K));
 }
 
 cudaError_t launch_linear_fwd(const LinearArgs& a, cudaStream_t stream) {
   char* ws = static_cast<char*>(a.workspace);
   Operand x{a.x, a.ldx}, w{a.w, a.ldw};
-  if (cudaError_t e = aligned_operand(x, a.M, a.K, ws, stream); e != cudaSuccess) return e;
-  if (cudaError_t e = aligned_operand(w, a.N, a.K, ws, stream); e != cudaSuccess) return e;
   Epilogue e{};
   e.bias = a.bias;
   e.bias_dtype = a.bias_dtype;
@@ -687,6 +852,14 @@ cudaError_t launch_linear_fwd(const LinearArgs& a, cudaStream_t stream) {
   e.ldy = a.ldy;
   e.z = static_cast<uint16_t*>(a.z);
   e.ldz = a.ldz;
+  switch (a.M) {
+    case 1: return gemv_rows<1>(a, e, stream);
+    case 2: return gemv_rows<2>(a, e, stream);
+    case 3: return gemv_rows<3>(a, e, stream);
+    case GEMV_ROWS: return gemv_rows<GEMV_ROWS>(a, e, stream);
+    default: break;
+  }
+  if (cudaError_t err = aligned_operands({&x, a.M, a.K}, {&w, a.N, a.K}, ws, stream); err != cudaSuccess) return err;
   return gemm<false, false>(x, w, a.M, a.N, a.K, e, stream);
 }
 
@@ -746,9 +919,11 @@ cudaError_t launch_linear_bwd(const LinearBwdArgs& a, cudaStream_t stream) {
       if (e != cudaSuccess) return e;
     }
   }
+  Operand w{a.w, a.ldw}, x{a.x, a.ldx};
+  if (cudaError_t e = aligned_operands({a.dx ? &w : nullptr, a.N, a.K}, {a.dw && a.x ? &x : nullptr, a.M, a.K}, ws, stream);
+      e != cudaSuccess)
+    return e;
   if (a.dx) {   // dx = dz w: K is N, w [N][K] holds its columns contiguously
-    Operand w{a.w, a.ldw};
-    if (cudaError_t e = aligned_operand(w, a.N, a.K, ws, stream); e != cudaSuccess) return e;
     Epilogue e{};
     e.y = a.dx;
     e.y_dtype = a.dx_dtype;
@@ -756,8 +931,7 @@ cudaError_t launch_linear_bwd(const LinearBwdArgs& a, cudaStream_t stream) {
     if (cudaError_t er = gemm<false, true>(dz, w, a.M, a.K, a.N, e, stream); er != cudaSuccess) return er;
   }
   if (a.dw) {   // dw = dz^T x: K is M, both operands hold M / N contiguously
-    Operand x{a.x, a.ldx};
-    if (a.ck.codes) {   // the checkpoint's values are exact in bf16
+    if (!a.x) {   // the checkpoint's values are exact in bf16
       const int64_t ld = pad8(a.K);
       CheckpointArgs c{};
       c.x = ws;
@@ -768,8 +942,6 @@ cudaError_t launch_linear_bwd(const LinearBwdArgs& a, cudaStream_t stream) {
       if (cudaError_t e = launch_checkpoint_unpack(c, stream); e != cudaSuccess) return e;
       x = Operand{ws, ld};
       ws += copy_bytes(a.M, a.K);
-    } else {
-      if (cudaError_t e = aligned_operand(x, a.M, a.K, ws, stream); e != cudaSuccess) return e;
     }
     Epilogue e{};
     e.y = a.dw;

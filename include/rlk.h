@@ -960,8 +960,8 @@ typedef enum {
  *                  itself (same address and stride, bf16).
  *  z               device bf16, M x ldz elements (ldz >= N), or NULL: the
  *                  pre-activation, for rlk_linear_bwd.
- *  workspace       aligned copies of x and w when their rows do not start on
- *                  16-byte boundaries (base and stride): then at least
+ *  workspace       aligned copies of x and w when M > 4 and their rows do not
+ *                  start on 16-byte boundaries (base and stride): then at least
  *                  rlk_workspace_size(RLK_OP_LINEAR, M, N, K) bytes serve, 16-byte
  *                  aligned, contents on entry do not matter; else it may be NULL.
  * Deterministic.  Calls of few rows split K over several CTAs, so a row's last

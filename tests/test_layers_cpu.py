@@ -143,7 +143,7 @@ def test_preference_binding_refuses():
 
 
 def lin(lib, **kw):
-    a = dict(x=FAKE, ldx=64, w=FAKE, ldw=64, b=FAKE, bd=1, r=FAKE, ldr=32, M=4, N=32, K=64, act=1, y=FAKE, yd=0, ldy=32,
+    a = dict(x=FAKE, ldx=64, w=FAKE, ldw=64, b=FAKE, bd=1, r=FAKE, ldr=32, M=5, N=32, K=64, act=1, y=FAKE, yd=0, ldy=32,
              z=FAKE, ldz=32, ws=None, wsb=0)
     a.update(kw)
     return lib.rlk_linear_fwd(a["x"], a["ldx"], a["w"], a["ldw"], a["b"], a["bd"], a["r"], a["ldr"], a["M"], a["N"], a["K"],
@@ -161,7 +161,7 @@ def test_linear_rejects(lib, armed, kw):
 
 def test_linear_workspace_and_accepts(lib, armed):
     assert lin(lib) == 4 and lin(lib, b=None, r=None, z=None, ldr=0, ldz=0) == 4 and lin(lib, M=0, x=None, w=None, y=None) == 0
-    need = lib.rlk_workspace_size(rlk.OP_LINEAR, 4, 32, 64)
+    need = lib.rlk_workspace_size(rlk.OP_LINEAR, 5, 32, 64)
     for odd in (dict(x=ctypes.c_void_p(0x10002)), dict(ldx=65), dict(ldw=66)):
         assert lin(lib, **odd) == 3 and lin(lib, **odd, ws=FAKE, wsb=need) == 4
         assert lin(lib, **odd, ws=ctypes.c_void_p(0x10008), wsb=need) == 3 and lin(lib, **odd, ws=FAKE, wsb=16) == 3
