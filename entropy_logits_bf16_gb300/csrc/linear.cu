@@ -79,21 +79,52 @@ struct GemmParams {
   Epilogue e;
 };
 
-__device__ __forceinline__ float activate(float z, int act) {
-  if (act == RLK_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
-  if (act == RLK_ACT_SILU) return __fdiv_rn(z, 1.f + expf(-z));
-  if (act == RLK_ACT_RELU) return z < 0.f ? 0.f : z;
-  return z;
+// 1 / v to 2^-22 or so (MUFU), enough for what is rounded to bf16 or compared
+// at a few 2^-24 of |z| + 1.
+__device__ __forceinline__ float rcp(float v) { return __fdividef(1.f, v); }
+
+// Phi(-|z|), Phi the normal distribution function: 1/2 erfc(|z| / sqrt 2) by
+// Abramowitz and Stegun 7.1.26, erfc(x) = (a1 t + ... + a5 t^5) exp(-x^2) with t = 1 / (1 + p x)
+// (absolute error 1.5e-7).  About 13 instructions; the product with the exponential keeps
+// the far tail free of cancellation.
+__device__ __forceinline__ float normal_tail(float z) {
+  const float x = fabsf(z) * 0.70710678118654752f;
+  const float t = rcp(__fmaf_rn(0.3275911f, x, 1.f));
+  float q = __fmaf_rn(1.061405429f, t, -1.453152027f);
+  q = __fmaf_rn(q, t, 1.421413741f);
+  q = __fmaf_rn(q, t, -0.284496736f);
+  q = __fmaf_rn(q, t, 0.254829592f);
+  return 0.5f * (q * t) * ex2(-(x * x) * kLog2e);
 }
-__device__ __forceinline__ float activation_slope(float z, int act) {
-  if (act == RLK_ACT_GELU)
+// act of W values; the choice is made once.
+template <int W>
+__device__ __forceinline__ void activate(float (&v)[W], int act) {
+  if (act == RLK_ACT_GELU) {
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      const float tail = v[j] * normal_tail(v[j]);
+      v[j] = v[j] > 0.f ? __fsub_rn(v[j], tail) : tail;
+    }
+  } else if (act == RLK_ACT_SILU) {
+#pragma unroll
+    for (int j = 0; j < W; ++j) v[j] = v[j] * rcp(1.f + ex2(-v[j] * kLog2e));
+  } else if (act == RLK_ACT_RELU) {
+#pragma unroll
+    for (int j = 0; j < W; ++j) v[j] = v[j] < 0.f ? 0.f : v[j];
+  }
+}
+// act'(z), to full fp32 accuracy: it goes into sums that stay in fp32.
+template <int ACT>
+__device__ __forceinline__ float activation_slope(float z) {
+  if (ACT == RLK_ACT_GELU)
     return 0.5f * (1.f + erff(z * 0.70710678118654752f)) +
            z * expf(-0.5f * z * z) * 0.39894228040143268f;
-  if (act == RLK_ACT_SILU) {
+  if (ACT == RLK_ACT_SILU) {
     const float s = 1.f / (1.f + expf(-z));
     return s * (1.f + z * (1.f - s));
   }
-  return z > 0.f ? 1.f : (z != z ? z : 0.f);   // ReLU
+  if (ACT == RLK_ACT_RELU) return z > 0.f ? 1.f : (z != z ? z : 0.f);
+  return 1.f;
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
@@ -130,10 +161,7 @@ __device__ __forceinline__ void finish8(const Epilogue& e, int64_t row, int64_t 
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] = __fadd_rn(v[j], bias[j]);
   if (e.z) store8(e.z + row * e.ldz + col, v, n);
-  if (e.act != RLK_ACT_NONE) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = activate(v[j], e.act);
-  }
+  activate(v, e.act);
   if (e.residual) {
     const uint32_t w[4] = {res.x, res.y, res.z, res.w};
 #pragma unroll
@@ -163,18 +191,40 @@ __device__ __forceinline__ void finish8(const Epilogue& e, int64_t row, int64_t 
       if (j < n) y[j] = e.accumulate ? __fadd_rn(y[j], v[j]) : v[j];
   }
 }
-// One column of one row, any alignment.
-__device__ __forceinline__ void finish1(const Epilogue& e, int64_t row, int64_t col, float v, float bias, uint16_t res) {
-  v = __fadd_rn(v, bias);
-  if (e.z) e.z[row * e.ldz + col] = (uint16_t)pack_bf16(v, 0.f);
-  if (e.act != RLK_ACT_NONE) v = activate(v, e.act);
-  if (e.residual) v = __fadd_rn(v, bf16_val(res));
+// One column of R rows from `row` on, any alignment; n of the rows exist.
+template <int R>
+__device__ __forceinline__ void finish_rows(const Epilogue& e, int64_t row, int n, int64_t col, float (&v)[R], float bias,
+                                            const uint16_t (&res)[R]) {
+#pragma unroll
+  for (int k = 0; k < R; ++k) v[k] = __fadd_rn(v[k], bias);
+  if (e.z) {
+    uint16_t* z = e.z + row * e.ldz + col;
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+      if (k < n) z[k * e.ldz] = (uint16_t)pack_bf16(v[k], 0.f);
+  }
+  activate(v, e.act);
+  if (e.residual) {
+#pragma unroll
+    for (int k = 0; k < R; ++k) v[k] = __fadd_rn(v[k], bf16_val(res[k]));
+  }
   if (e.y_dtype == 0) {
-    static_cast<uint16_t*>(e.y)[row * e.ldy + col] = (uint16_t)pack_bf16(v, 0.f);
+    uint16_t* y = static_cast<uint16_t*>(e.y) + row * e.ldy + col;
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+      if (k < n) y[k * e.ldy] = (uint16_t)pack_bf16(v[k], 0.f);
   } else {
     float* y = static_cast<float*>(e.y) + row * e.ldy + col;
-    *y = e.accumulate ? __fadd_rn(*y, v) : v;
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+      if (k < n) y[k * e.ldy] = e.accumulate ? __fadd_rn(y[k * e.ldy], v[k]) : v[k];
   }
+}
+template <int R>
+__device__ __forceinline__ void residual_rows(const Epilogue& e, int64_t row, int n, int64_t col, uint16_t (&res)[R]) {
+  const uint16_t* p = e.residual + row * e.ldr + col;
+#pragma unroll
+  for (int k = 0; k < R; ++k) res[k] = e.residual && k < n ? p[k * e.ldr] : 0;
 }
 
 // Tile t -> (row tile, column tile): groups of GROUP_M row tiles, row tiles
@@ -382,16 +432,18 @@ __global__ void __launch_bounds__(THREADS, 1)
         } else if (col0 + lane < p.N) {   // a column a lane: consecutive lanes share lines
           const float b = p.e.bias ? bias_at(p.e, col0 + lane) : 0.f;
           const int rows = (int)(p.M - row0 < 32 ? p.M - row0 : 32);
+          uint16_t next[8], res8[8];   // the residual of the next rows is on its way
+          residual_rows(p.e, row0, rows, col0 + lane, next);
 #pragma unroll 1
           for (int r0 = 0; r0 < rows; r0 += 8) {
-            uint16_t rv[8];
+            float o[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              rv[k] = p.e.residual && r0 + k < rows ? p.e.residual[(row0 + r0 + k) * p.e.ldr + col0 + lane] : 0;
-#pragma unroll 4
-            for (int k = 0; k < 8; ++k)
-              if (r0 + k < rows)
-                finish1(p.e, row0 + r0 + k, col0 + lane, st[(r0 + k) * 32 + (((lane >> 2) ^ k) << 2) + (lane & 3)], b, rv[k]);
+            for (int k = 0; k < 8; ++k) {
+              res8[k] = next[k];
+              o[k] = st[(r0 + k) * 32 + (((lane >> 2) ^ k) << 2) + (lane & 3)];
+            }
+            residual_rows(p.e, row0 + r0 + 8, rows - r0 - 8, col0 + lane, next);
+            finish_rows(p.e, row0 + r0, rows - r0, col0 + lane, o, b, res8);
           }
         }
         __syncwarp();
@@ -452,15 +504,17 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int64_t col = col0 + c;
         if (col >= p.N) continue;
         const uint32_t at = base + (uint32_t)(r * PLD + c0 + c) * 4u;
-        const uint16_t res = p.e.residual ? p.e.residual[(row0 + r) * p.e.ldr + col] : 0;
-        float part[MAX_SPLIT], v = 0.f;
+        uint16_t res[1];
+        residual_rows(p.e, row0 + r, 1, col, res);
+        float part[MAX_SPLIT], v[1] = {0.f};
 #pragma unroll
         for (int k = 0; k < MAX_SPLIT; ++k)
           if (k < cluster) part[k] = tc::ld_peer_f32(tc::peer_addr(at, (uint32_t)k));
 #pragma unroll
         for (int k = 0; k < MAX_SPLIT; ++k)
-          if (k < cluster) v = __fadd_rn(v, part[k]);
-        finish1(p.e, row0 + r, col, dead ? NAN : v, p.e.bias ? bias_at(p.e, col) : 0.f, res);
+          if (k < cluster) v[0] = __fadd_rn(v[0], part[k]);
+        if (dead) v[0] = NAN;
+        finish_rows(p.e, row0 + r, 1, col, v, p.e.bias ? bias_at(p.e, col) : 0.f, res);
       }
     }
     tc::cluster_sync();   // no CTA leaves while its shared memory is read
@@ -539,9 +593,11 @@ __global__ void __launch_bounds__(GEMV_T) linear_gemv_kernel(const uint16_t* x, 
   }
   __syncthreads();
   if (part != 0 || f >= N || lane >= R) return;
-  float v = 0.f;
-  for (int k = 0; k < wpf; ++k) v = __fadd_rn(v, s_part[warp + k][lane]);
-  finish1(e, lane, f, v, e.bias ? bias_at(e, f) : 0.f, e.residual ? e.residual[lane * e.ldr + f] : 0);
+  float v[1] = {0.f};
+  for (int k = 0; k < wpf; ++k) v[0] = __fadd_rn(v[0], s_part[warp + k][lane]);
+  uint16_t res[1];
+  residual_rows(e, lane, 1, f, res);
+  finish_rows(e, lane, 1, f, v, e.bias ? bias_at(e, f) : 0.f, res);
 }
 
 // ------------------------------------------------------------ around the products
@@ -581,14 +637,15 @@ __global__ void __launch_bounds__(ET) repack_kernel(Repack a, Repack b) {
 // flight.  Bound by memory (6 bytes an element).
 constexpr int DT = 128, DZ_ROWS = 4;
 
-template <int W>
+template <int W, int ACT>
 __global__ void __launch_bounds__(DT) linear_dz_kernel(LinearBwdArgs a, uint16_t* dz, int64_t ldd, float* db_part,
                                                        int64_t pitch, int parts) {
   const int64_t c = ((int64_t)blockIdx.x * DT + threadIdx.x) * W;
   if (c >= a.N) return;
   const uint16_t* dy = static_cast<const uint16_t*>(a.dy) + c;
   const uint16_t* z = static_cast<const uint16_t*>(a.z) + c;
-  const bool whole = W == 1 || c + W <= a.N, act = a.act != RLK_ACT_NONE;
+  const bool whole = W == 1 || c + W <= a.N;
+  constexpr bool act = ACT != RLK_ACT_NONE;
   float sum[W];
 #pragma unroll
   for (int j = 0; j < W; ++j) sum[j] = 0.f;
@@ -624,7 +681,7 @@ __global__ void __launch_bounds__(DT) linear_dz_kernel(LinearBwdArgs a, uint16_t
 #pragma unroll
       for (int j = 0; j < W; ++j) {
         v[j] = j % 2 ? bf16_hi(g[k][j / 2]) : bf16_lo(g[k][j / 2]);
-        if (act) v[j] = __fmul_rn(v[j], activation_slope(j % 2 ? bf16_hi(zz[k][j / 2]) : bf16_lo(zz[k][j / 2]), a.act));
+        if (act) v[j] = __fmul_rn(v[j], activation_slope<ACT>(j % 2 ? bf16_hi(zz[k][j / 2]) : bf16_lo(zz[k][j / 2])));
         sum[j] = __fadd_rn(sum[j], v[j]);
       }
       if (!dz) continue;
@@ -910,8 +967,15 @@ cudaError_t launch_linear_bwd(const LinearBwdArgs& a, cudaStream_t stream) {
     if (parts > most) parts = most;
     if (parts > kDbParts) parts = kDbParts;
     const dim3 grid(cols, (unsigned)parts);
-    if (vec) linear_dz_kernel<8><<<grid, DT, 0, stream>>>(a, dst, ld, part, pitch, (int)parts);
-    else linear_dz_kernel<1><<<grid, DT, 0, stream>>>(a, dst, ld, part, pitch, (int)parts);
+    auto kernel = vec ? (a.act == RLK_ACT_GELU   ? linear_dz_kernel<8, RLK_ACT_GELU>
+                         : a.act == RLK_ACT_SILU ? linear_dz_kernel<8, RLK_ACT_SILU>
+                         : a.act == RLK_ACT_RELU ? linear_dz_kernel<8, RLK_ACT_RELU>
+                                                 : linear_dz_kernel<8, RLK_ACT_NONE>)
+                      : (a.act == RLK_ACT_GELU   ? linear_dz_kernel<1, RLK_ACT_GELU>
+                         : a.act == RLK_ACT_SILU ? linear_dz_kernel<1, RLK_ACT_SILU>
+                         : a.act == RLK_ACT_RELU ? linear_dz_kernel<1, RLK_ACT_RELU>
+                                                 : linear_dz_kernel<1, RLK_ACT_NONE>);
+    kernel<<<grid, DT, 0, stream>>>(a, dst, ld, part, pitch, (int)parts);
     if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
     if (a.db) {
       const cudaError_t e = launch_after(linear_db_kernel, dim3((unsigned)((a.N + 31) / 32)), dim3(256), 0, stream,
