@@ -7,11 +7,13 @@
 // operands may each be stored with K or with M / N contiguous, so neither w nor
 // x nor dz is transposed in memory.  bf16 operands arrive by TMA (128-byte
 // swizzle) in a ring of 64-deep stages, one thread issues the tcgen05 MMAs
-// (128 x 256 x 16, fp32 accumulators in TMEM), eight warps run the epilogue on
-// registers read with tcgen05.ld.
-//  * Many tiles: persistent CTAs, one an SM; two TMEM accumulators, so a tile's
+// (fp32 accumulators in TMEM), eight warps run the epilogue on registers read
+// with tcgen05.ld.
+//  * Many tiles: persistent pairs of CTAs (cta_group::2), a tile of 256 x 256 a
+//    pair: each SM stages half of A's and half of B's rows, half the shared-memory
+//    traffic of two separate tiles.  Two TMEM accumulators, so a tile's
 //    epilogue runs under the next tile's products.  Tiles are walked in groups
-//    of 16 row tiles, so the CTAs at work share 16 A tiles and about 10 B tiles
+//    of 8 row tiles, so the pairs at work share 8 A tiles and about 10 B tiles
 //    in L2.
 //  * Few tiles (a call of few rows is bound by the weight's bytes, and needs
 //    every SM to fetch them): tiles of 128 x 128, and a cluster of 2 or 4 CTAs
@@ -44,14 +46,18 @@ constexpr uint32_t MN_BLOCK = 64 * BK * 2;     // a 64-element block of an MN-co
 constexpr uint32_t STAGING = 32 * 32 * 4;      // an epilogue warp's 32 x 32 piece of a tile
 constexpr uint32_t RING = 192 * 1024;          // bytes of the stage ring
 constexpr size_t SMEM_BYTES = RING + EPI_WARPS * STAGING + 1024 + 256;
-constexpr int GROUP_M = 16;
+constexpr int GROUP_M = 8;
 constexpr int MAX_SPLIT = 4;                   // CTAs that share a tile's K, at most
-// The two tile shapes: 128 x 256 in four stages, 128 x 128 in six.
+// The two shapes.  A pair of CTAs (one tile of 256 x 256, 128 rows of A and of B
+// each), or one CTA (a tile of 128 x 128, its K perhaps split over a cluster):
+// either way a CTA's stage is 128 rows of A and 128 of B.
+constexpr int BROWS = 128;
+constexpr uint32_t A_BYTES = BM * BK * 2, STAGE_BYTES = A_BYTES + BROWS * BK * 2;
+constexpr int STAGES = (int)(RING / STAGE_BYTES);
 template <bool SPLIT>
 struct Shape {
-  static constexpr int BN = SPLIT ? 128 : 256;
-  static constexpr uint32_t A_BYTES = BM * BK * 2, STAGE = A_BYTES + BN * BK * 2;
-  static constexpr int STAGES = (int)(RING / STAGE);
+  static constexpr int G = SPLIT ? 1 : 2;      // CTAs of a tile
+  static constexpr int TM = BM * G, BN = BROWS * G;
   static constexpr uint32_t TMEM_COLS = 2 * BN;
   static constexpr int PLD = BN + 4;           // row pitch (floats) of a partial tile: conflict-free float4 rows
 };
@@ -236,15 +242,15 @@ __device__ __forceinline__ void tile_coords(const GemmParams& p, int t, int& mt,
   nt = r / gm;
 }
 
-// SPLIT: a cluster of CTAs works on one tile, each on its share of K; else a
-// CTA works on whole tiles blockIdx.x, + gridDim.x, ...
+// SPLIT: a cluster of CTAs works on one tile of 128 x 128, each on its share of
+// K; else pair b works on tiles b, + the number of pairs, ... of 256 x 256.
 template <bool A_MN, bool B_MN, bool SPLIT>
 __global__ void __launch_bounds__(THREADS, 1)
     linear_gemm_kernel(const __grid_constant__ CUtensorMap map_a,
                        const __grid_constant__ CUtensorMap map_b, const GemmParams p, int cluster) {
   using S = Shape<SPLIT>;
-  constexpr int BN = S::BN, STAGES = S::STAGES, PLD = S::PLD;
-  constexpr uint32_t A_BYTES = S::A_BYTES, STAGE_BYTES = S::STAGE, TMEM_COLS = S::TMEM_COLS;
+  constexpr int G = S::G, TM = S::TM, BN = S::BN, PLD = S::PLD;
+  constexpr uint32_t TMEM_COLS = S::TMEM_COLS;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -256,7 +262,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * STAGES;
   const uint32_t accf0 = empty0 + 8 * STAGES, acce0 = accf0 + 16;
   const uint32_t drain_bar = smem_u32(bars + 2 * STAGES + 6);
-  constexpr uint32_t idesc = tc::idesc_bf16(A_MN, B_MN, BM, BN);
+  constexpr uint32_t idesc = tc::idesc_bf16(A_MN, B_MN, TM, BN);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -266,25 +272,30 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(accf0 + 8 * a, 1);
-      mbar_init(acce0 + 8 * a, EPI_WARPS);   // one arrive per epilogue warp
+      mbar_init(acce0 + 8 * a, EPI_WARPS * G);   // one arrive per epilogue warp of the tile's CTAs
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
   }
-  if (warp == 1) tc::alloc(smem_u32(tmem_slot), TMEM_COLS);
+  if (warp == 1) tc::alloc<G>(smem_u32(tmem_slot), TMEM_COLS);
   tc::fence_before();
   pdl_wait();   // the operands may come from the kernel before
   __syncthreads();
+  if (G == 2) tc::cluster_sync();   // the other CTA's barriers are there
   tc::fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  const uint32_t rank = SPLIT ? tc::cluster_rank() : 0u;
-  const int tile0 = p.first_tile + (SPLIT ? (int)(blockIdx.x / (unsigned)cluster) : (int)blockIdx.x);
-  const int tile_step = SPLIT ? p.n_tiles : (int)gridDim.x;
+  // SPLIT: which share of K; else: which half of the tile
+  const uint32_t rank = tc::cluster_rank();
+  const int per = SPLIT ? cluster : G;   // CTAs that work on one tile
+  const int tile0 = p.first_tile + (int)(blockIdx.x / (unsigned)per);
+  const int tile_step = SPLIT ? p.n_tiles : (int)(gridDim.x / G);
   const int k0 = SPLIT ? (int)((int64_t)rank * p.k_steps / cluster) : 0;
   const int k1 = SPLIT ? (int)((int64_t)(rank + 1) * p.k_steps / cluster) : p.k_steps;
+  const int a_off = SPLIT ? 0 : (int)rank * BM, b_off = SPLIT ? 0 : (int)rank * BROWS;
+  const bool leader = SPLIT || rank == 0;
 
   if (warp == 0) {
     // ------------------------------------------------------ TMA producer
@@ -301,39 +312,46 @@ __global__ void __launch_bounds__(THREADS, 1)
             break;
           }
           const uint32_t fb = full0 + 8 * stage;
-          mbar_expect_tx(fb, STAGE_BYTES);
           const uint32_t sa = base + stage * STAGE_BYTES, sb = sa + A_BYTES;
+          // a pair's copies all report to the even CTA, whose barrier expects them all
+          if (leader) mbar_expect_tx(fb, G * STAGE_BYTES);
+          const uint32_t to = G == 2 ? tc::peer_addr(fb, 0u) : fb;
+          auto load = [&](uint32_t dst, const CUtensorMap* map, int x, int y) {
+            if (G == 2) tc::load_2d_pair(dst, map, to, x, y);
+            else tc::load_2d(dst, map, to, x, y);
+          };
+          const int am = mt * TM + a_off, bn = nt * BN + b_off;
           if (A_MN) {
 #pragma unroll
-            for (int j = 0; j < BM / 64; ++j) tc::load_2d(sa + j * MN_BLOCK, &map_a, fb, mt * BM + j * 64, k * BK);
+            for (int j = 0; j < BM / 64; ++j) load(sa + j * MN_BLOCK, &map_a, am + j * 64, k * BK);
           } else {
-            tc::load_2d(sa, &map_a, fb, k * BK, mt * BM);
+            load(sa, &map_a, k * BK, am);
           }
           if (B_MN) {
 #pragma unroll
-            for (int j = 0; j < BN / 64; ++j) tc::load_2d(sb + j * MN_BLOCK, &map_b, fb, nt * BN + j * 64, k * BK);
+            for (int j = 0; j < BROWS / 64; ++j) load(sb + j * MN_BLOCK, &map_b, bn + j * 64, k * BK);
           } else {
-            tc::load_2d(sb, &map_b, fb, k * BK, nt * BN);
+            load(sb, &map_b, k * BK, bn);
           }
           used |= 1u << stage;
           last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
       }
-      if (!ok || *abort_flag) {   // let every issued copy land before the CTA exits
+      if ((!ok || *abort_flag) && leader) {   // let every issued copy land before the CTAs exit
         for (int s = 0; s < STAGES; ++s)
           if (used & (1u << s)) tc::drain(full0 + 8 * s, (last_parity >> s) & 1u);
       }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------ MMA issuer
-    if (lane == 0) {
+    if (lane == 0 && leader) {
       int stage = 0;
       uint32_t phase = 0, tile = 0;
       bool ok = true;
       for (int t = tile0; t < p.n_tiles && ok; t += tile_step, ++tile) {
         const uint32_t acc = tile & 1u, accph = (tile >> 1) & 1u;
-        if (!tc::wait(acce0 + 8 * acc, accph ^ 1u, abort_flag, p.wait_limit)) { ok = false; break; }
+        if (!tc::wait<G == 2>(acce0 + 8 * acc, accph ^ 1u, abort_flag, p.wait_limit)) { ok = false; break; }
         tc::fence_after();
         const uint32_t d_tmem = tmem + acc * BN;
         for (int k = k0; k < k1; ++k) {
@@ -345,15 +363,15 @@ __global__ void __launch_bounds__(THREADS, 1)
             // 16 K elements: 32 bytes inside a K-contiguous row, 16 rows of an MN-contiguous block
             const uint64_t da = A_MN ? tc::desc_mn(sa + kk * 2048, MN_BLOCK) : tc::desc_k(sa) + (uint64_t)(kk * 2);
             const uint64_t db = B_MN ? tc::desc_mn(sb + kk * 2048, MN_BLOCK) : tc::desc_k(sb) + (uint64_t)(kk * 2);
-            tc::mma(d_tmem, da, db, idesc, (k > k0 || kk > 0) ? 1u : 0u);
+            tc::mma<G>(d_tmem, da, db, idesc, (k > k0 || kk > 0) ? 1u : 0u);
           }
-          tc::commit(empty0 + 8 * stage);
+          tc::commit<G>(empty0 + 8 * stage);
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
-        if (ok) tc::commit(accf0 + 8 * acc);
+        if (ok) tc::commit<G>(accf0 + 8 * acc);
       }
       if (!ok) {   // every MMA already issued finishes before TMEM is freed
-        tc::commit(drain_bar);
+        tc::commit<G>(drain_bar);
         tc::drain(drain_bar, 0u);
       }
     }
@@ -375,7 +393,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       // after a wait has run out, this tile and the CTA's later ones are NaN
       ok = __all_sync(0xFFFFFFFFu, ok && tc::wait(accf0 + 8 * acc, accph, abort_flag, p.wait_limit));
       tc::fence_after();
-      const int64_t row0 = (int64_t)mt * BM + q * 32;
+      const int64_t row0 = (int64_t)mt * TM + a_off + q * 32;
 #pragma unroll 1
       for (int ch = 0; ch < BN / 64; ++ch) {
         const int c0 = half * (BN / 2) + ch * 32;
@@ -403,7 +421,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (ch == BN / 64 - 1) {   // the accumulator is in registers: its next tile may begin
           tc::fence_before();
           __syncwarp();
-          if (lane == 0 && ok) mbar_arrive(acce0 + 8 * acc);
+          if (lane == 0 && ok) {
+            if (G == 2) tc::arrive_peer(tc::peer_addr(acce0 + 8 * acc, 0u));
+            else mbar_arrive(acce0 + 8 * acc);
+          }
         }
         if (SPLIT) {
           if (row0 + lane < p.M && col0 < p.N) {
@@ -521,8 +542,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
   tc::fence_before();
   __syncthreads();
+  if (G == 2) tc::cluster_sync();   // the pair's products, copies and arrivals are all done
   tc::fence_after();
-  if (warp == 1) tc::dealloc(tmem, TMEM_COLS);
+  if (warp == 1) tc::dealloc<G>(tmem, TMEM_COLS);
 }
 
 // ------------------------------------------------------------ a few rows
@@ -798,7 +820,8 @@ cudaError_t launch_gemm(const CUtensorMap& ma, const CUtensorMap& mb, const Gemm
   if (cudaError_t e = set_smem<A_MN, B_MN, SPLIT>(); e != cudaSuccess) return e;
   const int tiles = p.n_tiles - p.first_tile;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(SPLIT ? tiles * split : (tiles < sm_count() ? tiles : sm_count())));
+  const int pairs = sm_count() / 2;
+  cfg.gridDim = dim3((unsigned)(SPLIT ? tiles * split : 2 * (tiles < pairs ? tiles : pairs)));
   cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = SMEM_BYTES;
   cfg.stream = stream;
@@ -806,11 +829,11 @@ cudaError_t launch_gemm(const CUtensorMap& ma, const CUtensorMap& mb, const Gemm
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = (unsigned)split;
+  at[1].val.clusterDim.x = (unsigned)(SPLIT ? split : 2);
   at[1].val.clusterDim.y = 1;
   at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = SPLIT ? 2 : 1;
+  cfg.numAttrs = 2;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, linear_gemm_kernel<A_MN, B_MN, SPLIT>, ma, mb, p, split);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -821,27 +844,24 @@ cudaError_t gemm(const Operand& a, const Operand& b, int64_t M, int64_t N, int64
   GemmParams p{};
   p.M = M;
   p.N = N;
-  p.n_mt = (int)((M + BM - 1) / BM);
   p.k_steps = (int)((K + BK - 1) / BK);
   p.wait_limit = debug_wait_limit();
   p.e = epi;
   p.e.vec = rows16(epi.y, epi.y_dtype, epi.ldy) && (!epi.z || rows16(epi.z, 0, epi.ldz)) &&
             (!epi.residual || rows16(epi.residual, 0, epi.ldr));
-  const int64_t wide = (int64_t)p.n_mt * ((N + 255) / 256);
-  if (wide > (1 << 30)) return cudaErrorInvalidValue;
-  // Tiles of 128 x 256 that would leave half of the SMs idle: tiles of 128 x 128
-  // instead, with K split over a cluster while SMs are left.
-  const bool few = 2 * wide <= sm_count();
+  const int64_t small = ((M + 127) / 128) * ((N + 127) / 128);
+  if (small > (1 << 30)) return cudaErrorInvalidValue;
+  // Tiles of 128 x 128, K split over a cluster while SMs are left, when one round
+  // of them does the call (or there are no rows for a pair); else pairs' tiles of 256 x 256.
+  const bool few = small <= sm_count() || M <= BM;
   CUtensorMap ma, mb;
-  if (!make_map(&ma, a, A_MN, M, K, BM) || !make_map(&mb, b, B_MN, N, K, few ? 128 : 256)) return cudaErrorInvalidValue;
-  if (!few) {
-    p.n_nt = (int)((N + 255) / 256);
-    p.n_tiles = (int)wide;
-    return launch_gemm<A_MN, B_MN, false>(ma, mb, p, 1, stream);
-  }
-  p.n_nt = (int)((N + 127) / 128);
+  if (!make_map(&ma, a, A_MN, M, K, BM) || !make_map(&mb, b, B_MN, N, K, BROWS)) return cudaErrorInvalidValue;
+  const int tm = few ? 128 : 256;
+  p.n_mt = (int)((M + tm - 1) / tm);
+  p.n_nt = (int)((N + tm - 1) / tm);
   p.n_tiles = p.n_mt * p.n_nt;
-  return launch_gemm<A_MN, B_MN, true>(ma, mb, p, split_for(p.n_tiles, p.k_steps), stream);
+  return few ? launch_gemm<A_MN, B_MN, true>(ma, mb, p, split_for(p.n_tiles, p.k_steps), stream)
+             : launch_gemm<A_MN, B_MN, false>(ma, mb, p, 1, stream);
 }
 
 size_t copy_bytes(int64_t rows, int64_t cols) { return pad256((size_t)rows * pad8(cols) * 2); }
