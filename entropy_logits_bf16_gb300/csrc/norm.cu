@@ -253,23 +253,37 @@ __device__ __forceinline__ void store_cols(void* p, int dtype, int64_t at, int H
   }
 }
 
-// Sums of two values over a group of n threads (a power of two, >= 4), on
-// every thread of it.  `buf` alternates between two halves of s_red, so one
-// barrier a sum is enough.
-__device__ __forceinline__ float2 group_sum(float2 v, int n, float2* s_red, int& buf) {
+// The threads of a row: n of them, either a power of two up to 128 with several
+// rows a CTA, or any multiple of 32 with one.
+struct Group {
+  int n, t, index, count;   // size, this thread, this group, groups of the CTA
+  __device__ __forceinline__ explicit Group(int size)
+      : n(size), t(size > 128 ? (int)threadIdx.x : (int)threadIdx.x & (size - 1)),
+        index(size > 128 ? 0 : (int)threadIdx.x / size), count((int)blockDim.x / size) {}
+  // all threads of the group (and of the CTA's other groups, where that takes a barrier)
+  __device__ __forceinline__ void sync() const {
+    if (n > 32) __syncthreads();
+    else __syncwarp();
+  }
+};
+
+// Sums of two values over the group, in a fixed order, on every thread.  `buf`
+// alternates between two halves of s_red, so one barrier a sum is enough.
+__device__ __forceinline__ float2 group_sum(float2 v, const Group& g, float2* s_red, int& buf) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int o = (n < 32 ? n : 32) / 2; o > 0; o >>= 1) {
+  for (int o = (g.n < 32 ? g.n : 32) / 2; o > 0; o >>= 1) {
     v.x = __fadd_rn(v.x, __shfl_xor_sync(0xFFFFFFFFu, v.x, o));
     v.y = __fadd_rn(v.y, __shfl_xor_sync(0xFFFFFFFFu, v.y, o));
   }
-  if (n > 32) {
-    const int nw = n / 32;
+  if (g.n > 32) {
     float2* s = s_red + buf * 32;
     buf ^= 1;
     if (lane == 0) s[warp] = v;
     __syncthreads();
-    v = s[(warp & ~(nw - 1)) + (lane & (nw - 1))];
-    for (int o = nw / 2; o > 0; o >>= 1) {
+    const int nw = g.n / 32, at = lane & 15;   // at most 16 warps
+    v = at < nw ? s[g.index * nw + at] : make_float2(0.f, 0.f);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) {
       v.x = __fadd_rn(v.x, __shfl_xor_sync(0xFFFFFFFFu, v.x, o));
       v.y = __fadd_rn(v.y, __shfl_xor_sync(0xFFFFFFFFu, v.y, o));
     }
@@ -315,65 +329,10 @@ __device__ __forceinline__ void write_checkpoint(const CheckpointView& ck, int64
   }
 }
 
-// n threads a row, blockDim.x / n rows a CTA.
-template <int XT, int VW, int E>
-__global__ void __launch_bounds__(kMaxGroup, E == 16 ? 2 : 1) norm_fwd_kernel(NormArgs a, int n) {
-  __shared__ float2 s_red[64];
-  int buf = 0;
-  const int t = threadIdx.x & (n - 1), H = (int)a.H;
-  const int64_t row = (int64_t)blockIdx.x * (blockDim.x / n) + threadIdx.x / n;
-  const bool live = row < a.T;
-  const float inv_h = __fdiv_rn(1.f, (float)H);
-  float x[E];
-  if (live) {
-    load_cols<VW>(a.x, XT, row * a.ldx, H, t, n, x);
-  } else {
-#pragma unroll
-    for (int e = 0; e < E; ++e) x[e] = 0.f;
-  }
-  float m = 0.f;
-  if (!a.rms) {
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) s = __fadd_rn(s, x[e]);
-    m = __fmul_rn(group_sum(make_float2(s, 0.f), n, s_red, buf).x, inv_h);
-  }
-  float s = 0.f;
-  const int n2 = fresh(n);
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const float d = col_of<VW>(e, t, n2) < H ? __fsub_rn(x[e], m) : 0.f;
-    s = __fmaf_rn(d, d, s);
-  }
-  const float var = __fmul_rn(group_sum(make_float2(s, 0.f), n, s_red, buf).x, inv_h);
-  const bool bad = !isfinite(var);
-  const float r = bad ? NAN : __fdiv_rn(1.f, __fsqrt_rn(__fadd_rn(var, a.eps)));
-  if (bad) m = NAN;
-  if (live && t == 0) {
-    if (a.mean && !a.rms) a.mean[row] = m;
-    if (a.rstd) a.rstd[row] = r;
-    if (bad && a.status) atomicOr(a.status, RLK_STATUS_NONFINITE);
-  }
-  if (a.ck.codes) write_checkpoint<VW>(a.ck, row, live, H, t, n, x);
-  if (!live) return;
-  float p[E];
-  if (a.weight) {
-    load_cols<VW>(a.weight, a.param_dtype, 0, H, t, n, p);
-  } else {
-#pragma unroll
-    for (int e = 0; e < E; ++e) p[e] = 1.f;
-  }
-#pragma unroll
-  for (int e = 0; e < E; ++e) x[e] = __fmul_rn(__fmul_rn(__fsub_rn(x[e], m), r), p[e]);
-  if (a.bias) {
-    load_cols<VW>(a.bias, a.param_dtype, 0, H, t, n, p);
-#pragma unroll
-    for (int e = 0; e < E; ++e) x[e] = __fadd_rn(x[e], p[e]);
-  }
-  store_cols<VW>(a.y, a.y_dtype, row * a.ldy, H, t, n, x);
-}
-
-constexpr int kFromCk = 2;   // backward: x from its checkpoint
+// ---- rows on their way to shared memory
+// Types: 0 bf16, 1 fp32, 2 checkpoint codes.
+constexpr int kFromCk = 2;
+constexpr int bytes_of(int type) { return type == 1 ? 4 : (type == 0 ? 2 : 1); }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -381,79 +340,327 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int by
 __device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-
-// Bytes of one thread's 8 columns of a row in a type (0 bf16, 1 fp32, 2 codes).
-constexpr int piece_bytes(int type) { return type == 1 ? 32 : (type == 0 ? 16 : 8); }
-
-// Starts the copy of this thread's columns into its place (k-th piece of
-// thread t at (k n + t) piece_bytes); a piece past the row copies nothing.
-template <int TYPE, int E>
-__device__ __forceinline__ void copy_cols(uint32_t dst, const void* p, int64_t at, int H, int t, int n) {
-  constexpr int es = TYPE == 1 ? 4 : (TYPE == 0 ? 2 : 1);
-#pragma unroll
-  for (int k = 0; k < E / 8; ++k) {
-    const int c = (k * n + t) * 8;
-    const int have = (H - c < 8 ? H - c : 8) * es;
-    if (have <= 0) continue;
-    const char* src = static_cast<const char*>(p) + (at + c) * es;
-    const uint32_t d = dst + (uint32_t)((k * n + t) * piece_bytes(TYPE));
-    if (TYPE == kFromCk) {
-      cp_async8(d, src, have);
-    } else {
-      cp_async16(d, src, have < 16 ? have : 16);
-      if (TYPE == 1 && have > 16) cp_async16(d + 16, src + 16, have - 16);
-    }
-  }
-}
-template <int TYPE, int E>
-__device__ __forceinline__ void take_cols(const uint8_t* s, int H, int t, int n, const float (&step)[E / 8],
-                                          float (&v)[E]) {
-#pragma unroll
-  for (int k = 0; k < E / 8; ++k) {
-    const int c = (k * n + t) * 8;
-    const uint8_t* p = s + (k * n + t) * piece_bytes(TYPE);
-    float* o = v + 8 * k;
-    if (TYPE == 1) {
-      const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-      o[0] = a.x; o[1] = a.y; o[2] = a.z; o[3] = a.w;
-      o[4] = b.x; o[5] = b.y; o[6] = b.z; o[7] = b.w;
-    } else if (TYPE == 0) {
-      const uint4 q = *reinterpret_cast<const uint4*>(p);
-      o[0] = bf16_lo(q.x); o[1] = bf16_hi(q.x); o[2] = bf16_lo(q.y); o[3] = bf16_hi(q.y);
-      o[4] = bf16_lo(q.z); o[5] = bf16_hi(q.z); o[6] = bf16_lo(q.w); o[7] = bf16_hi(q.w);
-    } else {
-      const uint2 q = *reinterpret_cast<const uint2*>(p);
-      const uint32_t w2[2] = {q.x, q.y};
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        o[j] = __fmul_rn((float)(int8_t)(w2[j / 4] >> (8 * (j % 4))), step[k]);
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (c + j >= H) o[j] = 0.f;
-  }
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// The oldest of `depth` rows on their way has landed (this thread's copies).
+__device__ __forceinline__ void cp_wait(int depth) {
+  if (depth == 4) asm volatile("cp.async.wait_group 3;" ::: "memory");
+  else if (depth == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-// XT: 0 bf16, 1 fp32, 2 a checkpoint; DT: type of dy.  E == 32: the partial dw,
-// db live in shared memory (a thread has no registers for 32 columns of
-// them).  `depth` rows (0, 1, 2) are on their way ahead of the one at work; 0:
-// the row is loaded when its turn comes (VW = 1, and rows that do not fit).
-template <int XT, int DT, int VW, int E>
-__global__ void __launch_bounds__(kMaxGroup, 1) norm_bwd_kernel(NormBwdArgs a, int n, int depth) {
-  constexpr bool SACC = E == 32;
+// Bytes of a row's place in shared memory.  VW = 8: the threads' 8-column
+// pieces; VW = 1: the row's bytes at its own distance from a 16-byte boundary.
+template <int TYPE, int VW, int E>
+__host__ __device__ __forceinline__ int place_bytes(int H, int n) {
+  return VW == 8 ? E * n * bytes_of(TYPE) : (H * bytes_of(TYPE) + 15) / 16 * 16 + 16;
+}
+
+// VW = 1: the element of a row that a thread carries to shared memory itself,
+// being outside the whole 16-byte units that cp.async copies: threads 0..7 those
+// before the first boundary, 8..15 those after the last.  -1: none.
+template <int TYPE>
+__device__ __forceinline__ int edge_byte(int to_boundary, int row_bytes, int t) {
+  constexpr int es = bytes_of(TYPE);
+  if (TYPE == kFromCk) return -1;   // rows of codes start on boundaries and are padded to whole units
+  const int head = to_boundary < row_bytes ? to_boundary : row_bytes;
+  if (t < 8) return t * es < head ? t * es : -1;
+  const int at = head + ((row_bytes - head) & ~15) + (t - 8) * es;
+  return t < 16 && at < row_bytes ? at : -1;
+}
+__device__ __forceinline__ int to_boundary(const void* p) { return (int)(-reinterpret_cast<uintptr_t>(p) & 15u); }
+
+// Starts the copy of a row (at element `at` of p) into its place, and returns the
+// edge element that this thread has to store there when it is used (VW = 1).
+template <int TYPE, int VW, int E>
+__device__ __forceinline__ uint32_t start_row(uint8_t* place, const void* p, int64_t at, int H, const Group& g) {
+  constexpr int es = bytes_of(TYPE);
+  const char* src = static_cast<const char*>(p) + at * es;
+  const uint32_t dst = smem_u32(place);
+  if (VW == 8) {
+#pragma unroll
+    for (int k = 0; k < E / 8; ++k) {
+      const int c = (k * g.n + g.t) * 8;
+      const int have = (H - c < 8 ? H - c : 8) * es;
+      if (have <= 0) continue;
+      if (TYPE == kFromCk) {
+        cp_async8(dst + c, src + c, have);
+      } else {
+        cp_async16(dst + c * es, src + c * es, have < 16 ? have : 16);
+        if (TYPE == 1 && have > 16) cp_async16(dst + c * es + 16, src + c * es + 16, have - 16);
+      }
+    }
+    return 0u;
+  }
+  const int row_bytes = H * es, gap = to_boundary(src);
+  const int head = gap < row_bytes ? gap : row_bytes;
+  const int body = TYPE == kFromCk ? (row_bytes + 15) & ~15 : (row_bytes - head) & ~15;
+  const uint32_t d = dst + (uint32_t)(reinterpret_cast<uintptr_t>(src) & 15u) + head;
+  for (int o = g.t * 16; o < body; o += g.n * 16) cp_async16(d + o, src + head + o, 16);
+  const int e = edge_byte<TYPE>(gap, row_bytes, g.t);
+  if (e < 0) return 0u;
+  return TYPE == 1 ? *reinterpret_cast<const uint32_t*>(src + e) : *reinterpret_cast<const uint16_t*>(src + e);
+}
+// VW = 1: stores the edge element of the row that started `at` there.
+template <int TYPE>
+__device__ __forceinline__ void store_edge(uint8_t* place, const void* p, int64_t at, int H, const Group& g, uint32_t v) {
+  constexpr int es = bytes_of(TYPE);
+  const char* src = static_cast<const char*>(p) + at * es;
+  const int e = edge_byte<TYPE>(to_boundary(src), H * es, g.t);
+  if (e < 0) return;
+  uint8_t* d = place + (reinterpret_cast<uintptr_t>(src) & 15u) + e;
+  if (TYPE == 1) *reinterpret_cast<uint32_t*>(d) = v;
+  else *reinterpret_cast<uint16_t*>(d) = (uint16_t)v;
+}
+
+// Codes q0..q3 of a word as floats: a byte under the exponent of 2^23 reads as
+// 2^23 + (q + 128).
+__device__ __forceinline__ float code_value(uint32_t flipped, int j) {
+  return __fsub_rn(__uint_as_float(__byte_perm(flipped, 0x4B000000u, 0x7440 + j)), 8388736.f);
+}
+
+// A thread's columns of a row in shared memory (0 past the end).  VW = 8: only
+// what this thread copied itself; VW = 1: after a barrier.
+template <int TYPE, int VW, int E>
+__device__ __forceinline__ void take_row(const uint8_t* place, const void* p, int64_t at, int H, const Group& g,
+                                         const float (&step)[VW == 8 ? E / 8 : E], float (&v)[E]) {
+  constexpr int es = bytes_of(TYPE);
+  if (VW == 8) {
+#pragma unroll
+    for (int k = 0; k < E / 8; ++k) {
+      const int c = (k * g.n + g.t) * 8;
+      const uint8_t* s = place + c * es;
+      float* o = v + 8 * k;
+      if (TYPE == 1) {
+        const float4 a = reinterpret_cast<const float4*>(s)[0], b = reinterpret_cast<const float4*>(s)[1];
+        o[0] = a.x; o[1] = a.y; o[2] = a.z; o[3] = a.w;
+        o[4] = b.x; o[5] = b.y; o[6] = b.z; o[7] = b.w;
+      } else if (TYPE == 0) {
+        const uint4 q = *reinterpret_cast<const uint4*>(s);
+        o[0] = bf16_lo(q.x); o[1] = bf16_hi(q.x); o[2] = bf16_lo(q.y); o[3] = bf16_hi(q.y);
+        o[4] = bf16_lo(q.z); o[5] = bf16_hi(q.z); o[6] = bf16_lo(q.w); o[7] = bf16_hi(q.w);
+      } else {
+        const uint2 q = *reinterpret_cast<const uint2*>(s);
+        const uint32_t w2[2] = {q.x ^ 0x80808080u, q.y ^ 0x80808080u};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = __fmul_rn(code_value(w2[j / 4], j % 4), step[k]);
+      }
+      if (c + 8 > H) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (c + j >= H) o[j] = 0.f;
+      }
+    }
+    return;
+  }
+  const uint8_t* s = place + ((reinterpret_cast<uintptr_t>(p) + at * es) & 15u) + g.t * es;
+  const int n = fresh(g.n), left = H - g.t;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const uint8_t* q = s + e * n * es;
+    if (e * n >= left) v[e] = 0.f;
+    else if (TYPE == 1) v[e] = *reinterpret_cast<const float*>(q);
+    else if (TYPE == 0) v[e] = bf16_val(*reinterpret_cast<const uint16_t*>(q));
+    else v[e] = __fmul_rn((float)*reinterpret_cast<const int8_t*>(q), step[VW == 8 ? 0 : e]);
+  }
+}
+
+// ---- forward
+// Persistent: a group takes rows index, + stride, ..., `depth` of them (1, 2, 4) on
+// their way to shared memory ahead of the one at work.  E = 16 keeps its columns of
+// weight and bias in registers.
+template <int XT, int VW, int E>
+__global__ void __launch_bounds__(kMaxGroup, 1) norm_fwd_kernel(NormArgs a, int n, int depth) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float2 s_red[64];
   int buf = 0;
-  const int t = threadIdx.x & (n - 1), H = (int)a.H, groups = blockDim.x / n, grp = threadIdx.x / n;
+  const Group g(n);
+  const int H = (int)a.H;
+  const int64_t stride = (int64_t)gridDim.x * g.count, row0 = (int64_t)blockIdx.x * g.count;
+  const int iters = row0 < a.T ? (int)((a.T - row0 + stride - 1) / stride) : 0;
+  const int size = place_bytes<XT, VW, E>(H, n);
+  uint8_t* mine = smem + (size_t)g.index * depth * size;
+  const float inv_h = __fdiv_rn(1.f, (float)H);
+  const float none[VW == 8 ? E / 8 : E] = {};
+
+  pdl_wait();   // the rows may come from the kernel before
+  uint32_t edge[2] = {0u, 0u};   // VW = 1: depth is at most 2
+  auto start = [&](int i) -> uint32_t {
+    const int64_t row = row0 + g.index + i * stride;
+    uint32_t e = 0u;
+    if (i < iters && row < a.T) e = start_row<XT, VW, E>(mine + (i & (depth - 1)) * size, a.x, row * a.ldx, H, g);
+    cp_commit();
+    return e;
+  };
+  edge[0] = start(0);
+  if (depth > 1) edge[1] = start(1);
+  for (int i = 2; i < depth; ++i) start(i);
+  constexpr bool KEEP = E == 16;
+  float w[KEEP ? E : 1], b[KEEP ? E : 1];
+  if constexpr (KEEP) {
+    if (a.weight) load_cols<VW>(a.weight, a.param_dtype, 0, H, g.t, n, w);
+    if (a.bias) load_cols<VW>(a.bias, a.param_dtype, 0, H, g.t, n, b);
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      if (!a.weight) w[e] = 1.f;
+      if (!a.bias) b[e] = 0.f;
+    }
+  }
+
+  for (int i = 0; i < iters; ++i) {
+    const int64_t row = row0 + g.index + i * stride;
+    const bool live = row < a.T;
+    uint8_t* place = mine + (i & (depth - 1)) * size;
+    float x[E];
+    if (VW == 1 && live) store_edge<XT>(place, a.x, row * a.ldx, H, g, edge[0]);
+    cp_wait(depth);
+    if (VW == 1) g.sync();
+    if (live) {
+      take_row<XT, VW, E>(place, a.x, row * a.ldx, H, g, none, x);
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[e] = 0.f;
+    }
+    if (VW == 8) start(i + depth);   // into the place just read: a thread reads only what it copied itself
+    float m = 0.f;
+    if (!a.rms) {
+      float s = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) s = __fadd_rn(s, x[e]);
+      m = __fmul_rn(group_sum(make_float2(s, 0.f), g, s_red, buf).x, inv_h);
+    }
+    float s = 0.f;
+    if (VW == 8) {
+#pragma unroll
+      for (int k = 0; k < E / 8; ++k) {
+        const int c = (k * n + g.t) * 8;
+        if (c + 8 <= H) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float d = __fsub_rn(x[8 * k + j], m);
+            s = __fmaf_rn(d, d, s);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float d = c + j < H ? __fsub_rn(x[8 * k + j], m) : 0.f;
+            s = __fmaf_rn(d, d, s);
+          }
+        }
+      }
+    } else {
+      const int n2 = fresh(n), left = H - g.t;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float d = e * n2 < left ? __fsub_rn(x[e], m) : 0.f;
+        s = __fmaf_rn(d, d, s);
+      }
+    }
+    const float var = __fmul_rn(group_sum(make_float2(s, 0.f), g, s_red, buf).x, inv_h);
+    if (VW == 1) {   // the sum's barrier: every thread has read the place
+      if (n <= 32) __syncwarp();
+      const uint32_t e = start(i + depth);
+      if (depth == 2) {
+        edge[0] = edge[1];
+        edge[1] = e;
+      } else {
+        edge[0] = e;
+      }
+    }
+    const bool bad = !isfinite(var);
+    const float r = bad ? NAN : __fdiv_rn(1.f, __fsqrt_rn(__fadd_rn(var, a.eps)));
+    if (bad) m = NAN;
+    if (live && g.t == 0) {
+      if (a.mean && !a.rms) a.mean[row] = m;
+      if (a.rstd) a.rstd[row] = r;
+      if (bad && a.status) atomicOr(a.status, RLK_STATUS_NONFINITE);
+    }
+    if (a.ck.codes) write_checkpoint<VW>(a.ck, row, live, H, g.t, n, x);
+    if constexpr (KEEP) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[e] = __fmaf_rn(__fmul_rn(__fsub_rn(x[e], m), r), w[e], b[e]);
+    } else {
+      float p[E];
+      if (a.weight) {
+        load_cols<VW>(a.weight, a.param_dtype, 0, H, g.t, n, p);
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] = __fmul_rn(__fmul_rn(__fsub_rn(x[e], m), r), p[e]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] = __fmul_rn(__fsub_rn(x[e], m), r);
+      }
+      if (a.bias) {
+        load_cols<VW>(a.bias, a.param_dtype, 0, H, g.t, n, p);
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] = __fadd_rn(x[e], p[e]);
+      }
+    }
+    if (live) store_cols<VW>(a.y, a.y_dtype, row * a.ldy, H, g.t, n, x);
+  }
+}
+
+// ---- backward
+// XT: type of x, 2: from its checkpoint; DT: type of dy.  Rows as in the
+// forward; `depth` 0: a row is loaded when its turn comes (rows that do not fit).
+// E = 32: the partial dw, db live in shared memory (a thread has no registers for
+// 32 columns of them).
+template <int XT, int DT, int VW, int E>
+__global__ void __launch_bounds__(kMaxGroup, 1) norm_bwd_kernel(NormBwdArgs a, int n, int depth) {
+  constexpr bool SACC = E == 32;
+  constexpr int STEPS = VW == 8 ? E / 8 : E;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float2 s_red[64];
+  int buf = 0;
+  const Group g(n);
+  const int H = (int)a.H;
   const float inv_h = __fdiv_rn(1.f, (float)H);
   float* s_acc = reinterpret_cast<float*>(smem);   // SACC: [2][E n]
-  const int dy_bytes = E / 8 * n * piece_bytes(DT), x_bytes = E / 8 * n * piece_bytes(XT);
-  uint8_t* mine = smem + (SACC ? 2 * E * n * 4 : 0) + grp * depth * (dy_bytes + x_bytes);
+  const int dy_size = place_bytes<DT, VW, E>(H, n), size = dy_size + place_bytes<XT, VW, E>(H, n);
+  uint8_t* mine = smem + (SACC ? 2 * E * n * 4 : 0) + (size_t)g.index * depth * size;
+  const int64_t stride = (int64_t)gridDim.x * g.count, row0 = (int64_t)blockIdx.x * g.count;
+  const int iters = row0 < a.T ? (int)((a.T - row0 + stride - 1) / stride) : 0;
+  const void* xp = XT == kFromCk ? static_cast<const void*>(a.ck.codes) : a.x;
+  const int64_t ldx = XT == kFromCk ? a.ck.ldc : a.ldx;
+
+  pdl_wait();
+  uint2 edge[2] = {make_uint2(0u, 0u), make_uint2(0u, 0u)};   // VW = 1: depth is at most 2
+  auto place = [&](int i) { return mine + (i & (depth - 1)) * size; };
+  auto start = [&](int i) -> uint2 {
+    const int64_t row = row0 + g.index + i * stride;
+    uint2 e = make_uint2(0u, 0u);
+    if (i < iters && row < a.T) {
+      e.x = start_row<DT, VW, E>(place(i), a.dy, row * a.lddy, H, g);
+      e.y = start_row<XT, VW, E>(place(i) + dy_size, xp, row * ldx, H, g);
+    }
+    cp_commit();
+    return e;
+  };
+  if (depth > 0) edge[0] = start(0);
+  if (depth > 1) edge[1] = start(1);
+  for (int i = 2; i < depth; ++i) start(i);
+  // a row's statistics and checkpoint steps, read one row ahead
+  float m1 = 0.f, r1 = 0.f;
+  uint32_t byte1[STEPS];
+  auto ahead = [&](int i) {
+    const int64_t row = row0 + g.index + i * stride;
+    const bool in = i < iters && row < a.T;
+    m1 = in && !a.rms ? a.mean[row] : 0.f;
+    r1 = in ? a.rstd[row] : 0.f;
+    if (XT == kFromCk) {
+      const uint8_t* sc = a.ck.scales + row * a.ck.lds;
+      const int n2 = VW == 8 ? g.n : fresh(g.n);
+#pragma unroll
+      for (int k = 0; k < STEPS; ++k) {
+        const int c = (k * n2 + g.t) * VW;
+        byte1[k] = in && c < H ? sc[c / kCkBlock] : 1u;
+      }
+    }
+  };
+  ahead(0);
 
   float w[E], dw[SACC ? 1 : E], db[SACC ? 1 : E];
   auto load_w = [&]() {
     if (a.weight) {
-      load_cols<VW>(a.weight, a.param_dtype, 0, H, t, n, w);
+      load_cols<VW>(a.weight, a.param_dtype, 0, H, g.t, n, w);
     } else {
 #pragma unroll
       for (int e = 0; e < E; ++e) w[e] = 1.f;
@@ -462,92 +669,84 @@ __global__ void __launch_bounds__(kMaxGroup, 1) norm_bwd_kernel(NormBwdArgs a, i
   if (!SACC) load_w();   // else with each row: there are no registers to keep it in
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    if (SACC) s_acc[e * n + t] = s_acc[(E + e) * n + t] = 0.f;
+    if (SACC) s_acc[e * n + g.t] = s_acc[(E + e) * n + g.t] = 0.f;
     else dw[e] = db[e] = 0.f;
   }
-  const int64_t stride = (int64_t)gridDim.x * groups;
-  const int64_t row0 = (int64_t)blockIdx.x * groups;
-  const int iters = row0 < a.T ? (int)((a.T - row0 + stride - 1) / stride) : 0;
-
-  auto place = [&](int i) { return mine + (i & (depth - 1)) * (dy_bytes + x_bytes); };
-  auto start = [&](int i) {
-    const int64_t row = row0 + grp + i * stride;
-    if (i < iters && row < a.T) {
-      uint8_t* at = place(i);
-      copy_cols<DT, E>(smem_u32(at), a.dy, row * a.lddy, H, t, n);
-      if (XT == kFromCk) copy_cols<XT, E>(smem_u32(at + dy_bytes), a.ck.codes, row * a.ck.ldc, H, t, n);
-      else copy_cols<XT, E>(smem_u32(at + dy_bytes), a.x, row * a.ldx, H, t, n);
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-  if (VW == 8)
-    for (int i = 0; i < depth; ++i) start(i);
 
   for (int i = 0; i < iters; ++i) {
-    const int64_t row = row0 + grp + i * stride;
+    const int64_t row = row0 + g.index + i * stride;
     const bool live = row < a.T;
-    const float m = live && !a.rms ? a.mean[row] : 0.f, r = live ? a.rstd[row] : 0.f;
-    float dy[E], h[E];
-    if (VW == 8 && depth > 0) {
-      float step[E / 8];
-      if (XT == kFromCk) {
+    const float m = m1, r = r1;
+    float step[STEPS];
+    if (XT == kFromCk) {
 #pragma unroll
-        for (int k = 0; k < E / 8; ++k) {
-          const int c = (k * n + t) * 8;
-          step[k] = live && c < H ? ck_step(a.ck.scales[row * a.ck.lds + c / kCkBlock]) : 0.f;
-        }
+      for (int k = 0; k < STEPS; ++k) step[k] = ck_step(byte1[k]);
+    }
+    float dy[E], h[E];
+    if (depth > 0) {
+      if (VW == 1 && live) {
+        store_edge<DT>(place(i), a.dy, row * a.lddy, H, g, edge[0].x);
+        store_edge<XT>(place(i) + dy_size, xp, row * ldx, H, g, edge[0].y);
       }
-      // this row's copies have landed when at most depth - 1 later rows' are pending
-      if (depth == 1) asm volatile("cp.async.wait_group 0;" ::: "memory");
-      else asm volatile("cp.async.wait_group 1;" ::: "memory");
+      cp_wait(depth);
+      if (VW == 1) g.sync();
       if (live) {
-        const uint8_t* at = place(i);
-        take_cols<DT>(at, H, t, n, step, dy);
-        take_cols<XT>(at + dy_bytes, H, t, n, step, h);
+        take_row<DT, VW, E>(place(i), a.dy, row * a.lddy, H, g, step, dy);
+        take_row<XT, VW, E>(place(i) + dy_size, xp, row * ldx, H, g, step, h);
       }
-      start(i + depth);   // into the place just read: a thread reads only what it copied itself
+      if (VW == 8) start(i + depth);   // into the place just read: a thread reads only what it copied itself
     } else if (live) {
-      load_cols<VW>(a.dy, DT, row * a.lddy, H, t, n, dy);
+      load_cols<VW>(a.dy, DT, row * a.lddy, H, g.t, n, dy);
       if (XT == kFromCk) {
         const int n2 = fresh(n);
         const int8_t* q = a.ck.codes + row * a.ck.ldc;
-        const uint8_t* sc = a.ck.scales + row * a.ck.lds;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          const int c = col_of<VW>(e, t, n2);
-          h[e] = c < H ? __fmul_rn((float)q[c], ck_step(sc[c / kCkBlock])) : 0.f;
+          const int c = col_of<VW>(e, g.t, n2);
+          h[e] = c < H ? __fmul_rn((float)q[c], step[VW == 8 ? e / 8 : e]) : 0.f;
         }
       } else {
-        load_cols<VW>(a.x, XT, row * a.ldx, H, t, n, h);
+        load_cols<VW>(a.x, XT, row * a.ldx, H, g.t, n, h);
       }
     }
     if (!live) {
 #pragma unroll
       for (int e = 0; e < E; ++e) dy[e] = h[e] = 0.f;
     }
+    ahead(i + 1);
     if (SACC) load_w();
     float2 s = make_float2(0.f, 0.f);
 #pragma unroll
     for (int e = 0; e < E; ++e) {   // past the row dy is 0, and h does not matter
       h[e] = __fmul_rn(__fsub_rn(h[e], m), r);
-      const float g = __fmul_rn(dy[e], w[e]);
-      s.x = __fadd_rn(s.x, g);
-      s.y = __fmaf_rn(g, h[e], s.y);
+      const float gr = __fmul_rn(dy[e], w[e]);
+      s.x = __fadd_rn(s.x, gr);
+      s.y = __fmaf_rn(gr, h[e], s.y);
       if (SACC) {
-        s_acc[e * n + t] = __fmaf_rn(dy[e], h[e], s_acc[e * n + t]);
-        s_acc[(E + e) * n + t] = __fadd_rn(s_acc[(E + e) * n + t], dy[e]);
+        s_acc[e * n + g.t] = __fmaf_rn(dy[e], h[e], s_acc[e * n + g.t]);
+        s_acc[(E + e) * n + g.t] = __fadd_rn(s_acc[(E + e) * n + g.t], dy[e]);
       } else {
         dw[e] = __fmaf_rn(dy[e], h[e], dw[e]);
         db[e] = __fadd_rn(db[e], dy[e]);
       }
-      dy[e] = g;
+      dy[e] = gr;
     }
-    s = group_sum(s, n, s_red, buf);
+    s = group_sum(s, g, s_red, buf);
+    if (VW == 1 && depth > 0) {   // the sum's barrier: every thread has read the place
+      if (n <= 32) __syncwarp();
+      const uint2 e = start(i + depth);
+      if (depth == 2) {
+        edge[0] = edge[1];
+        edge[1] = e;
+      } else {
+        edge[0] = e;
+      }
+    }
     const float mg = a.rms ? 0.f : __fmul_rn(s.x, inv_h), mgh = __fmul_rn(s.y, inv_h);
 #pragma unroll
     for (int e = 0; e < E; ++e)
       h[e] = __fmul_rn(r, __fsub_rn(__fsub_rn(dy[e], mg), __fmul_rn(h[e], mgh)));
-    if (live) store_cols<VW>(a.dx, a.dx_dtype, row * a.lddx, H, t, n, h);
+    if (live) store_cols<VW>(a.dx, a.dx_dtype, row * a.lddx, H, g.t, n, h);
   }
   if (!a.workspace) return;
   float* part = a.workspace + (int64_t)blockIdx.x * 2 * part_pitch(a.H);
@@ -556,30 +755,30 @@ __global__ void __launch_bounds__(kMaxGroup, 1) norm_bwd_kernel(NormBwdArgs a, i
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
 #pragma unroll
-      for (int e = 0; e < E; ++e) v[e] = s_acc[(k * E + e) * n + t];
-      store_cols<VW>(part + k * part_pitch(a.H), 1, 0, H, t, n, v);
+      for (int e = 0; e < E; ++e) v[e] = s_acc[(k * E + e) * n + g.t];
+      store_cols<VW>(part + k * part_pitch(a.H), 1, 0, H, g.t, n, v);
     }
     return;
   }
   if constexpr (!SACC) {
     // the CTA's groups, added in order (every copy has landed: the shared memory is free again)
-    if (groups > 1) {
+    if (g.count > 1) {
       asm volatile("cp.async.wait_group 0;" ::: "memory");
-      for (int g = 0; g < groups; ++g) {
+      for (int k = 0; k < g.count; ++k) {
         __syncthreads();
-        if (grp != g) continue;
+        if (g.index != k) continue;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          float* p = s_acc + e * n + t;
-          float* q = s_acc + (E + e) * n + t;
-          *p = dw[e] = g ? __fadd_rn(*p, dw[e]) : dw[e];
-          *q = db[e] = g ? __fadd_rn(*q, db[e]) : db[e];
+          float* p = s_acc + e * n + g.t;
+          float* q = s_acc + (E + e) * n + g.t;
+          *p = dw[e] = k ? __fadd_rn(*p, dw[e]) : dw[e];
+          *q = db[e] = k ? __fadd_rn(*q, db[e]) : db[e];
         }
       }
-      if (grp != groups - 1) return;
+      if (g.index != g.count - 1) return;
     }
-    store_cols<VW>(part, 1, 0, H, t, n, dw);
-    store_cols<VW>(part + part_pitch(a.H), 1, 0, H, t, n, db);
+    store_cols<VW>(part, 1, 0, H, g.t, n, dw);
+    store_cols<VW>(part + part_pitch(a.H), 1, 0, H, g.t, n, db);
   }
 }
 
@@ -608,55 +807,72 @@ __global__ void __launch_bounds__(256) norm_param_sum_kernel(NormBwdArgs a, int 
 // ------------------------------------------------------------ host side
 int parts_for(int64_t T) { return (int)(T < kNormParts ? T : kNormParts); }
 
-// Columns of a thread and threads of a row on chip.
+// Columns of a thread, and threads of a row on chip: a power of two up to 128,
+// then whole warps.  One column at a time (vec false) takes at least a warp.
 int cols_for(int64_t H) { return H > 16 * kMaxGroup ? 32 : 16; }
-int group_for(int64_t H) {
-  int n = 4;
-  while ((int64_t)n * cols_for(H) < H) n *= 2;
+int group_for(int64_t H, bool vec) {
+  const int64_t want = (H + cols_for(H) - 1) / cols_for(H);
+  if (want > 128) return (int)((want + 31) / 32 * 32);
+  int n = vec ? 4 : 32;
+  while (n < want) n *= 2;
   return n;
 }
+constexpr size_t kSmemMost = 227 * 1024 - 1024;
 bool rows16(const void* p, int dtype, int64_t ld) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % (dtype ? 4 : 8) == 0;
 }
 bool base16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
-template <int XT, int E>
-cudaError_t fwd(const NormArgs& a, bool vec, cudaStream_t stream) {
-  // threads of one column each make whole blocks of a checkpoint only by the warp
-  const int n = !vec && a.ck.codes && group_for(a.H) < 32 ? 32 : group_for(a.H);
-  const int block = n < 256 ? 256 : n, rows = block / n;
-  const int64_t grid = (a.T + rows - 1) / rows;
-  if (grid > INT32_MAX) return cudaErrorInvalidValue;
-  if (vec) norm_fwd_kernel<XT, 8, E><<<(unsigned)grid, block, 0, stream>>>(a, n);
-  else norm_fwd_kernel<XT, 1, E><<<(unsigned)grid, block, 0, stream>>>(a, n);
-  return cudaGetLastError();
+template <class K>
+cudaError_t allow_smem(K kernel, std::atomic<int>* done) {
+  const int ds = device_slot();
+  if (ds >= 0 && done[ds].load()) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMost);
+  if (e == cudaSuccess && ds >= 0) done[ds].store(1);
+  return e;
+}
+// Rows on their way that leave room for two CTAs an SM (one, of over 256 threads).
+int depth_for(size_t row, size_t fixed, int block, int most) {
+  const size_t room = block > 256 ? kSmemMost : kSmemMost / 2;
+  int d = most;
+  while (d > 0 && fixed + d * row > room) d /= 2;
+  return d;
+}
+
+template <int XT, int VW, int E>
+cudaError_t fwd(const NormArgs& a, cudaStream_t stream) {
+  auto kernel = norm_fwd_kernel<XT, VW, E>;
+  static std::atomic<int> done[64];
+  if (cudaError_t e = allow_smem(kernel, done); e != cudaSuccess) return e;
+  const int n = group_for(a.H, VW == 8), block = n > 128 ? n : 256, groups = block / n;
+  const size_t row = (size_t)groups * place_bytes<XT, VW, E>((int)a.H, n);
+  const int depth = depth_for(row, 0, block, VW == 8 ? 4 : 2);
+  const int64_t want = (a.T + groups - 1) / groups, cap = (int64_t)sm_count() * (block > 256 ? 1 : 2);
+  const cudaError_t e = launch_after(kernel, dim3((unsigned)(want < cap ? want : cap)), dim3(block), depth * row, stream, a, n, depth);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+template <int XT>
+cudaError_t fwd_for(const NormArgs& a, bool vec, cudaStream_t stream) {
+  if (cols_for(a.H) == 32) return vec ? fwd<XT, 8, 32>(a, stream) : fwd<XT, 1, 32>(a, stream);
+  return vec ? fwd<XT, 8, 16>(a, stream) : fwd<XT, 1, 16>(a, stream);
 }
 
 template <int XT, int DT, int VW, int E>
 cudaError_t bwd(const NormBwdArgs& a, int& parts, cudaStream_t stream) {
   auto kernel = norm_bwd_kernel<XT, DT, VW, E>;
-  const int n = group_for(a.H), block = n < 256 ? 256 : n, groups = block / n;
-  constexpr size_t most = 227 * 1024 - 1024;
+  static std::atomic<int> done[64];
+  if (cudaError_t e = allow_smem(kernel, done); e != cudaSuccess) return e;
+  const int n = group_for(a.H, VW == 8), block = n > 128 ? n : 256, groups = block / n;
   const size_t acc = (size_t)2 * E * n * sizeof(float);
-  const size_t row = (size_t)groups * (E / 8) * n * (piece_bytes(XT) + piece_bytes(DT));
-  // two rows ahead; one beside the sums in shared memory, if it fits there
-  int depth = VW == 8 ? (E == 16 ? 2 : 1) : 0;
-  if (E == 32 && acc + row > most) depth = 0;
+  const size_t row = (size_t)groups * (place_bytes<XT, VW, E>((int)a.H, n) + place_bytes<DT, VW, E>((int)a.H, n));
+  const int depth = depth_for(row, E == 32 ? acc : 0, block, VW == 8 ? 4 : 2);
   size_t smem = depth * row;
   if (E == 32) smem += acc;
   else if (groups > 1 && smem < acc) smem = acc;
-  static std::atomic<int> done[64];
-  const int ds = device_slot();
-  if (ds < 0 || !done[ds].load()) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
-    if (e != cudaSuccess) return e;
-    if (ds >= 0) done[ds].store(1);
-  }
-  // a CTA of 256 threads shares its SM with another
-  const int64_t want = (a.T + groups - 1) / groups, cap = n <= 256 ? kNormParts : kNormParts / 2;
+  const int64_t want = (a.T + groups - 1) / groups, cap = block > 256 ? kNormParts / 2 : kNormParts;
   parts = (int)(want < cap ? want : cap);
-  kernel<<<parts, block, smem, stream>>>(a, n, depth);
-  return cudaGetLastError();
+  const cudaError_t e = launch_after(kernel, dim3(parts), dim3(block), smem, stream, a, n, depth);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 template <int XT, int DT>
 cudaError_t bwd_for(const NormBwdArgs& a, bool vec, int& parts, cudaStream_t stream) {
@@ -673,8 +889,7 @@ size_t norm_bwd_workspace_bytes(int64_t T, int64_t H) {
 cudaError_t launch_norm_fwd(const NormArgs& a, cudaStream_t stream) {
   if (a.H <= kOnChip) {
     const bool vec = rows16(a.x, a.dtype, a.ldx) && rows16(a.y, a.y_dtype, a.ldy) && base16(a.weight) && base16(a.bias);
-    if (cols_for(a.H) == 32) return a.dtype ? fwd<1, 32>(a, vec, stream) : fwd<0, 32>(a, vec, stream);
-    return a.dtype ? fwd<1, 16>(a, vec, stream) : fwd<0, 16>(a, vec, stream);
+    return a.dtype ? fwd_for<1>(a, vec, stream) : fwd_for<0>(a, vec, stream);
   }
   const int64_t cap = (int64_t)sm_count() * 4;
   norm_fwd_wide_kernel<<<(unsigned)(a.T < cap ? a.T : cap), WT, 0, stream>>>(a);
