@@ -22,33 +22,34 @@ __device__ __forceinline__ float ld_elem(const void* p, int dtype, int64_t i) {
                : bf16_val(static_cast<const uint16_t*>(p)[i]);
 }
 
-// 16 columns from c on (0 past the row).
+// 16 columns from c on (0 past the row), as pairs.
 template <int DT>
-__device__ __forceinline__ void load16(const void* p, int64_t at, int c, int H, float (&v)[16]) {
+__device__ __forceinline__ void load16(const void* p, int64_t at, int c, int H, float2 (&v)[8]) {
   if (c + 16 <= H) {
     if (DT) {
       const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at + c);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const float4 f = q[k];
-        v[4 * k] = f.x; v[4 * k + 1] = f.y; v[4 * k + 2] = f.z; v[4 * k + 3] = f.w;
+        v[2 * k] = make_float2(f.x, f.y);
+        v[2 * k + 1] = make_float2(f.z, f.w);
       }
     } else {
       const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at + c);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const uint4 f = q[k];
-        const uint32_t w[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          v[8 * k + 2 * j] = bf16_lo(w[j]);
-          v[8 * k + 2 * j + 1] = bf16_hi(w[j]);
-        }
+        v[4 * k] = bf16x2_to_f2(f.x);
+        v[4 * k + 1] = bf16x2_to_f2(f.y);
+        v[4 * k + 2] = bf16x2_to_f2(f.z);
+        v[4 * k + 3] = bf16x2_to_f2(f.w);
       }
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) v[j] = c + j < H ? ld_elem(p, DT, at + c + j) : 0.f;
+    for (int j = 0; j < 8; ++j)
+      v[j] = make_float2(c + 2 * j < H ? ld_elem(p, DT, at + c + 2 * j) : 0.f,
+                         c + 2 * j + 1 < H ? ld_elem(p, DT, at + c + 2 * j + 1) : 0.f);
   }
 }
 
@@ -61,7 +62,7 @@ __global__ void __launch_bounds__(CT) checkpoint_pack_kernel(CheckpointArgs a, i
   // every thread of a pair makes every step: the shuffle needs both
   for (int c0 = 0; c0 < H; c0 += n * 16) {
     const int c = c0 + t * 16;
-    float v[ROWS][16];
+    float2 v[ROWS][8];
 #pragma unroll
     for (int k = 0; k < ROWS; ++k) {
       const int64_t row = r0 + k * per;
@@ -69,22 +70,30 @@ __global__ void __launch_bounds__(CT) checkpoint_pack_kernel(CheckpointArgs a, i
         load16<DT>(a.x, row * a.ldx, c, H, v[k]);
       } else {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[k][j] = 0.f;
+        for (int j = 0; j < 8; ++j) v[k][j] = both(0.f);
       }
     }
 #pragma unroll
     for (int k = 0; k < ROWS; ++k) {
       const int64_t row = r0 + k * per;
-      uint32_t amax = 0u;
+      // fmaxf passes over a NaN; 0 x is one where x is a NaN or an infinity
+      float2 nan = both(0.f);
+      float top = 0.f;
 #pragma unroll
-      for (int j = 0; j < 16; ++j) amax = max(amax, abs_bits(v[k][j]));
+      for (int j = 0; j < 8; ++j) {
+        top = fmaxf(top, fmaxf(fabsf(v[k][j].x), fabsf(v[k][j].y)));
+        nan = fma2(v[k][j], both(0.f), nan);
+      }
+      uint32_t amax = nan.x + nan.y == 0.f ? __float_as_uint(top) : 0x7FC00000u;
       amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
       const uint32_t byte = ck_scale_byte(amax);
       if (row >= a.T || c >= H) continue;
       bad = bad || byte == 255u;
-      uint32_t q[4] = {0u, 0u, 0u, 0u};
+      uint32_t q[4];
+      const float inv = ck_inv_step(byte);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) q[j / 4] |= ((uint32_t)ck_code(v[k][j], byte) & 255u) << (8 * (j % 4));
+      for (int j = 0; j < 4; ++j)
+        q[j] = byte < kCkTop ? ck_pack4(v[k][2 * j], v[k][2 * j + 1], inv) : ck_pack4_any(v[k][2 * j], v[k][2 * j + 1], byte);
       int8_t* dst = a.ck.codes + row * a.ck.ldc + c;
       if (c + 16 <= H) {
         *reinterpret_cast<uint4*>(dst) = make_uint4(q[0], q[1], q[2], q[3]);
@@ -118,35 +127,36 @@ __global__ void __launch_bounds__(CT) checkpoint_unpack_kernel(CheckpointArgs a,
       const int64_t row = r0 + k * per;
       if (row >= a.T) continue;
       const uint32_t w[4] = {q[k].x, q[k].y, q[k].z, q[k].w};
-      float v[16];
+      float2 v[8];
 #pragma unroll
-      for (int j = 0; j < 16; ++j) v[j] = __fmul_rn((float)(int8_t)(w[j / 4] >> (8 * (j % 4))), step[k]);
-      if (DT) {
-        float* d = static_cast<float*>(a.x) + row * a.ldx + c;
-        if (c + 16 <= H) {
+      for (int j = 0; j < 4; ++j) {
+        ck_unpack4(w[j], v[2 * j], v[2 * j + 1]);
+        v[2 * j] = mul2(v[2 * j], both(step[k]));
+        v[2 * j + 1] = mul2(v[2 * j + 1], both(step[k]));
+      }
+      if (c + 16 <= H) {
+        if (DT) {
+          float4* d = reinterpret_cast<float4*>(static_cast<float*>(a.x) + row * a.ldx + c);
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            reinterpret_cast<float4*>(d)[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+          for (int j = 0; j < 4; ++j) d[j] = make_float4(v[2 * j].x, v[2 * j].y, v[2 * j + 1].x, v[2 * j + 1].y);
         } else {
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (c + j < H) d[j] = v[j];
-        }
-      } else {
-        __nv_bfloat16* d = static_cast<__nv_bfloat16*>(a.x) + row * a.ldx + c;
-        if (c + 16 <= H) {
           uint32_t o[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[j].x, v[j].y);
             o[j] = *reinterpret_cast<const uint32_t*>(&h);
           }
-          reinterpret_cast<uint4*>(d)[0] = make_uint4(o[0], o[1], o[2], o[3]);
-          reinterpret_cast<uint4*>(d)[1] = make_uint4(o[4], o[5], o[6], o[7]);
-        } else {
+          uint4* d = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.x) + row * a.ldx + c);
+          d[0] = make_uint4(o[0], o[1], o[2], o[3]);
+          d[1] = make_uint4(o[4], o[5], o[6], o[7]);
+        }
+      } else {
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (c + j < H) d[j] = __float2bfloat16_rn(v[j]);
+        for (int j = 0; j < 16; ++j) {
+          if (c + j >= H) continue;
+          const float f = j % 2 ? v[j / 2].y : v[j / 2].x;
+          if (DT) static_cast<float*>(a.x)[row * a.ldx + c + j] = f;
+          else static_cast<__nv_bfloat16*>(a.x)[row * a.ldx + c + j] = __float2bfloat16_rn(f);
         }
       }
     }

@@ -33,6 +33,31 @@ __device__ __forceinline__ int ck_code(float x, uint32_t byte) {
   const int q = __float2int_rn(__fmul_rn(x, ck_inv_step(byte)));
   return byte == kCkTop ? max(-63, min(63, q)) : q;
 }
+// Four codes as the bytes of a word, of finite numbers in blocks with a step
+// below the topmost (byte < kCkTop): adding 1.5 2^23 to the exact x / step rounds
+// it to nearest even and leaves its low byte in the sum's.
+__device__ __forceinline__ uint32_t ck_pack4(float2 a, float2 b, float inv) {
+  const float2 magic = both(12582912.f);
+  a = fma2(a, both(inv), magic);
+  b = fma2(b, both(inv), magic);
+  const uint32_t lo = __byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040);
+  const uint32_t hi = __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040);
+  return __byte_perm(lo, hi, 0x5410);
+}
+__device__ __forceinline__ uint32_t ck_pack4_any(float2 a, float2 b, uint32_t byte) {
+  return ((uint32_t)ck_code(a.x, byte) & 255u) | ((uint32_t)ck_code(a.y, byte) & 255u) << 8 |
+         ((uint32_t)ck_code(b.x, byte) & 255u) << 16 | (uint32_t)ck_code(b.y, byte) << 24;
+}
+// The four codes of a word as floats: a byte (plus 128) under the exponent of
+// 2^23 reads as 2^23 + code + 128.
+__device__ __forceinline__ void ck_unpack4(uint32_t w, float2& a, float2& b) {
+  w ^= 0x80808080u;
+  const float2 off = both(-8388736.f);
+  a = add2(make_float2(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440)),
+                       __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7441))), off);
+  b = add2(make_float2(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7442)),
+                       __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7443))), off);
+}
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 
 }  // namespace rlk

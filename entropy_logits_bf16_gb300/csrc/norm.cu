@@ -158,12 +158,11 @@ __global__ void __launch_bounds__(256) norm_param_wide_kernel(NormBwdArgs a, int
 constexpr int kMaxGroup = 512;       // threads of a row, at most
 constexpr int64_t kOnChip = 32 * kMaxGroup;
 
-// Column of element e of thread t in a group of n threads: VW columns at a
-// time, consecutive threads on consecutive ones.
-template <int VW>
-__device__ __forceinline__ int col_of(int e, int t, int n) {
-  return ((e / VW) * n + t) * VW + e % VW;
-}
+// Element e of a thread's E columns is column ((e / VW) n + t) VW + e % VW: VW
+// columns at a time, consecutive threads on consecutive ones.  They are held
+// as pairs, so that most of the arithmetic goes two elements an instruction
+// (these kernels would otherwise be bound by issue).  FULL: the threads'
+// columns are exactly the row's (VW = 8), and nothing needs a bounds check.
 
 // The same number, but computed anew by the compiler: column offsets that
 // depend on it are not kept in registers over all rows.
@@ -171,86 +170,14 @@ __device__ __forceinline__ int fresh(int n) {
   asm volatile("" : "+r"(n));
   return n;
 }
-
-// A thread's columns of a row (0 past the end).
-template <int VW, int E>
-__device__ __forceinline__ void load_cols(const void* p, int dtype, int64_t at, int H, int t, int n,
-                                          float (&v)[E]) {
-  if (VW == 8) {
-#pragma unroll
-    for (int k = 0; k < E / 8; ++k) {
-      const int c = (k * n + t) * 8;
-      float* o = v + k * 8;
-      if (c + 8 <= H) {
-        if (dtype) {
-          const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + at + c);
-          const float4 b = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + at + c + 4);
-          o[0] = a.x; o[1] = a.y; o[2] = a.z; o[3] = a.w;
-          o[4] = b.x; o[5] = b.y; o[6] = b.z; o[7] = b.w;
-        } else {
-          const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at + c);
-          o[0] = bf16_lo(q.x); o[1] = bf16_hi(q.x); o[2] = bf16_lo(q.y); o[3] = bf16_hi(q.y);
-          o[4] = bf16_lo(q.z); o[5] = bf16_hi(q.z); o[6] = bf16_lo(q.w); o[7] = bf16_hi(q.w);
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = c + j < H ? ld_elem(p, dtype, at + c + j) : 0.f;
-      }
-    }
-  } else {
-    n = fresh(n);
-    if (dtype) {
-      const float* q = static_cast<const float*>(p) + at + t;
-#pragma unroll
-      for (int e = 0; e < E; ++e) v[e] = e * n < H - t ? q[e * n] : 0.f;
-    } else {
-      const uint16_t* q = static_cast<const uint16_t*>(p) + at + t;
-#pragma unroll
-      for (int e = 0; e < E; ++e) v[e] = e * n < H - t ? bf16_val(q[e * n]) : 0.f;
-    }
-  }
+__device__ __forceinline__ uint32_t pack_bf16(float2 v) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
-template <int VW, int E>
-__device__ __forceinline__ void store_cols(void* p, int dtype, int64_t at, int H, int t, int n, const float (&v)[E]) {
-  if (VW == 8) {
-#pragma unroll
-    for (int k = 0; k < E / 8; ++k) {
-      const int c = (k * n + t) * 8;
-      const float* o = v + k * 8;
-      if (c + 8 <= H) {
-        if (dtype) {
-          float4* d = reinterpret_cast<float4*>(static_cast<float*>(p) + at + c);
-          d[0] = make_float4(o[0], o[1], o[2], o[3]);
-          d[1] = make_float4(o[4], o[5], o[6], o[7]);
-        } else {
-          uint32_t q[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const __nv_bfloat162 h2 = __floats2bfloat162_rn(o[2 * j], o[2 * j + 1]);
-            q[j] = *reinterpret_cast<const uint32_t*>(&h2);
-          }
-          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + at + c) = make_uint4(q[0], q[1], q[2], q[3]);
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (c + j < H) st_elem(p, dtype, at + c + j, o[j]);
-      }
-    }
-  } else {
-    n = fresh(n);
-    if (dtype) {
-      float* q = static_cast<float*>(p) + at + t;
-#pragma unroll
-      for (int e = 0; e < E; ++e)
-        if (e * n < H - t) q[e * n] = v[e];
-    } else {
-      __nv_bfloat16* q = static_cast<__nv_bfloat16*>(p) + at + t;
-#pragma unroll
-      for (int e = 0; e < E; ++e)
-        if (e * n < H - t) q[e * n] = __float2bfloat16_rn(v[e]);
-    }
-  }
+// element e of a thread's pairs
+template <int E>
+__device__ __forceinline__ float& elem(float2 (&v)[E / 2], int e) {
+  return e % 2 ? v[e / 2].y : v[e / 2].x;
 }
 
 // The threads of a row: n of them, either a power of two up to 128 with several
@@ -267,40 +194,135 @@ struct Group {
   }
 };
 
-// Sums of two values over the group, in a fixed order, on every thread.  `buf`
+// Sums of NV values over the group, in a fixed order, on every thread.  `buf`
 // alternates between two halves of s_red, so one barrier a sum is enough.
-__device__ __forceinline__ float2 group_sum(float2 v, const Group& g, float2* s_red, int& buf) {
+template <int NV>
+__device__ __forceinline__ void group_sum(float (&v)[NV], const Group& g, float* s_red, int& buf) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int o = (g.n < 32 ? g.n : 32) / 2; o > 0; o >>= 1) {
-    v.x = __fadd_rn(v.x, __shfl_xor_sync(0xFFFFFFFFu, v.x, o));
-    v.y = __fadd_rn(v.y, __shfl_xor_sync(0xFFFFFFFFu, v.y, o));
-  }
-  if (g.n > 32) {
-    float2* s = s_red + buf * 32;
-    buf ^= 1;
-    if (lane == 0) s[warp] = v;
-    __syncthreads();
-    const int nw = g.n / 32, at = lane & 15;   // at most 16 warps
-    v = at < nw ? s[g.index * nw + at] : make_float2(0.f, 0.f);
+  if (g.n >= 32) {
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) {
-      v.x = __fadd_rn(v.x, __shfl_xor_sync(0xFFFFFFFFu, v.x, o));
-      v.y = __fadd_rn(v.y, __shfl_xor_sync(0xFFFFFFFFu, v.y, o));
+    for (int o = 16; o > 0; o >>= 1) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k) v[k] = __fadd_rn(v[k], __shfl_xor_sync(0xFFFFFFFFu, v[k], o));
+    }
+  } else {
+    for (int o = g.n / 2; o > 0; o >>= 1) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k) v[k] = __fadd_rn(v[k], __shfl_xor_sync(0xFFFFFFFFu, v[k], o));
     }
   }
-  return v;
+  if (g.n <= 32) return;
+  float* s = s_red + buf;
+  buf ^= 64;
+  if (lane == 0) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) s[warp * NV + k] = v[k];
+  }
+  __syncthreads();
+  const int nw = g.n / 32, at = lane & 15;   // at most 16 warps
+#pragma unroll
+  for (int k = 0; k < NV; ++k) v[k] = at < nw ? s[(g.index * nw + at) * NV + k] : 0.f;
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) v[k] = __fadd_rn(v[k], __shfl_xor_sync(0xFFFFFFFFu, v[k], o));
+  }
+}
+
+// A thread's columns of a row or of a parameter vector (0 past the end).
+template <int VW, int E, bool FULL>
+__device__ __forceinline__ void load_cols(const void* p, int dtype, int64_t at, int H, const Group& g,
+                                          float2 (&v)[E / 2]) {
+  if (VW == 8) {
+#pragma unroll
+    for (int k = 0; k < E / 8; ++k) {
+      const int c = (k * g.n + g.t) * 8;
+      float2* o = v + k * 4;
+      if (FULL || c + 8 <= H) {
+        if (dtype) {
+          const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at + c);
+          const float4 a = q[0], b = q[1];
+          o[0] = make_float2(a.x, a.y); o[1] = make_float2(a.z, a.w);
+          o[2] = make_float2(b.x, b.y); o[3] = make_float2(b.z, b.w);
+        } else {
+          const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at + c);
+          o[0] = bf16x2_to_f2(q.x); o[1] = bf16x2_to_f2(q.y); o[2] = bf16x2_to_f2(q.z); o[3] = bf16x2_to_f2(q.w);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) elem<E>(v, 8 * k + j) = c + j < H ? ld_elem(p, dtype, at + c + j) : 0.f;
+      }
+    }
+  } else {
+    const int n = fresh(g.n), left = H - g.t;
+    if (dtype) {
+      const float* q = static_cast<const float*>(p) + at + g.t;
+#pragma unroll
+      for (int e = 0; e < E; ++e) elem<E>(v, e) = e * n < left ? q[e * n] : 0.f;
+    } else {
+      const uint16_t* q = static_cast<const uint16_t*>(p) + at + g.t;
+#pragma unroll
+      for (int e = 0; e < E; ++e) elem<E>(v, e) = e * n < left ? bf16_val(q[e * n]) : 0.f;
+    }
+  }
+}
+template <int VW, int E, bool FULL>
+__device__ __forceinline__ void store_cols(void* p, int dtype, int64_t at, int H, const Group& g, float2 (&v)[E / 2]) {
+  if (VW == 8) {
+#pragma unroll
+    for (int k = 0; k < E / 8; ++k) {
+      const int c = (k * g.n + g.t) * 8;
+      const float2* o = v + k * 4;
+      if (FULL || c + 8 <= H) {
+        if (dtype) {
+          float4* d = reinterpret_cast<float4*>(static_cast<float*>(p) + at + c);
+          d[0] = make_float4(o[0].x, o[0].y, o[1].x, o[1].y);
+          d[1] = make_float4(o[2].x, o[2].y, o[3].x, o[3].y);
+        } else {
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + at + c) =
+              make_uint4(pack_bf16(o[0]), pack_bf16(o[1]), pack_bf16(o[2]), pack_bf16(o[3]));
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (c + j < H) st_elem(p, dtype, at + c + j, elem<E>(v, 8 * k + j));
+      }
+    }
+  } else {
+    const int n = fresh(g.n), left = H - g.t;
+    if (dtype) {
+      float* q = static_cast<float*>(p) + at + g.t;
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (e * n < left) q[e * n] = elem<E>(v, e);
+    } else {
+      __nv_bfloat16* q = static_cast<__nv_bfloat16*>(p) + at + g.t;
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (e * n < left) q[e * n] = __float2bfloat16_rn(elem<E>(v, e));
+    }
+  }
 }
 
 // The thread's columns of the row's checkpoint.  VW = 8: a block of 32 columns
-// is 4 neighbouring threads'; VW = 1: a warp's.
-template <int VW, int E>
-__device__ __forceinline__ void write_checkpoint(const CheckpointView& ck, int64_t t_row, bool live, int H, int t, int n,
-                                                 const float (&x)[E]) {
+// is 4 neighbouring threads'; VW = 1: a warp's.  `finite`: the whole row is.
+template <int VW, int E, bool FULL>
+__device__ __forceinline__ void write_checkpoint(const CheckpointView& ck, int64_t row, bool live, bool finite, int H,
+                                                 const Group& g, float2 (&x)[E / 2]) {
+  int8_t* codes = ck.codes + row * ck.ldc;
+  uint8_t* scales = ck.scales + row * ck.lds;
 #pragma unroll
   for (int k = 0; k < E / VW; ++k) {
     uint32_t amax = 0u;
+    if (finite) {
+      float f = 0.f;
 #pragma unroll
-    for (int j = 0; j < VW; ++j) amax = max(amax, abs_bits(x[k * VW + j]));
+      for (int j = 0; j < VW; ++j) f = fmaxf(f, fabsf(elem<E>(x, k * VW + j)));
+      amax = __float_as_uint(f);
+    } else {
+#pragma unroll
+      for (int j = 0; j < VW; ++j) amax = max(amax, abs_bits(elem<E>(x, k * VW + j)));
+    }
     if (VW == 8) {
       amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
       amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
@@ -308,24 +330,27 @@ __device__ __forceinline__ void write_checkpoint(const CheckpointView& ck, int64
       amax = __reduce_max_sync(0xFFFFFFFFu, amax);
     }
     const uint32_t byte = ck_scale_byte(amax);
-    const int c = (k * n + t) * VW;
-    if (!live || c >= H) continue;
-    int8_t* dst = ck.codes + t_row * ck.ldc + c;
-    if (VW == 8) {
-      uint32_t q[2] = {0u, 0u};
-#pragma unroll
-      for (int j = 0; j < 8; ++j) q[j / 4] |= ((uint32_t)ck_code(x[k * 8 + j], byte) & 255u) << (8 * (j % 4));
-      if (c + 8 <= H) {
-        *reinterpret_cast<uint2*>(dst) = make_uint2(q[0], q[1]);
+    const int c = (k * g.n + g.t) * VW;
+    if (!live || (!FULL && c >= H)) continue;
+    if constexpr (VW == 8) {
+      uint2 q;
+      if (byte < kCkTop) {
+        const float inv = ck_inv_step(byte);
+        q = make_uint2(ck_pack4(x[4 * k], x[4 * k + 1], inv), ck_pack4(x[4 * k + 2], x[4 * k + 3], inv));
+      } else {
+        q = make_uint2(ck_pack4_any(x[4 * k], x[4 * k + 1], byte), ck_pack4_any(x[4 * k + 2], x[4 * k + 3], byte));
+      }
+      if (FULL || c + 8 <= H) {
+        *reinterpret_cast<uint2*>(codes + c) = q;
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (c + j < H) dst[j] = (int8_t)(q[j / 4] >> (8 * (j % 4)));
+          if (c + j < H) codes[c + j] = (int8_t)((j < 4 ? q.x : q.y) >> (8 * (j % 4)));
       }
     } else {
-      *dst = (int8_t)ck_code(x[k], byte);
+      codes[c] = (int8_t)ck_code(elem<E>(x, k), byte);
     }
-    if (c % kCkBlock == 0) ck.scales[t_row * ck.lds + c / kCkBlock] = (uint8_t)byte;
+    if (c % kCkBlock == 0) scales[c / kCkBlock] = (uint8_t)byte;
   }
 }
 
@@ -371,7 +396,7 @@ __device__ __forceinline__ int to_boundary(const void* p) { return (int)(-reinte
 
 // Starts the copy of a row (at element `at` of p) into its place, and returns the
 // edge element that this thread has to store there when it is used (VW = 1).
-template <int TYPE, int VW, int E>
+template <int TYPE, int VW, int E, bool FULL>
 __device__ __forceinline__ uint32_t start_row(uint8_t* place, const void* p, int64_t at, int H, const Group& g) {
   constexpr int es = bytes_of(TYPE);
   const char* src = static_cast<const char*>(p) + at * es;
@@ -380,8 +405,8 @@ __device__ __forceinline__ uint32_t start_row(uint8_t* place, const void* p, int
 #pragma unroll
     for (int k = 0; k < E / 8; ++k) {
       const int c = (k * g.n + g.t) * 8;
-      const int have = (H - c < 8 ? H - c : 8) * es;
-      if (have <= 0) continue;
+      const int have = FULL ? 8 * es : (H - c < 8 ? H - c : 8) * es;
+      if (!FULL && have <= 0) continue;
       if (TYPE == kFromCk) {
         cp_async8(dst + c, src + c, have);
       } else {
@@ -412,66 +437,69 @@ __device__ __forceinline__ void store_edge(uint8_t* place, const void* p, int64_
   else *reinterpret_cast<uint16_t*>(d) = (uint16_t)v;
 }
 
-// Codes q0..q3 of a word as floats: a byte under the exponent of 2^23 reads as
-// 2^23 + (q + 128).
-__device__ __forceinline__ float code_value(uint32_t flipped, int j) {
-  return __fsub_rn(__uint_as_float(__byte_perm(flipped, 0x4B000000u, 0x7440 + j)), 8388736.f);
-}
-
-// A thread's columns of a row in shared memory (0 past the end).  VW = 8: only
-// what this thread copied itself; VW = 1: after a barrier.
-template <int TYPE, int VW, int E>
+// A thread's columns of a row in shared memory (0 past the end; codes times
+// their steps).  VW = 8: only what this thread copied itself; VW = 1: after a barrier.
+template <int TYPE, int VW, int E, bool FULL>
 __device__ __forceinline__ void take_row(const uint8_t* place, const void* p, int64_t at, int H, const Group& g,
-                                         const float (&step)[VW == 8 ? E / 8 : E], float (&v)[E]) {
+                                         const float (&step)[VW == 8 ? E / 8 : E], float2 (&v)[E / 2]) {
   constexpr int es = bytes_of(TYPE);
-  if (VW == 8) {
+  if constexpr (VW == 8) {
 #pragma unroll
     for (int k = 0; k < E / 8; ++k) {
       const int c = (k * g.n + g.t) * 8;
       const uint8_t* s = place + c * es;
-      float* o = v + 8 * k;
+      float2* o = v + 4 * k;
       if (TYPE == 1) {
         const float4 a = reinterpret_cast<const float4*>(s)[0], b = reinterpret_cast<const float4*>(s)[1];
-        o[0] = a.x; o[1] = a.y; o[2] = a.z; o[3] = a.w;
-        o[4] = b.x; o[5] = b.y; o[6] = b.z; o[7] = b.w;
+        o[0] = make_float2(a.x, a.y); o[1] = make_float2(a.z, a.w);
+        o[2] = make_float2(b.x, b.y); o[3] = make_float2(b.z, b.w);
       } else if (TYPE == 0) {
         const uint4 q = *reinterpret_cast<const uint4*>(s);
-        o[0] = bf16_lo(q.x); o[1] = bf16_hi(q.x); o[2] = bf16_lo(q.y); o[3] = bf16_hi(q.y);
-        o[4] = bf16_lo(q.z); o[5] = bf16_hi(q.z); o[6] = bf16_lo(q.w); o[7] = bf16_hi(q.w);
+        o[0] = bf16x2_to_f2(q.x); o[1] = bf16x2_to_f2(q.y); o[2] = bf16x2_to_f2(q.z); o[3] = bf16x2_to_f2(q.w);
       } else {
         const uint2 q = *reinterpret_cast<const uint2*>(s);
-        const uint32_t w2[2] = {q.x ^ 0x80808080u, q.y ^ 0x80808080u};
+        ck_unpack4(q.x, o[0], o[1]);
+        ck_unpack4(q.y, o[2], o[3]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = __fmul_rn(code_value(w2[j / 4], j % 4), step[k]);
+        for (int j = 0; j < 4; ++j) o[j] = mul2(o[j], both(step[k]));
       }
-      if (c + 8 > H) {
+      if (!FULL && c + 8 > H) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (c + j >= H) o[j] = 0.f;
+          if (c + j >= H) elem<E>(v, 8 * k + j) = 0.f;
       }
     }
-    return;
-  }
-  const uint8_t* s = place + ((reinterpret_cast<uintptr_t>(p) + at * es) & 15u) + g.t * es;
-  const int n = fresh(g.n), left = H - g.t;
+  } else {
+    const uint8_t* s = place + ((reinterpret_cast<uintptr_t>(p) + at * es) & 15u) + g.t * es;
+    const int n = fresh(g.n), left = H - g.t;
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const uint8_t* q = s + e * n * es;
-    if (e * n >= left) v[e] = 0.f;
-    else if (TYPE == 1) v[e] = *reinterpret_cast<const float*>(q);
-    else if (TYPE == 0) v[e] = bf16_val(*reinterpret_cast<const uint16_t*>(q));
-    else v[e] = __fmul_rn((float)*reinterpret_cast<const int8_t*>(q), step[VW == 8 ? 0 : e]);
+    for (int e = 0; e < E; ++e) {
+      const uint8_t* q = s + e * n * es;
+      float f = 0.f;
+      if (e * n < left) {
+        if (TYPE == 1) f = *reinterpret_cast<const float*>(q);
+        else if (TYPE == 0) f = bf16_val(*reinterpret_cast<const uint16_t*>(q));
+        else f = __fmul_rn((float)*reinterpret_cast<const int8_t*>(q), step[e]);
+      }
+      elem<E>(v, e) = f;
+    }
   }
+}
+
+template <int E>
+__device__ __forceinline__ void fill(float2 (&v)[E / 2], float f) {
+#pragma unroll
+  for (int j = 0; j < E / 2; ++j) v[j] = both(f);
 }
 
 // ---- forward
 // Persistent: a group takes rows index, + stride, ..., `depth` of them (1, 2, 4) on
 // their way to shared memory ahead of the one at work.  E = 16 keeps its columns of
 // weight and bias in registers.
-template <int XT, int VW, int E>
+template <int XT, int VW, int E, bool FULL>
 __global__ void __launch_bounds__(kMaxGroup, 1) norm_fwd_kernel(NormArgs a, int n, int depth) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float2 s_red[64];
+  __shared__ float s_red[128];
   int buf = 0;
   const Group g(n);
   const int H = (int)a.H;
@@ -487,75 +515,62 @@ __global__ void __launch_bounds__(kMaxGroup, 1) norm_fwd_kernel(NormArgs a, int 
   auto start = [&](int i) -> uint32_t {
     const int64_t row = row0 + g.index + i * stride;
     uint32_t e = 0u;
-    if (i < iters && row < a.T) e = start_row<XT, VW, E>(mine + (i & (depth - 1)) * size, a.x, row * a.ldx, H, g);
+    if (i < iters && row < a.T) e = start_row<XT, VW, E, FULL>(mine + (i & (depth - 1)) * size, a.x, row * a.ldx, H, g);
     cp_commit();
     return e;
   };
   edge[0] = start(0);
   if (depth > 1) edge[1] = start(1);
   for (int i = 2; i < depth; ++i) start(i);
+
   constexpr bool KEEP = E == 16;
-  float w[KEEP ? E : 1], b[KEEP ? E : 1];
+  float2 w[KEEP ? E / 2 : 1], b[KEEP ? E / 2 : 1];
   if constexpr (KEEP) {
-    if (a.weight) load_cols<VW>(a.weight, a.param_dtype, 0, H, g.t, n, w);
-    if (a.bias) load_cols<VW>(a.bias, a.param_dtype, 0, H, g.t, n, b);
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      if (!a.weight) w[e] = 1.f;
-      if (!a.bias) b[e] = 0.f;
-    }
+    if (a.weight) load_cols<VW, E, FULL>(a.weight, a.param_dtype, 0, H, g, w);
+    else fill<E>(w, 1.f);
+    if (a.bias) load_cols<VW, E, FULL>(a.bias, a.param_dtype, 0, H, g, b);
+    else fill<E>(b, 0.f);
   }
 
   for (int i = 0; i < iters; ++i) {
     const int64_t row = row0 + g.index + i * stride;
     const bool live = row < a.T;
     uint8_t* place = mine + (i & (depth - 1)) * size;
-    float x[E];
+    float2 x[E / 2];
     if (VW == 1 && live) store_edge<XT>(place, a.x, row * a.ldx, H, g, edge[0]);
     cp_wait(depth);
     if (VW == 1) g.sync();
-    if (live) {
-      take_row<XT, VW, E>(place, a.x, row * a.ldx, H, g, none, x);
-    } else {
-#pragma unroll
-      for (int e = 0; e < E; ++e) x[e] = 0.f;
-    }
+    if (live) take_row<XT, VW, E, FULL>(place, a.x, row * a.ldx, H, g, none, x);
+    else fill<E>(x, 0.f);
     if (VW == 8) start(i + depth);   // into the place just read: a thread reads only what it copied itself
     float m = 0.f;
     if (!a.rms) {
-      float s = 0.f;
+      float2 s = x[0];
 #pragma unroll
-      for (int e = 0; e < E; ++e) s = __fadd_rn(s, x[e]);
-      m = __fmul_rn(group_sum(make_float2(s, 0.f), g, s_red, buf).x, inv_h);
+      for (int j = 1; j < E / 2; ++j) s = add2(s, x[j]);
+      float v[1] = {__fadd_rn(s.x, s.y)};
+      group_sum(v, g, s_red, buf);
+      m = __fmul_rn(v[0], inv_h);
     }
-    float s = 0.f;
-    if (VW == 8) {
+    float2 s = both(0.f);
+    if (FULL || a.rms) {   // with m = 0 the zeros past the end add nothing
 #pragma unroll
-      for (int k = 0; k < E / 8; ++k) {
-        const int c = (k * n + g.t) * 8;
-        if (c + 8 <= H) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float d = __fsub_rn(x[8 * k + j], m);
-            s = __fmaf_rn(d, d, s);
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float d = c + j < H ? __fsub_rn(x[8 * k + j], m) : 0.f;
-            s = __fmaf_rn(d, d, s);
-          }
-        }
+      for (int j = 0; j < E / 2; ++j) {
+        const float2 d = add2(x[j], both(-m));
+        s = fma2(d, d, s);
       }
     } else {
-      const int n2 = fresh(n), left = H - g.t;
+      const int n2 = fresh(n);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const float d = e * n2 < left ? __fsub_rn(x[e], m) : 0.f;
-        s = __fmaf_rn(d, d, s);
+        const int c = ((e / VW) * n2 + g.t) * VW + e % VW;
+        const float d = c < H ? __fsub_rn(elem<E>(x, e), m) : 0.f;
+        s.x = __fmaf_rn(d, d, s.x);
       }
     }
-    const float var = __fmul_rn(group_sum(make_float2(s, 0.f), g, s_red, buf).x, inv_h);
+    float v[1] = {__fadd_rn(s.x, s.y)};
+    group_sum(v, g, s_red, buf);
+    const float var = __fmul_rn(v[0], inv_h);
     if (VW == 1) {   // the sum's barrier: every thread has read the place
       if (n <= 32) __syncwarp();
       const uint32_t e = start(i + depth);
@@ -574,27 +589,26 @@ __global__ void __launch_bounds__(kMaxGroup, 1) norm_fwd_kernel(NormArgs a, int 
       if (a.rstd) a.rstd[row] = r;
       if (bad && a.status) atomicOr(a.status, RLK_STATUS_NONFINITE);
     }
-    if (a.ck.codes) write_checkpoint<VW>(a.ck, row, live, H, g.t, n, x);
-    if constexpr (KEEP) {
+    if (a.ck.codes) write_checkpoint<VW, E, FULL>(a.ck, row, live, !bad, H, g, x);
 #pragma unroll
-      for (int e = 0; e < E; ++e) x[e] = __fmaf_rn(__fmul_rn(__fsub_rn(x[e], m), r), w[e], b[e]);
-    } else {
-      float p[E];
+    for (int j = 0; j < E / 2; ++j) {
+      x[j] = mul2(add2(x[j], both(-m)), both(r));
+      if constexpr (KEEP) x[j] = fma2(x[j], w[j], b[j]);
+    }
+    if constexpr (!KEEP) {
+      float2 p[E / 2];
       if (a.weight) {
-        load_cols<VW>(a.weight, a.param_dtype, 0, H, g.t, n, p);
+        load_cols<VW, E, FULL>(a.weight, a.param_dtype, 0, H, g, p);
 #pragma unroll
-        for (int e = 0; e < E; ++e) x[e] = __fmul_rn(__fmul_rn(__fsub_rn(x[e], m), r), p[e]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < E; ++e) x[e] = __fmul_rn(__fsub_rn(x[e], m), r);
+        for (int j = 0; j < E / 2; ++j) x[j] = mul2(x[j], p[j]);
       }
       if (a.bias) {
-        load_cols<VW>(a.bias, a.param_dtype, 0, H, g.t, n, p);
+        load_cols<VW, E, FULL>(a.bias, a.param_dtype, 0, H, g, p);
 #pragma unroll
-        for (int e = 0; e < E; ++e) x[e] = __fadd_rn(x[e], p[e]);
+        for (int j = 0; j < E / 2; ++j) x[j] = add2(x[j], p[j]);
       }
     }
-    if (live) store_cols<VW>(a.y, a.y_dtype, row * a.ldy, H, g.t, n, x);
+    if (live) store_cols<VW, E, FULL>(a.y, a.y_dtype, row * a.ldy, H, g, x);
   }
 }
 
@@ -603,17 +617,17 @@ __global__ void __launch_bounds__(kMaxGroup, 1) norm_fwd_kernel(NormArgs a, int 
 // forward; `depth` 0: a row is loaded when its turn comes (rows that do not fit).
 // E = 32: the partial dw, db live in shared memory (a thread has no registers for
 // 32 columns of them).
-template <int XT, int DT, int VW, int E>
+template <int XT, int DT, int VW, int E, bool FULL>
 __global__ void __launch_bounds__(kMaxGroup, 1) norm_bwd_kernel(NormBwdArgs a, int n, int depth) {
   constexpr bool SACC = E == 32;
   constexpr int STEPS = VW == 8 ? E / 8 : E;
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float2 s_red[64];
+  __shared__ float s_red[128];
   int buf = 0;
   const Group g(n);
   const int H = (int)a.H;
   const float inv_h = __fdiv_rn(1.f, (float)H);
-  float* s_acc = reinterpret_cast<float*>(smem);   // SACC: [2][E n]
+  float2* s_acc = reinterpret_cast<float2*>(smem);   // SACC: [2][E / 2][n]
   const int dy_size = place_bytes<DT, VW, E>(H, n), size = dy_size + place_bytes<XT, VW, E>(H, n);
   uint8_t* mine = smem + (SACC ? 2 * E * n * 4 : 0) + (size_t)g.index * depth * size;
   const int64_t stride = (int64_t)gridDim.x * g.count, row0 = (int64_t)blockIdx.x * g.count;
@@ -628,8 +642,8 @@ __global__ void __launch_bounds__(kMaxGroup, 1) norm_bwd_kernel(NormBwdArgs a, i
     const int64_t row = row0 + g.index + i * stride;
     uint2 e = make_uint2(0u, 0u);
     if (i < iters && row < a.T) {
-      e.x = start_row<DT, VW, E>(place(i), a.dy, row * a.lddy, H, g);
-      e.y = start_row<XT, VW, E>(place(i) + dy_size, xp, row * ldx, H, g);
+      e.x = start_row<DT, VW, E, FULL>(place(i), a.dy, row * a.lddy, H, g);
+      e.y = start_row<XT, VW, E, FULL>(place(i) + dy_size, xp, row * ldx, H, g);
     }
     cp_commit();
     return e;
@@ -651,26 +665,22 @@ __global__ void __launch_bounds__(kMaxGroup, 1) norm_bwd_kernel(NormBwdArgs a, i
 #pragma unroll
       for (int k = 0; k < STEPS; ++k) {
         const int c = (k * n2 + g.t) * VW;
-        byte1[k] = in && c < H ? sc[c / kCkBlock] : 1u;
+        byte1[k] = in && (FULL || c < H) ? sc[c / kCkBlock] : 1u;
       }
     }
   };
   ahead(0);
 
-  float w[E], dw[SACC ? 1 : E], db[SACC ? 1 : E];
+  float2 w[E / 2], dw[SACC ? 1 : E / 2], db[SACC ? 1 : E / 2];
   auto load_w = [&]() {
-    if (a.weight) {
-      load_cols<VW>(a.weight, a.param_dtype, 0, H, g.t, n, w);
-    } else {
-#pragma unroll
-      for (int e = 0; e < E; ++e) w[e] = 1.f;
-    }
+    if (a.weight) load_cols<VW, E, FULL>(a.weight, a.param_dtype, 0, H, g, w);
+    else fill<E>(w, 1.f);
   };
   if (!SACC) load_w();   // else with each row: there are no registers to keep it in
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    if (SACC) s_acc[e * n + g.t] = s_acc[(E + e) * n + g.t] = 0.f;
-    else dw[e] = db[e] = 0.f;
+  for (int j = 0; j < E / 2; ++j) {
+    if (SACC) s_acc[j * n + g.t] = s_acc[(E / 2 + j) * n + g.t] = both(0.f);
+    else dw[j] = db[j] = both(0.f);
   }
 
   for (int i = 0; i < iters; ++i) {
@@ -682,7 +692,11 @@ __global__ void __launch_bounds__(kMaxGroup, 1) norm_bwd_kernel(NormBwdArgs a, i
 #pragma unroll
       for (int k = 0; k < STEPS; ++k) step[k] = ck_step(byte1[k]);
     }
-    float dy[E], h[E];
+    float2 dy[E / 2], h[E / 2];
+    if (!live) {
+      fill<E>(dy, 0.f);
+      fill<E>(h, 0.f);
+    }
     if (depth > 0) {
       if (VW == 1 && live) {
         store_edge<DT>(place(i), a.dy, row * a.lddy, H, g, edge[0].x);
@@ -691,47 +705,44 @@ __global__ void __launch_bounds__(kMaxGroup, 1) norm_bwd_kernel(NormBwdArgs a, i
       cp_wait(depth);
       if (VW == 1) g.sync();
       if (live) {
-        take_row<DT, VW, E>(place(i), a.dy, row * a.lddy, H, g, step, dy);
-        take_row<XT, VW, E>(place(i) + dy_size, xp, row * ldx, H, g, step, h);
+        take_row<DT, VW, E, FULL>(place(i), a.dy, row * a.lddy, H, g, step, dy);
+        take_row<XT, VW, E, FULL>(place(i) + dy_size, xp, row * ldx, H, g, step, h);
       }
       if (VW == 8) start(i + depth);   // into the place just read: a thread reads only what it copied itself
     } else if (live) {
-      load_cols<VW>(a.dy, DT, row * a.lddy, H, g.t, n, dy);
+      load_cols<VW, E, FULL>(a.dy, DT, row * a.lddy, H, g, dy);
       if (XT == kFromCk) {
         const int n2 = fresh(n);
         const int8_t* q = a.ck.codes + row * a.ck.ldc;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          const int c = col_of<VW>(e, g.t, n2);
-          h[e] = c < H ? __fmul_rn((float)q[c], step[VW == 8 ? e / 8 : e]) : 0.f;
+          const int c = ((e / VW) * n2 + g.t) * VW + e % VW;
+          elem<E>(h, e) = c < H ? __fmul_rn((float)q[c], step[VW == 8 ? e / 8 : e]) : 0.f;
         }
       } else {
-        load_cols<VW>(a.x, XT, row * a.ldx, H, g.t, n, h);
+        load_cols<VW, E, FULL>(a.x, XT, row * a.ldx, H, g, h);
       }
-    }
-    if (!live) {
-#pragma unroll
-      for (int e = 0; e < E; ++e) dy[e] = h[e] = 0.f;
     }
     ahead(i + 1);
     if (SACC) load_w();
-    float2 s = make_float2(0.f, 0.f);
+    float2 s1 = both(0.f), s2 = both(0.f);
 #pragma unroll
-    for (int e = 0; e < E; ++e) {   // past the row dy is 0, and h does not matter
-      h[e] = __fmul_rn(__fsub_rn(h[e], m), r);
-      const float gr = __fmul_rn(dy[e], w[e]);
-      s.x = __fadd_rn(s.x, gr);
-      s.y = __fmaf_rn(gr, h[e], s.y);
+    for (int j = 0; j < E / 2; ++j) {   // past the row dy is 0, and h does not matter
+      h[j] = mul2(add2(h[j], both(-m)), both(r));
+      const float2 gr = mul2(dy[j], w[j]);
+      s1 = add2(s1, gr);
+      s2 = fma2(gr, h[j], s2);
       if (SACC) {
-        s_acc[e * n + g.t] = __fmaf_rn(dy[e], h[e], s_acc[e * n + g.t]);
-        s_acc[(E + e) * n + g.t] = __fadd_rn(s_acc[(E + e) * n + g.t], dy[e]);
+        s_acc[j * n + g.t] = fma2(dy[j], h[j], s_acc[j * n + g.t]);
+        s_acc[(E / 2 + j) * n + g.t] = add2(s_acc[(E / 2 + j) * n + g.t], dy[j]);
       } else {
-        dw[e] = __fmaf_rn(dy[e], h[e], dw[e]);
-        db[e] = __fadd_rn(db[e], dy[e]);
+        dw[j] = fma2(dy[j], h[j], dw[j]);
+        db[j] = add2(db[j], dy[j]);
       }
-      dy[e] = gr;
+      dy[j] = gr;
     }
-    s = group_sum(s, g, s_red, buf);
+    float v[2] = {__fadd_rn(s2.x, s2.y), __fadd_rn(s1.x, s1.y)};
+    group_sum(v, g, s_red, buf);
     if (VW == 1 && depth > 0) {   // the sum's barrier: every thread has read the place
       if (n <= 32) __syncwarp();
       const uint2 e = start(i + depth);
@@ -742,25 +753,23 @@ __global__ void __launch_bounds__(kMaxGroup, 1) norm_bwd_kernel(NormBwdArgs a, i
         edge[0] = e;
       }
     }
-    const float mg = a.rms ? 0.f : __fmul_rn(s.x, inv_h), mgh = __fmul_rn(s.y, inv_h);
+    const float mg = a.rms ? 0.f : __fmul_rn(v[1], inv_h), mgh = __fmul_rn(v[0], inv_h);
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-      h[e] = __fmul_rn(r, __fsub_rn(__fsub_rn(dy[e], mg), __fmul_rn(h[e], mgh)));
-    if (live) store_cols<VW>(a.dx, a.dx_dtype, row * a.lddx, H, g.t, n, h);
+    for (int j = 0; j < E / 2; ++j)
+      h[j] = mul2(both(r), fma2(h[j], both(-mgh), add2(dy[j], both(-mg))));
+    if (live) store_cols<VW, E, FULL>(a.dx, a.dx_dtype, row * a.lddx, H, g, h);
   }
   if (!a.workspace) return;
   float* part = a.workspace + (int64_t)blockIdx.x * 2 * part_pitch(a.H);
-  if (SACC) {
-    float v[E];
+  if constexpr (SACC) {
+    float2 v[E / 2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
 #pragma unroll
-      for (int e = 0; e < E; ++e) v[e] = s_acc[(k * E + e) * n + g.t];
-      store_cols<VW>(part + k * part_pitch(a.H), 1, 0, H, g.t, n, v);
+      for (int j = 0; j < E / 2; ++j) v[j] = s_acc[(k * E / 2 + j) * n + g.t];
+      store_cols<VW, E, FULL>(part + k * part_pitch(a.H), 1, 0, H, g, v);
     }
-    return;
-  }
-  if constexpr (!SACC) {
+  } else {
     // the CTA's groups, added in order (every copy has landed: the shared memory is free again)
     if (g.count > 1) {
       asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -768,17 +777,17 @@ __global__ void __launch_bounds__(kMaxGroup, 1) norm_bwd_kernel(NormBwdArgs a, i
         __syncthreads();
         if (g.index != k) continue;
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          float* p = s_acc + e * n + g.t;
-          float* q = s_acc + (E + e) * n + g.t;
-          *p = dw[e] = k ? __fadd_rn(*p, dw[e]) : dw[e];
-          *q = db[e] = k ? __fadd_rn(*q, db[e]) : db[e];
+        for (int j = 0; j < E / 2; ++j) {
+          float2* p = s_acc + j * n + g.t;
+          float2* q = s_acc + (E / 2 + j) * n + g.t;
+          *p = dw[j] = k ? add2(*p, dw[j]) : dw[j];
+          *q = db[j] = k ? add2(*q, db[j]) : db[j];
         }
       }
       if (g.index != g.count - 1) return;
     }
-    store_cols<VW>(part, 1, 0, H, g.t, n, dw);
-    store_cols<VW>(part + part_pitch(a.H), 1, 0, H, g.t, n, db);
+    store_cols<VW, E, FULL>(part, 1, 0, H, g, dw);
+    store_cols<VW, E, FULL>(part + part_pitch(a.H), 1, 0, H, g, db);
   }
 }
 
@@ -839,9 +848,9 @@ int depth_for(size_t row, size_t fixed, int block, int most) {
   return d;
 }
 
-template <int XT, int VW, int E>
+template <int XT, int VW, int E, bool FULL = false>
 cudaError_t fwd(const NormArgs& a, cudaStream_t stream) {
-  auto kernel = norm_fwd_kernel<XT, VW, E>;
+  auto kernel = norm_fwd_kernel<XT, VW, E, FULL>;
   static std::atomic<int> done[64];
   if (cudaError_t e = allow_smem(kernel, done); e != cudaSuccess) return e;
   const int n = group_for(a.H, VW == 8), block = n > 128 ? n : 256, groups = block / n;
@@ -851,15 +860,19 @@ cudaError_t fwd(const NormArgs& a, cudaStream_t stream) {
   const cudaError_t e = launch_after(kernel, dim3((unsigned)(want < cap ? want : cap)), dim3(block), depth * row, stream, a, n, depth);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
+// Whether the threads' columns are exactly the row's.
+bool full_row(int64_t H, bool vec) { return vec && (int64_t)group_for(H, true) * cols_for(H) == H; }
+
 template <int XT>
 cudaError_t fwd_for(const NormArgs& a, bool vec, cudaStream_t stream) {
+  if (full_row(a.H, vec)) return cols_for(a.H) == 32 ? fwd<XT, 8, 32, true>(a, stream) : fwd<XT, 8, 16, true>(a, stream);
   if (cols_for(a.H) == 32) return vec ? fwd<XT, 8, 32>(a, stream) : fwd<XT, 1, 32>(a, stream);
   return vec ? fwd<XT, 8, 16>(a, stream) : fwd<XT, 1, 16>(a, stream);
 }
 
-template <int XT, int DT, int VW, int E>
+template <int XT, int DT, int VW, int E, bool FULL = false>
 cudaError_t bwd(const NormBwdArgs& a, int& parts, cudaStream_t stream) {
-  auto kernel = norm_bwd_kernel<XT, DT, VW, E>;
+  auto kernel = norm_bwd_kernel<XT, DT, VW, E, FULL>;
   static std::atomic<int> done[64];
   if (cudaError_t e = allow_smem(kernel, done); e != cudaSuccess) return e;
   const int n = group_for(a.H, VW == 8), block = n > 128 ? n : 256, groups = block / n;
@@ -876,6 +889,8 @@ cudaError_t bwd(const NormBwdArgs& a, int& parts, cudaStream_t stream) {
 }
 template <int XT, int DT>
 cudaError_t bwd_for(const NormBwdArgs& a, bool vec, int& parts, cudaStream_t stream) {
+  if (full_row(a.H, vec))
+    return cols_for(a.H) == 32 ? bwd<XT, DT, 8, 32, true>(a, parts, stream) : bwd<XT, DT, 8, 16, true>(a, parts, stream);
   if (cols_for(a.H) == 32) return vec ? bwd<XT, DT, 8, 32>(a, parts, stream) : bwd<XT, DT, 1, 32>(a, parts, stream);
   return vec ? bwd<XT, DT, 8, 16>(a, parts, stream) : bwd<XT, DT, 1, 16>(a, parts, stream);
 }
