@@ -47,6 +47,14 @@ __device__ __forceinline__ float ck_value(const CheckpointView& ck, int64_t t, i
   return __fmul_rn((float)ck.codes[t * ck.ldc + c], ck_step(ck.scales[t * ck.lds + c / kCkBlock]));
 }
 
+// v^-1/2: the hardware's approximation (about 2^-22) and one Newton step
+// r (3 - v r^2) / 2; 0 and infinity as they come from the approximation.
+__device__ __forceinline__ float inv_sqrt(float v) {
+  const float r = rsqrtf(v);
+  const float e = __fmaf_rn(__fmul_rn(-v, r), r, 1.f);   // 1 - v r^2
+  return isfinite(e) ? __fmaf_rn(__fmul_rn(0.5f, r), e, r) : r;
+}
+
 // Sum over the CTA in a fixed order, on every thread.
 template <int NW>
 __device__ __forceinline__ float cta_sum(float v, float* s_red) {
@@ -162,7 +170,13 @@ constexpr int64_t kOnChip = 32 * kMaxGroup;
 // columns at a time, consecutive threads on consecutive ones.  They are held
 // as pairs, so that most of the arithmetic goes two elements an instruction
 // (these kernels would otherwise be bound by issue).  FULL: the threads'
-// columns are exactly the row's (VW = 8), and nothing needs a bounds check.
+// columns are exactly the row's (VW = 8), and nothing needs a bounds check; or
+// all but a thread's last TAIL columns are surely inside the row (VW = 1).
+constexpr int TAIL = 4;
+template <int VW, int E, bool FULL>
+__device__ __forceinline__ constexpr bool surely(int e) {
+  return FULL && (VW == 8 || e < E - TAIL);
+}
 
 // The same number, but computed anew by the compiler: column offsets that
 // depend on it are not kept in registers over all rows.
@@ -258,11 +272,11 @@ __device__ __forceinline__ void load_cols(const void* p, int dtype, int64_t at, 
     if (dtype) {
       const float* q = static_cast<const float*>(p) + at + g.t;
 #pragma unroll
-      for (int e = 0; e < E; ++e) elem<E>(v, e) = e * n < left ? q[e * n] : 0.f;
+      for (int e = 0; e < E; ++e) elem<E>(v, e) = surely<VW, E, FULL>(e) || e * n < left ? q[e * n] : 0.f;
     } else {
       const uint16_t* q = static_cast<const uint16_t*>(p) + at + g.t;
 #pragma unroll
-      for (int e = 0; e < E; ++e) elem<E>(v, e) = e * n < left ? bf16_val(q[e * n]) : 0.f;
+      for (int e = 0; e < E; ++e) elem<E>(v, e) = surely<VW, E, FULL>(e) || e * n < left ? bf16_val(q[e * n]) : 0.f;
     }
   }
 }
@@ -294,12 +308,12 @@ __device__ __forceinline__ void store_cols(void* p, int dtype, int64_t at, int H
       float* q = static_cast<float*>(p) + at + g.t;
 #pragma unroll
       for (int e = 0; e < E; ++e)
-        if (e * n < left) q[e * n] = elem<E>(v, e);
+        if (surely<VW, E, FULL>(e) || e * n < left) q[e * n] = elem<E>(v, e);
     } else {
       __nv_bfloat16* q = static_cast<__nv_bfloat16*>(p) + at + g.t;
 #pragma unroll
       for (int e = 0; e < E; ++e)
-        if (e * n < left) q[e * n] = __float2bfloat16_rn(elem<E>(v, e));
+        if (surely<VW, E, FULL>(e) || e * n < left) q[e * n] = __float2bfloat16_rn(elem<E>(v, e));
     }
   }
 }
@@ -331,7 +345,7 @@ __device__ __forceinline__ void write_checkpoint(const CheckpointView& ck, int64
     }
     const uint32_t byte = ck_scale_byte(amax);
     const int c = (k * g.n + g.t) * VW;
-    if (!live || (!FULL && c >= H)) continue;
+    if (!live || (!surely<VW, E, FULL>(k * VW) && c >= H)) continue;
     if constexpr (VW == 8) {
       uint2 q;
       if (byte < kCkTop) {
@@ -374,10 +388,11 @@ __device__ __forceinline__ void cp_wait(int depth) {
 }
 
 // Bytes of a row's place in shared memory.  VW = 8: the threads' 8-column
-// pieces; VW = 1: the row's bytes at its own distance from a 16-byte boundary.
+// pieces; VW = 1: the row's bytes at its own distance from a 16-byte boundary,
+// and zeros up to the threads' last column (and the distance).
 template <int TYPE, int VW, int E>
 __host__ __device__ __forceinline__ int place_bytes(int H, int n) {
-  return VW == 8 ? E * n * bytes_of(TYPE) : (H * bytes_of(TYPE) + 15) / 16 * 16 + 16;
+  return E * n * bytes_of(TYPE) + (VW == 8 ? 0 : 32);
 }
 
 // VW = 1: the element of a row that a thread carries to shared memory itself,
@@ -401,18 +416,29 @@ __device__ __forceinline__ uint32_t start_row(uint8_t* place, const void* p, int
   constexpr int es = bytes_of(TYPE);
   const char* src = static_cast<const char*>(p) + at * es;
   const uint32_t dst = smem_u32(place);
+  if (VW == 8 && TYPE == 1) {
+    // a thread's 8 columns are two 16-byte units: a warp's (a group's) are
+    // copied in order, so that no request asks for half a sector
+    const int m = g.n < 32 ? g.n : 32, u0 = g.t & (m - 1);
+#pragma unroll
+    for (int k = 0; k < E / 8; ++k) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int c = (k * g.n + (g.t - u0)) * 8 + (u0 + h * m) * 4;
+        const int have = FULL ? 16 : (H - c < 4 ? H - c : 4) * 4;
+        if (FULL || have > 0) cp_async16(dst + c * 4, src + c * 4, have);
+      }
+    }
+    return 0u;
+  }
   if (VW == 8) {
 #pragma unroll
     for (int k = 0; k < E / 8; ++k) {
       const int c = (k * g.n + g.t) * 8;
       const int have = FULL ? 8 * es : (H - c < 8 ? H - c : 8) * es;
       if (!FULL && have <= 0) continue;
-      if (TYPE == kFromCk) {
-        cp_async8(dst + c, src + c, have);
-      } else {
-        cp_async16(dst + c * es, src + c * es, have < 16 ? have : 16);
-        if (TYPE == 1 && have > 16) cp_async16(dst + c * es + 16, src + c * es + 16, have - 16);
-      }
+      if (TYPE == kFromCk) cp_async8(dst + c, src + c, have);
+      else cp_async16(dst + c * es, src + c * es, have);
     }
     return 0u;
   }
@@ -425,11 +451,19 @@ __device__ __forceinline__ uint32_t start_row(uint8_t* place, const void* p, int
   if (e < 0) return 0u;
   return TYPE == 1 ? *reinterpret_cast<const uint32_t*>(src + e) : *reinterpret_cast<const uint16_t*>(src + e);
 }
-// VW = 1: stores the edge element of the row that started `at` there.
+// VW = 1: stores the edge element of the row that started `at` there, and the
+// zeros behind the row where an earlier one may have ended later.
 template <int TYPE>
 __device__ __forceinline__ void store_edge(uint8_t* place, const void* p, int64_t at, int H, const Group& g, uint32_t v) {
   constexpr int es = bytes_of(TYPE);
+  if (TYPE == kFromCk) return;   // the codes past a row meet a dy of 0
   const char* src = static_cast<const char*>(p) + at * es;
+  const int z = H * es + (g.t - 16) * es;
+  if (g.t >= 16 && (g.t - 16) * es < 16) {
+    uint8_t* d = place + (reinterpret_cast<uintptr_t>(src) & 15u) + z;
+    if (TYPE == 1) *reinterpret_cast<uint32_t*>(d) = 0u;
+    else *reinterpret_cast<uint16_t*>(d) = 0;
+  }
   const int e = edge_byte<TYPE>(to_boundary(src), H * es, g.t);
   if (e < 0) return;
   uint8_t* d = place + (reinterpret_cast<uintptr_t>(src) & 15u) + e;
@@ -438,7 +472,7 @@ __device__ __forceinline__ void store_edge(uint8_t* place, const void* p, int64_
 }
 
 // A thread's columns of a row in shared memory (0 past the end; codes times
-// their steps).  VW = 8: only what this thread copied itself; VW = 1: after a barrier.
+// their steps).  VW = 8: what this thread or its warp copied; VW = 1: after a barrier.
 template <int TYPE, int VW, int E, bool FULL>
 __device__ __forceinline__ void take_row(const uint8_t* place, const void* p, int64_t at, int H, const Group& g,
                                          const float (&step)[VW == 8 ? E / 8 : E], float2 (&v)[E / 2]) {
@@ -471,19 +505,22 @@ __device__ __forceinline__ void take_row(const uint8_t* place, const void* p, in
     }
   } else {
     const uint8_t* s = place + ((reinterpret_cast<uintptr_t>(p) + at * es) & 15u) + g.t * es;
-    const int n = fresh(g.n), left = H - g.t;
+    const int n = fresh(g.n);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       const uint8_t* q = s + e * n * es;
-      float f = 0.f;
-      if (e * n < left) {
-        if (TYPE == 1) f = *reinterpret_cast<const float*>(q);
-        else if (TYPE == 0) f = bf16_val(*reinterpret_cast<const uint16_t*>(q));
-        else f = __fmul_rn((float)*reinterpret_cast<const int8_t*>(q), step[e]);
-      }
+      float f;
+      if (TYPE == 1) f = *reinterpret_cast<const float*>(q);
+      else if (TYPE == 0) f = bf16_val(*reinterpret_cast<const uint16_t*>(q));
+      else f = __fmul_rn((float)*reinterpret_cast<const int8_t*>(q), step[e]);
       elem<E>(v, e) = f;
     }
   }
+}
+// VW = 1: zeros in the places of `depth` rows, before the first copy.
+__device__ __forceinline__ void clear_places(uint8_t* mine, int bytes, const Group& g) {
+  for (int o = g.t * 16; o < bytes; o += g.n * 16) *reinterpret_cast<uint4*>(mine + o) = make_uint4(0u, 0u, 0u, 0u);
+  g.sync();
 }
 
 template <int E>
@@ -510,6 +547,7 @@ __global__ void __launch_bounds__(kMaxGroup, 1) norm_fwd_kernel(NormArgs a, int 
   const float inv_h = __fdiv_rn(1.f, (float)H);
   const float none[VW == 8 ? E / 8 : E] = {};
 
+  if (VW == 1) clear_places(mine, depth * size, g);
   pdl_wait();   // the rows may come from the kernel before
   uint32_t edge[2] = {0u, 0u};   // VW = 1: depth is at most 2
   auto start = [&](int i) -> uint32_t {
@@ -540,9 +578,13 @@ __global__ void __launch_bounds__(kMaxGroup, 1) norm_fwd_kernel(NormArgs a, int 
     if (VW == 1 && live) store_edge<XT>(place, a.x, row * a.ldx, H, g, edge[0]);
     cp_wait(depth);
     if (VW == 1) g.sync();
+    else if (XT == 1) __syncwarp();
     if (live) take_row<XT, VW, E, FULL>(place, a.x, row * a.ldx, H, g, none, x);
     else fill<E>(x, 0.f);
-    if (VW == 8) start(i + depth);   // into the place just read: a thread reads only what it copied itself
+    if (VW == 8) {   // into the place just read: a thread reads what it copied itself, or its warp did
+      if (XT == 1) __syncwarp();
+      start(i + depth);
+    }
     float m = 0.f;
     if (!a.rms) {
       float2 s = x[0];
@@ -553,7 +595,7 @@ __global__ void __launch_bounds__(kMaxGroup, 1) norm_fwd_kernel(NormArgs a, int 
       m = __fmul_rn(v[0], inv_h);
     }
     float2 s = both(0.f);
-    if (FULL || a.rms) {   // with m = 0 the zeros past the end add nothing
+    if ((FULL && VW == 8) || a.rms) {   // with m = 0 the zeros past the end add nothing
 #pragma unroll
       for (int j = 0; j < E / 2; ++j) {
         const float2 d = add2(x[j], both(-m));
@@ -564,8 +606,9 @@ __global__ void __launch_bounds__(kMaxGroup, 1) norm_fwd_kernel(NormArgs a, int 
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         const int c = ((e / VW) * n2 + g.t) * VW + e % VW;
-        const float d = c < H ? __fsub_rn(elem<E>(x, e), m) : 0.f;
-        s.x = __fmaf_rn(d, d, s.x);
+        const float d = surely<VW, E, FULL>(e) || c < H ? __fsub_rn(elem<E>(x, e), m) : 0.f;
+        if (e % 2) s.y = __fmaf_rn(d, d, s.y);
+        else s.x = __fmaf_rn(d, d, s.x);
       }
     }
     float v[1] = {__fadd_rn(s.x, s.y)};
@@ -582,7 +625,7 @@ __global__ void __launch_bounds__(kMaxGroup, 1) norm_fwd_kernel(NormArgs a, int 
       }
     }
     const bool bad = !isfinite(var);
-    const float r = bad ? NAN : __fdiv_rn(1.f, __fsqrt_rn(__fadd_rn(var, a.eps)));
+    const float r = bad ? NAN : inv_sqrt(__fadd_rn(var, a.eps));
     if (bad) m = NAN;
     if (live && g.t == 0) {
       if (a.mean && !a.rms) a.mean[row] = m;
@@ -635,6 +678,7 @@ __global__ void __launch_bounds__(kMaxGroup, 1) norm_bwd_kernel(NormBwdArgs a, i
   const void* xp = XT == kFromCk ? static_cast<const void*>(a.ck.codes) : a.x;
   const int64_t ldx = XT == kFromCk ? a.ck.ldc : a.ldx;
 
+  if (VW == 1) clear_places(mine, depth * size, g);
   pdl_wait();
   uint2 edge[2] = {make_uint2(0u, 0u), make_uint2(0u, 0u)};   // VW = 1: depth is at most 2
   auto place = [&](int i) { return mine + (i & (depth - 1)) * size; };
@@ -665,7 +709,7 @@ __global__ void __launch_bounds__(kMaxGroup, 1) norm_bwd_kernel(NormBwdArgs a, i
 #pragma unroll
       for (int k = 0; k < STEPS; ++k) {
         const int c = (k * n2 + g.t) * VW;
-        byte1[k] = in && (FULL || c < H) ? sc[c / kCkBlock] : 1u;
+        byte1[k] = in && (surely<VW, E, FULL>(k * VW) || c < H) ? sc[c / kCkBlock] : 1u;
       }
     }
   };
@@ -704,11 +748,15 @@ __global__ void __launch_bounds__(kMaxGroup, 1) norm_bwd_kernel(NormBwdArgs a, i
       }
       cp_wait(depth);
       if (VW == 1) g.sync();
+      else if (XT == 1 || DT == 1) __syncwarp();
       if (live) {
         take_row<DT, VW, E, FULL>(place(i), a.dy, row * a.lddy, H, g, step, dy);
         take_row<XT, VW, E, FULL>(place(i) + dy_size, xp, row * ldx, H, g, step, h);
       }
-      if (VW == 8) start(i + depth);   // into the place just read: a thread reads only what it copied itself
+      if (VW == 8) {   // into the place just read: a thread reads what it copied itself, or its warp did
+        if (XT == 1 || DT == 1) __syncwarp();
+        start(i + depth);
+      }
     } else if (live) {
       load_cols<VW, E, FULL>(a.dy, DT, row * a.lddy, H, g, dy);
       if (XT == kFromCk) {
@@ -860,12 +908,18 @@ cudaError_t fwd(const NormArgs& a, cudaStream_t stream) {
   const cudaError_t e = launch_after(kernel, dim3((unsigned)(want < cap ? want : cap)), dim3(block), depth * row, stream, a, n, depth);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
-// Whether the threads' columns are exactly the row's.
-bool full_row(int64_t H, bool vec) { return vec && (int64_t)group_for(H, true) * cols_for(H) == H; }
+// FULL of the kernels.
+bool full_row(int64_t H, bool vec) {
+  const int64_t n = group_for(H, vec), e = cols_for(H);
+  return vec ? n * e == H : n * (e - TAIL) <= H;
+}
 
 template <int XT>
 cudaError_t fwd_for(const NormArgs& a, bool vec, cudaStream_t stream) {
-  if (full_row(a.H, vec)) return cols_for(a.H) == 32 ? fwd<XT, 8, 32, true>(a, stream) : fwd<XT, 8, 16, true>(a, stream);
+  if (full_row(a.H, vec)) {
+    if (cols_for(a.H) == 32) return vec ? fwd<XT, 8, 32, true>(a, stream) : fwd<XT, 1, 32, true>(a, stream);
+    return vec ? fwd<XT, 8, 16, true>(a, stream) : fwd<XT, 1, 16, true>(a, stream);
+  }
   if (cols_for(a.H) == 32) return vec ? fwd<XT, 8, 32>(a, stream) : fwd<XT, 1, 32>(a, stream);
   return vec ? fwd<XT, 8, 16>(a, stream) : fwd<XT, 1, 16>(a, stream);
 }
@@ -889,8 +943,10 @@ cudaError_t bwd(const NormBwdArgs& a, int& parts, cudaStream_t stream) {
 }
 template <int XT, int DT>
 cudaError_t bwd_for(const NormBwdArgs& a, bool vec, int& parts, cudaStream_t stream) {
-  if (full_row(a.H, vec))
-    return cols_for(a.H) == 32 ? bwd<XT, DT, 8, 32, true>(a, parts, stream) : bwd<XT, DT, 8, 16, true>(a, parts, stream);
+  if (full_row(a.H, vec)) {
+    if (cols_for(a.H) == 32) return vec ? bwd<XT, DT, 8, 32, true>(a, parts, stream) : bwd<XT, DT, 1, 32, true>(a, parts, stream);
+    return vec ? bwd<XT, DT, 8, 16, true>(a, parts, stream) : bwd<XT, DT, 1, 16, true>(a, parts, stream);
+  }
   if (cols_for(a.H) == 32) return vec ? bwd<XT, DT, 8, 32>(a, parts, stream) : bwd<XT, DT, 1, 32>(a, parts, stream);
   return vec ? bwd<XT, DT, 8, 16>(a, parts, stream) : bwd<XT, DT, 1, 16>(a, parts, stream);
 }
