@@ -109,6 +109,8 @@ def build(force: bool = False) -> str:
 def load(path: str | None = None):
     """Load librlk.so (built in-tree by ``build()``) and declare its signatures."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -220,11 +222,14 @@ def load(path: str | None = None):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
-def _stream(device) -> ctypes.c_void_p:
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+def _stream(device) -> int:
+    """The current stream of the device as a raw handle (without building a
+    torch.cuda.Stream, which takes longer than a launch)."""
+    index = device.index
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index)
 
 
 def _need_cuda(*ts):
@@ -870,28 +875,45 @@ def sample_top_p(logits, temperature, top_p, uniforms, *, row_state=None, status
 _DTYPES = {torch.bfloat16: 0, torch.float32: 1}
 
 
-def _matrix(t, name):
-    """dtype index and row stride of a 2-D bf16 / fp32 tensor with unit stride along its rows."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be 2-D with unit stride along its rows")
+def _matrix(t, name, shape=None):
+    """dtype index and row stride of a 2-D bf16 / fp32 tensor (of ``shape``) with
+    unit stride along its rows."""
+    size = t.shape
+    if len(size) != 2:
+        raise ValueError(f"{name} must be 2-D")
+    ld, unit = t.stride()
+    if unit != 1 and size[1] > 1:
+        raise ValueError(f"{name} must have unit stride along its rows")
     dt = _DTYPES.get(t.dtype)
     if dt is None:
         raise ValueError(f"{name} must be bf16 or fp32")
-    return dt, (t.stride(0) if t.shape[0] > 1 else t.shape[1])
+    if shape is not None and size != shape:
+        raise ValueError(f"{name} must be {list(shape)}")
+    return dt, (ld if size[0] > 1 else size[1])
 
 
-def _params(H, *ts):
-    """dtype index of the parameter vectors given (fp32 when none is)."""
-    dts = {t.dtype for t in ts if t is not None}
-    if len(dts) > 1:
-        raise ValueError("weight and bias must have one dtype")
-    dt = _DTYPES.get(dts.pop()) if dts else 1
-    if dt is None:
-        raise ValueError("weight and bias must be bf16 or fp32")
-    for t in ts:
-        if t is not None and (t.dim() != 1 or t.numel() != H or not t.is_contiguous()):
-            raise ValueError(f"weight and bias must be contiguous [{H}]")
+def _param(t, H, name):
+    """dtype index of a contiguous [H] parameter vector."""
+    dt = _DTYPES.get(t.dtype)
+    if dt is None or t.shape != (H,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous bf16 or fp32 [{H}]")
     return dt
+
+
+def _params(H, weight, bias):
+    """dtype index of the parameter vectors given (fp32 when none is)."""
+    dt = 1 if weight is None else _param(weight, H, "weight")
+    if bias is not None:
+        db = _param(bias, H, "bias")
+        if weight is not None and db != dt:
+            raise ValueError("weight and bias must have one dtype")
+        dt = db
+    return dt
+
+
+def _vector(t, n, name):
+    if t.dtype != torch.float32 or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous fp32 [{n}]")
 
 
 class Checkpoint:
@@ -947,11 +969,9 @@ def checkpoint_unpack(checkpoint: Checkpoint, *, dtype=torch.bfloat16, out=None)
     lib = load()
     T, H = checkpoint.shape
     if out is None:
-        out = torch.empty((T, H), dtype=dtype, device=checkpoint.codes.device)
+        out = checkpoint.codes.new_empty((T, H), dtype=dtype)
     _need_cuda(out)
-    dt, ld = _matrix(out, "out")
-    if tuple(out.shape) != (T, H):
-        raise ValueError("out must be [T, H]")
+    dt, ld = _matrix(out, "out", (T, H))
     b = checkpoint.buffers()
     _check("rlk_checkpoint_unpack",
            lib.rlk_checkpoint_unpack(ctypes.byref(b), T, H, _ptr(out), dt, ld, _stream(out.device)))
@@ -969,19 +989,21 @@ def norm(x: torch.Tensor, weight=None, bias=None, *, kind: int = NORM_LAYER, eps
     T, H = x.shape
     pdt = _params(H, weight, bias)
     if out is None:
-        out = torch.empty((T, H), device=x.device, dtype=out_dtype or x.dtype)
-    ydt, ldy = _matrix(out, "out")
-    if tuple(out.shape) != (T, H):
-        raise ValueError("out must be [T, H]")
-    if checkpoint is not None and checkpoint.shape != (T, H):
-        raise ValueError("checkpoint must be of x's shape")
-    mean = None if kind == NORM_RMS else torch.empty(T, device=x.device, dtype=torch.float32)
-    rstd = torch.empty(T, device=x.device, dtype=torch.float32)
-    ck = None if checkpoint is None else ctypes.byref(checkpoint.buffers())
-    _check("rlk_norm_fwd",
-           lib.rlk_norm_fwd(_ptr(x), dt, T, H, ld, _ptr(weight), _ptr(bias), pdt, int(kind),
-                            float(eps), _ptr(out), ydt, ldy, _ptr(mean), _ptr(rstd), ck,
-                            _ptr(status_word), _stream(x.device)))
+        ydt, ldy = (dt if out_dtype is None else _DTYPES[out_dtype]), H
+        out = x.new_empty((T, H), dtype=out_dtype)
+    else:
+        ydt, ldy = _matrix(out, "out", (T, H))
+    ck = None
+    if checkpoint is not None:
+        if checkpoint.shape != (T, H):
+            raise ValueError("checkpoint must be of x's shape")
+        ck = ctypes.byref(checkpoint.buffers())
+    mean = None if kind == NORM_RMS else x.new_empty(T, dtype=torch.float32)
+    rstd = x.new_empty(T, dtype=torch.float32)
+    code = lib.rlk_norm_fwd(x.data_ptr(), dt, T, H, ld, _ptr(weight), _ptr(bias), pdt, kind, eps,
+                            out.data_ptr(), ydt, ldy, _ptr(mean), rstd.data_ptr(), ck,
+                            _ptr(status_word), _stream(x.device))
+    _check("rlk_norm_fwd", code)
     return out, mean, rstd
 
 
@@ -1001,35 +1023,32 @@ def norm_backward(dy: torch.Tensor, x, weight, mean, rstd, *, kind: int = NORM_L
     if tuple(x.shape) != (T, H):
         raise ValueError("x must have dy's shape")
     dt, ld = (0, H) if kept else _matrix(x, "x")
-    pdt = _params(H, weight)
-    for t in (mean, rstd):
-        if t is not None and (t.dtype != torch.float32 or t.numel() != T or not t.is_contiguous()):
-            raise ValueError("mean and rstd must be contiguous fp32 [T]")
+    pdt = _params(H, weight, None)
+    if mean is not None:
+        _vector(mean, T, "mean")
+    _vector(rstd, T, "rstd")
     if out is None:
-        out = torch.empty((T, H), device=dy.device,
-                          dtype=grad_dtype or (torch.bfloat16 if kept else x.dtype))
-    odt, ldo = _matrix(out, "out")
-    if tuple(out.shape) != (T, H):
-        raise ValueError("out must be [T, H]")
+        out = dy.new_empty((T, H), dtype=grad_dtype or (torch.bfloat16 if kept else x.dtype))
+    odt, ldo = _matrix(out, "out", (T, H))
     if accumulate and ((want_weight_grad and grad_weight is None) or (want_bias_grad and grad_bias is None)):
         raise ValueError("accumulate needs grad_weight and grad_bias")
-    if grad_weight is None and want_weight_grad:
-        grad_weight = torch.empty(H, device=dy.device, dtype=torch.float32)
-    if grad_bias is None and want_bias_grad:
-        grad_bias = torch.empty(H, device=dy.device, dtype=torch.float32)
-    for t in (grad_weight, grad_bias):
-        if t is not None and (t.dtype != torch.float32 or t.numel() != H or not t.is_contiguous()):
-            raise ValueError("grad_weight and grad_bias must be contiguous fp32 [H]")
+    if grad_weight is not None:
+        _vector(grad_weight, H, "grad_weight")
+    elif want_weight_grad:
+        grad_weight = dy.new_empty(H, dtype=torch.float32)
+    if grad_bias is not None:
+        _vector(grad_bias, H, "grad_bias")
+    elif want_bias_grad:
+        grad_bias = dy.new_empty(H, dtype=torch.float32)
     if workspace is None and (grad_weight is not None or grad_bias is not None):
-        workspace = torch.empty(max(int(lib.rlk_workspace_size(OP_NORM_BWD, T, H, 0)), 16),
-                                device=dy.device, dtype=torch.uint8)
+        workspace = dy.new_empty(max(lib.rlk_workspace_size(OP_NORM_BWD, T, H, 0), 16), dtype=torch.uint8)
     ck = None if kept is None else ctypes.byref(kept.buffers())
-    _check("rlk_norm_bwd",
-           lib.rlk_norm_bwd(_ptr(dy), gdt, ldg, None if kept else _ptr(x), dt, ld, ck, T, H,
-                            _ptr(weight), pdt, int(kind), _ptr(mean), _ptr(rstd), _ptr(out), odt,
+    code = lib.rlk_norm_bwd(dy.data_ptr(), gdt, ldg, None if kept else x.data_ptr(), dt, ld, ck, T, H,
+                            _ptr(weight), pdt, kind, _ptr(mean), rstd.data_ptr(), out.data_ptr(), odt,
                             ldo, _ptr(grad_weight), _ptr(grad_bias), int(bool(accumulate)),
                             _ptr(workspace), 0 if workspace is None else workspace.numel(),
-                            _stream(dy.device)))
+                            _stream(dy.device))
+    _check("rlk_norm_bwd", code)
     return out, grad_weight, grad_bias
 
 
@@ -1065,11 +1084,9 @@ def norm_autograd(x: torch.Tensor, weight=None, bias=None, *, kind: int = NORM_L
 # ------------------------------------------------------------ linear
 def _bf16(t, name, shape=None):
     """Row stride of a 2-D bf16 tensor (of ``shape``) with unit stride along its rows."""
-    dt, ld = _matrix(t, name)
+    dt, ld = _matrix(t, name, shape)
     if dt != 0:
         raise ValueError(f"{name} must be bf16")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be {list(shape)}")
     return ld
 
 
@@ -1087,22 +1104,21 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias=None, residual=None, *,
     N = weight.shape[0]
     if weight.shape[1] != K:
         raise ValueError("x and weight disagree on K")
-    bdt = _params(N, bias)
+    bdt = 1 if bias is None else _param(bias, N, "bias")
     ldr = 0 if residual is None else _bf16(residual, "residual", (M, N))
     if out is None:
-        out = torch.empty((M, N), device=x.device, dtype=out_dtype or torch.bfloat16)
-    ydt, ldy = _matrix(out, "out")
-    if tuple(out.shape) != (M, N):
-        raise ValueError("out must be [M, N]")
-    z = torch.empty((M, N), device=x.device, dtype=torch.bfloat16) if return_preact else None
-    if workspace is None and (x.data_ptr() % 16 or ldx % 8 or weight.data_ptr() % 16 or ldw % 8):
-        workspace = torch.empty(int(lib.rlk_workspace_size(OP_LINEAR, M, N, K)), device=x.device,
-                                dtype=torch.uint8)
-    _check("rlk_linear_fwd",
-           lib.rlk_linear_fwd(_ptr(x), ldx, _ptr(weight), ldw, _ptr(bias), bdt, _ptr(residual), ldr,
-                              M, N, K, int(activation), _ptr(out), ydt, ldy, _ptr(z), N,
-                              _ptr(workspace), 0 if workspace is None else workspace.numel(),
-                              _stream(x.device)))
+        ydt, ldy = (0 if out_dtype is None else _DTYPES[out_dtype]), N
+        out = x.new_empty((M, N), dtype=out_dtype)
+    else:
+        ydt, ldy = _matrix(out, "out", (M, N))
+    z = x.new_empty((M, N)) if return_preact else None
+    px, pw = x.data_ptr(), weight.data_ptr()
+    if workspace is None and (px % 16 or ldx % 8 or pw % 16 or ldw % 8):
+        workspace = x.new_empty(lib.rlk_workspace_size(OP_LINEAR, M, N, K), dtype=torch.uint8)
+    code = lib.rlk_linear_fwd(px, ldx, pw, ldw, _ptr(bias), bdt, _ptr(residual), ldr, M, N, K, activation,
+                              out.data_ptr(), ydt, ldy, _ptr(z), N, _ptr(workspace),
+                              0 if workspace is None else workspace.numel(), _stream(x.device))
+    _check("rlk_linear_fwd", code)
     return (out, z) if return_preact else out
 
 
@@ -1196,29 +1212,29 @@ def preference_loss(logp, logp_ref, seq_offsets, *, loss_mask=None, loss_type: i
     rewards [2 pairs] or None, stats[PREF_NSTATS] or None)."""
     lib = load()
     _need_cuda(logp, logp_ref, seq_offsets, loss_mask)
-    for t in (logp, logp_ref):
-        if t is not None and (t.dtype != torch.float32 or t.dim() != 1 or not t.is_contiguous()
-                              or t.numel() != logp.numel()):
-            raise ValueError("log-probs must be contiguous fp32 [n_tok]")
-    if seq_offsets.dtype != torch.int32 or not seq_offsets.is_contiguous() or seq_offsets.numel() % 2 != 1:
+    n_tok, offsets = logp.numel(), seq_offsets.numel()
+    _vector(logp, n_tok, "logp")
+    if logp_ref is not None:
+        _vector(logp_ref, n_tok, "logp_ref")
+    if seq_offsets.dtype != torch.int32 or not seq_offsets.is_contiguous() or offsets % 2 != 1:
         raise ValueError("seq_offsets must be contiguous int32 [2 pairs + 1]")
     if loss_mask is not None and (loss_mask.dtype != torch.uint8 or not loss_mask.is_contiguous()
-                                  or loss_mask.numel() != logp.numel()):
+                                  or loss_mask.numel() != n_tok):
         raise ValueError("loss_mask must be contiguous uint8 [n_tok]")
-    P, n_tok, dev = seq_offsets.numel() // 2, logp.numel(), logp.device
+    P = offsets // 2
     if workspace is None:
-        workspace = torch.empty(int(lib.rlk_workspace_size(OP_PREFERENCE_LOSS, n_tok, P, 0)),
-                                device=dev, dtype=torch.uint8)
-    cfg = PrefConfig(int(loss_type), float(beta), float(label_smoothing), float(margin),
-                     int(bool(length_normalise)))
-    loss = torch.empty(1, device=dev, dtype=torch.float32)
-    grad = torch.empty(n_tok, device=dev, dtype=torch.float32) if want_grad else None
-    reward = torch.empty(2 * P, device=dev, dtype=torch.float32) if want_reward else None
-    stats = torch.empty(PREF_NSTATS, device=dev, dtype=torch.float32) if want_stats else None
-    _check("rlk_preference_loss",
-           lib.rlk_preference_loss(_ptr(logp), _ptr(logp_ref), _ptr(loss_mask), _ptr(seq_offsets), P,
-                                   n_tok, ctypes.byref(cfg), _ptr(loss), _ptr(grad), _ptr(reward),
-                                   _ptr(stats), _ptr(workspace), workspace.numel(), _stream(dev)))
+        workspace = logp.new_empty(lib.rlk_workspace_size(OP_PREFERENCE_LOSS, n_tok, P, 0),
+                                   dtype=torch.uint8)
+    cfg = PrefConfig(loss_type, beta, label_smoothing, margin, int(bool(length_normalise)))
+    loss = logp.new_empty(1)
+    grad = logp.new_empty(n_tok) if want_grad else None
+    reward = logp.new_empty(2 * P) if want_reward else None
+    stats = logp.new_empty(PREF_NSTATS) if want_stats else None
+    code = lib.rlk_preference_loss(logp.data_ptr(), _ptr(logp_ref), _ptr(loss_mask), seq_offsets.data_ptr(),
+                                   P, n_tok, ctypes.byref(cfg), loss.data_ptr(), _ptr(grad), _ptr(reward),
+                                   _ptr(stats), workspace.data_ptr(), workspace.numel(),
+                                   _stream(logp.device))
+    _check("rlk_preference_loss", code)
     return loss, grad, reward, stats
 
 
