@@ -969,7 +969,7 @@ def checkpoint_unpack(checkpoint: Checkpoint, *, dtype=torch.bfloat16, out=None)
     lib = load()
     T, H = checkpoint.shape
     if out is None:
-        out = checkpoint.codes.new_empty((T, H), dtype=dtype)
+        out = torch.empty((T, H), dtype=dtype, device=checkpoint.codes.device)
     _need_cuda(out)
     dt, ld = _matrix(out, "out", (T, H))
     b = checkpoint.buffers()
@@ -988,9 +988,11 @@ def norm(x: torch.Tensor, weight=None, bias=None, *, kind: int = NORM_LAYER, eps
     dt, ld = _matrix(x, "x")
     T, H = x.shape
     pdt = _params(H, weight, bias)
+    dev = x.device
     if out is None:
         ydt, ldy = (dt if out_dtype is None else _DTYPES[out_dtype]), H
-        out = x.new_empty((T, H), dtype=out_dtype)
+        out = torch.empty_like(x) if out_dtype is None and ld == H else torch.empty(
+            (T, H), dtype=out_dtype or x.dtype, device=dev)
     else:
         ydt, ldy = _matrix(out, "out", (T, H))
     ck = None
@@ -998,11 +1000,11 @@ def norm(x: torch.Tensor, weight=None, bias=None, *, kind: int = NORM_LAYER, eps
         if checkpoint.shape != (T, H):
             raise ValueError("checkpoint must be of x's shape")
         ck = ctypes.byref(checkpoint.buffers())
-    mean = None if kind == NORM_RMS else x.new_empty(T, dtype=torch.float32)
-    rstd = x.new_empty(T, dtype=torch.float32)
+    mean = None if kind == NORM_RMS else torch.empty(T, dtype=torch.float32, device=dev)
+    rstd = torch.empty(T, dtype=torch.float32, device=dev)
     code = lib.rlk_norm_fwd(x.data_ptr(), dt, T, H, ld, _ptr(weight), _ptr(bias), pdt, kind, eps,
                             out.data_ptr(), ydt, ldy, _ptr(mean), rstd.data_ptr(), ck,
-                            _ptr(status_word), _stream(x.device))
+                            _ptr(status_word), _stream(dev))
     _check("rlk_norm_fwd", code)
     return out, mean, rstd
 
@@ -1020,6 +1022,7 @@ def norm_backward(dy: torch.Tensor, x, weight, mean, rstd, *, kind: int = NORM_L
     _need_cuda(dy, None if kept else x, weight, mean, rstd, out, grad_weight, grad_bias)
     gdt, ldg = _matrix(dy, "dy")
     T, H = dy.shape
+    dev = dy.device
     if tuple(x.shape) != (T, H):
         raise ValueError("x must have dy's shape")
     dt, ld = (0, H) if kept else _matrix(x, "x")
@@ -1028,26 +1031,27 @@ def norm_backward(dy: torch.Tensor, x, weight, mean, rstd, *, kind: int = NORM_L
         _vector(mean, T, "mean")
     _vector(rstd, T, "rstd")
     if out is None:
-        out = dy.new_empty((T, H), dtype=grad_dtype or (torch.bfloat16 if kept else x.dtype))
+        out = torch.empty((T, H), dtype=grad_dtype or (torch.bfloat16 if kept else x.dtype), device=dev)
     odt, ldo = _matrix(out, "out", (T, H))
     if accumulate and ((want_weight_grad and grad_weight is None) or (want_bias_grad and grad_bias is None)):
         raise ValueError("accumulate needs grad_weight and grad_bias")
     if grad_weight is not None:
         _vector(grad_weight, H, "grad_weight")
     elif want_weight_grad:
-        grad_weight = dy.new_empty(H, dtype=torch.float32)
+        grad_weight = torch.empty(H, dtype=torch.float32, device=dev)
     if grad_bias is not None:
         _vector(grad_bias, H, "grad_bias")
     elif want_bias_grad:
-        grad_bias = dy.new_empty(H, dtype=torch.float32)
+        grad_bias = torch.empty(H, dtype=torch.float32, device=dev)
     if workspace is None and (grad_weight is not None or grad_bias is not None):
-        workspace = dy.new_empty(max(lib.rlk_workspace_size(OP_NORM_BWD, T, H, 0), 16), dtype=torch.uint8)
+        workspace = torch.empty(max(lib.rlk_workspace_size(OP_NORM_BWD, T, H, 0), 16), dtype=torch.uint8,
+                                device=dev)
     ck = None if kept is None else ctypes.byref(kept.buffers())
     code = lib.rlk_norm_bwd(dy.data_ptr(), gdt, ldg, None if kept else x.data_ptr(), dt, ld, ck, T, H,
                             _ptr(weight), pdt, kind, _ptr(mean), rstd.data_ptr(), out.data_ptr(), odt,
                             ldo, _ptr(grad_weight), _ptr(grad_bias), int(bool(accumulate)),
                             _ptr(workspace), 0 if workspace is None else workspace.numel(),
-                            _stream(dy.device))
+                            _stream(dev))
     _check("rlk_norm_bwd", code)
     return out, grad_weight, grad_bias
 
@@ -1105,19 +1109,20 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias=None, residual=None, *,
     if weight.shape[1] != K:
         raise ValueError("x and weight disagree on K")
     bdt = 1 if bias is None else _param(bias, N, "bias")
+    dev = x.device
     ldr = 0 if residual is None else _bf16(residual, "residual", (M, N))
     if out is None:
         ydt, ldy = (0 if out_dtype is None else _DTYPES[out_dtype]), N
-        out = x.new_empty((M, N), dtype=out_dtype)
+        out = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=dev)
     else:
         ydt, ldy = _matrix(out, "out", (M, N))
-    z = x.new_empty((M, N)) if return_preact else None
+    z = torch.empty((M, N), dtype=torch.bfloat16, device=dev) if return_preact else None
     px, pw = x.data_ptr(), weight.data_ptr()
     if workspace is None and (px % 16 or ldx % 8 or pw % 16 or ldw % 8):
-        workspace = x.new_empty(lib.rlk_workspace_size(OP_LINEAR, M, N, K), dtype=torch.uint8)
+        workspace = torch.empty(lib.rlk_workspace_size(OP_LINEAR, M, N, K), dtype=torch.uint8, device=dev)
     code = lib.rlk_linear_fwd(px, ldx, pw, ldw, _ptr(bias), bdt, _ptr(residual), ldr, M, N, K, activation,
                               out.data_ptr(), ydt, ldy, _ptr(z), N, _ptr(workspace),
-                              0 if workspace is None else workspace.numel(), _stream(x.device))
+                              0 if workspace is None else workspace.numel(), _stream(dev))
     _check("rlk_linear_fwd", code)
     return (out, z) if return_preact else out
 
@@ -1221,19 +1226,19 @@ def preference_loss(logp, logp_ref, seq_offsets, *, loss_mask=None, loss_type: i
     if loss_mask is not None and (loss_mask.dtype != torch.uint8 or not loss_mask.is_contiguous()
                                   or loss_mask.numel() != n_tok):
         raise ValueError("loss_mask must be contiguous uint8 [n_tok]")
-    P = offsets // 2
+    P, dev = offsets // 2, logp.device
     if workspace is None:
-        workspace = logp.new_empty(lib.rlk_workspace_size(OP_PREFERENCE_LOSS, n_tok, P, 0),
-                                   dtype=torch.uint8)
+        workspace = torch.empty(lib.rlk_workspace_size(OP_PREFERENCE_LOSS, n_tok, P, 0),
+                                dtype=torch.uint8, device=dev)
     cfg = PrefConfig(loss_type, beta, label_smoothing, margin, int(bool(length_normalise)))
-    loss = logp.new_empty(1)
-    grad = logp.new_empty(n_tok) if want_grad else None
-    reward = logp.new_empty(2 * P) if want_reward else None
-    stats = logp.new_empty(PREF_NSTATS) if want_stats else None
+    loss = torch.empty(1, dtype=torch.float32, device=dev)
+    grad = torch.empty_like(logp) if want_grad else None
+    reward = torch.empty(2 * P, dtype=torch.float32, device=dev) if want_reward else None
+    stats = torch.empty(PREF_NSTATS, dtype=torch.float32, device=dev) if want_stats else None
     code = lib.rlk_preference_loss(logp.data_ptr(), _ptr(logp_ref), _ptr(loss_mask), seq_offsets.data_ptr(),
                                    P, n_tok, ctypes.byref(cfg), loss.data_ptr(), _ptr(grad), _ptr(reward),
                                    _ptr(stats), workspace.data_ptr(), workspace.numel(),
-                                   _stream(logp.device))
+                                   _stream(dev))
     _check("rlk_preference_loss", code)
     return loss, grad, reward, stats
 
