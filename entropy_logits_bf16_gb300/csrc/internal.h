@@ -256,9 +256,10 @@ struct PrefArgs {
   float* out_reward;
   float* out_stats;
   // set by the launcher
-  uint32_t* flag;          // 1: invalid offsets
-  float4* slots;           // segment sums (hi, lo, token count)
-  int split;               // CTAs per sequence
+  uint32_t* flags;         // [checks] 1: invalid offsets
+  int checks;
+  float2* sums;            // per sequence: sum, token count
+  int split;               // CTAs that write a sequence's gradient
 };
 size_t pref_workspace_bytes(int64_t n_tok, int64_t n_pairs);
 cudaError_t launch_preference_loss(PrefArgs a, void* workspace, cudaStream_t stream);
