@@ -45,6 +45,9 @@ __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) {
     if (mbar_try_wait(bar, parity)) return;
 }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
 __device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x,
                                         int y) {
   asm volatile(
