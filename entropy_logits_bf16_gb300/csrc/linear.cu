@@ -95,15 +95,16 @@ __device__ __forceinline__ float rcp(float v) { return __fdividef(1.f, v); }
 // Phi(-|z|), Phi the normal distribution function: 1/2 erfc(|z| / sqrt 2) by
 // Abramowitz and Stegun 7.1.26, erfc(x) = (a1 t + ... + a5 t^5) exp(-x^2) with t = 1 / (1 + p x)
 // (absolute error 1.5e-7).  About 13 instructions; the product with the exponential keeps
-// the far tail free of cancellation.
-__device__ __forceinline__ float normal_tail(float z) {
+// the far tail free of cancellation.  `bell`: exp(-z^2 / 2).
+__device__ __forceinline__ float normal_tail(float z, float& bell) {
   const float x = fabsf(z) * 0.70710678118654752f;
   const float t = rcp(__fmaf_rn(0.3275911f, x, 1.f));
   float q = __fmaf_rn(1.061405429f, t, -1.453152027f);
   q = __fmaf_rn(q, t, 1.421413741f);
   q = __fmaf_rn(q, t, -0.284496736f);
   q = __fmaf_rn(q, t, 0.254829592f);
-  return 0.5f * (q * t) * ex2(-(x * x) * kLog2e);
+  bell = ex2(-(x * x) * kLog2e);
+  return 0.5f * (q * t) * bell;
 }
 // act of W values; the choice is made once.
 template <int W>
@@ -111,8 +112,9 @@ __device__ __forceinline__ void activate(float (&v)[W], int act) {
   if (act == RLK_ACT_GELU) {
 #pragma unroll
     for (int j = 0; j < W; ++j) {
-      const float tail = v[j] * normal_tail(v[j]);
-      v[j] = v[j] > 0.f ? __fsub_rn(v[j], tail) : tail;
+      float bell;
+      const float tail = normal_tail(v[j], bell);
+      v[j] = v[j] * (v[j] > 0.f ? __fsub_rn(1.f, tail) : tail);
     }
   } else if (act == RLK_ACT_SILU) {
 #pragma unroll
@@ -122,15 +124,17 @@ __device__ __forceinline__ void activate(float (&v)[W], int act) {
     for (int j = 0; j < W; ++j) v[j] = v[j] < 0.f ? 0.f : v[j];
   }
 }
-// act'(z), to full fp32 accuracy: it goes into sums that stay in fp32.
+// act'(z), to a few 2^-24.
 template <int ACT>
 __device__ __forceinline__ float activation_slope(float z) {
-  if (ACT == RLK_ACT_GELU)
-    return 0.5f * (1.f + erff(z * 0.70710678118654752f)) +
-           z * expf(-0.5f * z * z) * 0.39894228040143268f;
+  if (ACT == RLK_ACT_GELU) {   // Phi(z) + z phi(z)
+    float bell;
+    const float tail = normal_tail(z, bell);
+    return __fmaf_rn(z * bell, 0.39894228040143268f, z > 0.f ? 1.f - tail : tail);
+  }
   if (ACT == RLK_ACT_SILU) {
-    const float s = 1.f / (1.f + expf(-z));
-    return s * (1.f + z * (1.f - s));
+    const float s = rcp(1.f + ex2(-z * kLog2e));
+    return s * __fmaf_rn(z, 1.f - s, 1.f);
   }
   if (ACT == RLK_ACT_RELU) return z > 0.f ? 1.f : (z != z ? z : 0.f);
   return 1.f;
@@ -751,7 +755,8 @@ __global__ void __launch_bounds__(DT) linear_dz_kernel(LinearBwdArgs a, uint16_t
     if (c + j < a.N) db_part[(int64_t)blockIdx.y * pitch + c + j] = sum[j];
 }
 
-// Adds the parts in order: 32 columns a CTA, warp w takes parts w, w + 8, ...
+// Adds the parts in order: 32 columns a CTA, warp w takes parts w, w + 8, ...,
+// 20 of them on their way together.
 __global__ void __launch_bounds__(256) linear_db_kernel(const float* part, int64_t pitch, int parts, int64_t N, float* db,
                                                         int accumulate) {
   pdl_wait();
@@ -759,9 +764,12 @@ __global__ void __launch_bounds__(256) linear_db_kernel(const float* part, int64
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t c = (int64_t)blockIdx.x * 32 + lane;
   float v = 0.f;
-  if (c < N) {
-#pragma unroll 8
-    for (int k = warp; k < parts; k += 8) v = __fadd_rn(v, part[(int64_t)k * pitch + c]);
+  for (int k0 = warp; k0 < parts; k0 += 160) {
+    float x[20];
+#pragma unroll
+    for (int u = 0; u < 20; ++u) x[u] = c < N && k0 + 8 * u < parts ? part[(int64_t)(k0 + 8 * u) * pitch + c] : 0.f;
+#pragma unroll
+    for (int u = 0; u < 20; ++u) v = __fadd_rn(v, x[u]);
   }
   s[warp][lane] = v;
   __syncthreads();

@@ -839,19 +839,23 @@ __global__ void __launch_bounds__(kMaxGroup, 1) norm_bwd_kernel(NormBwdArgs a, i
   }
 }
 
-// Adds the parts in order: 32 columns a CTA, warp w takes parts w, w + 8, ...
+// Adds the parts in order: 32 columns a CTA, warp w takes parts w, w + 8, ...,
+// 20 of them on their way together.
 __global__ void __launch_bounds__(256) norm_param_sum_kernel(NormBwdArgs a, int parts) {
   pdl_wait();
   __shared__ float s[8][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float* out = blockIdx.y ? a.db : a.dw;
   if (!out) return;
-  const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+  const int64_t c = (int64_t)blockIdx.x * 32 + lane, pitch = 2 * part_pitch(a.H);
+  const float* p = a.workspace + blockIdx.y * part_pitch(a.H) + c;
   float v = 0.f;
-  if (c < a.H) {
-    const float* p = a.workspace + blockIdx.y * part_pitch(a.H) + c;
-#pragma unroll 8
-    for (int k = warp; k < parts; k += 8) v = __fadd_rn(v, p[(int64_t)k * 2 * part_pitch(a.H)]);
+  for (int k0 = warp; k0 < parts; k0 += 160) {
+    float x[20];
+#pragma unroll
+    for (int u = 0; u < 20; ++u) x[u] = c < a.H && k0 + 8 * u < parts ? p[(k0 + 8 * u) * pitch] : 0.f;
+#pragma unroll
+    for (int u = 0; u < 20; ++u) v = __fadd_rn(v, x[u]);
   }
   s[warp][lane] = v;
   __syncthreads();

@@ -213,3 +213,18 @@ def test_autograd_matches_the_calls(cuda_lib):
             kept = cuda_lib.checkpoint_pack(x) if keep else x
             dx, dw, db = cuda_lib.linear_backward(dy, kept, w, z, activation=act, weight_grad_dtype=BF)
             assert all(torch.equal(p.grad, q) for p, q in zip(ps, (dx, dw, db, dy)))
+
+
+@pytest.mark.parametrize("M,N,K", [(2601, 2003, 4100), (4100, 2601, 2003), (2600, 2560, 4096)])
+def test_many_rounds_of_tiles(cuda_lib, M, N, K):
+    """More tiles of 256 x 256 than pairs of SMs, a ragged last round and a long K
+    (forward; and dw, whose K is M).  Small whole numbers, so every sum is exact."""
+    g = torch.Generator().manual_seed(M)
+    ints = lambda *s: torch.randint(-3, 4, s, generator=g).to(BF).cuda()
+    x, w, r, dy = ints(M, K), ints(N, K), ints(M, N), ints(M, N)
+    for _ in range(2):
+        y = cuda_lib.linear(x, w, None, r, out_dtype=F32)
+        dx, dw, db = cuda_lib.linear_backward(dy, x, w, grad_dtype=F32)
+        assert torch.equal(y, x.float() @ w.float().t() + r.float())
+        assert torch.equal(dx, dy.float() @ w.float()) and torch.equal(dw, dy.float().t() @ x.float())
+        assert torch.equal(db, dy.float().sum(0))
