@@ -10,8 +10,8 @@
 // threads), so each pass reads every element once:
 //  * forward: one row a group; deviations from the mean, then their squares.
 //  * backward: persistent CTAs; a thread keeps its columns of w and of the
-//    partial dw, db over all its rows, and copies its part of the next row into its own
-//    place in shared memory (cp.async) while it works on this one.  The CTAs' partials go to
+//    partial dw, db over all its rows, and the next rows are on their way to shared
+//    memory while it works on this one.  The CTAs' partials go to
 //    the workspace and a second kernel adds them in order.
 // Columns are taken 8 at a time (16-byte loads) where every row starts on a
 // 16-byte boundary, else one at a time with consecutive columns on
@@ -369,26 +369,43 @@ __device__ __forceinline__ void write_checkpoint(const CheckpointView& ck, int64
 }
 
 // ---- rows on their way to shared memory
+// Bulk copies: one thread of a group asks for whole rows, which keeps more bytes
+// on their way than loads or cp.async do (with those the kernels read 3.6
+// TB/s, whatever the depth).  A place has an mbarrier; every wait on one is
+// bounded, and a row that did not come in time is NaN.
 // Types: 0 bf16, 1 fp32, 2 checkpoint codes.
 constexpr int kFromCk = 2;
 constexpr int bytes_of(int type) { return type == 1 ? 4 : (type == 0 ? 2 : 1); }
+constexpr int kMaxDepth = 4;
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// The oldest of `depth` rows on their way has landed (this thread's copies).
-__device__ __forceinline__ void cp_wait(int depth) {
-  if (depth == 4) asm volatile("cp.async.wait_group 3;" ::: "memory");
-  else if (depth == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
-  else asm volatile("cp.async.wait_group 0;" ::: "memory");
-}
+// The mbarriers of a group's places, and where its copies stand.
+struct Places {
+  uint32_t bar;     // the first barrier
+  int depth, shift, issued;
+  volatile int* abort;
+  __device__ __forceinline__ Places(uint64_t* bars, const Group& g, int d, volatile int* flag)
+      : bar(smem_u32(bars + g.index * kMaxDepth)), depth(d), shift(d == 4 ? 2 : (d == 2 ? 1 : 0)), issued(0), abort(flag) {
+    if (threadIdx.x == 0) *abort = 0;
+    if (g.t == 0) {
+      for (int k = 0; k < depth; ++k) mbar_init(bar + 8 * k, 1);
+      fence_mbar_init();
+      fence_proxy_async_smem();
+    }
+    __syncthreads();
+  }
+  __device__ __forceinline__ int of(int i) const { return i & (depth - 1); }
+  __device__ __forceinline__ uint32_t bar_of(int i) const { return bar + 8 * of(i); }
+  __device__ __forceinline__ bool wait(int i) const { return mbar_wait_bounded(bar_of(i), (uint32_t)(i >> shift) & 1u, abort); }
+  // after a wait has run out: lets the copies already asked for land
+  __device__ __forceinline__ void drain() const {
+    if (!*abort) return;
+    for (int i = issued > depth ? issued - depth : 0; i < issued; ++i)
+      for (uint32_t k = 0; k < (1u << 22); ++k)
+        if (mbar_try_wait(bar_of(i), (uint32_t)(i >> shift) & 1u)) break;
+  }
+};
 
-// Bytes of a row's place in shared memory.  VW = 8: the threads' 8-column
-// pieces; VW = 1: the row's bytes at its own distance from a 16-byte boundary,
+// Bytes of a row's place in shared memory.  VW = 8: the threads' columns; VW = 1: the row's bytes at its own distance from a 16-byte boundary,
 // and zeros up to the threads' last column (and the distance).
 template <int TYPE, int VW, int E>
 __host__ __device__ __forceinline__ int place_bytes(int H, int n) {
@@ -396,7 +413,7 @@ __host__ __device__ __forceinline__ int place_bytes(int H, int n) {
 }
 
 // VW = 1: the element of a row that a thread carries to shared memory itself,
-// being outside the whole 16-byte units that cp.async copies: threads 0..7 those
+// being outside the whole 16-byte units of the bulk copy: threads 0..7 those
 // before the first boundary, 8..15 those after the last.  -1: none.
 template <int TYPE>
 __device__ __forceinline__ int edge_byte(int to_boundary, int row_bytes, int t) {
@@ -409,45 +426,27 @@ __device__ __forceinline__ int edge_byte(int to_boundary, int row_bytes, int t) 
 }
 __device__ __forceinline__ int to_boundary(const void* p) { return (int)(-reinterpret_cast<uintptr_t>(p) & 15u); }
 
-// Starts the copy of a row (at element `at` of p) into its place, and returns the
-// edge element that this thread has to store there when it is used (VW = 1).
-template <int TYPE, int VW, int E, bool FULL>
-__device__ __forceinline__ uint32_t start_row(uint8_t* place, const void* p, int64_t at, int H, const Group& g) {
+// The 16-byte units of a row (at element `at` of p) that a bulk copy brings, and
+// where they go in its place.
+struct Body {
+  const char* src;
+  int offset, bytes;
+};
+template <int TYPE, int VW>
+__device__ __forceinline__ Body body_of(const void* p, int64_t at, int H) {
   constexpr int es = bytes_of(TYPE);
   const char* src = static_cast<const char*>(p) + at * es;
-  const uint32_t dst = smem_u32(place);
-  if (VW == 8 && TYPE == 1) {
-    // a thread's 8 columns are two 16-byte units: a warp's (a group's) are
-    // copied in order, so that no request asks for half a sector
-    const int m = g.n < 32 ? g.n : 32, u0 = g.t & (m - 1);
-#pragma unroll
-    for (int k = 0; k < E / 8; ++k) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int c = (k * g.n + (g.t - u0)) * 8 + (u0 + h * m) * 4;
-        const int have = FULL ? 16 : (H - c < 4 ? H - c : 4) * 4;
-        if (FULL || have > 0) cp_async16(dst + c * 4, src + c * 4, have);
-      }
-    }
-    return 0u;
-  }
-  if (VW == 8) {
-#pragma unroll
-    for (int k = 0; k < E / 8; ++k) {
-      const int c = (k * g.n + g.t) * 8;
-      const int have = FULL ? 8 * es : (H - c < 8 ? H - c : 8) * es;
-      if (!FULL && have <= 0) continue;
-      if (TYPE == kFromCk) cp_async8(dst + c, src + c, have);
-      else cp_async16(dst + c * es, src + c * es, have);
-    }
-    return 0u;
-  }
-  const int row_bytes = H * es, gap = to_boundary(src);
-  const int head = gap < row_bytes ? gap : row_bytes;
-  const int body = TYPE == kFromCk ? (row_bytes + 15) & ~15 : (row_bytes - head) & ~15;
-  const uint32_t d = dst + (uint32_t)(reinterpret_cast<uintptr_t>(src) & 15u) + head;
-  for (int o = g.t * 16; o < body; o += g.n * 16) cp_async16(d + o, src + head + o, 16);
-  const int e = edge_byte<TYPE>(gap, row_bytes, g.t);
+  const int row_bytes = H * es;
+  if (VW == 8 || TYPE == kFromCk) return Body{src, 0, (row_bytes + 15) & ~15};   // whole units: see rows16
+  const int gap = to_boundary(src), head = gap < row_bytes ? gap : row_bytes;
+  return Body{src + head, (int)(reinterpret_cast<uintptr_t>(src) & 15u) + head, (row_bytes - head) & ~15};
+}
+// VW = 1: the edge element of a row that this thread has to store when the row is used.
+template <int TYPE>
+__device__ __forceinline__ uint32_t load_edge(const void* p, int64_t at, int H, const Group& g) {
+  constexpr int es = bytes_of(TYPE);
+  const char* src = static_cast<const char*>(p) + at * es;
+  const int e = edge_byte<TYPE>(to_boundary(src), H * es, g.t);
   if (e < 0) return 0u;
   return TYPE == 1 ? *reinterpret_cast<const uint32_t*>(src + e) : *reinterpret_cast<const uint16_t*>(src + e);
 }
@@ -472,7 +471,7 @@ __device__ __forceinline__ void store_edge(uint8_t* place, const void* p, int64_
 }
 
 // A thread's columns of a row in shared memory (0 past the end; codes times
-// their steps).  VW = 8: what this thread or its warp copied; VW = 1: after a barrier.
+// their steps).
 template <int TYPE, int VW, int E, bool FULL>
 __device__ __forceinline__ void take_row(const uint8_t* place, const void* p, int64_t at, int H, const Group& g,
                                          const float (&step)[VW == 8 ? E / 8 : E], float2 (&v)[E / 2]) {
@@ -520,6 +519,7 @@ __device__ __forceinline__ void take_row(const uint8_t* place, const void* p, in
 // VW = 1: zeros in the places of `depth` rows, before the first copy.
 __device__ __forceinline__ void clear_places(uint8_t* mine, int bytes, const Group& g) {
   for (int o = g.t * 16; o < bytes; o += g.n * 16) *reinterpret_cast<uint4*>(mine + o) = make_uint4(0u, 0u, 0u, 0u);
+  fence_proxy_async_smem();   // before the copies into them
   g.sync();
 }
 
@@ -547,15 +547,23 @@ __global__ void __launch_bounds__(kMaxGroup, 1) norm_fwd_kernel(NormArgs a, int 
   const float inv_h = __fdiv_rn(1.f, (float)H);
   const float none[VW == 8 ? E / 8 : E] = {};
 
+  __shared__ uint64_t s_bars[kMaxDepth * 64];
+  __shared__ int s_abort;
+  Places places(s_bars, g, depth, &s_abort);
   if (VW == 1) clear_places(mine, depth * size, g);
   pdl_wait();   // the rows may come from the kernel before
   uint32_t edge[2] = {0u, 0u};   // VW = 1: depth is at most 2
   auto start = [&](int i) -> uint32_t {
     const int64_t row = row0 + g.index + i * stride;
-    uint32_t e = 0u;
-    if (i < iters && row < a.T) e = start_row<XT, VW, E, FULL>(mine + (i & (depth - 1)) * size, a.x, row * a.ldx, H, g);
-    cp_commit();
-    return e;
+    if (i >= iters || row >= a.T || *places.abort) return 0u;
+    places.issued = i + 1;
+    if (g.t == 0) {
+      const Body b = body_of<XT, VW>(a.x, row * a.ldx, H);
+      fence_proxy_async_smem();   // the place was read
+      mbar_expect_tx(places.bar_of(i), b.bytes);
+      if (b.bytes > 0) bulk_copy_g2s(smem_u32(mine + places.of(i) * size + b.offset), b.src, b.bytes, places.bar_of(i));
+    }
+    return VW == 1 ? load_edge<XT>(a.x, row * a.ldx, H, g) : 0u;
   };
   edge[0] = start(0);
   if (depth > 1) edge[1] = start(1);
@@ -573,17 +581,18 @@ __global__ void __launch_bounds__(kMaxGroup, 1) norm_fwd_kernel(NormArgs a, int 
   for (int i = 0; i < iters; ++i) {
     const int64_t row = row0 + g.index + i * stride;
     const bool live = row < a.T;
-    uint8_t* place = mine + (i & (depth - 1)) * size;
+    const uint8_t* place = mine + places.of(i) * size;
     float2 x[E / 2];
-    if (VW == 1 && live) store_edge<XT>(place, a.x, row * a.ldx, H, g, edge[0]);
-    cp_wait(depth);
+    if (VW == 1 && live) store_edge<XT>(mine + places.of(i) * size, a.x, row * a.ldx, H, g, edge[0]);
+    const bool came = !live || places.wait(i);
     if (VW == 1) g.sync();
-    else if (XT == 1) __syncwarp();
-    if (live) take_row<XT, VW, E, FULL>(place, a.x, row * a.ldx, H, g, none, x);
-    else fill<E>(x, 0.f);
-    if (VW == 8) {   // into the place just read: a thread reads what it copied itself, or its warp did
-      if (XT == 1) __syncwarp();
-      start(i + depth);
+    if (!live) {
+      fill<E>(x, 0.f);
+    } else if (came) {
+      take_row<XT, VW, E, FULL>(place, a.x, row * a.ldx, H, g, none, x);
+    } else {
+      fill<E>(x, NAN);
+      if (a.status) atomicOr(a.status, RLK_STATUS_TIMEOUT);
     }
     float m = 0.f;
     if (!a.rms) {
@@ -614,15 +623,11 @@ __global__ void __launch_bounds__(kMaxGroup, 1) norm_fwd_kernel(NormArgs a, int 
     float v[1] = {__fadd_rn(s.x, s.y)};
     group_sum(v, g, s_red, buf);
     const float var = __fmul_rn(v[0], inv_h);
-    if (VW == 1) {   // the sum's barrier: every thread has read the place
+    {   // the sum's barrier: every thread has read the place
       if (n <= 32) __syncwarp();
       const uint32_t e = start(i + depth);
-      if (depth == 2) {
-        edge[0] = edge[1];
-        edge[1] = e;
-      } else {
-        edge[0] = e;
-      }
+      edge[0] = depth == 2 ? edge[1] : e;
+      edge[1] = e;
     }
     const bool bad = !isfinite(var);
     const float r = bad ? NAN : inv_sqrt(__fadd_rn(var, a.eps));
@@ -653,6 +658,7 @@ __global__ void __launch_bounds__(kMaxGroup, 1) norm_fwd_kernel(NormArgs a, int 
     }
     if (live) store_cols<VW, E, FULL>(a.y, a.y_dtype, row * a.ldy, H, g, x);
   }
+  if (g.t == 0) places.drain();
 }
 
 // ---- backward
@@ -678,18 +684,30 @@ __global__ void __launch_bounds__(kMaxGroup, 1) norm_bwd_kernel(NormBwdArgs a, i
   const void* xp = XT == kFromCk ? static_cast<const void*>(a.ck.codes) : a.x;
   const int64_t ldx = XT == kFromCk ? a.ck.ldc : a.ldx;
 
+  __shared__ uint64_t s_bars[kMaxDepth * 64];
+  __shared__ int s_abort;
+  Places places(s_bars, g, depth, &s_abort);
   if (VW == 1) clear_places(mine, depth * size, g);
   pdl_wait();
   uint2 edge[2] = {make_uint2(0u, 0u), make_uint2(0u, 0u)};   // VW = 1: depth is at most 2
-  auto place = [&](int i) { return mine + (i & (depth - 1)) * size; };
+  auto place = [&](int i) { return mine + places.of(i) * size; };
   auto start = [&](int i) -> uint2 {
     const int64_t row = row0 + g.index + i * stride;
     uint2 e = make_uint2(0u, 0u);
-    if (i < iters && row < a.T) {
-      e.x = start_row<DT, VW, E, FULL>(place(i), a.dy, row * a.lddy, H, g);
-      e.y = start_row<XT, VW, E, FULL>(place(i) + dy_size, xp, row * ldx, H, g);
+    if (i >= iters || row >= a.T || *places.abort) return e;
+    places.issued = i + 1;
+    if (g.t == 0) {
+      const Body y = body_of<DT, VW>(a.dy, row * a.lddy, H), x = body_of<XT, VW>(xp, row * ldx, H);
+      fence_proxy_async_smem();   // the place was read
+      const uint32_t bar = places.bar_of(i);
+      mbar_expect_tx(bar, y.bytes + x.bytes);
+      if (y.bytes > 0) bulk_copy_g2s(smem_u32(place(i) + y.offset), y.src, y.bytes, bar);
+      if (x.bytes > 0) bulk_copy_g2s(smem_u32(place(i) + dy_size + x.offset), x.src, x.bytes, bar);
     }
-    cp_commit();
+    if (VW == 1) {
+      e.x = load_edge<DT>(a.dy, row * a.lddy, H, g);
+      e.y = load_edge<XT>(xp, row * ldx, H, g);
+    }
     return e;
   };
   if (depth > 0) edge[0] = start(0);
@@ -746,16 +764,14 @@ __global__ void __launch_bounds__(kMaxGroup, 1) norm_bwd_kernel(NormBwdArgs a, i
         store_edge<DT>(place(i), a.dy, row * a.lddy, H, g, edge[0].x);
         store_edge<XT>(place(i) + dy_size, xp, row * ldx, H, g, edge[0].y);
       }
-      cp_wait(depth);
+      const bool came = !live || places.wait(i);
       if (VW == 1) g.sync();
-      else if (XT == 1 || DT == 1) __syncwarp();
-      if (live) {
+      if (live && came) {
         take_row<DT, VW, E, FULL>(place(i), a.dy, row * a.lddy, H, g, step, dy);
         take_row<XT, VW, E, FULL>(place(i) + dy_size, xp, row * ldx, H, g, step, h);
-      }
-      if (VW == 8) {   // into the place just read: a thread reads what it copied itself, or its warp did
-        if (XT == 1 || DT == 1) __syncwarp();
-        start(i + depth);
+      } else if (live) {
+        fill<E>(dy, NAN);
+        fill<E>(h, NAN);
       }
     } else if (live) {
       load_cols<VW, E, FULL>(a.dy, DT, row * a.lddy, H, g, dy);
@@ -791,15 +807,11 @@ __global__ void __launch_bounds__(kMaxGroup, 1) norm_bwd_kernel(NormBwdArgs a, i
     }
     float v[2] = {__fadd_rn(s2.x, s2.y), __fadd_rn(s1.x, s1.y)};
     group_sum(v, g, s_red, buf);
-    if (VW == 1 && depth > 0) {   // the sum's barrier: every thread has read the place
+    if (depth > 0) {   // the sum's barrier: every thread has read the place
       if (n <= 32) __syncwarp();
       const uint2 e = start(i + depth);
-      if (depth == 2) {
-        edge[0] = edge[1];
-        edge[1] = e;
-      } else {
-        edge[0] = e;
-      }
+      edge[0] = depth == 2 ? edge[1] : e;
+      edge[1] = e;
     }
     const float mg = a.rms ? 0.f : __fmul_rn(v[1], inv_h), mgh = __fmul_rn(v[0], inv_h);
 #pragma unroll
@@ -807,6 +819,7 @@ __global__ void __launch_bounds__(kMaxGroup, 1) norm_bwd_kernel(NormBwdArgs a, i
       h[j] = mul2(both(r), fma2(h[j], both(-mgh), add2(dy[j], both(-mg))));
     if (live) store_cols<VW, E, FULL>(a.dx, a.dx_dtype, row * a.lddx, H, g, h);
   }
+  if (g.t == 0) places.drain();
   if (!a.workspace) return;
   float* part = a.workspace + (int64_t)blockIdx.x * 2 * part_pitch(a.H);
   if constexpr (SACC) {
@@ -820,7 +833,6 @@ __global__ void __launch_bounds__(kMaxGroup, 1) norm_bwd_kernel(NormBwdArgs a, i
   } else {
     // the CTA's groups, added in order (every copy has landed: the shared memory is free again)
     if (g.count > 1) {
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
       for (int k = 0; k < g.count; ++k) {
         __syncthreads();
         if (g.index != k) continue;
@@ -878,7 +890,7 @@ int group_for(int64_t H, bool vec) {
   while (n < want) n *= 2;
   return n;
 }
-constexpr size_t kSmemMost = 227 * 1024 - 1024;
+constexpr size_t kSmemMost = 223 * 1024;   // dynamic, beside the kernels' own 3 KB
 bool rows16(const void* p, int dtype, int64_t ld) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % (dtype ? 4 : 8) == 0;
 }
@@ -894,7 +906,7 @@ cudaError_t allow_smem(K kernel, std::atomic<int>* done) {
 }
 // Rows on their way that leave room for two CTAs an SM (one, of over 256 threads).
 int depth_for(size_t row, size_t fixed, int block, int most) {
-  const size_t room = block > 256 ? kSmemMost : kSmemMost / 2;
+  const size_t room = block > 256 ? kSmemMost : 110 * 1024;
   int d = most;
   while (d > 0 && fixed + d * row > room) d /= 2;
   return d;
@@ -963,7 +975,7 @@ size_t norm_bwd_workspace_bytes(int64_t T, int64_t H) {
 
 cudaError_t launch_norm_fwd(const NormArgs& a, cudaStream_t stream) {
   if (a.H <= kOnChip) {
-    const bool vec = rows16(a.x, a.dtype, a.ldx) && rows16(a.y, a.y_dtype, a.ldy) && base16(a.weight) && base16(a.bias);
+    const bool vec = a.H % 8 == 0 && rows16(a.x, a.dtype, a.ldx) && rows16(a.y, a.y_dtype, a.ldy) && base16(a.weight) && base16(a.bias);
     return a.dtype ? fwd_for<1>(a, vec, stream) : fwd_for<0>(a, vec, stream);
   }
   const int64_t cap = (int64_t)sm_count() * 4;
@@ -976,7 +988,7 @@ cudaError_t launch_norm_bwd(const NormBwdArgs& args, cudaStream_t stream) {
   if (!a.dw && !a.db) a.workspace = nullptr;
   int parts = 0;
   if (a.T > 0 && a.H <= kOnChip) {
-    const bool vec = rows16(a.dy, a.dy_dtype, a.lddy) && rows16(a.dx, a.dx_dtype, a.lddx) && base16(a.weight) &&
+    const bool vec = a.H % 8 == 0 && rows16(a.dy, a.dy_dtype, a.lddy) && rows16(a.dx, a.dx_dtype, a.lddx) && base16(a.weight) &&
                      (!a.x || rows16(a.x, a.dtype, a.ldx));
     const int type = !a.x ? kFromCk : a.dtype;
     cudaError_t e;
