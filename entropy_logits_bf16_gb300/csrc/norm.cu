@@ -532,9 +532,11 @@ __device__ __forceinline__ void fill(float2 (&v)[E / 2], float f) {
 // ---- forward
 // Persistent: a group takes rows index, + stride, ..., `depth` of them (1, 2, 4) on
 // their way to shared memory ahead of the one at work.  E = 16 keeps its columns of
-// weight and bias in registers.
+// weight and bias in registers.  R rows are at work together (their sums share
+// barriers); depth >= R.
 template <int XT, int VW, int E, bool FULL>
 __global__ void __launch_bounds__(kMaxGroup, 1) norm_fwd_kernel(NormArgs a, int n, int depth) {
+  constexpr int R = VW == 8 && E == 16 ? 2 : 1;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float s_red[128];
   int buf = 0;
@@ -578,85 +580,103 @@ __global__ void __launch_bounds__(kMaxGroup, 1) norm_fwd_kernel(NormArgs a, int 
     else fill<E>(b, 0.f);
   }
 
-  for (int i = 0; i < iters; ++i) {
-    const int64_t row = row0 + g.index + i * stride;
-    const bool live = row < a.T;
-    const uint8_t* place = mine + places.of(i) * size;
-    float2 x[E / 2];
-    if (VW == 1 && live) store_edge<XT>(mine + places.of(i) * size, a.x, row * a.ldx, H, g, edge[0]);
-    const bool came = !live || places.wait(i);
-    if (VW == 1) g.sync();
-    if (!live) {
-      fill<E>(x, 0.f);
-    } else if (came) {
-      take_row<XT, VW, E, FULL>(place, a.x, row * a.ldx, H, g, none, x);
-    } else {
-      fill<E>(x, NAN);
-      if (a.status) atomicOr(a.status, RLK_STATUS_TIMEOUT);
+  for (int i = 0; i < iters; i += R) {
+    float2 x[R][E / 2];
+    float m[R], v[R];
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      const int64_t row = row0 + g.index + (i + q) * stride;
+      const bool live = i + q < iters && row < a.T;
+      uint8_t* place = mine + places.of(i + q) * size;
+      if (VW == 1 && live) store_edge<XT>(place, a.x, row * a.ldx, H, g, edge[0]);
+      const bool came = !live || places.wait(i + q);
+      if (VW == 1) g.sync();
+      if (!live) {
+        fill<E>(x[q], 0.f);
+      } else if (came) {
+        take_row<XT, VW, E, FULL>(place, a.x, row * a.ldx, H, g, none, x[q]);
+      } else {
+        fill<E>(x[q], NAN);
+        if (a.status) atomicOr(a.status, RLK_STATUS_TIMEOUT);
+      }
+      m[q] = 0.f;
     }
-    float m = 0.f;
     if (!a.rms) {
-      float2 s = x[0];
 #pragma unroll
-      for (int j = 1; j < E / 2; ++j) s = add2(s, x[j]);
-      float v[1] = {__fadd_rn(s.x, s.y)};
-      group_sum(v, g, s_red, buf);
-      m = __fmul_rn(v[0], inv_h);
-    }
-    float2 s = both(0.f);
-    if ((FULL && VW == 8) || a.rms) {   // with m = 0 the zeros past the end add nothing
+      for (int q = 0; q < R; ++q) {
+        float2 s = x[q][0];
 #pragma unroll
-      for (int j = 0; j < E / 2; ++j) {
-        const float2 d = add2(x[j], both(-m));
-        s = fma2(d, d, s);
+        for (int j = 1; j < E / 2; ++j) s = add2(s, x[q][j]);
+        m[q] = __fadd_rn(s.x, s.y);
       }
-    } else {
-      const int n2 = fresh(n);
+      group_sum(m, g, s_red, buf);
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const int c = ((e / VW) * n2 + g.t) * VW + e % VW;
-        const float d = surely<VW, E, FULL>(e) || c < H ? __fsub_rn(elem<E>(x, e), m) : 0.f;
-        if (e % 2) s.y = __fmaf_rn(d, d, s.y);
-        else s.x = __fmaf_rn(d, d, s.x);
-      }
+      for (int q = 0; q < R; ++q) m[q] = __fmul_rn(m[q], inv_h);
     }
-    float v[1] = {__fadd_rn(s.x, s.y)};
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      float2 s = both(0.f);
+      if ((FULL && VW == 8) || a.rms) {   // with m = 0 the zeros past the end add nothing
+#pragma unroll
+        for (int j = 0; j < E / 2; ++j) {
+          const float2 d = add2(x[q][j], both(-m[q]));
+          s = fma2(d, d, s);
+        }
+      } else {
+        const int n2 = fresh(n);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const int c = ((e / VW) * n2 + g.t) * VW + e % VW;
+          const float d = surely<VW, E, FULL>(e) || c < H ? __fsub_rn(elem<E>(x[q], e), m[q]) : 0.f;
+          if (e % 2) s.y = __fmaf_rn(d, d, s.y);
+          else s.x = __fmaf_rn(d, d, s.x);
+        }
+      }
+      v[q] = __fadd_rn(s.x, s.y);
+    }
     group_sum(v, g, s_red, buf);
-    const float var = __fmul_rn(v[0], inv_h);
-    {   // the sum's barrier: every thread has read the place
-      if (n <= 32) __syncwarp();
-      const uint32_t e = start(i + depth);
+    // the sum's barrier: every thread has read the places
+    if (n <= 32) __syncwarp();
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      const uint32_t e = start(i + q + depth);
       edge[0] = depth == 2 ? edge[1] : e;
       edge[1] = e;
     }
-    const bool bad = !isfinite(var);
-    const float r = bad ? NAN : inv_sqrt(__fadd_rn(var, a.eps));
-    if (bad) m = NAN;
-    if (live && g.t == 0) {
-      if (a.mean && !a.rms) a.mean[row] = m;
-      if (a.rstd) a.rstd[row] = r;
-      if (bad && a.status) atomicOr(a.status, RLK_STATUS_NONFINITE);
-    }
-    if (a.ck.codes) write_checkpoint<VW, E, FULL>(a.ck, row, live, !bad, H, g, x);
 #pragma unroll
-    for (int j = 0; j < E / 2; ++j) {
-      x[j] = mul2(add2(x[j], both(-m)), both(r));
-      if constexpr (KEEP) x[j] = fma2(x[j], w[j], b[j]);
-    }
-    if constexpr (!KEEP) {
-      float2 p[E / 2];
-      if (a.weight) {
-        load_cols<VW, E, FULL>(a.weight, a.param_dtype, 0, H, g, p);
-#pragma unroll
-        for (int j = 0; j < E / 2; ++j) x[j] = mul2(x[j], p[j]);
+    for (int q = 0; q < R; ++q) {
+      const int64_t row = row0 + g.index + (i + q) * stride;
+      const bool live = i + q < iters && row < a.T;
+      const float var = __fmul_rn(v[q], inv_h);
+      const bool bad = !isfinite(var);
+      const float r = bad ? NAN : inv_sqrt(__fadd_rn(var, a.eps));
+      if (bad) m[q] = NAN;
+      if (live && g.t == 0) {
+        if (a.mean && !a.rms) a.mean[row] = m[q];
+        if (a.rstd) a.rstd[row] = r;
+        if (bad && a.status) atomicOr(a.status, RLK_STATUS_NONFINITE);
       }
-      if (a.bias) {
-        load_cols<VW, E, FULL>(a.bias, a.param_dtype, 0, H, g, p);
+      if (a.ck.codes) write_checkpoint<VW, E, FULL>(a.ck, row, live, !bad, H, g, x[q]);
 #pragma unroll
-        for (int j = 0; j < E / 2; ++j) x[j] = add2(x[j], p[j]);
+      for (int j = 0; j < E / 2; ++j) {
+        x[q][j] = mul2(add2(x[q][j], both(-m[q])), both(r));
+        if constexpr (KEEP) x[q][j] = fma2(x[q][j], w[j], b[j]);
       }
+      if constexpr (!KEEP) {
+        float2 p[E / 2];
+        if (a.weight) {
+          load_cols<VW, E, FULL>(a.weight, a.param_dtype, 0, H, g, p);
+#pragma unroll
+          for (int j = 0; j < E / 2; ++j) x[q][j] = mul2(x[q][j], p[j]);
+        }
+        if (a.bias) {
+          load_cols<VW, E, FULL>(a.bias, a.param_dtype, 0, H, g, p);
+#pragma unroll
+          for (int j = 0; j < E / 2; ++j) x[q][j] = add2(x[q][j], p[j]);
+        }
+      }
+      if (live) store_cols<VW, E, FULL>(a.y, a.y_dtype, row * a.ldy, H, g, x[q]);
     }
-    if (live) store_cols<VW, E, FULL>(a.y, a.y_dtype, row * a.ldy, H, g, x);
   }
   if (g.t == 0) places.drain();
 }
