@@ -164,6 +164,14 @@ __global__ void __launch_bounds__(256) norm_param_wide_kernel(NormBwdArgs a, int
 // ------------------------------------------------------------ rows on chip
 // A thread has E = 16 columns, or 32 in rows of over 8192 columns.
 constexpr int kMaxGroup = 512;       // threads of a row, at most
+// Registers of a thread.  The VW = 1 path (below) has longer chains of instructions
+// to hide and takes fewer, so that two CTAs of up to 320 threads share an SM.
+template <int VW, int E>
+constexpr int regs_of() { return VW == 1 && E == 16 ? 96 : 128; }
+// Where the backward's partial dw, db are: in shared memory when there are no
+// registers for them.
+template <int VW, int E>
+constexpr bool sums_in_smem() { return VW == 1 || E == 32; }
 constexpr int64_t kOnChip = 32 * kMaxGroup;
 
 // Element e of a thread's E columns is column ((e / VW) n + t) VW + e % VW: VW
@@ -535,7 +543,7 @@ __device__ __forceinline__ void fill(float2 (&v)[E / 2], float f) {
 // weight and bias in registers.  R rows are at work together (their sums share
 // barriers); depth >= R.
 template <int XT, int VW, int E, bool FULL>
-__global__ void __launch_bounds__(kMaxGroup, 1) norm_fwd_kernel(NormArgs a, int n, int depth) {
+__global__ void __maxnreg__((regs_of<VW, E>())) norm_fwd_kernel(NormArgs a, int n, int depth) {
   constexpr int R = VW == 8 && E == 16 ? 2 : 1;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float s_red[128];
@@ -684,11 +692,9 @@ __global__ void __launch_bounds__(kMaxGroup, 1) norm_fwd_kernel(NormArgs a, int 
 // ---- backward
 // XT: type of x, 2: from its checkpoint; DT: type of dy.  Rows as in the
 // forward; `depth` 0: a row is loaded when its turn comes (rows that do not fit).
-// E = 32: the partial dw, db live in shared memory (a thread has no registers for
-// 32 columns of them).
 template <int XT, int DT, int VW, int E, bool FULL>
-__global__ void __launch_bounds__(kMaxGroup, 1) norm_bwd_kernel(NormBwdArgs a, int n, int depth) {
-  constexpr bool SACC = E == 32;
+__global__ void __maxnreg__((regs_of<VW, E>())) norm_bwd_kernel(NormBwdArgs a, int n, int depth) {
+  constexpr bool SACC = sums_in_smem<VW, E>(), KEEP = E == 16;
   constexpr int STEPS = VW == 8 ? E / 8 : E;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float s_red[128];
@@ -696,9 +702,10 @@ __global__ void __launch_bounds__(kMaxGroup, 1) norm_bwd_kernel(NormBwdArgs a, i
   const Group g(n);
   const int H = (int)a.H;
   const float inv_h = __fdiv_rn(1.f, (float)H);
-  float2* s_acc = reinterpret_cast<float2*>(smem);   // SACC: [2][E / 2][n]
+  float2* s_acc = reinterpret_cast<float2*>(smem);   // SACC: [groups][2][E / 2][n]
   const int dy_size = place_bytes<DT, VW, E>(H, n), size = dy_size + place_bytes<XT, VW, E>(H, n);
-  uint8_t* mine = smem + (SACC ? 2 * E * n * 4 : 0) + (size_t)g.index * depth * size;
+  uint8_t* mine = smem + (SACC ? g.count * 2 * E * n * 4 : 0) + (size_t)g.index * depth * size;
+  if (SACC) s_acc += g.index * E * n;
   const int64_t stride = (int64_t)gridDim.x * g.count, row0 = (int64_t)blockIdx.x * g.count;
   const int iters = row0 < a.T ? (int)((a.T - row0 + stride - 1) / stride) : 0;
   const void* xp = XT == kFromCk ? static_cast<const void*>(a.ck.codes) : a.x;
@@ -758,7 +765,7 @@ __global__ void __launch_bounds__(kMaxGroup, 1) norm_bwd_kernel(NormBwdArgs a, i
     if (a.weight) load_cols<VW, E, FULL>(a.weight, a.param_dtype, 0, H, g, w);
     else fill<E>(w, 1.f);
   };
-  if (!SACC) load_w();   // else with each row: there are no registers to keep it in
+  if (KEEP) load_w();   // else with each row: there are no registers to keep it in
 #pragma unroll
   for (int j = 0; j < E / 2; ++j) {
     if (SACC) s_acc[j * n + g.t] = s_acc[(E / 2 + j) * n + g.t] = both(0.f);
@@ -808,7 +815,7 @@ __global__ void __launch_bounds__(kMaxGroup, 1) norm_bwd_kernel(NormBwdArgs a, i
       }
     }
     ahead(i + 1);
-    if (SACC) load_w();
+    if (!KEEP) load_w();
     float2 s1 = both(0.f), s2 = both(0.f);
 #pragma unroll
     for (int j = 0; j < E / 2; ++j) {   // past the row dy is 0, and h does not matter
@@ -843,11 +850,16 @@ __global__ void __launch_bounds__(kMaxGroup, 1) norm_bwd_kernel(NormBwdArgs a, i
   if (!a.workspace) return;
   float* part = a.workspace + (int64_t)blockIdx.x * 2 * part_pitch(a.H);
   if constexpr (SACC) {
+    if (g.count > 1) __syncthreads();
+    if (g.index > 0) return;
     float2 v[E / 2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
 #pragma unroll
-      for (int j = 0; j < E / 2; ++j) v[j] = s_acc[(k * E / 2 + j) * n + g.t];
+      for (int j = 0; j < E / 2; ++j) {   // the CTA's groups, added in order
+        v[j] = s_acc[(k * E / 2 + j) * n + g.t];
+        for (int q = 1; q < g.count; ++q) v[j] = add2(v[j], s_acc[q * E * n + (k * E / 2 + j) * n + g.t]);
+      }
       store_cols<VW, E, FULL>(part + k * part_pitch(a.H), 1, 0, H, g, v);
     }
   } else {
@@ -924,9 +936,12 @@ cudaError_t allow_smem(K kernel, std::atomic<int>* done) {
   if (e == cudaSuccess && ds >= 0) done[ds].store(1);
   return e;
 }
-// Rows on their way that leave room for two CTAs an SM (one, of over 256 threads).
-int depth_for(size_t row, size_t fixed, int block, int most) {
-  const size_t room = block > 256 ? kSmemMost : 110 * 1024;
+// CTAs an SM: by the registers, two at most.
+template <int VW, int E>
+int ctas_for(int block) { return 2 * block * regs_of<VW, E>() <= 65536 ? 2 : 1; }
+// Rows on their way, as many (a power of two) as leave room for the SM's CTAs.
+int depth_for(size_t row, size_t fixed, int ctas, int most) {
+  const size_t room = ctas == 1 ? kSmemMost : 110 * 1024;
   int d = most;
   while (d > 0 && fixed + d * row > room) d /= 2;
   return d;
@@ -939,8 +954,8 @@ cudaError_t fwd(const NormArgs& a, cudaStream_t stream) {
   if (cudaError_t e = allow_smem(kernel, done); e != cudaSuccess) return e;
   const int n = group_for(a.H, VW == 8), block = n > 128 ? n : 256, groups = block / n;
   const size_t row = (size_t)groups * place_bytes<XT, VW, E>((int)a.H, n);
-  const int depth = depth_for(row, 0, block, VW == 8 ? 4 : 2);
-  const int64_t want = (a.T + groups - 1) / groups, cap = (int64_t)sm_count() * (block > 256 ? 1 : 2);
+  const int ctas = ctas_for<VW, E>(block), depth = depth_for(row, 0, ctas, VW == 8 ? 4 : 2);
+  const int64_t want = (a.T + groups - 1) / groups, cap = (int64_t)sm_count() * ctas;
   const cudaError_t e = launch_after(kernel, dim3((unsigned)(want < cap ? want : cap)), dim3(block), depth * row, stream, a, n, depth);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -966,13 +981,14 @@ cudaError_t bwd(const NormBwdArgs& a, int& parts, cudaStream_t stream) {
   static std::atomic<int> done[64];
   if (cudaError_t e = allow_smem(kernel, done); e != cudaSuccess) return e;
   const int n = group_for(a.H, VW == 8), block = n > 128 ? n : 256, groups = block / n;
-  const size_t acc = (size_t)2 * E * n * sizeof(float);
+  constexpr bool SACC = sums_in_smem<VW, E>();
+  const size_t acc = (size_t)2 * E * n * sizeof(float) * (SACC ? groups : 1);
   const size_t row = (size_t)groups * (place_bytes<XT, VW, E>((int)a.H, n) + place_bytes<DT, VW, E>((int)a.H, n));
-  const int depth = depth_for(row, E == 32 ? acc : 0, block, VW == 8 ? 4 : 2);
+  const int ctas = ctas_for<VW, E>(block), depth = depth_for(row, SACC ? acc : 0, ctas, VW == 8 ? 4 : 2);
   size_t smem = depth * row;
-  if (E == 32) smem += acc;
+  if (SACC) smem += acc;
   else if (groups > 1 && smem < acc) smem = acc;
-  const int64_t want = (a.T + groups - 1) / groups, cap = block > 256 ? kNormParts / 2 : kNormParts;
+  const int64_t want = (a.T + groups - 1) / groups, cap = kNormParts / 2 * ctas;
   parts = (int)(want < cap ? want : cap);
   const cudaError_t e = launch_after(kernel, dim3(parts), dim3(block), smem, stream, a, n, depth);
   return e != cudaSuccess ? e : cudaGetLastError();
