@@ -78,6 +78,7 @@ struct Epilogue {
   int64_t ldz;
   int accumulate;      // y (fp32) is added to
   int vec;             // rows of y, z and residual start on 16-byte boundaries
+  int even;            // they start on 4-byte boundaries, and N is even
 };
 struct GemmParams {
   int64_t M, N;
@@ -207,41 +208,76 @@ __device__ __forceinline__ void finish8(const Epilogue& e, int64_t row, int64_t 
       if (j < n) y[j] = e.accumulate ? __fadd_rn(y[j], v[j]) : v[j];
   }
 }
-// One column of R rows, `step` apart from `row` on, any alignment; those up to
-// n rows from `row` exist.
-template <int R>
-__device__ __forceinline__ void finish_rows(const Epilogue& e, int64_t row, int step, int n, int64_t col, float (&v)[R],
-                                            float bias, const uint16_t (&res)[R]) {
+// W columns (1, or 2 at an even place of rows that start on 4-byte boundaries) of R
+// rows, `step` apart from `row` on; those up to n rows from `row` exist.
+template <int R, int W>
+__device__ __forceinline__ void finish_rows(const Epilogue& e, int64_t row, int step, int n, int64_t col, float (&v)[R * W],
+                                            const float (&bias)[W], const uint32_t (&res)[R]) {
 #pragma unroll
-  for (int k = 0; k < R; ++k) v[k] = __fadd_rn(v[k], bias);
-  if (e.z) {
-    uint16_t* z = e.z + row * e.ldz + col;
+  for (int k = 0; k < R * W; ++k) v[k] = __fadd_rn(v[k], bias[k % W]);
+  auto store = [&](uint16_t* p, int64_t ld) {
 #pragma unroll
-    for (int k = 0; k < R; ++k)
-      if (k * step < n) z[k * step * e.ldz] = (uint16_t)pack_bf16(v[k], 0.f);
-  }
+    for (int k = 0; k < R; ++k) {
+      if (k * step >= n) continue;
+      if (W == 2) *reinterpret_cast<uint32_t*>(p + k * step * ld) = pack_bf16(v[k * W], v[k * W + W - 1]);
+      else p[k * step * ld] = (uint16_t)pack_bf16(v[k * W], 0.f);
+    }
+  };
+  if (e.z) store(e.z + row * e.ldz + col, e.ldz);
   activate(v, e.act);
   if (e.residual) {
 #pragma unroll
-    for (int k = 0; k < R; ++k) v[k] = __fadd_rn(v[k], bf16_val(res[k]));
+    for (int k = 0; k < R * W; ++k) v[k] = __fadd_rn(v[k], k % W ? bf16_hi(res[k / W]) : bf16_lo(res[k / W]));
   }
   if (e.y_dtype == 0) {
-    uint16_t* y = static_cast<uint16_t*>(e.y) + row * e.ldy + col;
-#pragma unroll
-    for (int k = 0; k < R; ++k)
-      if (k * step < n) y[k * step * e.ldy] = (uint16_t)pack_bf16(v[k], 0.f);
+    store(static_cast<uint16_t*>(e.y) + row * e.ldy + col, e.ldy);
   } else {
     float* y = static_cast<float*>(e.y) + row * e.ldy + col;
 #pragma unroll
-    for (int k = 0; k < R; ++k)
-      if (k * step < n) y[k * step * e.ldy] = e.accumulate ? __fadd_rn(y[k * step * e.ldy], v[k]) : v[k];
+    for (int k = 0; k < R * W; ++k) {
+      float* q = y + (k / W) * step * e.ldy + k % W;
+      if ((k / W) * step < n) *q = e.accumulate ? __fadd_rn(*q, v[k]) : v[k];
+    }
   }
 }
-template <int R>
-__device__ __forceinline__ void residual_rows(const Epilogue& e, int64_t row, int step, int n, int64_t col, uint16_t (&res)[R]) {
+template <int R, int W>
+__device__ __forceinline__ void residual_rows(const Epilogue& e, int64_t row, int step, int n, int64_t col,
+                                              uint32_t (&res)[R]) {
   const uint16_t* p = e.residual + row * e.ldr + col;
 #pragma unroll
-  for (int k = 0; k < R; ++k) res[k] = e.residual && k * step < n ? p[k * step * e.ldr] : 0;
+  for (int k = 0; k < R; ++k) {
+    res[k] = 0u;
+    if (e.residual && k * step < n)
+      res[k] = W == 2 ? *reinterpret_cast<const uint32_t*>(p + k * step * e.ldr) : p[k * step * e.ldr];
+  }
+}
+// The epilogue warp's 32 x 32 piece in `st`, W columns a lane (32 / W lanes share a
+// row): consecutive lanes share lines whatever the rows' alignment.
+template <int W>
+__device__ __forceinline__ void finish_piece(const Epilogue& e, const float* st, int64_t row0, int rows, int64_t col0,
+                                             int64_t N) {
+  constexpr int R = 8;
+  const int lane = threadIdx.x & 31, c = lane % (32 / W) * W, sub = lane / (32 / W);
+  if (col0 + c >= N) return;
+  float bias[W];
+#pragma unroll
+  for (int k = 0; k < W; ++k) bias[k] = e.bias ? bias_at(e, col0 + c + k) : 0.f;
+  uint32_t next[R], res[R];   // the residual of the next rows is on its way
+  residual_rows<R, W>(e, row0 + sub, W, rows - sub, col0 + c, next);
+#pragma unroll 1
+  for (int r0 = sub; r0 < rows; r0 += R * W) {
+    float o[R * W];
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      res[k] = next[k];
+      const int r = r0 + k * W;
+      const float* q = st + r * 32 + (((c >> 2) ^ (r & 7)) << 2) + (c & 3);
+#pragma unroll
+      for (int u = 0; u < W; ++u) o[k * W + u] = q[u];
+    }
+    residual_rows<R, W>(e, row0 + r0 + R * W, W, rows - r0 - R * W, col0 + c, next);
+    finish_rows<R, W>(e, row0 + r0, W, rows - r0, col0 + c, o, bias, res);
+  }
 }
 
 // Tile t -> (row tile, column tile): groups of GROUP_M row tiles, row tiles
@@ -475,22 +511,10 @@ __global__ void __launch_bounds__(THREADS, SPLIT ? 2 : 1)
             float o[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
             if (row0 + r < p.M && n > 0) finish8(p.e, row0 + r, col, n, o, bias, res[it]);
           }
-        } else if (col0 + lane < p.N) {   // a column a lane: consecutive lanes share lines
-          const float b = p.e.bias ? bias_at(p.e, col0 + lane) : 0.f;
+        } else {
           const int rows = (int)(p.M - row0 < 32 ? p.M - row0 : 32);
-          uint16_t next[8], res8[8];   // the residual of the next rows is on its way
-          residual_rows(p.e, row0, 1, rows, col0 + lane, next);
-#pragma unroll 1
-          for (int r0 = 0; r0 < rows; r0 += 8) {
-            float o[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              res8[k] = next[k];
-              o[k] = st[(r0 + k) * 32 + (((lane >> 2) ^ k) << 2) + (lane & 3)];
-            }
-            residual_rows(p.e, row0 + r0 + 8, 1, rows - r0 - 8, col0 + lane, next);
-            finish_rows(p.e, row0 + r0, 1, rows - r0, col0 + lane, o, b, res8);
-          }
+          if (p.e.even) finish_piece<2>(p.e, st, row0, rows, col0, p.N);
+          else finish_piece<1>(p.e, st, row0, rows, col0, p.N);
         }
         __syncwarp();
       }
@@ -550,10 +574,10 @@ __global__ void __launch_bounds__(THREADS, SPLIT ? 2 : 1)
       const int c = (int)threadIdx.x & (width - 1), step = T / width;
       const int64_t col = col0 + c;
       if (threadIdx.x < T && col < p.N) {
-        const float bias = p.e.bias ? bias_at(p.e, col) : 0.f;
+        const float bias[1] = {p.e.bias ? bias_at(p.e, col) : 0.f};
         for (int r0 = (int)threadIdx.x / width; r0 < rows; r0 += step * R) {
-          uint16_t res[R];
-          residual_rows(p.e, row0 + r0, step, rows - r0, col, res);
+          uint32_t res[R];
+          residual_rows<R, 1>(p.e, row0 + r0, step, rows - r0, col, res);
           float v[R];
 #pragma unroll
           for (int k = 0; k < R; ++k) v[k] = 0.f;
@@ -568,7 +592,7 @@ __global__ void __launch_bounds__(THREADS, SPLIT ? 2 : 1)
           }
 #pragma unroll
           for (int k = 0; k < R; ++k) v[k] = dead ? NAN : v[k];
-          finish_rows(p.e, row0 + r0, step, rows - r0, col, v, bias, res);
+          finish_rows<R, 1>(p.e, row0 + r0, step, rows - r0, col, v, bias, res);
         }
       }
     }
@@ -651,9 +675,10 @@ __global__ void __launch_bounds__(GEMV_T) linear_gemv_kernel(const uint16_t* x, 
   if (part != 0 || f >= N || lane >= R) return;
   float v[1] = {0.f};
   for (int k = 0; k < wpf; ++k) v[0] = __fadd_rn(v[0], s_part[warp + k][lane]);
-  uint16_t res[1];
-  residual_rows(e, lane, 1, 1, f, res);
-  finish_rows(e, lane, 1, 1, f, v, e.bias ? bias_at(e, f) : 0.f, res);
+  uint32_t res[1];
+  residual_rows<1, 1>(e, lane, 1, 1, f, res);
+  const float bias[1] = {e.bias ? bias_at(e, f) : 0.f};
+  finish_rows<1, 1>(e, lane, 1, 1, f, v, bias, res);
 }
 
 // ------------------------------------------------------------ around the products
@@ -842,11 +867,13 @@ cudaError_t set_smem() {
   return e;
 }
 
-// CTAs that share a tile's K when there are `tiles` tiles of 128 x 128: 4 or 2
-// where all fit on the SMs at once (two an SM) and each keeps at least four stages of K.
+// CTAs that share a tile's K when there are `tiles` tiles of 128 x 128: 2 or 4
+// while all have an SM and at least four stages of K each, or half an SM and at
+// least eight.  Measured (us): 64 tiles of K 1000, by 2 13.7, by 4 18.0; 128 tiles
+// of K 4096, whole 35.3, by 2 26.3.
 int split_for(int tiles, int k_steps) {
   int s = 1;
-  while (s < MAX_SPLIT && tiles * 2 * s <= 2 * sm_count() && k_steps >= 8 * s) s *= 2;
+  while (s < MAX_SPLIT && k_steps >= 8 * s && tiles * 2 * s <= (k_steps >= 16 * s ? 2 : 1) * sm_count()) s *= 2;
   return s;
 }
 
@@ -888,6 +915,9 @@ cudaError_t gemm(const Operand& a, const Operand& b, int64_t M, int64_t N, int64
   p.e = epi;
   p.e.vec = rows16(epi.y, epi.y_dtype, epi.ldy) && (!epi.z || rows16(epi.z, 0, epi.ldz)) &&
             (!epi.residual || rows16(epi.residual, 0, epi.ldr));
+  auto rows4 = [](const void* q, int64_t ld) { return reinterpret_cast<uintptr_t>(q) % 4 == 0 && ld % 2 == 0; };
+  p.e.even = N % 2 == 0 && (epi.y_dtype != 0 || rows4(epi.y, epi.ldy)) && (!epi.z || rows4(epi.z, epi.ldz)) &&
+             (!epi.residual || rows4(epi.residual, epi.ldr));
   const int64_t small = ((M + 127) / 128) * ((N + 127) / 128);
   if (small > (1 << 30)) return cudaErrorInvalidValue;
   // Tiles of 128 x 128, K split over a cluster while SMs are left, when there is
