@@ -9,6 +9,7 @@ tensors are not on a CUDA device, the call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -928,23 +929,26 @@ class Checkpoint:
         for t, cols in ((codes, H), (scales, blocks)):
             if t.dim() != 2 or t.shape[0] != T or t.shape[1] < cols or not t.is_contiguous():
                 raise ValueError("codes and scales must be contiguous [T, >= H] and [T, >= ceil(H / 32)]")
-        self.codes, self.scales, self.T, self.H = codes, scales, T, H
+        self._set(codes, scales, T, H, codes.shape[1], scales.shape[1])
 
-    @property
-    def shape(self):
-        return (self.T, self.H)
+    def _set(self, codes, scales, T, H, ld_codes, ld_scales):
+        self.codes, self.scales, self.shape = codes, scales, (T, H)
+        # the rlk_checkpoint that the entry points read during a call
+        self._struct = CheckpointBuffers(codes.data_ptr(), scales.data_ptr(), ld_codes, ld_scales)
+        return self
 
     def buffers(self):
-        return CheckpointBuffers(self.codes.data_ptr(), self.scales.data_ptr(),
-                                 self.codes.shape[1], self.scales.shape[1])
+        return ctypes.byref(self._struct)
 
 
 def new_checkpoint(T: int, H: int, device) -> Checkpoint:
-    """Room for the 8-bit checkpoint of an activation [T, H]."""
-    pad = lambda n: -(-n // 16) * 16
-    return Checkpoint(torch.empty((T, pad(H)), dtype=torch.int8, device=device),
-                      torch.empty((T, pad(-(-H // CHECKPOINT_BLOCK))), dtype=torch.uint8, device=device),
-                      T, H)
+    """Room for the 8-bit checkpoint of an activation [T, H] on a CUDA device."""
+    if torch.device(device).type != "cuda":
+        raise ValueError("librlk operates on CUDA tensors only")
+    ld_codes, ld_scales = (H + 15) // 16 * 16, (H + 511) // 512 * 16
+    return Checkpoint.__new__(Checkpoint)._set(
+        torch.empty((T, ld_codes), dtype=torch.int8, device=device),
+        torch.empty((T, ld_scales), dtype=torch.uint8, device=device), T, H, ld_codes, ld_scales)
 
 
 def checkpoint_pack(x: torch.Tensor, *, out: Checkpoint | None = None, status_word=None) -> Checkpoint:
@@ -957,9 +961,8 @@ def checkpoint_pack(x: torch.Tensor, *, out: Checkpoint | None = None, status_wo
         out = new_checkpoint(T, H, x.device)
     if out.shape != (T, H):
         raise ValueError("out must be a checkpoint of x's shape")
-    b = out.buffers()
     _check("rlk_checkpoint_pack",
-           lib.rlk_checkpoint_pack(_ptr(x), dt, T, H, ld, ctypes.byref(b), _ptr(status_word),
+           lib.rlk_checkpoint_pack(x.data_ptr(), dt, T, H, ld, out.buffers(), _ptr(status_word),
                                    _stream(x.device)))
     return out
 
@@ -972,9 +975,8 @@ def checkpoint_unpack(checkpoint: Checkpoint, *, dtype=torch.bfloat16, out=None)
         out = torch.empty((T, H), dtype=dtype, device=checkpoint.codes.device)
     _need_cuda(out)
     dt, ld = _matrix(out, "out", (T, H))
-    b = checkpoint.buffers()
     _check("rlk_checkpoint_unpack",
-           lib.rlk_checkpoint_unpack(ctypes.byref(b), T, H, _ptr(out), dt, ld, _stream(out.device)))
+           lib.rlk_checkpoint_unpack(checkpoint.buffers(), T, H, out.data_ptr(), dt, ld, _stream(out.device)))
     return out
 
 
@@ -999,7 +1001,7 @@ def norm(x: torch.Tensor, weight=None, bias=None, *, kind: int = NORM_LAYER, eps
     if checkpoint is not None:
         if checkpoint.shape != (T, H):
             raise ValueError("checkpoint must be of x's shape")
-        ck = ctypes.byref(checkpoint.buffers())
+        ck = checkpoint.buffers()
     mean = None if kind == NORM_RMS else torch.empty(T, dtype=torch.float32, device=dev)
     rstd = torch.empty(T, dtype=torch.float32, device=dev)
     code = lib.rlk_norm_fwd(x.data_ptr(), dt, T, H, ld, _ptr(weight), _ptr(bias), pdt, kind, eps,
@@ -1046,7 +1048,7 @@ def norm_backward(dy: torch.Tensor, x, weight, mean, rstd, *, kind: int = NORM_L
     if workspace is None and (grad_weight is not None or grad_bias is not None):
         workspace = torch.empty(max(lib.rlk_workspace_size(OP_NORM_BWD, T, H, 0), 16), dtype=torch.uint8,
                                 device=dev)
-    ck = None if kept is None else ctypes.byref(kept.buffers())
+    ck = None if kept is None else kept.buffers()
     code = lib.rlk_norm_bwd(dy.data_ptr(), gdt, ldg, None if kept else x.data_ptr(), dt, ld, ck, T, H,
                             _ptr(weight), pdt, kind, _ptr(mean), rstd.data_ptr(), out.data_ptr(), odt,
                             ldo, _ptr(grad_weight), _ptr(grad_bias), int(bool(accumulate)),
@@ -1164,7 +1166,7 @@ def linear_backward(dy: torch.Tensor, x, weight: torch.Tensor, preact=None, *,
     if workspace is None:
         workspace = torch.empty(int(lib.rlk_workspace_size(OP_LINEAR_BWD, M, N, K)), device=dev,
                                 dtype=torch.uint8)
-    ck = None if kept is None else ctypes.byref(kept.buffers())
+    ck = None if kept is None else kept.buffers()
     _check("rlk_linear_bwd",
            lib.rlk_linear_bwd(_ptr(dy), lddy, None if kept else _ptr(x), ldx, ck, _ptr(weight), ldw,
                               _ptr(preact), ldz, M, N, K, int(activation), _ptr(dx), xdt, K,
@@ -1207,6 +1209,12 @@ def linear_autograd(x: torch.Tensor, weight: torch.Tensor, bias=None, residual=N
 
 
 # ------------------------------------------------------------ preference loss
+@functools.lru_cache(maxsize=64)
+def _pref_config(*fields):
+    """A reference to an rlk_pref_config of these fields (the entry point only reads it)."""
+    return ctypes.byref(PrefConfig(*fields))
+
+
 def preference_loss(logp, logp_ref, seq_offsets, *, loss_mask=None, loss_type: int = PREF_SIGMOID,
                     beta: float = 0.1, label_smoothing: float = 0.0, margin: float = 0.0,
                     length_normalise: bool = False, want_grad: bool = True,
@@ -1230,13 +1238,13 @@ def preference_loss(logp, logp_ref, seq_offsets, *, loss_mask=None, loss_type: i
     if workspace is None:
         workspace = torch.empty(lib.rlk_workspace_size(OP_PREFERENCE_LOSS, n_tok, P, 0),
                                 dtype=torch.uint8, device=dev)
-    cfg = PrefConfig(loss_type, beta, label_smoothing, margin, int(bool(length_normalise)))
+    cfg = _pref_config(loss_type, beta, label_smoothing, margin, bool(length_normalise))
     loss = torch.empty(1, dtype=torch.float32, device=dev)
     grad = torch.empty_like(logp) if want_grad else None
     reward = torch.empty(2 * P, dtype=torch.float32, device=dev) if want_reward else None
     stats = torch.empty(PREF_NSTATS, dtype=torch.float32, device=dev) if want_stats else None
     code = lib.rlk_preference_loss(logp.data_ptr(), _ptr(logp_ref), _ptr(loss_mask), seq_offsets.data_ptr(),
-                                   P, n_tok, ctypes.byref(cfg), loss.data_ptr(), _ptr(grad), _ptr(reward),
+                                   P, n_tok, cfg, loss.data_ptr(), _ptr(grad), _ptr(reward),
                                    _ptr(stats), workspace.data_ptr(), workspace.numel(),
                                    _stream(dev))
     _check("rlk_preference_loss", code)
