@@ -262,13 +262,20 @@ __global__ void __launch_bounds__(PT) pref_grad_kernel(PrefArgs a) {
   }
   for (int64_t b = t0 + j0 * kGradToks; b < t1; b += (int64_t)a.split * kGradToks) {
     const int left = (int)(t1 - b < kGradToks ? t1 - b : kGradToks);
-    bool on[kGradToks / PT];
+    // four tokens a thread at a time: their mask bytes are on their way together
+    for (int k0 = 0; k0 < left; k0 += 4 * PT) {
+      uint32_t on[4];
 #pragma unroll
-    for (int k = 0; k < kGradToks / PT; ++k)
-      on[k] = k * PT + tid < left && (!a.mask || a.mask[b + k * PT + tid]);
+      for (int k = 0; k < 4; ++k) {
+        const int t = k0 + k * PT + tid;
+        on[k] = (t < left) & (a.mask != nullptr) ? a.mask[b + t] : 1u;
+      }
 #pragma unroll
-    for (int k = 0; k < kGradToks / PT; ++k)
-      if (k * PT + tid < left) a.out_grad[b + k * PT + tid] = on[k] ? g : 0.f;
+      for (int k = 0; k < 4; ++k) {
+        const int t = k0 + k * PT + tid;
+        if (t < left) a.out_grad[b + t] = on[k] ? g : 0.f;
+      }
+    }
   }
   // tokens before the first sequence and after the last
   if (j0 == 0 && s == 0)
