@@ -213,6 +213,7 @@ struct NormArgs {
   float* rstd;          // [T] or NULL
   CheckpointView ck;    // codes NULL: none
   uint32_t* status;
+  long long wait_limit = 0, withhold = -1;   // set by the launcher
 };
 struct NormBwdArgs {
   const void* dy;
@@ -235,6 +236,7 @@ struct NormBwdArgs {
   float* db;            // [H] or NULL
   int accumulate;
   float* workspace;     // [parts][2][H] partial parameter gradients
+  long long wait_limit = 0, withhold = -1;   // set by the launcher
 };
 size_t norm_bwd_workspace_bytes(int64_t T, int64_t H);
 cudaError_t launch_norm_fwd(const NormArgs& a, cudaStream_t stream);

@@ -86,6 +86,7 @@ struct GemmParams {
   int first_tile, n_tiles;   // tiles [first_tile, n_tiles) of the n_mt x n_nt
   int stages;
   long long wait_limit;
+  int withhold;              // debug: the stage of the first CTA whose barrier waits for an arrival that never comes (-1: none)
   Epilogue e;
 };
 
@@ -316,7 +317,7 @@ __global__ void __launch_bounds__(THREADS, SPLIT ? 2 : 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
-      mbar_init(full0 + 8 * s, 1);
+      mbar_init(full0 + 8 * s, 1 + (s == p.withhold && blockIdx.x == 0));
       mbar_init(empty0 + 8 * s, 1);
     }
     for (int a = 0; a < 2; ++a) {
@@ -912,6 +913,7 @@ cudaError_t gemm(const Operand& a, const Operand& b, int64_t M, int64_t N, int64
   p.N = N;
   p.k_steps = (int)((K + BK - 1) / BK);
   p.wait_limit = debug_wait_limit();
+  p.withhold = (int)debug_take_withheld();
   p.e = epi;
   p.e.vec = rows16(epi.y, epi.y_dtype, epi.ldy) && (!epi.z || rows16(epi.z, 0, epi.ldz)) &&
             (!epi.residual || rows16(epi.residual, 0, epi.ldr));

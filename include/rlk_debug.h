@@ -37,10 +37,10 @@ int rlk_debug_inject_launch_failures(int n);
 
 /*
  * rlk_debug_set_wait_limit -- the number of clock cycles any bounded device
- * wait of the logprob/entropy scorer and the LM-head kernel may take before
- * it gives up (default 2^31, about a second).  A wait that runs out sets
- * RLK_STATUS_TIMEOUT in the call's status word, the rows the kernel has not
- * finished get NaN outputs, copies already issued are allowed to land, and
+ * wait of the logprob/entropy scorer, the LM-head kernel, the norms and the
+ * linear layer's products may take before it gives up (default 2^31, about a
+ * second).  A wait that runs out sets RLK_STATUS_TIMEOUT in the call's status
+ * word (if it has one), the rows the kernel has not finished get NaN outputs, copies already issued are allowed to land, and
  * the kernel returns, so the context stays usable.  cycles <= 0 restores the
  * default.  Returns the previous limit.  Not thread-safe with respect to
  * concurrent launches.
@@ -55,6 +55,12 @@ long long rlk_debug_set_wait_limit(long long cycles);
  * the limit set above), which exercises the expiry path; nothing is left in
  * flight.  stage < 0 clears it.  The setting is consumed by one launch.
  * Returns 0.
+ *
+ * Launches of rlk_norm_fwd / _bwd (rows of up to 16384 columns; places of the
+ * first CTA's first group of threads) and of the products of rlk_linear_fwd /
+ * _bwd (more than 4 rows; stages of the first CTA) consume it too.  There all
+ * copies are issued, but the barrier of the place with that index (0 to 3, and
+ * 0 to 5; larger ones change nothing) waits for one arrival more.
  */
 int rlk_debug_withhold_copy(long long stage);
 
