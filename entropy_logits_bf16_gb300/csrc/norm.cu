@@ -174,24 +174,11 @@ template <int VW, int E>
 constexpr bool sums_in_smem() { return VW == 1 || E == 32; }
 constexpr int64_t kOnChip = 32 * kMaxGroup;
 
-// Element e of a thread's E columns is column ((e / VW) n + t) VW + e % VW: VW
-// columns at a time, consecutive threads on consecutive ones.  They are held
-// as pairs, so that most of the arithmetic goes two elements an instruction
-// (these kernels would otherwise be bound by issue).  FULL: the threads'
-// columns are exactly the row's (VW = 8), and nothing needs a bounds check; or
-// all but a thread's last TAIL columns are surely inside the row (VW = 1).
-constexpr int TAIL = 4;
-template <int VW, int E, bool FULL>
-__device__ __forceinline__ constexpr bool surely(int e) {
-  return FULL && (VW == 8 || e < E - TAIL);
-}
-
-// The same number, but computed anew by the compiler: column offsets that
-// depend on it are not kept in registers over all rows.
-__device__ __forceinline__ int fresh(int n) {
-  asm volatile("" : "+r"(n));
-  return n;
-}
+// The thread's E columns go VW at a time, consecutive threads on consecutive ones
+// (col_of).  They are held as pairs, so that most of the arithmetic goes two
+// elements an instruction (these kernels would otherwise be bound by issue).
+// FULL (VW = 8): the threads' columns are exactly the row's, and nothing needs a
+// bounds check.  VW = 1: that holds for every warp but the last (whole_warp).
 __device__ __forceinline__ uint32_t pack_bf16(float2 v) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -215,6 +202,18 @@ struct Group {
     else __syncwarp();
   }
 };
+
+// First of the k-th VW columns of the thread.  VW = 8: the group's threads side by
+// side.  VW = 1: a warp has 32 E columns of its own, so that a thread's lie at
+// distances known when this is compiled, and addresses take no arithmetic (with
+// the group side by side, at multiples of its size, 16 columns took a warp
+// some 700 instructions: 46 and 60 us forward and backward on 4099 rows of 5003).
+template <int VW, int E>
+__device__ __forceinline__ int col_of(int k, const Group& g) {
+  return VW == 8 ? (k * g.n + g.t) * 8 : (g.t >> 5) * (32 * E) + (g.t & 31) + 32 * k;
+}
+template <int E>
+__device__ __forceinline__ bool whole_warp(int H, const Group& g) { return ((g.t >> 5) + 1) * (32 * E) <= H; }
 
 // Sums of NV values over the group, in a fixed order, on every thread.  `buf`
 // alternates between two halves of s_red, so one barrier a sum is enough.
@@ -258,7 +257,7 @@ __device__ __forceinline__ void load_cols(const void* p, int dtype, int64_t at, 
   if (VW == 8) {
 #pragma unroll
     for (int k = 0; k < E / 8; ++k) {
-      const int c = (k * g.n + g.t) * 8;
+      const int c = col_of<8, E>(k, g);
       float2* o = v + k * 4;
       if (FULL || c + 8 <= H) {
         if (dtype) {
@@ -276,16 +275,30 @@ __device__ __forceinline__ void load_cols(const void* p, int dtype, int64_t at, 
       }
     }
   } else {
-    const int n = fresh(g.n), left = H - g.t;
+    const int c = col_of<1, E>(0, g), left = H - c;
     if (dtype) {
-      const float* q = static_cast<const float*>(p) + at + g.t;
+      const float* q = static_cast<const float*>(p) + at + c;
 #pragma unroll
-      for (int e = 0; e < E; ++e) elem<E>(v, e) = surely<VW, E, FULL>(e) || e * n < left ? q[e * n] : 0.f;
+      for (int e = 0; e < E; ++e) elem<E>(v, e) = 32 * e < left ? q[32 * e] : 0.f;
     } else {
-      const uint16_t* q = static_cast<const uint16_t*>(p) + at + g.t;
+      const uint16_t* q = static_cast<const uint16_t*>(p) + at + c;
 #pragma unroll
-      for (int e = 0; e < E; ++e) elem<E>(v, e) = surely<VW, E, FULL>(e) || e * n < left ? bf16_val(q[e * n]) : 0.f;
+      for (int e = 0; e < E; ++e) elem<E>(v, e) = 32 * e < left ? bf16_val(q[32 * e]) : 0.f;
     }
+  }
+}
+template <int E, bool ALL>
+__device__ __forceinline__ void store_single(void* p, int dtype, int64_t at, int left, float2 (&v)[E / 2]) {
+  if (dtype) {
+    float* q = static_cast<float*>(p) + at;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (ALL || 32 * e < left) q[32 * e] = elem<E>(v, e);
+  } else {
+    __nv_bfloat16* q = static_cast<__nv_bfloat16*>(p) + at;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (ALL || 32 * e < left) q[32 * e] = __float2bfloat16_rn(elem<E>(v, e));
   }
 }
 template <int VW, int E, bool FULL>
@@ -293,7 +306,7 @@ __device__ __forceinline__ void store_cols(void* p, int dtype, int64_t at, int H
   if (VW == 8) {
 #pragma unroll
     for (int k = 0; k < E / 8; ++k) {
-      const int c = (k * g.n + g.t) * 8;
+      const int c = col_of<8, E>(k, g);
       const float2* o = v + k * 4;
       if (FULL || c + 8 <= H) {
         if (dtype) {
@@ -311,18 +324,9 @@ __device__ __forceinline__ void store_cols(void* p, int dtype, int64_t at, int H
       }
     }
   } else {
-    const int n = fresh(g.n), left = H - g.t;
-    if (dtype) {
-      float* q = static_cast<float*>(p) + at + g.t;
-#pragma unroll
-      for (int e = 0; e < E; ++e)
-        if (surely<VW, E, FULL>(e) || e * n < left) q[e * n] = elem<E>(v, e);
-    } else {
-      __nv_bfloat16* q = static_cast<__nv_bfloat16*>(p) + at + g.t;
-#pragma unroll
-      for (int e = 0; e < E; ++e)
-        if (surely<VW, E, FULL>(e) || e * n < left) q[e * n] = __float2bfloat16_rn(elem<E>(v, e));
-    }
+    const int c = col_of<1, E>(0, g);
+    if (whole_warp<E>(H, g)) store_single<E, true>(p, dtype, at + c, 0, v);
+    else store_single<E, false>(p, dtype, at + c, H - c, v);
   }
 }
 
@@ -352,8 +356,8 @@ __device__ __forceinline__ void write_checkpoint(const CheckpointView& ck, int64
       amax = __reduce_max_sync(0xFFFFFFFFu, amax);
     }
     const uint32_t byte = ck_scale_byte(amax);
-    const int c = (k * g.n + g.t) * VW;
-    if (!live || (!surely<VW, E, FULL>(k * VW) && c >= H)) continue;
+    const int c = col_of<VW, E>(k, g);
+    if (!live || (!FULL && c >= H)) continue;
     if constexpr (VW == 8) {
       uint2 q;
       if (byte < kCkTop) {
@@ -473,6 +477,7 @@ __device__ __forceinline__ Body body_of(const void* p, int64_t at, int H) {
 template <int TYPE>
 __device__ __forceinline__ uint32_t load_edge(const void* p, int64_t at, int H, const Group& g) {
   constexpr int es = bytes_of(TYPE);
+  if (g.t >= 16) return 0u;
   const char* src = static_cast<const char*>(p) + at * es;
   const int e = edge_byte<TYPE>(to_boundary(src), H * es, g.t);
   if (e < 0) return 0u;
@@ -483,7 +488,7 @@ __device__ __forceinline__ uint32_t load_edge(const void* p, int64_t at, int H, 
 template <int TYPE>
 __device__ __forceinline__ void store_edge(uint8_t* place, const void* p, int64_t at, int H, const Group& g, uint32_t v) {
   constexpr int es = bytes_of(TYPE);
-  if (TYPE == kFromCk) return;   // the codes past a row meet a dy of 0
+  if (TYPE == kFromCk || g.t >= 32) return;   // the codes past a row meet a dy of 0
   const char* src = static_cast<const char*>(p) + at * es;
   const int z = H * es + (g.t - 16) * es;
   if (g.t >= 16 && (g.t - 16) * es < 16) {
@@ -507,7 +512,7 @@ __device__ __forceinline__ void take_row(const uint8_t* place, const void* p, in
   if constexpr (VW == 8) {
 #pragma unroll
     for (int k = 0; k < E / 8; ++k) {
-      const int c = (k * g.n + g.t) * 8;
+      const int c = col_of<8, E>(k, g);
       const uint8_t* s = place + c * es;
       float2* o = v + 4 * k;
       if (TYPE == 1) {
@@ -531,11 +536,10 @@ __device__ __forceinline__ void take_row(const uint8_t* place, const void* p, in
       }
     }
   } else {
-    const uint8_t* s = place + ((reinterpret_cast<uintptr_t>(p) + at * es) & 15u) + g.t * es;
-    const int n = fresh(g.n);
+    const uint8_t* s = place + ((reinterpret_cast<uintptr_t>(p) + at * es) & 15u) + col_of<1, E>(0, g) * es;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const uint8_t* q = s + e * n * es;
+      const uint8_t* q = s + 32 * e * es;
       float f;
       if (TYPE == 1) f = *reinterpret_cast<const float*>(q);
       else if (TYPE == 0) f = bf16_val(*reinterpret_cast<const uint16_t*>(q));
@@ -644,18 +648,16 @@ __global__ void __maxnreg__((regs_of<VW, E>())) norm_fwd_kernel(NormArgs a, int 
 #pragma unroll
     for (int q = 0; q < R; ++q) {
       float2 s = both(0.f);
-      if ((FULL && VW == 8) || a.rms) {   // with m = 0 the zeros past the end add nothing
+      if (VW == 8 ? FULL || a.rms : a.rms || whole_warp<E>(H, g)) {   // with m = 0 the zeros past the end add nothing
 #pragma unroll
         for (int j = 0; j < E / 2; ++j) {
           const float2 d = add2(x[q][j], both(-m[q]));
           s = fma2(d, d, s);
         }
       } else {
-        const int n2 = fresh(n);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          const int c = ((e / VW) * n2 + g.t) * VW + e % VW;
-          const float d = surely<VW, E, FULL>(e) || c < H ? __fsub_rn(elem<E>(x[q], e), m[q]) : 0.f;
+          const float d = col_of<VW, E>(e / VW, g) + e % VW < H ? __fsub_rn(elem<E>(x[q], e), m[q]) : 0.f;
           if (e % 2) s.y = __fmaf_rn(d, d, s.y);
           else s.x = __fmaf_rn(d, d, s.x);
         }
@@ -770,11 +772,10 @@ __global__ void __maxnreg__((regs_of<VW, E>())) norm_bwd_kernel(NormBwdArgs a, i
     r1 = in ? a.rstd[row] : 0.f;
     if (XT == kFromCk) {
       const uint8_t* sc = a.ck.scales + row * a.ck.lds;
-      const int n2 = VW == 8 ? g.n : fresh(g.n);
 #pragma unroll
       for (int k = 0; k < STEPS; ++k) {
-        const int c = (k * n2 + g.t) * VW;
-        byte1[k] = in && (surely<VW, E, FULL>(k * VW) || c < H) ? sc[c / kCkBlock] : 1u;
+        const int c = col_of<VW, E>(k, g);
+        byte1[k] = in && (FULL || c < H) ? sc[c / kCkBlock] : 1u;
       }
     }
   };
@@ -823,11 +824,10 @@ __global__ void __maxnreg__((regs_of<VW, E>())) norm_bwd_kernel(NormBwdArgs a, i
     } else if (live) {
       load_cols<VW, E, FULL>(a.dy, DT, row * a.lddy, H, g, dy);
       if (XT == kFromCk) {
-        const int n2 = fresh(n);
         const int8_t* q = a.ck.codes + row * a.ck.ldc;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          const int c = ((e / VW) * n2 + g.t) * VW + e % VW;
+          const int c = col_of<VW, E>(e / VW, g) + e % VW;
           elem<E>(h, e) = c < H ? __fmul_rn((float)q[c], step[VW == 8 ? e / 8 : e]) : 0.f;
         }
       } else {
@@ -979,20 +979,15 @@ cudaError_t fwd(const NormArgs& a, cudaStream_t stream) {
   const cudaError_t e = launch_after(kernel, dim3((unsigned)(want < cap ? want : cap)), dim3(block), depth * row, stream, a, n, depth);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
-// FULL of the kernels.
-bool full_row(int64_t H, bool vec) {
-  const int64_t n = group_for(H, vec), e = cols_for(H);
-  return vec ? n * e == H : n * (e - TAIL) <= H;
-}
+// FULL of the kernels for VW = 8.
+bool full_row(int64_t H) { return group_for(H, true) * cols_for(H) == H; }
 
 template <int XT>
 cudaError_t fwd_for(const NormArgs& a, bool vec, cudaStream_t stream) {
-  if (full_row(a.H, vec)) {
-    if (cols_for(a.H) == 32) return vec ? fwd<XT, 8, 32, true>(a, stream) : fwd<XT, 1, 32, true>(a, stream);
-    return vec ? fwd<XT, 8, 16, true>(a, stream) : fwd<XT, 1, 16, true>(a, stream);
-  }
-  if (cols_for(a.H) == 32) return vec ? fwd<XT, 8, 32>(a, stream) : fwd<XT, 1, 32>(a, stream);
-  return vec ? fwd<XT, 8, 16>(a, stream) : fwd<XT, 1, 16>(a, stream);
+  const bool wide = cols_for(a.H) == 32;
+  if (!vec) return wide ? fwd<XT, 1, 32>(a, stream) : fwd<XT, 1, 16>(a, stream);
+  if (full_row(a.H)) return wide ? fwd<XT, 8, 32, true>(a, stream) : fwd<XT, 8, 16, true>(a, stream);
+  return wide ? fwd<XT, 8, 32>(a, stream) : fwd<XT, 8, 16>(a, stream);
 }
 
 template <int XT, int DT, int VW, int E, bool FULL = false>
@@ -1015,12 +1010,10 @@ cudaError_t bwd(const NormBwdArgs& a, int& parts, cudaStream_t stream) {
 }
 template <int XT, int DT>
 cudaError_t bwd_for(const NormBwdArgs& a, bool vec, int& parts, cudaStream_t stream) {
-  if (full_row(a.H, vec)) {
-    if (cols_for(a.H) == 32) return vec ? bwd<XT, DT, 8, 32, true>(a, parts, stream) : bwd<XT, DT, 1, 32, true>(a, parts, stream);
-    return vec ? bwd<XT, DT, 8, 16, true>(a, parts, stream) : bwd<XT, DT, 1, 16, true>(a, parts, stream);
-  }
-  if (cols_for(a.H) == 32) return vec ? bwd<XT, DT, 8, 32>(a, parts, stream) : bwd<XT, DT, 1, 32>(a, parts, stream);
-  return vec ? bwd<XT, DT, 8, 16>(a, parts, stream) : bwd<XT, DT, 1, 16>(a, parts, stream);
+  const bool wide = cols_for(a.H) == 32;
+  if (!vec) return wide ? bwd<XT, DT, 1, 32>(a, parts, stream) : bwd<XT, DT, 1, 16>(a, parts, stream);
+  if (full_row(a.H)) return wide ? bwd<XT, DT, 8, 32, true>(a, parts, stream) : bwd<XT, DT, 8, 16, true>(a, parts, stream);
+  return wide ? bwd<XT, DT, 8, 32>(a, parts, stream) : bwd<XT, DT, 8, 16>(a, parts, stream);
 }
 
 }  // namespace
