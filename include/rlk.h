@@ -1,6 +1,7 @@
 /*
  * rlk.h -- C ABI of librlk: top-p log-probability / entropy of sampled tokens,
- * the GRPO/DAPO loss epilogue, and a fused LM-head variant, for one GB300 GPU.
+ * the GRPO/DAPO loss epilogue, a fused LM-head variant, and the layers and the
+ * preference loss on either side of it, for one GB300 GPU.
  *
  * Conventions shared by every entry point
  *  - All pointers are DEVICE pointers unless stated otherwise; scalars are
@@ -13,7 +14,8 @@
  *    logit) do not abort: the affected row's outputs become NaN and a bit is
  *    OR-ed into *out_status_word (when given); the caller reads it back.
  *  - Results are deterministic: bitwise identical across runs and independent
- *    of how rows are batched (row count, row order, position in the batch).
+ *    of how rows are batched (row count, row order, position in the batch),
+ *    but for what rlk_linear_fwd and the sums over rows say below.
  *
  * The pages this implements give semantics, not formulas:
  *  - RL-Kernel "Qwen3-8B VIME train-rollout consistency", section "ROCm MI300X
@@ -886,9 +888,12 @@ typedef enum { RLK_NORM_LAYER = 0, RLK_NORM_RMS = 1 } rlk_norm_kind;
  *  out_checkpoint  host pointer to the checkpoint's buffers, or NULL for none.
  *  out_status_word device uint32[1] or NULL.  A row with a NaN or an infinity,
  *                  or whose squares overflow fp32, gets NaN in y, mean and rstd
- *                  and RLK_STATUS_NONFINITE.
+ *                  and RLK_STATUS_NONFINITE.  A row whose copy to the chip did
+ *                  not come within the limit of its wait (about a second) gets
+ *                  the same, and RLK_STATUS_TIMEOUT.
  * A row's results do not depend on the other rows; a layout in which some row
- * does not start on a 16-byte boundary may sum a row in another order.
+ * does not start on a 16-byte boundary (or an H that is no multiple of 8) may
+ * sum a row in another order.
  * Errors: RLK_ERR_INVALID_ARG for T < 0, H outside its range, a stride below
  *  H, bad dtypes or kind, eps not finite and >= 0, null or misaligned pointers,
  *  a checkpoint outside its rules.  T == 0 returns RLK_OK without launching.
@@ -924,7 +929,8 @@ rlk_status rlk_norm_fwd(const void* x, rlk_dtype dtype, int64_t T, int64_t H, in
  *                  16-byte aligned (may be NULL when grad_weight and grad_bias
  *                  are); contents on entry do not matter.
  * A row whose rstd is NaN (the forward could not normalise it) gives NaN in its
- * grad_x row and in grad_weight.
+ * grad_x row and in grad_weight; a row that did not come within the limit of
+ * its wait gives NaN in all three.
  * Errors: as rlk_norm_fwd; RLK_ERR_WORKSPACE for a missing or short workspace.
  */
 rlk_status rlk_norm_bwd(const void* dy, rlk_dtype dy_dtype, int64_t lddy, const void* x,
@@ -966,7 +972,8 @@ typedef enum {
  *                  aligned, contents on entry do not matter; else it may be NULL.
  * Deterministic.  Calls of few rows split K over several CTAs, so a row's last
  * bits may differ between calls of a different M (never between runs).
- * NaN and infinities propagate as in the formula.
+ * NaN and infinities propagate as in the formula.  Tiles of y and z whose
+ * operands did not come within the limit of a wait (about a second) are NaN.
  * Errors: RLK_ERR_INVALID_ARG for sizes or strides outside the rules, bad
  *  dtypes or activation, null or misaligned pointers; RLK_ERR_WORKSPACE.
  *  M == 0 returns RLK_OK without launching.
@@ -1000,6 +1007,7 @@ rlk_status rlk_linear_fwd(const void* x, int64_t ldx, const void* w, int64_t ldw
  *                  16-byte aligned; contents on entry do not matter.
  * Deterministic for given sizes.  A call that needs less than the size above
  * (bf16 operands with 16-byte rows and no activation need no copies) accepts less.
+ * Tiles of grad_x and grad_w whose operands did not come in time are NaN.
  * Errors: as rlk_linear_fwd; RLK_ERR_UNSUPPORTED for accumulate with a bf16
  *  grad_w.  M == 0 zeroes grad_w and grad_bias (or leaves them, accumulating).
  */
