@@ -609,13 +609,45 @@ __global__ void __launch_bounds__(THREADS, SPLIT ? 2 : 1)
 // ------------------------------------------------------------ a few rows
 // Up to GEMV_ROWS rows: the weight's bytes bound the call and a tile of 128
 // rows would be almost empty, so each output feature is a dot product of its
-// own.  `wpf` warps share a feature (each takes every wpf-th piece of K), as
-// many as it takes to give every SM 32 warps; 16-byte loads, 8 in flight a lane.  Their
-// sums are joined in a fixed order.
+// own.  `wpf` warps share a feature (each takes a run of K), as
+// many as it takes to give every SM 32 warps.  Their sums are joined in a fixed order.
+// A load takes W columns: 8 where the rows of x and w start on 16-byte boundaries,
+// 2 where they do on 4-byte ones, else 1; up to 16 of them are in flight a lane, at
+// distances known when this is compiled (computed ones, and bounds tested at each load:
+// 9.1 us for one row of 4096 x 4096, now 7.6; 75 us for 4 rows of 2560 x 7490, now 23).
 constexpr int GEMV_ROWS = 4, GEMV_T = 256;
 
-template <int R, bool VEC>
-__global__ void __launch_bounds__(GEMV_T) linear_gemv_kernel(const uint16_t* x, int64_t ldx, const uint16_t* w,
+// W bf16 columns as they lie in memory, and as floats.
+template <int W>
+struct Cols;
+template <>
+struct Cols<8> {
+  using type = uint4;
+  static __device__ __forceinline__ void floats(uint4 q, float (&v)[8]) {
+    const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = bf16_lo(u[j]);
+      v[2 * j + 1] = bf16_hi(u[j]);
+    }
+  }
+};
+template <>
+struct Cols<2> {
+  using type = uint32_t;
+  static __device__ __forceinline__ void floats(uint32_t q, float (&v)[2]) {
+    v[0] = bf16_lo(q);
+    v[1] = bf16_hi(q);
+  }
+};
+template <>
+struct Cols<1> {
+  using type = uint16_t;
+  static __device__ __forceinline__ void floats(uint16_t q, float (&v)[1]) { v[0] = bf16_val(q); }
+};
+
+template <int R, int W>
+__global__ void __launch_bounds__(GEMV_T, 4) linear_gemv_kernel(const uint16_t* x, int64_t ldx, const uint16_t* w,
                                                              int64_t ldw, int64_t N, int K, int wpf, Epilogue e) {
   pdl_wait();
   __shared__ float s_part[GEMV_T / 32][R];
@@ -626,44 +658,54 @@ __global__ void __launch_bounds__(GEMV_T) linear_gemv_kernel(const uint16_t* x, 
   for (int m = 0; m < R; ++m) acc[m] = 0.f;
   if (f < N) {
     const uint16_t* wf = w + f * ldw;
-    if (VEC) {
-      constexpr int U = R == 1 ? 8 : 4;
-      for (int k0 = (part * 32 + lane) * 8; k0 < K; k0 += wpf * 256 * U) {
-        uint4 a[U];
+    using T = typename Cols<W>::type;
+    constexpr int U = W == 8 ? (R == 1 ? 8 : 4) : 16, STEP = 32 * W;
+    const int share = (K + wpf * STEP - 1) / (wpf * STEP) * STEP, k1 = K / W * W;   // a warp's columns: whole loads
+    const int end = min(k1, (part + 1) * share);
+    constexpr int B = W == 8 ? 1 : 8;   // loads of a row of x together
+    auto add = [&](const T* a, const uint16_t* xk) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int k = k0 + u * wpf * 256;
-          a[u] = k + 8 <= K ? __ldcs(reinterpret_cast<const uint4*>(wf + k)) : make_uint4(0u, 0u, 0u, 0u);
-        }
+      for (int m = 0; m < R; ++m) {
+        T b[B];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int k = k0 + u * wpf * 256;
-          if (k + 8 > K) continue;
-          const uint32_t aw[4] = {a[u].x, a[u].y, a[u].z, a[u].w};
+        for (int u = 0; u < B; ++u) b[u] = *reinterpret_cast<const T*>(xk + m * ldx + u * STEP);
 #pragma unroll
-          for (int m = 0; m < R; ++m) {
-            const uint4 b = *reinterpret_cast<const uint4*>(x + m * ldx + k);
-            const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
+        for (int u = 0; u < B; ++u) {
+          float av[W], bv[W];
+          Cols<W>::floats(a[u], av);
+          Cols<W>::floats(b[u], bv);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              acc[m] = __fmaf_rn(bf16_lo(aw[j]), bf16_lo(bw[j]), acc[m]);
-              acc[m] = __fmaf_rn(bf16_hi(aw[j]), bf16_hi(bw[j]), acc[m]);
-            }
-          }
+          for (int j = 0; j < W; ++j) acc[m] = __fmaf_rn(av[j], bv[j], acc[m]);
         }
       }
-      const int k = (K & ~7) + lane;   // the last K % 8 columns
-      if (part == 0 && k < K) {
+    };
+    int k0 = part * share + lane * W;
+    for (; k0 - lane * W + STEP * U <= end; k0 += STEP * U) {   // U loads of every lane's, at fixed distances
+      T a[U];
 #pragma unroll
-        for (int m = 0; m < R; ++m) acc[m] = __fmaf_rn(bf16_val(wf[k]), bf16_val(x[m * ldx + k]), acc[m]);
-      }
-    } else {
-#pragma unroll 8
-      for (int k = part * 32 + lane; k < K; k += wpf * 32) {
-        const float a = bf16_val(wf[k]);
+      for (int u = 0; u < U; ++u) a[u] = __ldcs(reinterpret_cast<const T*>(wf + k0 + u * STEP));
 #pragma unroll
-        for (int m = 0; m < R; ++m) acc[m] = __fmaf_rn(a, bf16_val(x[m * ldx + k]), acc[m]);
+      for (int u = 0; u < U; u += B) add(a + u, x + k0 + u * STEP);
+    }
+    T a[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) a[u] = k0 + u * STEP < end ? __ldcs(reinterpret_cast<const T*>(wf + k0 + u * STEP)) : T{};
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (k0 + u * STEP >= end) continue;
+      float av[W], bv[W];
+      Cols<W>::floats(a[u], av);
+#pragma unroll
+      for (int m = 0; m < R; ++m) {
+        Cols<W>::floats(*reinterpret_cast<const T*>(x + m * ldx + k0 + u * STEP), bv);
+#pragma unroll
+        for (int j = 0; j < W; ++j) acc[m] = __fmaf_rn(av[j], bv[j], acc[m]);
       }
+    }
+    const int k = K / W * W + lane;   // the last K % W columns
+    if (part == 0 && k < K) {
+#pragma unroll
+      for (int m = 0; m < R; ++m) acc[m] = __fmaf_rn(bf16_val(wf[k]), bf16_val(x[m * ldx + k]), acc[m]);
     }
   }
 #pragma unroll
@@ -854,6 +896,8 @@ bool rows16(const void* p, int dtype, int64_t ld) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % (dtype ? 4 : 8) == 0;
 }
 bool tma_rows(const void* p, int64_t ld) { return rows16(p, 0, ld); }
+// rows of bf16 that start on 4-byte boundaries
+bool rows4(const void* p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % 4 == 0 && ld % 2 == 0; }
 int64_t pad8(int64_t n) { return (n + 7) / 8 * 8; }
 size_t pad256(size_t n) { return (n + 255) & ~(size_t)255; }
 
@@ -917,7 +961,6 @@ cudaError_t gemm(const Operand& a, const Operand& b, int64_t M, int64_t N, int64
   p.e = epi;
   p.e.vec = rows16(epi.y, epi.y_dtype, epi.ldy) && (!epi.z || rows16(epi.z, 0, epi.ldz)) &&
             (!epi.residual || rows16(epi.residual, 0, epi.ldr));
-  auto rows4 = [](const void* q, int64_t ld) { return reinterpret_cast<uintptr_t>(q) % 4 == 0 && ld % 2 == 0; };
   p.e.even = N % 2 == 0 && (epi.y_dtype != 0 || rows4(epi.y, epi.ldy)) && (!epi.z || rows4(epi.z, epi.ldz)) &&
              (!epi.residual || rows4(epi.residual, epi.ldr));
   const int64_t small = ((M + 127) / 128) * ((N + 127) / 128);
@@ -940,16 +983,14 @@ size_t copy_bytes(int64_t rows, int64_t cols) { return pad256((size_t)rows * pad
 
 template <int R>
 cudaError_t gemv_rows(const LinearArgs& a, const Epilogue& e, cudaStream_t stream) {
-  const bool vec = tma_rows(a.x, a.ldx) && tma_rows(a.w, a.ldw);
-  const int64_t warps = (int64_t)sm_count() * 32, least = vec ? 512 : 64;   // columns of K that are worth a warp
+  const bool vec = tma_rows(a.x, a.ldx) && tma_rows(a.w, a.ldw), even = rows4(a.x, a.ldx) && rows4(a.w, a.ldw);
+  const int64_t warps = (int64_t)sm_count() * 32, least = vec ? 512 : (even ? 128 : 64);   // columns of K that are worth a warp
   int wpf = 1;
   while (wpf < GEMV_T / 32 && a.N * wpf * 2 <= warps && a.K >= least * wpf * 2) wpf *= 2;
   const dim3 grid((unsigned)((a.N * wpf + GEMV_T / 32 - 1) / (GEMV_T / 32)));
-  const uint16_t* x = static_cast<const uint16_t*>(a.x);
-  const uint16_t* w = static_cast<const uint16_t*>(a.w);
-  const cudaError_t err =
-      vec ? launch_after(linear_gemv_kernel<R, true>, grid, dim3(GEMV_T), 0, stream, x, a.ldx, w, a.ldw, a.N, (int)a.K, wpf, e)
-          : launch_after(linear_gemv_kernel<R, false>, grid, dim3(GEMV_T), 0, stream, x, a.ldx, w, a.ldw, a.N, (int)a.K, wpf, e);
+  const auto kernel = vec ? linear_gemv_kernel<R, 8> : (even ? linear_gemv_kernel<R, 2> : linear_gemv_kernel<R, 1>);
+  const cudaError_t err = launch_after(kernel, grid, dim3(GEMV_T), 0, stream, static_cast<const uint16_t*>(a.x), a.ldx,
+                                       static_cast<const uint16_t*>(a.w), a.ldw, a.N, (int)a.K, wpf, e);
   return err != cudaSuccess ? err : cudaGetLastError();
 }
 

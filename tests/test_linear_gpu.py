@@ -228,3 +228,14 @@ def test_many_rounds_of_tiles(cuda_lib, M, N, K):
         assert torch.equal(y, x.float() @ w.float().t() + r.float())
         assert torch.equal(dx, dy.float() @ w.float()) and torch.equal(dw, dy.float().t() @ x.float())
         assert torch.equal(db, dy.float().sum(0))
+
+
+@pytest.mark.parametrize("M", [1, 2, 3, 4])
+@pytest.mark.parametrize("N,K,pad", [(2560, 7490, 0), (300, 65, 1), (300, 66, 0), (300, 66, 1), (7, 1, 1), (5000, 4098, 0)])
+def test_few_rows_of_any_alignment(cuda_lib, M, N, K, pad):
+    """Rows on 4-byte and on 2-byte boundaries; whole numbers, so the sums are exact."""
+    x, w = (torch.full((r, K + pad), float("nan"), device="cuda", dtype=BF)[:, :K] for r in (M, N))
+    x.copy_((torch.arange(M * K, device="cuda") % 13 - 6).view(M, K))
+    w.copy_((torch.arange(N * K, device="cuda") * 7 % 11 - 5).view(N, K))
+    y = cuda_lib.linear(x, w, out_dtype=torch.float32)
+    assert torch.equal(y.double(), x.double() @ w.double().T)
