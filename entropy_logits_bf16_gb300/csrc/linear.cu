@@ -92,35 +92,56 @@ struct GemmParams {
 
 // 1 / v to 2^-22 or so (MUFU), enough for what is rounded to bf16 or compared
 // at a few 2^-24 of |z| + 1.
-__device__ __forceinline__ float rcp(float v) { return __fdividef(1.f, v); }
+__device__ __forceinline__ float rcp(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
 
 // Phi(-|z|), Phi the normal distribution function: 1/2 erfc(|z| / sqrt 2) by
 // Abramowitz and Stegun 7.1.26, erfc(x) = (a1 t + ... + a5 t^5) exp(-x^2) with t = 1 / (1 + p x)
-// (absolute error 1.5e-7).  About 13 instructions; the product with the exponential keeps
+// (absolute error 1.5e-7), two numbers an instruction; the product with the exponential keeps
 // the far tail free of cancellation.  `bell`: exp(-z^2 / 2).
-__device__ __forceinline__ float normal_tail(float z, float& bell) {
-  const float x = fabsf(z) * 0.70710678118654752f;
-  const float t = rcp(__fmaf_rn(0.3275911f, x, 1.f));
-  float q = __fmaf_rn(1.061405429f, t, -1.453152027f);
-  q = __fmaf_rn(q, t, 1.421413741f);
-  q = __fmaf_rn(q, t, -0.284496736f);
-  q = __fmaf_rn(q, t, 0.254829592f);
-  bell = ex2(-(x * x) * kLog2e);
-  return 0.5f * (q * t) * bell;
+__device__ __forceinline__ float2 normal_tail(float2 z, float2& bell) {
+  const float2 x = mul2(make_float2(fabsf(z.x), fabsf(z.y)), both(0.70710678118654752f));
+  const float2 d = fma2(both(0.3275911f), x, both(1.f)), t = make_float2(rcp(d.x), rcp(d.y));
+  float2 q = fma2(both(0.5f * 1.061405429f), t, both(0.5f * -1.453152027f));
+  q = fma2(q, t, both(0.5f * 1.421413741f));
+  q = fma2(q, t, both(0.5f * -0.284496736f));
+  q = fma2(q, t, both(0.5f * 0.254829592f));
+  const float2 e = mul2(mul2(x, x), both(-kLog2e));
+  bell = make_float2(ex2(e.x), ex2(e.y));
+  return mul2(mul2(q, t), bell);
+}
+// Phi(z) from Phi(-|z|).
+__device__ __forceinline__ float2 normal_below(float2 z, float2 tail) {
+  const float2 up = fma2(tail, both(-1.f), both(1.f));
+  return make_float2(z.x > 0.f ? up.x : tail.x, z.y > 0.f ? up.y : tail.y);
+}
+// 1 / (1 + exp(-z)).
+__device__ __forceinline__ float2 logistic(float2 z) {
+  const float2 e = mul2(z, both(-kLog2e)), d = add2(make_float2(ex2(e.x), ex2(e.y)), both(1.f));
+  return make_float2(rcp(d.x), rcp(d.y));
 }
 // act of W values; the choice is made once.
 template <int W>
 __device__ __forceinline__ void activate(float (&v)[W], int act) {
   if (act == RLK_ACT_GELU) {
 #pragma unroll
-    for (int j = 0; j < W; ++j) {
-      float bell;
-      const float tail = normal_tail(v[j], bell);
-      v[j] = v[j] * (v[j] > 0.f ? __fsub_rn(1.f, tail) : tail);
+    for (int j = 0; j < W; j += 2) {
+      const float2 z = make_float2(v[j], v[j + 1 < W ? j + 1 : j]);
+      float2 bell;
+      const float2 tail = normal_tail(z, bell), o = mul2(z, normal_below(z, tail));
+      v[j] = o.x;
+      if (j + 1 < W) v[j + 1] = o.y;
     }
   } else if (act == RLK_ACT_SILU) {
 #pragma unroll
-    for (int j = 0; j < W; ++j) v[j] = v[j] * rcp(1.f + ex2(-v[j] * kLog2e));
+    for (int j = 0; j < W; j += 2) {
+      const float2 z = make_float2(v[j], v[j + 1 < W ? j + 1 : j]), o = mul2(z, logistic(z));
+      v[j] = o.x;
+      if (j + 1 < W) v[j + 1] = o.y;
+    }
   } else if (act == RLK_ACT_RELU) {
 #pragma unroll
     for (int j = 0; j < W; ++j) v[j] = v[j] < 0.f ? 0.f : v[j];
@@ -128,18 +149,18 @@ __device__ __forceinline__ void activate(float (&v)[W], int act) {
 }
 // act'(z), to a few 2^-24.
 template <int ACT>
-__device__ __forceinline__ float activation_slope(float z) {
+__device__ __forceinline__ float2 activation_slope(float2 z) {
   if (ACT == RLK_ACT_GELU) {   // Phi(z) + z phi(z)
-    float bell;
-    const float tail = normal_tail(z, bell);
-    return __fmaf_rn(z * bell, 0.39894228040143268f, z > 0.f ? 1.f - tail : tail);
+    float2 bell;
+    const float2 tail = normal_tail(z, bell);
+    return fma2(mul2(z, bell), both(0.39894228040143268f), normal_below(z, tail));
   }
   if (ACT == RLK_ACT_SILU) {
-    const float s = rcp(1.f + ex2(-z * kLog2e));
-    return s * __fmaf_rn(z, 1.f - s, 1.f);
+    const float2 s = logistic(z);
+    return mul2(s, fma2(z, fma2(s, both(-1.f), both(1.f)), both(1.f)));
   }
-  if (ACT == RLK_ACT_RELU) return z > 0.f ? 1.f : (z != z ? z : 0.f);
-  return 1.f;
+  auto relu = [](float v) { return v > 0.f ? 1.f : (v != v ? v : 0.f); };
+  return make_float2(relu(z.x), relu(z.y));
 }
 
 __device__ __forceinline__ void prefetch_l2(const void* p) {
@@ -177,15 +198,20 @@ __device__ __forceinline__ uint4 residual8(const Epilogue& e, int64_t row, int64
 __device__ __forceinline__ void finish8(const Epilogue& e, int64_t row, int64_t col, int n, float (&v)[8],
                                         const float (&bias)[8], uint4 res) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = __fadd_rn(v[j], bias[j]);
+  for (int j = 0; j < 8; j += 2) {
+    const float2 o = add2(make_float2(v[j], v[j + 1]), make_float2(bias[j], bias[j + 1]));
+    v[j] = o.x;
+    v[j + 1] = o.y;
+  }
   if (e.z) store8(e.z + row * e.ldz + col, v, n);
   activate(v, e.act);
   if (e.residual) {
     const uint32_t w[4] = {res.x, res.y, res.z, res.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      v[2 * k] = __fadd_rn(v[2 * k], bf16_lo(w[k]));
-      v[2 * k + 1] = __fadd_rn(v[2 * k + 1], bf16_hi(w[k]));
+      const float2 o = add2(make_float2(v[2 * k], v[2 * k + 1]), bf16x2_to_f2(w[k]));
+      v[2 * k] = o.x;
+      v[2 * k + 1] = o.y;
     }
   }
   if (e.y_dtype == 0) {
@@ -803,10 +829,15 @@ __global__ void __launch_bounds__(DT) linear_dz_kernel(LinearBwdArgs a, uint16_t
       if (m >= a.M) continue;
       float v[W];
 #pragma unroll
-      for (int j = 0; j < W; ++j) {
-        v[j] = j % 2 ? bf16_hi(g[k][j / 2]) : bf16_lo(g[k][j / 2]);
-        if (act) v[j] = __fmul_rn(v[j], activation_slope<ACT>(j % 2 ? bf16_hi(zz[k][j / 2]) : bf16_lo(zz[k][j / 2])));
-        sum[j] = __fadd_rn(sum[j], v[j]);
+      for (int j = 0; j < W; j += 2) {   // (W = 1: the pair's second is not used)
+        float2 d = bf16x2_to_f2(g[k][j / 2]);
+        if (act) d = mul2(d, activation_slope<ACT>(bf16x2_to_f2(zz[k][j / 2])));
+        v[j] = d.x;
+        sum[j] = __fadd_rn(sum[j], d.x);
+        if (j + 1 < W) {
+          v[j + 1] = d.y;
+          sum[j + 1] = __fadd_rn(sum[j + 1], d.y);
+        }
       }
       if (!dz) continue;
       uint16_t* d = dz + m * ldd + c;
