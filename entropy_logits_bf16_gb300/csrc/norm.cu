@@ -7,18 +7,27 @@
 //
 // A few flops an element: bound by memory.  A row of up to 16384 columns lives
 // in the registers of a group of threads, 16 or 32 columns a thread (4 to 512
-// threads), so each pass reads every element once:
-//  * forward: one row a group; deviations from the mean, then their squares.
-//  * backward: persistent CTAs; a thread keeps its columns of w and of the
-//    partial dw, db over all its rows, and the next rows are on their way to shared
-//    memory while it works on this one.  The CTAs' partials go to
-//    the workspace and a second kernel adds them in order.
+// threads), so each pass reads every element once.  The CTAs are persistent,
+// and the next rows are on their way to shared memory (bulk copies) while a group works:
+//  * forward: a group has two rows at work (their sums share barriers); the
+//    mean first, then the squares of the deviations from it.  w and b stay in registers.
+//  * backward: a thread keeps its columns of w and of the partial dw, db over all
+//    its rows (dw, db in shared memory where registers are short).  The CTAs'
+//    partials go to the workspace and a second kernel adds them in order.
 // Columns are taken 8 at a time (16-byte loads) where every row starts on a
-// 16-byte boundary, else one at a time with consecutive columns on
-// consecutive threads (2-byte loads still coalesce into whole lines).  Wider rows
+// 16-byte boundary and H is a multiple of 8, else one at a time with
+// consecutive columns on consecutive threads.  Wider rows
 // take the any-width kernels: several passes over the row, and the parameter
 // gradients in a pass of their own.
 // Sums are fp32 in a fixed order.
+//
+// Measured, 16384 rows of 4096 bf16: RMS forward 52 us, backward from
+// fp32 dy 81 us; layer norm's forward with the checkpoint written 80 us
+// (52 M warp instructions against 31 M without it), its backward from the checkpoint
+// and bf16 dy 79 us: 4.2 TB/s, half of the issue slots; 16 warps an SM do not
+// cover the chains of instructions.  4099 rows of 5003
+// (one column at a time): 36 us and 61 us, bound by instructions
+// and barriers.  The parameter sums take 7 us.
 
 #include <math.h>
 
@@ -384,7 +393,7 @@ __device__ __forceinline__ void write_checkpoint(const CheckpointView& ck, int64
 // Bulk copies: one thread of a group asks for whole rows, which keeps more bytes
 // on their way than loads or cp.async did (reading fp32 dy and bf16 x by cp.async the
 // backward stayed at 3.6 TB/s of reads whatever the depth: 108 us on 16384 rows of
-// 4096; now 78 us).  A place has an mbarrier; every wait on one is
+// 4096; now 81 us).  A place has an mbarrier; every wait on one is
 // bounded, and a row that did not come in time is NaN.
 // Types: 0 bf16, 1 fp32, 2 checkpoint codes.
 constexpr int kFromCk = 2;
@@ -956,7 +965,8 @@ cudaError_t allow_smem(K kernel, std::atomic<int>* done) {
   if (e == cudaSuccess && ds >= 0) done[ds].store(1);
   return e;
 }
-// CTAs an SM: by the registers, two at most.
+// CTAs an SM: by the registers, two at most (three, with 80 registers and a row at a
+// time in the forward: 67 us on 16384 rows of 4096, layer norm; two, with two rows: 58).
 template <int VW, int E>
 int ctas_for(int block) { return 2 * block * regs_of<VW, E>() <= 65536 ? 2 : 1; }
 // Rows on their way, as many (a power of two) as leave room for the SM's CTAs.
