@@ -7,7 +7,7 @@
 // operands may each be stored with K or with M / N contiguous, so neither w nor
 // x nor dz is transposed in memory.  bf16 operands arrive by TMA (128-byte
 // swizzle) in a ring of 64-deep stages, one thread issues the tcgen05 MMAs
-// (fp32 accumulators in TMEM), eight warps run the epilogue on registers read
+// (fp32 accumulators in TMEM), the other warps run the epilogue on registers read
 // with tcgen05.ld.
 //  * Many tiles: persistent pairs of CTAs (cta_group::2), a tile of 256 x 256 a
 //    pair: each SM stages half of A's and half of B's rows, half the shared-memory
@@ -46,21 +46,24 @@ namespace rlk {
 namespace {
 
 constexpr int BM = 128, BK = 64;
-constexpr int EPI_WARPS = 8, THREADS = 64 + 32 * EPI_WARPS;
 constexpr uint32_t MN_BLOCK = 64 * BK * 2;     // a 64-element block of an MN-contiguous operand
 constexpr uint32_t STAGING = 32 * 32 * 4;      // an epilogue warp's 32 x 32 piece of a tile
 constexpr int GROUP_M = 8;
 constexpr int MAX_SPLIT = 4;                   // CTAs that share a tile's K, at most
 // The two shapes.  A pair of CTAs (one tile of 256 x 256, 128 rows of A and of B
-// each; six stages, one CTA an SM), or one CTA (a tile of 128 x 128, its K perhaps split
+// each; five stages, one CTA an SM), or one CTA (a tile of 128 x 128, its K perhaps split
 // over a cluster; a single accumulator; six stages, or three where there are more
 // CTAs than SMs, so that two share an SM and one's epilogue runs beside the other's
-// products).
+// products).  The pair's 16 epilogue warps take the sixth stage's room: with eight,
+// and six stages, products of a short K waited on the epilogue (16384 x 4096 x 512
+// with GELU 138 us, now 98; K 4096 the same within its noise).
 constexpr int BROWS = 128;
 constexpr uint32_t A_BYTES = BM * BK * 2, STAGE_BYTES = A_BYTES + BROWS * BK * 2;
 template <bool SPLIT>
 struct Shape {
   static constexpr int G = SPLIT ? 1 : 2;      // CTAs of a tile
+  static constexpr int EPI_WARPS = SPLIT ? 8 : 16, THREADS = 64 + 32 * EPI_WARPS;
+  static constexpr int STAGES = SPLIT ? 6 : 5; // at most
   static constexpr int TM = BM * G, BN = BROWS * G;
   static constexpr uint32_t TMEM_COLS = SPLIT ? BN : 2 * BN;
   static constexpr int PLD = BN + 4;           // row pitch (floats) of a partial tile: conflict-free float4 rows
@@ -324,12 +327,12 @@ __device__ __forceinline__ void tile_coords(const GemmParams& p, int t, int& mt,
 // SPLIT: a cluster of CTAs works on one tile of 128 x 128, each on its share of
 // K; else pair b works on tiles b, + the number of pairs, ... of 256 x 256.
 template <bool A_MN, bool B_MN, bool SPLIT>
-__global__ void __launch_bounds__(THREADS, SPLIT ? 2 : 1)
+__global__ void __launch_bounds__(Shape<SPLIT>::THREADS, SPLIT ? 2 : 1)
     linear_gemm_kernel(const __grid_constant__ CUtensorMap map_a,
                        const __grid_constant__ CUtensorMap map_b, const GemmParams p, int cluster) {
   using S = Shape<SPLIT>;
-  constexpr int G = S::G, TM = S::TM, BN = S::BN, PLD = S::PLD;
-  const int stages = SPLIT ? p.stages : MAX_STAGES;
+  constexpr int G = S::G, TM = S::TM, BN = S::BN, PLD = S::PLD, EPI_WARPS = S::EPI_WARPS;
+  const int stages = SPLIT ? p.stages : S::STAGES;
   const uint32_t ring = stages * STAGE_BYTES;
   constexpr uint32_t TMEM_COLS = S::TMEM_COLS;
   extern __shared__ uint8_t smem_raw[];
@@ -460,11 +463,12 @@ __global__ void __launch_bounds__(THREADS, SPLIT ? 2 : 1)
     }
   } else {
     // ------------------------------------------------------ epilogue
-    // Two warps a TMEM quadrant (32 rows), each with half of the columns, 32 at
-    // a time: tcgen05.ld gives a thread 32 columns of one row; a turn through the
+    // Two warps (a pair's tile: four) a TMEM quadrant (32 rows), each with its share of
+    // the columns, 32 at a time: tcgen05.ld gives a thread 32 columns of one row; a turn through the
     // warp's staging (16-byte units, swizzled: no bank conflicts) gives it 8
     // columns of 4 rows, so that a warp reads and writes whole 64-byte pieces of 8 rows.
-    const int q = warp & 3, half = (warp - 2) >> 2;
+    constexpr int PARTS = EPI_WARPS / 4, WIDTH = BN / PARTS;
+    const int q = warp & 3, part = (warp - 2) >> 2;
     const uint32_t lane_base = (uint32_t)(q * 32) << 16;
     float* st = staging + (warp - 2) * (STAGING / 4);
     uint32_t tile = 0;
@@ -473,12 +477,12 @@ __global__ void __launch_bounds__(THREADS, SPLIT ? 2 : 1)
       int mt, nt;
       tile_coords(p, t, mt, nt);
       const uint32_t acc = tile & 1u, accph = (tile >> 1) & 1u;
-      if (p.e.residual) {   // on its way to L2 while the products run: 3 lines a row hold half of the columns
-        const int64_t r = (int64_t)mt * TM + a_off + q * 32 + lane, c = (int64_t)nt * BN + half * (BN / 2);
+      if (p.e.residual) {   // on its way to L2 while the products run: the lines of a row that hold this warp's columns
+        const int64_t r = (int64_t)mt * TM + a_off + q * 32 + lane, c = (int64_t)nt * BN + part * WIDTH;
         if (r < p.M) {
 #pragma unroll
-          for (int k = 0; k < 3; ++k) {
-            const int64_t at = c + (k < 2 ? k * 64 : BN / 2 - 1);
+          for (int k = 0; k <= WIDTH / 64; ++k) {
+            const int64_t at = c + (k < WIDTH / 64 ? k * 64 : WIDTH - 1);
             if (at < p.N) prefetch_l2(p.e.residual + r * p.e.ldr + at);
           }
         }
@@ -488,8 +492,8 @@ __global__ void __launch_bounds__(THREADS, SPLIT ? 2 : 1)
       tc::fence_after();
       const int64_t row0 = (int64_t)mt * TM + a_off + q * 32;
 #pragma unroll 1
-      for (int ch = 0; ch < BN / 64; ++ch) {
-        const int c0 = half * (BN / 2) + ch * 32;
+      for (int ch = 0; ch < WIDTH / 32; ++ch) {
+        const int c0 = part * WIDTH + ch * 32;
         const int64_t col0 = (int64_t)nt * BN + c0;
         const int sub = lane & 3, r8 = lane >> 2;           // 8 columns, one of 8 rows
         const int64_t col = col0 + sub * 8;
@@ -511,7 +515,7 @@ __global__ void __launch_bounds__(THREADS, SPLIT ? 2 : 1)
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = NAN;
         }
-        if (ch == BN / 64 - 1) {   // the accumulator is in registers: its next tile may begin
+        if (ch == WIDTH / 32 - 1) {   // the accumulator is in registers: its next tile may begin
           tc::fence_before();
           __syncwarp();
           if (lane == 0 && ok) {
@@ -521,10 +525,10 @@ __global__ void __launch_bounds__(THREADS, SPLIT ? 2 : 1)
         }
         if (SPLIT) {
           if (row0 + lane < p.M && col0 < p.N) {
-            float* part = reinterpret_cast<float*>(base_ptr) + (q * 32 + lane) * PLD + c0;
+            float* own = reinterpret_cast<float*>(base_ptr) + (q * 32 + lane) * PLD + c0;
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-              reinterpret_cast<float4*>(part)[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+              reinterpret_cast<float4*>(own)[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
           }
           continue;
         }
@@ -566,7 +570,7 @@ __global__ void __launch_bounds__(THREADS, SPLIT ? 2 : 1)
     const int rows = (int)(p.M - row0 < BM ? p.M - row0 : BM);
     if (p.e.vec) {
       const int octs = width / 8;
-      for (int i = threadIdx.x; i < rows * octs; i += THREADS) {
+      for (int i = threadIdx.x; i < rows * octs; i += Shape<SPLIT>::THREADS) {
         const int r = i / octs, c = (i - r * octs) * 8;
         const int64_t col = col0 + c;
         if (col >= p.N) continue;
@@ -945,7 +949,7 @@ cudaError_t set_smem() {
   const int ds = device_slot();
   if (ds >= 0 && done[ds].load()) return cudaSuccess;
   const cudaError_t e = cudaFuncSetAttribute(linear_gemm_kernel<A_MN, B_MN, SPLIT>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape<SPLIT>::smem(MAX_STAGES));
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape<SPLIT>::smem(Shape<SPLIT>::STAGES));
   if (e == cudaSuccess && ds >= 0) done[ds].store(1);
   return e;
 }
@@ -970,8 +974,8 @@ cudaError_t launch_gemm(const CUtensorMap& ma, const CUtensorMap& mb, GemmParams
   cudaLaunchConfig_t cfg{};
   const int pairs = sm_count() / 2;
   cfg.gridDim = dim3((unsigned)(SPLIT ? tiles * split : 2 * (tiles < pairs ? tiles : pairs)));
-  cfg.blockDim = dim3(THREADS);
-  p.stages = SPLIT && tiles * split > sm_count() ? FEW_STAGES : MAX_STAGES;
+  cfg.blockDim = dim3(Shape<SPLIT>::THREADS);
+  p.stages = SPLIT && tiles * split > sm_count() ? FEW_STAGES : Shape<SPLIT>::STAGES;
   cfg.dynamicSmemBytes = Shape<SPLIT>::smem(p.stages);
   cfg.stream = stream;
   cudaLaunchAttribute at[2];
