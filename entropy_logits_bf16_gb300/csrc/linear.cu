@@ -28,9 +28,9 @@
 // unrounded.
 // Every wait is bounded; when one runs out the CTA's unfinished tiles are NaN.
 //
-// Measured: 16384 x 4096 x 4096 with bias, GELU, residual and z 333 us, 1650 TFLOP/s
-// (tensor pipe 85 % of its cycles); backward of 8192 x 4096 x 4096:
-// dx 156 us (87 %), dw 173 us (83 %: 256 tiles on 76
+// Measured: 16384 x 4096 x 4096 with bias, GELU, residual and z 337 us, 1630 TFLOP/s
+// (tensor pipe 79 % of its cycles); backward of 8192 x 4096 x 4096:
+// dx 154 us (87 %), dw 171 us (84 %: 256 tiles on 76
 // pairs are 3.4 rounds, and 4 are taken), dz and db 30 and 7 us.
 
 #include <math.h>
