@@ -846,16 +846,17 @@ bool checkpoint_ok(const rlk_checkpoint* c, int64_t H, rlk::CheckpointView& v) {
 }
 
 rlk_status checkpoint_args(const void* x, rlk_dtype dtype, int64_t T, int64_t H, int64_t ldx,
-                           const rlk_checkpoint* c, rlk::CheckpointArgs& a) {
+                           const rlk_checkpoint* c, uint32_t* status, rlk::CheckpointArgs& a) {
   if (!good_dtype(dtype) || T < 0 || H < 1 || H > kMaxWidth || ldx < H) return RLK_ERR_INVALID_ARG;
   if (T == 0) return RLK_OK;
-  if (!x || !elem_aligned(x, dtype) || !checkpoint_ok(c, H, a.ck)) return RLK_ERR_INVALID_ARG;
+  if (!x || !elem_aligned(x, dtype) || !aligned_to(status, 4) || !checkpoint_ok(c, H, a.ck))
+    return RLK_ERR_INVALID_ARG;
   a.x = const_cast<void*>(x);
   a.dtype = dtype_index(dtype);
   a.T = T;
   a.H = H;
   a.ldx = ldx;
-  a.status = nullptr;
+  a.status = status;
   return RLK_OK;
 }
 
@@ -869,9 +870,8 @@ rlk_status rlk_checkpoint_pack(const void* x, rlk_dtype dtype, int64_t T, int64_
                                const rlk_checkpoint* out, uint32_t* out_status_word,
                                rlk_stream stream) {
   rlk::CheckpointArgs a{};
-  const rlk_status st = checkpoint_args(x, dtype, T, H, ldx, out, a);
+  const rlk_status st = checkpoint_args(x, dtype, T, H, ldx, out, out_status_word, a);
   if (st != RLK_OK || T == 0) return st;
-  a.status = out_status_word;
   if (rlk::take_injected_failure()) return RLK_ERR_CUDA;
   return rlk::launch_checkpoint_pack(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? RLK_OK
@@ -881,7 +881,7 @@ rlk_status rlk_checkpoint_pack(const void* x, rlk_dtype dtype, int64_t T, int64_
 rlk_status rlk_checkpoint_unpack(const rlk_checkpoint* in, int64_t T, int64_t H, void* out,
                                  rlk_dtype dtype, int64_t ldo, rlk_stream stream) {
   rlk::CheckpointArgs a{};
-  const rlk_status st = checkpoint_args(out, dtype, T, H, ldo, in, a);
+  const rlk_status st = checkpoint_args(out, dtype, T, H, ldo, in, nullptr, a);
   if (st != RLK_OK || T == 0) return st;
   if (rlk::take_injected_failure()) return RLK_ERR_CUDA;
   return rlk::launch_checkpoint_unpack(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
@@ -901,7 +901,8 @@ rlk_status rlk_norm_fwd(const void* x, rlk_dtype dtype, int64_t T, int64_t H, in
   if (!(std::isfinite(eps) && eps >= 0.0f)) return RLK_ERR_INVALID_ARG;
   if (T == 0) return RLK_OK;
   if (!x || !y || !elem_aligned(x, dtype) || !elem_aligned(y, y_dtype) ||
-      !elem_aligned(weight, param_dtype) || !elem_aligned(bias, param_dtype))
+      !elem_aligned(weight, param_dtype) || !elem_aligned(bias, param_dtype) ||
+      !aligned_to(out_mean, 4) || !aligned_to(out_rstd, 4) || !aligned_to(out_status_word, 4))
     return RLK_ERR_INVALID_ARG;
   rlk::NormArgs a{};
   if (out_checkpoint && !checkpoint_ok(out_checkpoint, H, a.ck)) return RLK_ERR_INVALID_ARG;
@@ -944,7 +945,8 @@ rlk_status rlk_norm_bwd(const void* dy, rlk_dtype dy_dtype, int64_t lddy, const 
     if (!dy || !rstd || !grad_x || (kind == RLK_NORM_LAYER && !mean) || (!x == !checkpoint))
       return RLK_ERR_INVALID_ARG;
     if (!elem_aligned(dy, dy_dtype) || !elem_aligned(x, dtype) ||
-        !elem_aligned(weight, param_dtype) || !elem_aligned(grad_x, grad_dtype))
+        !elem_aligned(weight, param_dtype) || !elem_aligned(grad_x, grad_dtype) ||
+        !aligned_to(mean, 4) || !aligned_to(rstd, 4))
       return RLK_ERR_INVALID_ARG;
     if (checkpoint && !checkpoint_ok(checkpoint, H, a.ck)) return RLK_ERR_INVALID_ARG;
   }
@@ -1110,7 +1112,8 @@ rlk_status rlk_preference_loss(const float* logp, const float* logp_ref, const u
     return RLK_ERR_INVALID_ARG;
   if (!seq_offsets || !out_loss || (n_tok > 0 && !logp)) return RLK_ERR_INVALID_ARG;
   if (!aligned_to(logp, 4) || !aligned_to(logp_ref, 4) || !aligned_to(seq_offsets, 4) ||
-      !aligned_to(out_grad, 4) || !aligned_to(out_reward, 4))
+      !aligned_to(out_grad, 4) || !aligned_to(out_reward, 4) || !aligned_to(out_loss, 4) ||
+      !aligned_to(out_stats, 4))
     return RLK_ERR_INVALID_ARG;
   if (!workspace || workspace_bytes < rlk::pref_workspace_bytes(n_tok, n_pairs) ||
       !aligned_to(workspace, 16))
