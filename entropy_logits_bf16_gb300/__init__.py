@@ -1021,7 +1021,7 @@ def norm_backward(dy: torch.Tensor, x, weight, mean, rstd, *, kind: int = NORM_L
     adds into ``grad_weight`` / ``grad_bias``."""
     lib = load()
     kept = x if isinstance(x, Checkpoint) else None
-    _need_cuda(dy, None if kept else x, weight, mean, rstd, out, grad_weight, grad_bias)
+    _need_cuda(dy, None if kept else x, weight, mean, rstd, out, grad_weight, grad_bias, workspace)
     gdt, ldg = _matrix(dy, "dy")
     T, H = dy.shape
     dev = dy.device
@@ -1224,7 +1224,7 @@ def preference_loss(logp, logp_ref, seq_offsets, *, loss_mask=None, loss_type: i
     ``logp_ref`` None: reference-free.  Returns (loss[1], dL/dlogp or None,
     rewards [2 pairs] or None, stats[PREF_NSTATS] or None)."""
     lib = load()
-    _need_cuda(logp, logp_ref, seq_offsets, loss_mask)
+    _need_cuda(logp, logp_ref, seq_offsets, loss_mask, workspace)
     n_tok, offsets = logp.numel(), seq_offsets.numel()
     _vector(logp, n_tok, "logp")
     if logp_ref is not None:
