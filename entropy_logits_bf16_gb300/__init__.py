@@ -919,36 +919,35 @@ def _vector(t, n, name):
 
 class Checkpoint:
     """An activation [T, H] kept in 8 bits (rlk_checkpoint): int8 ``codes``
-    [T, >= H] and uint8 ``scales`` [T, >= ceil(H / 32)]."""
+    [T, >= H] and uint8 ``scales`` [T, >= ceil(H / 32)].  Both may be replaced
+    (moved off the device and back, say): a call takes the tensors that are there."""
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, T: int, H: int):
-        _need_cuda(codes, scales)
-        blocks = -(-H // CHECKPOINT_BLOCK)
-        if codes.dtype != torch.int8 or scales.dtype != torch.uint8:
-            raise ValueError("codes must be int8, scales uint8")
-        for t, cols in ((codes, H), (scales, blocks)):
-            if t.dim() != 2 or t.shape[0] != T or t.shape[1] < cols or not t.is_contiguous():
-                raise ValueError("codes and scales must be contiguous [T, >= H] and [T, >= ceil(H / 32)]")
-        self._set(codes, scales, T, H, codes.shape[1], scales.shape[1])
-
-    def _set(self, codes, scales, T, H, ld_codes, ld_scales):
         self.codes, self.scales, self.shape = codes, scales, (T, H)
-        # the rlk_checkpoint that the entry points read during a call
-        self._struct = CheckpointBuffers(codes.data_ptr(), scales.data_ptr(), ld_codes, ld_scales)
-        return self
+        self.buffers()
 
     def buffers(self):
-        return ctypes.byref(self._struct)
+        """A reference to the rlk_checkpoint of the tensors as they are now."""
+        codes, scales, (T, H) = self.codes, self.scales, self.shape
+        _need_cuda(codes, scales)
+        if codes.dtype != torch.int8 or scales.dtype != torch.uint8:
+            raise ValueError("codes must be int8, scales uint8")
+        if (codes.dim() != 2 or scales.dim() != 2 or codes.shape[0] != T or scales.shape[0] != T
+                or codes.shape[1] < H or scales.shape[1] * CHECKPOINT_BLOCK < H
+                or not codes.is_contiguous() or not scales.is_contiguous()):
+            raise ValueError("codes and scales must be contiguous [T, >= H] and [T, >= ceil(H / 32)]")
+        return ctypes.byref(CheckpointBuffers(codes.data_ptr(), scales.data_ptr(), codes.shape[1], scales.shape[1]))
 
 
 def new_checkpoint(T: int, H: int, device) -> Checkpoint:
     """Room for the 8-bit checkpoint of an activation [T, H] on a CUDA device."""
     if torch.device(device).type != "cuda":
         raise ValueError("librlk operates on CUDA tensors only")
-    ld_codes, ld_scales = (H + 15) // 16 * 16, (H + 511) // 512 * 16
-    return Checkpoint.__new__(Checkpoint)._set(
-        torch.empty((T, ld_codes), dtype=torch.int8, device=device),
-        torch.empty((T, ld_scales), dtype=torch.uint8, device=device), T, H, ld_codes, ld_scales)
+    ck = Checkpoint.__new__(Checkpoint)   # its tensors are looked at when they are used
+    ck.codes = torch.empty((T, (H + 15) // 16 * 16), dtype=torch.int8, device=device)
+    ck.scales = torch.empty((T, (H + 511) // 512 * 16), dtype=torch.uint8, device=device)
+    ck.shape = (T, H)
+    return ck
 
 
 def checkpoint_pack(x: torch.Tensor, *, out: Checkpoint | None = None, status_word=None) -> Checkpoint:

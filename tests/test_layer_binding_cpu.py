@@ -36,3 +36,29 @@ def test_workspaces_on_the_host_are_refused():
             call(cuda(1 << 16, dtype=torch.uint8))
         with pytest.raises(ValueError):
             call(torch.zeros(1 << 16, dtype=torch.uint8))
+
+
+def test_a_checkpoint_follows_its_tensors(lib, monkeypatch):
+    """Replaced tensors are the ones that the entry points get, whatever was there before."""
+    T, H = 4, 100
+    ck = rlk.Checkpoint(cuda(T, 112, dtype=torch.int8), cuda(T, 16, dtype=torch.uint8), T, H)
+    seen = []
+    monkeypatch.setattr(lib, "rlk_checkpoint_unpack", lambda c, *rest: seen.append(
+        (c._obj.codes, c._obj.scales, c._obj.ld_codes, c._obj.ld_scales)) or 0)
+    out = cuda(T, H)
+    rlk.checkpoint_unpack(ck, out=out)
+    first = ck.codes, ck.scales
+    ck.codes, ck.scales = cuda(T, 128, dtype=torch.int8), cuda(T, 4, dtype=torch.uint8)
+    rlk.checkpoint_unpack(ck, out=out)
+    assert seen == [(first[0].data_ptr(), first[1].data_ptr(), 112, 16), (ck.codes.data_ptr(), ck.scales.data_ptr(), 128, 4)]
+    good = ck.codes
+    for bad in (torch.zeros(T, 112, dtype=torch.int8), cuda(T, 112, dtype=torch.uint8), cuda(T, 96, dtype=torch.int8),
+                cuda(T + 1, 112, dtype=torch.int8), cuda(T, 224, dtype=torch.int8)[:, ::2]):
+        ck.codes = bad
+        with pytest.raises(ValueError):
+            rlk.checkpoint_unpack(ck, out=out)
+        with pytest.raises(ValueError):
+            rlk.Checkpoint(bad, ck.scales, T, H)
+    ck.codes, ck.scales = good, cuda(T, 3, dtype=torch.uint8)
+    with pytest.raises(ValueError):
+        rlk.checkpoint_unpack(ck, out=out)
