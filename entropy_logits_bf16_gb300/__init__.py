@@ -14,6 +14,7 @@ import os
 import threading
 
 import torch
+from torch.autograd.function import once_differentiable
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "librlk.so")
@@ -389,6 +390,7 @@ class _LogprobEntropy(torch.autograd.Function):
         return lp, ent
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, g_lp, g_ent):
         logits, token_ids, state = ctx.saved_tensors
         if g_lp is None and g_ent is None:
@@ -1068,6 +1070,7 @@ class _Norm(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         kept, scales, weight, mean, rstd = ctx.saved_tensors
         x = kept if scales is None else Checkpoint(kept, scales, kept.shape[0], ctx.H)
@@ -1187,6 +1190,7 @@ class _Linear(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         kept, scales, weight, z = ctx.saved_tensors
         x = kept if scales is None else Checkpoint(kept, scales, kept.shape[0], weight.shape[1])

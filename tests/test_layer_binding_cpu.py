@@ -62,3 +62,35 @@ def test_a_checkpoint_follows_its_tensors(lib, monkeypatch):
     ck.codes, ck.scales = good, cuda(T, 3, dtype=torch.uint8)
     with pytest.raises(ValueError):
         rlk.checkpoint_unpack(ck, out=out)
+
+
+def plain_norm(x, w, b, **kw):
+    r = (x * x).mean(1).rsqrt()
+    return x * r[:, None] * w, None, r
+
+
+def plain_calls(monkeypatch):
+    """Plain forms in place of the library's calls."""
+    monkeypatch.setattr(rlk, "norm", plain_norm)
+    monkeypatch.setattr(rlk, "norm_backward", lambda dy, x, w, m, r, **kw: (dy * w * r[:, None], (dy * x).sum(0), None))
+    monkeypatch.setattr(rlk, "linear", lambda x, w, b, r, **kw: (x @ w.t(), x @ w.t()) if kw else x @ w.t())
+    monkeypatch.setattr(rlk, "linear_backward", lambda dy, x, w, z, **kw: (dy @ w, dy.t() @ x, None))
+    monkeypatch.setattr(rlk, "logprob_entropy", lambda x, ids, *a, **kw: (x.sum(1), x.square().sum(1)))
+    monkeypatch.setattr(rlk, "logprob_entropy_backward", lambda x, ids, t, state, g, h: g[:, None] + 2 * x)
+
+
+@pytest.mark.parametrize("op", ["norm", "linear", "logprob"])
+def test_second_derivatives_are_refused(monkeypatch, op):
+    """The gradients are the library's numbers: autograd cannot go through them, and
+    says so instead of taking them for constants."""
+    plain_calls(monkeypatch)
+    x, w = torch.randn(4, 8, requires_grad=True), torch.randn(8, requires_grad=True)
+    if op == "norm":
+        y = rlk.norm_autograd(x, w, kind=rlk.NORM_RMS)
+    elif op == "linear":
+        y = rlk.linear_autograd(x, torch.randn(6, 8, requires_grad=True), activation=rlk.ACT_GELU)
+    else:
+        y = sum(rlk.logprob_entropy_autograd(x, torch.zeros(4, dtype=torch.int32), 1.0, 1.0))
+    g, = torch.autograd.grad(y.square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable|differentiate twice"):
+        (g.sum() + x.sum()).backward()
