@@ -878,6 +878,14 @@ def sample_top_p(logits, temperature, top_p, uniforms, *, row_state=None, status
 _DTYPES = {torch.bfloat16: 0, torch.float32: 1}
 
 
+def _dtype(dtype, name):
+    """dtype index of a bf16 / fp32 output asked for."""
+    dt = _DTYPES.get(dtype)
+    if dt is None:
+        raise ValueError(f"{name} must be bf16 or fp32")
+    return dt
+
+
 def _matrix(t, name, shape=None):
     """dtype index and row stride of a 2-D bf16 / fp32 tensor (of ``shape``) with
     unit stride along its rows."""
@@ -993,7 +1001,7 @@ def norm(x: torch.Tensor, weight=None, bias=None, *, kind: int = NORM_LAYER, eps
     pdt = _params(H, weight, bias)
     dev = x.device
     if out is None:
-        ydt, ldy = (dt if out_dtype is None else _DTYPES[out_dtype]), H
+        ydt, ldy = (dt if out_dtype is None else _dtype(out_dtype, "out_dtype")), H
         out = torch.empty_like(x) if out_dtype is None and ld == H else torch.empty(
             (T, H), dtype=out_dtype or x.dtype, device=dev)
     else:
@@ -1116,7 +1124,7 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias=None, residual=None, *,
     dev = x.device
     ldr = 0 if residual is None else _bf16(residual, "residual", (M, N))
     if out is None:
-        ydt, ldy = (0 if out_dtype is None else _DTYPES[out_dtype]), N
+        ydt, ldy = (0 if out_dtype is None else _dtype(out_dtype, "out_dtype")), N
         out = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=dev)
     else:
         ydt, ldy = _matrix(out, "out", (M, N))

@@ -94,3 +94,14 @@ def test_second_derivatives_are_refused(monkeypatch, op):
     g, = torch.autograd.grad(y.square().sum(), x, create_graph=True)
     with pytest.raises(RuntimeError, match="once_differentiable|differentiate twice"):
         (g.sum() + x.sum()).backward()
+
+
+def test_output_types_are_refused_like_inputs():
+    x, w = cuda(4, 64, dtype=BF), cuda(32, 64, dtype=BF)
+    for call in (lambda: rlk.norm(x, out_dtype=torch.float16), lambda: rlk.linear(x, w, out_dtype=torch.float64),
+                 lambda: rlk.linear_backward(cuda(4, 32, dtype=BF), x, w, grad_dtype=torch.float16),
+                 lambda: rlk.norm_backward(x, x, None, None, cuda(4), kind=rlk.NORM_RMS, grad_dtype=torch.float16),
+                 lambda: rlk.checkpoint_unpack(rlk.Checkpoint(cuda(4, 64, dtype=torch.int8), cuda(4, 2, dtype=torch.uint8), 4, 64),
+                                               out=cuda(4, 64, dtype=torch.float16))):
+        with pytest.raises(ValueError):
+            call()
