@@ -1059,7 +1059,12 @@ cudaError_t aligned_operands(Copied x, Copied w, char*& ws, cudaStream_t stream)
 }
 
 constexpr int kDbParts = 304;   // most row parts of the bias gradient
-size_t db_bytes(int64_t N) { return pad256((size_t)kDbParts * pad8(N) * sizeof(float)); }
+// A part has DZ_ROWS rows or more.
+int64_t db_parts_most(int64_t M) {
+  const int64_t p = (M + DZ_ROWS - 1) / DZ_ROWS;
+  return p < kDbParts ? p : kDbParts;
+}
+size_t db_bytes(int64_t M, int64_t N) { return pad256((size_t)db_parts_most(M) * pad8(N) * sizeof(float)); }
 
 }  // namespace
 
@@ -1096,12 +1101,12 @@ cudaError_t launch_linear_fwd(const LinearArgs& a, cudaStream_t stream) {
 }
 
 size_t linear_bwd_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-  return copy_bytes(M, N) + copy_bytes(M, K) + copy_bytes(N, K) + db_bytes(N);
+  return copy_bytes(M, N) + copy_bytes(M, K) + copy_bytes(N, K) + db_bytes(M, N);
 }
 
 size_t linear_bwd_workspace_needed(const LinearBwdArgs& a) {
   const bool products = a.dx || a.dw;
-  size_t n = a.db ? db_bytes(a.N) : 0;
+  size_t n = a.db ? db_bytes(a.M, a.N) : 0;
   if (products && (a.act != RLK_ACT_NONE || !tma_rows(a.dy, a.lddy))) n += copy_bytes(a.M, a.N);
   if (a.dx && !tma_rows(a.w, a.ldw)) n += copy_bytes(a.N, a.K);
   if (a.dw && (a.ck.codes || !tma_rows(a.x, a.ldx))) n += copy_bytes(a.M, a.K);
@@ -1132,15 +1137,14 @@ cudaError_t launch_linear_bwd(const LinearBwdArgs& a, cudaStream_t stream) {
     float* part = nullptr;
     if (a.db) {
       part = reinterpret_cast<float*>(ws);
-      ws += db_bytes(a.N);
+      ws += db_bytes(a.M, a.N);
     }
     const int64_t pitch = pad8(a.N);
     const bool vec = tma_rows(a.dy, a.lddy) && (a.act == RLK_ACT_NONE || tma_rows(a.z, a.ldz));
     const unsigned cols = (unsigned)((a.N + DT * (vec ? 8 : 1) - 1) / (DT * (vec ? 8 : 1)));
-    // about 8 CTAs an SM, each with DZ_ROWS rows or more
-    int64_t parts = ((int64_t)sm_count() * 8 + cols - 1) / cols, most = (a.M + DZ_ROWS - 1) / DZ_ROWS;
+    // about 8 CTAs an SM
+    int64_t parts = ((int64_t)sm_count() * 8 + cols - 1) / cols, most = db_parts_most(a.M);
     if (parts > most) parts = most;
-    if (parts > kDbParts) parts = kDbParts;
     const dim3 grid(cols, (unsigned)parts);
     auto kernel = vec ? (a.act == RLK_ACT_GELU   ? linear_dz_kernel<8, RLK_ACT_GELU>
                          : a.act == RLK_ACT_SILU ? linear_dz_kernel<8, RLK_ACT_SILU>

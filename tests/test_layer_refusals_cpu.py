@@ -1,5 +1,6 @@
-"""Refusals of pointers that the layer operators' kernels read or write four bytes
-at a time: a misaligned one is an invalid argument, on the host."""
+"""What the layers' entry points accept, on the host: a misaligned pointer to what the
+kernels read or write four bytes at a time is an invalid argument, and a linear
+layer's backward needs the workspace that it uses and no more."""
 import ctypes
 
 import pytest
@@ -49,3 +50,20 @@ def test_preference_loss(lib, at):
     config = ctypes.byref(rlk.PrefConfig(0, 0.1, 0.0, 0.0, 0))
     assert lib.rlk_preference_loss(FAKE, FAKE, None, FAKE, 2, 50, config, p["loss"], p["grad"], p["reward"], p["stats"],
                                    FAKE, 1 << 20, None) == (1 if at else 4)
+
+
+def linear_bwd(lib, M, N, K, ws_bytes, dx=FAKE, dw=FAKE, db=FAKE):
+    """Aligned operands, no activation: nothing is copied."""
+    pad = (N + 7) // 8 * 8, (K + 7) // 8 * 8
+    return lib.rlk_linear_bwd(FAKE, pad[0], FAKE, pad[1], None, FAKE, pad[1], None, 0, M, N, K, 0, dx, 0, pad[1], dw, 1,
+                              pad[1], db, 0, FAKE, ws_bytes, None)
+
+
+@pytest.mark.parametrize("M,N", [(1, 64), (5, 1 << 20), (64, 4099), (1215, 4096), (1216, 4096), (1217, 4096), (16384, 4096)])
+def test_the_bias_gradients_partial_sums_take_rows_into_account(lib, M, N):
+    """A partial sum covers four rows or more, and there are 304 at most."""
+    most = min(304, -(-M // 4)) * ((N + 7) // 8 * 8) * 4
+    need = -(-most // 256) * 256
+    assert linear_bwd(lib, M, N, 64, need) == 4 and linear_bwd(lib, M, N, 64, need - 1) == 3
+    copies = sum(-(-rows * ((cols + 7) // 8 * 8) * 2 // 256) * 256 for rows, cols in ((M, N), (M, 64), (N, 64)))
+    assert lib.rlk_workspace_size(rlk.OP_LINEAR_BWD, M, N, 64) == copies + need
