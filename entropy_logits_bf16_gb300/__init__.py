@@ -1106,6 +1106,12 @@ def _bf16(t, name, shape=None):
     return ld
 
 
+def _copied(rows, cols, ptr, ld):
+    """Bytes of the workspace for the copy that a product's bf16 operand needs when
+    its rows do not start on 16-byte boundaries."""
+    return 0 if ptr % 16 == 0 and ld % 8 == 0 else -(-rows * (-(-cols // 8) * 16) // 256) * 256
+
+
 def linear(x: torch.Tensor, weight: torch.Tensor, bias=None, residual=None, *,
            activation: int = ACT_NONE, return_preact: bool = False, out=None, out_dtype=None,
            workspace=None):
@@ -1130,8 +1136,9 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias=None, residual=None, *,
         ydt, ldy = _matrix(out, "out", (M, N))
     z = torch.empty((M, N), dtype=torch.bfloat16, device=dev) if return_preact else None
     px, pw = x.data_ptr(), weight.data_ptr()
-    if workspace is None and (px % 16 or ldx % 8 or pw % 16 or ldw % 8):
-        workspace = torch.empty(lib.rlk_workspace_size(OP_LINEAR, M, N, K), dtype=torch.uint8, device=dev)
+    if workspace is None and M > 4:   # fewer rows are not copied
+        need = _copied(M, K, px, ldx) + _copied(N, K, pw, ldw)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     code = lib.rlk_linear_fwd(px, ldx, pw, ldw, _ptr(bias), bdt, _ptr(residual), ldr, M, N, K, activation,
                               out.data_ptr(), ydt, ldy, _ptr(z), N, _ptr(workspace),
                               0 if workspace is None else workspace.numel(), _stream(dev))
@@ -1173,15 +1180,26 @@ def linear_backward(dy: torch.Tensor, x, weight: torch.Tensor, preact=None, *,
     if grad_bias is not None and (grad_bias.dtype != torch.float32 or grad_bias.numel() != N
                                   or not grad_bias.is_contiguous()):
         raise ValueError("grad_bias must be contiguous fp32 [N]")
-    if workspace is None:
-        workspace = torch.empty(int(lib.rlk_workspace_size(OP_LINEAR_BWD, M, N, K)), device=dev,
-                                dtype=torch.uint8)
+    px = None if x is None or kept else x.data_ptr()
+    if workspace is None and M > 0:   # what this call uses: copies of operands, partial sums of the bias gradient
+        all_copies = _copied(M, N, 1, 0) + _copied(N, K, 1, 0) + _copied(M, K, 1, 0)
+        need = 0
+        if grad_bias is not None:
+            need += lib.rlk_workspace_size(OP_LINEAR_BWD, M, N, K) - all_copies
+        if dx is not None or grad_weight is not None:
+            need += _copied(M, N, dy.data_ptr() if activation == ACT_NONE else 1, lddy)
+        if dx is not None:
+            need += _copied(N, K, weight.data_ptr(), ldw)
+        if grad_weight is not None:
+            need += _copied(M, K, px or 1, ldx)
+        workspace = torch.empty(need, device=dev, dtype=torch.uint8) if need else None
     ck = None if kept is None else kept.buffers()
     _check("rlk_linear_bwd",
-           lib.rlk_linear_bwd(_ptr(dy), lddy, None if kept else _ptr(x), ldx, ck, _ptr(weight), ldw,
+           lib.rlk_linear_bwd(_ptr(dy), lddy, px, ldx, ck, _ptr(weight), ldw,
                               _ptr(preact), ldz, M, N, K, int(activation), _ptr(dx), xdt, K,
                               _ptr(grad_weight), wdt, ldgw, _ptr(grad_bias), int(bool(accumulate)),
-                              _ptr(workspace), workspace.numel(), _stream(dev)))
+                              _ptr(workspace), 0 if workspace is None else workspace.numel(),
+                              _stream(dev)))
     return dx, grad_weight, grad_bias
 
 

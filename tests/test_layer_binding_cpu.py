@@ -105,3 +105,45 @@ def test_output_types_are_refused_like_inputs():
                                                out=cuda(4, 64, dtype=torch.float16))):
         with pytest.raises(ValueError):
             call()
+
+
+def laid_out(rows, cols, how):
+    """bf16 rows that start on 16-byte boundaries, or whose stride or base is off them."""
+    if how == "aligned":
+        return cuda(rows, cols + 8 - cols % 8, dtype=BF)[:, :cols]
+    return cuda(rows, cols + 1, dtype=BF)[:, :cols] if how == "stride" else cuda(rows, cols + 16 - cols % 8, dtype=BF)[:, 3:3 + cols]
+
+
+def exactly(real, seen):
+    """The entry point with the workspace given, and with a byte less."""
+    def call(*a):
+        *head, ws, size, stream = a
+        seen.append(size)
+        if size:
+            assert real(*head, ws, size - 1, stream) == 3
+        return real(*a)
+    return call
+
+
+@pytest.mark.parametrize("M", [1, 4, 5, 33])
+@pytest.mark.parametrize("N,K", [(96, 130), (31, 64)])
+@pytest.mark.parametrize("x_how", ["aligned", "stride", "base"])
+@pytest.mark.parametrize("w_how", ["aligned", "stride", "base"])
+def test_linear_asks_for_the_workspace_that_it_uses(lib, monkeypatch, M, N, K, x_how, w_how):
+    seen = []
+    monkeypatch.setattr(lib, "rlk_linear_fwd", exactly(lib.rlk_linear_fwd, seen))
+    monkeypatch.setattr(lib, "rlk_linear_bwd", exactly(lib.rlk_linear_bwd, seen))
+    x, w = laid_out(M, K, x_how), laid_out(N, K, w_how)
+    with pytest.raises(rlk.RlkError) as e:
+        rlk.linear(x, w)
+    assert e.value.code == 4 and (seen[-1] > 0) == (M > 4 and (x_how, w_how) != ("aligned", "aligned"))
+    kept = rlk.Checkpoint(cuda(M, -(-K // 16) * 16, dtype=torch.int8), cuda(M, 16, dtype=torch.uint8), M, K)
+    for act in (rlk.ACT_NONE, rlk.ACT_GELU):
+        for dy_how in ("aligned", "stride"):
+            for wants in range(1, 8):
+                for src in (x, kept):
+                    dy, z = laid_out(M, N, dy_how), cuda(M, N, dtype=BF) if act else None
+                    with pytest.raises(rlk.RlkError) as e:
+                        rlk.linear_backward(dy, src, w, z, activation=act, want_x_grad=bool(wants & 1),
+                                            want_weight_grad=bool(wants & 2), want_bias_grad=bool(wants & 4))
+                    assert e.value.code == 4
