@@ -424,10 +424,12 @@ __global__ void __launch_bounds__(Shape<SPLIT>::THREADS, SPLIT ? 2 : 1)
           if (++stage == stages) { stage = 0; phase ^= 1u; }
         }
       }
-      if ((!ok || *abort_flag) && leader) {   // let every issued copy land before the CTAs exit
+      // Every copy lands before the CTAs exit (bounded), also when another role's wait runs
+      // out only after the last copy was asked for.  (A pair's odd CTA may have asked for
+      // stages that the even one no longer did; after that its own roles wait out the limit.)
+      if (leader)
         for (int s = 0; s < stages; ++s)
           if (used & (1u << s)) tc::drain(full0 + 8 * s, (last_parity >> s) & 1u);
-      }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------ MMA issuer
