@@ -332,15 +332,13 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
         }
       }
-      // If any role gave up, let every issued copy land before the CTA exits
-      // (each wait bounded).
-      if (!ok || *abort_flag) {
-        for (int s2 = 0; s2 < STAGES; ++s2) {
-          if (!(issued_mask & (1u << s2))) continue;
-          const uint32_t par = (issued_parity >> s2) & 1u;
-          for (uint32_t i = 0; i < SPIN_LIMIT; ++i)
-            if (mbar_try_wait(full0 + 8 * s2, par)) break;
-        }
+      // Every issued copy lands before the CTA exits (each wait bounded), also when
+      // another role gives up only after the last copy was issued.
+      for (int s2 = 0; s2 < STAGES; ++s2) {
+        if (!(issued_mask & (1u << s2))) continue;
+        const uint32_t par = (issued_parity >> s2) & 1u;
+        for (uint32_t i = 0; i < SPIN_LIMIT; ++i)
+          if (mbar_try_wait(full0 + 8 * s2, par)) break;
       }
     }
   } else if (warp == 1) {
@@ -689,13 +687,12 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (++stage == GSTAGES) { stage = 0; phase ^= 1u; }
         }
       }
-      if (!ok || *abort_flag) {   // let every issued copy land before the CTA exits
-        for (int s2 = 0; s2 < GSTAGES; ++s2) {
-          if (!(issued_mask & (1u << s2))) continue;
-          const uint32_t par = (issued_parity >> s2) & 1u;
-          for (uint32_t i = 0; i < SPIN_LIMIT; ++i)
-            if (mbar_try_wait(full0 + 8 * s2, par)) break;
-        }
+      // as above: every issued copy lands before the CTA exits
+      for (int s2 = 0; s2 < GSTAGES; ++s2) {
+        if (!(issued_mask & (1u << s2))) continue;
+        const uint32_t par = (issued_parity >> s2) & 1u;
+        for (uint32_t i = 0; i < SPIN_LIMIT; ++i)
+          if (mbar_try_wait(full0 + 8 * s2, par)) break;
       }
     }
   } else if (warp == 1) {
