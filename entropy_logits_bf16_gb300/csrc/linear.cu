@@ -91,7 +91,7 @@ struct Epilogue {
 struct GemmParams {
   int64_t M, N;
   int n_mt, n_nt, k_steps;
-  int first_tile, n_tiles;   // tiles [first_tile, n_tiles) of the n_mt x n_nt
+  int n_tiles;               // n_mt x n_nt
   int stages;
   long long wait_limit;
   int withhold;              // debug: the stage of the first CTA whose barrier waits for an arrival that never comes (-1: none)
@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(Shape<SPLIT>::THREADS, SPLIT ? 2 : 1)
   // SPLIT: which share of K; else: which half of the tile
   const uint32_t rank = tc::cluster_rank();
   const int per = SPLIT ? cluster : G;   // CTAs that work on one tile
-  const int tile0 = p.first_tile + (int)(blockIdx.x / (unsigned)per);
+  const int tile0 = (int)(blockIdx.x / (unsigned)per);
   const int tile_step = SPLIT ? p.n_tiles : (int)(gridDim.x / G);
   const int k0 = SPLIT ? (int)((int64_t)rank * p.k_steps / cluster) : 0;
   const int k1 = SPLIT ? (int)((int64_t)(rank + 1) * p.k_steps / cluster) : p.k_steps;
@@ -966,13 +966,12 @@ int split_for(int tiles, int k_steps) {
   return s;
 }
 
-// One launch over tiles [p.first_tile, p.n_tiles), as a programmatic dependent
-// of the kernel before it.
+// One launch over the tiles, as a programmatic dependent of the kernel before it.
 template <bool A_MN, bool B_MN, bool SPLIT>
 cudaError_t launch_gemm(const CUtensorMap& ma, const CUtensorMap& mb, GemmParams p, int split,
                         cudaStream_t stream) {
   if (cudaError_t e = set_smem<A_MN, B_MN, SPLIT>(); e != cudaSuccess) return e;
-  const int tiles = p.n_tiles - p.first_tile;
+  const int tiles = p.n_tiles;
   cudaLaunchConfig_t cfg{};
   const int pairs = sm_count() / 2;
   cfg.gridDim = dim3((unsigned)(SPLIT ? tiles * split : 2 * (tiles < pairs ? tiles : pairs)));
