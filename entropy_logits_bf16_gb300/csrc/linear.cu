@@ -98,26 +98,30 @@ struct GemmParams {
   Epilogue e;
 };
 
-// 1 / v to 2^-22 or so (MUFU), enough for what is rounded to bf16 or compared
-// at a few 2^-24 of |z| + 1.
+// 1 / v to 2^-23 (MUFU; a result below 2^-126 is 0).
 __device__ __forceinline__ float rcp(float v) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
 
-// Phi(-|z|), Phi the normal distribution function: 1/2 erfc(|z| / sqrt 2) by
-// Abramowitz and Stegun 7.1.26, erfc(x) = (a1 t + ... + a5 t^5) exp(-x^2) with t = 1 / (1 + p x)
-// (absolute error 1.5e-7), two numbers an instruction; the product with the exponential keeps
-// the far tail free of cancellation.  `bell`: exp(-z^2 / 2).
+// Phi(-|z|), Phi the normal distribution function, two numbers an instruction, to a
+// relative (2 z^2 + 24) 2^-24 (half an ulp of z alone moves it by z^2 2^-24):
+// Phi(-|z|) = t q(t) exp(-z^2 / 2) with t = 1 / (1 + 0.305 |z|).  t q(t) is half the scaled
+// complementary error function erfcx(|z| / sqrt 2); q is its minimax fit in t, by relative
+// error (9.4e-8) over |z| <= 13.3, beyond which the exponential is below 2^-126 and is 0.
+// `bell`: exp(-z^2 / 2).
 __device__ __forceinline__ float2 normal_tail(float2 z, float2& bell) {
-  const float2 x = mul2(make_float2(fabsf(z.x), fabsf(z.y)), both(0.70710678118654752f));
-  const float2 d = fma2(both(0.3275911f), x, both(1.f)), t = make_float2(rcp(d.x), rcp(d.y));
-  float2 q = fma2(both(0.5f * 1.061405429f), t, both(0.5f * -1.453152027f));
-  q = fma2(q, t, both(0.5f * 1.421413741f));
-  q = fma2(q, t, both(0.5f * -0.284496736f));
-  q = fma2(q, t, both(0.5f * 0.254829592f));
-  const float2 e = mul2(mul2(x, x), both(-kLog2e));
+  const float2 d = fma2(make_float2(fabsf(z.x), fabsf(z.y)), both(0.305f), both(1.f));
+  const float2 t = make_float2(rcp(d.x), rcp(d.y));
+  float2 q = fma2(both(0.0366991907f), t, both(-0.1529883f));
+  q = fma2(q, t, both(0.185716853f));
+  q = fma2(q, t, both(-0.0379767865f));
+  q = fma2(q, t, both(0.121021658f));
+  q = fma2(q, t, both(0.103420876f));
+  q = fma2(q, t, both(0.122466817f));
+  q = fma2(q, t, both(0.121639736f));
+  const float2 e = mul2(mul2(z, z), both(-0.5f * kLog2e));
   bell = make_float2(ex2(e.x), ex2(e.y));
   return mul2(mul2(q, t), bell);
 }
@@ -126,7 +130,7 @@ __device__ __forceinline__ float2 normal_below(float2 z, float2 tail) {
   const float2 up = fma2(tail, both(-1.f), both(1.f));
   return make_float2(z.x > 0.f ? up.x : tail.x, z.y > 0.f ? up.y : tail.y);
 }
-// 1 / (1 + exp(-z)).
+// 1 / (1 + exp(-z)), to a relative (2 |z| + 24) 2^-24.
 __device__ __forceinline__ float2 logistic(float2 z) {
   const float2 e = mul2(z, both(-kLog2e)), d = add2(make_float2(ex2(e.x), ex2(e.y)), both(1.f));
   return make_float2(rcp(d.x), rcp(d.y));
@@ -155,7 +159,7 @@ __device__ __forceinline__ void activate(float (&v)[W], int act) {
     for (int j = 0; j < W; ++j) v[j] = v[j] < 0.f ? 0.f : v[j];
   }
 }
-// act'(z), to a few 2^-24.
+// act'(z), to the same.
 template <int ACT>
 __device__ __forceinline__ float2 activation_slope(float2 z) {
   if (ACT == RLK_ACT_GELU) {   // Phi(z) + z phi(z)

@@ -972,6 +972,8 @@ typedef enum {
  *                  aligned, contents on entry do not matter; else it may be NULL.
  * Deterministic.  Calls of few rows split K over several CTAs, so a row's last
  * bits may differ between calls of a different M (never between runs).
+ * act is taken of the fp32 z to a relative (2 z^2 + 24) 2^-24 (GELU) or
+ * (2 |z| + 24) 2^-24 (SiLU); where it would be below 2^-126 or so it is 0.
  * NaN and infinities propagate as in the formula.  Tiles of y and z whose
  * operands did not come within the limit of a wait (about a second) are NaN.
  * Errors: RLK_ERR_INVALID_ARG for sizes or strides outside the rules, bad
