@@ -64,6 +64,14 @@ __device__ __forceinline__ float inv_sqrt(float v) {
   return isfinite(e) ? __fmaf_rn(__fmul_rn(0.5f, r), e, r) : r;
 }
 
+// sum / n by the rounded reciprocal and one correction: the nearest fp32, or next to it,
+// and exact where the quotient is.  (The product alone may be an ulp off the mean of a
+// constant row, which eps then divides: y of +-0.5 where 29952 fills 1000 columns.)
+__device__ __forceinline__ float mean_of(float sum, float n, float inv_n) {
+  const float q = __fmul_rn(sum, inv_n);
+  return __fmaf_rn(__fmaf_rn(-q, n, sum), inv_n, q);
+}
+
 // Sum over the CTA in a fixed order, on every thread.
 template <int NW>
 __device__ __forceinline__ float cta_sum(float v, float* s_red) {
@@ -90,7 +98,7 @@ __global__ void __launch_bounds__(WT) norm_fwd_wide_kernel(NormArgs a) {
     float m = 0.f, s = 0.f;
     if (!a.rms) {
       for (int64_t c = tid; c < a.H; c += WT) s = __fadd_rn(s, ld_elem(a.x, a.dtype, x0 + c));
-      m = __fmul_rn(cta_sum<WT / 32>(s, s_red), inv_h);
+      m = mean_of(cta_sum<WT / 32>(s, s_red), (float)a.H, inv_h);
       s = 0.f;
     }
     for (int64_t c = tid; c < a.H; c += WT) {
@@ -652,7 +660,7 @@ __global__ void __maxnreg__((regs_of<VW, E>())) norm_fwd_kernel(NormArgs a, int 
       }
       group_sum(m, g, s_red, buf);
 #pragma unroll
-      for (int q = 0; q < R; ++q) m[q] = __fmul_rn(m[q], inv_h);
+      for (int q = 0; q < R; ++q) m[q] = mean_of(m[q], (float)H, inv_h);
     }
 #pragma unroll
     for (int q = 0; q < R; ++q) {
