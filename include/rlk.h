@@ -912,7 +912,8 @@ rlk_status rlk_norm_fwd(const void* x, rlk_dtype dtype, int64_t T, int64_t H, in
  *   grad_x = r_t (g - mean(g) - h mean(g h))      (RLK_NORM_RMS: without mean(g)),
  *   grad_weight (+)= sum_t dy h,   grad_bias (+)= sum_t dy,
  * in fp32, each output rounded once.  The parameter gradients are summed in an
- * order that depends on T and H only: the same bits on every run.
+ * order that depends on T, H and the layout (whether every row and the weight start on
+ * 16-byte boundaries): the same bits on every run of a call, not between layouts.
  *
  * Arguments
  *  dy              device, dy_dtype, T x lddy elements (rlk_lmhead_logprob_bwd's
@@ -1007,8 +1008,10 @@ rlk_status rlk_linear_fwd(const void* x, int64_t ldx, const void* w, int64_t ldw
  *  accumulate      non-zero: grad_w (RLK_F32 only) and grad_bias are added to.
  *  workspace       at least rlk_workspace_size(RLK_OP_LINEAR_BWD, M, N, K) bytes,
  *                  16-byte aligned; contents on entry do not matter.
- * Deterministic for given sizes.  A call that needs less than the size above
+ * Deterministic for given sizes and layout (rows off 16-byte boundaries sum grad_bias
+ * in another order).  A call that needs less than the size above
  * (bf16 operands with 16-byte rows and no activation need no copies) accepts less.
+ * A checkpoint is unpacked into the workspace as a whole, 2 M K bytes while the call runs.
  * Tiles of grad_x and grad_w whose operands did not come in time are NaN.
  * Errors: as rlk_linear_fwd; RLK_ERR_UNSUPPORTED for accumulate with a bf16
  *  grad_w.  M == 0 zeroes grad_w and grad_bias (or leaves them, accumulating).
