@@ -943,14 +943,15 @@ class Checkpoint:
     def buffers(self):
         """A reference to the rlk_checkpoint of the tensors as they are now."""
         codes, scales, (T, H) = self.codes, self.scales, self.shape
-        _need_cuda(codes, scales)
-        if codes.dtype != torch.int8 or scales.dtype != torch.uint8:
+        if not (codes.is_cuda and scales.is_cuda):
+            raise ValueError("librlk operates on CUDA tensors only")
+        if codes.dtype is not torch.int8 or scales.dtype is not torch.uint8:
             raise ValueError("codes must be int8, scales uint8")
-        if (codes.dim() != 2 or scales.dim() != 2 or codes.shape[0] != T or scales.shape[0] != T
-                or codes.shape[1] < H or scales.shape[1] * CHECKPOINT_BLOCK < H
+        a, b = codes.shape, scales.shape
+        if (len(a) != 2 or len(b) != 2 or a[0] != T or b[0] != T or a[1] < H or b[1] * CHECKPOINT_BLOCK < H
                 or not codes.is_contiguous() or not scales.is_contiguous()):
             raise ValueError("codes and scales must be contiguous [T, >= H] and [T, >= ceil(H / 32)]")
-        return ctypes.byref(CheckpointBuffers(codes.data_ptr(), scales.data_ptr(), codes.shape[1], scales.shape[1]))
+        return ctypes.byref(CheckpointBuffers(codes.data_ptr(), scales.data_ptr(), a[1], b[1]))
 
 
 def new_checkpoint(T: int, H: int, device) -> Checkpoint:
