@@ -59,7 +59,7 @@ constexpr int MAX_SPLIT = 4;                   // CTAs that share a tile's K, at
 // CTAs than SMs, so that two share an SM and one's epilogue runs beside the other's
 // products).  The pair's 16 epilogue warps take the sixth stage's room: with eight,
 // and six stages, products of a short K waited on the epilogue (16384 x 4096 x 512
-// with GELU 138 us, now 98; K 4096 the same within its noise).
+// with GELU 138 us against 98, 102 with the GELU of now; K 4096 the same within its noise).
 constexpr int BROWS = 128;
 constexpr uint32_t A_BYTES = BM * BK * 2, STAGE_BYTES = A_BYTES + BROWS * BK * 2;
 template <bool SPLIT>
