@@ -33,6 +33,7 @@ OP_LINEAR, OP_LINEAR_BWD = 9, 10
 ACT_NONE, ACT_GELU, ACT_SILU, ACT_RELU = 0, 1, 2, 3
 PREF_SIGMOID, PREF_IPO, PREF_HINGE = 0, 1, 2
 PREF_NSTATS = 6
+MAX_TOKENS, MAX_ALTERNATIVES = 1024, 128   # of a row in token_logprobs
 PREF_STAT_NAMES = ("loss", "pairs", "accuracy", "margin", "chosen", "rejected")
 NORM_LAYER, NORM_RMS = 0, 1
 CHECKPOINT_BLOCK = 32   # columns that share one checkpoint scale
@@ -81,7 +82,7 @@ EXPORTS = ("rlk_version", "rlk_status_string", "rlk_workspace_size", "rlk_logpro
            "rlk_logprob_entropy_canonical_topp",
            "rlk_grpo_loss_noalloc", "rlk_checkpoint_pack", "rlk_checkpoint_unpack",
            "rlk_norm_fwd", "rlk_norm_bwd", "rlk_preference_loss", "rlk_linear_fwd",
-           "rlk_linear_bwd")
+           "rlk_linear_bwd", "rlk_token_logprobs_fwd", "rlk_token_logprobs_bwd")
 NOALLOC_MAX_SEQ = 16384
 DEBUG_EXPORTS = ("rlk_lmhead_logits_debug", "rlk_debug_inject_launch_failures",
                  "rlk_debug_set_wait_limit", "rlk_debug_withhold_copy",
@@ -219,6 +220,12 @@ def load(path: str | None = None):
                                        ctypes.c_int, vp, ctypes.c_int, i64, vp, ctypes.c_int, i64, vp,
                                        ctypes.c_int, vp, sz, vp]
         lib.rlk_linear_bwd.restype = ctypes.c_int
+        lib.rlk_token_logprobs_fwd.argtypes = [vp, ctypes.c_int, i64, i64, i64, vp, i32, f32, i32, vp, vp,
+                                               vp, vp, vp, vp, vp]
+        lib.rlk_token_logprobs_fwd.restype = ctypes.c_int
+        lib.rlk_token_logprobs_bwd.argtypes = [vp, ctypes.c_int, i64, i64, i64, vp, i32, f32, vp, vp, vp,
+                                               vp, i32, vp, vp, ctypes.c_int, i64, vp, vp]
+        lib.rlk_token_logprobs_bwd.restype = ctypes.c_int
         _lib = lib
         return lib
 
@@ -1283,6 +1290,125 @@ def preference_loss(logp, logp_ref, seq_offsets, *, loss_mask=None, loss_type: i
                                    _stream(dev))
     _check("rlk_preference_loss", code)
     return loss, grad, reward, stats
+
+
+# ------------------------------------------------------------ given tokens and alternatives
+def new_token_state(T: int, device) -> torch.Tensor:
+    """Room for what ``token_logprobs`` keeps for its backward (rlk_token_state[T])."""
+    return torch.empty((T, 4), dtype=torch.float32, device=device)
+
+
+def _token_state(state, T):
+    if state.dtype != torch.float32 or state.shape != (T, 4) or not state.is_contiguous():
+        raise ValueError("state must come from new_token_state(T)")
+
+
+def _token_ids(token_ids, T):
+    """Tokens a row of contiguous int32 [T] or [T, C] ids."""
+    if token_ids is None:
+        return 0
+    if (token_ids.dtype != torch.int32 or not token_ids.is_contiguous() or token_ids.dim() not in (1, 2)
+            or token_ids.shape[0] != T):
+        raise ValueError("token_ids must be contiguous int32 [T] or [T, C]")
+    return 1 if token_ids.dim() == 1 else token_ids.shape[1]
+
+
+def token_logprobs(logits: torch.Tensor, token_ids, temperature: float = 1.0, *, n_top: int = 0,
+                   state: torch.Tensor | None = None, status_word=None):
+    """Log-probabilities of given tokens over the whole vocabulary, the entropy
+    and the ``n_top`` largest alternatives of each row of logits (CUDA [T, V]
+    bf16 or fp32, rows may be strided; -inf rules a token out).  ``token_ids``:
+    CUDA int32 [T], [T, C] (-1: an empty place) or None.  Returns (logprob shaped
+    like token_ids or None, entropy [T], top_ids int32 [T, n_top] or None, their
+    log-probabilities or None).  ``state`` (from ``new_token_state``) receives
+    what ``token_logprobs_backward`` needs."""
+    lib = load()
+    _need_cuda(logits, token_ids, state, status_word)
+    dt = _logits_dtype(logits)
+    T, V = logits.shape
+    C = _token_ids(token_ids, T)
+    if state is not None:
+        _token_state(state, T)
+    dev = logits.device
+    f32 = torch.float32
+    lp = None if token_ids is None else torch.empty(token_ids.shape, dtype=f32, device=dev)
+    ent = torch.empty(T, dtype=f32, device=dev)
+    ids = torch.empty((T, n_top), dtype=torch.int32, device=dev) if n_top else None
+    top = torch.empty((T, n_top), dtype=f32, device=dev) if n_top else None
+    code = lib.rlk_token_logprobs_fwd(logits.data_ptr(), dt, T, V, logits.stride(0) if T > 1 else V,
+                                      _ptr(token_ids), C, temperature, n_top, _ptr(lp), ent.data_ptr(),
+                                      _ptr(ids), _ptr(top), _ptr(state), _ptr(status_word), _stream(dev))
+    _check("rlk_token_logprobs_fwd", code)
+    return lp, ent, ids, top
+
+
+def token_logprobs_backward(logits: torch.Tensor, token_ids, temperature: float, state: torch.Tensor,
+                            grad_logprob=None, grad_entropy=None, *, top_ids=None, grad_top=None,
+                            out=None, grad_dtype=None, status_word=None):
+    """dL/dlogits [T, V] of ``token_logprobs`` for the gradients of its outputs
+    (fp32, each or None); ``top_ids`` from the forward with ``grad_top``.
+    ``grad_dtype`` (bf16 or fp32) defaults to the logits' dtype; ``out`` may be
+    a strided [T, V] tensor."""
+    lib = load()
+    _need_cuda(logits, token_ids, state, grad_logprob, grad_entropy, top_ids, grad_top, out, status_word)
+    dt = _logits_dtype(logits)
+    T, V = logits.shape
+    C = _token_ids(token_ids, T)
+    _token_state(state, T)
+    if grad_logprob is not None and (token_ids is None or grad_logprob.dtype != torch.float32
+                                     or grad_logprob.shape != token_ids.shape or not grad_logprob.is_contiguous()):
+        raise ValueError("grad_logprob must be contiguous fp32, shaped like token_ids")
+    if grad_entropy is not None:
+        _vector(grad_entropy, T, "grad_entropy")
+    n_top = 0
+    if grad_top is not None:
+        if (top_ids is None or top_ids.dtype != torch.int32 or top_ids.dim() != 2 or top_ids.shape[0] != T
+                or not top_ids.is_contiguous()):
+            raise ValueError("grad_top needs top_ids, contiguous int32 [T, n_top]")
+        if grad_top.dtype != torch.float32 or grad_top.shape != top_ids.shape or not grad_top.is_contiguous():
+            raise ValueError("grad_top must be contiguous fp32, shaped like top_ids")
+        n_top = top_ids.shape[1]
+    if out is None:
+        out = torch.empty((T, V), dtype=grad_dtype or logits.dtype, device=logits.device)
+    elif grad_dtype is not None and out.dtype != grad_dtype:
+        raise ValueError("out must be of grad_dtype")
+    gd, ldg = _matrix(out, "out", (T, V))
+    code = lib.rlk_token_logprobs_bwd(logits.data_ptr(), dt, T, V, logits.stride(0) if T > 1 else V,
+                                      _ptr(token_ids), C, temperature, state.data_ptr(), _ptr(grad_logprob),
+                                      _ptr(grad_entropy), _ptr(top_ids) if n_top else None, n_top,
+                                      _ptr(grad_top), out.data_ptr(), gd, ldg, _ptr(status_word),
+                                      _stream(logits.device))
+    _check("rlk_token_logprobs_bwd", code)
+    return out
+
+
+class _TokenLogprobs(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, token_ids, temperature, n_top):
+        state = new_token_state(logits.shape[0], logits.device)
+        lp, ent, ids, top = token_logprobs(logits, token_ids, temperature, n_top=n_top, state=state)
+        ctx.save_for_backward(logits, token_ids, state, ids)
+        ctx.temperature = temperature
+        ctx.set_materialize_grads(False)
+        if ids is not None:
+            ctx.mark_non_differentiable(ids)
+        return lp, ent, ids, top
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, g_lp, g_ent, _, g_top):
+        logits, token_ids, state, ids = ctx.saved_tensors
+        if g_lp is None and g_ent is None and g_top is None:
+            return None, None, None, None
+        flat = lambda g: None if g is None else g.contiguous()
+        g = token_logprobs_backward(logits, token_ids, ctx.temperature, state, flat(g_lp), flat(g_ent),
+                                    top_ids=ids, grad_top=flat(g_top))
+        return g, None, None, None
+
+
+def token_logprobs_autograd(logits: torch.Tensor, token_ids, temperature: float = 1.0, *, n_top: int = 0):
+    """``token_logprobs`` as a differentiable op."""
+    return _TokenLogprobs.apply(logits, token_ids, temperature, n_top)
 
 
 def inject_launch_failures(n: int) -> int:

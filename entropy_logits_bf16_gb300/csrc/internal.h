@@ -266,6 +266,43 @@ struct PrefArgs {
 size_t pref_workspace_bytes(int64_t n_tok, int64_t n_pairs);
 cudaError_t launch_preference_loss(PrefArgs a, void* workspace, cudaStream_t stream);
 
+// Log-probabilities of given tokens, entropy and top alternatives (token_logprobs.cu).
+struct TokenArgs {
+  const void* logits;
+  int dtype;            // 0 bf16, 1 fp32
+  int64_t T, V, ld;
+  const int32_t* ids;   // [T][C]
+  int C;
+  float temperature;
+  int top;
+  float* out_logprob;   // [T][C]
+  float* out_entropy;   // [T] or NULL
+  int32_t* out_top_ids;     // [T][top]
+  float* out_top_logprob;   // [T][top]
+  float* state;         // [T][4] (largest logit, log2 S, H, temperature) or NULL
+  uint32_t* status;
+};
+struct TokenBwdArgs {
+  const void* logits;
+  int dtype;
+  int64_t T, V, ld;
+  const int32_t* ids;
+  int C;
+  float temperature;
+  const float* state;
+  const float* grad_logprob;   // [T][C] or NULL
+  const float* grad_entropy;   // [T] or NULL
+  const int32_t* top_ids;      // [T][top]
+  int top;
+  const float* grad_top;       // [T][top]
+  void* grad;
+  int grad_dtype;
+  int64_t ldg;
+  uint32_t* status;
+};
+cudaError_t launch_token_logprobs(const TokenArgs& a, cudaStream_t stream);
+cudaError_t launch_token_logprobs_backward(const TokenBwdArgs& a, cudaStream_t stream);
+
 // Matrix product with a fused epilogue and its backward (linear.cu).
 struct LinearArgs {
   const void* x;

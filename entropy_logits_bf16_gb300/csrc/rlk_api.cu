@@ -1141,6 +1141,97 @@ rlk_status rlk_preference_loss(const float* logp, const float* logp_ref, const u
              : RLK_ERR_CUDA;
 }
 
+namespace {
+
+bool token_sizes_ok(const void* logits, rlk_dtype dtype, int64_t T, int64_t V, int64_t ld,
+                    int32_t n_tokens, float temperature, int32_t n_top) {
+  return good_dtype(dtype) && T >= 0 && T <= (int64_t(1) << 27) && V >= 1 && V <= (int64_t(1) << 24) && ld >= V &&
+         n_tokens >= 0 && n_tokens <= RLK_MAX_TOKENS && n_top >= 0 && n_top <= RLK_MAX_ALTERNATIVES &&
+         finite_positive(temperature) && std::isfinite(1.4426950408889634f / temperature) && elem_aligned(logits, dtype);
+}
+
+}  // namespace
+
+// The layout the Python binding mirrors.
+static_assert(sizeof(rlk_token_state) == 16, "rlk_token_state layout");
+
+rlk_status rlk_token_logprobs_fwd(const void* logits, rlk_dtype dtype, int64_t T, int64_t V,
+                                  int64_t ld, const int32_t* token_ids, int32_t n_tokens,
+                                  float temperature, int32_t n_top, float* out_logprob,
+                                  float* out_entropy, int32_t* out_top_ids,
+                                  float* out_top_logprob, rlk_token_state* out_state,
+                                  uint32_t* out_status_word, rlk_stream stream) {
+  if (!token_sizes_ok(logits, dtype, T, V, ld, n_tokens, temperature, n_top)) return RLK_ERR_INVALID_ARG;
+  if (T == 0) return RLK_OK;
+  if (!logits || (n_tokens > 0 && (!token_ids || !out_logprob)) || (n_top > 0 && (!out_top_ids || !out_top_logprob)))
+    return RLK_ERR_INVALID_ARG;
+  if (!aligned_to(token_ids, 4) || !aligned_to(out_logprob, 4) || !aligned_to(out_entropy, 4) ||
+      !aligned_to(out_top_ids, 4) || !aligned_to(out_top_logprob, 4) || !aligned_to(out_state, 16) ||
+      !aligned_to(out_status_word, 4))
+    return RLK_ERR_INVALID_ARG;
+  rlk::TokenArgs a{};
+  a.logits = logits;
+  a.dtype = dtype_index(dtype);
+  a.T = T;
+  a.V = V;
+  a.ld = ld;
+  a.ids = token_ids;
+  a.C = n_tokens;
+  a.temperature = temperature;
+  a.top = n_top;
+  a.out_logprob = out_logprob;
+  a.out_entropy = out_entropy;
+  a.out_top_ids = out_top_ids;
+  a.out_top_logprob = out_top_logprob;
+  a.state = reinterpret_cast<float*>(out_state);
+  a.status = out_status_word;
+  if (rlk::take_injected_failure()) return RLK_ERR_CUDA;
+  return rlk::launch_token_logprobs(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? RLK_OK
+             : RLK_ERR_CUDA;
+}
+
+rlk_status rlk_token_logprobs_bwd(const void* logits, rlk_dtype dtype, int64_t T, int64_t V,
+                                  int64_t ld, const int32_t* token_ids, int32_t n_tokens,
+                                  float temperature, const rlk_token_state* state,
+                                  const float* grad_logprob, const float* grad_entropy,
+                                  const int32_t* top_ids, int32_t n_top, const float* grad_top,
+                                  void* grad_logits, rlk_dtype grad_dtype, int64_t ldg,
+                                  uint32_t* out_status_word, rlk_stream stream) {
+  if (!token_sizes_ok(logits, dtype, T, V, ld, n_tokens, temperature, n_top) || !good_dtype(grad_dtype) || ldg < V)
+    return RLK_ERR_INVALID_ARG;
+  if (T == 0) return RLK_OK;
+  if (!logits || !state || !grad_logits || (n_tokens > 0 && !token_ids) || (n_top > 0 && (!top_ids || !grad_top)))
+    return RLK_ERR_INVALID_ARG;
+  if (!aligned_to(token_ids, 4) || !aligned_to(state, 16) || !aligned_to(grad_logprob, 4) ||
+      !aligned_to(grad_entropy, 4) || !aligned_to(top_ids, 4) || !aligned_to(grad_top, 4) ||
+      !elem_aligned(grad_logits, grad_dtype) || !aligned_to(out_status_word, 4))
+    return RLK_ERR_INVALID_ARG;
+  rlk::TokenBwdArgs a{};
+  a.logits = logits;
+  a.dtype = dtype_index(dtype);
+  a.T = T;
+  a.V = V;
+  a.ld = ld;
+  a.ids = token_ids;
+  a.C = n_tokens;
+  a.temperature = temperature;
+  a.state = reinterpret_cast<const float*>(state);
+  a.grad_logprob = grad_logprob;
+  a.grad_entropy = grad_entropy;
+  a.top_ids = top_ids;
+  a.top = n_top;
+  a.grad_top = grad_top;
+  a.grad = grad_logits;
+  a.grad_dtype = dtype_index(grad_dtype);
+  a.ldg = ldg;
+  a.status = out_status_word;
+  if (rlk::take_injected_failure()) return RLK_ERR_CUDA;
+  return rlk::launch_token_logprobs_backward(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? RLK_OK
+             : RLK_ERR_CUDA;
+}
+
 int rlk_debug_inject_launch_failures(int n) {
   return rlk::g_injected_failures.exchange(n < 0 ? 0 : n);
 }

@@ -1091,6 +1091,102 @@ rlk_status rlk_preference_loss(const float* logp, const float* logp_ref, const u
                                float* out_reward, float* out_stats, void* workspace,
                                size_t workspace_bytes, rlk_stream stream);
 
+/*
+ * The operators of a distillation step: a teacher's top alternatives at each
+ * position (rlk_token_logprobs_fwd on its logits) are scored under the student
+ * (the same on its logits, with its backward), whose block is a gated
+ * feed-forward one (rlk_gated_linear_fwd, then rlk_linear_fwd), and the
+ * gradients of its matrices become orthogonalised updates (rlk_orthogonalise).
+ */
+
+#define RLK_MAX_TOKENS 1024        /* given tokens a row                          */
+#define RLK_MAX_ALTERNATIVES 128   /* top alternatives a row                      */
+
+/* What the forward keeps of a row for the backward (16 bytes). */
+typedef struct rlk_token_state {
+  float max_logit;     /* M                                                       */
+  float log2_sum;      /* log2 sum e^((z - M) / T)                                */
+  float entropy;       /* H                                                       */
+  float temperature;   /* T                                                       */
+} rlk_token_state;
+
+/*
+ * rlk_token_logprobs_fwd -- log-probabilities of given tokens over the whole
+ * vocabulary, the entropy, and the row's top alternatives.
+ *
+ *   p_i = e^(z_i / T) / sum_j e^(z_j / T),   logprob_c = ln p[token_c],
+ *   H = -sum_i p_i ln p_i,
+ *   alternatives: the n_top largest logits in order, equal ones by the lower id,
+ *   each with its log-probability.
+ * A logit of -inf rules its token out (p = 0, log-probability -inf, no part of
+ * H, never an alternative).  One pass over the logits; sums in fp32.
+ *
+ * Arguments
+ *  logits          device, dtype `dtype`, T x ld elements (ld >= V, unit stride
+ *                  along V; any alignment of its type).
+ *  T, V            rows; 1 <= V <= 2^24.
+ *  token_ids       device int32[T][n_tokens] (NULL when n_tokens is 0).  -1 is an
+ *                  empty place (log-probability 0); a token may be given twice.
+ *  n_tokens        0 to RLK_MAX_TOKENS, the same for every row.
+ *  temperature     finite, > 0.
+ *  n_top           0 to RLK_MAX_ALTERNATIVES.
+ *  out_logprob     device float[T][n_tokens] (NULL when n_tokens is 0).
+ *  out_entropy     device float[T] or NULL.
+ *  out_top_ids     device int32[T][n_top], out_top_logprob float[T][n_top] (NULL when
+ *                  n_top is 0).  Where a row has fewer logits above -inf, the last
+ *                  places hold -1 and -inf.
+ *  out_state       device rlk_token_state[T], 16-byte aligned, or NULL.
+ *  out_status_word device uint32[1] or NULL.  A row with a NaN or +inf, or
+ *                  without any logit above -inf, gets NaN (alternatives: -1 and
+ *                  NaN; empty places: 0) and RLK_STATUS_NONFINITE.  A token below
+ *                  -1 or not below V gets NaN and RLK_STATUS_BAD_TOKEN_ID.
+ * A row's bits depend on its values only, not on the batch, the layout or the
+ * other arguments.
+ * Errors: RLK_ERR_INVALID_ARG for sizes outside their ranges, ld < V, a bad
+ *  dtype or temperature, null or misaligned pointers.  T == 0 returns RLK_OK
+ *  without launching.
+ */
+rlk_status rlk_token_logprobs_fwd(const void* logits, rlk_dtype dtype, int64_t T, int64_t V,
+                                  int64_t ld, const int32_t* token_ids, int32_t n_tokens,
+                                  float temperature, int32_t n_top, float* out_logprob,
+                                  float* out_entropy, int32_t* out_top_ids,
+                                  float* out_top_logprob, rlk_token_state* out_state,
+                                  uint32_t* out_status_word, rlk_stream stream);
+
+/*
+ * rlk_token_logprobs_bwd -- gradient of rlk_token_logprobs_fwd.
+ *
+ * For L = sum g_c logprob_c + g_H H + sum h_j top_logprob_j, the sums over a
+ * row's tokens and alternatives:
+ *   dL/dz_i = (1 / T) [ sum_{c: token_c = i} g_c + sum_{j: top_j = i} h_j
+ *                       - p_i (sum_c g_c + sum_j h_j + g_H (ln p_i + H)) ].
+ * An empty place, and a token that is ruled out (its log-probability is -inf
+ * whatever the other logits are), has no term in it.
+ *
+ * Arguments
+ *  logits .. temperature   as in the forward (the same values).
+ *  state           device rlk_token_state[T] from the forward.
+ *  grad_logprob    device float[T][n_tokens] or NULL (0).
+ *  grad_entropy    device float[T] or NULL (0).
+ *  top_ids, n_top, grad_top   device int32[T][n_top] from the forward and float[T][n_top];
+ *                  n_top 0 for none.
+ *  grad_logits     device, grad_dtype, T x ldg elements (ldg >= V); may not overlap
+ *                  the logits.
+ *  out_status_word device uint32[1] or NULL: RLK_STATUS_BAD_TOKEN_ID, or
+ *                  RLK_STATUS_BAD_PARAM for a state of another temperature.
+ * A row that the forward could not score, with a token out of range, or whose
+ * state is of another temperature gets NaN.  No atomics: the same bits on
+ * every run.
+ * Errors: as rlk_token_logprobs_fwd.
+ */
+rlk_status rlk_token_logprobs_bwd(const void* logits, rlk_dtype dtype, int64_t T, int64_t V,
+                                  int64_t ld, const int32_t* token_ids, int32_t n_tokens,
+                                  float temperature, const rlk_token_state* state,
+                                  const float* grad_logprob, const float* grad_entropy,
+                                  const int32_t* top_ids, int32_t n_top, const float* grad_top,
+                                  void* grad_logits, rlk_dtype grad_dtype, int64_t ldg,
+                                  uint32_t* out_status_word, rlk_stream stream);
+
 #ifdef __cplusplus
 }  /* extern "C" */
 #endif
