@@ -30,6 +30,7 @@ OP_CANONICAL_TOPP = 6
 OP_NORM_BWD = 7
 OP_PREFERENCE_LOSS = 8
 OP_LINEAR, OP_LINEAR_BWD = 9, 10
+OP_GATED_LINEAR, OP_GATED_LINEAR_BWD = 11, 12
 ACT_NONE, ACT_GELU, ACT_SILU, ACT_RELU = 0, 1, 2, 3
 PREF_SIGMOID, PREF_IPO, PREF_HINGE = 0, 1, 2
 PREF_NSTATS = 6
@@ -82,7 +83,8 @@ EXPORTS = ("rlk_version", "rlk_status_string", "rlk_workspace_size", "rlk_logpro
            "rlk_logprob_entropy_canonical_topp",
            "rlk_grpo_loss_noalloc", "rlk_checkpoint_pack", "rlk_checkpoint_unpack",
            "rlk_norm_fwd", "rlk_norm_bwd", "rlk_preference_loss", "rlk_linear_fwd",
-           "rlk_linear_bwd", "rlk_token_logprobs_fwd", "rlk_token_logprobs_bwd")
+           "rlk_linear_bwd", "rlk_token_logprobs_fwd", "rlk_token_logprobs_bwd",
+           "rlk_gated_linear_fwd", "rlk_gated_linear_bwd")
 NOALLOC_MAX_SEQ = 16384
 DEBUG_EXPORTS = ("rlk_lmhead_logits_debug", "rlk_debug_inject_launch_failures",
                  "rlk_debug_set_wait_limit", "rlk_debug_withhold_copy",
@@ -226,6 +228,13 @@ def load(path: str | None = None):
         lib.rlk_token_logprobs_bwd.argtypes = [vp, ctypes.c_int, i64, i64, i64, vp, i32, f32, vp, vp, vp,
                                                vp, i32, vp, vp, ctypes.c_int, i64, vp, vp]
         lib.rlk_token_logprobs_bwd.restype = ctypes.c_int
+        lib.rlk_gated_linear_fwd.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, ctypes.c_int, i64, i64, i64,
+                                             ctypes.c_int, vp, ctypes.c_int, i64, vp, vp, i64, vp, sz, vp]
+        lib.rlk_gated_linear_fwd.restype = ctypes.c_int
+        lib.rlk_gated_linear_bwd.argtypes = [vp, i64, vp, i64, ck, vp, i64, vp, i64, vp, i64, vp, i64, i64, i64,
+                                             i64, ctypes.c_int, vp, ctypes.c_int, i64, vp, i64, vp, i64,
+                                             ctypes.c_int, vp, vp, ctypes.c_int, vp, sz, vp]
+        lib.rlk_gated_linear_bwd.restype = ctypes.c_int
         _lib = lib
         return lib
 
@@ -922,13 +931,13 @@ def _param(t, H, name):
     return dt
 
 
-def _params(H, weight, bias):
+def _params(H, weight, bias, name="weight", name_bias="bias"):
     """dtype index of the parameter vectors given (fp32 when none is)."""
-    dt = 1 if weight is None else _param(weight, H, "weight")
+    dt = 1 if weight is None else _param(weight, H, name)
     if bias is not None:
-        db = _param(bias, H, "bias")
+        db = _param(bias, H, name_bias)
         if weight is not None and db != dt:
-            raise ValueError("weight and bias must have one dtype")
+            raise ValueError(f"{name} and {name_bias} must have one dtype")
         dt = db
     return dt
 
@@ -1247,6 +1256,142 @@ def linear_autograd(x: torch.Tensor, weight: torch.Tensor, bias=None, residual=N
     """``linear`` as a differentiable op; ``keep_8bit`` keeps x for the backward
     as its 8-bit checkpoint instead of the tensor."""
     return _Linear.apply(x, weight, bias, residual, activation, keep_8bit)
+
+
+# ------------------------------------------------------------ gated linear
+def gated_linear(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, bias_gate=None, bias_up=None, *,
+                 activation: int = ACT_SILU, return_preact: bool = False, out=None, out_dtype=None,
+                 workspace=None):
+    """act(x w_gate^T + bias_gate) * (x w_up^T + bias_up): x [M, K], weights
+    [N, K] CUDA bf16 (rows may be strided), biases [N] bf16 or fp32.  Returns y
+    (bf16, or ``out_dtype`` fp32), or (y, gate, up) with the bf16 projections
+    for ``gated_linear_backward``."""
+    lib = load()
+    _need_cuda(x, w_gate, w_up, bias_gate, bias_up, out, workspace)
+    ldx, ldg, ldu = _bf16(x, "x"), _bf16(w_gate, "w_gate"), _bf16(w_up, "w_up")
+    M, K = x.shape
+    N = w_gate.shape[0]
+    if w_gate.shape[1] != K or w_up.shape != w_gate.shape:
+        raise ValueError("x, w_gate and w_up disagree on K or N")
+    bdt = _params(N, bias_gate, bias_up, "bias_gate", "bias_up")
+    dev = x.device
+    if out is None:
+        ydt, ldy = (0 if out_dtype is None else _dtype(out_dtype, "out_dtype")), N
+        out = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=dev)
+    else:
+        ydt, ldy = _matrix(out, "out", (M, N))
+    gate = torch.empty((M, N), dtype=torch.bfloat16, device=dev) if return_preact else None
+    up = torch.empty((M, N), dtype=torch.bfloat16, device=dev) if return_preact else None
+    px, pg, pu = x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr()
+    if workspace is None and M > 4:   # fewer rows are not copied
+        need = _copied(M, K, px, ldx) + _copied(N, K, pg, ldg) + _copied(N, K, pu, ldu)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    code = lib.rlk_gated_linear_fwd(px, ldx, pg, ldg, pu, ldu, _ptr(bias_gate), _ptr(bias_up), bdt, M, N, K,
+                                    activation, out.data_ptr(), ydt, ldy, _ptr(gate), _ptr(up), N,
+                                    _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream(dev))
+    _check("rlk_gated_linear_fwd", code)
+    return (out, gate, up) if return_preact else out
+
+
+def gated_linear_backward(dy: torch.Tensor, x, w_gate: torch.Tensor, w_up: torch.Tensor, gate: torch.Tensor,
+                          up: torch.Tensor, *, activation: int = ACT_SILU, grad_dtype=torch.bfloat16,
+                          weight_grad_dtype=torch.float32, want_x_grad: bool = True,
+                          want_weight_grad: bool = True, want_bias_grad: bool = True, grad_w_gate=None,
+                          grad_w_up=None, grad_bias_gate=None, grad_bias_up=None, accumulate: bool = False,
+                          workspace=None):
+    """Gradients of ``gated_linear``: (dL/dx [M, K], dL/dw_gate, dL/dw_up [N, K],
+    dL/dbias_gate, dL/dbias_up fp32 [N]), None where not wanted.  ``gate`` and
+    ``up`` from the forward; ``x`` its input or that one's ``Checkpoint``.
+    ``accumulate`` adds into the weights' (fp32) and biases' gradients given."""
+    lib = load()
+    kept = x if isinstance(x, Checkpoint) else None
+    _need_cuda(dy, None if kept else x, w_gate, w_up, gate, up, grad_w_gate, grad_w_up, grad_bias_gate,
+               grad_bias_up, workspace)
+    lddy, ldwg, ldwu = _bf16(dy, "dy"), _bf16(w_gate, "w_gate"), _bf16(w_up, "w_up")
+    M, N = dy.shape
+    K = w_gate.shape[1]
+    if w_gate.shape[0] != N or w_up.shape != w_gate.shape or (x is not None and tuple(x.shape) != (M, K)):
+        raise ValueError("dy, x, w_gate and w_up disagree on M, N or K")
+    ldg, ldu = _bf16(gate, "gate", (M, N)), _bf16(up, "up", (M, N))
+    ldx = 0 if x is None or kept else _bf16(x, "x")
+    if accumulate and ((want_weight_grad and (grad_w_gate is None or grad_w_up is None))
+                       or (want_bias_grad and (grad_bias_gate is None or grad_bias_up is None))):
+        raise ValueError("accumulate needs the gradients to add to")
+    dev = dy.device
+    dx = torch.empty((M, K), device=dev, dtype=grad_dtype) if want_x_grad else None
+    xdt = 0 if dx is None else _matrix(dx, "dx")[0]
+    wdt, ldgwg, ldgwu = 1, K, K
+    if want_weight_grad or grad_w_gate is not None or grad_w_up is not None:
+        like = grad_w_gate if grad_w_gate is not None else grad_w_up
+        dt = weight_grad_dtype if like is None else like.dtype
+        if grad_w_gate is None:
+            grad_w_gate = torch.empty((N, K), device=dev, dtype=dt)
+        if grad_w_up is None:
+            grad_w_up = torch.empty((N, K), device=dev, dtype=dt)
+        wdt, ldgwg = _matrix(grad_w_gate, "grad_w_gate", (N, K))
+        other, ldgwu = _matrix(grad_w_up, "grad_w_up", (N, K))
+        if other != wdt:
+            raise ValueError("grad_w_gate and grad_w_up must have one dtype")
+    if want_bias_grad or grad_bias_gate is not None or grad_bias_up is not None:
+        if grad_bias_gate is None:
+            grad_bias_gate = torch.empty(N, device=dev, dtype=torch.float32)
+        if grad_bias_up is None:
+            grad_bias_up = torch.empty(N, device=dev, dtype=torch.float32)
+        _vector(grad_bias_gate, N, "grad_bias_gate")
+        _vector(grad_bias_up, N, "grad_bias_up")
+    px = None if x is None or kept else x.data_ptr()
+    if workspace is None and M > 0:   # what this call uses: dg and du, copies of operands, partial sums
+        need = 0
+        if grad_bias_gate is not None:
+            need += (lib.rlk_workspace_size(OP_GATED_LINEAR_BWD, M, N, K) - 2 * _copied(M, N, 1, 0)
+                     - 2 * _copied(N, K, 1, 0) - _copied(M, K, 1, 0))
+        if dx is not None or grad_w_gate is not None:
+            need += 2 * _copied(M, N, 1, 0)
+        if dx is not None:
+            need += _copied(N, K, w_gate.data_ptr(), ldwg) + _copied(N, K, w_up.data_ptr(), ldwu)
+        if grad_w_gate is not None:
+            need += _copied(M, K, px or 1, ldx)
+        workspace = torch.empty(need, device=dev, dtype=torch.uint8) if need else None
+    ck = None if kept is None else kept.buffers()
+    _check("rlk_gated_linear_bwd",
+           lib.rlk_gated_linear_bwd(_ptr(dy), lddy, px, ldx, ck, _ptr(w_gate), ldwg, _ptr(w_up), ldwu, _ptr(gate),
+                                    ldg, _ptr(up), ldu, M, N, K, int(activation), _ptr(dx), xdt, K,
+                                    _ptr(grad_w_gate), ldgwg, _ptr(grad_w_up), ldgwu, wdt,
+                                    _ptr(grad_bias_gate), _ptr(grad_bias_up), int(bool(accumulate)),
+                                    _ptr(workspace), 0 if workspace is None else workspace.numel(),
+                                    _stream(dev)))
+    return dx, grad_w_gate, grad_w_up, grad_bias_gate, grad_bias_up
+
+
+class _GatedLinear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w_gate, w_up, bias_gate, bias_up, activation, keep8):
+        y, gate, up = gated_linear(x, w_gate, w_up, bias_gate, bias_up, activation=activation, return_preact=True)
+        ck = checkpoint_pack(x) if keep8 else None
+        ctx.save_for_backward(ck.codes if keep8 else x, ck.scales if keep8 else None, w_gate, w_up, gate, up)
+        ctx.activation = activation
+        ctx.bias_dtypes = [None if b is None else b.dtype for b in (bias_gate, bias_up)]
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        kept, scales, w_gate, w_up, gate, up = ctx.saved_tensors
+        x = kept if scales is None else Checkpoint(kept, scales, kept.shape[0], w_gate.shape[1])
+        need = ctx.needs_input_grad
+        dx, dwg, dwu, dbg, dbu = gated_linear_backward(
+            dy.contiguous(), x, w_gate, w_up, gate, up, activation=ctx.activation, weight_grad_dtype=w_gate.dtype,
+            want_x_grad=need[0], want_weight_grad=need[1] or need[2], want_bias_grad=need[3] or need[4])
+        of = lambda g, want, dtype: g.to(dtype) if want and g is not None else None
+        return (dx, dwg if need[1] else None, dwu if need[2] else None, of(dbg, need[3], ctx.bias_dtypes[0]),
+                of(dbu, need[4], ctx.bias_dtypes[1]), None, None)
+
+
+def gated_linear_autograd(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, bias_gate=None, bias_up=None, *,
+                          activation: int = ACT_SILU, keep_8bit: bool = False):
+    """``gated_linear`` as a differentiable op; ``keep_8bit`` keeps x for the
+    backward as its 8-bit checkpoint instead of the tensor."""
+    return _GatedLinear.apply(x, w_gate, w_up, bias_gate, bias_up, activation, keep_8bit)
 
 
 # ------------------------------------------------------------ preference loss

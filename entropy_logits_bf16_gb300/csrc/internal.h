@@ -350,6 +350,64 @@ size_t linear_bwd_workspace_bytes(int64_t M, int64_t N, int64_t K);
 size_t linear_bwd_workspace_needed(const LinearBwdArgs& a);
 cudaError_t launch_linear_fwd(const LinearArgs& a, cudaStream_t stream);
 cudaError_t launch_linear_bwd(const LinearBwdArgs& a, cudaStream_t stream);
+// Parts of it that the gated layer uses too: copies of one or two bf16 matrices with rows on
+// 16-byte boundaries (columns past the end 0), sum[c] (+)= the parts' columns in order, zeros.
+struct Repack {
+  const uint16_t* src;
+  int64_t ld, rows, cols;
+  uint16_t* dst;
+  int64_t ldd;
+};
+cudaError_t launch_repack(const Repack& a, const Repack& b, cudaStream_t stream);
+cudaError_t launch_add_parts(const float* part, int64_t pitch, int parts, int64_t N, float* sum, int accumulate,
+                             cudaStream_t stream);
+cudaError_t launch_zero(void* p, int dtype, int64_t ld, int64_t rows, int64_t cols, cudaStream_t stream);
+
+// Gated linear layer and its backward (gated.cu); [0] gate, [1] up.
+struct GatedArgs {
+  const void* x;
+  int64_t ldx;
+  const void* w[2];
+  int64_t ldw[2];
+  const void* bias[2];
+  int bias_dtype;
+  int64_t M, N, K;
+  int act;              // rlk_activation
+  void* y;
+  int y_dtype;
+  int64_t ldy;
+  void* z[2];           // both or neither
+  int64_t ldz;
+  void* workspace;
+};
+struct GatedBwdArgs {
+  const void* dy;
+  int64_t lddy;
+  const void* x;        // NULL: from ck
+  int64_t ldx;
+  CheckpointView ck;
+  const void* w[2];
+  int64_t ldw[2];
+  const void* z[2];
+  int64_t ldz[2];
+  int64_t M, N, K;
+  int act;
+  void* dx;
+  int dx_dtype;
+  int64_t lddx;
+  void* dw[2];          // both or neither
+  int dw_dtype;
+  int64_t lddw[2];
+  float* db[2];         // both or neither
+  int accumulate;
+  void* workspace;
+};
+size_t gated_workspace_bytes(int64_t M, int64_t N, int64_t K);        // the most a call may need
+size_t gated_workspace_needed(const GatedArgs& a);                    // what this one needs
+size_t gated_bwd_workspace_bytes(int64_t M, int64_t N, int64_t K);
+size_t gated_bwd_workspace_needed(const GatedBwdArgs& a);
+cudaError_t launch_gated_fwd(const GatedArgs& a, cudaStream_t stream);
+cudaError_t launch_gated_bwd(const GatedBwdArgs& a, cudaStream_t stream);
 
 cudaError_t launch_sample(const SampleArgs& a, cudaStream_t stream);
 cudaError_t launch_shard_partials(const ShardArgs& a, cudaStream_t stream);

@@ -40,6 +40,7 @@
 
 #include <atomic>
 
+#include "activation.cuh"
 #include "checkpoint.cuh"
 #include "internal.h"
 #include "rlk.h"
@@ -101,102 +102,8 @@ struct GemmParams {
   Epilogue e;
 };
 
-// 1 / v to 2^-23 (MUFU; a result below 2^-126 is 0).
-__device__ __forceinline__ float rcp(float v) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
-}
-
-// Phi(-|z|), Phi the normal distribution function, two numbers an instruction, to a
-// relative (2 z^2 + 24) 2^-24 (half an ulp of z alone moves it by z^2 2^-24):
-// Phi(-|z|) = t q(t) exp(-z^2 / 2) with t = 1 / (1 + 0.305 |z|).  t q(t) is half the scaled
-// complementary error function erfcx(|z| / sqrt 2); q is its minimax fit in t, by relative
-// error (9.4e-8) over |z| <= 13.3, beyond which the exponential is below 2^-126 and is 0.
-// `bell`: exp(-z^2 / 2).
-__device__ __forceinline__ float2 normal_tail(float2 z, float2& bell) {
-  const float2 d = fma2(make_float2(fabsf(z.x), fabsf(z.y)), both(0.305f), both(1.f));
-  const float2 t = make_float2(rcp(d.x), rcp(d.y));
-  float2 q = fma2(both(0.0366991907f), t, both(-0.1529883f));
-  q = fma2(q, t, both(0.185716853f));
-  q = fma2(q, t, both(-0.0379767865f));
-  q = fma2(q, t, both(0.121021658f));
-  q = fma2(q, t, both(0.103420876f));
-  q = fma2(q, t, both(0.122466817f));
-  q = fma2(q, t, both(0.121639736f));
-  const float2 e = mul2(mul2(z, z), both(-0.5f * kLog2e));
-  bell = make_float2(ex2(e.x), ex2(e.y));
-  return mul2(mul2(q, t), bell);
-}
-// Phi(z) from Phi(-|z|).
-__device__ __forceinline__ float2 normal_below(float2 z, float2 tail) {
-  const float2 up = fma2(tail, both(-1.f), both(1.f));
-  return make_float2(z.x > 0.f ? up.x : tail.x, z.y > 0.f ? up.y : tail.y);
-}
-// 1 / (1 + exp(-z)), to a relative (2 |z| + 24) 2^-24.
-__device__ __forceinline__ float2 logistic(float2 z) {
-  const float2 e = mul2(z, both(-kLog2e)), d = add2(make_float2(ex2(e.x), ex2(e.y)), both(1.f));
-  return make_float2(rcp(d.x), rcp(d.y));
-}
-// act of W values; the choice is made once.
-template <int W>
-__device__ __forceinline__ void activate(float (&v)[W], int act) {
-  if (act == RLK_ACT_GELU) {
-#pragma unroll
-    for (int j = 0; j < W; j += 2) {
-      const float2 z = make_float2(v[j], v[j + 1 < W ? j + 1 : j]);
-      float2 bell;
-      const float2 tail = normal_tail(z, bell), o = mul2(z, normal_below(z, tail));
-      v[j] = o.x;
-      if (j + 1 < W) v[j + 1] = o.y;
-    }
-  } else if (act == RLK_ACT_SILU) {
-#pragma unroll
-    for (int j = 0; j < W; j += 2) {
-      const float2 z = make_float2(v[j], v[j + 1 < W ? j + 1 : j]), o = mul2(z, logistic(z));
-      v[j] = o.x;
-      if (j + 1 < W) v[j + 1] = o.y;
-    }
-  } else if (act == RLK_ACT_RELU) {
-#pragma unroll
-    for (int j = 0; j < W; ++j) v[j] = v[j] < 0.f ? 0.f : v[j];
-  }
-}
-// act'(z), to the same.
-template <int ACT>
-__device__ __forceinline__ float2 activation_slope(float2 z) {
-  if (ACT == RLK_ACT_GELU) {   // Phi(z) + z phi(z)
-    float2 bell;
-    const float2 tail = normal_tail(z, bell);
-    return fma2(mul2(z, bell), both(0.39894228040143268f), normal_below(z, tail));
-  }
-  if (ACT == RLK_ACT_SILU) {
-    const float2 s = logistic(z);
-    return mul2(s, fma2(z, fma2(s, both(-1.f), both(1.f)), both(1.f)));
-  }
-  auto relu = [](float v) { return v > 0.f ? 1.f : (v != v ? v : 0.f); };
-  return make_float2(relu(z.x), relu(z.y));
-}
-
 __device__ __forceinline__ void prefetch_l2(const void* p) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
-}
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// The epilogue of 8 columns of one row whose y, z and residual start on 16-byte
-// boundaries there; n of the columns exist.
-__device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8], int n) {
-  if (n == 8) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
-                                              pack_bf16(v[6], v[7]));
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j < n) p[j] = (uint16_t)pack_bf16(v[j], 0.f);
-  }
 }
 __device__ __forceinline__ float bias_at(const Epilogue& e, int64_t col) {
   return e.bias_dtype ? static_cast<const float*>(e.bias)[col] : bf16_val(static_cast<const uint16_t*>(e.bias)[col]);
@@ -773,14 +680,8 @@ __global__ void __launch_bounds__(GEMV_T, 4) linear_gemv_kernel(const uint16_t* 
 // ------------------------------------------------------------ around the products
 constexpr int ET = 256;
 
-// bf16 matrices copied to rows that start on 16-byte boundaries: a warp a row, 8
+// bf16 matrices copied to rows that start on 16-byte boundaries (Repack): a warp a row, 8
 // columns a lane.
-struct Repack {
-  const uint16_t* src;
-  int64_t ld, rows, cols;
-  uint16_t* dst;
-  int64_t ldd;
-};
 __global__ void __launch_bounds__(ET) repack_kernel(Repack a, Repack b) {
   pdl_wait();
   const int lane = threadIdx.x & 31;
@@ -1060,10 +961,7 @@ cudaError_t aligned_operands(Copied x, Copied w, char*& ws, cudaStream_t stream)
     r[n++] = Repack{static_cast<const uint16_t*>(c.o->p), c.o->ld, c.rows, c.cols, dst, pad8(c.cols)};
     *c.o = Operand{dst, pad8(c.cols)};
   }
-  if (n == 0) return cudaSuccess;
-  const int64_t want = (r[0].rows + r[1].rows + ET / 32 - 1) / (ET / 32), cap = (int64_t)sm_count() * 16;
-  const cudaError_t e = launch_after(repack_kernel, dim3((unsigned)(want < cap ? want : cap)), dim3(ET), 0, stream, r[0], r[1]);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return n == 0 ? cudaSuccess : launch_repack(r[0], r[1], stream);
 }
 
 constexpr int kDbParts = 304;   // most row parts of the bias gradient
@@ -1075,6 +973,23 @@ int64_t db_parts_most(int64_t M) {
 size_t db_bytes(int64_t M, int64_t N) { return pad256((size_t)db_parts_most(M) * pad8(N) * sizeof(float)); }
 
 }  // namespace
+
+cudaError_t launch_repack(const Repack& a, const Repack& b, cudaStream_t stream) {
+  const int64_t want = (a.rows + b.rows + ET / 32 - 1) / (ET / 32), cap = (int64_t)sm_count() * 16;
+  const cudaError_t e = launch_after(repack_kernel, dim3((unsigned)(want < cap ? want : cap)), dim3(ET), 0, stream, a, b);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+cudaError_t launch_add_parts(const float* part, int64_t pitch, int parts, int64_t N, float* sum, int accumulate,
+                             cudaStream_t stream) {
+  const cudaError_t e = launch_after(linear_db_kernel, dim3((unsigned)((N + 31) / 32)), dim3(256), 0, stream, part, pitch, parts,
+                                     N, sum, accumulate);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+cudaError_t launch_zero(void* p, int dtype, int64_t ld, int64_t rows, int64_t cols, cudaStream_t stream) {
+  const int64_t cap = (int64_t)sm_count() * 8;
+  linear_zero_kernel<<<(unsigned)(rows < cap ? rows : cap), ET, 0, stream>>>(p, dtype, ld, rows, cols);
+  return cudaGetLastError();
+}
 
 size_t linear_workspace_bytes(int64_t M, int64_t N, int64_t K) { return copy_bytes(M, K) + copy_bytes(N, K); }
 
@@ -1124,11 +1039,10 @@ size_t linear_bwd_workspace_needed(const LinearBwdArgs& a) {
 cudaError_t launch_linear_bwd(const LinearBwdArgs& a, cudaStream_t stream) {
   char* ws = static_cast<char*>(a.workspace);
   if (a.M == 0) {   // sums over no rows
-    const int64_t cap = (int64_t)sm_count() * 8;
-    if (a.dw && !a.accumulate)
-      linear_zero_kernel<<<(unsigned)(a.N < cap ? a.N : cap), ET, 0, stream>>>(a.dw, a.dw_dtype, a.lddw, a.N, a.K);
-    if (a.db && !a.accumulate) linear_zero_kernel<<<1, ET, 0, stream>>>(a.db, 1, a.N, 1, a.N);
-    return cudaGetLastError();
+    cudaError_t e = cudaSuccess;
+    if (a.dw && !a.accumulate) e = launch_zero(a.dw, a.dw_dtype, a.lddw, a.N, a.K, stream);
+    if (e == cudaSuccess && a.db && !a.accumulate) e = launch_zero(a.db, 1, a.N, 1, a.N, stream);
+    return e;
   }
   // dz, and the bias gradient with it
   Operand dz{a.dy, a.lddy};
@@ -1165,8 +1079,7 @@ cudaError_t launch_linear_bwd(const LinearBwdArgs& a, cudaStream_t stream) {
     kernel<<<grid, DT, 0, stream>>>(a, dst, ld, part, pitch, (int)parts);
     if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
     if (a.db) {
-      const cudaError_t e = launch_after(linear_db_kernel, dim3((unsigned)((a.N + 31) / 32)), dim3(256), 0, stream,
-                                         (const float*)part, pitch, (int)parts, a.N, a.db, a.accumulate);
+      const cudaError_t e = launch_add_parts(part, pitch, (int)parts, a.N, a.db, a.accumulate, stream);
       if (e != cudaSuccess) return e;
     }
   }

@@ -145,6 +145,8 @@ size_t rlk_workspace_size(int op, int64_t T, int64_t V, int64_t H) {
     case RLK_OP_PREFERENCE_LOSS: return rlk::pref_workspace_bytes(T, V);
     case RLK_OP_LINEAR: return rlk::linear_workspace_bytes(T, V, H);
     case RLK_OP_LINEAR_BWD: return rlk::linear_bwd_workspace_bytes(T, V, H);
+    case RLK_OP_GATED_LINEAR: return rlk::gated_workspace_bytes(T, V, H);
+    case RLK_OP_GATED_LINEAR_BWD: return rlk::gated_bwd_workspace_bytes(T, V, H);
     case RLK_OP_CANONICAL:
       return V < 1 ? 0 : (size_t)V * (size_t)T * sizeof(rlk_shard_partial);
     case RLK_OP_CANONICAL_TOPP:
@@ -1228,6 +1230,120 @@ rlk_status rlk_token_logprobs_bwd(const void* logits, rlk_dtype dtype, int64_t T
   a.status = out_status_word;
   if (rlk::take_injected_failure()) return RLK_ERR_CUDA;
   return rlk::launch_token_logprobs_backward(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? RLK_OK
+             : RLK_ERR_CUDA;
+}
+
+rlk_status rlk_gated_linear_fwd(const void* x, int64_t ldx, const void* w_gate, int64_t ldwg,
+                                const void* w_up, int64_t ldwu, const void* bias_gate,
+                                const void* bias_up, rlk_dtype bias_dtype, int64_t M, int64_t N,
+                                int64_t K, rlk_activation act, void* y, rlk_dtype y_dtype,
+                                int64_t ldy, void* out_gate, void* out_up, int64_t ldz,
+                                void* workspace, size_t workspace_bytes, rlk_stream stream) {
+  if (!linear_sizes_ok(M, N, K, act) || !good_dtype(bias_dtype) || !good_dtype(y_dtype))
+    return RLK_ERR_INVALID_ARG;
+  if (ldx < K || ldwg < K || ldwu < K || ldy < N || !out_gate != !out_up || (out_gate && ldz < N))
+    return RLK_ERR_INVALID_ARG;
+  if (M == 0) return RLK_OK;
+  if (!x || !w_gate || !w_up || !y || !aligned_to(x, 2) || !aligned_to(w_gate, 2) || !aligned_to(w_up, 2) ||
+      !elem_aligned(bias_gate, bias_dtype) || !elem_aligned(bias_up, bias_dtype) || !elem_aligned(y, y_dtype) ||
+      !aligned_to(out_gate, 2) || !aligned_to(out_up, 2))
+    return RLK_ERR_INVALID_ARG;
+  rlk::GatedArgs a{};
+  a.x = x;
+  a.ldx = ldx;
+  a.w[0] = w_gate;
+  a.w[1] = w_up;
+  a.ldw[0] = ldwg;
+  a.ldw[1] = ldwu;
+  a.bias[0] = bias_gate;
+  a.bias[1] = bias_up;
+  a.bias_dtype = dtype_index(bias_dtype);
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.act = (int)act;
+  a.y = y;
+  a.y_dtype = dtype_index(y_dtype);
+  a.ldy = ldy;
+  a.z[0] = out_gate;
+  a.z[1] = out_up;
+  a.ldz = ldz;
+  a.workspace = workspace;
+  if (!workspace_ok(workspace, workspace_bytes, rlk::gated_workspace_needed(a)))
+    return RLK_ERR_WORKSPACE;
+  if (rlk::take_injected_failure()) return RLK_ERR_CUDA;
+  return rlk::launch_gated_fwd(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? RLK_OK
+             : RLK_ERR_CUDA;
+}
+
+rlk_status rlk_gated_linear_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                                const rlk_checkpoint* checkpoint, const void* w_gate,
+                                int64_t ldwg, const void* w_up, int64_t ldwu, const void* gate,
+                                int64_t ldg, const void* up, int64_t ldu, int64_t M, int64_t N,
+                                int64_t K, rlk_activation act, void* grad_x,
+                                rlk_dtype grad_x_dtype, int64_t ldgx, void* grad_w_gate,
+                                int64_t ldgwg, void* grad_w_up, int64_t ldgwu,
+                                rlk_dtype grad_w_dtype, float* grad_bias_gate,
+                                float* grad_bias_up, int accumulate, void* workspace,
+                                size_t workspace_bytes, rlk_stream stream) {
+  if (!linear_sizes_ok(M, N, K, act) || !good_dtype(grad_x_dtype) || !good_dtype(grad_w_dtype))
+    return RLK_ERR_INVALID_ARG;
+  if (!grad_w_gate != !grad_w_up || !grad_bias_gate != !grad_bias_up) return RLK_ERR_INVALID_ARG;
+  if (lddy < N || (grad_x && ldgx < K) || (grad_w_gate && (ldgwg < K || ldgwu < K)))
+    return RLK_ERR_INVALID_ARG;
+  if (!elem_aligned(grad_x, grad_x_dtype) || !elem_aligned(grad_w_gate, grad_w_dtype) ||
+      !elem_aligned(grad_w_up, grad_w_dtype) || !aligned_to(grad_bias_gate, 4) ||
+      !aligned_to(grad_bias_up, 4))
+    return RLK_ERR_INVALID_ARG;
+  rlk::GatedBwdArgs a{};
+  if (M > 0) {
+    if (!dy || !aligned_to(dy, 2) || !gate || !up || ldg < N || ldu < N || !aligned_to(gate, 2) ||
+        !aligned_to(up, 2))
+      return RLK_ERR_INVALID_ARG;
+    if (grad_x && (!w_gate || !w_up || ldwg < K || ldwu < K || !aligned_to(w_gate, 2) || !aligned_to(w_up, 2)))
+      return RLK_ERR_INVALID_ARG;
+    if (grad_w_gate) {
+      if (!x == !checkpoint) return RLK_ERR_INVALID_ARG;
+      if (x && (ldx < K || !aligned_to(x, 2))) return RLK_ERR_INVALID_ARG;
+      if (checkpoint && !checkpoint_ok(checkpoint, K, a.ck)) return RLK_ERR_INVALID_ARG;
+    }
+  }
+  if (accumulate && grad_w_gate && grad_w_dtype != RLK_F32) return RLK_ERR_UNSUPPORTED;
+  a.dy = dy;
+  a.lddy = lddy;
+  a.x = x;
+  a.ldx = ldx;
+  a.w[0] = w_gate;
+  a.w[1] = w_up;
+  a.ldw[0] = ldwg;
+  a.ldw[1] = ldwu;
+  a.z[0] = gate;
+  a.z[1] = up;
+  a.ldz[0] = ldg;
+  a.ldz[1] = ldu;
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.act = (int)act;
+  a.dx = grad_x;
+  a.dx_dtype = dtype_index(grad_x_dtype);
+  a.lddx = ldgx;
+  a.dw[0] = grad_w_gate;
+  a.dw[1] = grad_w_up;
+  a.dw_dtype = dtype_index(grad_w_dtype);
+  a.lddw[0] = ldgwg;
+  a.lddw[1] = ldgwu;
+  a.db[0] = grad_bias_gate;
+  a.db[1] = grad_bias_up;
+  a.accumulate = accumulate != 0;
+  a.workspace = workspace;
+  if (!grad_w_gate && !grad_bias_gate && (M == 0 || !grad_x)) return RLK_OK;
+  if (M > 0 && !workspace_ok(workspace, workspace_bytes, rlk::gated_bwd_workspace_needed(a)))
+    return RLK_ERR_WORKSPACE;
+  if (rlk::take_injected_failure()) return RLK_ERR_CUDA;
+  return rlk::launch_gated_bwd(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? RLK_OK
              : RLK_ERR_CUDA;
 }

@@ -90,6 +90,10 @@ constexpr uint32_t idesc_bf16(bool a_mn, bool b_mn, int m, int n) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
          ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
+// The same with fp16 or bf16 operands (both of one type).
+constexpr uint32_t idesc_16(bool f16, bool a_mn, bool b_mn, int m, int n) {
+  return idesc_bf16(a_mn, b_mn, m, n) & (f16 ? ~((1u << 7) | (1u << 10)) : ~0u);
+}
 // G = 2: the pair of CTAs of a cluster works on one tile of twice the rows.  Each
 // holds its half of A's rows and of B's rows (N) at the same place in its shared
 // memory and gets its half of the accumulator's rows; one thread of the even

@@ -89,7 +89,8 @@ typedef enum {
 enum { RLK_OP_LOGPROB_ENTROPY = 0, RLK_OP_GRPO_LOSS = 1, RLK_OP_LMHEAD = 2,
        RLK_OP_LMHEAD_BWD = 3, RLK_OP_LMHEAD_TOPP = 4, RLK_OP_CANONICAL = 5,
        RLK_OP_CANONICAL_TOPP = 6, RLK_OP_NORM_BWD = 7, RLK_OP_PREFERENCE_LOSS = 8,
-       RLK_OP_LINEAR = 9, RLK_OP_LINEAR_BWD = 10 };
+       RLK_OP_LINEAR = 9, RLK_OP_LINEAR_BWD = 10, RLK_OP_GATED_LINEAR = 11,
+       RLK_OP_GATED_LINEAR_BWD = 12 };
 
 /* Bits OR-ed into *out_status_word by the kernels. */
 #define RLK_STATUS_BAD_TOKEN_ID 0x1u   /* a token id outside [0, V)          */
@@ -156,6 +157,8 @@ const char* rlk_status_string(rlk_status status);
  *  RLK_OP_PREFERENCE_LOSS: T packed tokens, V = n_pairs, H unused
  *  RLK_OP_LINEAR:          T rows, V = N output features, H = K input features
  *  RLK_OP_LINEAR_BWD:      the same (rlk_linear_bwd)
+ *  RLK_OP_GATED_LINEAR:    the same (rlk_gated_linear_fwd)
+ *  RLK_OP_GATED_LINEAR_BWD: the same (rlk_gated_linear_bwd)
  * Returns 0 for an unknown op or negative sizes. */
 size_t rlk_workspace_size(int op, int64_t T, int64_t V, int64_t H);
 
@@ -1186,6 +1189,89 @@ rlk_status rlk_token_logprobs_bwd(const void* logits, rlk_dtype dtype, int64_t T
                                   const int32_t* top_ids, int32_t n_top, const float* grad_top,
                                   void* grad_logits, rlk_dtype grad_dtype, int64_t ldg,
                                   uint32_t* out_status_word, rlk_stream stream);
+
+/*
+ * rlk_gated_linear_fwd -- the gated half of a feed-forward block: two
+ * projections of x, an activation of the first and their product, in one kernel.
+ *
+ *   g = x w_gate^T + bias_gate,  u = x w_up^T + bias_up,  y = act(g) u,
+ * bf16 inputs, fp32 accumulation on the tensor cores, the epilogue in fp32; y
+ * is formed of the unrounded g and u; y, g and u are rounded once each.
+ *
+ * Arguments
+ *  x               device bf16, M x ldx elements (ldx >= K).
+ *  w_gate, w_up    device bf16, N x ldwg / ldwu elements (>= K), one row an output
+ *                  feature (the halves of one [2 N][K] matrix serve).
+ *  bias_gate, bias_up   device [N] of bias_dtype, each or NULL.
+ *  M, N, K         M >= 0; 1 <= N, K <= 2^24.
+ *  act             rlk_activation (RLK_ACT_SILU and RLK_ACT_GELU are the usual ones;
+ *                  RLK_ACT_NONE gives g u).
+ *  y               device, y_dtype, M x ldy elements (ldy >= N); may not overlap the
+ *                  inputs.
+ *  out_gate, out_up   device bf16, M x ldz elements (ldz >= N) each: g and u for
+ *                  rlk_gated_linear_bwd; both or neither (NULL).
+ *  workspace       aligned copies of x and the weights when M > 4 and their rows do
+ *                  not start on 16-byte boundaries: then at least
+ *                  rlk_workspace_size(RLK_OP_GATED_LINEAR, M, N, K) bytes serve,
+ *                  16-byte aligned, contents on entry do not matter; else it may be
+ *                  NULL.
+ * Deterministic; a row's last bits may differ between calls of a different M,
+ * as in rlk_linear_fwd, whose bounds of act hold here too.  NaN and infinities
+ * propagate as in the formula (act(g) = 0 times an infinite u is NaN).  Tiles
+ * whose operands did not come within the limit of a wait (about a second) are NaN.
+ * Errors: RLK_ERR_INVALID_ARG for sizes or strides outside the rules, bad
+ *  dtypes or activation, one of out_gate and out_up without the other, null or
+ *  misaligned pointers; RLK_ERR_WORKSPACE.  M == 0 returns RLK_OK without launching.
+ */
+rlk_status rlk_gated_linear_fwd(const void* x, int64_t ldx, const void* w_gate, int64_t ldwg,
+                                const void* w_up, int64_t ldwu, const void* bias_gate,
+                                const void* bias_up, rlk_dtype bias_dtype, int64_t M, int64_t N,
+                                int64_t K, rlk_activation act, void* y, rlk_dtype y_dtype,
+                                int64_t ldy, void* out_gate, void* out_up, int64_t ldz,
+                                void* workspace, size_t workspace_bytes, rlk_stream stream);
+
+/*
+ * rlk_gated_linear_bwd -- gradients of rlk_gated_linear_fwd.
+ *
+ *   dg = dy u act'(g),  du = dy act(g),   grad_x = dg w_gate + du w_up,
+ *   grad_w_gate (+)= dg^T x,  grad_w_up (+)= du^T x,
+ *   grad_bias_gate (+)= sum_m dg,  grad_bias_up (+)= sum_m du.
+ * dg and du are formed in fp32; the bias gradients sum them unrounded, and the
+ * products take them rounded to bf16, as the tensor cores need.  grad_x is one
+ * sum over both halves, rounded once.
+ *
+ * Arguments
+ *  dy              device bf16, M x lddy elements (lddy >= N).
+ *  x, ldx          the forward's input; or NULL with
+ *  checkpoint      its 8-bit checkpoint (exactly one of the two when the weights'
+ *                  gradients are given, neither is needed otherwise).
+ *  w_gate, w_up    the forward's (not needed without grad_x).
+ *  gate, up        the forward's out_gate and out_up, strides ldg and ldu.
+ *  grad_x          device, grad_x_dtype, M x ldgx elements (ldgx >= K), or NULL.
+ *  grad_w_gate, grad_w_up   device, grad_w_dtype, N x ldgwg / ldgwu elements (>= K);
+ *                  both or neither (NULL).
+ *  grad_bias_gate, grad_bias_up   device float[N]; both or neither (NULL).
+ *  accumulate      non-zero: the weights' (RLK_F32 only) and biases' gradients are
+ *                  added to.
+ *  workspace       at least rlk_workspace_size(RLK_OP_GATED_LINEAR_BWD, M, N, K)
+ *                  bytes, 16-byte aligned, contents on entry do not matter (a call
+ *                  that needs less accepts less).
+ * Deterministic for given sizes and layout.  Tiles whose operands did not come in
+ * time are NaN.
+ * Errors: as rlk_gated_linear_fwd; RLK_ERR_UNSUPPORTED for accumulate with bf16
+ *  weight gradients.  M == 0 zeroes the weights' and biases' gradients (or leaves
+ *  them, accumulating).
+ */
+rlk_status rlk_gated_linear_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                                const rlk_checkpoint* checkpoint, const void* w_gate,
+                                int64_t ldwg, const void* w_up, int64_t ldwu, const void* gate,
+                                int64_t ldg, const void* up, int64_t ldu, int64_t M, int64_t N,
+                                int64_t K, rlk_activation act, void* grad_x,
+                                rlk_dtype grad_x_dtype, int64_t ldgx, void* grad_w_gate,
+                                int64_t ldgwg, void* grad_w_up, int64_t ldgwu,
+                                rlk_dtype grad_w_dtype, float* grad_bias_gate,
+                                float* grad_bias_up, int accumulate, void* workspace,
+                                size_t workspace_bytes, rlk_stream stream);
 
 #ifdef __cplusplus
 }  /* extern "C" */

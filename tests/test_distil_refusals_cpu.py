@@ -35,13 +35,52 @@ def test_token_logprobs_backward_refuses(lib, change):
     assert lib.rlk_token_logprobs_bwd(*a.values(), None) == BAD
 
 
+GATED = dict(x=P, ldx=64, wg=P, ldwg=64, wu=P, ldwu=64, bg=P, bu=P, bdt=1, M=8, N=32, K=64, act=2, y=P, ydt=0, ldy=32, g=P, u=P, ldz=32, ws=0, wsb=0)
+GATED_BWD = dict(dy=P, lddy=32, x=P, ldx=64, ck=None, wg=P, ldwg=64, wu=P, ldwu=64, g=P, ldg=32, u=P, ldu=32, M=8, N=32, K=64, act=2, dx=P, dxt=0, ldgx=64,
+                 dwg=P, ldgwg=64, dwu=P, ldgwu=64, dwt=1, dbg=P, dbu=P, acc=0, ws=P, wsb=1 << 30)
+
+
+@pytest.mark.parametrize("change", [dict(M=-1), dict(M=1 << 31), dict(N=0), dict(N=(1 << 24) + 1, ldy=1 << 25, ldz=1 << 25), dict(K=0), dict(ldx=63), dict(ldwg=63), dict(ldwu=63),
+                                    dict(ldy=31), dict(ldz=31), dict(act=4), dict(act=-1), dict(bdt=2), dict(ydt=2), dict(x=0), dict(wg=0), dict(wu=0), dict(y=0), dict(x=P + 1),
+                                    dict(wg=P + 1), dict(wu=P + 1), dict(bg=P + 2), dict(bu=P + 2), dict(y=P + 1), dict(ydt=1, y=P + 2), dict(g=0), dict(u=0), dict(g=P + 1),
+                                    dict(u=P + 1)], ids=str)
+def test_gated_linear_refuses(lib, change):
+    assert lib.rlk_gated_linear_fwd(*{**GATED, **change}.values(), None) == BAD
+
+
+def test_gated_linear_workspace(lib):
+    for change in (dict(x=P + 2), dict(ldx=65), dict(wg=P + 2), dict(ldwg=66), dict(wu=P + 2), dict(ldwu=67)):
+        assert lib.rlk_gated_linear_fwd(*{**GATED, **change}.values(), None) == 3
+        assert lib.rlk_gated_linear_fwd(*{**GATED, **change, "ws": P + 8, "wsb": 1 << 30}.values(), None) == 3
+    assert lib.rlk_gated_linear_bwd(*{**GATED_BWD, "ws": 0}.values(), None) == 3
+    assert lib.rlk_gated_linear_bwd(*{**GATED_BWD, "wsb": 1000}.values(), None) == 3
+    need = lib.rlk_workspace_size(rlk.OP_GATED_LINEAR, 8, 32, 64)
+    assert need == 256 * ((8 * 64 * 2 + 255) // 256) + 2 * 32 * 64 * 2
+    assert lib.rlk_workspace_size(rlk.OP_GATED_LINEAR, -1, 32, 64) == 0
+
+
+@pytest.mark.parametrize("change", [dict(M=-1), dict(N=0), dict(K=0), dict(act=4), dict(lddy=31), dict(ldx=63), dict(ldwg=63), dict(ldwu=63), dict(ldg=31), dict(ldu=31),
+                                    dict(ldgx=63), dict(ldgwg=63), dict(ldgwu=63), dict(dxt=2), dict(dwt=2), dict(dy=0), dict(x=0), dict(wg=0), dict(wu=0), dict(g=0), dict(u=0),
+                                    dict(dy=P + 1), dict(x=P + 1), dict(wg=P + 1), dict(wu=P + 1), dict(g=P + 1), dict(u=P + 1), dict(dx=P + 1), dict(dwg=P + 2), dict(dwu=P + 2),
+                                    dict(dwg=0), dict(dwu=0), dict(dbg=0), dict(dbu=0), dict(dbg=P + 2), dict(dbu=P + 2)], ids=str)
+def test_gated_linear_backward_refuses(lib, change):
+    assert lib.rlk_gated_linear_bwd(*{**GATED_BWD, **change}.values(), None) == BAD
+
+
+def test_gated_linear_backward_accumulates_in_fp32_only(lib):
+    assert lib.rlk_gated_linear_bwd(*{**GATED_BWD, "acc": 1, "dwt": 0}.values(), None) == 2
+
+
 def test_no_rows(lib):
+    assert lib.rlk_gated_linear_fwd(*{**GATED, "M": 0, "x": 0}.values(), None) == OK
+    assert lib.rlk_gated_linear_bwd(*{**GATED_BWD, "M": 0, "dwg": 0, "dwu": 0, "dbg": 0, "dbu": 0}.values(), None) == OK
     assert lib.rlk_token_logprobs_fwd(*{**FWD, "T": 0, "logits": 0}.values(), None) == OK
     assert lib.rlk_token_logprobs_bwd(*{**BWD, "T": 0, "logits": 0}.values(), None) == OK
 
 
 def test_injected_failures(lib):
-    for call, args in ((lib.rlk_token_logprobs_fwd, FWD), (lib.rlk_token_logprobs_bwd, BWD)):
+    for call, args in ((lib.rlk_token_logprobs_fwd, FWD), (lib.rlk_token_logprobs_bwd, BWD), (lib.rlk_gated_linear_fwd, GATED),
+                       (lib.rlk_gated_linear_bwd, GATED_BWD)):
         rlk.inject_launch_failures(1)
         assert call(*args.values(), None) == 4
     assert rlk.inject_launch_failures(0) == 0
