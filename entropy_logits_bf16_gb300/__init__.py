@@ -31,6 +31,7 @@ OP_NORM_BWD = 7
 OP_PREFERENCE_LOSS = 8
 OP_LINEAR, OP_LINEAR_BWD = 9, 10
 OP_GATED_LINEAR, OP_GATED_LINEAR_BWD = 11, 12
+OP_ORTHOGONALISE = 13
 ACT_NONE, ACT_GELU, ACT_SILU, ACT_RELU = 0, 1, 2, 3
 PREF_SIGMOID, PREF_IPO, PREF_HINGE = 0, 1, 2
 PREF_NSTATS = 6
@@ -84,7 +85,7 @@ EXPORTS = ("rlk_version", "rlk_status_string", "rlk_workspace_size", "rlk_logpro
            "rlk_grpo_loss_noalloc", "rlk_checkpoint_pack", "rlk_checkpoint_unpack",
            "rlk_norm_fwd", "rlk_norm_bwd", "rlk_preference_loss", "rlk_linear_fwd",
            "rlk_linear_bwd", "rlk_token_logprobs_fwd", "rlk_token_logprobs_bwd",
-           "rlk_gated_linear_fwd", "rlk_gated_linear_bwd")
+           "rlk_gated_linear_fwd", "rlk_gated_linear_bwd", "rlk_orthogonalise")
 NOALLOC_MAX_SEQ = 16384
 DEBUG_EXPORTS = ("rlk_lmhead_logits_debug", "rlk_debug_inject_launch_failures",
                  "rlk_debug_set_wait_limit", "rlk_debug_withhold_copy",
@@ -235,6 +236,9 @@ def load(path: str | None = None):
                                              i64, ctypes.c_int, vp, ctypes.c_int, i64, vp, i64, vp, i64,
                                              ctypes.c_int, vp, vp, ctypes.c_int, vp, sz, vp]
         lib.rlk_gated_linear_bwd.restype = ctypes.c_int
+        lib.rlk_orthogonalise.argtypes = [vp, ctypes.c_int, i64, i64, i64, i64, i64, i32, vp, f32, vp, i64, i64,
+                                          vp, vp, sz, vp]
+        lib.rlk_orthogonalise.restype = ctypes.c_int
         _lib = lib
         return lib
 
@@ -1392,6 +1396,54 @@ def gated_linear_autograd(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Ten
     """``gated_linear`` as a differentiable op; ``keep_8bit`` keeps x for the
     backward as its 8-bit checkpoint instead of the tensor."""
     return _GatedLinear.apply(x, w_gate, w_up, bias_gate, bias_up, activation, keep_8bit)
+
+
+# ------------------------------------------------------------ orthogonalised updates
+MUON_COEFFICIENTS = (3.4445, -4.7750, 2.0315)
+
+
+@functools.lru_cache(maxsize=64)
+def _coefficients(a, b, c):
+    return (ctypes.c_float * 3)(a, b, c)
+
+
+def _stacked(t, name):
+    """(matrices, rows, columns, row stride, matrix stride) of a [m, n] or [B, m, n] tensor."""
+    if t.dim() not in (2, 3):
+        raise ValueError(f"{name} must be [m, n] or [B, m, n]")
+    m, n = t.shape[-2:]
+    ld, unit = t.stride()[-2:]
+    if unit != 1 and n > 1:
+        raise ValueError(f"{name} must have unit stride along its rows")
+    B, matrix = (1, 0) if t.dim() == 2 else (t.shape[0], t.stride(0))
+    return B, m, n, (ld if m > 1 else n), matrix
+
+
+def orthogonalise(update: torch.Tensor, *, steps: int = 5, coefficients=MUON_COEFFICIENTS, eps: float = 1e-7, out=None,
+                  workspace=None, status_word=None):
+    """``update`` ([m, n], or a stack [B, m, n]; CUDA bf16 or fp32, rows and
+    matrices may be strided) made nearly orthogonal by ``steps`` Newton-Schulz
+    products, bf16 (as an optimiser does between the momentum and the weights).
+    ``out`` may be a bf16 ``update`` itself."""
+    lib = load()
+    _need_cuda(update, out, workspace, status_word)
+    dt = _DTYPES.get(update.dtype)
+    if dt is None:
+        raise ValueError("update must be bf16 or fp32")
+    B, m, n, ld, matrix = _stacked(update, "update")
+    dev = update.device
+    if out is None:
+        out = torch.empty(update.shape, dtype=torch.bfloat16, device=dev)
+    elif out.dtype != torch.bfloat16 or out.shape != update.shape:
+        raise ValueError("out must be bf16, shaped like update")
+    ldo, out_matrix = _stacked(out, "out")[3:]
+    if workspace is None and B > 0:
+        workspace = torch.empty(lib.rlk_workspace_size(OP_ORTHOGONALISE, B, m, n), dtype=torch.uint8, device=dev)
+    code = lib.rlk_orthogonalise(update.data_ptr(), dt, B, m, n, ld, matrix, steps, _coefficients(*coefficients), eps,
+                                 out.data_ptr(), ldo, out_matrix, _ptr(status_word), _ptr(workspace),
+                                 0 if workspace is None else workspace.numel(), _stream(dev))
+    _check("rlk_orthogonalise", code)
+    return out
 
 
 # ------------------------------------------------------------ preference loss

@@ -13,7 +13,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "librlk.so")
 SOURCES = ["rlk_api.cu", "logprob_entropy.cu", "lpe_stream.cu", "lpe_backward.cu", "support.cu", "vocab_parallel.cu", "sampler.cu", "grpo_loss.cu", "lmhead.cu",
-           "checkpoint.cu", "norm.cu", "preference_loss.cu", "linear.cu", "token_logprobs.cu", "gated.cu"]
+           "checkpoint.cu", "norm.cu", "preference_loss.cu", "linear.cu", "token_logprobs.cu", "gated.cu", "orthogonalise.cu"]
 HEADERS = ["common.cuh", "internal.h", "checkpoint.cuh", "tensor_core.cuh", "activation.cuh", "gemm.cuh"]
 INCLUDES = ["rlk.h", "rlk_debug.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -67,7 +67,7 @@ __device__ __forceinline__ void gated_element(const GatedOut& o, int64_t row, in
 }
 
 struct ForwardOp {
-  static constexpr bool A_MN = false, B_MN = false, F16 = false, DUAL = true, SYM = false;
+  static constexpr bool A_MN = false, B_MN = false, F16 = false, DUAL = true, SYM = false, STACKED = false;
   struct Params {
     Loop loop;
     int64_t M, N;
@@ -77,7 +77,7 @@ struct ForwardOp {
   static __device__ __forceinline__ Tile tile(const Params& p, int t, int tm, int bn) {
     int mt, nt;
     gemm::grouped(t, p.n_mt, p.n_nt, mt, nt);
-    return Tile{mt * tm, nt * bn, 0, 0, (int64_t)mt * tm, (int64_t)nt * bn, p.M, p.N, 0, false};
+    return Tile{mt * tm, nt * bn, (int64_t)mt * tm, (int64_t)nt * bn, p.M, p.N, 0, false};
   }
   static __device__ __forceinline__ void source(const Params&, const Tile&, int&, int&, int&) {}
   static __device__ __forceinline__ bool vec(const Params& p) { return p.vec != 0; }
@@ -144,7 +144,7 @@ struct StoreOut {
 // else two products (of which the second takes a[1]), one after the other in the tiles' order.
 template <bool A_MN_, bool KCAT>
 struct StoreOp {
-  static constexpr bool A_MN = A_MN_, B_MN = true, F16 = false, DUAL = false, SYM = false;
+  static constexpr bool A_MN = A_MN_, B_MN = true, F16 = false, DUAL = false, SYM = false, STACKED = false;
   struct Params {
     Loop loop;
     int64_t M, N;
@@ -156,7 +156,7 @@ struct StoreOp {
     const int which = KCAT ? 0 : t / (p.n_mt * p.n_nt);
     int mt, nt;
     gemm::grouped(t - which * p.n_mt * p.n_nt, p.n_mt, p.n_nt, mt, nt);
-    return Tile{mt * tm, nt * bn, 0, 0, (int64_t)mt * tm, (int64_t)nt * bn, p.M, p.N, which, false};
+    return Tile{mt * tm, nt * bn, (int64_t)mt * tm, (int64_t)nt * bn, p.M, p.N, which, false};
   }
   static __device__ __forceinline__ void source(const Params& p, const Tile& tl, int& k, int& ia, int& ib) {
     if (KCAT) {

@@ -16,7 +16,8 @@
 //   DUAL         B's tile is one half of rows of b[0] and one of b[1]: two products that
 //                share A, joined column by column in the epilogue
 //   SYM          D is symmetric: tiles above the diagonal are not computed, off-diagonal ones
-//                are stored twice (pairs' tiles only)
+//                are stored twice
+//   STACKED      maps are of stacks of matrices, of which a tile takes number `which`
 //   Params       with `Loop loop`
 //   tile(p, t, tm, bn)   the place of tile t
 //   source(p, tl, k, ia, ib)   which maps step k takes; k made the step in them
@@ -24,7 +25,7 @@
 //                waited for); Cols, cols8: what it needs for its columns
 //   finish8, finish1   D's 8 columns of a row / one element, to memory; finish8 leaves in v what
 //                was stored (SYM)
-//   turned8      SYM: 8 of D's rows of one column
+//   turned8, turned1   SYM: 8 (1) of D's rows of one column
 #pragma once
 
 #include <math.h>
@@ -61,10 +62,9 @@ struct Maps {
 };
 struct Tile {
   int a_row, b_row;      // first index of the operands' rows (M, N); MN-contiguous: column
-  int a_k, b_k;          // added to the K coordinate
   int64_t row, col;      // first row and column of D
   int64_t rows, cols;    // D's extents
-  int which;             // of several products
+  int which;             // of several products or matrices
   bool turned;           // SYM: also stored transposed
 };
 struct Loop {
@@ -158,12 +158,17 @@ __global__ void __launch_bounds__(Shape<SPLIT>::THREADS, SPLIT ? 2 : 1)
           if (leader) mbar_expect_tx(fb, G * STAGE_BYTES);
           const uint32_t to = G == 2 ? tc::peer_addr(fb, 0u) : fb;
           auto load = [&](uint32_t dst, const CUtensorMap* map, int x, int y) {
-            if (G == 2) tc::load_2d_pair(dst, map, to, x, y);
-            else tc::load_2d(dst, map, to, x, y);
+            if constexpr (Op::STACKED) {
+              if (G == 2) tc::load_3d_pair(dst, map, to, x, y, tl.which);
+              else tc::load_3d(dst, map, to, x, y, tl.which);
+            } else {
+              if (G == 2) tc::load_2d_pair(dst, map, to, x, y);
+              else tc::load_2d(dst, map, to, x, y);
+            }
           };
           int ks = k, ia = 0, ib = 0;
           Op::source(p, tl, ks, ia, ib);
-          const int am = tl.a_row + a_off, ak = tl.a_k + ks * BK, bk = tl.b_k + ks * BK;
+          const int am = tl.a_row + a_off, ak = ks * BK, bk = ks * BK;
           if (Op::A_MN) {
 #pragma unroll
             for (int j = 0; j < BM / 64; ++j) load(sa + j * MN_BLOCK, &maps.a[ia], am + j * 64, ak);
@@ -382,9 +387,11 @@ __global__ void __launch_bounds__(Shape<SPLIT>::THREADS, SPLIT ? 2 : 1)
     const int width = OUT / cluster, c0 = (int)rank * width;
     const int rows = (int)(tl.rows - tl.row < BM ? tl.rows - tl.row : BM);
     if (Op::vec(p)) {
+      // consecutive threads along a row; along a column where D is stored transposed too
       const int octs = width / 8;
-      for (int i = threadIdx.x; i < rows * octs; i += S::THREADS) {
-        const int r = i / octs, c = c0 + (i - r * octs) * 8;
+      for (int i = threadIdx.x; i < (Op::SYM ? BM : rows) * octs; i += S::THREADS) {
+        const int r = Op::SYM ? i % BM : i / octs, c = c0 + (Op::SYM ? i / BM : i - r * octs) * 8;
+        if (r >= rows) continue;
         const int64_t col = tl.col + c;
         if (col >= tl.cols) continue;
         const int n = (int)(tl.cols - col < 8 ? tl.cols - col : 8);
@@ -417,6 +424,13 @@ __global__ void __launch_bounds__(Shape<SPLIT>::THREADS, SPLIT ? 2 : 1)
         typename Op::Cols cols{};
         Op::cols8(p, tl, col, n, cols);
         Op::finish8(p, tl, tl.row + r, col, n, v, u, aux, cols);
+        if constexpr (Op::SYM) {
+          if (tl.turned) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (j < n) Op::turned1(p, tl, tl.row + r, col + j, v[j]);
+          }
+        }
       }
     } else {
       for (int i = threadIdx.x; i < rows * width; i += S::THREADS) {

@@ -409,6 +409,21 @@ size_t gated_bwd_workspace_needed(const GatedBwdArgs& a);
 cudaError_t launch_gated_fwd(const GatedArgs& a, cudaStream_t stream);
 cudaError_t launch_gated_bwd(const GatedBwdArgs& a, cudaStream_t stream);
 
+// Newton-Schulz products (orthogonalise.cu).
+struct OrthArgs {
+  const void* g;
+  int dtype;            // 0 bf16, 1 fp32
+  int64_t B, m, n, ldg, g_matrix;
+  int steps;
+  float coef[3], eps;
+  void* out;            // bf16
+  int64_t ldo, out_matrix;
+  uint32_t* status;
+  void* workspace;
+};
+size_t orth_workspace_bytes(int64_t B, int64_t m, int64_t n);
+cudaError_t launch_orthogonalise(const OrthArgs& a, cudaStream_t stream);
+
 cudaError_t launch_sample(const SampleArgs& a, cudaStream_t stream);
 cudaError_t launch_shard_partials(const ShardArgs& a, cudaStream_t stream);
 cudaError_t launch_shard_combine(const ShardCombineArgs& a, cudaStream_t stream);

@@ -1,0 +1,542 @@
+// rlk_orthogonalise: the polar factor of an update, nearly, by Newton-Schulz products.
+//
+//   X_0 = G / (|G|_F + eps);   A = X X^T,  P = b A + c A^2,  X <- a X + P X,  `steps` times
+// (rows <= columns; else A = X^T X and X <- a X + X P).  Each step maps the singular values by
+// s -> a s + b s^3 + c s^5 and leaves the singular vectors.
+//
+// Three products a step on the tcgen05 kernel of gemm.cuh.  A and P are symmetric, so only the
+// tiles on and below the diagonal are computed and the others stored from them.  Nothing is
+// transposed in memory: X is taken with its rows' or its columns' index contiguous.  A stack
+// of matrices is one launch a product, by three-dimensional tensor maps.
+//
+// Numbers.  The products' operands are fp16 (11 bits where bf16 has 8, at the same rate), held
+// times 2^10: the iterates' entries lie between about 1 / (longer side) and 1.2, so that a matrix
+// of up to 2^14 on a side keeps its typical entries among fp16's normal numbers, and an entry
+// may grow to 64.  X is held in two fp16 (value and rest, 22 bits), since a X carries the small
+// singular values on unrounded: with one, each step's rounding noise is multiplied by a like
+// they are (an update of rank 64 over noise 1 / 50 of it: 0.013 of the result off, with two
+// 0.0004; bf16 0.11).
+// The rounding of A, P and X moves each singular value by up to 0.05 of it in five steps (the
+// polynomial's slope adds up: first-order sum over the steps with u = 2^-11), about 0.0015 on
+// the average of many.  Where the shorter side is kPrecise or less there may be few to average
+// over, and the call is bound by its launches: A and P are held in two fp16 as well, and each
+// product is three (values, value times rest both ways), one sum in the accumulator.
+#include <cuda_fp16.h>
+#include <math.h>
+
+#include "activation.cuh"
+#include "gemm.cuh"
+
+namespace rlk {
+namespace {
+
+using gemm::Loop;
+using gemm::Maps;
+using gemm::Operand;
+using gemm::Tile;
+
+constexpr float kDown = 1.f / 1024.f;   // the operands' scale is 2^10
+constexpr int kPrecise = 256;
+
+int64_t pad8(int64_t n) { return (n + 7) / 8 * 8; }
+size_t pad256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+__device__ __forceinline__ uint32_t pack_half(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 unpack_half(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
+__device__ __forceinline__ void halves(const uint4& q, float (&v)[8]) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 f = unpack_half(w[j]);
+    v[2 * j] = f.x;
+    v[2 * j + 1] = f.y;
+  }
+}
+__device__ __forceinline__ uint4 to_halves(const float (&v)[8]) {
+  return make_uint4(pack_half(v[0], v[1]), pack_half(v[2], v[3]), pack_half(v[4], v[5]), pack_half(v[6], v[7]));
+}
+
+// A stack of B matrices of the iteration, each number in two fp16 (rest may be NULL: one); rows
+// of pad8(columns), columns past the end hold anything.
+struct Buffer {
+  uint16_t *value, *rest;
+  int64_t ld, matrix;   // strides in elements
+  __device__ __forceinline__ int64_t at(int b, int64_t row, int64_t col) const { return b * matrix + row * ld + col; }
+  __device__ __forceinline__ void store8(int64_t i, const float (&v)[8]) const {
+    const uint4 h = to_halves(v);
+    *reinterpret_cast<uint4*>(value + i) = h;
+    if (!rest) return;
+    float x[8];
+    halves(h, x);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = __fsub_rn(v[j], x[j]);
+    *reinterpret_cast<uint4*>(rest + i) = to_halves(x);
+  }
+  __device__ __forceinline__ void store1(int64_t i, float v) const {
+    const uint16_t h = (uint16_t)pack_half(v, 0.f);
+    value[i] = h;
+    if (rest) rest[i] = (uint16_t)pack_half(__fsub_rn(v, unpack_half(h).x), 0.f);
+  }
+};
+// 8 numbers of one, asked for ahead.
+struct Eight {
+  uint4 value, rest;
+  __device__ __forceinline__ void ask(const Buffer& b, int64_t i) {
+    value = *reinterpret_cast<const uint4*>(b.value + i);
+    if (b.rest) rest = *reinterpret_cast<const uint4*>(b.rest + i);   // (else 0)
+  }
+  __device__ __forceinline__ void floats(float (&v)[8]) const {
+    float r[8];
+    halves(value, v);
+    halves(rest, r);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = __fadd_rn(v[j], r[j]);
+  }
+};
+// Step k of a product that is one or three sums of `steps` steps: values, value times rest, rest
+// times value.
+__device__ __forceinline__ void of_three(int steps, int& k, int& ia, int& ib) {
+  const int term = k / steps;
+  k -= term * steps;
+  ia = term == 2;
+  ib = term == 1;
+}
+
+// Tile t of stacked matrices, `per` tiles each.
+__device__ __forceinline__ Tile stacked(int t, int per, int n_mt, int n_nt, int tm, int tn, int64_t rows, int64_t cols, bool sym) {
+  const int b = t / per, r = t - b * per;
+  int mt, nt;
+  if (sym) {   // row mt of the triangle starts at mt (mt + 1) / 2
+    mt = (int)((sqrtf(8.f * (float)r + 1.f) - 1.f) * 0.5f);
+    while ((mt + 1) * (mt + 2) / 2 <= r) ++mt;
+    while (mt * (mt + 1) / 2 > r) --mt;
+    nt = r - mt * (mt + 1) / 2;
+  } else {
+    gemm::grouped(r, n_mt, n_nt, mt, nt);
+  }
+  return Tile{mt * tm, nt * tn, (int64_t)mt * tm, (int64_t)nt * tn, rows, cols, b, sym && mt != nt};
+}
+
+// A = X X^T (MN: X^T X), and P = b A + c A A (POLY).
+template <bool MN, bool POLY>
+struct SquareOp {
+  static constexpr bool A_MN = MN, B_MN = MN, F16 = true, DUAL = false, SYM = true, STACKED = true;
+  struct Params {
+    Loop loop;
+    int per, side, steps;
+    float scale, b;    // of the accumulators; of A (POLY)
+    Buffer a, out;
+  };
+  static __device__ __forceinline__ Tile tile(const Params& p, int t, int tm, int tn) {
+    return stacked(t, p.per, 0, 0, tm, tn, p.side, p.side, true);
+  }
+  static __device__ __forceinline__ void source(const Params& p, const Tile&, int& k, int& ia, int& ib) {
+    of_three(p.steps, k, ia, ib);
+  }
+  static __device__ __forceinline__ bool vec(const Params&) { return true; }
+  struct Aux {
+    Eight a;
+  };
+  static __device__ __forceinline__ void aux8(const Params& p, const Tile& tl, int64_t row, int64_t col, int, Aux& x) {
+    if (POLY) x.a.ask(p.a, p.a.at(tl.which, row, col));
+  }
+  struct Cols {};
+  static __device__ __forceinline__ void cols8(const Params&, const Tile&, int64_t, int, Cols&) {}
+  static __device__ __forceinline__ void finish8(const Params& p, const Tile& tl, int64_t row, int64_t col, int, float (&v)[8],
+                                                 float (&)[8], const Aux& x, const Cols&) {
+    float a[8];
+    if (POLY) x.a.floats(a);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = POLY ? __fmaf_rn(v[j], p.scale, __fmul_rn(a[j], p.b)) : __fmul_rn(v[j], p.scale);
+    p.out.store8(p.out.at(tl.which, row, col), v);   // rows are padded to 8 columns
+  }
+  static __device__ __forceinline__ void finish1(const Params&, const Tile&, int64_t, int64_t, float, float) {}
+  // v: column col of rows row .. row + 7
+  static __device__ __forceinline__ void turned8(const Params& p, const Tile& tl, int64_t row, int64_t col, const float (&v)[8]) {
+    if (col < p.side && row < p.side) p.out.store8(p.out.at(tl.which, col, row), v);
+  }
+  static __device__ __forceinline__ void turned1(const Params& p, const Tile& tl, int64_t row, int64_t col, float v) {
+    p.out.store1(p.out.at(tl.which, col, row), v);
+  }
+};
+
+// X <- a X + P X (TALL: a X + X P), to two fp16 or, the last time, to the caller's bf16.
+template <bool TALL>
+struct ApplyOp {
+  static constexpr bool A_MN = false, B_MN = !TALL, F16 = true, DUAL = false, SYM = false, STACKED = true;
+  struct Params {
+    Loop loop;
+    int per, n_mt, n_nt, steps;
+    int64_t m, n;
+    float a;
+    Buffer x, to;
+    uint16_t* out;          // bf16, or NULL
+    int64_t ldo, out_matrix;
+    int out_vec;            // its rows start on 16-byte boundaries
+  };
+  static __device__ __forceinline__ Tile tile(const Params& p, int t, int tm, int tn) {
+    return stacked(t, p.per, p.n_mt, p.n_nt, tm, tn, p.m, p.n, false);
+  }
+  static __device__ __forceinline__ void source(const Params& p, const Tile&, int& k, int& ia, int& ib) {
+    of_three(p.steps, k, ia, ib);
+  }
+  static __device__ __forceinline__ bool vec(const Params&) { return true; }
+  struct Aux {
+    Eight x;
+  };
+  static __device__ __forceinline__ void aux8(const Params& p, const Tile& tl, int64_t row, int64_t col, int, Aux& x) {
+    x.x.ask(p.x, p.x.at(tl.which, row, col));
+  }
+  struct Cols {};
+  static __device__ __forceinline__ void cols8(const Params&, const Tile&, int64_t, int, Cols&) {}
+  static __device__ __forceinline__ void finish8(const Params& p, const Tile& tl, int64_t row, int64_t col, int n, float (&v)[8],
+                                                 float (&)[8], const Aux& x, const Cols&) {
+    float h[8];
+    x.x.floats(h);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = __fmaf_rn(v[j], kDown, __fmul_rn(p.a, h[j]));
+    if (p.out) {
+      uint16_t* o = p.out + tl.which * p.out_matrix + row * p.ldo + col;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], kDown);
+      if (p.out_vec) {
+        store8(o, v, n);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j < n) o[j] = (uint16_t)pack_bf16(v[j], 0.f);
+      }
+      return;
+    }
+    p.to.store8(p.to.at(tl.which, row, col), v);
+  }
+  static __device__ __forceinline__ void finish1(const Params&, const Tile&, int64_t, int64_t, float, float) {}
+};
+
+// ------------------------------------------------------------ the start
+constexpr int OT = 256;
+
+// 8 columns of a row as floats, 0 past the end; vec: rows start on 16-byte boundaries.
+template <int DT>
+__device__ __forceinline__ void load8(const void* g, int64_t at, int n, bool vec, float (&v)[8]) {
+  if (DT == 0) {
+    const uint16_t* p = static_cast<const uint16_t*>(g) + at;
+    if (vec && n == 8) {
+      const uint4 q = *reinterpret_cast<const uint4*>(p);
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[2 * j] = bf16_lo(w[j]);
+        v[2 * j + 1] = bf16_hi(w[j]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = j < n ? bf16_val(p[j]) : 0.f;
+    }
+  } else {
+    const float* p = static_cast<const float*>(g) + at;
+    if (vec && n == 8) {
+      const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = j < n ? p[j] : 0.f;
+    }
+  }
+}
+
+// Sums of squares in three ranges, so that none over- or underflows: of numbers of 2^40 and
+// more (times 2^-96), of less than 2^-40 (times 2^96), of the others; a group of 8 goes by its
+// largest.
+struct Squares {
+  float small, mid, big;
+};
+constexpr float kBig = 0x1p40f, kSmall = 0x1p-40f;
+__device__ __forceinline__ void add_squares(Squares& s, const float (&v)[8]) {
+  float top = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(v[j]));
+  const float f = top >= kBig ? 0x1p-96f : (top < kSmall ? 0x1p96f : 1.f);
+  float sum = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float x = __fmul_rn(v[j], f);
+    sum = __fmaf_rn(x, x, sum);
+  }
+  if (top >= kBig) s.big = __fadd_rn(s.big, sum);
+  else if (top < kSmall) s.small = __fadd_rn(s.small, sum);
+  else s.mid = __fadd_rn(s.mid, sum);
+}
+
+struct Start {
+  const void* g;
+  int64_t ldg, g_matrix;
+  int64_t m, n;
+  int vec;
+  float eps;
+  int parts;             // of a matrix's sum
+  Squares* sums;         // [B][parts]
+  Buffer x;
+  uint32_t* status;
+};
+
+template <int DT>
+__global__ void __launch_bounds__(OT) orth_norm_kernel(const Start a) {
+  const int b = blockIdx.y;
+  const int64_t base = b * a.g_matrix, octs = (a.n + 7) / 8;
+  Squares s{0.f, 0.f, 0.f};
+  for (int64_t r = blockIdx.x; r < a.m; r += a.parts)
+    for (int64_t i = threadIdx.x; i < octs; i += OT) {
+      float v[8];
+      load8<DT>(a.g, base + r * a.ldg + i * 8, (int)(a.n - i * 8 < 8 ? a.n - i * 8 : 8), a.vec, v);
+      add_squares(s, v);
+    }
+  __shared__ Squares sh[OT / 32];
+  float w[3] = {s.small, s.mid, s.big};
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int k = 0; k < 3; ++k) w[k] = __fadd_rn(w[k], __shfl_xor_sync(0xFFFFFFFFu, w[k], o));
+  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = Squares{w[0], w[1], w[2]};
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    Squares t = sh[0];
+    for (int k = 1; k < OT / 32; ++k) {
+      t.small = __fadd_rn(t.small, sh[k].small);
+      t.mid = __fadd_rn(t.mid, sh[k].mid);
+      t.big = __fadd_rn(t.big, sh[k].big);
+    }
+    a.sums[b * a.parts + blockIdx.x] = t;
+  }
+}
+
+// X_0 = G times one factor, as two powers of two and a number in [1, 2) (the factor itself may
+// be outside fp32's range).
+template <int DT>
+__global__ void __launch_bounds__(OT) orth_start_kernel(const Start a) {
+  pdl_wait();
+  __shared__ float s_f[3];
+  const int b = blockIdx.y;
+  if (threadIdx.x < 32) {
+    double s[3] = {0.0, 0.0, 0.0};
+    for (int k = threadIdx.x; k < a.parts; k += 32) {
+      const Squares q = a.sums[b * a.parts + k];
+      s[0] += (double)q.small;
+      s[1] += (double)q.mid;
+      s[2] += (double)q.big;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+      for (int k = 0; k < 3; ++k) s[k] += __shfl_xor_sync(0xFFFFFFFFu, s[k], o);
+    if (threadIdx.x == 0) {
+      const double norm = sqrt(s[0] * 0x1p-192 + s[1] + s[2] * 0x1p192) + (double)a.eps;
+      if (!(norm < 1e300)) {
+        s_f[0] = NAN;
+        s_f[1] = s_f[2] = 1.f;
+        if (a.status && blockIdx.x == 0) atomicOr(a.status, RLK_STATUS_NONFINITE);
+      } else if (norm == 0.0) {   // eps is 0 and so is G
+        s_f[0] = 0.f;
+        s_f[1] = s_f[2] = 1.f;
+      } else {
+        int e;
+        s_f[0] = (float)(1.0 / frexp(norm, &e));   // in (1, 2]
+        s_f[1] = ldexpf(1.f, -(e / 2) + 5);          // and times 2^10
+        s_f[2] = ldexpf(1.f, -(e - e / 2) + 5);
+      }
+    }
+  }
+  __syncthreads();
+  const float f0 = s_f[0], f1 = s_f[1], f2 = s_f[2];
+  const int64_t base = b * a.g_matrix, octs = (a.n + 7) / 8;
+  for (int64_t r = blockIdx.x; r < a.m; r += gridDim.x)
+    for (int64_t i = threadIdx.x; i < octs; i += OT) {
+      float v[8];
+      load8<DT>(a.g, base + r * a.ldg + i * 8, (int)(a.n - i * 8 < 8 ? a.n - i * 8 : 8), a.vec, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(__fmul_rn(__fmul_rn(v[j], f1), f2), f0);
+      a.x.store8(a.x.at(b, r, i * 8), v);
+    }
+}
+
+// ------------------------------------------------------------ host side
+constexpr int kNormParts = 1024;   // most parts of all matrices' sums, or one each
+
+struct Layout {
+  int64_t side, x_ld, p_ld;
+  int parts;
+  bool precise;
+  size_t x, p, sums;    // bytes of a stack of X, of A or P (one fp16 a number), of the sums
+  size_t total() const { return 4 * x + (precise ? 4 : 2) * p + sums; }
+};
+Layout layout(int64_t B, int64_t m, int64_t n) {
+  Layout l{};
+  l.side = m < n ? m : n;
+  l.precise = l.side <= kPrecise;
+  l.x_ld = pad8(n);
+  l.p_ld = pad8(l.side);
+  int64_t parts = kNormParts / (B > 0 ? B : 1);
+  if (parts > m) parts = m;
+  l.parts = (int)(parts < 1 ? 1 : parts);
+  l.x = pad256((size_t)B * m * l.x_ld * 2);
+  l.p = pad256((size_t)B * l.side * l.p_ld * 2);
+  l.sums = pad256((size_t)B * l.parts * sizeof(Squares));
+  return l;
+}
+
+// Maps of a stack of [rows][cols] matrices: boxes of 64 columns and `box` rows.
+bool stack_map(CUtensorMap* map, void* p, const Buffer& o, int64_t B, int64_t rows, int64_t cols, uint32_t box) {
+  gemm::EncodeTiledFn f = gemm::encode_fn();
+  if (!f) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)B};
+  const cuuint64_t strides[2] = {(cuuint64_t)o.ld * 2, (cuuint64_t)o.matrix * 2};
+  const cuuint32_t boxes[3] = {64u, box, 1u}, estr[3] = {1, 1, 1};
+  return f(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, p, dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Pairs' tiles where small ones would be more than the SMs, as for the linear layer; tiles of
+// a symmetric product on and below the diagonal.
+template <class Op>
+cudaError_t run_square(const Maps& maps, typename Op::Params& p, int64_t B, cudaStream_t stream) {
+  auto triangle = [&](int64_t tm) {
+    const int64_t t = (p.side + tm - 1) / tm;
+    return t * (t + 1) / 2;
+  };
+  const bool few = p.side <= 128 || B * triangle(128) <= sm_count();
+  const int64_t per = triangle(few ? 128 : 256);
+  if (B * per > (1 << 30)) return cudaErrorInvalidValue;
+  p.per = (int)per;
+  p.loop.n_tiles = (int)(B * per);
+  return few ? gemm::launch<Op, true>(maps, p, stream) : gemm::launch<Op, false>(maps, p, stream);
+}
+template <class Op>
+cudaError_t run_apply(const Maps& maps, typename Op::Params& p, int64_t B, cudaStream_t stream) {
+  const int64_t small = B * ((p.m + 127) / 128) * ((p.n + 127) / 128);
+  const bool few = p.m <= 128 || small <= sm_count();
+  const int tm = few ? 128 : 256;
+  p.n_mt = (int)((p.m + tm - 1) / tm);
+  p.n_nt = (int)((p.n + tm - 1) / tm);
+  if (small > (1 << 30)) return cudaErrorInvalidValue;
+  p.per = p.n_mt * p.n_nt;
+  p.loop.n_tiles = (int)(B * p.per);
+  return few ? gemm::launch<Op, true>(maps, p, stream) : gemm::launch<Op, false>(maps, p, stream);
+}
+
+template <bool TALL>
+cudaError_t iterate(const OrthArgs& a, const Layout& l, cudaStream_t stream) {
+  char* ws = static_cast<char*>(a.workspace);
+  auto take = [&](size_t bytes) {
+    char* p = ws;
+    ws += bytes;
+    return reinterpret_cast<uint16_t*>(p);
+  };
+  Buffer x[2], gram{}, poly{};
+  for (Buffer& b : x) b = Buffer{take(l.x), take(l.x), l.x_ld, l.x_ld * a.m};
+  for (Buffer* b : {&gram, &poly}) *b = Buffer{take(l.p), l.precise ? take(l.p) : nullptr, l.p_ld, l.p_ld * l.side};
+  Start s{};
+  s.g = a.g;
+  s.ldg = a.ldg;
+  s.g_matrix = a.g_matrix;
+  s.m = a.m;
+  s.n = a.n;
+  const int64_t group = a.dtype ? 4 : 8;
+  s.vec = reinterpret_cast<uintptr_t>(a.g) % 16 == 0 && (a.m == 1 || a.ldg % group == 0) && (a.B == 1 || a.g_matrix % group == 0);
+  s.eps = a.eps;
+  s.parts = l.parts;
+  s.sums = reinterpret_cast<Squares*>(ws);
+  s.x = x[0];
+  s.status = a.status;
+  const dim3 sums((unsigned)l.parts, (unsigned)a.B);
+  if (a.dtype == 0) orth_norm_kernel<0><<<sums, OT, 0, stream>>>(s);
+  else orth_norm_kernel<1><<<sums, OT, 0, stream>>>(s);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  int64_t rows = (int64_t)sm_count() * 8 / a.B;
+  rows = rows < 1 ? 1 : (rows > a.m ? a.m : rows);
+  e = launch_after(a.dtype == 0 ? orth_start_kernel<0> : orth_start_kernel<1>, dim3((unsigned)rows, (unsigned)a.B), dim3(OT), 0, stream, s);
+  if (e != cudaSuccess) return e;
+
+  using Gram = SquareOp<TALL, false>;
+  using Poly = SquareOp<false, true>;
+  using Apply = ApplyOp<TALL>;
+  // maps of both halves of X in boxes of 128 rows, and of 64 (its columns' index contiguous), of A, of P
+  CUtensorMap of_x[2][2][2], of_gram[2], of_poly[2];
+  bool ok = true;
+  for (int h = 0; h < 2; ++h) {
+    for (int i = 0; i < 2; ++i)
+      for (int j = 0; j < 2; ++j)
+        ok = ok && stack_map(&of_x[i][j][h], h ? x[i].rest : x[i].value, x[i], a.B, a.m, a.n, j ? 64 : 128);
+    const bool two = h && l.precise;   // else never taken
+    ok = ok && stack_map(&of_gram[h], two ? gram.rest : gram.value, gram, a.B, l.side, l.side, 128) &&
+         stack_map(&of_poly[h], two ? poly.rest : poly.value, poly, a.B, l.side, l.side, 128);
+  }
+  if (!ok) return cudaErrorInvalidValue;
+  auto set = [](CUtensorMap (&to)[2], const CUtensorMap (&from)[2]) {
+    to[0] = from[0];
+    to[1] = from[1];
+  };
+  const int64_t longer = a.m < a.n ? a.n : a.m;
+  const int terms = l.precise ? 3 : 1, side_steps = (int)((l.side + gemm::BK - 1) / gemm::BK);
+  for (int k = 0; k < a.steps; ++k) {
+    const int i = k & 1;
+    Maps maps;
+    set(maps.a, of_x[i][TALL]);
+    set(maps.b, of_x[i][TALL]);
+    typename Gram::Params g{};
+    g.steps = (int)((longer + gemm::BK - 1) / gemm::BK);
+    g.loop.k_steps = terms * g.steps;
+    g.side = (int)l.side;
+    g.scale = kDown;
+    g.out = gram;
+    if ((e = run_square<Gram>(maps, g, a.B, stream)) != cudaSuccess) return e;
+    set(maps.a, of_gram);
+    set(maps.b, of_gram);
+    typename Poly::Params q{};
+    q.steps = side_steps;
+    q.loop.k_steps = terms * side_steps;
+    q.side = (int)l.side;
+    q.scale = a.coef[2] * kDown;
+    q.b = a.coef[1];
+    q.a = gram;
+    q.out = poly;
+    if ((e = run_square<Poly>(maps, q, a.B, stream)) != cudaSuccess) return e;
+    if (TALL) {
+      set(maps.a, of_x[i][0]);
+      set(maps.b, of_poly);
+    } else {
+      set(maps.a, of_poly);
+      set(maps.b, of_x[i][1]);
+    }
+    typename Apply::Params p{};
+    p.steps = side_steps;
+    p.loop.k_steps = terms * side_steps;
+    p.m = a.m;
+    p.n = a.n;
+    p.a = a.coef[0];
+    p.x = x[i];
+    p.to = x[i ^ 1];
+    if (k == a.steps - 1) {
+      p.out = static_cast<uint16_t*>(a.out);
+      p.ldo = a.ldo;
+      p.out_matrix = a.out_matrix;
+      p.out_vec = reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && (a.m == 1 || a.ldo % 8 == 0) && (a.B == 1 || a.out_matrix % 8 == 0);
+    }
+    if ((e = run_apply<Apply>(maps, p, a.B, stream)) != cudaSuccess) return e;
+  }
+  return e;
+}
+
+}  // namespace
+
+size_t orth_workspace_bytes(int64_t B, int64_t m, int64_t n) { return layout(B, m, n).total(); }
+
+cudaError_t launch_orthogonalise(const OrthArgs& a, cudaStream_t stream) {
+  const Layout l = layout(a.B, a.m, a.n);
+  return a.m > a.n ? iterate<true>(a, l, stream) : iterate<false>(a, l, stream);
+}
+
+}  // namespace rlk

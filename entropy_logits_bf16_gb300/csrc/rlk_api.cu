@@ -133,6 +133,8 @@ const char* rlk_status_string(rlk_status status) {
   return "unknown status";
 }
 
+constexpr int64_t kMaxMatrices = 65535, kMaxSide = 65536;   // of rlk_orthogonalise
+
 size_t rlk_workspace_size(int op, int64_t T, int64_t V, int64_t H) {
   if (T < 0 || V < 0 || H < 0) return 0;
   switch (op) {
@@ -147,6 +149,8 @@ size_t rlk_workspace_size(int op, int64_t T, int64_t V, int64_t H) {
     case RLK_OP_LINEAR_BWD: return rlk::linear_bwd_workspace_bytes(T, V, H);
     case RLK_OP_GATED_LINEAR: return rlk::gated_workspace_bytes(T, V, H);
     case RLK_OP_GATED_LINEAR_BWD: return rlk::gated_bwd_workspace_bytes(T, V, H);
+    case RLK_OP_ORTHOGONALISE:
+      return T > kMaxMatrices || V > kMaxSide || H > kMaxSide ? 0 : rlk::orth_workspace_bytes(T, V, H);
     case RLK_OP_CANONICAL:
       return V < 1 ? 0 : (size_t)V * (size_t)T * sizeof(rlk_shard_partial);
     case RLK_OP_CANONICAL_TOPP:
@@ -1344,6 +1348,45 @@ rlk_status rlk_gated_linear_bwd(const void* dy, int64_t lddy, const void* x, int
     return RLK_ERR_WORKSPACE;
   if (rlk::take_injected_failure()) return RLK_ERR_CUDA;
   return rlk::launch_gated_bwd(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? RLK_OK
+             : RLK_ERR_CUDA;
+}
+
+rlk_status rlk_orthogonalise(const void* g, rlk_dtype dtype, int64_t n_matrices, int64_t m,
+                             int64_t n, int64_t ldg, int64_t matrix_stride, int32_t steps,
+                             const float* coefficients, float eps, void* out, int64_t ldo,
+                             int64_t out_matrix_stride, uint32_t* out_status_word,
+                             void* workspace, size_t workspace_bytes, rlk_stream stream) {
+  if (!good_dtype(dtype) || n_matrices < 0 || n_matrices > kMaxMatrices || m < 1 || m > kMaxSide || n < 1 ||
+      n > kMaxSide || steps < 1 || steps > 64 || !coefficients || !(std::isfinite(eps) && eps >= 0.0f))
+    return RLK_ERR_INVALID_ARG;
+  for (int i = 0; i < 3; ++i)
+    if (!(std::fabs(coefficients[i]) <= 16.0f)) return RLK_ERR_INVALID_ARG;
+  if ((m > 1 && (ldg < n || ldo < n)) || matrix_stride < 0) return RLK_ERR_INVALID_ARG;
+  if (n_matrices > 1 && out_matrix_stride < (m > 1 ? (m - 1) * ldo : 0) + n) return RLK_ERR_INVALID_ARG;
+  if (n_matrices == 0) return RLK_OK;
+  if (!g || !out || !elem_aligned(g, dtype) || !aligned_to(out, 2) || !aligned_to(out_status_word, 4))
+    return RLK_ERR_INVALID_ARG;
+  if (!workspace || workspace_bytes < rlk::orth_workspace_bytes(n_matrices, m, n) || !aligned_to(workspace, 16))
+    return RLK_ERR_WORKSPACE;
+  rlk::OrthArgs a{};
+  a.g = g;
+  a.dtype = dtype_index(dtype);
+  a.B = n_matrices;
+  a.m = m;
+  a.n = n;
+  a.ldg = m > 1 ? ldg : n;
+  a.g_matrix = matrix_stride;
+  a.steps = steps;
+  for (int i = 0; i < 3; ++i) a.coef[i] = coefficients[i];
+  a.eps = eps;
+  a.out = out;
+  a.ldo = m > 1 ? ldo : n;
+  a.out_matrix = out_matrix_stride;
+  a.status = out_status_word;
+  a.workspace = workspace;
+  if (rlk::take_injected_failure()) return RLK_ERR_CUDA;
+  return rlk::launch_orthogonalise(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? RLK_OK
              : RLK_ERR_CUDA;
 }

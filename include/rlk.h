@@ -90,7 +90,7 @@ enum { RLK_OP_LOGPROB_ENTROPY = 0, RLK_OP_GRPO_LOSS = 1, RLK_OP_LMHEAD = 2,
        RLK_OP_LMHEAD_BWD = 3, RLK_OP_LMHEAD_TOPP = 4, RLK_OP_CANONICAL = 5,
        RLK_OP_CANONICAL_TOPP = 6, RLK_OP_NORM_BWD = 7, RLK_OP_PREFERENCE_LOSS = 8,
        RLK_OP_LINEAR = 9, RLK_OP_LINEAR_BWD = 10, RLK_OP_GATED_LINEAR = 11,
-       RLK_OP_GATED_LINEAR_BWD = 12 };
+       RLK_OP_GATED_LINEAR_BWD = 12, RLK_OP_ORTHOGONALISE = 13 };
 
 /* Bits OR-ed into *out_status_word by the kernels. */
 #define RLK_STATUS_BAD_TOKEN_ID 0x1u   /* a token id outside [0, V)          */
@@ -159,6 +159,7 @@ const char* rlk_status_string(rlk_status status);
  *  RLK_OP_LINEAR_BWD:      the same (rlk_linear_bwd)
  *  RLK_OP_GATED_LINEAR:    the same (rlk_gated_linear_fwd)
  *  RLK_OP_GATED_LINEAR_BWD: the same (rlk_gated_linear_bwd)
+ *  RLK_OP_ORTHOGONALISE:   T matrices of V = m rows and H = n columns
  * Returns 0 for an unknown op or negative sizes. */
 size_t rlk_workspace_size(int op, int64_t T, int64_t V, int64_t H);
 
@@ -1272,6 +1273,57 @@ rlk_status rlk_gated_linear_bwd(const void* dy, int64_t lddy, const void* x, int
                                 rlk_dtype grad_w_dtype, float* grad_bias_gate,
                                 float* grad_bias_up, int accumulate, void* workspace,
                                 size_t workspace_bytes, rlk_stream stream);
+
+/*
+ * rlk_orthogonalise -- updates made nearly orthogonal by Newton-Schulz products
+ * (the step of the Muon optimiser between the momentum and the weights).
+ *
+ * For each matrix G (m x n) of a stack:
+ *   X = G / (|G|_F + eps), then `steps` times
+ *   m <= n:  A = X X^T,  X <- a X + (b A + c A A) X
+ *   m > n:   A = X^T X,  X <- a X + X (b A + c A A)
+ * with (a, b, c) = coefficients: the singular values go through
+ * s -> a s + b s^3 + c s^5, the singular vectors stay.
+ * The norm is formed in fp32 without over- or underflow, the factor applied in
+ * fp32; the products take fp16 operands (scaled by a power of two) with fp32
+ * accumulation, X is carried in 22 bits between the steps, and the result is
+ * rounded once to bf16.  Where the shorter side is over 256 the operands have 11
+ * bits: each singular value is off by up to 0.05 of it after five steps, the
+ * whole by about 0.0015 of its root mean square (bf16's rounding alone costs
+ * 0.0017); up to 256 they have 22, and the rounding to bf16 is what remains.
+ *
+ * Arguments
+ *  g               device, dtype `dtype`: element (i, r, c) at
+ *                  g[i * matrix_stride + r * ldg + c].
+ *  n_matrices, m, n   0 to 65535 matrices; 1 <= m, n <= 65536.
+ *  ldg, matrix_stride   ldg >= n (any, for m == 1); matrix_stride >= 0 (it may be 0
+ *                  or overlap rows: g is only read).
+ *  steps           1 to 64.
+ *  coefficients    host pointer to a, b, c (read before the call returns): finite,
+ *                  each at most 16 in magnitude.  An iteration that they make
+ *                  diverge past entries of 64 ends in infinities or NaN; entries below
+ *                  2^-24 count with their bits above 2^-34 only.
+ *  eps             finite, >= 0 (with 0 a matrix of zeros gives zeros).
+ *  out             device bf16, laid out by ldo (>= n) and out_matrix_stride (>= m rows:
+ *                  (m - 1) ldo + n); may be g itself (same address and strides, bf16),
+ *                  may not overlap it otherwise.
+ *  out_status_word device uint32[1] or NULL: a matrix with a NaN or an infinity gives
+ *                  NaN and RLK_STATUS_NONFINITE; the others are not affected.
+ *  workspace       at least rlk_workspace_size(RLK_OP_ORTHOGONALISE, n_matrices, m, n)
+ *                  bytes (about 8 m n + 4 min(m, n)^2 a matrix, or + 8), 16-byte aligned,
+ *                  contents on entry do not matter.
+ * Deterministic.  A matrix's last bits may depend on how many are in the call
+ * (sums are split by the tiles there are).  Tiles whose operands did not come
+ * within the limit of a wait (about a second) are NaN.
+ * Errors: RLK_ERR_INVALID_ARG for sizes, strides or numbers outside the rules, a
+ *  bad dtype, null or misaligned pointers; RLK_ERR_WORKSPACE.  n_matrices == 0
+ *  returns RLK_OK without launching.
+ */
+rlk_status rlk_orthogonalise(const void* g, rlk_dtype dtype, int64_t n_matrices, int64_t m,
+                             int64_t n, int64_t ldg, int64_t matrix_stride, int32_t steps,
+                             const float* coefficients, float eps, void* out, int64_t ldo,
+                             int64_t out_matrix_stride, uint32_t* out_status_word,
+                             void* workspace, size_t workspace_bytes, rlk_stream stream);
 
 #ifdef __cplusplus
 }  /* extern "C" */

@@ -71,7 +71,28 @@ def test_gated_linear_backward_accumulates_in_fp32_only(lib):
     assert lib.rlk_gated_linear_bwd(*{**GATED_BWD, "acc": 1, "dwt": 0}.values(), None) == 2
 
 
-def test_no_rows(lib):
+COEF = (ctypes.c_float * 3)(3.4445, -4.7750, 2.0315)
+ORTH = dict(g=P, dtype=0, B=2, m=8, n=16, ldg=16, stride=128, steps=5, coef=COEF, eps=1e-7, out=P, ldo=16, ostride=128, status=P, ws=P, wsb=1 << 30)
+
+
+@pytest.mark.parametrize("change", [dict(dtype=2), dict(B=-1), dict(B=65536), dict(m=0), dict(m=65537), dict(n=0), dict(n=65537, ldg=70000, ldo=70000), dict(ldg=15), dict(ldo=15),
+                                    dict(stride=-1), dict(ostride=127), dict(steps=0), dict(steps=65), dict(coef=None), dict(coef=(ctypes.c_float * 3)(1, 17, 0)),
+                                    dict(coef=(ctypes.c_float * 3)(float("nan"), 0, 0)), dict(eps=-1.0), dict(eps=float("nan")), dict(g=0), dict(out=0), dict(g=P + 1),
+                                    dict(dtype=1, g=P + 2), dict(out=P + 1), dict(status=P + 2)], ids=lambda c: "-".join(c))
+def test_orthogonalise_refuses(lib, change):
+    assert lib.rlk_orthogonalise(*{**ORTH, **change}.values(), None) == BAD
+
+
+def test_orthogonalise_workspace(lib):
+    need = lib.rlk_workspace_size(rlk.OP_ORTHOGONALISE, 2, 8, 16)
+    assert need >= 2 * (4 * 8 * 16 * 2 + 2 * 8 * 8 * 2)
+    for change in (dict(ws=0), dict(ws=P + 8), dict(wsb=need - 1)):
+        assert lib.rlk_orthogonalise(*{**ORTH, **change}.values(), None) == 3
+    assert lib.rlk_workspace_size(rlk.OP_ORTHOGONALISE, 70000, 8, 16) == 0
+
+
+def test_nothing_to_do(lib):
+    assert lib.rlk_orthogonalise(*{**ORTH, "B": 0, "g": 0, "ws": 0}.values(), None) == OK
     assert lib.rlk_gated_linear_fwd(*{**GATED, "M": 0, "x": 0}.values(), None) == OK
     assert lib.rlk_gated_linear_bwd(*{**GATED_BWD, "M": 0, "dwg": 0, "dwu": 0, "dbg": 0, "dbu": 0}.values(), None) == OK
     assert lib.rlk_token_logprobs_fwd(*{**FWD, "T": 0, "logits": 0}.values(), None) == OK
@@ -80,7 +101,7 @@ def test_no_rows(lib):
 
 def test_injected_failures(lib):
     for call, args in ((lib.rlk_token_logprobs_fwd, FWD), (lib.rlk_token_logprobs_bwd, BWD), (lib.rlk_gated_linear_fwd, GATED),
-                       (lib.rlk_gated_linear_bwd, GATED_BWD)):
+                       (lib.rlk_gated_linear_bwd, GATED_BWD), (lib.rlk_orthogonalise, ORTH)):
         rlk.inject_launch_failures(1)
         assert call(*args.values(), None) == 4
     assert rlk.inject_launch_failures(0) == 0
