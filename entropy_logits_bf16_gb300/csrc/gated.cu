@@ -52,18 +52,37 @@ __device__ __forceinline__ float gated_bias(const GatedOut& o, int which, int64_
   return o.bias_dtype ? static_cast<const float*>(o.bias[which])[col]
                       : bf16_val(static_cast<const uint16_t*>(o.bias[which])[col]);
 }
-__device__ __forceinline__ void gated_element(const GatedOut& o, int64_t row, int64_t col, float g, float u) {
-  if (o.bias[0]) g = __fadd_rn(g, gated_bias(o, 0, col));
-  if (o.bias[1]) u = __fadd_rn(u, gated_bias(o, 1, col));
-  if (o.z[0]) {
-    o.z[0][row * o.ldz + col] = (uint16_t)pack_bf16(g, 0.f);
-    o.z[1][row * o.ldz + col] = (uint16_t)pack_bf16(u, 0.f);
+// One column of R rows `step` apart, of which those up to n rows on exist.
+template <int R>
+__device__ __forceinline__ void gated_column(const GatedOut& o, int64_t row, int step, int n, int64_t col, float (&g)[R], float (&u)[R]) {
+  if (o.bias[0]) {
+    const float b = gated_bias(o, 0, col);
+#pragma unroll
+    for (int k = 0; k < R; ++k) g[k] = __fadd_rn(g[k], b);
   }
-  float a[1] = {g};
-  activate(a, o.act);
-  const float y = __fmul_rn(a[0], u);
-  if (o.y_dtype) static_cast<float*>(o.y)[row * o.ldy + col] = y;
-  else static_cast<uint16_t*>(o.y)[row * o.ldy + col] = (uint16_t)pack_bf16(y, 0.f);
+  if (o.bias[1]) {
+    const float b = gated_bias(o, 1, col);
+#pragma unroll
+    for (int k = 0; k < R; ++k) u[k] = __fadd_rn(u[k], b);
+  }
+  if (o.z[0]) {
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      if (k * step >= n) continue;
+      const int64_t at = (row + k * step) * o.ldz + col;
+      o.z[0][at] = (uint16_t)pack_bf16(g[k], 0.f);
+      o.z[1][at] = (uint16_t)pack_bf16(u[k], 0.f);
+    }
+  }
+  activate(g, o.act);
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    if (k * step >= n) continue;
+    const float y = __fmul_rn(g[k], u[k]);
+    const int64_t at = (row + k * step) * o.ldy + col;
+    if (o.y_dtype) static_cast<float*>(o.y)[at] = y;
+    else static_cast<uint16_t*>(o.y)[at] = (uint16_t)pack_bf16(y, 0.f);
+  }
 }
 
 struct ForwardOp {
@@ -130,8 +149,9 @@ struct ForwardOp {
         if (j < n) y[j] = g[j];
     }
   }
-  static __device__ __forceinline__ void finish1(const Params& p, const Tile&, int64_t row, int64_t col, float g, float u) {
-    gated_element(p.out, row, col, g, u);
+  static __device__ __forceinline__ void column8(const Params& p, const Tile&, int64_t row, int step, int n, int64_t col,
+                                                 float (&g)[8], float (&u)[8]) {
+    gated_column<8>(p.out, row, step, n, col, g, u);
   }
 };
 
@@ -197,13 +217,19 @@ struct StoreOp {
         if (j < n) y[j] = p.accumulate ? __fadd_rn(y[j], v[j]) : v[j];
     }
   }
-  static __device__ __forceinline__ void finish1(const Params& p, const Tile& tl, int64_t row, int64_t col, float v, float) {
+  static __device__ __forceinline__ void column8(const Params& p, const Tile& tl, int64_t row, int step, int n, int64_t col,
+                                                 float (&v)[8], float (&)[8]) {
     const StoreOut& o = p.out[tl.which];
-    if (p.y_dtype == 0) {
-      static_cast<uint16_t*>(o.y)[row * o.ld + col] = (uint16_t)pack_bf16(v, 0.f);
-    } else {
-      float* y = static_cast<float*>(o.y) + row * o.ld + col;
-      *y = p.accumulate ? __fadd_rn(*y, v) : v;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (k * step >= n) continue;
+      const int64_t at = (row + k * step) * o.ld + col;
+      if (p.y_dtype == 0) {
+        static_cast<uint16_t*>(o.y)[at] = (uint16_t)pack_bf16(v[k], 0.f);
+      } else {
+        float* y = static_cast<float*>(o.y) + at;
+        *y = p.accumulate ? __fadd_rn(*y, v[k]) : v[k];
+      }
     }
   }
 };
@@ -333,12 +359,12 @@ __global__ void __launch_bounds__(FEW_T, R <= 2 ? 4 : 3) gated_few_rows_kernel(c
   }
   __syncthreads();
   if (part != 0 || f >= a.N || lane >= R) return;
-  float g = 0.f, u = 0.f;
+  float g[1] = {0.f}, u[1] = {0.f};
   for (int k = 0; k < a.wpf; ++k) {
-    g = __fadd_rn(g, s_part[warp + k][2 * lane]);
-    u = __fadd_rn(u, s_part[warp + k][2 * lane + 1]);
+    g[0] = __fadd_rn(g[0], s_part[warp + k][2 * lane]);
+    u[0] = __fadd_rn(u[0], s_part[warp + k][2 * lane + 1]);
   }
-  gated_element(a.out, lane, f, g, u);
+  gated_column<1>(a.out, lane, 1, 1, f, g, u);
 }
 
 template <int R>
@@ -517,7 +543,8 @@ cudaError_t launch_gated_fwd(const GatedArgs& a, cudaStream_t stream) {
   if (cudaError_t e = aligned_operands({{&x, a.M, a.K}, {&wg, a.N, a.K}, {&wu, a.N, a.K}}, ws, stream); e != cudaSuccess) return e;
   const bool few = few_tiles(a.M, a.N, 1, 64);
   Maps maps;
-  if (!gemm::make_map(&maps.a[0], false, x, false, a.M, a.K) ||
+  const int a_rows = few && a.M < 128 ? (int)pad8(a.M) : 128;
+  if (!gemm::make_map(&maps.a[0], false, x, false, a.M, a.K, a_rows) ||
       !gemm::make_map(&maps.b[0], false, wg, false, a.N, a.K, few ? 64 : 128) ||
       !gemm::make_map(&maps.b[1], false, wu, false, a.N, a.K, few ? 64 : 128))
     return cudaErrorInvalidValue;
@@ -526,6 +553,7 @@ cudaError_t launch_gated_fwd(const GatedArgs& a, cudaStream_t stream) {
   p.M = a.M;
   p.N = a.N;
   p.loop.k_steps = (int)((a.K + gemm::BK - 1) / gemm::BK);
+  p.loop.a_rows = a_rows;
   p.vec = rows16(a.y, a.y_dtype, a.ldy) && (!a.z[0] || (rows16(a.z[0], 0, a.ldz) && rows16(a.z[1], 0, a.ldz)));
   p.out = out;
   return run_tiles<ForwardOp>(maps, p, 1, 64, few, stream);
@@ -594,7 +622,9 @@ cudaError_t launch_gated_bwd(const GatedBwdArgs& a, cudaStream_t stream) {
   Maps maps;
   if (a.dx) {   // K runs over N twice; the weights [N][K] hold its columns contiguously
     using Op = StoreOp<false, true>;
-    if (!gemm::make_map(&maps.a[0], false, g, false, a.M, a.N) || !gemm::make_map(&maps.a[1], false, u, false, a.M, a.N) ||
+    const bool few = few_tiles(a.M, a.K, 1, 128);
+    const int a_rows = few && a.M < 128 ? (int)pad8(a.M) : 128;
+    if (!gemm::make_map(&maps.a[0], false, g, false, a.M, a.N, a_rows) || !gemm::make_map(&maps.a[1], false, u, false, a.M, a.N, a_rows) ||
         !gemm::make_map(&maps.b[0], false, wg, true, a.K, a.N) || !gemm::make_map(&maps.b[1], false, wu, true, a.K, a.N))
       return cudaErrorInvalidValue;
     Op::Params p{};
@@ -602,10 +632,11 @@ cudaError_t launch_gated_bwd(const GatedBwdArgs& a, cudaStream_t stream) {
     p.N = a.K;
     p.half = (int)((a.N + gemm::BK - 1) / gemm::BK);
     p.loop.k_steps = 2 * p.half;
+    p.loop.a_rows = a_rows;
     p.vec = rows16(a.dx, a.dx_dtype, a.lddx);
     p.y_dtype = a.dx_dtype;
     p.out[0] = StoreOut{a.dx, a.lddx};
-    if ((e = run_tiles<Op>(maps, p, 1, 128, few_tiles(p.M, p.N, 1, 128), stream)) != cudaSuccess) return e;
+    if ((e = run_tiles<Op>(maps, p, 1, 128, few, stream)) != cudaSuccess) return e;
   }
   if (a.dw[0]) {   // K is M; every operand holds its rows' index contiguously
     if (!a.x) {    // the checkpoint's values are exact in bf16

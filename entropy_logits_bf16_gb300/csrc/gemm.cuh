@@ -23,8 +23,8 @@
 //   source(p, tl, k, ia, ib)   which maps step k takes; k made the step in them
 //   Aux, aux8    what finish8 needs from memory for its row (asked for before the accumulator is
 //                waited for); Cols, cols8: what it needs for its columns
-//   finish8, finish1   D's 8 columns of a row / one element, to memory; finish8 leaves in v what
-//                was stored (SYM)
+//   finish8, column8   D's 8 columns of a row / one column of 8 rows `step` apart (of which those
+//                up to n rows on exist), to memory; finish8 leaves in v what was stored (SYM)
 //   turned8, turned1   SYM: 8 (1) of D's rows of one column
 #pragma once
 
@@ -69,6 +69,7 @@ struct Tile {
 };
 struct Loop {
   int n_tiles, k_steps, stages;
+  int a_rows;            // rows of A's boxes (K-contiguous, tiles of 128 x 128; else 128)
   long long wait_limit;
   int withhold;          // debug: the stage of the first CTA whose barrier waits for an arrival that never comes (-1: none)
 };
@@ -120,6 +121,9 @@ __global__ void __launch_bounds__(Shape<SPLIT>::THREADS, SPLIT ? 2 : 1)
     *abort_flag = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
+    tc::prefetch_map(&maps.a[0]);
+    tc::prefetch_map(&maps.b[0]);
+    if (Op::DUAL) tc::prefetch_map(&maps.b[1]);
   }
   if (warp == 1) tc::alloc<G>(smem_u32(tmem_slot), TMEM_COLS);
   tc::fence_before();
@@ -138,6 +142,8 @@ __global__ void __launch_bounds__(Shape<SPLIT>::THREADS, SPLIT ? 2 : 1)
   const int k1 = SPLIT ? (int)((int64_t)(rank + 1) * p.loop.k_steps / cluster) : p.loop.k_steps;
   const int a_off = SPLIT ? 0 : (int)rank * BM;
   const bool leader = SPLIT || rank == 0;
+  // a tile of fewer rows is fetched without the rest (whose accumulators nobody looks at)
+  const uint32_t bytes = G * STAGE_BYTES - (SPLIT && !Op::A_MN ? (uint32_t)(BM - p.loop.a_rows) * BK * 2 : 0u);
 
   if (warp == 0) {
     // ------------------------------------------------------ TMA producer
@@ -155,7 +161,7 @@ __global__ void __launch_bounds__(Shape<SPLIT>::THREADS, SPLIT ? 2 : 1)
           const uint32_t fb = full0 + 8 * stage;
           const uint32_t sa = base + stage * STAGE_BYTES, sb = sa + A_BYTES;
           // a pair's copies all report to the even CTA, whose barrier expects them all
-          if (leader) mbar_expect_tx(fb, G * STAGE_BYTES);
+          if (leader) mbar_expect_tx(fb, bytes);
           const uint32_t to = G == 2 ? tc::peer_addr(fb, 0u) : fb;
           auto load = [&](uint32_t dst, const CUtensorMap* map, int x, int y) {
             if constexpr (Op::STACKED) {
@@ -353,22 +359,29 @@ __global__ void __launch_bounds__(Shape<SPLIT>::THREADS, SPLIT ? 2 : 1)
               }
             }
           } else {
+            // a lane: one column, 8 rows at a time, so that a warp stores 32 consecutive columns
             const int rows = (int)(tl.rows - row0 < 32 ? tl.rows - row0 : 32);
-            float o[Op::DUAL ? 32 : 1];
-            if constexpr (Op::DUAL) {
+            float o[TWICE ? 32 : 1];
+            if constexpr (TWICE) {
 #pragma unroll
               for (int r = 0; r < 32; ++r) o[r] = get1(r);
               __syncwarp();
               read32(v, OUT + c0);
               release();
               stage_in(v);
+            }
+            if (col0 + lane < tl.cols) {
 #pragma unroll
-              for (int r = 0; r < 32; ++r)
-                if (r < rows && col0 + lane < tl.cols) Op::finish1(p, tl, row0 + r, col0 + lane, o[r], get1(r));
-            } else {
-#pragma unroll 8
-              for (int r = 0; r < rows; ++r)
-                if (col0 + lane < tl.cols) Op::finish1(p, tl, row0 + r, col0 + lane, get1(r), 0.f);
+              for (int r = 0; r < 32; r += 8) {
+                if (r >= rows) continue;
+                float x[8], w[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                  w[j] = get1(r + j);
+                  x[j] = TWICE ? o[TWICE ? r + j : 0] : w[j];
+                }
+                Op::column8(p, tl, row0 + r, 1, rows - r, col0 + lane, x, w);
+              }
             }
             __syncwarp();
           }
@@ -377,26 +390,39 @@ __global__ void __launch_bounds__(Shape<SPLIT>::THREADS, SPLIT ? 2 : 1)
     }
   }
   if constexpr (SPLIT) {
+    const Tile tl = Op::tile(p, tile0, TM, OUT);
+    const int width = OUT / cluster, c0 = (int)rank * width;   // this CTA's share of the columns, all rows
+    const int rows = (int)(tl.rows - tl.row < BM ? tl.rows - tl.row : BM);
+    // 8 columns of a row at a time: consecutive threads along a row; along a column where D is
+    // stored transposed too.  What an item needs from memory is asked for an item ahead.
+    const int octs = width / 8, items = (Op::SYM ? BM : rows) * octs;
+    auto place = [&](int i, int& r, int& c, int& n) {
+      r = Op::SYM ? i % BM : i / octs;
+      c = c0 + (Op::SYM ? i / BM : i - r * octs) * 8;
+      const int64_t left = tl.cols - tl.col - c;
+      n = i < items && r < rows ? (int)(left < 8 ? (left > 0 ? left : 0) : 8) : 0;
+    };
+    const bool vec = Op::vec(p);
+    typename Op::Aux next{};
+    if (vec) {
+      int r, c, n;
+      place((int)threadIdx.x, r, c, n);
+      if (n > 0) Op::aux8(p, tl, tl.row + r, tl.col + c, n, next);
+    }
     __syncwarp();
     tc::cluster_sync();   // every partial tile is in its CTA's shared memory
     bool dead = false;    // a wait of some CTA of the cluster ran out
     const uint32_t abort_at = smem_u32(bars + 2 * MAX_STAGES + 4);
     for (int k = 0; k < cluster; ++k) dead = tc::ld_peer_u32(tc::peer_addr(abort_at, (uint32_t)k)) != 0u || dead;
-    // this CTA's share of the columns, all rows
-    const Tile tl = Op::tile(p, tile0, TM, OUT);
-    const int width = OUT / cluster, c0 = (int)rank * width;
-    const int rows = (int)(tl.rows - tl.row < BM ? tl.rows - tl.row : BM);
-    if (Op::vec(p)) {
-      // consecutive threads along a row; along a column where D is stored transposed too
-      const int octs = width / 8;
-      for (int i = threadIdx.x; i < (Op::SYM ? BM : rows) * octs; i += S::THREADS) {
-        const int r = Op::SYM ? i % BM : i / octs, c = c0 + (Op::SYM ? i / BM : i - r * octs) * 8;
-        if (r >= rows) continue;
+    if (vec) {
+      for (int i = threadIdx.x; i < items; i += S::THREADS) {
+        int r, c, n, r2, c2, n2;
+        place(i, r, c, n);
+        place(i + S::THREADS, r2, c2, n2);
+        const typename Op::Aux aux = next;
+        if (n2 > 0) Op::aux8(p, tl, tl.row + r2, tl.col + c2, n2, next);
+        if (n == 0) continue;
         const int64_t col = tl.col + c;
-        if (col >= tl.cols) continue;
-        const int n = (int)(tl.cols - col < 8 ? tl.cols - col : 8);
-        typename Op::Aux aux{};
-        Op::aux8(p, tl, tl.row + r, col, n, aux);
         float v[8], u[8];
         auto add8 = [&](float (&x)[8], int at_col) {
           const uint32_t at = base + (uint32_t)(r * PLD + at_col) * 4u;
@@ -433,24 +459,31 @@ __global__ void __launch_bounds__(Shape<SPLIT>::THREADS, SPLIT ? 2 : 1)
         }
       }
     } else {
-      for (int i = threadIdx.x; i < rows * width; i += S::THREADS) {
-        const int r = i / width, c = c0 + (i - r * width);
-        if (tl.col + c >= tl.cols) continue;
-        auto add1 = [&](int at_col) {
-          const uint32_t at = base + (uint32_t)(r * PLD + at_col) * 4u;
-          float part[MAX_SPLIT], x = dead ? NAN : 0.f;
+      // a column a thread, 8 rows at a time
+      constexpr int T = 256;
+      const int c = c0 + ((int)threadIdx.x & (width - 1)), step = T / width;
+      if (threadIdx.x < T && tl.col + c < tl.cols) {
+        for (int r0 = (int)threadIdx.x / width; r0 < rows; r0 += step * 8) {
+          float v[8], u[8];
+          auto add1 = [&](float (&x)[8], int at_col) {
 #pragma unroll
-          for (int k = 0; k < MAX_SPLIT; ++k) part[k] = k < cluster ? tc::ld_peer_f32(tc::peer_addr(at, (uint32_t)k)) : 0.f;
+            for (int k = 0; k < 8; ++k) x[k] = dead ? NAN : 0.f;
+            for (int q = 0; q < cluster; ++q) {
+              const uint32_t peer = tc::peer_addr(base + (uint32_t)(r0 * PLD + at_col) * 4u, (uint32_t)q);
+              float part[8];   // in flight together
 #pragma unroll
-          for (int k = 0; k < MAX_SPLIT; ++k)
-            if (k < cluster) x = __fadd_rn(x, part[k]);
-          return x;
-        };
-        const float v = add1(c);
-        Op::finish1(p, tl, tl.row + r, tl.col + c, v, Op::DUAL ? add1(OUT + c) : 0.f);
+              for (int k = 0; k < 8; ++k) part[k] = r0 + k * step < rows ? tc::ld_peer_f32(peer + (uint32_t)(k * step * PLD) * 4u) : 0.f;
+#pragma unroll
+              for (int k = 0; k < 8; ++k) x[k] = __fadd_rn(x[k], part[k]);
+            }
+          };
+          add1(v, c);
+          if constexpr (Op::DUAL) add1(u, OUT + c);
+          Op::column8(p, tl, tl.row + r0, step, rows - r0, tl.col + c, v, u);
+        }
       }
     }
-    tc::cluster_sync();   // no CTA leaves while its shared memory is read
+    tc::cluster_leave();   // no CTA leaves while its shared memory is read
   }
   tc::fence_before();
   __syncthreads();
@@ -522,6 +555,7 @@ template <class Op, bool SPLIT>
 cudaError_t launch(const Maps& maps, typename Op::Params p, cudaStream_t stream) {
   if (cudaError_t e = set_smem<Op, SPLIT>(); e != cudaSuccess) return e;
   const int tiles = p.loop.n_tiles, split = SPLIT ? split_for(tiles, p.loop.k_steps) : 1;
+  if (!SPLIT || p.loop.a_rows == 0) p.loop.a_rows = BM;
   p.loop.wait_limit = debug_wait_limit();
   p.loop.withhold = (int)debug_take_withheld();
   p.loop.stages = SPLIT && tiles * split > sm_count() ? FEW_STAGES : Shape<SPLIT>::STAGES;

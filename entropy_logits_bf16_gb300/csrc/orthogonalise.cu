@@ -153,7 +153,7 @@ struct SquareOp {
     for (int j = 0; j < 8; ++j) v[j] = POLY ? __fmaf_rn(v[j], p.scale, __fmul_rn(a[j], p.b)) : __fmul_rn(v[j], p.scale);
     p.out.store8(p.out.at(tl.which, row, col), v);   // rows are padded to 8 columns
   }
-  static __device__ __forceinline__ void finish1(const Params&, const Tile&, int64_t, int64_t, float, float) {}
+  static __device__ __forceinline__ void column8(const Params&, const Tile&, int64_t, int, int, int64_t, float (&)[8], float (&)[8]) {}
   // v: column col of rows row .. row + 7
   static __device__ __forceinline__ void turned8(const Params& p, const Tile& tl, int64_t row, int64_t col, const float (&v)[8]) {
     if (col < p.side && row < p.side) p.out.store8(p.out.at(tl.which, col, row), v);
@@ -183,7 +183,7 @@ struct ApplyOp {
   static __device__ __forceinline__ void source(const Params& p, const Tile&, int& k, int& ia, int& ib) {
     of_three(p.steps, k, ia, ib);
   }
-  static __device__ __forceinline__ bool vec(const Params&) { return true; }
+  static __device__ __forceinline__ bool vec(const Params& p) { return !p.out || p.out_vec; }
   struct Aux {
     Eight x;
   };
@@ -202,22 +202,33 @@ struct ApplyOp {
       uint16_t* o = p.out + tl.which * p.out_matrix + row * p.ldo + col;
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], kDown);
-      if (p.out_vec) {
-        store8(o, v, n);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (j < n) o[j] = (uint16_t)pack_bf16(v[j], 0.f);
-      }
+      store8(o, v, n);
       return;
     }
     p.to.store8(p.to.at(tl.which, row, col), v);
   }
-  static __device__ __forceinline__ void finish1(const Params&, const Tile&, int64_t, int64_t, float, float) {}
+  // the caller's rows that do not start on 16-byte boundaries
+  static __device__ __forceinline__ void column8(const Params& p, const Tile& tl, int64_t row, int step, int n, int64_t col,
+                                                 float (&v)[8], float (&)[8]) {
+    uint16_t h[8], r[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int64_t at = p.x.at(tl.which, row + k * step, col);
+      h[k] = k * step < n ? p.x.value[at] : 0u;
+      r[k] = k * step < n ? p.x.rest[at] : 0u;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float x = __fadd_rn(unpack_half(h[k]).x, unpack_half(r[k]).x);
+      const float y = __fmul_rn(__fmaf_rn(v[k], kDown, __fmul_rn(p.a, x)), kDown);
+      if (k * step < n) p.out[tl.which * p.out_matrix + (row + k * step) * p.ldo + col] = (uint16_t)pack_bf16(y, 0.f);
+    }
+  }
 };
 
 // ------------------------------------------------------------ the start
 constexpr int OT = 256;
+constexpr int kNormParts = 512;   // most parts of a matrix's sum
 
 // 8 columns of a row as floats, 0 past the end; vec: rows start on 16-byte boundaries.
 template <int DT>
@@ -322,11 +333,15 @@ __global__ void __launch_bounds__(OT) orth_start_kernel(const Start a) {
   const int b = blockIdx.y;
   if (threadIdx.x < 32) {
     double s[3] = {0.0, 0.0, 0.0};
-    for (int k = threadIdx.x; k < a.parts; k += 32) {
-      const Squares q = a.sums[b * a.parts + k];
-      s[0] += (double)q.small;
-      s[1] += (double)q.mid;
-      s[2] += (double)q.big;
+    Squares q[kNormParts / 32];   // all in flight together
+#pragma unroll
+    for (int k = 0; k < kNormParts / 32; ++k)
+      q[k] = (int)threadIdx.x + 32 * k < a.parts ? a.sums[b * a.parts + threadIdx.x + 32 * k] : Squares{0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < kNormParts / 32; ++k) {
+      s[0] += (double)q[k].small;
+      s[1] += (double)q[k].mid;
+      s[2] += (double)q[k].big;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
@@ -363,8 +378,6 @@ __global__ void __launch_bounds__(OT) orth_start_kernel(const Start a) {
 }
 
 // ------------------------------------------------------------ host side
-constexpr int kNormParts = 1024;   // most parts of all matrices' sums, or one each
-
 struct Layout {
   int64_t side, x_ld, p_ld;
   int parts;
@@ -378,9 +391,11 @@ Layout layout(int64_t B, int64_t m, int64_t n) {
   l.precise = l.side <= kPrecise;
   l.x_ld = pad8(n);
   l.p_ld = pad8(l.side);
-  int64_t parts = kNormParts / (B > 0 ? B : 1);
-  if (parts > m) parts = m;
-  l.parts = (int)(parts < 1 ? 1 : parts);
+  // rows of 2048 numbers or more for each part, and about 1200 parts in all
+  const int64_t least = (2048 + n - 1) / n, most = B < 2 ? kNormParts : 1216 / B + 1;
+  int64_t parts = (m + least - 1) / least;
+  parts = parts > most ? most : parts;
+  l.parts = (int)(parts > kNormParts ? kNormParts : parts);
   l.x = pad256((size_t)B * m * l.x_ld * 2);
   l.p = pad256((size_t)B * l.side * l.p_ld * 2);
   l.sums = pad256((size_t)B * l.parts * sizeof(Squares));

@@ -31,8 +31,11 @@
 namespace rlk {
 namespace {
 
-constexpr int VW = 32;            // virtual warps of a row
+constexpr int MAX_VW = 32;        // most virtual warps of a row
 constexpr int MAX_TOP = RLK_MAX_ALTERNATIVES;
+// Rows of up to kShortRow bytes are cut into 16 virtual warps (half the threads a row); few rows
+// of kLongRow and more are shared by CTAs.
+constexpr int64_t kShortRow = 32768, kLongRow = 131072;
 constexpr int CAP = 1024;         // candidates that are sorted
 constexpr int MAX_UNITS = 512;    // units that are read again
 constexpr float CLAMP = -200.f;   // 2^-200 is 0 in fp32, and 0 x -200 is 0 (0 x -inf would be NaN)
@@ -41,6 +44,18 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
+}
+
+// Barriers of the NT threads that work on a row (another warp may fetch for them).
+template <int NT>
+__device__ __forceinline__ void sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(NT) : "memory");
+}
+template <int NT>
+__device__ __forceinline__ int sync_count(bool p) {
+  int n;
+  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %1, 0;\n bar.red.popc.u32 %0, 1, %2, p;\n}\n" : "=r"(n) : "r"((int)p), "n"(NT) : "memory");
+  return n;
 }
 
 // One 16-byte group of a row as floats; DT 0 bf16 (8 logits), 1 fp32 (4).
@@ -129,9 +144,18 @@ struct Row {
       return __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(p) + at));
     }
     // the two aligned words that the group lies in, where both are inside the row
-    if (g == 0 || at + 32 - (int)sh > end) return edge(p, V, g);
+    if ((g == 0 && sh) || at + 32 - (int)sh > end) return edge(p, V, g);
     const uint4* a = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(p) + at - sh);
-    const uint4 x = __ldg(a), y = __ldg(a + 1);
+    return shifted(__ldg(a), __ldg(a + 1));
+  }
+  // The same from the copy of the row's whole aligned words, of which group g's first is at `at`.
+  __device__ __forceinline__ uint4 from_copy(const uint8_t* at, int g) const {
+    const int64_t end = (int64_t)V * (int)sizeof(elem), to = (int64_t)g * 16 + (ALIGNED ? 16 : 32 - (int)sh);
+    if (to > end || (!ALIGNED && g == 0 && sh)) return edge(p, V, g);
+    const uint4 x = *reinterpret_cast<const uint4*>(at);
+    return ALIGNED ? x : shifted(x, *reinterpret_cast<const uint4*>(at + 16));
+  }
+  __device__ __forceinline__ uint4 shifted(const uint4& x, const uint4& y) const {
     uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
     if (sh & 8u) {
 #pragma unroll
@@ -199,7 +223,7 @@ __device__ __forceinline__ Part join(float m, float top, float s, float t, float
 }
 
 struct Shared {
-  Part part[VW];
+  Part part[MAX_VW];
   float M, lnS;
   int bad;
   int n_units, n_cand;
@@ -229,7 +253,7 @@ __device__ void sort_candidates(Shared& sh, int n, int K) {
     int P = 512;
     while (P < n) P *= 2;
     for (int i = n + threadIdx.x; i < P; i += NT) sh.cand[i] = 0ull;
-    __syncthreads();
+    sync<NT>();
     for (int k = 2; k <= P; k *= 2)
       for (int j = k / 2; j > 0; j /= 2) {
         for (int i = threadIdx.x; i < P / 2; i += NT) {
@@ -240,19 +264,19 @@ __device__ void sort_candidates(Shared& sh, int n, int K) {
             sh.cand[b] = x;
           }
         }
-        __syncthreads();
+        sync<NT>();
       }
     for (int i = threadIdx.x; i < K && i < n; i += NT) sh.sorted[i] = sh.cand[i];
   }
   if (threadIdx.x == 0) sh.n_sorted = n < K ? n : K;
-  __syncthreads();
+  sync<NT>();
 }
 
-// The CTA's share of a row: virtual warps [v0, v0 + 32 / cluster).  `f(group)` for each of its
+// The CTA's share of a row: nv of its VW virtual warps, from v0 on.  `f(group)` for each of its
 // groups, any order over the threads.
-template <int NT, class F>
+template <int NT, int VW, class F>
 __device__ __forceinline__ void each_group(int groups, int v0, int nv, F f) {
-  const int per = nv * 32;   // groups of the CTA in 32 chunks of the row
+  const int per = nv * 32;   // groups of the CTA in a round of VW chunks of the row
   for (int i = threadIdx.x;; i += NT) {
     const int g = i / per * (VW * 32) + v0 * 32 + i % per;
     if (i / per * (VW * 32) >= groups) break;
@@ -262,22 +286,22 @@ __device__ __forceinline__ void each_group(int groups, int v0, int nv, F f) {
 
 // The CTA's K largest logits when the fast way found too many candidates: the K-th largest
 // logit by bisection over its bits, then what is above it, then the first of its ties.
-template <int NT, int DT, bool ALIGNED>
+template <int NT, int VW, int DT, bool ALIGNED>
 __device__ void select_by_bisection(Shared& sh, const Row<DT, ALIGNED>& row, int v0, int nv, int K) {
   using G = Group<DT>;
   const int groups = row.groups();
   auto count = [&](uint32_t least) {   // logits of the CTA at or above
     int n = 0;
-    each_group<NT>(groups, v0, nv, [&](int g) {
+    each_group<NT, VW>(groups, v0, nv, [&](int g) {
       float v[G::E];
       G::floats(row.load(g), v);
 #pragma unroll
       for (int j = 0; j < G::E; ++j) n += G::key(v[j]) >= least;
     });
     n = __reduce_add_sync(0xFFFFFFFFu, n);
-    __syncthreads();
+    sync<NT>();
     if ((threadIdx.x & 31) == 0) sh.scan[threadIdx.x >> 5] = n;
-    __syncthreads();
+    sync<NT>();
     n = 0;
     for (int w = 0; w < NT / 32; ++w) n += sh.scan[w];
     return n;
@@ -288,10 +312,10 @@ __device__ void select_by_bisection(Shared& sh, const Row<DT, ALIGNED>& row, int
     if (count(c) >= K) kth = c;
   }
   if (kth < G::kLowest) kth = G::kLowest;
-  __syncthreads();
+  sync<NT>();
   if (threadIdx.x == 0) sh.n_cand = 0;
-  __syncthreads();
-  each_group<NT>(groups, v0, nv, [&](int g) {   // fewer than K of them
+  sync<NT>();
+  each_group<NT, VW>(groups, v0, nv, [&](int g) {   // fewer than K of them
     float v[G::E];
     G::floats(row.load(g), v);
 #pragma unroll
@@ -301,9 +325,9 @@ __device__ void select_by_bisection(Shared& sh, const Row<DT, ALIGNED>& row, int
         if (at < CAP) sh.cand[at] = rank_key(G::key(v[j]), g * G::E + j);
       }
   });
-  __syncthreads();
+  sync<NT>();
   int have = sh.n_cand;
-  __syncthreads();
+  sync<NT>();
   // ties in the order of their index: NT groups at a time, the counts before a thread's by a scan
   const int per = nv * 32;
   for (int i0 = 0; have < K; i0 += NT) {
@@ -326,7 +350,7 @@ __device__ void select_by_bisection(Shared& sh, const Row<DT, ALIGNED>& row, int
     }
     if (lane == 31) sh.scan[threadIdx.x >> 5] = before;
     before -= __popc(mask);
-    __syncthreads();
+    sync<NT>();
     int all = 0;
     for (int w = 0; w < NT / 32; ++w) {
       if (w < (int)(threadIdx.x >> 5)) before += sh.scan[w];
@@ -338,112 +362,113 @@ __device__ void select_by_bisection(Shared& sh, const Row<DT, ALIGNED>& row, int
         sh.cand[at++] = rank_key(kth, g * G::E + j);
       }
     have += all;
-    __syncthreads();
+    sync<NT>();
   }
   if (threadIdx.x == 0) sh.n_cand = have < K ? have : K;
-  __syncthreads();
+  sync<NT>();
 }
 
 // Thread's largest logits (`tops`, one a virtual warp of its warp) -> the CTA's K largest in
-// sh.sorted.
-template <int NT, int DT, bool ALIGNED, int S>
-__device__ void select_top(Shared& sh, const Row<DT, ALIGNED>& row, int v0, int nv, const float (&tops)[S], int K) {
+// sh.sorted.  `meanwhile` is run by all threads while the units that are read again are on
+// their way.
+template <int NT, int VW, int DT, bool ALIGNED, int S, class F>
+__device__ __forceinline__ void select_top(Shared& sh, const Row<DT, ALIGNED>& row, int v0, int nv, const float (&tops)[S], int K,
+                                           F meanwhile) {
   using G = Group<DT>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   float mine = tops[0];
 #pragma unroll
   for (int j = 1; j < S; ++j) mine = max_nan(mine, tops[j]);
   const uint32_t key = G::key(mine) >> G::SHIFT;
-  uint32_t least = 0u;   // the largest value that K threads reach, by its upper 16 bits
+  // a value that K threads reach, and not many more: by bisection over its upper 16 bits
+  uint32_t least = 0u;
 #pragma unroll 1
   for (int b = 15; b >= 0; --b) {
     const uint32_t c = least | 1u << b;
-    if (__syncthreads_count(key >= c) >= K) least = c;
+    const int n = sync_count<NT>(key >= c);
+    if (n < K) continue;
+    least = c;
+    if (n <= K + K / 4 + 4) break;
   }
   least <<= G::SHIFT;
   if (least < G::kLowest) least = G::kLowest;
   if (threadIdx.x == 0) sh.n_units = sh.n_cand = 0;
-  __syncthreads();
+  sync<NT>();
 #pragma unroll
   for (int j = 0; j < S; ++j)
     if (G::key(tops[j]) >= least) {
       const int at = atomicAdd(&sh.n_units, 1);
       if (at < MAX_UNITS) sh.units[at] = (uint32_t)((v0 + warp + j * (NT / 32)) * 32 + lane);
     }
-  __syncthreads();
+  sync<NT>();
   const int groups = row.groups(), units = sh.n_units;
   const int rounds = (groups + VW * 32 - 1) / (VW * 32);   // groups of a unit
   bool many = units > MAX_UNITS;
   if (!many) {
-    for (int i = threadIdx.x; i < units * rounds; i += NT) {
-      const int g = i / units * (VW * 32) + (int)sh.units[i % units];
-      if (g >= groups) continue;
-      float v[G::E];
-      G::floats(row.load(g), v);
+    constexpr int R = 2;
+    const int total = units * rounds;
+    int base = 0;
+    do {   // all threads together
+      uint4 q[R];
+      int g[R];
 #pragma unroll
-      for (int j = 0; j < G::E; ++j)
-        if (G::key(v[j]) >= least) {
-          const int at = atomicAdd(&sh.n_cand, 1);
-          if (at < CAP) sh.cand[at] = rank_key(G::key(v[j]), g * G::E + j);
-        }
-    }
-    __syncthreads();
+      for (int u = 0; u < R; ++u) {
+        const int i = base + (int)threadIdx.x + u * NT;
+        g[u] = i < total ? i / units * (VW * 32) + (int)sh.units[i % units] : groups;
+        if (g[u] < groups) q[u] = row.load(g[u]);
+      }
+      if (base == 0) meanwhile();
+#pragma unroll
+      for (int u = 0; u < R; ++u) {
+        if (g[u] >= groups || !(G::key(G::largest(q[u])) >= least)) continue;   // (a NaN's key is above or below all)
+        float v[G::E];
+        G::floats(q[u], v);
+#pragma unroll
+        for (int j = 0; j < G::E; ++j)
+          if (G::key(v[j]) >= least) {
+            const int at = atomicAdd(&sh.n_cand, 1);
+            if (at < CAP) sh.cand[at] = rank_key(G::key(v[j]), g[u] * G::E + j);
+          }
+      }
+      base += R * NT;
+    } while (base < total);
+    sync<NT>();
     many = sh.n_cand > CAP;
+  } else {
+    meanwhile();
   }
-  if (many) select_by_bisection<NT, DT, ALIGNED>(sh, row, v0, nv, K);
+  if (many) select_by_bisection<NT, VW, DT, ALIGNED>(sh, row, v0, nv, K);
   sort_candidates<NT>(sh, sh.n_cand, K);
 }
 
-// C CTAs a row, NT threads each; a warp holds S virtual warps.
-template <int DT, bool ALIGNED, int C>
-__global__ void __launch_bounds__(C == 8 ? 128 : 256, C == 8 ? 4 : 4) token_forward_kernel(TokenArgs a, float c, float inv_t) {
-  constexpr int NT = C == 8 ? 128 : 256, WARPS = NT / 32, NV = VW / C, S = NV / WARPS;
-  static_assert(S >= 1, "");
-  using G = Group<DT>;
-  pdl_wait();
-  __shared__ Shared sh;
-  const int rank = C == 1 ? 0 : (int)tc::cluster_rank();
-  const int64_t t = blockIdx.x / C;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, v0 = rank * NV;
-  const Row<DT, ALIGNED> row(a.logits, t, a.ld, a.V);
-  const int groups = row.groups();
-  const float slack = __fdiv_rn(16.f, c);
+// C CTAs a row of VW virtual warps; a warp holds S of them.
+template <int C, int VW>
+struct Cut {
+  static constexpr int NT = VW == 16 ? 128 : 256, WARPS = NT / 32, NV = VW / C, S = NV / WARPS;
+  static_assert(S >= 1 && S * WARPS * C == VW, "every warp has the same share");
+};
 
-  // the first given token of each thread is on its way while the row is read
-  int id0 = -1;
-  float z0 = 0.f;
-  bool bad_id = false;
-  auto token = [&](int64_t i, int& id, float& z) {
+// The given tokens of a row, a thread's first asked for while the row is read.
+template <int DT>
+struct Given {
+  int id = -1;
+  float z = 0.f;
+  bool bad = false;
+  __device__ __forceinline__ void ask(const TokenArgs& a, int64_t t, const typename Group<DT>::elem* row, int64_t i) {
     id = a.ids[t * a.C + i];
-    const bool in = id >= 0 && id < a.V;
-    if (id < -1 || id >= a.V) bad_id = true;
-    z = in ? G::value(row.p[id]) : 0.f;
-  };
-  if (rank == 0 && threadIdx.x < a.C) token(threadIdx.x, id0, z0);
+    if (id < -1 || id >= a.V) bad = true;
+    z = id >= 0 && id < a.V ? Group<DT>::value(row[id]) : 0.f;
+  }
+};
 
-  Sums sums[S];
-  constexpr int U = S == 4 ? 1 : (S == 2 ? 2 : 4);   // rounds (of 32 chunks of the row) in flight together
-  const int g0 = (v0 + warp) * 32 + lane;
-  int r = 0;
-  const int whole = (groups - 1) / (VW * 32);          // rounds in which every lane has a group
-  for (; r + U <= whole; r += U) {
-    uint4 q[U][S];
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int j = 0; j < S; ++j) q[u][j] = row.template load<true>((r + u) * (VW * 32) + g0 + j * (WARPS * 32));
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int j = 0; j < S; ++j) absorb<DT>(sums[j], q[u][j], c, slack);
-  }
-  for (; r * (VW * 32) < groups; ++r) {
-#pragma unroll
-    for (int j = 0; j < S; ++j) {
-      const int g = r * (VW * 32) + g0 + j * (WARPS * 32);
-      if (g < groups) absorb<DT>(sums[j], row.load(g), c, slack);
-    }
-  }
+// What follows the pass over a row: the CTA's sums joined, the alternatives, the outputs (by
+// the cluster's first CTA).
+template <int DT, bool ALIGNED, int C, int VW>
+__device__ __forceinline__ void end_of_row(Shared& sh, const TokenArgs& a, int64_t t, const Row<DT, ALIGNED>& row, int rank,
+                                           const Sums (&sums)[Cut<C, VW>::S], Given<DT>& given, float c, float inv_t) {
+  using G = Group<DT>;
+  constexpr int NT = Cut<C, VW>::NT, WARPS = Cut<C, VW>::WARPS, NV = Cut<C, VW>::NV, S = Cut<C, VW>::S;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, v0 = rank * NV;
   float tops[S];
 #pragma unroll
   for (int j = 0; j < S; ++j) {
@@ -451,12 +476,34 @@ __global__ void __launch_bounds__(C == 8 ? 128 : 256, C == 8 ? 4 : 4) token_forw
     const Part p = join(sums[j].m, sums[j].top, __fadd_rn(sums[j].s.x, sums[j].s.y), __fadd_rn(sums[j].t.x, sums[j].t.y), c);
     if (lane == 0) sh.part[v0 + warp + j * WARPS] = p;
   }
-  __syncthreads();
-  if (a.top > 0) select_top<NT, DT, ALIGNED, S>(sh, row, v0, NV, tops, a.top);
+  sync<NT>();
+  // the row's sums, from all its virtual warps, by the last warp
+  auto conclude = [&] {
+    if (warp != WARPS - 1) return;
+    const Part p = lane < VW ? sh.part[lane] : Part{-INFINITY, 0.f, 0.f};
+    const Part all = join(p.top, p.top, p.s, p.t, c);
+    const bool bad = !(all.top > -INFINITY && all.top < INFINITY) || all.s != all.s;
+    if (lane == 0) {
+      sh.M = bad ? NAN : all.top;
+      sh.lnS = bad ? NAN : logf(all.s);
+      sh.bad = bad;
+      const float H = bad ? NAN : __fmaf_rn(-kLn2, __fdiv_rn(all.t, all.s), sh.lnS);
+      if (a.out_entropy) a.out_entropy[t] = H;
+      if (a.state) *reinterpret_cast<float4*>(a.state + 4 * t) = make_float4(sh.M, bad ? NAN : log2f(all.s), H, a.temperature);
+      if (bad && a.status) atomicOr(a.status, RLK_STATUS_NONFINITE);
+    }
+  };
+  if (a.top > 0)
+    select_top<NT, VW, DT, ALIGNED, S>(sh, row, v0, NV, tops, a.top, [&] {
+      if (C == 1) {
+        __syncwarp();
+        conclude();
+      }
+    });
   if (C > 1) {
     tc::cluster_sync();
     if (rank != 0) {
-      tc::cluster_sync();   // rank 0 has read what this CTA holds
+      tc::cluster_leave();   // rank 0 has read what this CTA holds
       return;
     }
     // the other CTAs' parts and alternatives
@@ -477,34 +524,23 @@ __global__ void __launch_bounds__(C == 8 ? 128 : 256, C == 8 ? 4 : 4) token_forw
         }
         base += n;
       }
-      __syncthreads();
+      sync<NT>();
       sort_candidates<NT>(sh, base, a.top);
     }
-    __syncthreads();
-    tc::cluster_sync();
+    sync<NT>();
+    tc::cluster_leave();
   }
-  if (warp == 0) {
-    const Part p = sh.part[lane];
-    const Part all = join(p.top, p.top, p.s, p.t, c);
-    const bool bad = !(all.top > -INFINITY && all.top < INFINITY) || all.s != all.s;
-    if (lane == 0) {
-      sh.M = bad ? NAN : all.top;
-      sh.lnS = bad ? NAN : logf(all.s);
-      sh.bad = bad;
-      const float H = bad ? NAN : __fmaf_rn(-kLn2, __fdiv_rn(all.t, all.s), sh.lnS);
-      if (a.out_entropy) a.out_entropy[t] = H;
-      if (a.state) *reinterpret_cast<float4*>(a.state + 4 * t) = make_float4(sh.M, bad ? NAN : log2f(all.s), H, a.temperature);
-      if (bad && a.status) atomicOr(a.status, RLK_STATUS_NONFINITE);
-    }
+  if (C > 1 || a.top == 0) {
+    conclude();
+    sync<NT>();
   }
-  __syncthreads();
   const float M = sh.M, lnS = sh.lnS;
   auto logprob = [&](float z) { return __fsub_rn(__fmul_rn(__fsub_rn(z, M), inv_t), lnS); };
   for (int64_t i = threadIdx.x; i < a.C; i += NT) {
-    if (i >= NT) token(i, id0, z0);
-    a.out_logprob[t * a.C + i] = id0 == -1 ? 0.f : (id0 < 0 || id0 >= a.V ? NAN : logprob(z0));
+    if (i >= NT) given.ask(a, t, row.p, i);
+    a.out_logprob[t * a.C + i] = given.id == -1 ? 0.f : (given.id < 0 || given.id >= a.V ? NAN : logprob(given.z));
   }
-  if (bad_id && a.status) atomicOr(a.status, RLK_STATUS_BAD_TOKEN_ID);
+  if (given.bad && a.status) atomicOr(a.status, RLK_STATUS_BAD_TOKEN_ID);
   for (int i = threadIdx.x; i < a.top; i += NT) {
     int id = -1;
     float lp = sh.bad ? NAN : -INFINITY;
@@ -515,6 +551,150 @@ __global__ void __launch_bounds__(C == 8 ? 128 : 256, C == 8 ? 4 : 4) token_forw
     }
     a.out_top_ids[t * a.top + i] = id;
     a.out_top_logprob[t * a.top + i] = lp;
+  }
+}
+
+// A row to each cluster of C CTAs, read straight into registers.
+template <int DT, bool ALIGNED, int C, int VW>
+__global__ void __launch_bounds__(Cut<C, VW>::NT, 1024 / Cut<C, VW>::NT) token_forward_kernel(TokenArgs a, float c, float inv_t) {
+  using K = Cut<C, VW>;
+  constexpr int WARPS = K::WARPS, S = K::S;
+  pdl_wait();
+  __shared__ Shared sh;
+  const int rank = C == 1 ? 0 : (int)tc::cluster_rank();
+  const int64_t t = blockIdx.x / C;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Row<DT, ALIGNED> row(a.logits, t, a.ld, a.V);
+  const int groups = row.groups();
+  const float slack = __fdiv_rn(16.f, c);
+  Given<DT> given;
+  if (rank == 0 && (int)threadIdx.x < a.C) given.ask(a, t, row.p, threadIdx.x);
+
+  Sums sums[S];
+  constexpr int U = S == 4 ? 1 : (S == 2 ? 2 : 4);   // rounds (of VW chunks of the row) in flight together
+  const int g0 = (rank * K::NV + warp) * 32 + lane;
+  int r = 0;
+  const int whole = (groups - 1) / (VW * 32);          // rounds in which every lane has a group
+  for (; r + U <= whole; r += U) {
+    uint4 q[U][S];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < S; ++j) q[u][j] = row.template load<true>((r + u) * (VW * 32) + g0 + j * (WARPS * 32));
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < S; ++j) absorb<DT>(sums[j], q[u][j], c, slack);
+  }
+  for (; r * (VW * 32) < groups; ++r) {
+#pragma unroll
+    for (int j = 0; j < S; ++j) {
+      const int g = r * (VW * 32) + g0 + j * (WARPS * 32);
+      if (g < groups) absorb<DT>(sums[j], row.load(g), c, slack);
+    }
+  }
+  end_of_row<DT, ALIGNED, C, VW>(sh, a, t, row, rank, sums, given, c, inv_t);
+}
+
+// Many long rows: persistent CTAs, each with a ring of shared memory that one more warp keeps
+// full by bulk copies, also with the next row while this one's alternatives are selected.  A
+// stage is a round (32 chunks, 16 KB).
+constexpr int RING = 3, ROUND = 32 * 32 * 16, SLOT = ROUND + 16;   // (+ the word that an unaligned round's last group ends in)
+constexpr int RING_CTAS = 3;   // of an SM
+template <int DT, bool ALIGNED>
+__global__ void __launch_bounds__(Cut<1, 32>::NT + 32, RING_CTAS)
+    token_stream_kernel(TokenArgs a, float c, float inv_t, long long limit, int withhold) {
+  using K = Cut<1, 32>;
+  constexpr int NT = K::NT, WARPS = K::WARPS, S = K::S;
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ Shared sh;
+  __shared__ uint64_t s_bars[2 * RING];
+  __shared__ int s_abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t full = smem_u32(s_bars), empty = full + 8 * RING;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < RING; ++i) {
+      mbar_init(full + 8 * i, 1 + (i == withhold && blockIdx.x == 0));
+      mbar_init(empty + 8 * i, WARPS);
+    }
+    s_abort = 0;
+    fence_mbar_init();
+  }
+  pdl_wait();
+  __syncthreads();
+  const int groups = Row<DT, ALIGNED>(a.logits, 0, a.ld, a.V).groups(), rounds = (groups + 1023) / 1024;
+  const int64_t bytes = a.V * (DT ? 4 : 2);
+  if (warp == WARPS) {
+    if (lane == 0) {
+      uint32_t slot = 0, phase = 0, used = 0u, parity = 0u;
+      bool ok = true;
+      for (int64_t t = blockIdx.x; t < a.T && ok; t += gridDim.x) {
+        const Row<DT, ALIGNED> row(a.logits, t, a.ld, a.V);
+        // the row's whole aligned words, by their distance from the word that it starts in
+        const char* word0 = reinterpret_cast<const char*>(row.p) - row.sh;
+        const int64_t first = row.sh ? 16 : 0, last = (row.sh + bytes) & ~(int64_t)15;
+        for (int r = 0; r < rounds; ++r) {
+          if (!tc::wait(empty + 8 * slot, phase ^ 1u, &s_abort, limit)) {
+            ok = false;
+            break;
+          }
+          fence_proxy_async_smem();   // the slot was read before
+          int64_t from = (int64_t)r * ROUND, to = from + ROUND + (ALIGNED ? 0 : 16);
+          const uint32_t dst = smem_u32(ring) + slot * SLOT + (from < first ? (uint32_t)(first - from) : 0u);
+          from = from < first ? first : from;
+          to = to < last ? to : last;
+          if (to > from) {
+            mbar_expect_tx(full + 8 * slot, (uint32_t)(to - from));
+            bulk_copy_g2s(dst, word0 + from, (uint32_t)(to - from), full + 8 * slot);
+            used |= 1u << slot;
+            parity = (parity & ~(1u << slot)) | (phase << slot);
+          } else {
+            mbar_arrive(full + 8 * slot);
+          }
+          if (++slot == RING) {
+            slot = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      for (int i = 0; i < RING; ++i)   // every copy lands before the CTA exits
+        if (used >> i & 1u) tc::drain(full + 8 * i, parity >> i & 1u);
+    }
+    return;
+  }
+  const float slack = __fdiv_rn(16.f, c);
+  uint32_t slot = 0, phase = 0;
+  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+    const Row<DT, ALIGNED> row(a.logits, t, a.ld, a.V);
+    Given<DT> given;
+    if ((int)threadIdx.x < a.C) given.ask(a, t, row.p, threadIdx.x);
+    Sums sums[S];
+    bool ok = true;
+    for (int r = 0; r < rounds; ++r) {
+      ok = ok && tc::wait(full + 8 * slot, phase, &s_abort, limit);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      uint4 q[S];
+      const int g0 = r * 1024 + warp * 32 + lane;
+      const uint8_t* at = ring + slot * SLOT + (warp * 32 + lane) * 16;
+#pragma unroll
+      for (int j = 0; j < S; ++j)
+        if (ok && g0 + j * (WARPS * 32) < groups) q[j] = row.from_copy(at + j * (WARPS * 512), g0 + j * (WARPS * 32));
+      __syncwarp();
+      if (lane == 0 && ok) mbar_arrive(empty + 8 * slot);
+#pragma unroll
+      for (int j = 0; j < S; ++j)
+        if (ok && g0 + j * (WARPS * 32) < groups) absorb<DT>(sums[j], q[j], c, slack);
+      if (++slot == RING) {
+        slot = 0;
+        phase ^= 1u;
+      }
+    }
+    if (!ok) {   // a wait ran out: this row and the CTA's later ones are NaN
+      sums[0].top = NAN;
+      if (lane == 0 && a.status) atomicOr(a.status, RLK_STATUS_TIMEOUT);
+    }
+    end_of_row<DT, ALIGNED, 1, 32>(sh, a, t, row, 0, sums, given, c, inv_t);
+    sync<NT>();   // the next row's parts go where this one's were
   }
 }
 
@@ -658,11 +838,11 @@ __global__ void __launch_bounds__(BT, 4) token_backward_kernel(TokenBwdArgs a, f
   }
 }
 
-template <int DT, bool ALIGNED, int C>
+template <int DT, bool ALIGNED, int C, int VW>
 cudaError_t launch_forward(const TokenArgs& a, float c, float inv_t, cudaStream_t stream) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(a.T * C));
-  cfg.blockDim = dim3(C == 8 ? 128 : 256);
+  cfg.blockDim = dim3(Cut<C, VW>::NT);
   cfg.stream = stream;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -673,17 +853,32 @@ cudaError_t launch_forward(const TokenArgs& a, float c, float inv_t, cudaStream_
   at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = C > 1 ? 2 : 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, token_forward_kernel<DT, ALIGNED, C>, a, c, inv_t);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, token_forward_kernel<DT, ALIGNED, C, VW>, a, c, inv_t);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+template <int DT, bool ALIGNED>
+cudaError_t launch_stream(const TokenArgs& a, float c, float inv_t, cudaStream_t stream) {
+  static std::atomic<int> done[64];
+  const auto kernel = token_stream_kernel<DT, ALIGNED>;
+  const int ds = device_slot();
+  if (ds < 0 || !done[ds].load()) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, RING * SLOT);
+    if (e != cudaSuccess) return e;
+    if (ds >= 0) done[ds].store(1);
+  }
+  const int64_t most = (int64_t)sm_count() * RING_CTAS;
+  const cudaError_t e = launch_after(kernel, dim3((unsigned)(a.T < most ? a.T : most)), dim3(Cut<1, 32>::NT + 32), RING * SLOT, stream,
+                                     a, c, inv_t, debug_wait_limit(), (int)debug_take_withheld());
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 template <int DT, bool ALIGNED>
 cudaError_t forward_by_rows(const TokenArgs& a, float c, float inv_t, cudaStream_t stream) {
-  // CTAs a row: as many as there are SMs for, since one SM reads a row of 300 KB in several us
-  const int64_t sms = sm_count();
-  if (a.T * 8 <= 2 * sms) return launch_forward<DT, ALIGNED, 8>(a, c, inv_t, stream);
-  if (a.T * 4 <= 2 * sms) return launch_forward<DT, ALIGNED, 4>(a, c, inv_t, stream);
-  if (a.T * 2 <= 2 * sms) return launch_forward<DT, ALIGNED, 2>(a, c, inv_t, stream);
-  return launch_forward<DT, ALIGNED, 1>(a, c, inv_t, stream);
+  const int64_t sms = sm_count(), bytes = a.V * (a.dtype ? 4 : 2);
+  if (bytes <= kShortRow) return launch_forward<DT, ALIGNED, 1, 16>(a, c, inv_t, stream);
+  if (bytes >= kLongRow && a.T * 4 <= sms) return launch_forward<DT, ALIGNED, 4, 32>(a, c, inv_t, stream);
+  if (bytes >= kLongRow && a.T <= 2 * sms) return launch_forward<DT, ALIGNED, 2, 32>(a, c, inv_t, stream);
+  if (a.T <= 2 * sms) return launch_forward<DT, ALIGNED, 1, 32>(a, c, inv_t, stream);
+  return launch_stream<DT, ALIGNED>(a, c, inv_t, stream);
 }
 
 }  // namespace

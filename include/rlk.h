@@ -1143,7 +1143,9 @@ typedef struct rlk_token_state {
  *  out_status_word device uint32[1] or NULL.  A row with a NaN or +inf, or
  *                  without any logit above -inf, gets NaN (alternatives: -1 and
  *                  NaN; empty places: 0) and RLK_STATUS_NONFINITE.  A token below
- *                  -1 or not below V gets NaN and RLK_STATUS_BAD_TOKEN_ID.
+ *                  -1 or not below V gets NaN and RLK_STATUS_BAD_TOKEN_ID.  A row
+ *                  that did not come within the limit of its wait (about a
+ *                  second) gets NaN, and RLK_STATUS_TIMEOUT too.
  * A row's bits depend on its values only, not on the batch, the layout or the
  * other arguments.
  * Errors: RLK_ERR_INVALID_ARG for sizes outside their ranges, ld < V, a bad

@@ -277,3 +277,41 @@ def test_offsets_past_32_bits(cuda_lib):
     g = torch.ones(T, 2, device="cuda")
     dz = rlk.token_logprobs_backward(z, ids, 1.0, state, g)
     assert torch.equal(dz[-3:], rlk.token_logprobs_backward(z[-3:], ids[-3:], 1.0, state[-3:].contiguous(), g[-3:]))
+
+
+@pytest.mark.parametrize("stage", [0, 2])
+@pytest.mark.parametrize("V", [40000, 70001])
+def test_waits_that_run_out(cuda_lib, stage, V):
+    """Many long rows come through a ring of copies: a debug setting makes the first CTA wait for
+    an arrival that never comes.  Its rows are NaN, the others keep their bits, the next call is clean."""
+    rlk, T = cuda_lib, 1000
+    z = logits(T, V, BF16, 1)
+    ids = given(T, V, 3, 1)
+    want = rlk.token_logprobs(z, ids, 1.0, n_top=5)
+    word = torch.zeros(1, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    rlk.set_wait_limit(2_000_000)   # about a millisecond
+    try:
+        rlk.withhold_copy(stage)
+        got = rlk.token_logprobs(z, ids, 1.0, n_top=5, status_word=word)
+        torch.cuda.synchronize()
+    finally:
+        rlk.withhold_copy(-1)
+        rlk.set_wait_limit(0)
+    bad = torch.isnan(got[1])
+    assert word.item() & rlk.STATUS_TIMEOUT and bad[0] and 0 < int(bad.sum()) < T
+    assert torch.isnan(got[0][bad][ids[bad] >= 0]).all() and torch.isnan(got[3][bad]).all() and (got[2][bad] == -1).all()
+    assert all(torch.equal(a[~bad], b[~bad]) for a, b in zip(got, want))
+    assert all(torch.equal(a, b) for a, b in zip(rlk.token_logprobs(z, ids, 1.0, n_top=5), want))
+
+
+def test_rows_of_one_call_through_the_ring(cuda_lib):
+    """Every row of a batch that goes through the ring is what it is alone."""
+    for dtype, V, lead in ((BF16, 33001, 1), (F32, 9002, 3), (BF16, 16385, 0)):
+        z = logits(500, V, dtype, 3, "masked")
+        z = odd_layout(z, lead) if lead else z
+        ids = given(500, V, 2, 1)
+        all_ = cuda_lib.token_logprobs(z, ids, 0.8, n_top=7)
+        for r in (0, 1, 170, 455, 456, 457, 499):
+            for a, b in zip(all_, cuda_lib.token_logprobs(z[r:r + 1], ids[r:r + 1], 0.8, n_top=7)):
+                assert torch.equal(a[r:r + 1].view(torch.int32), b.view(torch.int32)), (dtype, V, r)
