@@ -127,7 +127,8 @@ __global__ void __launch_bounds__(Shape<SPLIT>::THREADS, SPLIT ? 2 : 1)
   }
   if (warp == 1) tc::alloc<G>(smem_u32(tmem_slot), TMEM_COLS);
   tc::fence_before();
-  pdl_wait();   // the operands may come from the kernel before
+  pdl_trigger();   // the next kernel gets ready where there is room, and waits for this one's end
+  pdl_wait();      // the operands may come from the kernel before
   __syncthreads();
   if (G == 2) tc::cluster_sync();   // the other CTA's barriers are there
   tc::fence_after();
@@ -541,12 +542,10 @@ cudaError_t set_smem() {
 }
 
 // CTAs that share a tile's K when there are `tiles` tiles of 128 x 128: 2 or 4 while all have
-// an SM and at least four stages of K each, or half an SM and at least eight (the linear
-// layer's rule, measured there: 64 tiles of K 1000, by 2 13.7 us, by 4 18.0; 128 tiles of K
-// 4096, whole 35.3, by 2 26.3).
+// an SM and two stages of K each, or half an SM and at least eight.
 inline int split_for(int tiles, int k_steps) {
   int s = 1;
-  while (s < MAX_SPLIT && k_steps >= 8 * s && tiles * 2 * s <= (k_steps >= 16 * s ? 2 : 1) * sm_count()) s *= 2;
+  while (s < MAX_SPLIT && ((k_steps >= 4 * s && tiles * 2 * s <= sm_count()) || (k_steps >= 16 * s && tiles * 2 * s <= 2 * sm_count()))) s *= 2;
   return s;
 }
 

@@ -20,7 +20,8 @@
 // polynomial's slope adds up: first-order sum over the steps with u = 2^-11), about 0.0015 on
 // the average of many.  Where the shorter side is kPrecise or less there may be few to average
 // over, and the call is bound by its launches: A and P are held in two fp16 as well, and each
-// product is three (values, value times rest both ways), one sum in the accumulator.
+// product is three (values, value times rest both ways), one sum in the accumulator (64 x 64:
+// 107 us in all, 95 with one product each; at 256 x 256 163 and 137).
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -36,7 +37,7 @@ using gemm::Operand;
 using gemm::Tile;
 
 constexpr float kDown = 1.f / 1024.f;   // the operands' scale is 2^10
-constexpr int kPrecise = 256;
+constexpr int kPrecise = 128;
 
 int64_t pad8(int64_t n) { return (n + 7) / 8 * 8; }
 size_t pad256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -127,11 +128,12 @@ struct SquareOp {
   struct Params {
     Loop loop;
     int per, side, steps;
+    int whole;         // tiles a side where all are computed, 0: those on and below the diagonal
     float scale, b;    // of the accumulators; of A (POLY)
     Buffer a, out;
   };
   static __device__ __forceinline__ Tile tile(const Params& p, int t, int tm, int tn) {
-    return stacked(t, p.per, 0, 0, tm, tn, p.side, p.side, true);
+    return stacked(t, p.per, p.whole, p.whole, tm, tn, p.side, p.side, p.whole == 0);
   }
   static __device__ __forceinline__ void source(const Params& p, const Tile&, int& k, int& ia, int& ib) {
     of_three(p.steps, k, ia, ib);
@@ -296,15 +298,18 @@ struct Start {
 
 template <int DT>
 __global__ void __launch_bounds__(OT) orth_norm_kernel(const Start a) {
+  pdl_trigger();
   const int b = blockIdx.y;
-  const int64_t base = b * a.g_matrix, octs = (a.n + 7) / 8;
+  const int64_t base = b * a.g_matrix;
+  const unsigned octs = (unsigned)(a.n + 7) / 8, all = (unsigned)a.m * octs, step = (unsigned)a.parts * OT;
   Squares s{0.f, 0.f, 0.f};
-  for (int64_t r = blockIdx.x; r < a.m; r += a.parts)
-    for (int64_t i = threadIdx.x; i < octs; i += OT) {
-      float v[8];
-      load8<DT>(a.g, base + r * a.ldg + i * 8, (int)(a.n - i * 8 < 8 ? a.n - i * 8 : 8), a.vec, v);
-      add_squares(s, v);
-    }
+#pragma unroll 2
+  for (unsigned i = blockIdx.x * OT + threadIdx.x; i < all; i += step) {
+    const unsigned r = i / octs, c = (i - r * octs) * 8;
+    float v[8];
+    load8<DT>(a.g, base + r * a.ldg + c, a.n - c < 8 ? (int)(a.n - c) : 8, a.vec, v);
+    add_squares(s, v);
+  }
   __shared__ Squares sh[OT / 32];
   float w[3] = {s.small, s.mid, s.big};
 #pragma unroll
@@ -328,6 +333,7 @@ __global__ void __launch_bounds__(OT) orth_norm_kernel(const Start a) {
 // be outside fp32's range).
 template <int DT>
 __global__ void __launch_bounds__(OT) orth_start_kernel(const Start a) {
+  pdl_trigger();
   pdl_wait();
   __shared__ float s_f[3];
   const int b = blockIdx.y;
@@ -366,15 +372,17 @@ __global__ void __launch_bounds__(OT) orth_start_kernel(const Start a) {
   }
   __syncthreads();
   const float f0 = s_f[0], f1 = s_f[1], f2 = s_f[2];
-  const int64_t base = b * a.g_matrix, octs = (a.n + 7) / 8;
-  for (int64_t r = blockIdx.x; r < a.m; r += gridDim.x)
-    for (int64_t i = threadIdx.x; i < octs; i += OT) {
-      float v[8];
-      load8<DT>(a.g, base + r * a.ldg + i * 8, (int)(a.n - i * 8 < 8 ? a.n - i * 8 : 8), a.vec, v);
+  const int64_t base = b * a.g_matrix;
+  const unsigned octs = (unsigned)(a.n + 7) / 8, all = (unsigned)a.m * octs, step = gridDim.x * OT;
+#pragma unroll 2
+  for (unsigned i = blockIdx.x * OT + threadIdx.x; i < all; i += step) {
+    const unsigned r = i / octs, c = (i - r * octs) * 8;
+    float v[8];
+    load8<DT>(a.g, base + r * a.ldg + c, a.n - c < 8 ? (int)(a.n - c) : 8, a.vec, v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(__fmul_rn(__fmul_rn(v[j], f1), f2), f0);
-      a.x.store8(a.x.at(b, r, i * 8), v);
-    }
+    for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(__fmul_rn(__fmul_rn(v[j], f1), f2), f0);
+    a.x.store8(a.x.at(b, r, c), v);
+  }
 }
 
 // ------------------------------------------------------------ host side
@@ -391,11 +399,10 @@ Layout layout(int64_t B, int64_t m, int64_t n) {
   l.precise = l.side <= kPrecise;
   l.x_ld = pad8(n);
   l.p_ld = pad8(l.side);
-  // rows of 2048 numbers or more for each part, and about 1200 parts in all
-  const int64_t least = (2048 + n - 1) / n, most = B < 2 ? kNormParts : 1216 / B + 1;
-  int64_t parts = (m + least - 1) / least;
-  parts = parts > most ? most : parts;
-  l.parts = (int)(parts > kNormParts ? kNormParts : parts);
+  // a part: eight groups of 8 numbers a thread or more, and about 1200 parts in all
+  const int64_t octs = m * ((n + 7) / 8), most = B < 3 ? kNormParts : 1216 / B + 1;
+  const int64_t parts = (octs + OT * 8 - 1) / (OT * 8);
+  l.parts = (int)(parts > most ? most : parts);
   l.x = pad256((size_t)B * m * l.x_ld * 2);
   l.p = pad256((size_t)B * l.side * l.p_ld * 2);
   l.sums = pad256((size_t)B * l.parts * sizeof(Squares));
@@ -414,7 +421,8 @@ bool stack_map(CUtensorMap* map, void* p, const Buffer& o, int64_t B, int64_t ro
 }
 
 // Pairs' tiles where small ones would be more than the SMs, as for the linear layer; tiles of
-// a symmetric product on and below the diagonal.
+// a symmetric product on and below the diagonal, but all of them where there are SMs for all
+// with K split by four.
 template <class Op>
 cudaError_t run_square(const Maps& maps, typename Op::Params& p, int64_t B, cudaStream_t stream) {
   auto triangle = [&](int64_t tm) {
@@ -422,7 +430,9 @@ cudaError_t run_square(const Maps& maps, typename Op::Params& p, int64_t B, cuda
     return t * (t + 1) / 2;
   };
   const bool few = p.side <= 128 || B * triangle(128) <= sm_count();
-  const int64_t per = triangle(few ? 128 : 256);
+  const int64_t t = (p.side + 127) / 128;
+  p.whole = few && 4 * B * t * t <= sm_count() ? (int)t : 0;
+  const int64_t per = p.whole ? t * t : triangle(few ? 128 : 256);
   if (B * per > (1 << 30)) return cudaErrorInvalidValue;
   p.per = (int)per;
   p.loop.n_tiles = (int)(B * per);
@@ -470,9 +480,10 @@ cudaError_t iterate(const OrthArgs& a, const Layout& l, cudaStream_t stream) {
   else orth_norm_kernel<1><<<sums, OT, 0, stream>>>(s);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  int64_t rows = (int64_t)sm_count() * 8 / a.B;
-  rows = rows < 1 ? 1 : (rows > a.m ? a.m : rows);
-  e = launch_after(a.dtype == 0 ? orth_start_kernel<0> : orth_start_kernel<1>, dim3((unsigned)rows, (unsigned)a.B), dim3(OT), 0, stream, s);
+  const int64_t ctas = (a.m * ((a.n + 7) / 8) + OT - 1) / OT;   // a group of 8 a thread, up to 8 CTAs an SM
+  int64_t grid = ((int64_t)sm_count() * 8 + a.B - 1) / a.B;
+  grid = grid > ctas ? ctas : grid;
+  e = launch_after(a.dtype == 0 ? orth_start_kernel<0> : orth_start_kernel<1>, dim3((unsigned)grid, (unsigned)a.B), dim3(OT), 0, stream, s);
   if (e != cudaSuccess) return e;
 
   using Gram = SquareOp<TALL, false>;

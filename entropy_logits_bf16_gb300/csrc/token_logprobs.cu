@@ -149,11 +149,11 @@ struct Row {
     return shifted(__ldg(a), __ldg(a + 1));
   }
   // The same from the copy of the row's whole aligned words, of which group g's first is at `at`.
+  // INNER: not the first of the row, and two groups after this one exist
+  template <bool INNER = false>
   __device__ __forceinline__ uint4 from_copy(const uint8_t* at, int g) const {
-    const int64_t end = (int64_t)V * (int)sizeof(elem), to = (int64_t)g * 16 + (ALIGNED ? 16 : 32 - (int)sh);
-    if (to > end || (!ALIGNED && g == 0 && sh)) return edge(p, V, g);
-    const uint4 x = *reinterpret_cast<const uint4*>(at);
-    return ALIGNED ? x : shifted(x, *reinterpret_cast<const uint4*>(at + 16));
+    if (!INNER && ((g == 0 && sh) || (int64_t)g * 16 + 32 - (int)sh > (int64_t)V * (int)sizeof(elem))) return edge(p, V, g);
+    return shifted(*reinterpret_cast<const uint4*>(at), *reinterpret_cast<const uint4*>(at + 16));
   }
   __device__ __forceinline__ uint4 shifted(const uint4& x, const uint4& y) const {
     uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
@@ -246,6 +246,7 @@ __device__ void sort_candidates(Shared& sh, int n, int K) {
     for (int i = threadIdx.x; i < n; i += NT) {
       const unsigned long long mine = sh.cand[i];
       int r = 0;
+#pragma unroll 8
       for (int j = 0; j < n; ++j) r += sh.cand[j] > mine;
       if (r < K) sh.sorted[r] = mine;
     }
@@ -596,12 +597,12 @@ __global__ void __launch_bounds__(Cut<C, VW>::NT, 1024 / Cut<C, VW>::NT) token_f
   end_of_row<DT, ALIGNED, C, VW>(sh, a, t, row, rank, sums, given, c, inv_t);
 }
 
-// Many long rows: persistent CTAs, each with a ring of shared memory that one more warp keeps
+// Many rows off 16-byte boundaries: persistent CTAs, each with a ring of shared memory that one more warp keeps
 // full by bulk copies, also with the next row while this one's alternatives are selected.  A
 // stage is a round (32 chunks, 16 KB).
 constexpr int RING = 3, ROUND = 32 * 32 * 16, SLOT = ROUND + 16;   // (+ the word that an unaligned round's last group ends in)
 constexpr int RING_CTAS = 3;   // of an SM
-template <int DT, bool ALIGNED>
+template <int DT>
 __global__ void __launch_bounds__(Cut<1, 32>::NT + 32, RING_CTAS)
     token_stream_kernel(TokenArgs a, float c, float inv_t, long long limit, int withhold) {
   using K = Cut<1, 32>;
@@ -622,14 +623,14 @@ __global__ void __launch_bounds__(Cut<1, 32>::NT + 32, RING_CTAS)
   }
   pdl_wait();
   __syncthreads();
-  const int groups = Row<DT, ALIGNED>(a.logits, 0, a.ld, a.V).groups(), rounds = (groups + 1023) / 1024;
+  const int groups = Row<DT, false>(a.logits, 0, a.ld, a.V).groups(), rounds = (groups + 1023) / 1024;
   const int64_t bytes = a.V * (DT ? 4 : 2);
   if (warp == WARPS) {
     if (lane == 0) {
       uint32_t slot = 0, phase = 0, used = 0u, parity = 0u;
       bool ok = true;
       for (int64_t t = blockIdx.x; t < a.T && ok; t += gridDim.x) {
-        const Row<DT, ALIGNED> row(a.logits, t, a.ld, a.V);
+        const Row<DT, false> row(a.logits, t, a.ld, a.V);
         // the row's whole aligned words, by their distance from the word that it starts in
         const char* word0 = reinterpret_cast<const char*>(row.p) - row.sh;
         const int64_t first = row.sh ? 16 : 0, last = (row.sh + bytes) & ~(int64_t)15;
@@ -639,7 +640,7 @@ __global__ void __launch_bounds__(Cut<1, 32>::NT + 32, RING_CTAS)
             break;
           }
           fence_proxy_async_smem();   // the slot was read before
-          int64_t from = (int64_t)r * ROUND, to = from + ROUND + (ALIGNED ? 0 : 16);
+          int64_t from = (int64_t)r * ROUND, to = from + SLOT;
           const uint32_t dst = smem_u32(ring) + slot * SLOT + (from < first ? (uint32_t)(first - from) : 0u);
           from = from < first ? first : from;
           to = to < last ? to : last;
@@ -663,37 +664,48 @@ __global__ void __launch_bounds__(Cut<1, 32>::NT + 32, RING_CTAS)
     return;
   }
   const float slack = __fdiv_rn(16.f, c);
+  const int inner = (groups - 2) / 1024;   // rounds whose groups all have two after them
   uint32_t slot = 0, phase = 0;
+  bool ok = true;   // once a wait has run out, no later one counts (a barrier's parity could pass for it)
   for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-    const Row<DT, ALIGNED> row(a.logits, t, a.ld, a.V);
+    const Row<DT, false> row(a.logits, t, a.ld, a.V);
     Given<DT> given;
     if ((int)threadIdx.x < a.C) given.ask(a, t, row.p, threadIdx.x);
     Sums sums[S];
-    bool ok = true;
-    for (int r = 0; r < rounds; ++r) {
-      ok = ok && tc::wait(full + 8 * slot, phase, &s_abort, limit);
-      ok = __all_sync(0xFFFFFFFFu, ok);
+    for (int r = 0; r < rounds && ok; ++r) {
+      ok = __all_sync(0xFFFFFFFFu, tc::wait(full + 8 * slot, phase, &s_abort, limit));
+      if (!ok) break;
       uint4 q[S];
       const int g0 = r * 1024 + warp * 32 + lane;
       const uint8_t* at = ring + slot * SLOT + (warp * 32 + lane) * 16;
-#pragma unroll
-      for (int j = 0; j < S; ++j)
-        if (ok && g0 + j * (WARPS * 32) < groups) q[j] = row.from_copy(at + j * (WARPS * 512), g0 + j * (WARPS * 32));
-      __syncwarp();
-      if (lane == 0 && ok) mbar_arrive(empty + 8 * slot);
-#pragma unroll
-      for (int j = 0; j < S; ++j)
-        if (ok && g0 + j * (WARPS * 32) < groups) absorb<DT>(sums[j], q[j], c, slack);
+      const uint32_t done = empty + 8 * slot;
       if (++slot == RING) {
         slot = 0;
         phase ^= 1u;
+      }
+      if (r < inner && r > 0) {
+#pragma unroll
+        for (int j = 0; j < S; ++j) q[j] = row.template from_copy<true>(at + j * (WARPS * 512), g0 + j * (WARPS * 32));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(done);
+#pragma unroll
+        for (int j = 0; j < S; ++j) absorb<DT>(sums[j], q[j], c, slack);
+      } else {
+#pragma unroll
+        for (int j = 0; j < S; ++j)
+          if (g0 + j * (WARPS * 32) < groups) q[j] = row.from_copy(at + j * (WARPS * 512), g0 + j * (WARPS * 32));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(done);
+#pragma unroll
+        for (int j = 0; j < S; ++j)
+          if (g0 + j * (WARPS * 32) < groups) absorb<DT>(sums[j], q[j], c, slack);
       }
     }
     if (!ok) {   // a wait ran out: this row and the CTA's later ones are NaN
       sums[0].top = NAN;
       if (lane == 0 && a.status) atomicOr(a.status, RLK_STATUS_TIMEOUT);
     }
-    end_of_row<DT, ALIGNED, 1, 32>(sh, a, t, row, 0, sums, given, c, inv_t);
+    end_of_row<DT, false, 1, 32>(sh, a, t, row, 0, sums, given, c, inv_t);
     sync<NT>();   // the next row's parts go where this one's were
   }
 }
@@ -856,10 +868,10 @@ cudaError_t launch_forward(const TokenArgs& a, float c, float inv_t, cudaStream_
   const cudaError_t e = cudaLaunchKernelEx(&cfg, token_forward_kernel<DT, ALIGNED, C, VW>, a, c, inv_t);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
-template <int DT, bool ALIGNED>
+template <int DT>
 cudaError_t launch_stream(const TokenArgs& a, float c, float inv_t, cudaStream_t stream) {
   static std::atomic<int> done[64];
-  const auto kernel = token_stream_kernel<DT, ALIGNED>;
+  const auto kernel = token_stream_kernel<DT>;
   const int ds = device_slot();
   if (ds < 0 || !done[ds].load()) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, RING * SLOT);
@@ -877,8 +889,12 @@ cudaError_t forward_by_rows(const TokenArgs& a, float c, float inv_t, cudaStream
   if (bytes <= kShortRow) return launch_forward<DT, ALIGNED, 1, 16>(a, c, inv_t, stream);
   if (bytes >= kLongRow && a.T * 4 <= sms) return launch_forward<DT, ALIGNED, 4, 32>(a, c, inv_t, stream);
   if (bytes >= kLongRow && a.T <= 2 * sms) return launch_forward<DT, ALIGNED, 2, 32>(a, c, inv_t, stream);
-  if (a.T <= 2 * sms) return launch_forward<DT, ALIGNED, 1, 32>(a, c, inv_t, stream);
-  return launch_stream<DT, ALIGNED>(a, c, inv_t, stream);
+  // Rows off 16-byte boundaries go through the ring (their groups span two words, of which few
+  // fit into registers on their way): 777 x 50021 fp32 with 50 alternatives 51 us, 78 straight;
+  // aligned ones straight into registers with a third more warps: 4096 x 151936 bf16 195 us, 214
+  // through the ring.
+  if (ALIGNED || a.T <= 2 * sms) return launch_forward<DT, ALIGNED, 1, 32>(a, c, inv_t, stream);
+  return launch_stream<DT>(a, c, inv_t, stream);
 }
 
 }  // namespace
