@@ -86,7 +86,7 @@ __device__ __forceinline__ void gated_column(const GatedOut& o, int64_t row, int
 }
 
 struct ForwardOp {
-  static constexpr bool A_MN = false, B_MN = false, F16 = false, DUAL = true, SYM = false, STACKED = false;
+  static constexpr bool A_MN = false, B_MN = false, F16 = false, DUAL = true, STACKED = false, TRI_A = false, TRI_B = false;
   struct Params {
     Loop loop;
     int64_t M, N;
@@ -96,9 +96,9 @@ struct ForwardOp {
   static __device__ __forceinline__ Tile tile(const Params& p, int t, int tm, int bn) {
     int mt, nt;
     gemm::grouped(t, p.n_mt, p.n_nt, mt, nt);
-    return Tile{mt * tm, nt * bn, (int64_t)mt * tm, (int64_t)nt * bn, p.M, p.N, 0, false};
+    return Tile{mt * tm, nt * bn, (int64_t)mt * tm, (int64_t)nt * bn, p.M, p.N, 0};
   }
-  static __device__ __forceinline__ void source(const Params&, const Tile&, int&, int&, int&) {}
+  static __device__ __forceinline__ void source(const Tile&, int, int&, int&) {}
   static __device__ __forceinline__ bool vec(const Params& p) { return p.vec != 0; }
   struct Aux {};
   static __device__ __forceinline__ void aux8(const Params&, const Tile&, int64_t, int64_t, int, Aux&) {}
@@ -164,11 +164,11 @@ struct StoreOut {
 // else two products (of which the second takes a[1]), one after the other in the tiles' order.
 template <bool A_MN_, bool KCAT>
 struct StoreOp {
-  static constexpr bool A_MN = A_MN_, B_MN = true, F16 = false, DUAL = false, SYM = false, STACKED = false;
+  static constexpr bool A_MN = A_MN_, B_MN = true, F16 = false, DUAL = false, STACKED = false, TRI_A = false, TRI_B = false;
   struct Params {
     Loop loop;
     int64_t M, N;
-    int n_mt, n_nt, vec, half;   // half: K's steps in the first maps
+    int n_mt, n_nt, vec;
     int y_dtype, accumulate;
     StoreOut out[2];
   };
@@ -176,17 +176,11 @@ struct StoreOp {
     const int which = KCAT ? 0 : t / (p.n_mt * p.n_nt);
     int mt, nt;
     gemm::grouped(t - which * p.n_mt * p.n_nt, p.n_mt, p.n_nt, mt, nt);
-    return Tile{mt * tm, nt * bn, (int64_t)mt * tm, (int64_t)nt * bn, p.M, p.N, which, false};
+    return Tile{mt * tm, nt * bn, (int64_t)mt * tm, (int64_t)nt * bn, p.M, p.N, which};
   }
-  static __device__ __forceinline__ void source(const Params& p, const Tile& tl, int& k, int& ia, int& ib) {
-    if (KCAT) {
-      if (k >= p.half) {
-        k -= p.half;
-        ia = ib = 1;
-      }
-    } else {
-      ia = tl.which;
-    }
+  static __device__ __forceinline__ void source(const Tile& tl, int part, int& ia, int& ib) {
+    if (KCAT) ia = ib = part;
+    else ia = tl.which;
   }
   static __device__ __forceinline__ bool vec(const Params& p) { return p.vec != 0; }
   struct Aux {};
@@ -542,7 +536,7 @@ cudaError_t launch_gated_fwd(const GatedArgs& a, cudaStream_t stream) {
   Operand x{a.x, a.ldx}, wg{a.w[0], a.ldw[0]}, wu{a.w[1], a.ldw[1]};
   if (cudaError_t e = aligned_operands({{&x, a.M, a.K}, {&wg, a.N, a.K}, {&wu, a.N, a.K}}, ws, stream); e != cudaSuccess) return e;
   const bool few = few_tiles(a.M, a.N, 1, 64);
-  Maps maps;
+  Maps maps{};
   const int a_rows = few && a.M < 128 ? (int)pad8(a.M) : 128;
   if (!gemm::make_map(&maps.a[0], false, x, false, a.M, a.K, a_rows) ||
       !gemm::make_map(&maps.b[0], false, wg, false, a.N, a.K, few ? 64 : 128) ||
@@ -619,7 +613,7 @@ cudaError_t launch_gated_bwd(const GatedBwdArgs& a, cudaStream_t stream) {
   if ((e = aligned_operands({{a.dx ? &wg : nullptr, a.N, a.K}, {a.dx ? &wu : nullptr, a.N, a.K}, {a.dw[0] && a.x ? &x : nullptr, a.M, a.K}},
                             ws, stream)) != cudaSuccess)
     return e;
-  Maps maps;
+  Maps maps{};
   if (a.dx) {   // K runs over N twice; the weights [N][K] hold its columns contiguously
     using Op = StoreOp<false, true>;
     const bool few = few_tiles(a.M, a.K, 1, 128);
@@ -630,8 +624,8 @@ cudaError_t launch_gated_bwd(const GatedBwdArgs& a, cudaStream_t stream) {
     Op::Params p{};
     p.M = a.M;
     p.N = a.K;
-    p.half = (int)((a.N + gemm::BK - 1) / gemm::BK);
-    p.loop.k_steps = 2 * p.half;
+    p.loop.part_steps = (int)((a.N + gemm::BK - 1) / gemm::BK);
+    p.loop.k_steps = 2 * p.loop.part_steps;
     p.loop.a_rows = a_rows;
     p.vec = rows16(a.dx, a.dx_dtype, a.lddx);
     p.y_dtype = a.dx_dtype;

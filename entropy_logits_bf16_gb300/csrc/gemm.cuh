@@ -15,22 +15,23 @@
 //   F16          operands fp16, else bf16
 //   DUAL         B's tile is one half of rows of b[0] and one of b[1]: two products that
 //                share A, joined column by column in the epilogue
-//   SYM          D is symmetric: tiles above the diagonal are not computed, off-diagonal ones
-//                are stored twice
+//   TRI_A, TRI_B  the operand is a symmetric matrix (K-contiguous) of which the blocks of loop.tri x
+//                loop.tri above the diagonal are not in memory (0: all are): such a step takes the block's
+//                mirror image, MN-contiguous
 //   STACKED      maps are of stacks of matrices, of which a tile takes number `which`
 //   Params       with `Loop loop`
 //   tile(p, t, tm, bn)   the place of tile t
-//   source(p, tl, k, ia, ib)   which maps step k takes; k made the step in them
+//   source(tl, part, ia, ib)   which maps the steps of a part of K take (loop.part_steps each)
 //   Aux, aux8    what finish8 needs from memory for its row (asked for before the accumulator is
 //                waited for); Cols, cols8: what it needs for its columns
 //   finish8, column8   D's 8 columns of a row / one column of 8 rows `step` apart (of which those
-//                up to n rows on exist), to memory; finish8 leaves in v what was stored (SYM)
-//   turned8, turned1   SYM: 8 (1) of D's rows of one column
+//                up to n rows on exist), to memory
 #pragma once
 
 #include <math.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "internal.h"
 #include "tensor_core.cuh"
@@ -60,15 +61,21 @@ static_assert(BM * Shape<true>::PLD * 4 <= FEW_STAGES * STAGE_BYTES, "a partial 
 struct Maps {
   CUtensorMap a[2], b[2];
 };
+struct TriMaps : Maps {
+  CUtensorMap ta[2], tb[2];   // the mirror images of TRI operands
+};
+template <class Op>
+using MapsOf = std::conditional_t<Op::TRI_A || Op::TRI_B, TriMaps, Maps>;
 struct Tile {
   int a_row, b_row;      // first index of the operands' rows (M, N); MN-contiguous: column
   int64_t row, col;      // first row and column of D
   int64_t rows, cols;    // D's extents
   int which;             // of several products or matrices
-  bool turned;           // SYM: also stored transposed
 };
 struct Loop {
   int n_tiles, k_steps, stages;
+  int part_steps;        // K's steps fall into parts of so many, each from maps of its own (0: one part)
+  int tri;               // side of a TRI operand's blocks (a multiple of a tile's rows), or 0
   int a_rows;            // rows of A's boxes (K-contiguous, tiles of 128 x 128; else 128)
   long long wait_limit;
   int withhold;          // debug: the stage of the first CTA whose barrier waits for an arrival that never comes (-1: none)
@@ -84,9 +91,13 @@ __device__ __forceinline__ void grouped(int t, int n_mt, int n_nt, int& mt, int&
   nt = r / gm;
 }
 
+// The first step of K whose columns lie above the diagonal's blocks for rows from `row` on (a tile
+// and a stage lie in one block each).
+__device__ __forceinline__ int mirror_from(const Loop& l, int row) { return l.tri ? (row / l.tri + 1) * (l.tri / BK) : 0x7FFFFFFF; }
+
 template <class Op, bool SPLIT>
 __global__ void __launch_bounds__(Shape<SPLIT>::THREADS, SPLIT ? 2 : 1)
-    gemm_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ typename Op::Params p, int cluster) {
+    gemm_tiles_kernel(const __grid_constant__ MapsOf<Op> maps, const __grid_constant__ typename Op::Params p, int cluster) {
   using S = Shape<SPLIT>;
   constexpr int G = S::G, TM = S::TM, BN = S::BN, PLD = S::PLD, EPI_WARPS = S::EPI_WARPS;
   constexpr int OUT = Op::DUAL ? BN / 2 : BN;   // D's columns of a tile
@@ -154,6 +165,10 @@ __global__ void __launch_bounds__(Shape<SPLIT>::THREADS, SPLIT ? 2 : 1)
       bool ok = true;
       for (int t = tile0; t < p.loop.n_tiles && ok; t += tile_step) {
         const Tile tl = Op::tile(p, t, TM, OUT);
+        const int am = tl.a_row + a_off, bn = tl.b_row + (SPLIT ? 0 : (int)rank * BROWS);
+        const int a_mirror = Op::TRI_A ? mirror_from(p.loop, am) : 0, b_mirror = Op::TRI_B ? mirror_from(p.loop, bn) : 0;
+        int part = k0 / p.loop.part_steps, ks = k0 - part * p.loop.part_steps, ia = 0, ib = 0;
+        Op::source(tl, part, ia, ib);
         for (int k = k0; k < k1; ++k) {
           if (!tc::wait(empty0 + 8 * stage, phase ^ 1u, abort_flag, limit) || *abort_flag) {
             ok = false;
@@ -173,12 +188,12 @@ __global__ void __launch_bounds__(Shape<SPLIT>::THREADS, SPLIT ? 2 : 1)
               else tc::load_2d(dst, map, to, x, y);
             }
           };
-          int ks = k, ia = 0, ib = 0;
-          Op::source(p, tl, ks, ia, ib);
-          const int am = tl.a_row + a_off, ak = ks * BK, bk = ks * BK;
-          if (Op::A_MN) {
+          const int ak = ks * BK, bk = ak;
+          if (Op::A_MN || (Op::TRI_A && ks >= a_mirror)) {
+            const CUtensorMap* map = &maps.a[ia];
+            if constexpr (Op::TRI_A) map = &maps.ta[ia];
 #pragma unroll
-            for (int j = 0; j < BM / 64; ++j) load(sa + j * MN_BLOCK, &maps.a[ia], am + j * 64, ak);
+            for (int j = 0; j < BM / 64; ++j) load(sa + j * MN_BLOCK, map, am + j * 64, ak);
           } else {
             load(sa, &maps.a[ia], ak, am);
           }
@@ -188,10 +203,11 @@ __global__ void __launch_bounds__(Shape<SPLIT>::THREADS, SPLIT ? 2 : 1)
           } else if (Op::DUAL) {     // 128 rows of one in each CTA
             load(sb, &maps.b[rank], bk, tl.b_row);
           } else {
-            const int bn = tl.b_row + (SPLIT ? 0 : (int)rank * BROWS);
-            if (Op::B_MN) {
+            if (Op::B_MN || (Op::TRI_B && ks >= b_mirror)) {
+              const CUtensorMap* map = &maps.b[ib];
+              if constexpr (Op::TRI_B) map = &maps.tb[ib];
 #pragma unroll
-              for (int j = 0; j < BROWS / 64; ++j) load(sb + j * MN_BLOCK, &maps.b[ib], bn + j * 64, bk);
+              for (int j = 0; j < BROWS / 64; ++j) load(sb + j * MN_BLOCK, map, bn + j * 64, bk);
             } else {
               load(sb, &maps.b[ib], bk, bn);
             }
@@ -199,6 +215,10 @@ __global__ void __launch_bounds__(Shape<SPLIT>::THREADS, SPLIT ? 2 : 1)
           used |= 1u << stage;
           last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
           if (++stage == stages) { stage = 0; phase ^= 1u; }
+          if (++ks == p.loop.part_steps) {
+            ks = ia = ib = 0;
+            Op::source(tl, ++part, ia, ib);
+          }
         }
       }
       // Every copy lands before the CTAs exit (bounded), also when another role's wait runs
@@ -213,23 +233,33 @@ __global__ void __launch_bounds__(Shape<SPLIT>::THREADS, SPLIT ? 2 : 1)
     if (lane == 0 && leader) {
       int stage = 0;
       uint32_t phase = 0, tile = 0;
+      const uint64_t a0_k = tc::desc_k(base), a0_mn = tc::desc_mn(base, MN_BLOCK);
+      const uint64_t b0_k = tc::desc_k(base + A_BYTES), b0_mn = tc::desc_mn(base + A_BYTES, MN_BLOCK);
       bool ok = true;
       for (int t = tile0; t < p.loop.n_tiles && ok; t += tile_step, ++tile) {
         const uint32_t acc = tile & 1u, accph = (tile >> 1) & 1u;
         if (!tc::wait<G == 2>(acce0 + 8 * acc, accph ^ 1u, abort_flag, limit)) { ok = false; break; }
         tc::fence_after();
         const uint32_t d_tmem = tmem + acc * BN;
+        int a_mirror = 0, b_mirror = 0, ks = 0;
+        if constexpr (Op::TRI_A || Op::TRI_B) {
+          const Tile tl = Op::tile(p, t, TM, OUT);
+          a_mirror = mirror_from(p.loop, tl.a_row);
+          b_mirror = mirror_from(p.loop, tl.b_row);
+          ks = k0 % p.loop.part_steps;
+        }
         for (int k = k0; k < k1; ++k) {
           if (!tc::wait(full0 + 8 * stage, phase, abort_flag, limit)) { ok = false; break; }
           tc::fence_after();
-          const uint32_t sa = base + stage * STAGE_BYTES, sb = sa + A_BYTES;
+          // 16 K elements: 32 bytes inside a K-contiguous row, 16 rows of an MN-contiguous block
+          const bool a_mn = Op::A_MN || (Op::TRI_A && ks >= a_mirror), b_mn = Op::B_MN || (Op::TRI_B && ks >= b_mirror);
+          const uint64_t at = (uint64_t)(stage * (int)(STAGE_BYTES >> 4));   // (the address fields do not overflow)
+          const uint64_t da = (a_mn ? a0_mn : a0_k) + at, db = (b_mn ? b0_mn : b0_k) + at;
+          const uint64_t a16 = a_mn ? 2048 / 16 : 2, b16 = b_mn ? 2048 / 16 : 2;
+          const uint32_t id = idesc | (uint32_t)a_mn << 15 | (uint32_t)b_mn << 16;
 #pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk) {
-            // 16 K elements: 32 bytes inside a K-contiguous row, 16 rows of an MN-contiguous block
-            const uint64_t da = Op::A_MN ? tc::desc_mn(sa + kk * 2048, MN_BLOCK) : tc::desc_k(sa) + (uint64_t)(kk * 2);
-            const uint64_t db = Op::B_MN ? tc::desc_mn(sb + kk * 2048, MN_BLOCK) : tc::desc_k(sb) + (uint64_t)(kk * 2);
-            tc::mma<G>(d_tmem, da, db, idesc, (k > k0 || kk > 0) ? 1u : 0u);
-          }
+          for (int kk = 0; kk < BK / 16; ++kk) tc::mma<G>(d_tmem, da + kk * a16, db + kk * b16, id, (k > k0 || kk > 0) ? 1u : 0u);
+          if ((Op::TRI_A || Op::TRI_B) && ++ks == p.loop.part_steps) ks = 0;
           tc::commit<G>(empty0 + 8 * stage);
           if (++stage == stages) { stage = 0; phase ^= 1u; }
         }
@@ -319,11 +349,11 @@ __global__ void __launch_bounds__(Shape<SPLIT>::THREADS, SPLIT ? 2 : 1)
           const int n = (int)(tl.cols - col < 8 ? (tl.cols - col > 0 ? tl.cols - col : 0) : 8);
           stage_in(v);
           if (Op::vec(p)) {
-            float o[4][8];
-#pragma unroll
-            for (int it = 0; it < 4; ++it) get8(it * 8 + r8, o[it]);
-            __syncwarp();
+            float o[TWICE ? 4 : 1][8];
             if constexpr (TWICE) {
+#pragma unroll
+              for (int it = 0; it < 4; ++it) get8(it * 8 + r8, o[it]);
+              __syncwarp();
               read32(v, OUT + c0);
               release();
               stage_in(v);
@@ -334,31 +364,11 @@ __global__ void __launch_bounds__(Shape<SPLIT>::THREADS, SPLIT ? 2 : 1)
             for (int it = 0; it < 4; ++it) {
               const int r = it * 8 + r8;
               float w[8];
-              if constexpr (Op::DUAL) get8(r, w);
-              if (row0 + r < tl.rows && n > 0) Op::finish8(p, tl, row0 + r, col, n, o[it], w, aux[it], cols);
-              if constexpr (Op::SYM) {
-                if (tl.turned) {
-                  float4* dst = reinterpret_cast<float4*>(st + r * 32);
-                  dst[(2 * sub) ^ (r & 7)] = make_float4(o[it][0], o[it][1], o[it][2], o[it][3]);
-                  dst[(2 * sub + 1) ^ (r & 7)] = make_float4(o[it][4], o[it][5], o[it][6], o[it][7]);
-                }
-              }
+              get8(r, TWICE ? w : o[0]);
+              if (row0 + r < tl.rows && n > 0) Op::finish8(p, tl, row0 + r, col, n, o[TWICE ? it : 0], w, aux[it], cols);
             }
             if (ch + 1 < WIDTH / 32) ask(col0 + 32);
             __syncwarp();
-            if constexpr (Op::SYM) {
-              if (tl.turned) {   // a lane: 8 rows (sub) of one column (8 it + r8)
-#pragma unroll
-                for (int it = 0; it < 4; ++it) {
-                  const int c = it * 8 + r8;
-                  float w[8];
-#pragma unroll
-                  for (int j = 0; j < 8; ++j) w[j] = st[(sub * 8 + j) * 32 + (((c >> 2) ^ j) << 2) + (c & 3)];
-                  Op::turned8(p, tl, row0 + sub * 8, col0 + c, w);
-                }
-                __syncwarp();
-              }
-            }
           } else {
             // a lane: one column, 8 rows at a time, so that a warp stores 32 consecutive columns
             const int rows = (int)(tl.rows - row0 < 32 ? tl.rows - row0 : 32);
@@ -394,14 +404,14 @@ __global__ void __launch_bounds__(Shape<SPLIT>::THREADS, SPLIT ? 2 : 1)
     const Tile tl = Op::tile(p, tile0, TM, OUT);
     const int width = OUT / cluster, c0 = (int)rank * width;   // this CTA's share of the columns, all rows
     const int rows = (int)(tl.rows - tl.row < BM ? tl.rows - tl.row : BM);
-    // 8 columns of a row at a time: consecutive threads along a row; along a column where D is
-    // stored transposed too.  What an item needs from memory is asked for an item ahead.
-    const int octs = width / 8, items = (Op::SYM ? BM : rows) * octs;
+    // 8 columns of a row at a time, consecutive threads along a row.  What an item needs from
+    // memory is asked for an item ahead.
+    const int octs = width / 8, items = rows * octs;
     auto place = [&](int i, int& r, int& c, int& n) {
-      r = Op::SYM ? i % BM : i / octs;
-      c = c0 + (Op::SYM ? i / BM : i - r * octs) * 8;
+      r = i / octs;
+      c = c0 + (i - r * octs) * 8;
       const int64_t left = tl.cols - tl.col - c;
-      n = i < items && r < rows ? (int)(left < 8 ? (left > 0 ? left : 0) : 8) : 0;
+      n = i < items ? (int)(left < 8 ? (left > 0 ? left : 0) : 8) : 0;
     };
     const bool vec = Op::vec(p);
     typename Op::Aux next{};
@@ -451,13 +461,6 @@ __global__ void __launch_bounds__(Shape<SPLIT>::THREADS, SPLIT ? 2 : 1)
         typename Op::Cols cols{};
         Op::cols8(p, tl, col, n, cols);
         Op::finish8(p, tl, tl.row + r, col, n, v, u, aux, cols);
-        if constexpr (Op::SYM) {
-          if (tl.turned) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (j < n) Op::turned1(p, tl, tl.row + r, col + j, v[j]);
-          }
-        }
       }
     } else {
       // a column a thread, 8 rows at a time
@@ -542,7 +545,8 @@ cudaError_t set_smem() {
 }
 
 // CTAs that share a tile's K when there are `tiles` tiles of 128 x 128: 2 or 4 while all have
-// an SM and two stages of K each, or half an SM and at least eight.
+// an SM and two stages of K each, or half an SM and at least eight.  (40 tiles of 16 stages by
+// 4 on 152 SMs, eight of which then have two CTAs: 1.8 us slower than by 2.)
 inline int split_for(int tiles, int k_steps) {
   int s = 1;
   while (s < MAX_SPLIT && ((k_steps >= 4 * s && tiles * 2 * s <= sm_count()) || (k_steps >= 16 * s && tiles * 2 * s <= 2 * sm_count()))) s *= 2;
@@ -551,10 +555,11 @@ inline int split_for(int tiles, int k_steps) {
 
 // One launch over p.loop.n_tiles tiles, as a programmatic dependent of the kernel before it.
 template <class Op, bool SPLIT>
-cudaError_t launch(const Maps& maps, typename Op::Params p, cudaStream_t stream) {
+cudaError_t launch(const MapsOf<Op>& maps, typename Op::Params p, cudaStream_t stream) {
   if (cudaError_t e = set_smem<Op, SPLIT>(); e != cudaSuccess) return e;
   const int tiles = p.loop.n_tiles, split = SPLIT ? split_for(tiles, p.loop.k_steps) : 1;
   if (!SPLIT || p.loop.a_rows == 0) p.loop.a_rows = BM;
+  if (p.loop.part_steps == 0) p.loop.part_steps = p.loop.k_steps;
   p.loop.wait_limit = debug_wait_limit();
   p.loop.withhold = (int)debug_take_withheld();
   p.loop.stages = SPLIT && tiles * split > sm_count() ? FEW_STAGES : Shape<SPLIT>::STAGES;

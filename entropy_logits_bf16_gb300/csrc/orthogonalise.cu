@@ -4,10 +4,12 @@
 // (rows <= columns; else A = X^T X and X <- a X + X P).  Each step maps the singular values by
 // s -> a s + b s^3 + c s^5 and leaves the singular vectors.
 //
-// Three products a step on the tcgen05 kernel of gemm.cuh.  A and P are symmetric, so only the
-// tiles on and below the diagonal are computed and the others stored from them.  Nothing is
-// transposed in memory: X is taken with its rows' or its columns' index contiguous.  A stack
-// of matrices is one launch a product, by three-dimensional tensor maps.
+// Three products a step on the tcgen05 kernel of gemm.cuh.  A and P are symmetric: only their
+// blocks of 256 x 256 (or 128 x 128) on and below the diagonal are computed and stored, and a product takes a
+// missing block as the mirror image of the one that is there, with the other index contiguous
+// (storing each twice took a third of these products' epilogues).  Nothing is transposed in
+// memory: X too is taken with its rows' or its columns' index contiguous.  A stack of matrices
+// is one launch a product, by three-dimensional tensor maps.
 //
 // Numbers.  The products' operands are fp16 (11 bits where bf16 has 8, at the same rate), held
 // times 2^10: the iterates' entries lie between about 1 / (longer side) and 1.2, so that a matrix
@@ -32,7 +34,6 @@ namespace rlk {
 namespace {
 
 using gemm::Loop;
-using gemm::Maps;
 using gemm::Operand;
 using gemm::Tile;
 
@@ -47,17 +48,15 @@ __device__ __forceinline__ uint32_t pack_half(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 __device__ __forceinline__ float2 unpack_half(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
-__device__ __forceinline__ void halves(const uint4& q, float (&v)[8]) {
-  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float2 f = unpack_half(w[j]);
-    v[2 * j] = f.x;
-    v[2 * j + 1] = f.y;
-  }
+// Eight numbers as four pairs.
+__device__ __forceinline__ void halves(const uint4& q, float2 (&v)[4]) {
+  v[0] = unpack_half(q.x);
+  v[1] = unpack_half(q.y);
+  v[2] = unpack_half(q.z);
+  v[3] = unpack_half(q.w);
 }
-__device__ __forceinline__ uint4 to_halves(const float (&v)[8]) {
-  return make_uint4(pack_half(v[0], v[1]), pack_half(v[2], v[3]), pack_half(v[4], v[5]), pack_half(v[6], v[7]));
+__device__ __forceinline__ uint4 to_halves(const float2 (&v)[4]) {
+  return make_uint4(pack_half(v[0].x, v[0].y), pack_half(v[1].x, v[1].y), pack_half(v[2].x, v[2].y), pack_half(v[3].x, v[3].y));
 }
 
 // A stack of B matrices of the iteration, each number in two fp16 (rest may be NULL: one); rows
@@ -66,20 +65,15 @@ struct Buffer {
   uint16_t *value, *rest;
   int64_t ld, matrix;   // strides in elements
   __device__ __forceinline__ int64_t at(int b, int64_t row, int64_t col) const { return b * matrix + row * ld + col; }
-  __device__ __forceinline__ void store8(int64_t i, const float (&v)[8]) const {
+  __device__ __forceinline__ void store8(int64_t i, const float2 (&v)[4]) const {
     const uint4 h = to_halves(v);
     *reinterpret_cast<uint4*>(value + i) = h;
     if (!rest) return;
-    float x[8];
+    float2 x[4];
     halves(h, x);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = __fsub_rn(v[j], x[j]);
+    for (int j = 0; j < 4; ++j) x[j] = fma2(x[j], both(-1.f), v[j]);
     *reinterpret_cast<uint4*>(rest + i) = to_halves(x);
-  }
-  __device__ __forceinline__ void store1(int64_t i, float v) const {
-    const uint16_t h = (uint16_t)pack_half(v, 0.f);
-    value[i] = h;
-    if (rest) rest[i] = (uint16_t)pack_half(__fsub_rn(v, unpack_half(h).x), 0.f);
   }
 };
 // 8 numbers of one, asked for ahead.
@@ -87,57 +81,59 @@ struct Eight {
   uint4 value, rest;
   __device__ __forceinline__ void ask(const Buffer& b, int64_t i) {
     value = *reinterpret_cast<const uint4*>(b.value + i);
-    if (b.rest) rest = *reinterpret_cast<const uint4*>(b.rest + i);   // (else 0)
+    if (b.rest) rest = *reinterpret_cast<const uint4*>(b.rest + i);
   }
-  __device__ __forceinline__ void floats(float (&v)[8]) const {
-    float r[8];
-    halves(value, v);
-    halves(rest, r);
+  // their product with f, plus v
+  __device__ __forceinline__ void add_to(const Buffer& b, float f, float2 (&v)[4]) const {
+    float2 x[4];
+    halves(value, x);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = __fadd_rn(v[j], r[j]);
+    for (int j = 0; j < 4; ++j) v[j] = fma2(x[j], both(f), v[j]);
+    if (!b.rest) return;
+    halves(rest, x);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = fma2(x[j], both(f), v[j]);
   }
 };
-// Step k of a product that is one or three sums of `steps` steps: values, value times rest, rest
-// times value.
-__device__ __forceinline__ void of_three(int steps, int& k, int& ia, int& ib) {
-  const int term = k / steps;
-  k -= term * steps;
-  ia = term == 2;
-  ib = term == 1;
+// A product is one or three sums (parts): values, values times rest, rest times values.
+__device__ __forceinline__ void of_three(int part, int& ia, int& ib) {
+  ia = part == 2;
+  ib = part == 1;
 }
 
-// Tile t of stacked matrices, `per` tiles each.
-__device__ __forceinline__ Tile stacked(int t, int per, int n_mt, int n_nt, int tm, int tn, int64_t rows, int64_t cols, bool sym) {
+// Tile t of stacked matrices, `per` tiles each; tri: of the blocks of tri x tri on and below the
+// diagonal, row by row (a block is a tile, or four).
+__device__ __forceinline__ Tile stacked(int t, int per, int n_mt, int n_nt, int tm, int tn, int64_t rows, int64_t cols, int tri) {
   const int b = t / per, r = t - b * per;
   int mt, nt;
-  if (sym) {   // row mt of the triangle starts at mt (mt + 1) / 2
-    mt = (int)((sqrtf(8.f * (float)r + 1.f) - 1.f) * 0.5f);
-    while ((mt + 1) * (mt + 2) / 2 <= r) ++mt;
-    while (mt * (mt + 1) / 2 > r) --mt;
-    nt = r - mt * (mt + 1) / 2;
+  if (tri) {
+    const int in = tri / tm, q = r / (in * in), u = r - q * in * in;   // in: 1 or 2
+    mt = (int)((sqrtf(8.f * (float)q + 1.f) - 1.f) * 0.5f);                   // row mt starts at mt (mt + 1) / 2
+    while ((mt + 1) * (mt + 2) / 2 <= q) ++mt;
+    while (mt * (mt + 1) / 2 > q) --mt;
+    nt = (q - mt * (mt + 1) / 2) * in + u % in;
+    mt = mt * in + u / in;
   } else {
     gemm::grouped(r, n_mt, n_nt, mt, nt);
   }
-  return Tile{mt * tm, nt * tn, (int64_t)mt * tm, (int64_t)nt * tn, rows, cols, b, sym && mt != nt};
+  return Tile{mt * tm, nt * tn, (int64_t)mt * tm, (int64_t)nt * tn, rows, cols, b};
 }
 
 // A = X X^T (MN: X^T X), and P = b A + c A A (POLY).
 template <bool MN, bool POLY>
 struct SquareOp {
-  static constexpr bool A_MN = MN, B_MN = MN, F16 = true, DUAL = false, SYM = true, STACKED = true;
+  static constexpr bool A_MN = MN, B_MN = MN, F16 = true, DUAL = false, STACKED = true, TRI_A = POLY, TRI_B = POLY;
   struct Params {
     Loop loop;
-    int per, side, steps;
-    int whole;         // tiles a side where all are computed, 0: those on and below the diagonal
+    int per, side;
+    int whole;         // tiles a side where all are computed, 0: the blocks on and below the diagonal
     float scale, b;    // of the accumulators; of A (POLY)
     Buffer a, out;
   };
   static __device__ __forceinline__ Tile tile(const Params& p, int t, int tm, int tn) {
-    return stacked(t, p.per, p.whole, p.whole, tm, tn, p.side, p.side, p.whole == 0);
+    return stacked(t, p.per, p.whole, p.whole, tm, tn, p.side, p.side, p.loop.tri);
   }
-  static __device__ __forceinline__ void source(const Params& p, const Tile&, int& k, int& ia, int& ib) {
-    of_three(p.steps, k, ia, ib);
-  }
+  static __device__ __forceinline__ void source(const Tile&, int part, int& ia, int& ib) { of_three(part, ia, ib); }
   static __device__ __forceinline__ bool vec(const Params&) { return true; }
   struct Aux {
     Eight a;
@@ -149,29 +145,22 @@ struct SquareOp {
   static __device__ __forceinline__ void cols8(const Params&, const Tile&, int64_t, int, Cols&) {}
   static __device__ __forceinline__ void finish8(const Params& p, const Tile& tl, int64_t row, int64_t col, int, float (&v)[8],
                                                  float (&)[8], const Aux& x, const Cols&) {
-    float a[8];
-    if (POLY) x.a.floats(a);
+    float2 o[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = POLY ? __fmaf_rn(v[j], p.scale, __fmul_rn(a[j], p.b)) : __fmul_rn(v[j], p.scale);
-    p.out.store8(p.out.at(tl.which, row, col), v);   // rows are padded to 8 columns
+    for (int j = 0; j < 4; ++j) o[j] = mul2(make_float2(v[2 * j], v[2 * j + 1]), both(p.scale));
+    if (POLY) x.a.add_to(p.a, p.b, o);
+    p.out.store8(p.out.at(tl.which, row, col), o);   // rows are padded to 8 columns
   }
   static __device__ __forceinline__ void column8(const Params&, const Tile&, int64_t, int, int, int64_t, float (&)[8], float (&)[8]) {}
-  // v: column col of rows row .. row + 7
-  static __device__ __forceinline__ void turned8(const Params& p, const Tile& tl, int64_t row, int64_t col, const float (&v)[8]) {
-    if (col < p.side && row < p.side) p.out.store8(p.out.at(tl.which, col, row), v);
-  }
-  static __device__ __forceinline__ void turned1(const Params& p, const Tile& tl, int64_t row, int64_t col, float v) {
-    p.out.store1(p.out.at(tl.which, col, row), v);
-  }
 };
 
 // X <- a X + P X (TALL: a X + X P), to two fp16 or, the last time, to the caller's bf16.
 template <bool TALL>
 struct ApplyOp {
-  static constexpr bool A_MN = false, B_MN = !TALL, F16 = true, DUAL = false, SYM = false, STACKED = true;
+  static constexpr bool A_MN = false, B_MN = !TALL, F16 = true, DUAL = false, STACKED = true, TRI_A = !TALL, TRI_B = TALL;
   struct Params {
     Loop loop;
-    int per, n_mt, n_nt, steps;
+    int per, n_mt, n_nt;
     int64_t m, n;
     float a;
     Buffer x, to;
@@ -180,11 +169,9 @@ struct ApplyOp {
     int out_vec;            // its rows start on 16-byte boundaries
   };
   static __device__ __forceinline__ Tile tile(const Params& p, int t, int tm, int tn) {
-    return stacked(t, p.per, p.n_mt, p.n_nt, tm, tn, p.m, p.n, false);
+    return stacked(t, p.per, p.n_mt, p.n_nt, tm, tn, p.m, p.n, 0);
   }
-  static __device__ __forceinline__ void source(const Params& p, const Tile&, int& k, int& ia, int& ib) {
-    of_three(p.steps, k, ia, ib);
-  }
+  static __device__ __forceinline__ void source(const Tile&, int part, int& ia, int& ib) { of_three(part, ia, ib); }
   static __device__ __forceinline__ bool vec(const Params& p) { return !p.out || p.out_vec; }
   struct Aux {
     Eight x;
@@ -196,18 +183,20 @@ struct ApplyOp {
   static __device__ __forceinline__ void cols8(const Params&, const Tile&, int64_t, int, Cols&) {}
   static __device__ __forceinline__ void finish8(const Params& p, const Tile& tl, int64_t row, int64_t col, int n, float (&v)[8],
                                                  float (&)[8], const Aux& x, const Cols&) {
-    float h[8];
-    x.x.floats(h);
+    float2 o[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = __fmaf_rn(v[j], kDown, __fmul_rn(p.a, h[j]));
+    for (int j = 0; j < 4; ++j) o[j] = mul2(make_float2(v[2 * j], v[2 * j + 1]), both(kDown));
+    x.x.add_to(p.x, p.a, o);
     if (p.out) {
-      uint16_t* o = p.out + tl.which * p.out_matrix + row * p.ldo + col;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], kDown);
-      store8(o, v, n);
+      for (int j = 0; j < 4; ++j) {
+        v[2 * j] = __fmul_rn(o[j].x, kDown);
+        v[2 * j + 1] = __fmul_rn(o[j].y, kDown);
+      }
+      store8(p.out + tl.which * p.out_matrix + row * p.ldo + col, v, n);
       return;
     }
-    p.to.store8(p.to.at(tl.which, row, col), v);
+    p.to.store8(p.to.at(tl.which, row, col), o);
   }
   // the caller's rows that do not start on 16-byte boundaries
   static __device__ __forceinline__ void column8(const Params& p, const Tile& tl, int64_t row, int step, int n, int64_t col,
@@ -379,9 +368,10 @@ __global__ void __launch_bounds__(OT) orth_start_kernel(const Start a) {
     const unsigned r = i / octs, c = (i - r * octs) * 8;
     float v[8];
     load8<DT>(a.g, base + r * a.ldg + c, a.n - c < 8 ? (int)(a.n - c) : 8, a.vec, v);
+    float2 x[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(__fmul_rn(__fmul_rn(v[j], f1), f2), f0);
-    a.x.store8(a.x.at(b, r, c), v);
+    for (int j = 0; j < 4; ++j) x[j] = mul2(mul2(mul2(make_float2(v[2 * j], v[2 * j + 1]), both(f1)), both(f2)), both(f0));
+    a.x.store8(a.x.at(b, r, c), x);
   }
 }
 
@@ -420,35 +410,53 @@ bool stack_map(CUtensorMap* map, void* p, const Buffer& o, int64_t B, int64_t ro
            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Pairs' tiles where small ones would be more than the SMs, as for the linear layer; tiles of
-// a symmetric product on and below the diagonal, but all of them where there are SMs for all
-// with K split by four.
-template <class Op>
-cudaError_t run_square(const Maps& maps, typename Op::Params& p, int64_t B, cudaStream_t stream) {
-  auto triangle = [&](int64_t tm) {
-    const int64_t t = (p.side + tm - 1) / tm;
-    return t * (t + 1) / 2;
-  };
-  const bool few = p.side <= 128 || B * triangle(128) <= sm_count();
-  const int64_t t = (p.side + 127) / 128;
-  p.whole = few && 4 * B * t * t <= sm_count() ? (int)t : 0;
-  const int64_t per = p.whole ? t * t : triangle(few ? 128 : 256);
-  if (B * per > (1 << 30)) return cudaErrorInvalidValue;
-  p.per = (int)per;
-  p.loop.n_tiles = (int)(B * per);
-  return few ? gemm::launch<Op, true>(maps, p, stream) : gemm::launch<Op, false>(maps, p, stream);
+// The tiles of the products: small ones where there is an SM for each, else pairs', as for the
+// linear layer.  Of A and P all where there are SMs for all with K split by four; else the
+// blocks on and below the diagonal, of 128 where X's tiles are small ones too.  A pair's tile
+// needs blocks of 256, so X's are also small ones, two an SM, where those of A and P then get K
+// split by four and with blocks of 256 would not (1024 x 4096: 230 us in all, 254 with pairs).
+struct Cover {
+  bool few, x_few;
+  int whole, tri, per;   // tiles a side where all of A's are there, else 0; blocks' side, or 0; A's tiles of a matrix
+  bool fits;
+};
+Cover cover(int64_t B, int64_t m, int64_t n) {
+  const int64_t side = m < n ? m : n, sms = sm_count(), t = (side + 127) / 128, u = (side + 255) / 256;
+  const int64_t of128 = B * t * (t + 1) / 2, of256 = B * u * (u + 1) / 2, x_small = B * ((m + 127) / 128) * ((n + 127) / 128);
+  Cover c{};
+  c.x_few = m <= 128 || x_small <= sms;
+  if (side <= 128 || 4 * B * t * t <= sms) {
+    c.few = true;
+    c.whole = (int)t;
+  } else if (of128 <= sms && (c.x_few || (x_small <= 2 * sms && 4 * of128 <= sms && 16 * of256 > sms))) {
+    c.few = c.x_few = true;
+    c.tri = 128;
+  } else {
+    c.few = 4 * of256 <= sms;
+    c.tri = 256;
+  }
+  const int64_t per = c.whole ? t * t : (c.tri == 128 ? t * (t + 1) / 2 : u * (u + 1) / 2 * (c.few ? 4 : 1));
+  c.per = (int)per;
+  c.fits = B * per <= (1 << 30) && x_small <= (1 << 30);
+  return c;
 }
 template <class Op>
-cudaError_t run_apply(const Maps& maps, typename Op::Params& p, int64_t B, cudaStream_t stream) {
-  const int64_t small = B * ((p.m + 127) / 128) * ((p.n + 127) / 128);
-  const bool few = p.m <= 128 || small <= sm_count();
-  const int tm = few ? 128 : 256;
+cudaError_t run_square(const gemm::MapsOf<Op>& maps, typename Op::Params& p, int64_t B, const Cover& c, cudaStream_t stream) {
+  p.whole = c.whole;
+  p.per = c.per;
+  p.loop.n_tiles = (int)(B * c.per);
+  p.loop.tri = c.tri;
+  return c.few ? gemm::launch<Op, true>(maps, p, stream) : gemm::launch<Op, false>(maps, p, stream);
+}
+template <class Op>
+cudaError_t run_apply(const gemm::MapsOf<Op>& maps, typename Op::Params& p, int64_t B, const Cover& c, cudaStream_t stream) {
+  const int tm = c.x_few ? 128 : 256;
   p.n_mt = (int)((p.m + tm - 1) / tm);
   p.n_nt = (int)((p.n + tm - 1) / tm);
-  if (small > (1 << 30)) return cudaErrorInvalidValue;
   p.per = p.n_mt * p.n_nt;
   p.loop.n_tiles = (int)(B * p.per);
-  return few ? gemm::launch<Op, true>(maps, p, stream) : gemm::launch<Op, false>(maps, p, stream);
+  p.loop.tri = c.tri;
+  return c.x_few ? gemm::launch<Op, true>(maps, p, stream) : gemm::launch<Op, false>(maps, p, stream);
 }
 
 template <bool TALL>
@@ -489,17 +497,20 @@ cudaError_t iterate(const OrthArgs& a, const Layout& l, cudaStream_t stream) {
   using Gram = SquareOp<TALL, false>;
   using Poly = SquareOp<false, true>;
   using Apply = ApplyOp<TALL>;
-  // maps of both halves of X in boxes of 128 rows, and of 64 (its columns' index contiguous), of A, of P
-  CUtensorMap of_x[2][2][2], of_gram[2], of_poly[2];
+  // maps of both halves of X, A and P in boxes of 128 rows, and of 64 (their columns' index contiguous)
+  CUtensorMap of_x[2][2][2], of_gram[2][2], of_poly[2][2];
   bool ok = true;
   for (int h = 0; h < 2; ++h) {
     for (int i = 0; i < 2; ++i)
       for (int j = 0; j < 2; ++j)
         ok = ok && stack_map(&of_x[i][j][h], h ? x[i].rest : x[i].value, x[i], a.B, a.m, a.n, j ? 64 : 128);
     const bool two = h && l.precise;   // else never taken
-    ok = ok && stack_map(&of_gram[h], two ? gram.rest : gram.value, gram, a.B, l.side, l.side, 128) &&
-         stack_map(&of_poly[h], two ? poly.rest : poly.value, poly, a.B, l.side, l.side, 128);
+    for (int j = 0; j < 2; ++j)
+      ok = ok && stack_map(&of_gram[j][h], two ? gram.rest : gram.value, gram, a.B, l.side, l.side, j ? 64 : 128) &&
+           stack_map(&of_poly[j][h], two ? poly.rest : poly.value, poly, a.B, l.side, l.side, j ? 64 : 128);
   }
+  const Cover cov = cover(a.B, a.m, a.n);
+  ok = ok && cov.fits;
   if (!ok) return cudaErrorInvalidValue;
   auto set = [](CUtensorMap (&to)[2], const CUtensorMap (&from)[2]) {
     to[0] = from[0];
@@ -509,36 +520,40 @@ cudaError_t iterate(const OrthArgs& a, const Layout& l, cudaStream_t stream) {
   const int terms = l.precise ? 3 : 1, side_steps = (int)((l.side + gemm::BK - 1) / gemm::BK);
   for (int k = 0; k < a.steps; ++k) {
     const int i = k & 1;
-    Maps maps;
+    gemm::TriMaps maps{};
     set(maps.a, of_x[i][TALL]);
     set(maps.b, of_x[i][TALL]);
     typename Gram::Params g{};
-    g.steps = (int)((longer + gemm::BK - 1) / gemm::BK);
-    g.loop.k_steps = terms * g.steps;
+    g.loop.part_steps = (int)((longer + gemm::BK - 1) / gemm::BK);
+    g.loop.k_steps = terms * g.loop.part_steps;
     g.side = (int)l.side;
     g.scale = kDown;
     g.out = gram;
-    if ((e = run_square<Gram>(maps, g, a.B, stream)) != cudaSuccess) return e;
-    set(maps.a, of_gram);
-    set(maps.b, of_gram);
+    if ((e = run_square<Gram>(maps, g, a.B, cov, stream)) != cudaSuccess) return e;
+    set(maps.a, of_gram[0]);
+    set(maps.b, of_gram[0]);
+    set(maps.ta, of_gram[1]);
+    set(maps.tb, of_gram[1]);
     typename Poly::Params q{};
-    q.steps = side_steps;
+    q.loop.part_steps = side_steps;
     q.loop.k_steps = terms * side_steps;
     q.side = (int)l.side;
     q.scale = a.coef[2] * kDown;
     q.b = a.coef[1];
     q.a = gram;
     q.out = poly;
-    if ((e = run_square<Poly>(maps, q, a.B, stream)) != cudaSuccess) return e;
+    if ((e = run_square<Poly>(maps, q, a.B, cov, stream)) != cudaSuccess) return e;
     if (TALL) {
       set(maps.a, of_x[i][0]);
-      set(maps.b, of_poly);
+      set(maps.b, of_poly[0]);
+      set(maps.tb, of_poly[1]);
     } else {
-      set(maps.a, of_poly);
+      set(maps.a, of_poly[0]);
+      set(maps.ta, of_poly[1]);
       set(maps.b, of_x[i][1]);
     }
     typename Apply::Params p{};
-    p.steps = side_steps;
+    p.loop.part_steps = side_steps;
     p.loop.k_steps = terms * side_steps;
     p.m = a.m;
     p.n = a.n;
@@ -551,7 +566,7 @@ cudaError_t iterate(const OrthArgs& a, const Layout& l, cudaStream_t stream) {
       p.out_matrix = a.out_matrix;
       p.out_vec = reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && (a.m == 1 || a.ldo % 8 == 0) && (a.B == 1 || a.out_matrix % 8 == 0);
     }
-    if ((e = run_apply<Apply>(maps, p, a.B, stream)) != cudaSuccess) return e;
+    if ((e = run_apply<Apply>(maps, p, a.B, cov, stream)) != cudaSuccess) return e;
   }
   return e;
 }

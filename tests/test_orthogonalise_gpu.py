@@ -54,7 +54,8 @@ def low_rank(shape, seed, dtype):
 
 
 SHAPES = [(1, 1, 1), (1, 1, 9), (1, 7, 1), (2, 3, 5), (1, 64, 64), (3, 65, 63), (1, 128, 300), (2, 300, 129), (1, 257, 1000), (1, 1000, 257), (1, 512, 512), (24, 130, 200),
-          (1, 2000, 1700), (1, 1700, 2300), (5, 640, 520), (3, 256, 256), (2, 255, 700), (2, 129, 129)]
+          (1, 2000, 1700), (1, 1700, 2300), (5, 640, 520), (3, 256, 256), (2, 255, 700), (2, 129, 129),
+          (1, 1003, 2731), (1, 2731, 1003), (1, 900, 1000), (1, 2600, 2700), (30, 300, 400), (30, 400, 300)]
 
 
 @pytest.mark.parametrize("shape", SHAPES, ids=str)
