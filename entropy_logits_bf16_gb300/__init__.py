@@ -1524,6 +1524,8 @@ def token_logprobs(logits: torch.Tensor, token_ids, temperature: float = 1.0, *,
     dt = _logits_dtype(logits)
     T, V = logits.shape
     C = _token_ids(token_ids, T)
+    if not 0 <= n_top <= MAX_ALTERNATIVES or C > MAX_TOKENS:
+        raise ValueError(f"at most {MAX_TOKENS} tokens and {MAX_ALTERNATIVES} alternatives a row")
     if state is not None:
         _token_state(state, T)
     dev = logits.device

@@ -1209,6 +1209,7 @@ rlk_status rlk_token_logprobs_bwd(const void* logits, rlk_dtype dtype, int64_t T
   if (T == 0) return RLK_OK;
   if (!logits || !state || !grad_logits || (n_tokens > 0 && !token_ids) || (n_top > 0 && (!top_ids || !grad_top)))
     return RLK_ERR_INVALID_ARG;
+  if (logits == grad_logits) return RLK_ERR_INVALID_ARG;   // the logits are read after parts of it are written
   if (!aligned_to(token_ids, 4) || !aligned_to(state, 16) || !aligned_to(grad_logprob, 4) ||
       !aligned_to(grad_entropy, 4) || !aligned_to(top_ids, 4) || !aligned_to(grad_top, 4) ||
       !elem_aligned(grad_logits, grad_dtype) || !aligned_to(out_status_word, 4))

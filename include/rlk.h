@@ -1177,7 +1177,7 @@ rlk_status rlk_token_logprobs_fwd(const void* logits, rlk_dtype dtype, int64_t T
  *  top_ids, n_top, grad_top   device int32[T][n_top] from the forward and float[T][n_top];
  *                  n_top 0 for none.
  *  grad_logits     device, grad_dtype, T x ldg elements (ldg >= V); may not overlap
- *                  the logits.
+ *                  the logits (their address itself is refused).
  *  out_status_word device uint32[1] or NULL: RLK_STATUS_BAD_TOKEN_ID, or
  *                  RLK_STATUS_BAD_PARAM for a state of another temperature.
  * A row that the forward could not score, with a token out of range, or whose

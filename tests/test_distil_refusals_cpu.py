@@ -16,7 +16,7 @@ def lib():
 
 
 FWD = dict(logits=P, dtype=0, T=2, V=100, ld=100, ids=P, n=3, temperature=1.0, top=4, lp=P, ent=P, ti=P, tl=P, state=P, status=P)
-BWD = dict(logits=P, dtype=0, T=2, V=100, ld=100, ids=P, n=3, temperature=1.0, state=P, glp=P, gh=P, ti=P, top=4, gt=P, out=P, gd=0, ldg=100, status=P)
+BWD = dict(logits=P, dtype=0, T=2, V=100, ld=100, ids=P, n=3, temperature=1.0, state=P, glp=P, gh=P, ti=P, top=4, gt=P, out=P + 4096, gd=0, ldg=100, status=P)
 SIZES = [dict(T=-1), dict(V=0), dict(V=(1 << 24) + 1, ld=1 << 25), dict(ld=99), dict(n=-1), dict(n=1025), dict(top=-1), dict(top=129), dict(temperature=0.0),
          dict(temperature=-1.0), dict(temperature=float("inf")), dict(temperature=float("nan")), dict(temperature=1e-39), dict(dtype=2), dict(logits=0), dict(logits=P + 1),
          dict(dtype=1, logits=P + 2), dict(ids=0), dict(ids=P + 2), dict(status=P + 1), dict(state=P + 8)]
@@ -28,7 +28,7 @@ def test_token_logprobs_refuses(lib, change):
     assert lib.rlk_token_logprobs_fwd(*a.values(), None) == BAD
 
 
-@pytest.mark.parametrize("change", SIZES + [dict(state=0), dict(glp=P + 2), dict(gh=P + 1), dict(ti=0), dict(ti=P + 2), dict(gt=0), dict(gt=P + 2), dict(out=0), dict(out=P + 1),
+@pytest.mark.parametrize("change", SIZES + [dict(state=0), dict(glp=P + 2), dict(gh=P + 1), dict(ti=0), dict(ti=P + 2), dict(gt=0), dict(gt=P + 2), dict(out=0), dict(out=P), dict(out=P + 1),
                                             dict(gd=1, out=P + 2), dict(gd=3), dict(ldg=99)], ids=str)
 def test_token_logprobs_backward_refuses(lib, change):
     a = {**BWD, **change}

@@ -284,7 +284,7 @@ def test_offsets_past_32_bits(cuda_lib):
 def test_waits_that_run_out(cuda_lib, stage, V):
     """Many long rows off 16-byte boundaries come through a ring of copies: a debug setting makes the first CTA wait for
     an arrival that never comes.  Its rows are NaN, the others keep their bits, the next call is clean."""
-    rlk, T = cuda_lib, 1000
+    rlk, T = cuda_lib, 500
     z = logits(T, V, BF16, 1)
     ids = given(T, V, 3, 1)
     want = rlk.token_logprobs(z, ids, 1.0, n_top=5)
@@ -315,3 +315,50 @@ def test_rows_of_one_call_through_the_ring(cuda_lib):
         for r in (0, 1, 170, 455, 456, 457, 499):
             for a, b in zip(all_, cuda_lib.token_logprobs(z[r:r + 1], ids[r:r + 1], 0.8, n_top=7)):
                 assert torch.equal(a[r:r + 1].view(torch.int32), b.view(torch.int32)), (dtype, V, r)
+
+
+@pytest.mark.parametrize("V,top", [(1, 128), (7, 20), (100, 128), (127, 128)])
+@pytest.mark.parametrize("T", [1, 30, 400])
+def test_more_alternatives_than_tokens(cuda_lib, V, top, T):
+    z = logits(T, V, BF16, V)
+    ids = given(T, V, 2, 1)
+    keep = torch.arange(0, T, max(1, T // 5))
+    got = cuda_lib.token_logprobs(z, ids, 1.0, n_top=top)
+    assert (got[2][:, V:] == -1).all() and (got[3][:, V:] == -math.inf).all() and (got[2][:, :V].sort(1)[0] == torch.arange(V, device="cuda")).all()
+    check(cuda_lib, z[keep], ids[keep], 1.0, top)
+
+
+def test_python_refusals(cuda_lib):
+    rlk = cuda_lib
+    z, ids = torch.randn(4, 50, device="cuda"), torch.zeros(4, 2, dtype=torch.int32, device="cuda")
+    state = rlk.new_token_state(4, "cuda")
+    _, _, ti, _ = rlk.token_logprobs(z, ids, 1.0, n_top=3, state=state)
+    g = torch.ones(4, 3, device="cuda")
+    for bad in (lambda: rlk.token_logprobs(z.half(), ids), lambda: rlk.token_logprobs(z.cpu(), ids), lambda: rlk.token_logprobs(z, ids.cpu()), lambda: rlk.token_logprobs(z, ids.long()),
+                lambda: rlk.token_logprobs(z, ids[:3]), lambda: rlk.token_logprobs(z, ids.t()), lambda: rlk.token_logprobs(z.t(), ids), lambda: rlk.token_logprobs(z[0], ids),
+                lambda: rlk.token_logprobs(z, ids, n_top=129), lambda: rlk.token_logprobs(z, ids, n_top=-1), lambda: rlk.token_logprobs(z, ids, state=state[:3]),
+                lambda: rlk.token_logprobs(z, torch.zeros(4, 1025, dtype=torch.int32, device="cuda")),
+                lambda: rlk.token_logprobs_backward(z, ids, 1.0, state, torch.ones(4, device="cuda")), lambda: rlk.token_logprobs_backward(z, None, 1.0, state, torch.ones(4, 2, device="cuda")),
+                lambda: rlk.token_logprobs_backward(z, ids, 1.0, state, grad_top=g), lambda: rlk.token_logprobs_backward(z, ids, 1.0, state, top_ids=ti, grad_top=g[:, :2]),
+                lambda: rlk.token_logprobs_backward(z, ids, 1.0, state, out=torch.empty(4, 49, device="cuda")),
+                lambda: rlk.token_logprobs_backward(z, ids, 1.0, state, out=torch.empty(4, 50, device="cuda"), grad_dtype=BF16),
+                lambda: rlk.token_logprobs_backward(z, ids, 1.0, state, None, torch.ones(3, device="cuda"))):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: rlk.token_logprobs(z, ids, 0.0), lambda: rlk.token_logprobs(z, ids, float("nan")), lambda: rlk.token_logprobs(z[:1].expand(4, 50), ids),
+                lambda: rlk.token_logprobs_backward(z, ids, 1.0, state, out=z)):
+        with pytest.raises(rlk.RlkError):
+            bad()
+
+
+@pytest.mark.parametrize("temp", [1e-30, 1e-4, 1e4, 1e30, 3e38])
+def test_temperatures(cuda_lib, temp):
+    z = logits(3, 3000, F32, 2)
+    got = cuda_lib.token_logprobs(z, given(3, 3000, 3, 1), temp, n_top=3)
+    x = z.double().cpu() / temp
+    lp = torch.log_softmax(x, 1)
+    h = -(lp.exp() * lp).nan_to_num(0.0).sum(1)
+    # d = (z - M) / T to three roundings of it, S to 50 e; the entropy's terms w d likewise
+    assert ((got[1].double().cpu() - h).abs() <= 2 ** -24 * (100 + 8 * h + 3000 / 512 * (1 + h))).all()
+    best = lp.max(1)[0]
+    assert torch.allclose(got[3][:, 0].double().cpu(), best, atol=2 ** -24 * 80, rtol=2 ** -21)
