@@ -285,7 +285,7 @@ def test_waits_that_run_out(cuda_lib, stage, V):
     """Many long rows off 16-byte boundaries come through a ring of copies: a debug setting makes the first CTA wait for
     an arrival that never comes.  Its rows are NaN, the others keep their bits, the next call is clean."""
     rlk, T = cuda_lib, 500
-    z = logits(T, V, BF16, 1)
+    z = logits(2, V, BF16, 1).repeat(T // 2, 1)
     ids = given(T, V, 3, 1)
     want = rlk.token_logprobs(z, ids, 1.0, n_top=5)
     word = torch.zeros(1, dtype=torch.int32, device="cuda")
