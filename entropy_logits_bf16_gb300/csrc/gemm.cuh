@@ -91,9 +91,27 @@ __device__ __forceinline__ void grouped(int t, int n_mt, int n_nt, int& mt, int&
   nt = r / gm;
 }
 
-// The first step of K whose columns lie above the diagonal's blocks for rows from `row` on (a tile
-// and a stage lie in one block each).
-__device__ __forceinline__ int mirror_from(const Loop& l, int row) { return l.tri ? (row / l.tri + 1) * (l.tri / BK) : 0x7FFFFFFF; }
+// Calls steps(A's layout, B's layout, from, to) for the runs of [k0, k1) in which neither
+// changes (true: MN-contiguous); `first`: the step of K's start.
+template <class Op, class F>
+__device__ __forceinline__ void by_layout(const Loop& l, int a_row, int b_row, int first, int k0, int k1, F& steps) {
+  using A = std::bool_constant<Op::A_MN>;
+  using B = std::bool_constant<Op::B_MN>;
+  using Mirror = std::true_type;
+  if constexpr (Op::TRI_A || Op::TRI_B) {
+    auto from = [&](int row) {
+      const int k = l.tri ? first + (row / l.tri + 1) * (l.tri / BK) : k1;   // the first step whose columns lie above the diagonal's blocks
+      return k < k0 ? k0 : (k < k1 ? k : k1);
+    };
+    const int a = Op::TRI_A ? from(a_row) : k1, b = Op::TRI_B ? from(b_row) : k1, one = a < b ? a : b, two = a < b ? b : a;
+    steps(A{}, B{}, k0, one);
+    if (Op::TRI_A && a < b) steps(Mirror{}, B{}, one, two);
+    if (Op::TRI_B && b < a) steps(A{}, Mirror{}, one, two);
+    if (Op::TRI_A && Op::TRI_B) steps(Mirror{}, Mirror{}, two, k1);
+  } else {
+    steps(A{}, B{}, k0, k1);
+  }
+}
 
 template <class Op, bool SPLIT>
 __global__ void __launch_bounds__(Shape<SPLIT>::THREADS, SPLIT ? 2 : 1)
@@ -116,7 +134,6 @@ __global__ void __launch_bounds__(Shape<SPLIT>::THREADS, SPLIT ? 2 : 1)
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * MAX_STAGES;
   const uint32_t accf0 = empty0 + 8 * MAX_STAGES, acce0 = accf0 + 16;
   const uint32_t drain_bar = smem_u32(bars + 2 * MAX_STAGES + 6);
-  constexpr uint32_t idesc = tc::idesc_16(Op::F16, Op::A_MN, Op::B_MN, TM, BN);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -159,110 +176,115 @@ __global__ void __launch_bounds__(Shape<SPLIT>::THREADS, SPLIT ? 2 : 1)
 
   if (warp == 0) {
     // ------------------------------------------------------ TMA producer
+    // One thread, whose instructions bound the products unless its loop is short (800 cycles a
+    // step of the pairs' tiles with the layouts chosen in it, 512 are the tensor cores').
     if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0, used = 0u, last_parity = 0u;   // per stage: issued at all, parity of the last issue
+      int stage = 0, issued = 0;   // issued: turns of the ring begun
+      uint32_t phase = 0;
       bool ok = true;
+      // a pair's copies all report to the even CTA, whose barrier expects them all
+      const uint32_t report = G == 2 ? tc::peer_addr(full0, 0u) : full0;
       for (int t = tile0; t < p.loop.n_tiles && ok; t += tile_step) {
         const Tile tl = Op::tile(p, t, TM, OUT);
         const int am = tl.a_row + a_off, bn = tl.b_row + (SPLIT ? 0 : (int)rank * BROWS);
-        const int a_mirror = Op::TRI_A ? mirror_from(p.loop, am) : 0, b_mirror = Op::TRI_B ? mirror_from(p.loop, bn) : 0;
-        int part = k0 / p.loop.part_steps, ks = k0 - part * p.loop.part_steps, ia = 0, ib = 0;
-        Op::source(tl, part, ia, ib);
-        for (int k = k0; k < k1; ++k) {
-          if (!tc::wait(empty0 + 8 * stage, phase ^ 1u, abort_flag, limit) || *abort_flag) {
-            ok = false;
-            break;
-          }
-          const uint32_t fb = full0 + 8 * stage;
-          const uint32_t sa = base + stage * STAGE_BYTES, sb = sa + A_BYTES;
-          // a pair's copies all report to the even CTA, whose barrier expects them all
-          if (leader) mbar_expect_tx(fb, bytes);
-          const uint32_t to = G == 2 ? tc::peer_addr(fb, 0u) : fb;
-          auto load = [&](uint32_t dst, const CUtensorMap* map, int x, int y) {
-            if constexpr (Op::STACKED) {
-              if (G == 2) tc::load_3d_pair(dst, map, to, x, y, tl.which);
-              else tc::load_3d(dst, map, to, x, y, tl.which);
-            } else {
-              if (G == 2) tc::load_2d_pair(dst, map, to, x, y);
-              else tc::load_2d(dst, map, to, x, y);
+        for (int k = k0, part = k0 / p.loop.part_steps; k < k1 && ok; ++part) {
+          const int first = part * p.loop.part_steps, last = first + p.loop.part_steps < k1 ? first + p.loop.part_steps : k1;
+          int ia = 0, ib = 0;
+          Op::source(tl, part, ia, ib);
+          const CUtensorMap *ma = &maps.a[ia], *mb = &maps.b[ib], *mta = ma, *mtb = mb;
+          if constexpr (Op::TRI_A) mta = &maps.ta[ia];
+          if constexpr (Op::TRI_B) mtb = &maps.tb[ib];
+          // steps [from, to) with these layouts
+          auto steps = [&](auto a_layout, auto b_layout, int from, int to) {
+            constexpr bool a_mn = decltype(a_layout)::value, b_mn = decltype(b_layout)::value;
+            const CUtensorMap *xa = a_mn ? mta : ma, *xb = b_mn ? mtb : mb;
+            int x = (from - first) * BK;   // the K coordinate
+#pragma unroll 1
+            for (int i = from; i < to; ++i, x += BK) {
+              if (!tc::wait(empty0 + 8 * stage, phase ^ 1u, abort_flag, limit) || ((i & 3) == 0 && *abort_flag)) {
+                ok = false;
+                return;
+              }
+              const uint32_t sa = base + stage * STAGE_BYTES, sb = sa + A_BYTES, to_bar = report + 8 * stage;
+              if (leader) mbar_expect_tx(full0 + 8 * stage, bytes);
+              auto load = [&](uint32_t dst, const CUtensorMap* map, int cx, int cy) {
+                if constexpr (Op::STACKED) {
+                  if (G == 2) tc::load_3d_pair(dst, map, to_bar, cx, cy, tl.which);
+                  else tc::load_3d(dst, map, to_bar, cx, cy, tl.which);
+                } else {
+                  if (G == 2) tc::load_2d_pair(dst, map, to_bar, cx, cy);
+                  else tc::load_2d(dst, map, to_bar, cx, cy);
+                }
+              };
+              if (a_mn) {
+#pragma unroll
+                for (int j = 0; j < BM / 64; ++j) load(sa + j * MN_BLOCK, xa, am + j * 64, x);
+              } else {
+                load(sa, xa, x, am);
+              }
+              if (Op::DUAL && SPLIT) {   // 64 rows of each
+                load(sb, &maps.b[0], x, tl.b_row);
+                load(sb + 64 * BK * 2, &maps.b[1], x, tl.b_row);
+              } else if (Op::DUAL) {     // 128 rows of one in each CTA
+                load(sb, &maps.b[rank], x, tl.b_row);
+              } else if (b_mn) {
+#pragma unroll
+                for (int j = 0; j < BROWS / 64; ++j) load(sb + j * MN_BLOCK, xb, bn + j * 64, x);
+              } else {
+                load(sb, xb, x, bn);
+              }
+              if (++stage == stages) { stage = 0; phase ^= 1u; ++issued; }
             }
           };
-          const int ak = ks * BK, bk = ak;
-          if (Op::A_MN || (Op::TRI_A && ks >= a_mirror)) {
-            const CUtensorMap* map = &maps.a[ia];
-            if constexpr (Op::TRI_A) map = &maps.ta[ia];
-#pragma unroll
-            for (int j = 0; j < BM / 64; ++j) load(sa + j * MN_BLOCK, map, am + j * 64, ak);
-          } else {
-            load(sa, &maps.a[ia], ak, am);
-          }
-          if (Op::DUAL && SPLIT) {   // 64 rows of each
-            load(sb, &maps.b[0], bk, tl.b_row);
-            load(sb + 64 * BK * 2, &maps.b[1], bk, tl.b_row);
-          } else if (Op::DUAL) {     // 128 rows of one in each CTA
-            load(sb, &maps.b[rank], bk, tl.b_row);
-          } else {
-            if (Op::B_MN || (Op::TRI_B && ks >= b_mirror)) {
-              const CUtensorMap* map = &maps.b[ib];
-              if constexpr (Op::TRI_B) map = &maps.tb[ib];
-#pragma unroll
-              for (int j = 0; j < BROWS / 64; ++j) load(sb + j * MN_BLOCK, map, bn + j * 64, bk);
-            } else {
-              load(sb, &maps.b[ib], bk, bn);
-            }
-          }
-          used |= 1u << stage;
-          last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
-          if (++stage == stages) { stage = 0; phase ^= 1u; }
-          if (++ks == p.loop.part_steps) {
-            ks = ia = ib = 0;
-            Op::source(tl, ++part, ia, ib);
-          }
+          by_layout<Op>(p.loop, am, bn, first, k, last, steps);
+          k = last;
         }
       }
       // Every copy lands before the CTAs exit (bounded), also when another role's wait runs
       // out only after the last copy was asked for.  (A pair's odd CTA may have asked for
       // stages that the even one no longer did; after that its own roles wait out the limit.)
       if (leader)
-        for (int s = 0; s < stages; ++s)
-          if (used & (1u << s)) tc::drain(full0 + 8 * s, (last_parity >> s) & 1u);
+        for (int s = 0; s < stages; ++s)   // a stage's last turn: this one, or the one before
+          if (s < stage || issued > 0) tc::drain(full0 + 8 * s, (uint32_t)(s < stage ? issued : issued - 1) & 1u);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------ MMA issuer
     if (lane == 0 && leader) {
       int stage = 0;
       uint32_t phase = 0, tile = 0;
-      const uint64_t a0_k = tc::desc_k(base), a0_mn = tc::desc_mn(base, MN_BLOCK);
-      const uint64_t b0_k = tc::desc_k(base + A_BYTES), b0_mn = tc::desc_mn(base + A_BYTES, MN_BLOCK);
       bool ok = true;
       for (int t = tile0; t < p.loop.n_tiles && ok; t += tile_step, ++tile) {
         const uint32_t acc = tile & 1u, accph = (tile >> 1) & 1u;
         if (!tc::wait<G == 2>(acce0 + 8 * acc, accph ^ 1u, abort_flag, limit)) { ok = false; break; }
         tc::fence_after();
         const uint32_t d_tmem = tmem + acc * BN;
-        int a_mirror = 0, b_mirror = 0, ks = 0;
+        // steps [from, to), with the operands' layouts known when this is compiled
+        auto steps = [&](auto a_layout, auto b_layout, int from, int to) {
+          constexpr bool a_mn = decltype(a_layout)::value, b_mn = decltype(b_layout)::value;
+          constexpr uint32_t id = tc::idesc_16(Op::F16, a_mn, b_mn, TM, BN);
+#pragma unroll 1
+          for (int k = from; k < to && ok; ++k) {
+            if (!tc::wait(full0 + 8 * stage, phase, abort_flag, limit)) { ok = false; break; }
+            tc::fence_after();
+            const uint32_t sa = base + stage * STAGE_BYTES, sb = sa + A_BYTES;
+#pragma unroll
+            for (int kk = 0; kk < BK / 16; ++kk) {
+              // 16 K elements: 32 bytes inside a K-contiguous row, 16 rows of an MN-contiguous block
+              const uint64_t da = a_mn ? tc::desc_mn(sa + kk * 2048, MN_BLOCK) : tc::desc_k(sa) + (uint64_t)(kk * 2);
+              const uint64_t db = b_mn ? tc::desc_mn(sb + kk * 2048, MN_BLOCK) : tc::desc_k(sb) + (uint64_t)(kk * 2);
+              tc::mma<G>(d_tmem, da, db, id, (k > k0 || kk > 0) ? 1u : 0u);
+            }
+            tc::commit<G>(empty0 + 8 * stage);
+            if (++stage == stages) { stage = 0; phase ^= 1u; }
+          }
+        };
+        int a_row = 0, b_row = 0;
         if constexpr (Op::TRI_A || Op::TRI_B) {
           const Tile tl = Op::tile(p, t, TM, OUT);
-          a_mirror = mirror_from(p.loop, tl.a_row);
-          b_mirror = mirror_from(p.loop, tl.b_row);
-          ks = k0 % p.loop.part_steps;
+          a_row = tl.a_row;
+          b_row = tl.b_row;
         }
-        for (int k = k0; k < k1; ++k) {
-          if (!tc::wait(full0 + 8 * stage, phase, abort_flag, limit)) { ok = false; break; }
-          tc::fence_after();
-          // 16 K elements: 32 bytes inside a K-contiguous row, 16 rows of an MN-contiguous block
-          const bool a_mn = Op::A_MN || (Op::TRI_A && ks >= a_mirror), b_mn = Op::B_MN || (Op::TRI_B && ks >= b_mirror);
-          const uint64_t at = (uint64_t)(stage * (int)(STAGE_BYTES >> 4));   // (the address fields do not overflow)
-          const uint64_t da = (a_mn ? a0_mn : a0_k) + at, db = (b_mn ? b0_mn : b0_k) + at;
-          const uint64_t a16 = a_mn ? 2048 / 16 : 2, b16 = b_mn ? 2048 / 16 : 2;
-          const uint32_t id = idesc | (uint32_t)a_mn << 15 | (uint32_t)b_mn << 16;
-#pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk) tc::mma<G>(d_tmem, da + kk * a16, db + kk * b16, id, (k > k0 || kk > 0) ? 1u : 0u);
-          if ((Op::TRI_A || Op::TRI_B) && ++ks == p.loop.part_steps) ks = 0;
-          tc::commit<G>(empty0 + 8 * stage);
-          if (++stage == stages) { stage = 0; phase ^= 1u; }
-        }
+        by_layout<Op>(p.loop, a_row, b_row, 0, k0, k1, steps);   // (mirrored operands have one part)
         if (ok) tc::commit<G>(accf0 + 8 * acc);
       }
       if (!ok) {   // every MMA already issued finishes before TMEM is freed
