@@ -4,7 +4,8 @@
 // (rows <= columns; else A = X^T X and X <- a X + X P).  Each step maps the singular values by
 // s -> a s + b s^3 + c s^5 and leaves the singular vectors.
 //
-// Three products a step on the tcgen05 kernel of gemm.cuh.  A and P are symmetric: only their
+// Up to 128 x 1024 one kernel for all steps (below).  Else three products a step on the tcgen05
+// kernel of gemm.cuh.  A and P are symmetric: only their
 // blocks of 256 x 256 (or 128 x 128) on and below the diagonal are computed and stored, and a product takes a
 // missing block as the mirror image of the one that is there, with the other index contiguous
 // (storing each twice took a third of these products' epilogues).  Nothing is transposed in
@@ -21,9 +22,9 @@
 // The rounding of A, P and X moves each singular value by up to 0.05 of it in five steps (the
 // polynomial's slope adds up: first-order sum over the steps with u = 2^-11), about 0.0015 on
 // the average of many.  Where the shorter side is kPrecise or less there may be few to average
-// over, and the call is bound by its launches: A and P are held in two fp16 as well, and each
-// product is three (values, value times rest both ways), one sum in the accumulator (64 x 64:
-// 107 us in all, 95 with one product each; at 256 x 256 163 and 137).
+// over, and the call is bound by its chain: A and P are held in two fp16 as well, and each
+// product is three (values, value times rest both ways), one sum in the accumulator (as launches,
+// 64 x 64: 107 us in all, 95 with one product each; at 256 x 256 163 and 137).
 //
 // Measured: 4096 x 14336 2.84 to 2.92 ms (1.36 PFLOP/s with halves of A and P counted; A 86 % of the tensor
 // pipe, X 61 to 70 %: operands at the 64 bytes a cycle that an SM takes from L2, and 16 bytes an element in
@@ -380,6 +381,278 @@ __global__ void __launch_bounds__(OT) orth_start_kernel(const Start a) {
   }
 }
 
+// ------------------------------------------------------------ small matrices, in one kernel
+// Up to 128 x 1024 (either way) the whole iteration stays in the shared memory of a cluster: a
+// CTA holds 128 of the longer side's columns (TALL: rows) of X, both halves of each number, and
+// all of A, then P, in the 128-byte swizzle that TMA brought X in.  The same bytes are a K-contiguous
+// operand where X's columns are summed over and an MN-contiguous one where its rows are.  A step:
+// each CTA's share of A in TMEM; the shares joined through distributed shared memory, each CTA
+// its part of A for all (in rank order: the same bits in all); A A, P and X's product locally.
+// Bound by the chain of a step's products and epilogues, about 7 us where there is one CTA, 15
+// with eight (one 64 x 64 48 us in all where 17 launches take 124, 128 x 512 76 and 154).
+constexpr int RT = 256, RES_MOST = 8;   // threads; CTAs of a cluster, 128 of the longer side each
+constexpr uint32_t RES_HALF = 128 * 128 * 2, RES_PITCH = 132;   // bytes of 128 x 128 fp16; floats of a row of shares
+constexpr size_t RES_SMEM = 4 * RES_HALF + 128 * RES_PITCH * 4 + 1024 + 64;
+
+struct Resident {
+  int64_t m, n;
+  int steps, cluster;
+  float a, b, c;
+  uint16_t* out;          // bf16
+  int64_t ldo, out_matrix;
+  int out_vec;
+  long long limit;
+  int withhold;           // debug: the first CTA's load waits for an arrival that never comes
+};
+struct Halves {
+  CUtensorMap value, rest;
+};
+
+__device__ __forceinline__ void store_peer16(uint32_t addr, uint4 v) {
+  asm volatile("st.shared::cluster.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+template <bool TALL>
+__global__ void __launch_bounds__(RT, 1) orth_resident_kernel(const __grid_constant__ Halves maps, const Resident p) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+  uint8_t* mem = smem_raw + (base - raw);
+  constexpr uint32_t XH = 0, XL = RES_HALF, AH = 2 * RES_HALF, AL = 3 * RES_HALF, F = 4 * RES_HALF;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(mem + F + 128 * RES_PITCH * 4);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 3);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 4);
+  const uint32_t loaded = smem_u32(bars), done = loaded + 8, drain_bar = loaded + 16;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, C = p.cluster;
+  const int rank = (int)tc::cluster_rank(), matrix = (int)(blockIdx.x / (unsigned)C);
+  const int row = (warp & 3) * 32 + lane, half = warp >> 2;   // this thread's row of a 128 x 128 tile, and 64 of its columns
+  if (threadIdx.x == 0) {
+    mbar_init(loaded, 1 + (p.withhold >= 0 && blockIdx.x == 0));
+    mbar_init(done, 1);
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    fence_proxy_async_smem();
+    tc::prefetch_map(&maps.value);
+    tc::prefetch_map(&maps.rest);
+  }
+  if (warp == 0) tc::alloc<1>(smem_u32(tmem_slot), 128);
+  tc::fence_before();
+  __syncthreads();
+  pdl_trigger();   // the next kernel's CTAs may come: this one has its TMEM
+  pdl_wait();
+  tc::fence_after();
+  const uint32_t tmem = *tmem_slot;
+  if (threadIdx.x == 0) {
+    mbar_expect_tx(loaded, 2 * RES_HALF);
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {   // 64 columns a block of 128 rows
+      const int x = TALL ? b * 64 : rank * 128 + b * 64, y = TALL ? rank * 128 : 0;
+      tc::load_3d(base + XH + b * (RES_HALF / 2), &maps.value, loaded, x, y, matrix);
+      tc::load_3d(base + XL + b * (RES_HALF / 2), &maps.rest, loaded, x, y, matrix);
+    }
+  }
+  bool ok = tc::wait(loaded, 0u, abort_flag, p.limit);
+  uint32_t phase = 0u;
+
+  // where 8 numbers of a row lie (unit: 8 columns)
+  auto at = [](int r, int unit) { return (uint32_t)((unit >> 3) * (int)(RES_HALF / 2) + r * 128 + (((unit & 7) ^ (r & 7)) << 4)); };
+  // D = A B^T of three terms, K 128; then every thread waits for it
+  auto product = [&](auto a_layout, auto b_layout, uint32_t a_value, uint32_t a_rest, uint32_t b_value, uint32_t b_rest) {
+    constexpr bool a_mn = decltype(a_layout)::value, b_mn = decltype(b_layout)::value;
+    constexpr uint32_t id = tc::idesc_16(true, a_mn, b_mn, 128, 128);
+    if (threadIdx.x == 0 && !*abort_flag) {
+      fence_proxy_async();
+      tc::fence_after();
+#pragma unroll 1
+      for (int term = 0; term < 3; ++term) {
+        const uint32_t a = base + (term == 2 ? a_rest : a_value), b = base + (term == 1 ? b_rest : b_value);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {   // 16 of K: 32 bytes of a K-contiguous row, 16 rows of MN-contiguous blocks
+          const uint64_t da = a_mn ? tc::desc_mn(a + i * 2048, RES_HALF / 2) : tc::desc_k(a + (i >> 2) * (RES_HALF / 2)) + (uint64_t)((i & 3) * 2);
+          const uint64_t db = b_mn ? tc::desc_mn(b + i * 2048, RES_HALF / 2) : tc::desc_k(b + (i >> 2) * (RES_HALF / 2)) + (uint64_t)((i & 3) * 2);
+          tc::mma<1>(tmem, da, db, id, (term > 0 || i > 0) ? 1u : 0u);
+        }
+      }
+      tc::commit<1>(done);
+    }
+    ok = ok && tc::wait(done, phase, abort_flag, p.limit);
+    phase ^= 1u;
+    tc::fence_after();
+  };
+  float v[2][32];
+  auto read = [&] {   // this thread's 64 numbers of D
+    const uint32_t from = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * 64;
+    const bool good = __all_sync(0xFFFFFFFFu, ok);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (good) {
+        tc::ld32(from + h * 32, v[h]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[h][j] = NAN;
+      }
+    }
+    tc::fence_before();
+  };
+  auto eight = [&](int j, float f, float2 (&o)[4]) {   // group j of the 64, times f
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = mul2(make_float2(v[j >> 2][(j & 3) * 8 + 2 * i], v[j >> 2][(j & 3) * 8 + 2 * i + 1]), both(f));
+  };
+  auto add_kept = [&](uint32_t value, uint32_t rest, uint32_t off, float f, float2 (&o)[4]) {
+    float2 x[4];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      halves(*reinterpret_cast<const uint4*>(mem + (k ? rest : value) + off), x);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = fma2(x[i], both(f), o[i]);
+    }
+  };
+  auto split = [&](const float2 (&o)[4], uint4& value, uint4& rest) {
+    float2 x[4];
+    value = to_halves(o);
+    halves(value, x);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = fma2(x[i], both(-1.f), o[i]);
+    rest = to_halves(x);
+  };
+  auto keep = [&](uint32_t value, uint32_t rest, uint32_t off, const float2 (&o)[4]) {
+    uint4 h, l;
+    split(o, h, l);
+    *reinterpret_cast<uint4*>(mem + value + off) = h;
+    *reinterpret_cast<uint4*>(mem + rest + off) = l;
+  };
+  using K = std::false_type;    // K-contiguous
+  using MN = std::true_type;    // MN-contiguous
+
+  for (int step = 0; step < p.steps; ++step) {
+    // A = X X^T (TALL: X^T X)
+    product(std::bool_constant<TALL>{}, std::bool_constant<TALL>{}, XH, XL, XH, XL);
+    read();
+    if (C == 1) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float2 o[4];
+        eight(j, kDown, o);
+        keep(AH, AL, at(row, half * 8 + j), o);
+      }
+      fence_proxy_async();
+      __syncthreads();
+    } else {
+      float4* share = reinterpret_cast<float4*>(mem + F + (row * RES_PITCH + half * 64) * 4);
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        share[j] = make_float4(v[j >> 3][(j & 7) * 4], v[j >> 3][(j & 7) * 4 + 1], v[j >> 3][(j & 7) * 4 + 2], v[j >> 3][(j & 7) * 4 + 3]);
+      tc::cluster_sync();   // all shares are there, and every CTA is through with P
+      const int first = 2048 * rank / C, last = 2048 * (rank + 1) / C;   // groups of 8: 16 a row
+      for (int i = first + (int)threadIdx.x; i < last; i += RT) {
+        const int r = i >> 4, u = i & 15;
+        const uint32_t from = base + F + (uint32_t)(r * (int)RES_PITCH + u * 8) * 4u;
+        float4 q[2 * RES_MOST];   // all in flight together
+#pragma unroll
+        for (int k = 0; k < RES_MOST; ++k)
+          if (k < C) {
+            const uint32_t peer = tc::peer_addr(from, (uint32_t)k);
+            q[2 * k] = tc::ld_peer4(peer);
+            q[2 * k + 1] = tc::ld_peer4(peer + 16u);
+          }
+        float2 o[4] = {both(0.f), both(0.f), both(0.f), both(0.f)};
+#pragma unroll
+        for (int k = 0; k < RES_MOST; ++k)
+          if (k < C) {
+            o[0] = add2(o[0], make_float2(q[2 * k].x, q[2 * k].y));
+            o[1] = add2(o[1], make_float2(q[2 * k].z, q[2 * k].w));
+            o[2] = add2(o[2], make_float2(q[2 * k + 1].x, q[2 * k + 1].y));
+            o[3] = add2(o[3], make_float2(q[2 * k + 1].z, q[2 * k + 1].w));
+          }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[k] = mul2(o[k], both(kDown));
+        uint4 h, l;
+        split(o, h, l);
+        const uint32_t to = at(r, u);
+#pragma unroll
+        for (int k = 0; k < RES_MOST; ++k)
+          if (k < C) {
+            store_peer16(tc::peer_addr(base + AH + to, (uint32_t)k), h);
+            store_peer16(tc::peer_addr(base + AL + to, (uint32_t)k), l);
+          }
+      }
+      fence_proxy_async();
+      __syncwarp();
+      tc::cluster_sync();   // A is whole in every CTA
+    }
+    // P = b A + c A A, in A's place
+    product(K{}, K{}, AH, AL, AH, AL);
+    read();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float2 o[4];
+      const uint32_t off = at(row, half * 8 + j);
+      eight(j, p.c * kDown, o);
+      add_kept(AH, AL, off, p.b, o);
+      keep(AH, AL, off, o);
+    }
+    fence_proxy_async();
+    __syncthreads();
+    // X <- a X + P X (TALL: a X + X P)
+    if constexpr (TALL) product(K{}, K{}, XH, XL, AH, AL);
+    else product(K{}, MN{}, AH, AL, XH, XL);
+    read();
+    if (step == p.steps - 1) break;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float2 o[4];
+      const uint32_t off = at(row, half * 8 + j);
+      eight(j, kDown, o);
+      add_kept(XH, XL, off, p.a, o);
+      keep(XH, XL, off, o);
+    }
+    fence_proxy_async();
+    __syncthreads();
+  }
+  // a wait that ran out in one CTA spoils the matrix
+  __syncthreads();
+  tc::cluster_sync();
+  bool dead = false;
+  for (int k = 0; k < C; ++k) dead = tc::ld_peer_u32(tc::peer_addr(smem_u32(bars + 3), (uint32_t)k)) != 0u || dead;
+  const int64_t r0 = TALL ? rank * 128 + row : row, c0 = (TALL ? 0 : rank * 128) + half * 64;
+  if (r0 < p.m) {
+    uint16_t* to = p.out + matrix * p.out_matrix + r0 * p.ldo + c0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int n = (int)(p.n - c0 - j * 8 < 8 ? p.n - c0 - j * 8 : 8);
+      if (n <= 0) continue;
+      float2 o[4];
+      eight(j, kDown, o);
+      add_kept(XH, XL, at(row, half * 8 + j), p.a, o);
+      float w[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        w[2 * i] = dead ? NAN : __fmul_rn(o[i].x, kDown);
+        w[2 * i + 1] = dead ? NAN : __fmul_rn(o[i].y, kDown);
+      }
+      if (p.out_vec) {
+        store8(to + j * 8, w, n);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i < n) to[j * 8 + i] = (uint16_t)pack_bf16(w[i], 0.f);
+      }
+    }
+  }
+  if (threadIdx.x == 0 && *abort_flag) {   // what was asked for has landed, and been multiplied, before the CTA exits
+    if (p.withhold >= 0 && blockIdx.x == 0) mbar_arrive(loaded);
+    tc::drain(loaded, 0u);
+    tc::commit<1>(drain_bar);
+    tc::drain(drain_bar, 0u);
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::cluster_leave();   // no CTA leaves while its shared memory is read
+  tc::fence_after();
+  if (warp == 0) tc::dealloc<1>(tmem, 128);
+}
+
 // ------------------------------------------------------------ host side
 struct Layout {
   int64_t side, x_ld, p_ld;
@@ -402,6 +675,11 @@ Layout layout(int64_t B, int64_t m, int64_t n) {
   l.p = pad256((size_t)B * l.side * l.p_ld * 2);
   l.sums = pad256((size_t)B * l.parts * sizeof(Squares));
   return l;
+}
+
+// Whether the rows of the caller's result start on 16-byte boundaries.
+bool out_vec(const OrthArgs& a) {
+  return reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && (a.m == 1 || a.ldo % 8 == 0) && (a.B == 1 || a.out_matrix % 8 == 0);
 }
 
 // Maps of a stack of [rows][cols] matrices: boxes of 64 columns and `box` rows.
@@ -464,6 +742,61 @@ cudaError_t run_apply(const gemm::MapsOf<Op>& maps, typename Op::Params& p, int6
   return c.x_few ? gemm::launch<Op, true>(maps, p, stream) : gemm::launch<Op, false>(maps, p, stream);
 }
 
+// The CTAs of a matrix's cluster, or 0 where the products are launches of their own.  A cluster
+// waits on its own chain, so many matrices of several CTAs each fill the SMs less well than
+// products of the whole stack (us, this and launches: 128 x 256 68 of them 80 and 184, 760 602
+// and 853; 64 x 512 68 156 and 170, 103 221 and 219; 128 x 768 46 181 and 248, 91 336 and 323;
+// 128 x 1024 one 90 and 164, 17 178 and 195, 34 263 and 220).
+int resident_cluster(int64_t B, int64_t side, int64_t longer) {
+  const int64_t c = (longer + 127) / 128;
+  if (side > 128 || c > RES_MOST) return 0;
+  return c <= 2 || B * c <= (c <= 6 ? 2 : 1) * (int64_t)sm_count() ? (int)c : 0;
+}
+
+template <bool TALL>
+cudaError_t launch_resident(const OrthArgs& a, const Buffer& x, int cluster, cudaStream_t stream) {
+  static std::atomic<int> done[64];
+  const int ds = device_slot();
+  if (ds < 0 || !done[ds].load()) {
+    const cudaError_t e = cudaFuncSetAttribute(orth_resident_kernel<TALL>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)RES_SMEM);
+    if (e != cudaSuccess) return e;
+    if (ds >= 0) done[ds].store(1);
+  }
+  Halves maps;
+  if (!stack_map(&maps.value, x.value, x, a.B, a.m, a.n, 128) || !stack_map(&maps.rest, x.rest, x, a.B, a.m, a.n, 128))
+    return cudaErrorInvalidValue;
+  Resident p{};
+  p.m = a.m;
+  p.n = a.n;
+  p.steps = a.steps;
+  p.cluster = cluster;
+  p.a = a.coef[0];
+  p.b = a.coef[1];
+  p.c = a.coef[2];
+  p.out = static_cast<uint16_t*>(a.out);
+  p.ldo = a.ldo;
+  p.out_matrix = a.out_matrix;
+  p.out_vec = out_vec(a);
+  p.limit = debug_wait_limit();
+  p.withhold = (int)debug_take_withheld();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(a.B * cluster));
+  cfg.blockDim = dim3(RT);
+  cfg.dynamicSmemBytes = RES_SMEM;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)cluster;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, orth_resident_kernel<TALL>, maps, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 template <bool TALL>
 cudaError_t iterate(const OrthArgs& a, const Layout& l, cudaStream_t stream) {
   char* ws = static_cast<char*>(a.workspace);
@@ -499,6 +832,9 @@ cudaError_t iterate(const OrthArgs& a, const Layout& l, cudaStream_t stream) {
   e = launch_after(a.dtype == 0 ? orth_start_kernel<0> : orth_start_kernel<1>, dim3((unsigned)grid, (unsigned)a.B), dim3(OT), 0, stream, s);
   if (e != cudaSuccess) return e;
 
+  const int64_t longer = a.m < a.n ? a.n : a.m;
+  if (const int cluster = resident_cluster(a.B, l.side, longer)) return launch_resident<TALL>(a, x[0], cluster, stream);
+
   using Gram = SquareOp<TALL, false>;
   using Poly = SquareOp<false, true>;
   using Apply = ApplyOp<TALL>;
@@ -521,7 +857,6 @@ cudaError_t iterate(const OrthArgs& a, const Layout& l, cudaStream_t stream) {
     to[0] = from[0];
     to[1] = from[1];
   };
-  const int64_t longer = a.m < a.n ? a.n : a.m;
   const int terms = l.precise ? 3 : 1, side_steps = (int)((l.side + gemm::BK - 1) / gemm::BK);
   for (int k = 0; k < a.steps; ++k) {
     const int i = k & 1;
@@ -569,7 +904,7 @@ cudaError_t iterate(const OrthArgs& a, const Layout& l, cudaStream_t stream) {
       p.out = static_cast<uint16_t*>(a.out);
       p.ldo = a.ldo;
       p.out_matrix = a.out_matrix;
-      p.out_vec = reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && (a.m == 1 || a.ldo % 8 == 0) && (a.B == 1 || a.out_matrix % 8 == 0);
+      p.out_vec = out_vec(a);
     }
     if ((e = run_apply<Apply>(maps, p, a.B, cov, stream)) != cudaSuccess) return e;
   }

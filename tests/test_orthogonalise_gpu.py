@@ -198,3 +198,74 @@ def test_waits_that_run_out(cuda_lib, shape):
     assert torch.isnan(got).any()
     for _ in range(3):
         assert torch.equal(rlk.orthogonalise(g), want)
+
+
+# up to 128 x 1024 and its transpose, one kernel: one to eight CTAs, 128 of the longer side each
+SMALL = [(1, 128, 128), (1, 128, 1024), (1, 1024, 128), (2, 5, 1000), (2, 1000, 5), (40, 100, 260), (40, 260, 100), (1, 90, 897), (1, 897, 90),
+         (3, 640, 17), (3, 17, 640), (1, 385, 128), (1, 128, 511), (200, 65, 70), (1, 1, 1024), (1, 1024, 1), (1, 128, 1025), (1, 1025, 128), (1, 129, 130)]
+
+
+@pytest.mark.parametrize("shape", SMALL, ids=str)
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("make", [lambda s, k, t: randn(s, k, t), low_rank], ids=["noise", "low_rank"])
+def test_small_shapes(cuda_lib, shape, dtype, make):
+    g = make(shape, 4, dtype)
+    got = cuda_lib.orthogonalise(g)
+    check(got, orth64(g))
+    assert torch.equal(cuda_lib.orthogonalise(g), got)
+    assert torch.equal(cuda_lib.orthogonalise(g[-1]), got[-1])
+
+
+@pytest.mark.parametrize("shape", [(3, 128, 1000), (3, 1000, 128), (150, 30, 500), (150, 500, 30)])
+@pytest.mark.parametrize("steps", [1, 2, 8])
+def test_small_in_place_strided_and_captured(cuda_lib, shape, steps):
+    rlk = cuda_lib
+    B, m, n = shape
+    for lead in (0, 3):
+        room = torch.full((B, m + 2, n + 11), 7.0, dtype=BF, device="cuda")
+        g = room[:, 1:m + 1, lead:lead + n]
+        g.copy_(randn(shape, 5))
+        want = rlk.orthogonalise(g.contiguous(), steps=steps)
+        check(want, orth64(g, steps))
+        kept = g.clone()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            rlk.orthogonalise(g, steps=steps, out=g)
+        for _ in range(2):
+            g.copy_(kept)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(g, want)
+        seen = torch.zeros_like(room, dtype=torch.bool)
+        seen[:, 1:m + 1, lead:lead + n] = True
+        assert (room[~seen] == 7).all()
+
+
+@pytest.mark.parametrize("shape", [(4, 100, 1000), (4, 1000, 100), (170, 128, 128)])
+def test_a_bad_small_matrix_leaves_the_others(cuda_lib, shape):
+    g = randn(shape, 1)
+    want = cuda_lib.orthogonalise(g)
+    g[1, -1, -1] = float("nan")
+    got = cuda_lib.orthogonalise(g)
+    rest = torch.arange(shape[0]) != 1
+    assert torch.isnan(got[1]).all() and torch.equal(got[rest], want[rest])
+
+
+@pytest.mark.parametrize("shape", [(1, 100, 100), (3, 120, 1024), (3, 1024, 120), (170, 60, 250)])
+def test_small_waits_that_run_out(cuda_lib, shape):
+    """The first matrix is NaN, whichever of its CTAs gave up; the others and the next call are right."""
+    rlk = cuda_lib
+    g = randn(shape, 1)
+    want = rlk.orthogonalise(g)
+    torch.cuda.synchronize()
+    rlk.set_wait_limit(2_000_000)   # about a millisecond
+    try:
+        rlk.withhold_copy(0)
+        got = rlk.orthogonalise(g)
+        torch.cuda.synchronize()
+    finally:
+        rlk.withhold_copy(-1)
+        rlk.set_wait_limit(0)
+    assert torch.isnan(got[0]).all() and torch.equal(got[1:], want[1:])
+    for _ in range(3):
+        assert torch.equal(rlk.orthogonalise(g), want)
