@@ -257,8 +257,8 @@ __device__ __forceinline__ void load8(const void* g, int64_t at, int n, bool vec
 }
 
 // Sums of squares in three ranges, so that none over- or underflows: of numbers of 2^40 and
-// more (times 2^-96), of less than 2^-40 (times 2^96), of the others; a group of 8 goes by its
-// largest.
+// more (times 2^-96), of less than 2^-40 (times 2^80: the sum of 2^32 squares stays under 2^112,
+// and the least number's square is 2^-138), of the others; a group of 8 goes by its largest.
 struct Squares {
   float small, mid, big;
 };
@@ -267,7 +267,7 @@ __device__ __forceinline__ void add_squares(Squares& s, const float (&v)[8]) {
   float top = 0.f;
 #pragma unroll
   for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(v[j]));
-  const float f = top >= kBig ? 0x1p-96f : (top < kSmall ? 0x1p96f : 1.f);
+  const float f = top >= kBig ? 0x1p-96f : (top < kSmall ? 0x1p80f : 1.f);
   float sum = 0.f;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(OT) orth_start_kernel(const Start a) {
 #pragma unroll
       for (int k = 0; k < 3; ++k) s[k] += __shfl_xor_sync(0xFFFFFFFFu, s[k], o);
     if (threadIdx.x == 0) {
-      const double norm = sqrt(s[0] * 0x1p-192 + s[1] + s[2] * 0x1p192) + (double)a.eps;
+      const double norm = sqrt(s[0] * 0x1p-160 + s[1] + s[2] * 0x1p192) + (double)a.eps;
       if (!(norm < 1e300)) {
         s_f[0] = NAN;
         s_f[1] = s_f[2] = 1.f;

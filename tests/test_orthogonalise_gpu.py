@@ -269,3 +269,18 @@ def test_small_waits_that_run_out(cuda_lib, shape):
     assert torch.isnan(got[0]).all() and torch.equal(got[1:], want[1:])
     for _ in range(3):
         assert torch.equal(rlk.orthogonalise(g), want)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("exponent", [-41, 39, 126, -120])
+def test_many_numbers_of_one_size(cuda_lib, dtype, exponent):
+    """2^26 numbers on one side of a range's border: their sums of squares stay in fp32, and a power of two changes nothing."""
+    g = torch.where(randn((65536, 1024), 1, dtype) > 0, 1.875, -1.875).to(dtype)
+    assert torch.equal(cuda_lib.orthogonalise(g * 2.0 ** exponent, eps=0.0), cuda_lib.orthogonalise(g, eps=0.0))
+
+
+def test_least_numbers(cuda_lib):
+    """Below 2^-126: a power of two's multiples of the least fp32 number are exact, and so are their squares' sums."""
+    q = torch.randint(-8, 9, (64, 96), generator=torch.Generator().manual_seed(1)).float().cuda()
+    q[0, 0] = 8.0
+    check(cuda_lib.orthogonalise(q * 2.0 ** -149, eps=0.0), orth64(q, eps=0.0))
