@@ -333,34 +333,48 @@ __global__ void __launch_bounds__(OT) orth_start_kernel(const Start a) {
   __shared__ float s_f[3];
   const int b = blockIdx.y;
   if (threadIdx.x < 32) {
-    double s[3] = {0.0, 0.0, 0.0};
+    float s[3] = {0.f, 0.f, 0.f};
     Squares q[kNormParts / 32];   // all in flight together
 #pragma unroll
     for (int k = 0; k < kNormParts / 32; ++k)
       q[k] = (int)threadIdx.x + 32 * k < a.parts ? a.sums[b * a.parts + threadIdx.x + 32 * k] : Squares{0.f, 0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < kNormParts / 32; ++k) {
-      s[0] += (double)q[k].small;
-      s[1] += (double)q[k].mid;
-      s[2] += (double)q[k].big;
+      s[0] = __fadd_rn(s[0], q[k].small);
+      s[1] = __fadd_rn(s[1], q[k].mid);
+      s[2] = __fadd_rn(s[2], q[k].big);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
-      for (int k = 0; k < 3; ++k) s[k] += __shfl_xor_sync(0xFFFFFFFFu, s[k], o);
+      for (int k = 0; k < 3; ++k) s[k] = __fadd_rn(s[k], __shfl_xor_sync(0xFFFFFFFFu, s[k], o));
     if (threadIdx.x == 0) {
-      const double norm = sqrt(s[0] * 0x1p-160 + s[1] + s[2] * 0x1p192) + (double)a.eps;
-      if (!(norm < 1e300)) {
+      // the norm plus eps as n 2^e, in fp32 (in fp64, which runs at 1/64 of its rate here, this kernel took 8 us)
+      float n;
+      int e;
+      if (s[2] > 0.f) {          // n from 2^-56 to 2^48
+        e = 96;
+        n = __fadd_rn(sqrtf(__fadd_rn(s[2], __fmul_rn(__fmul_rn(s[1], 0x1p-96f), 0x1p-96f))), __fmul_rn(a.eps, 0x1p-96f));
+      } else if (s[1] > 0.f || a.eps >= kSmall) {
+        e = 0;
+        n = __fadd_rn(sqrtf(__fadd_rn(s[1], __fmul_rn(__fmul_rn(s[0], 0x1p-80f), 0x1p-80f))), a.eps);
+      } else {                   // up to 2^56
+        e = -80;
+        n = __fadd_rn(sqrtf(s[0]), __fmul_rn(a.eps, 0x1p80f));
+      }
+      const bool finite = isfinite(s[0]) && isfinite(s[1]) && isfinite(s[2]) && isfinite(n);
+      if (!finite) {
         s_f[0] = NAN;
         s_f[1] = s_f[2] = 1.f;
         if (a.status && blockIdx.x == 0) atomicOr(a.status, RLK_STATUS_NONFINITE);
-      } else if (norm == 0.0) {   // eps is 0 and so is G
+      } else if (n == 0.f) {   // eps is 0 and so is G
         s_f[0] = 0.f;
         s_f[1] = s_f[2] = 1.f;
       } else {
-        int e;
-        s_f[0] = (float)(1.0 / frexp(norm, &e));   // in (1, 2]
-        s_f[1] = ldexpf(1.f, -(e / 2) + 5);          // and times 2^10
+        int of_n;
+        s_f[0] = __frcp_rn(frexpf(n, &of_n));   // in (1, 2]
+        e += of_n;
+        s_f[1] = ldexpf(1.f, -(e / 2) + 5);     // and times 2^10
         s_f[2] = ldexpf(1.f, -(e - e / 2) + 5);
       }
     }
