@@ -28,7 +28,7 @@
 //
 // Measured: 4096 x 14336 2.84 to 2.92 ms (1.36 PFLOP/s with halves of A and P counted; A 86 % of the tensor
 // pipe, X 61 to 70 %: operands at the 64 bytes a cycle that an SM takes from L2, and 16 bytes an element in
-// its epilogue), 4096 x 4096 1.0 ms, 24 x 512 x 1024 320 to 338 us, 2731 x 1003 243 us, 256 x 256 130 us: the
+// its epilogue), 4096 x 4096 1.0 ms, 24 x 512 x 1024 320 to 338 us, 2731 x 1003 237 us, 256 x 256 126 us: the
 // last three by what a launch costs besides its products (8 to 15 us each, 17 launches).
 #include <cuda_fp16.h>
 #include <math.h>
@@ -402,8 +402,9 @@ __global__ void __launch_bounds__(OT) orth_start_kernel(const Start a) {
 // operand where X's columns are summed over and an MN-contiguous one where its rows are.  A step:
 // each CTA's share of A in TMEM; the shares joined through distributed shared memory, each CTA
 // its part of A for all (in rank order: the same bits in all); A A, P and X's product locally.
-// Bound by the chain of a step's products and epilogues, about 7 us where there is one CTA, 15
-// with eight (one 64 x 64 48 us in all where 17 launches take 124, 128 x 512 76 and 154).
+// Bound by the chain of a step's products and epilogues, about 6 us where there is one CTA, 14
+// with eight (one 64 x 64 45 us in all where 17 launches take 122, 128 x 512 72 and 152): a
+// chain of latencies, the tensor pipe 34 % busy and the issue slots 23 % (twice the threads change nothing).
 constexpr int RT = 256, RES_MOST = 8;   // threads; CTAs of a cluster, 128 of the longer side each
 constexpr uint32_t RES_HALF = 128 * 128 * 2, RES_PITCH = 132;   // bytes of 128 x 128 fp16; floats of a row of shares
 constexpr size_t RES_SMEM = 4 * RES_HALF + 128 * RES_PITCH * 4 + 1024 + 64;
@@ -760,7 +761,7 @@ cudaError_t run_apply(const gemm::MapsOf<Op>& maps, typename Op::Params& p, int6
 // waits on its own chain, so many matrices of several CTAs each fill the SMs less well than
 // products of the whole stack (us, this and launches: 128 x 256 68 of them 80 and 184, 760 602
 // and 853; 64 x 512 68 156 and 170, 103 221 and 219; 128 x 768 46 181 and 248, 91 336 and 323;
-// 128 x 1024 one 90 and 164, 17 178 and 195, 34 263 and 220).
+// 128 x 1024 one 90 and 164, 17 178 and 195, 34 263 and 220; both with a start that took 4 to 10 us more).
 int resident_cluster(int64_t B, int64_t side, int64_t longer) {
   const int64_t c = (longer + 127) / 128;
   if (side > 128 || c > RES_MOST) return 0;

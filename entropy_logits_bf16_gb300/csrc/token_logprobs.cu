@@ -9,7 +9,7 @@
 //
 // Forward: one read of the row.  A row is cut into groups of 16 bytes by index, 32 groups a
 // chunk; chunk c belongs to virtual warp c mod 32, whose lanes keep a running reference, S and
-// sum w d each and are joined in a fixed order.  A row is worked on by a cluster of 1 to 8 CTAs
+// sum w d each and are joined in a fixed order.  A row is worked on by a cluster of 1, 2 or 4 CTAs
 // (few rows: more of them, so that every SM reads), which only changes which CTA holds which
 // virtual warps, so a row's bits do not depend on the batch.  Rows that start off 16-byte
 // boundaries are read as aligned words and shifted, into the same groups.

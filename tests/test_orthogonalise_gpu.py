@@ -202,7 +202,8 @@ def test_waits_that_run_out(cuda_lib, shape):
 
 # up to 128 x 1024 and its transpose, one kernel: one to eight CTAs, 128 of the longer side each
 SMALL = [(1, 128, 128), (1, 128, 1024), (1, 1024, 128), (2, 5, 1000), (2, 1000, 5), (40, 100, 260), (40, 260, 100), (1, 90, 897), (1, 897, 90),
-         (3, 640, 17), (3, 17, 640), (1, 385, 128), (1, 128, 511), (200, 65, 70), (1, 1, 1024), (1, 1024, 1), (1, 128, 1025), (1, 1025, 128), (1, 129, 130)]
+         (3, 640, 17), (3, 17, 640), (1, 385, 128), (1, 128, 511), (200, 65, 70), (1, 1, 1024), (1, 1024, 1), (1, 128, 1025), (1, 1025, 128), (1, 129, 130),
+         (2, 100, 800), (2, 800, 100), (2, 33, 700), (2, 700, 33)]
 
 
 @pytest.mark.parametrize("shape", SMALL, ids=str)
