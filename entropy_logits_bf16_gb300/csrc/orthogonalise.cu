@@ -403,8 +403,9 @@ __global__ void __launch_bounds__(OT) orth_start_kernel(const Start a) {
 // each CTA's share of A in TMEM; the shares joined through distributed shared memory, each CTA
 // its part of A for all (in rank order: the same bits in all); A A, P and X's product locally.
 // Bound by the chain of a step's products and epilogues, about 6 us where there is one CTA, 14
-// with eight (one 64 x 64 45 us in all where 17 launches take 122, 128 x 512 72 and 152): a
-// chain of latencies, the tensor pipe 34 % busy and the issue slots 23 % (twice the threads change nothing).
+// with eight (one 64 x 64 42 us in all where 17 launches take 122, 128 x 512 69 and 152): a
+// chain of latencies, the tensor pipe 34 % busy and the issue slots 23 % (twice the threads change nothing;
+// fences of all memory instead of this CTA's shared memory cost 3 us).
 constexpr int RT = 256, RES_MOST = 8;   // threads; CTAs of a cluster, 128 of the longer side each
 constexpr uint32_t RES_HALF = 128 * 128 * 2, RES_PITCH = 132;   // bytes of 128 x 128 fp16; floats of a row of shares
 constexpr size_t RES_SMEM = 4 * RES_HALF + 128 * RES_PITCH * 4 + 1024 + 64;
@@ -477,7 +478,7 @@ __global__ void __launch_bounds__(RT, 1) orth_resident_kernel(const __grid_const
     constexpr bool a_mn = decltype(a_layout)::value, b_mn = decltype(b_layout)::value;
     constexpr uint32_t id = tc::idesc_16(true, a_mn, b_mn, 128, 128);
     if (threadIdx.x == 0 && !*abort_flag) {
-      fence_proxy_async();
+      fence_proxy_async_smem();
       tc::fence_after();
 #pragma unroll 1
       for (int term = 0; term < 3; ++term) {
@@ -551,7 +552,7 @@ __global__ void __launch_bounds__(RT, 1) orth_resident_kernel(const __grid_const
         eight(j, kDown, o);
         keep(AH, AL, at(row, half * 8 + j), o);
       }
-      fence_proxy_async();
+      fence_proxy_async_smem();
       __syncthreads();
     } else {
       float4* share = reinterpret_cast<float4*>(mem + F + (row * RES_PITCH + half * 64) * 4);
@@ -607,7 +608,7 @@ __global__ void __launch_bounds__(RT, 1) orth_resident_kernel(const __grid_const
       add_kept(AH, AL, off, p.b, o);
       keep(AH, AL, off, o);
     }
-    fence_proxy_async();
+    fence_proxy_async_smem();
     __syncthreads();
     // X <- a X + P X (TALL: a X + X P)
     if constexpr (TALL) product(K{}, K{}, XH, XL, AH, AL);
@@ -622,7 +623,7 @@ __global__ void __launch_bounds__(RT, 1) orth_resident_kernel(const __grid_const
       add_kept(XH, XL, off, p.a, o);
       keep(XH, XL, off, o);
     }
-    fence_proxy_async();
+    fence_proxy_async_smem();
     __syncthreads();
   }
   // a wait that ran out in one CTA spoils the matrix
