@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(OT) orth_start_kernel(const Start a) {
 // its part of A for all (in rank order: the same bits in all); A A, P and X's product locally.
 // Bound by the chain of a step's products and epilogues, about 6 us where there is one CTA, 14
 // with eight (one 64 x 64 42 us in all where 17 launches take 122, 128 x 512 69 and 152): a
-// chain of latencies, the tensor pipe 34 % busy and the issue slots 23 % (twice the threads change nothing;
+// chain of latencies, the tensor pipe 37 % busy and the issue slots 25 % (twice the threads change nothing;
 // fences of all memory instead of this CTA's shared memory cost 3 us).
 constexpr int RT = 256, RES_MOST = 8;   // threads; CTAs of a cluster, 128 of the longer side each
 constexpr uint32_t RES_HALF = 128 * 128 * 2, RES_PITCH = 132;   // bytes of 128 x 128 fp16; floats of a row of shares
