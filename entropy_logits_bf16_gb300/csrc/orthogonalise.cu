@@ -14,8 +14,10 @@
 //
 // Numbers.  The products' operands are fp16 (11 bits where bf16 has 8, at the same rate), held
 // times 2^10: the iterates' entries lie between about 1 / (longer side) and 1.2, so that a matrix
-// of up to 2^14 on a side keeps its typical entries among fp16's normal numbers, and an entry
-// may grow to 64.  X is held in two fp16 (value and rest, 22 bits), since a X carries the small
+// of up to 2^14 on a side keeps its typical entries among fp16's normal numbers, and the entries
+// of A and P may grow to 63.9 (A's diagonal are the squared norms of X's rows, so those to 7.99 and
+// X's entries no further).  What passes that is infinite, and the result is then NaN or infinite
+// (b times an infinite A is NaN even for b = 0), which the last product reports.  X is held in two fp16 (value and rest, 22 bits), since a X carries the small
 // singular values on unrounded: with one, each step's rounding noise is multiplied by a like
 // they are (an update of rank 64 over noise 1 / 50 of it: 0.013 of the result off, with two
 // 0.0004; bf16 0.11).
@@ -45,6 +47,19 @@ using gemm::Tile;
 
 constexpr float kDown = 1.f / 1024.f;   // the operands' scale is 2^10
 constexpr int kPrecise = 128;
+
+// Adds a bit to the caller's status word; many threads may, so each looks first.
+__device__ __forceinline__ void report(uint32_t* status, uint32_t bit) {
+  if (status && !(*static_cast<volatile uint32_t*>(status) & bit)) atomicOr(status, bit);
+}
+// Whether one of the first n is infinite or NaN (0 times it is NaN).
+__device__ __forceinline__ bool not_finite(const float (&v)[8], int n) {
+  float z = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (j < n) z = __fmaf_rn(v[j], 0.f, z);
+  return z != 0.f;
+}
 
 int64_t pad8(int64_t n) { return (n + 7) / 8 * 8; }
 size_t pad256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -173,6 +188,7 @@ struct ApplyOp {
     uint16_t* out;          // bf16, or NULL
     int64_t ldo, out_matrix;
     int out_vec;            // its rows start on 16-byte boundaries
+    uint32_t* status;
   };
   static __device__ __forceinline__ Tile tile(const Params& p, int t, int tm, int tn) {
     return stacked(t, p.per, p.n_mt, p.n_nt, tm, tn, p.m, p.n, 0);
@@ -200,6 +216,7 @@ struct ApplyOp {
         v[2 * j + 1] = __fmul_rn(o[j].y, kDown);
       }
       store8(p.out + tl.which * p.out_matrix + row * p.ldo + col, v, n);
+      if (not_finite(v, n)) report(p.status, RLK_STATUS_NONFINITE);
       return;
     }
     p.to.store8(p.to.at(tl.which, row, col), o);
@@ -218,7 +235,10 @@ struct ApplyOp {
     for (int k = 0; k < 8; ++k) {
       const float x = __fadd_rn(unpack_half(h[k]).x, unpack_half(r[k]).x);
       const float y = __fmul_rn(__fmaf_rn(v[k], kDown, __fmul_rn(p.a, x)), kDown);
-      if (k * step < n) p.out[tl.which * p.out_matrix + (row + k * step) * p.ldo + col] = (uint16_t)pack_bf16(y, 0.f);
+      if (k * step < n) {
+        p.out[tl.which * p.out_matrix + (row + k * step) * p.ldo + col] = (uint16_t)pack_bf16(y, 0.f);
+        if (!isfinite(y)) report(p.status, RLK_STATUS_NONFINITE);
+      }
     }
   }
 };
@@ -366,7 +386,7 @@ __global__ void __launch_bounds__(OT) orth_start_kernel(const Start a) {
       if (!finite) {
         s_f[0] = NAN;
         s_f[1] = s_f[2] = 1.f;
-        if (a.status && blockIdx.x == 0) atomicOr(a.status, RLK_STATUS_NONFINITE);
+        if (blockIdx.x == 0) report(a.status, RLK_STATUS_NONFINITE);
       } else if (n == 0.f) {   // eps is 0 and so is G
         s_f[0] = 0.f;
         s_f[1] = s_f[2] = 1.f;
@@ -417,6 +437,7 @@ struct Resident {
   uint16_t* out;          // bf16
   int64_t ldo, out_matrix;
   int out_vec;
+  uint32_t* status;
   long long limit;
   int withhold;           // debug: the first CTA's load waits for an arrival that never comes
 };
@@ -647,6 +668,7 @@ __global__ void __launch_bounds__(RT, 1) orth_resident_kernel(const __grid_const
         w[2 * i] = dead ? NAN : __fmul_rn(o[i].x, kDown);
         w[2 * i + 1] = dead ? NAN : __fmul_rn(o[i].y, kDown);
       }
+      if (not_finite(w, n)) report(p.status, RLK_STATUS_NONFINITE);
       if (p.out_vec) {
         store8(to + j * 8, w, n);
       } else {
@@ -793,6 +815,7 @@ cudaError_t launch_resident(const OrthArgs& a, const Buffer& x, int cluster, cud
   p.ldo = a.ldo;
   p.out_matrix = a.out_matrix;
   p.out_vec = out_vec(a);
+  p.status = a.status;
   p.limit = debug_wait_limit();
   p.withhold = (int)debug_take_withheld();
   cudaLaunchConfig_t cfg{};
@@ -921,6 +944,7 @@ cudaError_t iterate(const OrthArgs& a, const Layout& l, cudaStream_t stream) {
       p.ldo = a.ldo;
       p.out_matrix = a.out_matrix;
       p.out_vec = out_vec(a);
+      p.status = a.status;
     }
     if ((e = run_apply<Apply>(maps, p, a.B, cov, stream)) != cudaSuccess) return e;
   }

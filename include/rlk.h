@@ -1302,15 +1302,19 @@ rlk_status rlk_gated_linear_bwd(const void* dy, int64_t lddy, const void* x, int
  *                  or overlap rows: g is only read).
  *  steps           1 to 64.
  *  coefficients    host pointer to a, b, c (read before the call returns): finite,
- *                  each at most 16 in magnitude.  An iteration that they make
- *                  diverge past entries of 64 ends in infinities or NaN; entries below
- *                  2^-24 count with their bits above 2^-34 only.
+ *                  each at most 16 in magnitude.  Every step's A and b A + c A A have to
+ *                  keep their entries at 63.9 or less in magnitude (for A: the norms of
+ *                  X's rows, or columns for m > n, at 7.99 or less before each step;
+ *                  singular values of up to 7.99 suffice).  An iteration that passes
+ *                  that ends in infinities or NaN; entries below 2^-24 count with their
+ *                  bits above 2^-34 only.
  *  eps             finite, >= 0 (with 0 a matrix of zeros gives zeros).
  *  out             device bf16, laid out by ldo (>= n) and out_matrix_stride (>= m rows:
  *                  (m - 1) ldo + n); may be g itself (same address and strides, bf16),
  *                  may not overlap it otherwise.
  *  out_status_word device uint32[1] or NULL: a matrix with a NaN or an infinity gives
- *                  NaN and RLK_STATUS_NONFINITE; the others are not affected.
+ *                  NaN and RLK_STATUS_NONFINITE; the others are not affected.  A result
+ *                  with a NaN or an infinity gives that bit whatever its cause.
  *  workspace       at least rlk_workspace_size(RLK_OP_ORTHOGONALISE, n_matrices, m, n)
  *                  bytes (about 8 m n + 4 min(m, n)^2 a matrix, or + 8), 16-byte aligned,
  *                  contents on entry do not matter.
