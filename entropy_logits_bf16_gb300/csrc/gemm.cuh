@@ -8,7 +8,8 @@
 //    accumulators, so that a tile's epilogue runs under the next tile's products.
 //  * Few tiles: 128 x 128 a CTA, K split over a cluster of up to 4 CTAs whose partial tiles are
 //    added in rank order through distributed shared memory.
-// Every wait is bounded; when one runs out the CTA's unfinished tiles are NaN.
+// Every wait is bounded; when one runs out the CTA's unfinished tiles are NaN and the status
+// word, where the call has one, gets RLK_STATUS_TIMEOUT.
 //
 // An Op has
 //   A_MN, B_MN   whether an operand holds its rows' index contiguously
@@ -34,6 +35,7 @@
 #include <type_traits>
 
 #include "internal.h"
+#include "rlk.h"
 #include "tensor_core.cuh"
 
 namespace rlk {
@@ -78,9 +80,14 @@ struct Loop {
   int tri;               // side of a TRI operand's blocks (a multiple of a tile's rows), or 0
   int a_rows;            // rows of A's boxes (K-contiguous, tiles of 128 x 128; else 128)
   long long wait_limit;
+  uint32_t* status;      // RLK_STATUS_TIMEOUT goes here when a wait runs out (NULL: the call has no such word)
   int withhold;          // debug: the stage of the first CTA whose barrier waits for an arrival that never comes (-1: none)
 };
 
+// Adds a bit to the caller's status word; many threads may, so each looks first.
+__device__ __forceinline__ void report(uint32_t* status, uint32_t bit) {
+  if (status && !(*static_cast<volatile uint32_t*>(status) & bit)) atomicOr(status, bit);
+}
 // Tile t of n_mt x n_nt: groups of 8 row tiles, row tiles fastest inside a group, so that the
 // CTAs at work share tiles of both operands in L2.
 __device__ __forceinline__ void grouped(int t, int n_mt, int n_nt, int& mt, int& nt) {
@@ -319,6 +326,7 @@ __global__ void __launch_bounds__(Shape<SPLIT>::THREADS, SPLIT ? 2 : 1)
       if (!SPLIT && Op::vec(p)) ask(tl.col + part * WIDTH);   // on its way while the products run
       // after a wait has run out, this tile and the CTA's later ones are NaN
       ok = __all_sync(0xFFFFFFFFu, ok && tc::wait(accf0 + 8 * acc, accph, abort_flag, limit));
+      if (!ok && lane == 0) report(p.loop.status, RLK_STATUS_TIMEOUT);
       tc::fence_after();
 #pragma unroll 1
       for (int ch = 0; ch < WIDTH / 32; ++ch) {
@@ -447,6 +455,7 @@ __global__ void __launch_bounds__(Shape<SPLIT>::THREADS, SPLIT ? 2 : 1)
     bool dead = false;    // a wait of some CTA of the cluster ran out
     const uint32_t abort_at = smem_u32(bars + 2 * MAX_STAGES + 4);
     for (int k = 0; k < cluster; ++k) dead = tc::ld_peer_u32(tc::peer_addr(abort_at, (uint32_t)k)) != 0u || dead;
+    if (dead && threadIdx.x == 0) report(p.loop.status, RLK_STATUS_TIMEOUT);
     if (vec) {
       for (int i = threadIdx.x; i < items; i += S::THREADS) {
         int r, c, n, r2, c2, n2;

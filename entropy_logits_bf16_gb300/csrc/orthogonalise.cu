@@ -44,14 +44,11 @@ namespace {
 using gemm::Loop;
 using gemm::Operand;
 using gemm::Tile;
+using gemm::report;
 
 constexpr float kDown = 1.f / 1024.f;   // the operands' scale is 2^10
 constexpr int kPrecise = 128;
 
-// Adds a bit to the caller's status word; many threads may, so each looks first.
-__device__ __forceinline__ void report(uint32_t* status, uint32_t bit) {
-  if (status && !(*static_cast<volatile uint32_t*>(status) & bit)) atomicOr(status, bit);
-}
 // Whether one of the first n is infinite or NaN (0 times it is NaN).
 __device__ __forceinline__ bool not_finite(const float (&v)[8], int n) {
   float z = 0.f;
@@ -188,7 +185,6 @@ struct ApplyOp {
     uint16_t* out;          // bf16, or NULL
     int64_t ldo, out_matrix;
     int out_vec;            // its rows start on 16-byte boundaries
-    uint32_t* status;
   };
   static __device__ __forceinline__ Tile tile(const Params& p, int t, int tm, int tn) {
     return stacked(t, p.per, p.n_mt, p.n_nt, tm, tn, p.m, p.n, 0);
@@ -216,7 +212,7 @@ struct ApplyOp {
         v[2 * j + 1] = __fmul_rn(o[j].y, kDown);
       }
       store8(p.out + tl.which * p.out_matrix + row * p.ldo + col, v, n);
-      if (not_finite(v, n)) report(p.status, RLK_STATUS_NONFINITE);
+      if (not_finite(v, n)) report(p.loop.status, RLK_STATUS_NONFINITE);
       return;
     }
     p.to.store8(p.to.at(tl.which, row, col), o);
@@ -237,7 +233,7 @@ struct ApplyOp {
       const float y = __fmul_rn(__fmaf_rn(v[k], kDown, __fmul_rn(p.a, x)), kDown);
       if (k * step < n) {
         p.out[tl.which * p.out_matrix + (row + k * step) * p.ldo + col] = (uint16_t)pack_bf16(y, 0.f);
-        if (!isfinite(y)) report(p.status, RLK_STATUS_NONFINITE);
+        if (!isfinite(y)) report(p.loop.status, RLK_STATUS_NONFINITE);
       }
     }
   }
@@ -652,6 +648,7 @@ __global__ void __launch_bounds__(RT, 1) orth_resident_kernel(const __grid_const
   tc::cluster_sync();
   bool dead = false;
   for (int k = 0; k < C; ++k) dead = tc::ld_peer_u32(tc::peer_addr(smem_u32(bars + 3), (uint32_t)k)) != 0u || dead;
+  if (dead && threadIdx.x == 0) report(p.status, RLK_STATUS_TIMEOUT);
   const int64_t r0 = TALL ? rank * 128 + row : row, c0 = (TALL ? 0 : rank * 128) + half * 64;
   if (r0 < p.m) {
     uint16_t* to = p.out + matrix * p.out_matrix + r0 * p.ldo + c0;
@@ -903,6 +900,7 @@ cudaError_t iterate(const OrthArgs& a, const Layout& l, cudaStream_t stream) {
     set(maps.a, of_x[i][TALL]);
     set(maps.b, of_x[i][TALL]);
     typename Gram::Params g{};
+    g.loop.status = a.status;
     g.loop.part_steps = (int)((longer + gemm::BK - 1) / gemm::BK);
     g.loop.k_steps = terms * g.loop.part_steps;
     g.side = (int)l.side;
@@ -914,6 +912,7 @@ cudaError_t iterate(const OrthArgs& a, const Layout& l, cudaStream_t stream) {
     set(maps.ta, of_gram[1]);
     set(maps.tb, of_gram[1]);
     typename Poly::Params q{};
+    q.loop.status = a.status;
     q.loop.part_steps = side_steps;
     q.loop.k_steps = terms * side_steps;
     q.side = (int)l.side;
@@ -932,6 +931,7 @@ cudaError_t iterate(const OrthArgs& a, const Layout& l, cudaStream_t stream) {
       set(maps.b, of_x[i][1]);
     }
     typename Apply::Params p{};
+    p.loop.status = a.status;
     p.loop.part_steps = side_steps;
     p.loop.k_steps = terms * side_steps;
     p.m = a.m;
@@ -944,7 +944,6 @@ cudaError_t iterate(const OrthArgs& a, const Layout& l, cudaStream_t stream) {
       p.ldo = a.ldo;
       p.out_matrix = a.out_matrix;
       p.out_vec = out_vec(a);
-      p.status = a.status;
     }
     if ((e = run_apply<Apply>(maps, p, a.B, cov, stream)) != cudaSuccess) return e;
   }

@@ -1321,7 +1321,7 @@ rlk_status rlk_gated_linear_bwd(const void* dy, int64_t lddy, const void* x, int
  * Deterministic.  A matrix's last bits may depend on how many are in the call
  * (sums are split by the tiles there are).  Tiles whose operands did not come
  * within the limit of a wait (about a second) are NaN (up to 128 x 1024 the
- * whole matrix may be).
+ * whole matrix may be), and RLK_STATUS_TIMEOUT is set too.
  * Errors: RLK_ERR_INVALID_ARG for sizes, strides or numbers outside the rules, a
  *  bad dtype, null or misaligned pointers; RLK_ERR_WORKSPACE.  n_matrices == 0
  *  returns RLK_OK without launching.
