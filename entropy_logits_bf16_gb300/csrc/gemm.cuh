@@ -162,9 +162,11 @@ __global__ void __launch_bounds__(Shape<SPLIT>::THREADS, SPLIT ? 2 : 1)
   }
   if (warp == 1) tc::alloc<G>(smem_u32(tmem_slot), TMEM_COLS);
   tc::fence_before();
-  pdl_trigger();   // the next kernel gets ready where there is room, and waits for this one's end
-  pdl_wait();      // the operands may come from the kernel before
   __syncthreads();
+  // The next kernel gets ready where there is room, and waits for this one's end: only now that
+  // this CTA has its TMEM, which the other's would else hold while they wait for this grid.
+  pdl_trigger();
+  pdl_wait();      // the operands may come from the kernel before
   if (G == 2) tc::cluster_sync();   // the other CTA's barriers are there
   tc::fence_after();
   const uint32_t tmem = *tmem_slot;
