@@ -181,6 +181,7 @@ struct Row {
 
 // A lane's share of a virtual warp: sums relative to a reference m that trails the largest
 // logit seen (`top`) by at most `slack`, 16 powers of two, so that it hardly ever moves.
+// (Temperatures over 3.8e36: less, so that z - m stays in fp32 from the first reference on, -FLT_MAX.)
 struct Sums {
   float m = -FLT_MAX, top = -INFINITY;
   float2 s = make_float2(0.f, 0.f), t = make_float2(0.f, 0.f);
@@ -575,7 +576,7 @@ __global__ void __launch_bounds__(Cut<C, VW>::NT, 1024 / Cut<C, VW>::NT) token_f
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Row<DT, ALIGNED> row(a.logits, t, a.ld, a.V);
   const int groups = row.groups();
-  const float slack = __fdiv_rn(16.f, c);
+  const float slack = fminf(__fdiv_rn(16.f, c), 0x1p125f);
   Given<DT> given;
   if (rank == 0 && (int)threadIdx.x < a.C) given.ask(a, t, row.p, threadIdx.x);
 
@@ -672,7 +673,7 @@ __global__ void __launch_bounds__(Cut<1, 32>::NT + 32, RING_CTAS)
     }
     return;
   }
-  const float slack = __fdiv_rn(16.f, c);
+  const float slack = fminf(__fdiv_rn(16.f, c), 0x1p125f);
   const int inner = (groups - 2) / 1024;   // rounds whose groups all have two after them
   uint32_t slot = 0, phase = 0;
   bool ok = true;   // once a wait has run out, no later one counts (a barrier's parity could pass for it)

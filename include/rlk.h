@@ -1123,7 +1123,8 @@ typedef struct rlk_token_state {
  *   alternatives: the n_top largest logits in order, equal ones by the lower id,
  *   each with its log-probability.
  * A logit of -inf rules its token out (p = 0, log-probability -inf, no part of
- * H, never an alternative).  One pass over the logits; sums in fp32.
+ * H, never an alternative).  One pass over the logits; sums in fp32, and the
+ * logits' distances from the row's largest: one beyond 3.4e38 counts as infinite.
  *
  * Arguments
  *  logits          device, dtype `dtype`, T x ld elements (ld >= V, unit stride
