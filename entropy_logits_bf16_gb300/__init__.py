@@ -1321,6 +1321,9 @@ def gated_linear_backward(dy: torch.Tensor, x, w_gate: torch.Tensor, w_up: torch
     if accumulate and ((want_weight_grad and (grad_w_gate is None or grad_w_up is None))
                        or (want_bias_grad and (grad_bias_gate is None or grad_bias_up is None))):
         raise ValueError("accumulate needs the gradients to add to")
+    for a, b in ((grad_w_gate, grad_w_up), (grad_bias_gate, grad_bias_up)):
+        if a is not None and b is not None and a.data_ptr() == b.data_ptr():
+            raise ValueError("the gate's and up's gradients must be tensors of their own")
     dev = dy.device
     dx = torch.empty((M, K), device=dev, dtype=grad_dtype) if want_x_grad else None
     xdt = 0 if dx is None else _matrix(dx, "dx")[0]

@@ -1213,7 +1213,8 @@ rlk_status rlk_token_logprobs_bwd(const void* logits, rlk_dtype dtype, int64_t T
  *  y               device, y_dtype, M x ldy elements (ldy >= N); may not overlap the
  *                  inputs.
  *  out_gate, out_up   device bf16, M x ldz elements (ldz >= N) each: g and u for
- *                  rlk_gated_linear_bwd; both or neither (NULL).
+ *                  rlk_gated_linear_bwd; both or neither (NULL); no output may overlap
+ *                  another or the inputs.
  *  workspace       aligned copies of x and the weights when M > 4 and their rows do
  *                  not start on 16-byte boundaries: then at least
  *                  rlk_workspace_size(RLK_OP_GATED_LINEAR, M, N, K) bytes serve,
@@ -1255,6 +1256,7 @@ rlk_status rlk_gated_linear_fwd(const void* x, int64_t ldx, const void* w_gate, 
  *  grad_w_gate, grad_w_up   device, grad_w_dtype, N x ldgwg / ldgwu elements (>= K);
  *                  both or neither (NULL).
  *  grad_bias_gate, grad_bias_up   device float[N]; both or neither (NULL).
+ *                  No gradient may overlap another or an input.
  *  accumulate      non-zero: the weights' (RLK_F32 only) and biases' gradients are
  *                  added to.
  *  workspace       at least rlk_workspace_size(RLK_OP_GATED_LINEAR_BWD, M, N, K)
