@@ -750,10 +750,10 @@ __global__ void __launch_bounds__(BT, 4) token_backward_kernel(TokenBwdArgs a, f
   const float M = st.x, log2S = st.y, H = st.z;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 
-  // where 16-byte groups of the run start, and whether the gradient's groups start there too
+  // where 16-byte groups of the run start, and whether the gradient's groups can be stored whole there
   const uintptr_t za = reinterpret_cast<uintptr_t>(z + first), oa = reinterpret_cast<uintptr_t>(out) + (uintptr_t)first * (OT ? 4 : 2);
   int head = (int)((16u - (za & 15u)) & 15u) / (int)sizeof(*z);
-  const bool vec = ((oa + (uintptr_t)head * (OT ? 4 : 2)) & 15u) == 0;
+  const bool vec = (oa + (uintptr_t)head * (OT ? 4 : 2)) % (OT ? 16 : 2 * E) == 0;   // the size of its stores
   if (head > last - first) head = last - first;
   const int body = vec ? (last - first - head) / E : 0;   // whole groups
   const uint4* zg = reinterpret_cast<const uint4*>(z + first + head);
