@@ -777,15 +777,20 @@ cudaError_t run_apply(const gemm::MapsOf<Op>& maps, typename Op::Params& p, int6
   return c.x_few ? gemm::launch<Op, true>(maps, p, stream) : gemm::launch<Op, false>(maps, p, stream);
 }
 
-// The CTAs of a matrix's cluster, or 0 where the products are launches of their own.  A cluster
-// waits on its own chain, so many matrices of several CTAs each fill the SMs less well than
-// products of the whole stack (us, this and launches: 128 x 256 68 of them 80 and 184, 760 602
-// and 853; 64 x 512 68 156 and 170, 103 221 and 219; 128 x 768 46 181 and 248, 91 336 and 323;
-// 128 x 1024 one 90 and 164, 17 178 and 195, 34 263 and 220; both with a start that took 4 to 10 us more).
+// The CTAs of a matrix's cluster, or 0 where the products are launches of their own.  The SMs hold
+// 76 clusters of 2 at a time, 46, 36, 28, 23, 15 and 15 of 3 to 8, and a round of them takes as long
+// as one matrix, where launches fill the SMs evenly.  The limits are two such rounds, or one where seven
+// or eight CTAs share a matrix of up to 64, whose launches are shorter.  Replayed, us, one kernel and
+// launches: 760 of 128 x 256 555 and 810; 90 of 128 x 384 137 and 201, 96 of 64 x 384 175 and 142; 68 of
+// 128 x 512 135 and 176, 74 187 and 178; 68 of 64 x 512 131 and 135, 76 185 and 137; 44 of 128 x 768 155 and
+// 211, 48 214 and 211; 24 of 128 x 1024 162 and 183, 33 231 and 184; 14 of 64 x 1024 85 and 130, 16 150 and
+// 131.  (By the SMs, not by asking for the clusters that fit: that differs between cards, and with it
+// the bits of a call.  The limits lose where a third round still pays: 60 of 128 x 768 225 and 260.)
 int resident_cluster(int64_t B, int64_t side, int64_t longer) {
-  const int64_t c = (longer + 127) / 128;
+  const int64_t c = (longer + 127) / 128, sms = sm_count();
   if (side > 128 || c > RES_MOST) return 0;
-  return c <= 2 || B * c <= (c <= 6 ? 2 : 1) * (int64_t)sm_count() ? (int)c : 0;
+  const int64_t most = c <= 6 ? sms * 9 / 5 : (side > 64 ? sms * 11 / 8 : sms * 2 / 3);
+  return c <= 2 || B * c <= most ? (int)c : 0;
 }
 
 template <bool TALL>
