@@ -14,8 +14,10 @@
 //
 // Measured: 8192 x 14336 x 4096 with SiLU, projections kept, 1010 to 1090 us (1.76 to 1.9 PFLOP/s; tensor
 // pipe 88 % of its cycles), 1160 to 1210 in a loop under the power cap; backward of 8192 x 8192 x 4096 1340 to
-// 1400 us (dx 93 %, both dW 85 %, dg and du 110 us); one row of 14336 x 4096 35 us (6.66 TB/s); 64 rows 50;
-// 1531 x 2731 x 1001 off 16 bytes with GELU 35 (17 of them copies).
+// 1440 us (dx 93 %, both dW 85 %, dg and du 110 us), fp32 weight gradients 1465, accumulated 1520, x from its
+// checkpoint 1440; one row of 14336 x 4096 35 us (6.66 TB/s); 8 rows 48, 64 rows 50 to 51, 128 rows 55 (224 tiles
+// on 152 SMs: 72 of them work on two); 1531 x 2731 x 1001 off 16 bytes with GELU 33 to 37 (17 of them copies; 1536 x
+// 2736 x 1008 22.5), its backward 94 (74).
 //
 // dg and du are rounded to bf16 for the products, as the tensor cores need (relative 2^-8 a
 // term, of either sign); the bias gradients sum them unrounded.
@@ -256,6 +258,9 @@ bool few_tiles(int64_t M, int64_t N, int products, int out) {
 // a run of K), U loads of each weight in flight a lane, at distances known when this is
 // compiled.  W columns a load: 8, 2 or 1 by the alignment of the rows of x and the weights.
 // Their sums are joined in a fixed order.
+// Up to four rows whatever the weights, as in the linear layer (us, this and tiles: 14336 x 4096 1 row
+// 36 and 47, 2 rows 39 and 47; 2048 x 1024 4 rows 5.2 and 6.9.  3 and 4 rows of large weights would be faster as tiles,
+// 52 and 54 here and 47 there, 4096 x 14336 75 and 78 and 48: the converted weights meet each row's loads of x.)
 constexpr int FEW_ROWS = 4, FEW_T = 256;
 template <int W>
 struct Word;

@@ -26,12 +26,15 @@
 // the average of many.  Where the shorter side is kPrecise or less there may be few to average
 // over, and the call is bound by its chain: A and P are held in two fp16 as well, and each
 // product is three (values, value times rest both ways), one sum in the accumulator (as launches,
-// 64 x 64: 107 us in all, 95 with one product each; at 256 x 256 163 and 137).
+// replayed: 64 x 64 109 us, 98 with one product each; 256 x 256 144 and 123).  The errors add up less well
+// where few directions or many steps count (2-norm, the bf16 rounding's 0.0017 included: noise 0.0021 to 0.0024,
+// 300 x 700 with one row of numbers 0.0040, ten steps on 300 x 700 0.0045).
 //
-// Measured: 4096 x 14336 2.84 to 2.92 ms (1.36 PFLOP/s with halves of A and P counted; A 86 % of the tensor
-// pipe, X 61 to 70 %: operands at the 64 bytes a cycle that an SM takes from L2, and 16 bytes an element in
-// its epilogue), 4096 x 4096 1.0 ms, 24 x 512 x 1024 320 to 338 us, 2731 x 1003 237 us, 256 x 256 126 us: the
-// last three by what a launch costs besides its products (8 to 15 us each, 17 launches).
+// Measured (replayed graphs, the start included): 4096 x 14336 2.84 to 3.0 ms (1.32 to 1.39 PFLOP/s with halves of
+// A and P counted; A 86 % of the tensor pipe, X 61 to 70 %: operands at the 64 bytes a cycle that an SM takes
+// from L2, and 16 bytes an element in its epilogue), 4096 x 4096 1.0 to 1.09 ms, 24 x 512 x 1024 311 to 338 us,
+// 2731 x 1003 228 to 237 us, 256 x 256 122 to 126 us: the last three by what a launch costs besides its products
+// (8 to 15 us each, 17 launches).
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -42,7 +45,6 @@ namespace rlk {
 namespace {
 
 using gemm::Loop;
-using gemm::Operand;
 using gemm::Tile;
 using gemm::report;
 
@@ -419,8 +421,8 @@ __global__ void __launch_bounds__(OT) orth_start_kernel(const Start a) {
 // each CTA's share of A in TMEM; the shares joined through distributed shared memory, each CTA
 // its part of A for all (in rank order: the same bits in all); A A, P and X's product locally.
 // Bound by the chain of a step's products and epilogues, about 6 us where there is one CTA, 14
-// with eight (one 64 x 64 42 us in all where 17 launches take 122, 128 x 512 69 and 152): a
-// chain of latencies, the tensor pipe 37 % busy and the issue slots 25 % (twice the threads change nothing;
+// with eight (replayed, the start included: one 64 x 64 37 us where 17 launches take 109, 128 x 512
+// 64 and 138, 128 x 1024 78 and 146): a chain of latencies, the tensor pipe 37 % busy and the issue slots 25 % (twice the threads change nothing;
 // fences of all memory instead of this CTA's shared memory cost 3 us).
 constexpr int RT = 256, RES_MOST = 8;   // threads; CTAs of a cluster, 128 of the longer side each
 constexpr uint32_t RES_HALF = 128 * 128 * 2, RES_PITCH = 132;   // bytes of 128 x 128 fp16; floats of a row of shares
@@ -732,7 +734,12 @@ bool stack_map(CUtensorMap* map, void* p, const Buffer& o, int64_t B, int64_t ro
 // linear layer.  Of A and P all where there are SMs for all with K split by four; else the
 // blocks on and below the diagonal, of 128 where X's tiles are small ones too.  A pair's tile
 // needs blocks of 256, so X's are also small ones, two an SM, where those of A and P then get K
-// split by four and with blocks of 256 would not (1024 x 4096: 230 us in all, 254 with pairs).
+// split by four and with blocks of 256 would not.  Replayed, us, blocks of 128 with small tiles for X
+// and blocks of 256: inside those limits 896 x 2560 191 and 211, 1024 x 4096 223 and 241, 1024 x 4864
+// 230 and 247, 2 of 640 x 3584 207 and 264; outside 640 x 4096 203 and 198 (K split by four both ways),
+// 768 x 4096 212 and 203, 3 of 512 x 2560 194 and 189, 1152 x 2560 243 and 234.  All of A where there is an SM
+// for a quarter of each tile: 384 x 3200, four of them 220, blocks of 128 192, of 256 253; 3 of 512 x 1536 162 as
+// all, 173.  (The limits lose at 1152 x 4096, 259 and 290, and 2 of 768 x 3200, 235 and 258.)
 struct Cover {
   bool few, x_few;
   int whole, tri, per;   // tiles a side where all of A's are there, else 0; blocks' side, or 0; A's tiles of a matrix

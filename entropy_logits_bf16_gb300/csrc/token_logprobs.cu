@@ -25,8 +25,9 @@
 // look, which waits for memory), and the others of the SM do not quite fill in.  (A sketch of all
 // groups' maxima in shared memory made the second look small, and took the L1 cache that the loads
 // pass through: 262 us.)  777 x 50021 fp32, rows off 16 bytes, 50 alternatives 50 us (3.1 TB/s): 5.1
-// rows an SM, the last of them alone.  Backward, 4096 x 151936 bf16 with 64 tokens a row 391 us
-// (6.4 TB/s).
+// rows an SM, the last of them alone.  Backward, 4096 x 151936 bf16 with 64 tokens a row 383 to 391 us
+// (6.4 TB/s); 777 x 50021 fp32 55 us, to bf16 43 (floors 46 and 34), to rows that start elsewhere on 16 bytes
+// than the logits' 175 (one element a thread).
 #include <float.h>
 #include <math.h>
 

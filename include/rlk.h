@@ -1295,7 +1295,8 @@ rlk_status rlk_gated_linear_bwd(const void* dy, int64_t lddy, const void* x, int
  * rounded once to bf16.  Where the shorter side is over 128 the operands have 11
  * bits: each singular value is off by up to 0.05 of it after five steps, the
  * whole by about 0.0015 of its root mean square (bf16's rounding alone costs
- * 0.0017); up to 128 they have 22, and the rounding to bf16 is what remains.
+ * 0.0017), by up to 0.0042 where few directions or more steps count; up to 128
+ * they have 22, and the rounding to bf16 is what remains.
  *
  * Arguments
  *  g               device, dtype `dtype`: element (i, r, c) at
